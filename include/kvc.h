@@ -57,8 +57,8 @@ typedef enum {
   KVC_ECAPACITY = -3, /* the append would exceed the capacity; nothing was written */
   KVC_ECUDA = -4,     /* a CUDA runtime call failed (no device, bad stream, launch error) */
   KVC_ETIMEOUT = -5,  /* a bounded device-side wait gave up (read by kvc_sync_status) */
-  KVC_EDEVICE = -6    /* reserved for data a kernel cannot encode exactly (read by
-                         kvc_sync_status); no current kernel reports it */
+  KVC_EDEVICE = -6    /* an index or parent on the device was outside the layer's rows
+                         (kvc_gather, kvc_accept; read by kvc_sync_status) */
 } kvc_status;
 
 enum {
@@ -253,6 +253,91 @@ kvc_status kvc_attend(const kvc_layer *keys, const kvc_layer *values, const floa
 kvc_status kvc_attend_workspace_bytes(const kvc_layer *keys, const kvc_layer *values, int32_t Hq,
                                       size_t *out);
 
+/* Attention of drafted tokens over the cache (speculative decoding): the last
+ * N stored tokens of a key and a value layer are drafts, appended before the
+ * call, and every draft attends at once over the context and over the drafts
+ * that the mask lets it see.  For batch entry b, query head hq and draft i,
+ * with ctx = length - N and h = hq / (Hq / H):
+ *   out[b, hq, i] = sum_t softmax_t(scale * q[b, hq, i] . k_hat[b, h, t]) v_hat[b, h, t]
+ * over the tokens t with first[b] <= t < ctx and the drafts t = ctx + j with
+ * mask[b, i, j] != 0, with k_hat and v_hat as in kvc_attend (the codes are not
+ * reconstructed).  A draft that sees no token gets a row of zeros; what a
+ * hidden token stores, infinities and NaN among it, has no effect.
+ *
+ *  keys       a KVC_MODE_UNIFORM or KVC_MODE_CODEBOOK layer (with or without a
+ *             residual sketch and outlier stream), D at most 256.
+ *  values     a KVC_MODE_INT8 or KVC_MODE_UNIFORM layer with the keys' B, H, D,
+ *             device and length.
+ *  q          device, q_dtype: draft i of head hq of batch b starts at
+ *             q + b*q_stride_b + hq*q_stride_h + i*q_stride_t (elements); the D
+ *             values of a row are contiguous.
+ *  Hq         query heads, any multiple of H.
+ *  N          drafts, 1 .. length.  N = 1 without a mask is a plain decode step.
+ *  mask       device bytes [N][N] (row: the draft that looks, column: the one
+ *             seen), entry b at mask + b*mask_stride_b (0: one mask for the
+ *             batch); NULL: drafts form a chain, j <= i.
+ *  first      device int32 [B], the first visible token of each entry (left
+ *             padding); NULL: 0.  Below 0 reads as 0; at or past ctx hides the
+ *             whole context.
+ *  scale      the score scale; 0 means 1 / sqrt(D).
+ *  out        device, the value layer's out_dtype, element strides as for q.
+ * The workspace is caller-owned scratch, overwritten by the call: calls that
+ * may overlap need one each. */
+typedef struct {
+  const void *q;
+  int32_t q_dtype;
+  int32_t Hq, N;
+  int64_t q_stride_b, q_stride_h, q_stride_t;
+  const uint8_t *mask;
+  int64_t mask_stride_b;
+  const int32_t *first;
+  float scale;
+  void *out;
+  int64_t out_stride_b, out_stride_h, out_stride_t;
+} kvc_tree_desc;
+
+/* Workspace bytes kvc_attend_tree needs for these layers at their current
+ * length, Hq query heads and N drafts (host-only). */
+kvc_status kvc_attend_tree_workspace_bytes(const kvc_layer *keys, const kvc_layer *values,
+                                           int32_t Hq, int32_t N, size_t *out);
+
+/* Run it, asynchronously on `stream`.  workspace: device, 256-byte aligned.
+ * KVC_EINVAL for unsupported modes or shapes, mismatched layers, overlapping
+ * rows of out, host pointers or a short workspace; nothing is launched then. */
+kvc_status kvc_attend_tree(const kvc_layer *keys, const kvc_layer *values,
+                           const kvc_tree_desc *desc, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* Append n rows of `src` to `dst` as they are stored, codes and side words,
+ * without decoding them (a prompt's cache forked into beams, beams reordered
+ * into a second layer, a cache compacted to the tokens a policy keeps).  For
+ * every batch entry b of dst, row length + j of each head is row
+ *   index ? index[b * n + j] : start + j
+ * of batch entry parent ? parent[b] : b of src.
+ *
+ *  parent  device int32 [dst B]; NULL: the same entry (equal B).
+ *  index   device int32 [dst B][n], any order, rows may repeat; NULL:
+ *          consecutive rows from `start`.  With index, start must be 0.
+ * The layers have the same mode, heads and frozen parameters (B, capacity and
+ * dtypes may differ), and every pair of slots between which rows may move has
+ * the same basis and outlier channels.  An entry of parent or index outside
+ * src moves nothing (those rows of dst keep the bytes they had) and
+ * kvc_sync_status(dst) reports KVC_EDEVICE.  dst's length grows by n.
+ * Asynchronous on `stream`.  KVC_ECAPACITY if n does not fit, KVC_EINVAL for
+ * mismatched layers, dst == src, a range outside src or host pointers; nothing
+ * is written then. */
+kvc_status kvc_gather(kvc_layer *dst, const kvc_layer *src, const int32_t *parent,
+                      const int32_t *index, int64_t start, int64_t n, void *stream);
+
+/* Keep n of the last N rows of every batch entry (the accepted ones of N
+ * drafts) and drop the others, in place: with base = length - N, row base + j
+ * becomes what row base + index[b * n + j] was, and the length becomes
+ * base + n.  index: device int32 [B][n], any order, entries may repeat
+ * (0 <= n <= N; NULL if n == 0).  An entry outside [0, N) leaves its row as it
+ * was and kvc_sync_status reports KVC_EDEVICE.  Asynchronous on `stream`.
+ * n up to 98304. */
+kvc_status kvc_accept(kvc_layer *layer, int64_t N, const int32_t *index, int64_t n, void *stream);
+
 /* Order-0 Huffman accounting of the stored codes (kvtc_cache page, module
  * docstring "Byte accounting" and KVTCKVCache.entropy_coding_gain).  Not on
  * the hot path: the store stays fixed width; these calls report what an
@@ -410,8 +495,8 @@ kvc_status kvc_fit_uniform(const kvc_fit_desc *desc, void *workspace, size_t wor
 kvc_status kvc_set_wait_limit(kvc_layer *layer, int64_t ns);
 
 /* Synchronise `stream`, then read and clear the layer's device error word:
- * KVC_OK, KVC_ETIMEOUT (a bounded wait gave up) or KVC_EDEVICE (data the kernel
- * cannot encode exactly).  KVC_ECUDA if the synchronisation itself failed. */
+ * KVC_OK, KVC_ETIMEOUT (a bounded wait gave up) or KVC_EDEVICE (an index outside
+ * the layer's rows).  KVC_ECUDA if the synchronisation itself failed. */
 kvc_status kvc_sync_status(kvc_layer *layer, void *stream);
 
 /* Synchronise `stream` and copy the layer's counters to host out[6]:

@@ -19,7 +19,7 @@ import math
 
 import numpy as np
 
-__all__ = ["softmax", "attend_rows", "attend"]
+__all__ = ["softmax", "attend_rows", "attend", "tree_visible", "attend_tree_rows"]
 
 
 def softmax(s):
@@ -58,3 +58,31 @@ def attend(klayer, vlayer, q, scale=None):
             h = hq // rep
             out[b, hq] = attend_rows(q[b, hq], K[b, h], V[b, h], scale)
     return out
+
+
+def tree_visible(N, S, first=0, mask=None):
+    """Which of S stored tokens each of the last N (drafted) tokens sees, bool
+    [N, S]: the context t < S - N from ``first`` on, and draft j where
+    mask[i, j] (default: j <= i)."""
+    see = np.zeros((N, S), dtype=bool)
+    ctx = S - N
+    see[:, :ctx] = np.arange(ctx) >= first
+    see[:, ctx:] = np.tril(np.ones((N, N), dtype=bool)) if mask is None else np.asarray(mask) != 0
+    return see
+
+
+def attend_tree_rows(q, K, V, scale, visible):
+    """Drafts q [N, D] over decoded keys K and values V [S, D], draft i over the
+    tokens visible[i]; a draft that sees none gets zeros.  Returns the output
+    [N, D] and the weights [N, S]."""
+    q, K, V = (np.asarray(a, dtype=np.float64) for a in (q, K, V))
+    p = np.zeros(visible.shape)
+    for i in range(q.shape[0]):
+        t = np.flatnonzero(visible[i])
+        if len(t):
+            p[i, t] = softmax(scale * (K[t] @ q[i]))
+    out = np.zeros((q.shape[0], V.shape[1]))
+    for i in range(q.shape[0]):
+        t = np.flatnonzero(p[i])
+        out[i] = p[i, t] @ V[t]
+    return out, p

@@ -12,6 +12,7 @@ is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -21,7 +22,7 @@ import numpy as np
 
 __all__ = ["KVCacheLayer", "load_library", "library_path", "KvcError", "MODES", "DTYPES",
            "EXPORTED_SYMBOLS", "store_bytes", "attend", "attend_workspace_bytes", "fit_uniform",
-           "fit_outliers"]
+           "fit_outliers", "attend_tree", "attend_tree_workspace_bytes"]
 
 MODES = {"uniform": 0, "group": 1, "codebook": 2, "int8": 3}
 DTYPES = {"f32": 0, "f16": 1, "bf16": 2}
@@ -37,7 +38,8 @@ EXPORTED_SYMBOLS = (
     "kvc_append_noalloc", "kvc_set_wait_limit", "kvc_attend", "kvc_attend_workspace_bytes",
     "kvc_code_histogram_bytes", "kvc_code_histogram", "kvc_entropy_bytes",
     "kvc_fit_uniform_workspace_bytes", "kvc_fit_uniform", "kvc_store_bytes_prod",
-    "kvc_init_layer_prod", "kvc_fit_outliers",
+    "kvc_init_layer_prod", "kvc_fit_outliers", "kvc_attend_tree_workspace_bytes",
+    "kvc_attend_tree", "kvc_gather", "kvc_accept",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -83,6 +85,16 @@ class _FitDesc(ctypes.Structure):
 class _ProdDesc(ctypes.Structure):
     _fields_ = [("m", c_int32), ("S", POINTER(c_float)), ("n_outliers", c_int32),
                 ("channels", POINTER(c_int32)), ("split_from", c_int64)]
+
+
+class _TreeDesc(ctypes.Structure):
+    _fields_ = [
+        ("q", c_void_p), ("q_dtype", c_int32), ("Hq", c_int32), ("N", c_int32),
+        ("q_stride_b", c_int64), ("q_stride_h", c_int64), ("q_stride_t", c_int64),
+        ("mask", c_void_p), ("mask_stride_b", c_int64), ("first", c_void_p), ("scale", c_float),
+        ("out", c_void_p), ("out_stride_b", c_int64), ("out_stride_h", c_int64),
+        ("out_stride_t", c_int64),
+    ]
 
 
 class _Bytes(ctypes.Structure):
@@ -141,6 +153,11 @@ def load_library():
             "kvc_init_layer_prod": (c_int32, [POINTER(_Desc), POINTER(_ProdDesc), POINTER(c_void_p)]),
             "kvc_fit_outliers": (c_int32, [P, c_int32, c_int32, c_int32, c_int32, c_int64, c_int64,
                                            c_int64, c_int64, c_int32, P, P]),
+            "kvc_attend_tree_workspace_bytes": (c_int32, [P, P, c_int32, c_int32,
+                                                          POINTER(c_size_t)]),
+            "kvc_attend_tree": (c_int32, [P, P, POINTER(_TreeDesc), P, c_size_t, P]),
+            "kvc_gather": (c_int32, [P, P, P, P, c_int64, c_int64, P]),
+            "kvc_accept": (c_int32, [P, c_int64, P, c_int64, P]),
             "kvc_sync_status": (c_int32, [P, P]),
             "kvc_counters": (c_int32, [P, POINTER(c_int64), c_int32, P]),
             "kvc_destroy": (None, [P]),
@@ -239,6 +256,11 @@ def _stream_ptr(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return c_void_p(stream.cuda_stream)
+
+
+def _dev_ptr(t):
+    """A tensor's address; NULL for None and for an empty one."""
+    return None if t is None or t.numel() == 0 else c_void_p(t.data_ptr())
 
 
 _TORCH_DT = None
@@ -343,6 +365,41 @@ class KVCacheLayer:
         _check(self._lib.kvc_fetch(self._h, c_void_p(out.data_ptr()), out.shape[2], byref(s_out),
                                    _stream_ptr(stream, self.device)))
         return out
+
+    # -- rows moved as they are stored -------------------------------------------------------
+    def gather(self, src: "KVCacheLayer", parent=None, index=None, start: int = 0, n=None,
+               stream=None):
+        """Append rows of ``src`` (a layer with the same frozen parameters) as
+        they are stored (kvc_gather).  Batch entry b takes them from entry
+        parent[b] (int32 [B], default b): rows index[b] (int32 [B, n]), or n
+        consecutive ones from ``start`` (default: up to the end of src)."""
+        import torch
+
+        if parent is not None:
+            if parent.dtype != torch.int32 or parent.shape != (self.B,) or not parent.is_contiguous():
+                raise ValueError(f"parent must be a contiguous int32 tensor [{self.B}]")
+        if index is not None:
+            if (index.dtype != torch.int32 or index.dim() != 2 or index.shape[0] != self.B
+                    or not index.is_contiguous()):
+                raise ValueError(f"index must be a contiguous int32 tensor [{self.B}, n]")
+            if n is not None and n != index.shape[1]:
+                raise ValueError("n disagrees with index")
+            n = index.shape[1]
+        elif n is None:
+            n = max(len(src) - int(start), 0)
+        _check(self._lib.kvc_gather(self._h, src._h, _dev_ptr(parent), _dev_ptr(index), int(start),
+                                    int(n), _stream_ptr(stream, self.device)))
+
+    def accept(self, index, N: int, stream=None):
+        """Of the last N tokens keep rows index[b] (int32 [B, n], counted from
+        the first of the N) and drop the others (kvc_accept)."""
+        import torch
+
+        if (index.dtype != torch.int32 or index.dim() != 2 or index.shape[0] != self.B
+                or not index.is_contiguous()):
+            raise ValueError(f"index must be a contiguous int32 tensor [{self.B}, n]")
+        _check(self._lib.kvc_accept(self._h, int(N), _dev_ptr(index), index.shape[1],
+                                    _stream_ptr(stream, self.device)))
 
     # -- state -----------------------------------------------------------------------------
     def trim(self, n: int) -> int:
@@ -459,6 +516,66 @@ def attend(keys: "KVCacheLayer", values: "KVCacheLayer", q, scale: float = 0.0, 
                           c_void_p(out.data_ptr()), c_void_p(workspace.data_ptr()),
                           workspace.numel() * workspace.element_size(),
                           _stream_ptr(stream, q.device)))
+    return out
+
+
+def attend_tree_workspace_bytes(keys: "KVCacheLayer", values: "KVCacheLayer", Hq: int,
+                                N: int) -> int:
+    """Device workspace bytes kvc_attend_tree needs at the layers' current length."""
+    n = c_size_t()
+    _check(load_library().kvc_attend_tree_workspace_bytes(keys._h, values._h, int(Hq), int(N),
+                                                          byref(n)))
+    return int(n.value)
+
+
+def attend_tree(keys: "KVCacheLayer", values: "KVCacheLayer", q, mask=None, first=None,
+                scale: float = 0.0, out=None, workspace=None, stream=None):
+    """Attention of drafted tokens over the cache (kvc_attend_tree): q
+    [B, Hq, N, D] (fp32, fp16 or bf16; last dimension contiguous), the drafts
+    being the last N stored tokens of ``keys`` and ``values``.  mask: bool
+    [N, N] or [B, N, N], mask[.., i, j] true where draft i sees draft j
+    (default: a chain, j <= i).  first: int32 [B], the first visible token of
+    every batch entry (left padding).  Returns out [B, Hq, N, D] in the value
+    layer's out_dtype, zero rows where a draft sees no token."""
+    import torch
+
+    lib = load_library()
+    rev = {v: k for k, v in _torch_dtypes().items()}
+    if q.dim() != 4 or q.dtype not in rev or q.stride(3) != 1:
+        raise ValueError("q must be [B, Hq, N, D] fp32/fp16/bf16 with a contiguous last dimension")
+    B, Hq, N, D = q.shape
+    if B != keys.B or D != keys.D:
+        raise ValueError(f"q must be [{keys.B}, Hq, N, {keys.D}], got {tuple(q.shape)}")
+    mask_stride = 0
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) not in ((N, N), (B, N, N)):
+            raise ValueError(f"mask must be a bool tensor [{N}, {N}] or [{B}, {N}, {N}]")
+        if mask.stride(-1) != 1 or (N > 1 and mask.stride(-2) != N):
+            raise ValueError("the rows of mask must be contiguous")
+        mask_stride = mask.stride(0) if mask.dim() == 3 else 0
+    if first is not None and (first.dtype != torch.int32 or tuple(first.shape) != (B,)
+                              or not first.is_contiguous()):
+        raise ValueError(f"first must be a contiguous int32 tensor [{B}]")
+    n = c_size_t()
+    _check(lib.kvc_attend_tree_workspace_bytes(keys._h, values._h, Hq, N, byref(n)))
+    # what the call allocates belongs to the stream that uses it
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        if out is None:
+            out = torch.empty(B, Hq, N, D, dtype=_torch_dtypes()[values.out_dtype], device=keys.device)
+        if workspace is None:
+            workspace = torch.empty(int(n.value), dtype=torch.uint8, device=keys.device)
+    if (out.shape != q.shape or out.dtype != _torch_dtypes()[values.out_dtype]
+            or out.stride(3) != 1):
+        raise ValueError("out must be [B, Hq, N, D] of the value layer's out_dtype, last dimension contiguous")
+    d = _TreeDesc(q=q.data_ptr(), q_dtype=DTYPES[rev[q.dtype]], Hq=Hq, N=N, q_stride_b=q.stride(0),
+                  q_stride_h=q.stride(1), q_stride_t=q.stride(2),
+                  mask=None if mask is None else mask.data_ptr(), mask_stride_b=mask_stride,
+                  first=None if first is None else first.data_ptr(), scale=float(scale),
+                  out=out.data_ptr(), out_stride_b=out.stride(0), out_stride_h=out.stride(1),
+                  out_stride_t=out.stride(2))
+    _check(lib.kvc_attend_tree(keys._h, values._h, byref(d), c_void_p(workspace.data_ptr()),
+                               workspace.numel() * workspace.element_size(),
+                               _stream_ptr(stream, keys.device)))
     return out
 
 

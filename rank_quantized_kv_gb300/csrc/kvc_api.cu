@@ -33,6 +33,8 @@ struct kvc_layer {
   std::vector<int32_t> basis_host;   // per slot
   std::vector<int64_t> pay_host, side_host;
   std::vector<int32_t> seg_host;     // [nb][kMaxSeg][4] width segments
+  std::vector<int32_t> channels_host;  // [n_slots][n_out] outlier channels
+  uint64_t format[2] = {0, 0};       // hash of everything a stored row decodes by
   kvc::TcPlan tc{};                  // tensor-core path tables (kvc_tc.cu)
 };
 
@@ -514,6 +516,43 @@ kvc_status kvc_init_layer_prod(const kvc_layer_desc* d, const kvc_prod_desc* pro
   return init_from_geo(d, g, out);
 }
 
+// Hash of everything that a stored row decodes by, but its basis number and
+// outlier channels (which belong to a slot): two layers with equal hashes read
+// each other's rows.  Two independent 64-bit multiplicative hashes.
+static void format_hash(const kvc_layer_desc* d, const Geo& g, uint64_t out[2]) {
+  uint64_t a = 0x9E3779B97F4A7C15ull, b = 0xD1B54A32D192ED03ull;
+  auto word = [&](uint64_t v) {
+    a = (a ^ v) * 0xBF58476D1CE4E5B9ull;
+    a ^= a >> 29;
+    b = (b + v) * 0x94D049BB133111EBull;
+    b ^= b >> 31;
+  };
+  auto real = [&](float f) {
+    uint32_t u;
+    std::memcpy(&u, &f, 4);
+    word(u);
+  };
+  for (int v : {d->mode, d->D, d->heads_per_group, g.r, g.nb, g.cb_levels, g.prod, g.m, g.n_out,
+                g.side_bytes, d->mode == KVC_MODE_GROUP ? d->group_size : 0})
+    word((uint64_t)(uint32_t)v);
+  if (d->mode != KVC_MODE_INT8) {
+    const size_t nv = (size_t)g.nb * g.d_in * g.r;
+    for (size_t i = 0; i < nv; ++i) real(d->V[i]);
+    for (size_t i = 0; i < (size_t)g.nb * g.d_in; ++i) real(d->mean ? d->mean[i] : 0.f);
+    for (size_t i = 0; i < g.bits.size(); ++i) {
+      word(g.bits[i]);
+      if (d->mode == KVC_MODE_UNIFORM && g.bits[i]) {
+        real(d->qmin[i]);
+        real(d->qstep[i]);
+      }
+    }
+    for (int j = 0; j < g.cb_levels; ++j) real(d->codebook[j]);
+    for (float f : g.S) real(f);
+  }
+  out[0] = a;
+  out[1] = b;
+}
+
 static kvc_status init_from_geo(const kvc_layer_desc* d, Geo& g, kvc_layer** out) {
   kvc_status st;
   if (!d->store) return fail(KVC_EINVAL, "store is NULL");
@@ -585,6 +624,8 @@ static kvc_status init_from_geo(const kvc_layer_desc* d, Geo& g, kvc_layer** out
   L->pay_host = g.pay_off;
   L->seg_host = g.seg;
   L->side_host = g.side_off;
+  L->channels_host = g.channels;
+  format_hash(d, g, L->format);
   *out = L;
   return succeed();
 }
@@ -799,6 +840,193 @@ kvc_status kvc_attend(const kvc_layer* K, const kvc_layer* V, const float* q, in
   return succeed();
 }
 
+// Checks shared by the tree attention's entry points; fills the shape fields of t.
+static kvc_status tree_check(const kvc_layer* K, const kvc_layer* V, int32_t Hq, int32_t N,
+                             kvc::TreeArgs& t, size_t* ws_bytes) {
+  if (!K || !V) return fail(KVC_ESTATE, "key or value layer is NULL");
+  if (K->mode != KVC_MODE_UNIFORM && K->mode != KVC_MODE_CODEBOOK)
+    return fail(KVC_EINVAL, "keys must be a uniform or codebook layer");
+  if ((V->mode != KVC_MODE_INT8 && V->mode != KVC_MODE_UNIFORM) || V->p.prod)
+    return fail(KVC_EINVAL, "values must be an int8 or uniform layer");
+  if (K->B != V->B || K->H != V->H || K->D != V->D)
+    return fail(KVC_EINVAL, "key and value layers differ in B, H or D");
+  if (K->device != V->device) return fail(KVC_EINVAL, "key and value layers are on different devices");
+  if (K->len != V->len) return fail(KVC_EINVAL, "key and value layers hold different lengths");
+  if (K->D > 256) return fail(KVC_EINVAL, "D must be at most 256");
+  if (Hq < K->H || Hq % K->H) return fail(KVC_EINVAL, "Hq must be a multiple of H");
+  if (N < 1 || N > K->len)
+    return fail(KVC_EINVAL, "N %d drafted tokens: need 1 .. length (%lld)", N, (long long)K->len);
+  if (K->ncpos > 256 || (V->mode == KVC_MODE_UNIFORM && V->ncpos > 256))
+    return fail(KVC_EINVAL, "more than 256 packed positions");
+  // kernels number (slot, row) pairs and (job, CTA) pairs in 32 bits
+  if ((int64_t)K->B * Hq * N > (1 << 30)) return fail(KVC_EINVAL, "too many query rows");
+  t.Hq = Hq;
+  t.rep = Hq / K->H;
+  t.N = N;
+  t.S = K->len;
+  t.ctx = K->len - N;
+  t.NCk = std::max(8, K->ncpos);
+  t.Dv = V->mode == KVC_MODE_INT8 ? V->D : std::max(8, V->ncpos);
+  t.Pk_max = K->pmax;
+  t.Pv_max = V->pmax;
+  t.out_bf16 = V->p.out_dtype == KVC_BF16 ? 1 : 0;
+  t.rows = t.rep * N;
+  if (K->p.prod) {
+    t.prod = 1;
+    t.m = K->p.m;
+    t.n_out = K->p.n_out;
+    t.kcode = K->p.code_bytes;
+    t.knw = K->side_bytes / 2;
+  }
+  DeviceGuard dg(K->device);
+  if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
+  *ws_bytes = kvc::tree_plan(K->p, t, kvc::sm_count());
+  return KVC_OK;
+}
+
+kvc_status kvc_attend_tree_workspace_bytes(const kvc_layer* K, const kvc_layer* V, int32_t Hq,
+                                           int32_t N, size_t* out) {
+  if (!out) return fail(KVC_EINVAL, "out is NULL");
+  kvc::TreeArgs t;
+  size_t n = 0;
+  const kvc_status st = tree_check(K, V, Hq, N, t, &n);
+  if (st) return st;
+  *out = n;
+  return succeed();
+}
+
+kvc_status kvc_attend_tree(const kvc_layer* K, const kvc_layer* V, const kvc_tree_desc* d,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (!d) return fail(KVC_EINVAL, "descriptor is NULL");
+  kvc::TreeArgs t;
+  size_t need = 0;
+  const kvc_status st = tree_check(K, V, d->Hq, d->N, t, &need);
+  if (st) return st;
+  if (!(d->scale >= 0.f) || !std::isfinite(d->scale)) return fail(KVC_EINVAL, "scale must be finite and >= 0");
+  if (d->q_dtype != KVC_F32 && d->q_dtype != KVC_F16 && d->q_dtype != KVC_BF16)
+    return fail(KVC_EINVAL, "q_dtype must be KVC_F32, KVC_F16 or KVC_BF16");
+  if (!d->q || !d->out) return fail(KVC_EINVAL, "q or out is NULL");
+  if (!workspace || workspace_bytes < need)
+    return fail(KVC_EINVAL, "workspace is NULL or below kvc_attend_tree_workspace_bytes()");
+  if ((uintptr_t)workspace % 256) return fail(KVC_EINVAL, "workspace must be 256-byte aligned");
+  if (d->q_stride_b < 0 || d->q_stride_h < 0 || d->q_stride_t < 0 || d->mask_stride_b < 0)
+    return fail(KVC_EINVAL, "strides must be >= 0");
+  const int64_t D = K->D;
+  if ((K->B > 1 && d->out_stride_b < D) || (d->Hq > 1 && d->out_stride_h < D) ||
+      (d->N > 1 && d->out_stride_t < D) || d->out_stride_b < 0 || d->out_stride_h < 0 ||
+      d->out_stride_t < 0)
+    return fail(KVC_EINVAL, "rows of out overlap");
+  if ((uintptr_t)d->q % (d->q_dtype == KVC_F32 ? 4 : 2) || (uintptr_t)d->out % 2 ||
+      (uintptr_t)d->first % 4)
+    return fail(KVC_EINVAL, "an array is not aligned to its element size");
+  DeviceGuard dg(K->device);
+  if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
+  const void* ptrs[] = {d->q, d->out, workspace, d->mask, d->first};
+  for (const void* p : ptrs)
+    if (p && !is_device_ptr(p, K->device))
+      return fail(KVC_EINVAL, "q, mask, first, out and the workspace must be device memory of the layers' device");
+  t.q = d->q;
+  t.q_dtype = d->q_dtype;
+  t.q_sb = d->q_stride_b;
+  t.q_sh = d->q_stride_h;
+  t.q_st = d->q_stride_t;
+  t.mask = d->mask;
+  t.mask_sb = d->mask_stride_b;
+  t.first = d->first;
+  t.out = d->out;
+  t.o_sb = d->out_stride_b;
+  t.o_sh = d->out_stride_h;
+  t.o_st = d->out_stride_t;
+  const double sc = d->scale > 0.f ? (double)d->scale : 1.0 / std::sqrt((double)K->D);
+  t.scale_log2 = (float)(sc * 1.4426950408889634);
+  int nk = 0;
+  const cudaError_t e = kvc::launch_attend_tree(K->p, V->p, t, workspace,
+                                                static_cast<cudaStream_t>(stream), &nk);
+  const_cast<kvc_layer*>(K)->launches += nk;
+  if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+  return succeed();
+}
+
+kvc_status kvc_gather(kvc_layer* dst, const kvc_layer* src, const int32_t* parent,
+                      const int32_t* index, int64_t start, int64_t n, void* stream) {
+  if (!dst || !src) return fail(KVC_ESTATE, "layer is NULL");
+  if (dst == src) return fail(KVC_EINVAL, "source and destination are the same layer");
+  if (n < 0 || start < 0) return fail(KVC_EINVAL, "n and start must be >= 0");
+  if (dst->device != src->device) return fail(KVC_EINVAL, "the layers are on different devices");
+  if (dst->H != src->H || dst->format[0] != src->format[0] || dst->format[1] != src->format[1])
+    return fail(KVC_EINVAL, "the layers differ in heads or frozen parameters");
+  if (!parent && dst->B != src->B) return fail(KVC_EINVAL, "layers of different batches need parent");
+  // a row decodes by its slot's basis and outlier channels: they must agree for
+  // every pair of slots between which rows may move
+  const int Hg = dst->n_slots / dst->B, no = dst->p.n_out;
+  for (int b = 0; b < dst->B; ++b)
+    for (int s = parent ? 0 : b; s < (parent ? src->B : b + 1); ++s)
+      for (int h = 0; h < Hg; ++h) {
+        const int ds = b * Hg + h, ss = s * Hg + h;
+        if (dst->basis_host[ds] != src->basis_host[ss])
+          return fail(KVC_EINVAL, "slot %d has another basis than the source's slot %d", ds, ss);
+        if (no && !std::equal(&dst->channels_host[(size_t)ds * no],
+                              &dst->channels_host[(size_t)ds * no] + no,
+                              &src->channels_host[(size_t)ss * no]))
+          return fail(KVC_EINVAL, "slot %d has other outlier channels than the source's slot %d", ds, ss);
+      }
+  if (!index && n > src->len - start)
+    return fail(KVC_EINVAL, "rows %lld .. %lld of a source of length %lld", (long long)start,
+                (long long)(start + n), (long long)src->len);
+  if (index && start) return fail(KVC_EINVAL, "start goes with consecutive rows, not with index");
+  if (n > dst->capacity - dst->len)
+    return fail(KVC_ECAPACITY, "gather of %lld tokens exceeds capacity %lld (length %lld)",
+                (long long)n, (long long)dst->capacity, (long long)dst->len);
+  if (n == 0) return succeed();
+  if ((uintptr_t)parent % 4 || (uintptr_t)index % 4)
+    return fail(KVC_EINVAL, "parent and index must be 4-byte aligned");
+  DeviceGuard dg(dst->device);
+  if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
+  if ((parent && !is_device_ptr(parent, dst->device)) || (index && !is_device_ptr(index, dst->device)))
+    return fail(KVC_EINVAL, "parent and index must be device memory of the layers' device");
+  kvc::GatherArgs a;
+  a.parent = parent;
+  a.index = index;
+  a.n = n;
+  a.dst_row0 = dst->len;
+  a.src_row0 = start;
+  a.src_len = src->len;
+  int nk = 0;
+  const cudaError_t e = kvc::launch_gather(dst->p, src->p, a, dst->pmax, kvc::sm_count(),
+                                           static_cast<cudaStream_t>(stream), &nk);
+  dst->launches += nk;
+  if (e != cudaSuccess) return cuda_fail(e, "gather launch");
+  dst->len += n;
+  return succeed();
+}
+
+kvc_status kvc_accept(kvc_layer* L, int64_t N, const int32_t* index, int64_t n, void* stream) {
+  if (!L) return fail(KVC_ESTATE, "layer is NULL");
+  if (N < 0 || N > L->len)
+    return fail(KVC_EINVAL, "N %lld outside [0, length %lld]", (long long)N, (long long)L->len);
+  if (n < 0 || n > N) return fail(KVC_EINVAL, "n %lld outside [0, N %lld]", (long long)n, (long long)N);
+  if (n > 0) {
+    if (!index) return fail(KVC_EINVAL, "index is NULL");
+    if ((uintptr_t)index % 4) return fail(KVC_EINVAL, "index must be 4-byte aligned");
+    if (!kvc::accept_columns_per_block(n, 16)) return fail(KVC_EINVAL, "n %lld is too large", (long long)n);
+    DeviceGuard dg(L->device);
+    if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
+    if (!is_device_ptr(index, L->device))
+      return fail(KVC_EINVAL, "index must be device memory of the layer's device");
+    kvc::AcceptArgs a;
+    a.index = index;
+    a.n = n;
+    a.N = N;
+    a.base = L->len - N;
+    int nk = 0;
+    const cudaError_t e = kvc::launch_accept(L->p, a, L->pmax, static_cast<cudaStream_t>(stream), &nk);
+    L->launches += nk;
+    if (e != cudaSuccess) return cuda_fail(e, "accept launch");
+  }
+  L->len += n - N;
+  return succeed();
+}
+
 kvc_status kvc_code_histogram_bytes(const kvc_layer* L, size_t* out) {
   if (!L) return fail(KVC_ESTATE, "layer is NULL");
   if (!out) return fail(KVC_EINVAL, "out is NULL");
@@ -980,6 +1208,7 @@ kvc_status kvc_sync_status(kvc_layer* L, void* stream) {
     if (e != cudaSuccess) return cuda_fail(e, "clear error word");
   }
   if (err == kvc::kErrTimeout) return fail(KVC_ETIMEOUT, "a bounded device wait gave up");
+  if (err == kvc::kErrIndex) return fail(KVC_EDEVICE, "an index or parent outside the layer's rows");
   if (err == kvc::kErrRange) return fail(KVC_EDEVICE, "input outside the exactly encodable range");
   if (err) return fail(KVC_EDEVICE, "device error %d", err);
   return succeed();

@@ -1,0 +1,580 @@
+// Attention of N drafted tokens per sequence over the stored codes.  The
+// drafted tokens are the last N stored tokens of a key and a value layer; a
+// drafted token sees the context (every earlier stored token, from first[b]
+// on) and those drafted tokens that the mask gives it, so a whole tree of
+// drafts is scored in one pass over the cache.
+//
+// With centred codes c' = code - 2^(b-1) of a b-bit component, and u = V^T q:
+//   scores   uniform keys   q . k_hat = sum_j (u_j step_j) c'_j + c1,
+//                           c1 = sum_j u_j (lo_j + 2^(b_j-1) step_j) + q . mean;
+//            codebook keys  q . k_hat = n sum_j u_j c[idx_j], with a residual
+//                           sketch plus sqrt(pi/2)/m ||r|| sum_j (S q)_j (2 bit_j - 1)
+//                           and with an outlier stream plus s sum_l q_{ch_l} o8_l;
+//   weights  softmax over the visible tokens, online and in base 2 (scale
+//            log2(e) folded into the key weights and c1); a hidden token's
+//            weight is 0 whatever its codes, norm or scale hold;
+//   output   int8 values    sum_t p_t s_t q8_t;
+//            uniform values (lo + 2^(b-1) step + step sum_t p_t c'_t) V^T + mean;
+//            zero for a row that sees no token.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "kvc_internal.h"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kThreads = 128;      // 4 warps
+constexpr int kRows = 8;           // rows of a job
+constexpr int kPrepRows = 16;      // rows of a prep block
+constexpr unsigned kFull = 0xffffffffu;
+
+// Packed position j of basis beta: component (-1: padding) and width.
+__device__ int position_component(const Params& p, int beta, int j, int* width) {
+  int nch = 0;
+  for (int s = 0; s < kMaxSeg; ++s) {
+    const int32_t* e = p.seg + ((size_t)beta * kMaxSeg + s) * 4;
+    if (!e[3]) break;
+    const int n = (e[3] + 7) / 8;
+    if (j < (nch + n) * 8) {
+      const int m = j - nch * 8;
+      *width = e[1];
+      return m < e[3] ? p.order[(size_t)beta * p.r + e[2] + m] : -1;
+    }
+    nch += n;
+  }
+  return -1;
+}
+
+// Chunk c (8 packed positions) of basis beta: first byte | width << 16 |
+// valid << 31, 0 past the last one.
+__device__ uint32_t chunk_entry(const Params& p, int beta, int c) {
+  int nch = 0;
+  for (int s = 0; s < kMaxSeg; ++s) {
+    const int32_t* e = p.seg + ((size_t)beta * kMaxSeg + s) * 4;
+    if (!e[3]) break;
+    const int n = (e[3] + 7) / 8;
+    if (c < nch + n) return (uint32_t)(e[0] + e[1] * (c - nch)) | ((uint32_t)e[1] << 16) | (1u << 31);
+    nch += n;
+  }
+  return 0u;
+}
+
+__device__ __forceinline__ uint2 bits_at(const unsigned char* base, int a) {
+  const uint32_t* wp = reinterpret_cast<const uint32_t*>(base) + (a >> 2);
+  const uint32_t w0 = wp[0], w1 = wp[1], w2 = wp[2];
+  const uint32_t sh = 8 * (a & 3);
+  return make_uint2(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh));
+}
+
+__device__ __forceinline__ uint32_t chunk_code(uint2 b, int w, int e) {
+  if (w == 8) return ((e < 4 ? b.x : b.y) >> (8 * (e & 3))) & 0xffu;
+  return (b.x >> (w * e)) & ((1u << w) - 1u);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float load_q(const TreeArgs& t, int64_t i) {
+  if (t.q_dtype == KVC_F32) return static_cast<const float*>(t.q)[i];
+  if (t.q_dtype == KVC_F16) return __half2float(static_cast<const __half*>(t.q)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(t.q)[i]);
+}
+
+// ---------------------------------------------------------------- prep
+
+// One block per (slot, 16 rows): the key weights at every packed position,
+// w_j = scale log2(e) u_j coef_j (coef = step in uniform mode, 1 for a
+// codebook), and c1.  Thread j holds one position of all the block's rows, so
+// V is read once per 16 rows.
+__global__ void __launch_bounds__(kThreads) tree_prep_kernel(const Params kp, const TreeArgs t) {
+  __shared__ __align__(16) float qs[256][kPrepRows];
+  __shared__ float red[kPrepRows][kThreads / 32];
+  const int blocks = (t.rows + kPrepRows - 1) / kPrepRows;
+  const int slot = blockIdx.x / blocks, r0 = (blockIdx.x - slot * blocks) * kPrepRows;
+  const int b = slot / kp.H, h = slot - b * kp.H;
+  const int beta = kp.basis_of[slot];
+  const int D = kp.D, tid = threadIdx.x;
+  const int nr = min(kPrepRows, t.rows - r0);
+  for (int e = tid; e < kPrepRows * D; e += kThreads) {
+    const int r = e / D, i = e - r * D;
+    float v = 0.f;
+    if (r < nr) {
+      const int row = r0 + r, g = row / t.N, n = row - g * t.N;
+      v = load_q(t, b * t.q_sb + (int64_t)(h * t.rep + g) * t.q_sh + n * t.q_st + i);
+    }
+    qs[i][r] = v;
+  }
+  __syncthreads();
+  const bool uniform = kp.mode == KVC_MODE_UNIFORM;
+  float c1[kPrepRows];
+#pragma unroll
+  for (int r = 0; r < kPrepRows; ++r) c1[r] = 0.f;
+  const size_t row0 = (size_t)slot * t.rows + r0;
+  auto dot = [&](const float* col, int stride, float (&s)[kPrepRows]) {
+#pragma unroll
+    for (int r = 0; r < kPrepRows; ++r) s[r] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < D; ++i) {
+      const float v = col[(size_t)i * stride];
+#pragma unroll
+      for (int r = 0; r < kPrepRows; ++r) s[r] = fmaf(qs[i][r], v, s[r]);
+    }
+  };
+  for (int j = tid; j < t.NCk; j += kThreads) {
+    int width = 0;
+    const int k = position_component(kp, beta, j, &width);
+    float u[kPrepRows];
+    float coef = 0.f, off = 0.f;
+    if (k >= 0) {
+      const size_t bk = (size_t)beta * kp.r + k;
+      dot(kp.V + (size_t)beta * D * kp.r + k, kp.r, u);
+      coef = uniform ? kp.step[bk] : 1.f;
+      if (uniform) off = fmaf((float)(1 << (width - 1)), kp.step[bk], kp.lo[bk]);
+    }
+#pragma unroll
+    for (int r = 0; r < kPrepRows; ++r) {
+      if (r >= nr) break;
+      t.w[(row0 + r) * t.NCk + j] = k >= 0 ? t.scale_log2 * u[r] * coef : 0.f;
+      if (k >= 0) c1[r] = fmaf(u[r], off, c1[r]);
+    }
+  }
+  if (t.prod) {  // sketch weights sqrt(pi/2)/m (S q)_j, outlier weights q[ch_l]
+    const int nx = t.m + t.n_out;
+    const float coef = t.m ? 1.2533141373155003f / (float)t.m : 0.f;
+    for (int j = tid; j < nx; j += kThreads) {
+      float u[kPrepRows];
+      if (j < t.m) {
+        dot(kp.W3 + (size_t)(D + j) * D, 1, u);
+      } else {
+        const int ch = kp.channels[(size_t)slot * t.n_out + j - t.m];
+#pragma unroll
+        for (int r = 0; r < kPrepRows; ++r) u[r] = qs[ch][r];
+      }
+#pragma unroll
+      for (int r = 0; r < kPrepRows; ++r)
+        if (r < nr) t.wx[(row0 + r) * nx + j] = t.scale_log2 * (j < t.m ? coef : 1.f) * u[r];
+    }
+  }
+  if (uniform)
+    for (int i = tid; i < D; i += kThreads) {
+      const float v = kp.mean[(size_t)beta * D + i];
+#pragma unroll
+      for (int r = 0; r < kPrepRows; ++r) c1[r] = fmaf(qs[i][r], v, c1[r]);
+    }
+#pragma unroll
+  for (int r = 0; r < kPrepRows; ++r) {
+    const float s = warp_sum(c1[r]);
+    if ((tid & 31) == 0) red[r][tid >> 5] = s;
+  }
+  __syncthreads();
+  if (tid < nr) {
+    float s = 0.f;
+    for (int i = 0; i < kThreads / 32; ++i) s += red[tid][i];
+    t.c1[row0 + tid] = t.scale_log2 * s;
+  }
+}
+
+// ---------------------------------------------------------------- main
+
+// The run of tiles of CTA c is [total c / grid, total (c + 1) / grid).
+__device__ __forceinline__ int64_t run_begin(const TreeArgs& t, int64_t c) {
+  return t.total * c / t.grid;
+}
+
+// Dynamic shared memory: ws [NCk][8], wxs [m + n_out][8], per warp krow [32 Pk + 16] and vrow
+// [32 Pv + 16] (uniform values) and ps [32][8]; merge [4][8][2 + Dv].
+template <int KMODE, int VMODE>
+__global__ void __launch_bounds__(kThreads)
+    tree_main_kernel(const Params kp, const Params vp, const TreeArgs t, int kstage, int vstage) {
+  extern __shared__ __align__(16) unsigned char sm[];
+  __shared__ uint32_t kch[32], vch[32];
+  __shared__ float cbv[256];
+  __shared__ float c1s[kRows];
+  constexpr bool VU = VMODE == KVC_MODE_UNIFORM;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int NCk = t.NCk, Dv = t.Dv, nx = t.m + t.n_out;
+  const int stride = 2 + Dv;
+  float* ws = reinterpret_cast<float*>(sm);
+  float* wxs = ws + NCk * kRows;
+  unsigned char* wbase =
+      reinterpret_cast<unsigned char*>(wxs + nx * kRows) + (size_t)warp * (kstage + vstage + 32 * kRows * 4);
+  unsigned char* krow = wbase;
+  unsigned char* vrow = wbase + kstage;
+  float* ps = reinterpret_cast<float*>(wbase + kstage + vstage);
+  float* merge = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(wxs + nx * kRows) +
+                                          4 * (size_t)(kstage + vstage + 32 * kRows * 4));
+  if (KMODE == KVC_MODE_CODEBOOK)
+    for (int j = tid; j < kp.cb_levels; j += kThreads) cbv[j] = kp.codebook[j];
+
+  const int64_t run1 = run_begin(t, blockIdx.x + 1);
+  for (int64_t at = run_begin(t, blockIdx.x); at < run1;) {
+    const int job = (int)(at / t.tps);
+    const int64_t tile0 = at - job * t.tps;
+    const int64_t tile1 = min(t.tps, tile0 + (run1 - at));
+    at += tile1 - tile0;
+    const int slot = job / t.row_tiles, r0 = (job - slot * t.row_tiles) * kRows;
+    const int nr = min(kRows, t.rows - r0);
+    const int b = slot / kp.H;
+    const int kbeta = kp.basis_of[slot], vbeta = VU ? vp.basis_of[slot] : 0;
+    const int Pk = kp.P[kbeta], Pv = VU ? vp.P[vbeta] : vp.D;
+    __syncthreads();  // the previous job's tables and partial have been read
+    if (tid < 32) {
+      kch[tid] = chunk_entry(kp, kbeta, tid);
+      vch[tid] = VU ? chunk_entry(vp, vbeta, tid) : 0u;
+    }
+    const size_t row0 = (size_t)slot * t.rows + r0;
+    for (int e = tid; e < kRows * NCk; e += kThreads) {
+      const int j = e / kRows, g = e - j * kRows;
+      ws[e] = g < nr ? t.w[(row0 + g) * NCk + j] : 0.f;
+    }
+    for (int e = tid; e < kRows * nx; e += kThreads) {
+      const int j = e / kRows, g = e - j * kRows;
+      wxs[e] = g < nr ? t.wx[(row0 + g) * nx + j] : 0.f;
+    }
+    if (tid < kRows) c1s[tid] = tid < nr ? t.c1[row0 + tid] : 0.f;
+    __syncthreads();
+    int nchk = 0, nchv = 0;
+    while (nchk < 32 && (kch[nchk] >> 31)) ++nchk;
+    if (VU)
+      while (nchv < 32 && (vch[nchv] >> 31)) ++nchv;
+    int LG = 1;  // uniform values: LG chunk lanes x (32 / LG) token groups
+    while (LG < nchv) LG *= 2;
+    const int vc = lane & (LG - 1), tg = lane / LG, TG = 32 / LG;
+    const unsigned char* kbase = kp.store + kp.pay_off[slot];
+    const __half* knorm = reinterpret_cast<const __half*>(kp.store + kp.side_off[slot]);
+    const unsigned char* vbase = vp.store + vp.pay_off[slot];
+    const __half* vscale = reinterpret_cast<const __half*>(vp.store + vp.side_off[slot]);
+    const int64_t first = t.first ? t.first[b] : 0;
+    const uint8_t* mask = t.mask ? t.mask + b * t.mask_sb : nullptr;
+
+    float m[kRows], l[kRows], acc[kRows][8];
+#pragma unroll
+    for (int g = 0; g < kRows; ++g) {
+      m[g] = -INFINITY;
+      l[g] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[g][e] = 0.f;
+    }
+    const int64_t t1 = min(t.S, tile1 * kTreeTile);
+    for (int64_t tb = tile0 * kTreeTile + 32 * warp; tb < t1; tb += kTreeTile) {
+      // blocks of hidden context only
+      if (tb + 32 <= min(first, t.ctx)) continue;
+      const int nrow = (int)min((int64_t)32, t1 - tb);
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(kbase + tb * Pk);
+        const int nv = (nrow * Pk + 15) >> 4;
+        for (int i = lane; i < nv; i += 32) reinterpret_cast<uint4*>(krow)[i] = src[i];
+        if (VU) {
+          const uint4* vs = reinterpret_cast<const uint4*>(vbase + tb * Pv);
+          const int nvv = (nrow * Pv + 15) >> 4;
+          for (int i = lane; i < nvv; i += 32) reinterpret_cast<uint4*>(vrow)[i] = vs[i];
+        }
+      }
+      __syncwarp();
+      const int64_t tok = tb + lane;
+      const bool live = lane < nrow;
+      float sc[kRows];
+#pragma unroll
+      for (int g = 0; g < kRows; ++g) sc[g] = 0.f;
+      float sv = 1.f;  // value scale
+      if (live) {
+        const int row = lane * Pk;
+        for (int c = 0; c < nchk; ++c) {
+          const uint32_t ent = kch[c];
+          const int w = (int)((ent >> 16) & 0xfu);
+          const uint2 bits = bits_at(krow, row + (int)(ent & 0xffffu));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t code = chunk_code(bits, w, e);
+            const float v = KMODE == KVC_MODE_CODEBOOK ? cbv[code] : (float)((int)code - (1 << (w - 1)));
+            const float4* wp = reinterpret_cast<const float4*>(ws + (8 * c + e) * kRows);
+            const float4 a = wp[0], bb = wp[1];
+            sc[0] = fmaf(a.x, v, sc[0]); sc[1] = fmaf(a.y, v, sc[1]);
+            sc[2] = fmaf(a.z, v, sc[2]); sc[3] = fmaf(a.w, v, sc[3]);
+            sc[4] = fmaf(bb.x, v, sc[4]); sc[5] = fmaf(bb.y, v, sc[5]);
+            sc[6] = fmaf(bb.z, v, sc[6]); sc[7] = fmaf(bb.w, v, sc[7]);
+          }
+        }
+        if (KMODE == KVC_MODE_CODEBOOK) {
+          const int64_t sw = tok * t.knw;
+          const float n = __half2float(knorm[sw]);
+#pragma unroll
+          for (int g = 0; g < kRows; ++g) sc[g] *= n;
+          if (t.m) {  // + ||r|| sum_j w_j (2 bit_j - 1)
+            const unsigned char* sb = krow + row + t.kcode;
+            float qj[kRows];
+#pragma unroll
+            for (int g = 0; g < kRows; ++g) qj[g] = 0.f;
+            for (int j = 0; j < t.m; ++j) {
+              const float f = (sb[j >> 3] >> (j & 7)) & 1u ? 1.f : -1.f;
+#pragma unroll
+              for (int g = 0; g < kRows; ++g) qj[g] = fmaf(wxs[j * kRows + g], f, qj[g]);
+            }
+            const float gam = __half2float(knorm[sw + 1]);
+#pragma unroll
+            for (int g = 0; g < kRows; ++g) sc[g] = fmaf(gam, qj[g], sc[g]);
+          }
+          if (t.n_out) {  // + s sum_l q[ch_l] o8_l
+            const int8_t* o8 = reinterpret_cast<const int8_t*>(krow + row + t.kcode + (t.m >> 3));
+            float qo[kRows];
+#pragma unroll
+            for (int g = 0; g < kRows; ++g) qo[g] = 0.f;
+            for (int j = 0; j < t.n_out; ++j) {
+              const float v = (float)o8[j];
+#pragma unroll
+              for (int g = 0; g < kRows; ++g) qo[g] = fmaf(wxs[(t.m + j) * kRows + g], v, qo[g]);
+            }
+            const float os = __half2float(knorm[sw + t.knw - 1]);
+#pragma unroll
+            for (int g = 0; g < kRows; ++g) sc[g] = fmaf(os, qo[g], sc[g]);
+          }
+        }
+        if (!VU) sv = __half2float(vscale[tok]);
+      }
+      // visibility, then the online softmax
+      const int64_t draft = tok - t.ctx;
+#pragma unroll
+      for (int g = 0; g < kRows; ++g) {
+        bool see = live && g < nr;
+        if (draft < 0) {
+          see = see && tok >= first;
+        } else if (see) {
+          const int n = (r0 + g) % t.N;
+          see = mask ? mask[(int64_t)n * t.N + draft] != 0 : draft <= n;
+        }
+        const float s = see ? sc[g] + c1s[g] : -INFINITY;
+        const float mn = fmaxf(m[g], warp_max(s));
+        const float ref = mn == -INFINITY ? 0.f : mn;  // nothing visible yet
+        const float corr = exp2f(m[g] - ref);
+        const float pt = see ? exp2f(s - ref) : 0.f;
+        l[g] = l[g] * corr + warp_sum(pt);
+        m[g] = mn;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[g][e] *= corr;
+        ps[lane * kRows + g] = see ? pt * sv : 0.f;
+      }
+      __syncwarp();
+      if (!VU) {
+        // lane owns channels lane, lane + 32, ..
+        for (int tt = 0; tt < nrow; ++tt) {
+          const int8_t* vr = reinterpret_cast<const int8_t*>(vbase + (tb + tt) * (int64_t)Pv) + lane;
+          float pv[kRows];
+#pragma unroll
+          for (int g = 0; g < kRows; ++g) pv[g] = ps[tt * kRows + g];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (lane + 32 * e >= Dv) break;
+            const float v = (float)vr[32 * e];
+#pragma unroll
+            for (int g = 0; g < kRows; ++g) acc[g][e] = fmaf(pv[g], v, acc[g][e]);
+          }
+        }
+      } else if (vc < nchv) {
+        const uint32_t ent = vch[vc];
+        const int w = (int)((ent >> 16) & 0xfu), off = (int)(ent & 0xffffu);
+        for (int tt = tg; tt < nrow; tt += TG) {
+          const uint2 bits = bits_at(vrow, tt * Pv + off);
+          float pv[kRows];
+#pragma unroll
+          for (int g = 0; g < kRows; ++g) pv[g] = ps[tt * kRows + g];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v = (float)((int)chunk_code(bits, w, e) - (1 << (w - 1)));
+#pragma unroll
+            for (int g = 0; g < kRows; ++g) acc[g][e] = fmaf(pv[g], v, acc[g][e]);
+          }
+        }
+      }
+      __syncwarp();  // staging and ps are rewritten by the next block
+    }
+    if (VU)
+      for (int o = LG; o < 32; o <<= 1)
+#pragma unroll
+        for (int g = 0; g < kRows; ++g)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[g][e] += __shfl_xor_sync(kFull, acc[g][e], o);
+    // the warps' states into one partial: [row][m, l, acc[Dv]]
+    for (int e = lane; e < kRows * stride; e += 32) merge[(size_t)warp * kRows * stride + e] = 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int g = 0; g < kRows; ++g) {
+      float* mg = merge + ((size_t)warp * kRows + g) * stride;
+      if (lane == 0) {
+        mg[0] = m[g];
+        mg[1] = l[g];
+      }
+      if (!VU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (lane + 32 * e < Dv) mg[2 + lane + 32 * e] = acc[g][e];
+      } else if (tg == 0 && vc < nchv) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mg[2 + vc * 8 + e] = acc[g][e];
+      }
+    }
+    __syncthreads();
+    float* out = t.part + ((size_t)job + blockIdx.x) * t.rt * stride;
+    for (int e = tid; e < nr * stride; e += kThreads) {
+      const int g = e / stride, d = e - g * stride;
+      float M = -INFINITY;
+      for (int w4 = 0; w4 < 4; ++w4) M = fmaxf(M, merge[((size_t)w4 * kRows + g) * stride]);
+      float v = d == 0 ? M : 0.f;
+      if (d)
+        for (int w4 = 0; w4 < 4; ++w4) {
+          const float* mg = merge + ((size_t)w4 * kRows + g) * stride;
+          // (a warp without tokens has l = 0; one with NaN scores has m = -inf too)
+          if (mg[1] != 0.f) v = fmaf(exp2f(mg[0] - M), mg[d], v);
+        }
+      out[(size_t)g * stride + d] = v;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- combine
+
+// One block per (slot, row): merge the partials of the row's job, normalise and
+// write the output row (uniform values: project the weighted mean latent).
+__global__ void __launch_bounds__(kThreads)
+    tree_combine_kernel(const Params kp, const Params vp, const TreeArgs t) {
+  __shared__ float zb[256];
+  __shared__ int comp[256];
+  const int slot = blockIdx.x / t.rows, row = blockIdx.x - slot * t.rows, tid = threadIdx.x;
+  const int b = slot / kp.H, h = slot - b * kp.H;
+  const int jt = row / t.rt, job = slot * t.row_tiles + jt, rr = row - jt * t.rt;
+  const int stride = 2 + t.Dv;
+  // the CTAs whose runs hold the job's tiles
+  const int64_t lo = job * t.tps, hi = lo + t.tps;
+  int64_t c0 = lo * t.grid / t.total;
+  while (run_begin(t, c0 + 1) <= lo) ++c0;
+  while (run_begin(t, c0) > lo) --c0;
+  int64_t c1 = c0;
+  while (run_begin(t, c1 + 1) < hi) ++c1;
+  const float* part = t.part + (((size_t)job + c0) * t.rt + rr) * stride;
+  const size_t ps = (size_t)t.rt * stride;
+  const int np = (int)(c1 - c0) + 1;
+  float M = -INFINITY;
+  for (int s = 0; s < np; ++s) M = fmaxf(M, part[s * ps]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int s = 0; s < np; ++s) L = fmaf(exp2f(part[s * ps] - ref), part[s * ps + 1], L);
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // nothing visible: zero
+  const bool vu = vp.mode == KVC_MODE_UNIFORM;
+  const int g = row / t.N, n = row - g * t.N;
+  const int64_t o = b * t.o_sb + (int64_t)(h * t.rep + g) * t.o_sh + n * t.o_st;
+  auto put = [&](int i, float v) {
+    if (t.out_bf16) reinterpret_cast<__nv_bfloat16*>(t.out)[o + i] = __float2bfloat16_rn(v);
+    else reinterpret_cast<__half*>(t.out)[o + i] = __float2half_rn(v);
+  };
+  const int beta = vu ? vp.basis_of[slot] : 0;
+  for (int d = tid; d < t.Dv; d += kThreads) {
+    float v = 0.f;
+    for (int s = 0; s < np; ++s) v = fmaf(exp2f(part[s * ps] - ref), part[s * ps + 2 + d], v);
+    v *= inv;
+    if (!vu) {
+      put(d, v);
+      continue;
+    }
+    int width = 0;
+    const int k = position_component(vp, beta, d, &width);
+    comp[d] = k;
+    if (k >= 0) {
+      const size_t bk = (size_t)beta * vp.r + k;
+      zb[d] = fmaf(vp.step[bk], v + (float)(1 << (width - 1)), vp.lo[bk]);  // the mean latent
+    }
+  }
+  if (!vu) return;
+  __syncthreads();
+  for (int i = tid; i < vp.D; i += kThreads) {
+    float v = vp.mean[(size_t)beta * vp.D + i];
+    const float* Vrow = vp.V + ((size_t)beta * vp.D + i) * vp.r;
+    for (int j = 0; j < t.Dv; ++j)
+      if (comp[j] >= 0) v = fmaf(zb[j], Vrow[comp[j]], v);
+    put(i, inv == 0.f ? 0.f : v);
+  }
+}
+
+using MainKernel = void (*)(const Params, const Params, const TreeArgs, int, int);
+
+MainKernel main_kernel_for(int kmode, int vmode) {
+  if (kmode == KVC_MODE_UNIFORM)
+    return vmode == KVC_MODE_UNIFORM ? tree_main_kernel<KVC_MODE_UNIFORM, KVC_MODE_UNIFORM>
+                                     : tree_main_kernel<KVC_MODE_UNIFORM, KVC_MODE_INT8>;
+  return vmode == KVC_MODE_UNIFORM ? tree_main_kernel<KVC_MODE_CODEBOOK, KVC_MODE_UNIFORM>
+                                   : tree_main_kernel<KVC_MODE_CODEBOOK, KVC_MODE_INT8>;
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+size_t w_bytes(const Params& kp, const TreeArgs& t) {
+  return align256((size_t)kp.n_slots * t.rows * t.NCk * 4);
+}
+size_t c1_bytes(const Params& kp, const TreeArgs& t) {
+  return align256((size_t)kp.n_slots * t.rows * 4);
+}
+size_t wx_bytes(const Params& kp, const TreeArgs& t) {
+  return align256((size_t)kp.n_slots * t.rows * (t.m + t.n_out) * 4);
+}
+
+cudaError_t launch_main(const Params& kp, const Params& vp, const TreeArgs& t, cudaStream_t s,
+                        int* nk) {
+  const int kstage = (32 * t.Pk_max + 16 + 15) / 16 * 16;
+  const int vstage = vp.mode == KVC_MODE_UNIFORM ? (32 * t.Pv_max + 16 + 15) / 16 * 16 : 0;
+  const size_t smem = (size_t)kRows * (t.NCk + t.m + t.n_out) * 4 +
+                      4 * (size_t)(kstage + vstage + 32 * kRows * 4) +
+                      4 * (size_t)kRows * (2 + t.Dv) * 4;
+  MainKernel k = main_kernel_for(kp.mode, vp.mode);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  k<<<(unsigned)t.grid, kThreads, smem, s>>>(kp, vp, t, kstage, vstage);
+  ++*nk;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t tree_plan(const Params& kp, TreeArgs& t, int sms) {
+  t.rt = kRows;
+  t.row_tiles = (t.rows + t.rt - 1) / t.rt;
+  const int64_t jobs = (int64_t)kp.n_slots * t.row_tiles;
+  t.tps = (t.S + kTreeTile - 1) / kTreeTile;
+  t.total = jobs * t.tps;
+  t.grid = (int)std::min<int64_t>(t.total, 12 * (int64_t)sms);
+  const size_t part = (size_t)(jobs + t.grid - 1) * t.rt * (2 + t.Dv) * 4;
+  return w_bytes(kp, t) + c1_bytes(kp, t) + wx_bytes(kp, t) + align256(part);
+}
+
+cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, void* workspace,
+                               cudaStream_t s, int* nk) {
+  auto* ws = static_cast<unsigned char*>(workspace);
+  t.w = reinterpret_cast<float*>(ws);
+  ws += w_bytes(kp, t);
+  t.c1 = reinterpret_cast<float*>(ws);
+  ws += c1_bytes(kp, t);
+  t.wx = reinterpret_cast<float*>(ws);
+  ws += wx_bytes(kp, t);
+  t.part = reinterpret_cast<float*>(ws);
+  tree_prep_kernel<<<(unsigned)kp.n_slots * ((t.rows + kPrepRows - 1) / kPrepRows), kThreads, 0,
+                     s>>>(kp, t);
+  ++*nk;
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_main(kp, vp, t, s, nk);
+  if (e != cudaSuccess) return e;
+  tree_combine_kernel<<<(unsigned)kp.n_slots * t.rows, kThreads, 0, s>>>(kp, vp, t);
+  ++*nk;
+  return cudaGetLastError();
+}
+
+}  // namespace kvc

@@ -17,7 +17,7 @@ constexpr int kMaxRank = 1024;
 constexpr int kMaxGroupSize = 32;
 
 // Device error codes written to Params::err (first writer wins).
-enum : int { kErrNone = 0, kErrTimeout = 1, kErrRange = 2 };
+enum : int { kErrNone = 0, kErrTimeout = 1, kErrRange = 2, kErrIndex = 3 };
 
 // Frozen per-layer parameters in kernel layouts.  Every pointer is device
 // memory inside the layer's parameter block.  Passed by value to kernels.
@@ -117,6 +117,61 @@ size_t attend_plan(int B, int Hq, int n_slots, int rep, int64_t S, int NCk, int 
                    int extra, int* splits, int64_t* span);
 cudaError_t launch_attend(const Params& kp, const Params& vp, AttendArgs a, void* workspace,
                           cudaStream_t s, int* nk);
+
+// Attention of drafted tokens over the cache (kvc_attend_tree.cu).  A slot has
+// rep * N query rows, row i being query head h * rep + i / N of drafted token
+// i % N.  They are cut into jobs of at most `rt` rows; a job walks its slot's
+// stored tokens in tiles of 128.  The tiles of all jobs are one line that is
+// cut into equal runs, one per CTA, so a CTA holds the ends of some jobs; each
+// (job, CTA) pair leaves one partial, number job + CTA (both only ever grow
+// along the line, so the number is unique).
+constexpr int kTreeTile = 128;
+struct TreeArgs {
+  const void* q = nullptr;
+  int q_dtype = 0;
+  int64_t q_sb = 0, q_sh = 0, q_st = 0;  // element strides of batch, head, token
+  const uint8_t* mask = nullptr;         // [N][N] bytes per batch entry; null: causal
+  int64_t mask_sb = 0;                   // bytes between batch entries (0: shared)
+  const int32_t* first = nullptr;        // [B] first visible token (null: 0)
+  void* out = nullptr;
+  int out_bf16 = 0;
+  int64_t o_sb = 0, o_sh = 0, o_st = 0;
+  int Hq = 0, rep = 0, N = 0;
+  float scale_log2 = 0.f;                // score scale times log2(e)
+  int64_t S = 0, ctx = 0;                // stored tokens; those before the drafts
+  int rows = 0, rt = 0, row_tiles = 0;   // rows of a slot, of a job; jobs of a slot
+  int64_t tps = 0, total = 0;            // tiles of a job, of the line
+  int grid = 0;                          // CTAs
+  int NCk = 0, Dv = 0;                   // as in AttendArgs
+  int Pk_max = 0, Pv_max = 0;
+  int prod = 0, m = 0, n_out = 0, kcode = 0, knw = 1;
+  float* w = nullptr;                    // workspace: [n_slots rows][NCk] key weights
+  float* c1 = nullptr;                   // workspace: [n_slots rows] score offsets
+  float* wx = nullptr;                   // workspace: [n_slots rows][m + n_out]
+  float* part = nullptr;                 // workspace: [jobs + grid - 1][rt][2 + Dv]
+};
+// Fill the job fields of t (rows, jobs, tiles, CTAs); the workspace bytes.
+size_t tree_plan(const Params& kp, TreeArgs& t, int sms);
+cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, void* workspace,
+                               cudaStream_t s, int* nk);
+
+// Stored rows moved between and inside layers (kvc_rows.cu).
+struct GatherArgs {
+  const int32_t* parent = nullptr;  // [B] source batch entries (null: the same)
+  const int32_t* index = nullptr;   // [B][n] source rows (null: src_row0 ..)
+  int64_t n = 0;                    // rows appended
+  int64_t dst_row0 = 0, src_row0 = 0, src_len = 0;
+};
+struct AcceptArgs {
+  const int32_t* index = nullptr;  // [B][n] rows kept, from the first of the last N
+  int64_t n = 0, N = 0, base = 0;
+  int cw = 0, pay_chunks = 0;      // row bytes per block; blocks over the packed row
+};
+cudaError_t launch_gather(const Params& dp, const Params& sp, const GatherArgs& a, int pmax,
+                          int sms, cudaStream_t s, int* nk);
+// Row bytes that one accept block stages for n rows, 0 when n is too large.
+int accept_columns_per_block(int64_t n, int widest);
+cudaError_t launch_accept(const Params& p, AcceptArgs a, int pmax, cudaStream_t s, int* nk);
 
 // On-device prefill fit of the uniform mode (kvc_fit.cu).  Every pointer is
 // device memory; the float64 scratch lives in the caller's workspace.
