@@ -8,6 +8,8 @@
 #include <string>
 #include <vector>
 
+#include <cuda_fp16.h>
+
 #include "kvc_internal.h"
 #include "kvc_tc.h"
 
@@ -34,6 +36,7 @@ struct kvc_layer {
   std::vector<int64_t> pay_host, side_host;
   std::vector<int32_t> seg_host;     // [nb][kMaxSeg][4] width segments
   std::vector<int32_t> channels_host;  // [n_slots][n_out] outlier channels
+  float cb_mul = 1.f;                // scale at which the centroids fall nearest to fp16 values
   uint64_t format[2] = {0, 0};       // hash of everything a stored row decodes by
   kvc::TcPlan tc{};                  // tensor-core path tables (kvc_tc.cu)
 };
@@ -516,6 +519,39 @@ kvc_status kvc_init_layer_prod(const kvc_layer_desc* d, const kvc_prod_desc* pro
   return init_from_geo(d, g, out);
 }
 
+// The scale m for which the fp16 values nearest to m c_j lie closest to them
+// (least sum of squares over the levels, relative to m): a kernel that
+// multiplies the centroids in fp16 takes m c and divides its other factor by m.
+// 4096 steps over a factor of two bring eight levels within about a seventh of
+// fp16's half step; the largest level is put in [16, 32), far from both ends of
+// fp16's range.
+static float centroid_scale(const float* c, int n) {
+  float big = 0.f;
+  for (int j = 0; j < n; ++j) big = std::max(big, std::fabs(c[j]));
+  if (!(big > 0.f)) return 1.f;
+  int e;
+  std::frexp(big, &e);  // big in [2^(e-1), 2^e)
+  const float base = std::ldexp(1.f, 5 - e);
+  float best = base;
+  double least = INFINITY;
+  const int steps = 4096 * 8 / std::max(n, 8);  // the same work for every codebook
+  for (int i = 0; i < steps; ++i) {
+    const float m = base * (0.5f + 0.5f * (float)i / (float)steps);
+    double s = 0.0;
+    for (int j = 0; j < n; ++j) {
+      const float v = m * c[j];
+      const double d = (double)__half2float(__float2half_rn(v)) - (double)v;
+      s += d * d;
+    }
+    s /= (double)m * m;
+    if (s < least) {
+      least = s;
+      best = m;
+    }
+  }
+  return best;
+}
+
 // Hash of everything that a stored row decodes by, but its basis number and
 // outlier channels (which belong to a slot): two layers with equal hashes read
 // each other's rows.  Two independent 64-bit multiplicative hashes.
@@ -626,6 +662,7 @@ static kvc_status init_from_geo(const kvc_layer_desc* d, Geo& g, kvc_layer** out
   L->side_host = g.side_off;
   L->channels_host = g.channels;
   format_hash(d, g, L->format);
+  if (g.cb_levels) L->cb_mul = centroid_scale(d->codebook, g.cb_levels);
   *out = L;
   return succeed();
 }
@@ -880,6 +917,9 @@ static kvc_status tree_check(const kvc_layer* K, const kvc_layer* V, int32_t Hq,
   }
   DeviceGuard dg(K->device);
   if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
+  if (K->path == KVC_PATH_AUTO) t.tc = kvc::tree_tc_rows(K->p, V->p, t);
+  t.cb_mul = K->cb_mul;
+  t.w_mul = 1.f / K->cb_mul;
   *ws_bytes = kvc::tree_plan(K->p, t, kvc::sm_count());
   return KVC_OK;
 }

@@ -545,12 +545,13 @@ cudaError_t launch_main(const Params& kp, const Params& vp, const TreeArgs& t, c
 }  // namespace
 
 size_t tree_plan(const Params& kp, TreeArgs& t, int sms) {
-  t.rt = kRows;
+  t.rt = t.tc ? t.tc : kRows;
   t.row_tiles = (t.rows + t.rt - 1) / t.rt;
   const int64_t jobs = (int64_t)kp.n_slots * t.row_tiles;
   t.tps = (t.S + kTreeTile - 1) / kTreeTile;
   t.total = jobs * t.tps;
-  t.grid = (int)std::min<int64_t>(t.total, 12 * (int64_t)sms);
+  // one CTA per SM on the tensor cores, else about twelve
+  t.grid = (int)std::min<int64_t>(t.total, (t.tc ? 1 : 12) * (int64_t)sms);
   const size_t part = (size_t)(jobs + t.grid - 1) * t.rt * (2 + t.Dv) * 4;
   return w_bytes(kp, t) + c1_bytes(kp, t) + wx_bytes(kp, t) + align256(part);
 }
@@ -570,7 +571,11 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
   ++*nk;
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_main(kp, vp, t, s, nk);
+  if (t.tc) {
+    e = launch_tree_tc(kp, vp, t, s, nk);
+  } else {
+    e = launch_main(kp, vp, t, s, nk);
+  }
   if (e != cudaSuccess) return e;
   tree_combine_kernel<<<(unsigned)kp.n_slots * t.rows, kThreads, 0, s>>>(kp, vp, t);
   ++*nk;

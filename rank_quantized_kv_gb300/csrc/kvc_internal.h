@@ -145,11 +145,18 @@ struct TreeArgs {
   int NCk = 0, Dv = 0;                   // as in AttendArgs
   int Pk_max = 0, Pv_max = 0;
   int prod = 0, m = 0, n_out = 0, kcode = 0, knw = 1;
+  int tc = 0;                            // tensor-core kernel: its columns (rows of a job), 0: CUDA cores
+  float cb_mul = 1.f, w_mul = 1.f;       // tensor cores: scale of the centroids, its inverse
   float* w = nullptr;                    // workspace: [n_slots rows][NCk] key weights
   float* c1 = nullptr;                   // workspace: [n_slots rows] score offsets
   float* wx = nullptr;                   // workspace: [n_slots rows][m + n_out]
   float* part = nullptr;                 // workspace: [jobs + grid - 1][rt][2 + Dv]
 };
+// Rows of a tensor-core job for these layers (kvc_attend_tree_tc.cu), 0 where
+// that kernel does not take them; its launcher.
+int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t);
+cudaError_t launch_tree_tc(const Params& kp, const Params& vp, const TreeArgs& t, cudaStream_t s,
+                           int* nk);
 // Fill the job fields of t (rows, jobs, tiles, CTAs); the workspace bytes.
 size_t tree_plan(const Params& kp, TreeArgs& t, int sms);
 cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, void* workspace,

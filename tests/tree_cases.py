@@ -42,7 +42,9 @@ def make_layers(kvc, kmode, vmode, B, H, D, S, seed, out="f16", bits=3, capacity
     if kmode == "uniform":
         pk = fit_uniform(xk.double().numpy(), min(max(S, 2), 256), min(32, D), [0, 1, 2, 3, 4, 8], D + D // 4)
     else:
-        pk = fit_codebook(D, 2 if kmode == "prod" else bits)
+        pk = fit_codebook(D, 2 if kmode == "prod" else min(bits, 4))
+        if bits == 8 and kmode != "prod":  # 256 levels: evenly spaced will do
+            pk["codebook"] = (np.linspace(-4, 4, 256) / math.sqrt(D)).astype(np.float32)
     if kmode == "prod":
         rng = np.random.default_rng(seed)
         kx = dict(sketch=rng.standard_normal((48, D)).astype(np.float32), split_from=5,
