@@ -18,10 +18,12 @@
 //            zero for a row that sees no token.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_pipeline.h>
 
 #include <algorithm>
 
 #include "kvc_internal.h"
+#include "kvc_launch.cuh"
 
 namespace kvc {
 
@@ -29,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 128;      // 4 warps
 constexpr int kRows = 8;           // rows of a job
-constexpr int kPrepRows = 16;      // rows of a prep block
+constexpr int kPrepRows = 32, kPrepThreads = 256;  // rows and threads of a prep block
 constexpr unsigned kFull = 0xffffffffu;
 
 // Packed position j of basis beta: component (-1: padding) and width.
@@ -94,95 +96,126 @@ __device__ __forceinline__ float load_q(const TreeArgs& t, int64_t i) {
 
 // ---------------------------------------------------------------- prep
 
-// One block per (slot, 16 rows): the key weights at every packed position,
-// w_j = scale log2(e) u_j coef_j (coef = step in uniform mode, 1 for a
-// codebook), and c1.  Thread j holds one position of all the block's rows, so
-// V is read once per 16 rows.
-__global__ void __launch_bounds__(kThreads) tree_prep_kernel(const Params kp, const TreeArgs t) {
-  __shared__ __align__(16) float qs[256][kPrepRows];
-  __shared__ float red[kPrepRows][kThreads / 32];
+// The key weights at every packed position, w_j = scale log2(e) u_j coef_j
+// (coef = step in uniform mode, 1 for a codebook), and c1.  One block per (slot,
+// 32 rows): u = q V as a register-tiled product, 8 rows x 2 columns a thread,
+// over 128 columns at a time; q stays in shared memory, V passes through it 32
+// rows at a time.  Bound: fp32 FMA (rows D r of them) for wide trees, else the
+// latency of one pass.
+constexpr int kPrepCols = 128, kPrepK = 32;
+
+__global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp, const TreeArgs t) {
+  extern __shared__ __align__(16) float sm_f[];
+  const int D = kp.D, r = kp.r, tid = threadIdx.x;
   const int blocks = (t.rows + kPrepRows - 1) / kPrepRows;
   const int slot = blockIdx.x / blocks, r0 = (blockIdx.x - slot * blocks) * kPrepRows;
   const int b = slot / kp.H, h = slot - b * kp.H;
   const int beta = kp.basis_of[slot];
-  const int D = kp.D, tid = threadIdx.x;
   const int nr = min(kPrepRows, t.rows - r0);
-  for (int e = tid; e < kPrepRows * D; e += kThreads) {
-    const int r = e / D, i = e - r * D;
+  float* qs = sm_f;                            // [D][32] rows of q, transposed
+  float* vs = qs + D * kPrepRows;              // [2][32][128] rows of V
+  float* us = vs + 2 * kPrepK * kPrepCols;     // [32][r] products
+  grid_dependents_launch();
+  const float* V = kp.V + (size_t)beta * D * r;
+  const int stages = (D + kPrepK - 1) / kPrepK;
+  // row k0 + i of V, columns c0 ..: one 4-byte asynchronous copy per element
+  // (a row of V starts at any multiple of 4 bytes)
+  auto load_v = [&](int st, int c0, int buf) {
+    for (int e = tid; e < kPrepK * kPrepCols; e += kPrepThreads) {
+      const int i = e / kPrepCols, c = e - i * kPrepCols, k = st * kPrepK + i;
+      float* dst = vs + buf * kPrepK * kPrepCols + e;
+      if (k < D && c0 + c < r) __pipeline_memcpy_async(dst, V + (size_t)k * r + c0 + c, 4);
+      else *dst = 0.f;
+    }
+    __pipeline_commit();
+  };
+  load_v(0, 0, 0);
+  for (int e = tid; e < kPrepRows * D; e += kPrepThreads) {
+    const int row = e / D, i = e - row * D;
     float v = 0.f;
-    if (r < nr) {
-      const int row = r0 + r, g = row / t.N, n = row - g * t.N;
+    if (row < nr) {
+      const int x = r0 + row, g = x / t.N, n = x - g * t.N;
       v = load_q(t, b * t.q_sb + (int64_t)(h * t.rep + g) * t.q_sh + n * t.q_st + i);
     }
-    qs[i][r] = v;
+    qs[i * kPrepRows + row] = v;
+  }
+  const int ty = tid >> 6, tx = tid & 63;  // 4 row groups of 8, 64 column pairs
+  for (int c0 = 0; c0 < r; c0 += kPrepCols) {
+    float2 acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = make_float2(0.f, 0.f);
+    if (c0) load_v(0, c0, 0);
+    for (int st = 0; st < stages; ++st) {
+      if (st + 1 < stages) load_v(st + 1, c0, (st + 1) & 1);
+      __pipeline_wait_prior(st + 1 < stages ? 1 : 0);
+      __syncthreads();
+      const float* vb = vs + (st & 1) * kPrepK * kPrepCols + 2 * tx;
+      const float* qb = qs + st * kPrepK * kPrepRows + 8 * ty;
+      const int kn = min(kPrepK, D - st * kPrepK);
+#pragma unroll 8
+      for (int k = 0; k < kn; ++k) {
+        const float2 v = *reinterpret_cast<const float2*>(vb + k * kPrepCols);
+        const float4 q0 = *reinterpret_cast<const float4*>(qb + k * kPrepRows);
+        const float4 q1 = *reinterpret_cast<const float4*>(qb + k * kPrepRows + 4);
+        const float q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = __ffma2_rn(make_float2(q[e], q[e]), v, acc[e]);
+      }
+      __syncthreads();  // the other buffer is refilled next
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = c0 + 2 * tx;
+      if (c < r) us[(8 * ty + e) * r + c] = acc[e].x;
+      if (c + 1 < r) us[(8 * ty + e) * r + c + 1] = acc[e].y;
+    }
   }
   __syncthreads();
   const bool uniform = kp.mode == KVC_MODE_UNIFORM;
-  float c1[kPrepRows];
-#pragma unroll
-  for (int r = 0; r < kPrepRows; ++r) c1[r] = 0.f;
   const size_t row0 = (size_t)slot * t.rows + r0;
-  auto dot = [&](const float* col, int stride, float (&s)[kPrepRows]) {
-#pragma unroll
-    for (int r = 0; r < kPrepRows; ++r) s[r] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < D; ++i) {
-      const float v = col[(size_t)i * stride];
-#pragma unroll
-      for (int r = 0; r < kPrepRows; ++r) s[r] = fmaf(qs[i][r], v, s[r]);
-    }
-  };
-  for (int j = tid; j < t.NCk; j += kThreads) {
+  for (int j = tid; j < t.NCk; j += kPrepThreads) {  // this thread's positions of all rows
     int width = 0;
     const int k = position_component(kp, beta, j, &width);
-    float u[kPrepRows];
-    float coef = 0.f, off = 0.f;
-    if (k >= 0) {
-      const size_t bk = (size_t)beta * kp.r + k;
-      dot(kp.V + (size_t)beta * D * kp.r + k, kp.r, u);
-      coef = uniform ? kp.step[bk] : 1.f;
-      if (uniform) off = fmaf((float)(1 << (width - 1)), kp.step[bk], kp.lo[bk]);
-    }
-#pragma unroll
-    for (int r = 0; r < kPrepRows; ++r) {
-      if (r >= nr) break;
-      t.w[(row0 + r) * t.NCk + j] = k >= 0 ? t.scale_log2 * u[r] * coef : 0.f;
-      if (k >= 0) c1[r] = fmaf(u[r], off, c1[r]);
-    }
+    const float f = k < 0 ? 0.f : t.scale_log2 * (uniform ? kp.step[(size_t)beta * r + k] : 1.f);
+    for (int row = 0; row < nr; ++row) t.w[(row0 + row) * t.NCk + j] = k < 0 ? 0.f : f * us[row * r + k];
   }
-  if (t.prod) {  // sketch weights sqrt(pi/2)/m (S q)_j, outlier weights q[ch_l]
-    const int nx = t.m + t.n_out;
-    const float coef = t.m ? 1.2533141373155003f / (float)t.m : 0.f;
-    for (int j = tid; j < nx; j += kThreads) {
-      float u[kPrepRows];
-      if (j < t.m) {
-        dot(kp.W3 + (size_t)(D + j) * D, 1, u);
-      } else {
-        const int ch = kp.channels[(size_t)slot * t.n_out + j - t.m];
-#pragma unroll
-        for (int r = 0; r < kPrepRows; ++r) u[r] = qs[ch][r];
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int row = warp; row < nr; row += kPrepThreads / 32) {  // c1, a warp a row
+    float c1 = 0.f;
+    if (uniform) {
+      for (int k = lane; k < r; k += 32) {
+        const size_t bk = (size_t)beta * r + k;
+        const int width = kp.bits[bk];
+        if (width) c1 = fmaf(us[row * r + k], fmaf((float)(1 << (width - 1)), kp.step[bk], kp.lo[bk]), c1);
       }
-#pragma unroll
-      for (int r = 0; r < kPrepRows; ++r)
-        if (r < nr) t.wx[(row0 + r) * nx + j] = t.scale_log2 * (j < t.m ? coef : 1.f) * u[r];
+      for (int i = lane; i < D; i += 32) c1 = fmaf(qs[i * kPrepRows + row], kp.mean[(size_t)beta * D + i], c1);
     }
+    c1 = warp_sum(c1);
+    if (lane == 0) t.c1[row0 + row] = t.scale_log2 * c1;
   }
-  if (uniform)
-    for (int i = tid; i < D; i += kThreads) {
-      const float v = kp.mean[(size_t)beta * D + i];
-#pragma unroll
-      for (int r = 0; r < kPrepRows; ++r) c1[r] = fmaf(qs[i][r], v, c1[r]);
-    }
-#pragma unroll
-  for (int r = 0; r < kPrepRows; ++r) {
-    const float s = warp_sum(c1[r]);
-    if ((tid & 31) == 0) red[r][tid >> 5] = s;
-  }
+}
+
+// Keys with a residual sketch or an outlier stream: the sketch weights
+// sqrt(pi/2)/m (S q)_j and the outlier weights q[ch_l], one block per row.
+__global__ void __launch_bounds__(kThreads) tree_prep_prod_kernel(const Params kp, const TreeArgs t) {
+  __shared__ float qs[kProdMaxD];
+  const int slot = blockIdx.x / t.rows, row = blockIdx.x - slot * t.rows;
+  const int b = slot / kp.H, h = slot - b * kp.H, g = row / t.N, n = row - g * t.N;
+  const int D = kp.D, nx = t.m + t.n_out;
+  for (int i = threadIdx.x; i < D; i += kThreads)
+    qs[i] = load_q(t, b * t.q_sb + (int64_t)(h * t.rep + g) * t.q_sh + n * t.q_st + i);
   __syncthreads();
-  if (tid < nr) {
-    float s = 0.f;
-    for (int i = 0; i < kThreads / 32; ++i) s += red[tid][i];
-    t.c1[row0 + tid] = t.scale_log2 * s;
+  const float coef = t.m ? 1.2533141373155003f / (float)t.m : 0.f;
+  for (int j = threadIdx.x; j < nx; j += kThreads) {
+    float u = 0.f;
+    if (j < t.m) {
+      const float* s = kp.W3 + (size_t)(D + j) * D;
+      for (int i = 0; i < D; ++i) u = fmaf(s[i], qs[i], u);
+      u *= coef;
+    } else {
+      u = qs[kp.channels[(size_t)slot * t.n_out + j - t.m]];
+    }
+    t.wx[(size_t)blockIdx.x * nx + j] = t.scale_log2 * u;
   }
 }
 
@@ -218,6 +251,7 @@ __global__ void __launch_bounds__(kThreads)
   if (KMODE == KVC_MODE_CODEBOOK)
     for (int j = tid; j < kp.cb_levels; j += kThreads) cbv[j] = kp.codebook[j];
 
+  grid_dependency_wait();  // the key weights come from the launch before
   const int64_t run1 = run_begin(t, blockIdx.x + 1);
   for (int64_t at = run_begin(t, blockIdx.x); at < run1;) {
     const int job = (int)(at / t.tps);
@@ -425,7 +459,7 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     __syncthreads();
-    float* out = t.part + ((size_t)job + blockIdx.x) * t.rt * stride;
+    const size_t prow = ((size_t)job + blockIdx.x) * t.rt;
     for (int e = tid; e < nr * stride; e += kThreads) {
       const int g = e / stride, d = e - g * stride;
       float M = -INFINITY;
@@ -437,23 +471,46 @@ __global__ void __launch_bounds__(kThreads)
           // (a warp without tokens has l = 0; one with NaN scores has m = -inf too)
           if (mg[1] != 0.f) v = fmaf(exp2f(mg[0] - M), mg[d], v);
         }
-      out[(size_t)g * stride + d] = v;
+      if (d == 0) t.ml[prow + g].x = v;
+      else if (d == 1) t.ml[prow + g].y = v;
+      else t.part[(prow + g) * t.Dvp + d - 2] = v;
     }
   }
 }
 
 // ---------------------------------------------------------------- combine
 
-// One block per (slot, row): merge the partials of the row's job, normalise and
-// write the output row (uniform values: project the weighted mean latent).
-__global__ void __launch_bounds__(kThreads)
+constexpr int kCombineWarps = 8;
+
+// One warp per row, eight rows of a slot per block: merge the partials of the
+// row's job, normalise and write the output row (uniform values: project the
+// weighted mean latent).  Lane l holds four consecutive sums from 4 l, and the
+// four of the next 128.
+__global__ void __launch_bounds__(kCombineWarps * 32)
     tree_combine_kernel(const Params kp, const Params vp, const TreeArgs t) {
-  __shared__ float zb[256];
-  __shared__ int comp[256];
-  const int slot = blockIdx.x / t.rows, row = blockIdx.x - slot * t.rows, tid = threadIdx.x;
+  __shared__ float zb[kCombineWarps][256];
+  __shared__ short comp[256];       // uniform values: component of a packed position
+  __shared__ float zs[256], zo[256];  // its step, and its offset lo + 2^(b-1) step
+  const int blocks = (t.rows + kCombineWarps - 1) / kCombineWarps;
+  const int slot = blockIdx.x / blocks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = (blockIdx.x - slot * blocks) * kCombineWarps + warp;
   const int b = slot / kp.H, h = slot - b * kp.H;
+  const bool vu = vp.mode == KVC_MODE_UNIFORM;
+  const int beta = vu ? vp.basis_of[slot] : 0;
+  if (vu) {
+    for (int j = threadIdx.x; j < t.Dv; j += kCombineWarps * 32) {
+      int width = 0;
+      const int k = position_component(vp, beta, j, &width);
+      const size_t bk = (size_t)beta * vp.r + (k < 0 ? 0 : k);
+      comp[j] = (short)k;
+      zs[j] = vp.step[bk];
+      zo[j] = k < 0 ? 0.f : fmaf((float)(1 << (width - 1)), vp.step[bk], vp.lo[bk]);
+    }
+    __syncthreads();
+  }
+  grid_dependency_wait();
+  if (row >= t.rows) return;
   const int jt = row / t.rt, job = slot * t.row_tiles + jt, rr = row - jt * t.rt;
-  const int stride = 2 + t.Dv;
   // the CTAs whose runs hold the job's tiles
   const int64_t lo = job * t.tps, hi = lo + t.tps;
   int64_t c0 = lo * t.grid / t.total;
@@ -461,47 +518,106 @@ __global__ void __launch_bounds__(kThreads)
   while (run_begin(t, c0) > lo) --c0;
   int64_t c1 = c0;
   while (run_begin(t, c1 + 1) < hi) ++c1;
-  const float* part = t.part + (((size_t)job + c0) * t.rt + rr) * stride;
-  const size_t ps = (size_t)t.rt * stride;
   const int np = (int)(c1 - c0) + 1;
+  const float2* ml = t.ml + ((size_t)job + c0) * t.rt + rr;
+  const float* part = t.part + (((size_t)job + c0) * t.rt + rr) * t.Dvp;
+  // lanes take the partials' references and sums, 32 at a time
   float M = -INFINITY;
-  for (int s = 0; s < np; ++s) M = fmaxf(M, part[s * ps]);
+  for (int s = lane; s < np; s += 32) M = fmaxf(M, ml[(size_t)s * t.rt].x);
+  M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  for (int s = 0; s < np; ++s) L = fmaf(exp2f(part[s * ps] - ref), part[s * ps + 1], L);
-  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // nothing visible: zero
-  const bool vu = vp.mode == KVC_MODE_UNIFORM;
-  const int g = row / t.N, n = row - g * t.N;
-  const int64_t o = b * t.o_sb + (int64_t)(h * t.rep + g) * t.o_sh + n * t.o_st;
-  auto put = [&](int i, float v) {
-    if (t.out_bf16) reinterpret_cast<__nv_bfloat16*>(t.out)[o + i] = __float2bfloat16_rn(v);
-    else reinterpret_cast<__half*>(t.out)[o + i] = __float2half_rn(v);
-  };
-  const int beta = vu ? vp.basis_of[slot] : 0;
-  for (int d = tid; d < t.Dv; d += kThreads) {
-    float v = 0.f;
-    for (int s = 0; s < np; ++s) v = fmaf(exp2f(part[s * ps] - ref), part[s * ps + 2 + d], v);
-    v *= inv;
-    if (!vu) {
-      put(d, v);
-      continue;
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int s0 = 0; s0 < np; s0 += 32) {
+    const int s = s0 + lane;
+    float f = 0.f;
+    if (s < np) {
+      const float2 v = ml[(size_t)s * t.rt];
+      f = exp2f(v.x - ref);
+      // a run that saw nothing has l = 0 (and weighted sums of 0)
+      if (v.y == 0.f) f = 0.f;
+      else L = fmaf(f, v.y, L);
     }
-    int width = 0;
-    const int k = position_component(vp, beta, d, &width);
-    comp[d] = k;
-    if (k >= 0) {
-      const size_t bk = (size_t)beta * vp.r + k;
-      zb[d] = fmaf(vp.step[bk], v + (float)(1 << (width - 1)), vp.lo[bk]);  // the mean latent
+    const int n = min(32, np - s0);
+#pragma unroll 4
+    for (int e = 0; e < n; ++e) {
+      const float fe = __shfl_sync(kFull, f, e);
+      const float* p = part + (size_t)(s0 + e) * t.rt * t.Dvp;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int d = 4 * lane + 128 * u;
+        if (d < t.Dvp) {
+          const float4 v = *reinterpret_cast<const float4*>(p + d);
+          acc[u].x = fmaf(fe, v.x, acc[u].x);
+          acc[u].y = fmaf(fe, v.y, acc[u].y);
+          acc[u].z = fmaf(fe, v.z, acc[u].z);
+          acc[u].w = fmaf(fe, v.w, acc[u].w);
+        }
+      }
     }
   }
-  if (!vu) return;
-  __syncthreads();
-  for (int i = tid; i < vp.D; i += kThreads) {
-    float v = vp.mean[(size_t)beta * vp.D + i];
-    const float* Vrow = vp.V + ((size_t)beta * vp.D + i) * vp.r;
-    for (int j = 0; j < t.Dv; ++j)
-      if (comp[j] >= 0) v = fmaf(zb[j], Vrow[comp[j]], v);
-    put(i, inv == 0.f ? 0.f : v);
+  L = warp_sum(L);
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // nothing visible: zero
+  const int g = row / t.N, n = row - g * t.N;
+  const int64_t o = b * t.o_sb + (int64_t)(h * t.rep + g) * t.o_sh + n * t.o_st;
+  auto put = [&](int d, float4 v) {  // four consecutive values
+    if (t.out_bf16) {
+      __nv_bfloat16 r[4] = {__float2bfloat16_rn(v.x), __float2bfloat16_rn(v.y), __float2bfloat16_rn(v.z),
+                            __float2bfloat16_rn(v.w)};
+      auto* out = reinterpret_cast<__nv_bfloat16*>(t.out) + o + d;
+      if (t.o_vec) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(r);
+      else
+        for (int e = 0; e < 4 && d + e < vp.D; ++e) out[e] = r[e];
+    } else {
+      __half r[4] = {__float2half_rn(v.x), __float2half_rn(v.y), __float2half_rn(v.z), __float2half_rn(v.w)};
+      auto* out = reinterpret_cast<__half*>(t.out) + o + d;
+      if (t.o_vec) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(r);
+      else
+        for (int e = 0; e < 4 && d + e < vp.D; ++e) out[e] = r[e];
+    }
+  };
+  if (!vu) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int d = 4 * lane + 128 * u;
+      if (d < vp.D)
+        put(d, make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv));
+    }
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float v[4] = {acc[u].x, acc[u].y, acc[u].z, acc[u].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = 4 * lane + 128 * u + e;
+      if (d < t.Dv) zb[warp][d] = fmaf(zs[d], v[e] * inv, zo[d]);  // the mean latent
+    }
+  }
+  __syncwarp();
+  for (int i = 4 * lane; i < vp.D; i += 128) {
+    const float* mu = vp.mean + (size_t)beta * vp.D;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = i + e < vp.D ? mu[i + e] : 0.f;
+#pragma unroll 4
+    for (int j = 0; j < t.Dv; ++j) {
+      const int k = comp[j];
+      if (k < 0) continue;
+      const float zj = zb[warp][j];
+      const float* col = vp.Vt + ((size_t)beta * vp.r + k) * vp.D + i;
+      if ((vp.D & 3) == 0) {
+        const float4 c = *reinterpret_cast<const float4*>(col);
+        v[0] = fmaf(zj, c.x, v[0]);
+        v[1] = fmaf(zj, c.y, v[1]);
+        v[2] = fmaf(zj, c.z, v[2]);
+        v[3] = fmaf(zj, c.w, v[3]);
+      } else {
+        for (int e = 0; e < 4 && i + e < vp.D; ++e) v[e] = fmaf(zj, col[e], v[e]);
+      }
+    }
+    if (inv == 0.f) v[0] = v[1] = v[2] = v[3] = 0.f;
+    put(i, make_float4(v[0], v[1], v[2], v[3]));
   }
 }
 
@@ -523,6 +639,9 @@ size_t w_bytes(const Params& kp, const TreeArgs& t) {
 size_t c1_bytes(const Params& kp, const TreeArgs& t) {
   return align256((size_t)kp.n_slots * t.rows * 4);
 }
+size_t ml_bytes(int64_t jobs, const TreeArgs& t) {
+  return align256((size_t)(jobs + t.grid - 1) * t.rt * 8);
+}
 size_t wx_bytes(const Params& kp, const TreeArgs& t) {
   return align256((size_t)kp.n_slots * t.rows * (t.m + t.n_out) * 4);
 }
@@ -537,9 +656,8 @@ cudaError_t launch_main(const Params& kp, const Params& vp, const TreeArgs& t, c
   MainKernel k = main_kernel_for(kp.mode, vp.mode);
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k<<<(unsigned)t.grid, kThreads, smem, s>>>(kp, vp, t, kstage, vstage);
   ++*nk;
-  return cudaGetLastError();
+  return launch_dependent(k, (unsigned)t.grid, kThreads, smem, s, kp, vp, t, kstage, vstage);
 }
 
 }  // namespace
@@ -552,8 +670,9 @@ size_t tree_plan(const Params& kp, TreeArgs& t, int sms) {
   t.total = jobs * t.tps;
   // one CTA per SM on the tensor cores, else about twelve
   t.grid = (int)std::min<int64_t>(t.total, (t.tc ? 1 : 12) * (int64_t)sms);
-  const size_t part = (size_t)(jobs + t.grid - 1) * t.rt * (2 + t.Dv) * 4;
-  return w_bytes(kp, t) + c1_bytes(kp, t) + wx_bytes(kp, t) + align256(part);
+  t.Dvp = (t.Dv + 3) / 4 * 4;
+  return w_bytes(kp, t) + c1_bytes(kp, t) + wx_bytes(kp, t) + ml_bytes(jobs, t) +
+         align256((size_t)(jobs + t.grid - 1) * t.rt * t.Dvp * 4);
 }
 
 cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, void* workspace,
@@ -565,21 +684,31 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
   ws += c1_bytes(kp, t);
   t.wx = reinterpret_cast<float*>(ws);
   ws += wx_bytes(kp, t);
+  t.ml = reinterpret_cast<float2*>(ws);
+  ws += ml_bytes((int64_t)kp.n_slots * t.row_tiles, t);
   t.part = reinterpret_cast<float*>(ws);
-  tree_prep_kernel<<<(unsigned)kp.n_slots * ((t.rows + kPrepRows - 1) / kPrepRows), kThreads, 0,
-                     s>>>(kp, t);
-  ++*nk;
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (t.tc) {
-    e = launch_tree_tc(kp, vp, t, s, nk);
-  } else {
-    e = launch_main(kp, vp, t, s, nk);
+  cudaError_t e;
+  if (t.prod) {
+    tree_prep_prod_kernel<<<(unsigned)kp.n_slots * t.rows, kThreads, 0, s>>>(kp, t);
+    ++*nk;
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
   }
+  const size_t smem =
+      (size_t)(kp.D * kPrepRows + 2 * kPrepK * kPrepCols + kPrepRows * kp.r) * sizeof(float);
+  e = cudaFuncSetAttribute(tree_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  tree_combine_kernel<<<(unsigned)kp.n_slots * t.rows, kThreads, 0, s>>>(kp, vp, t);
+  const int prep_blocks = (t.rows + kPrepRows - 1) / kPrepRows;
+  tree_prep_kernel<<<(unsigned)kp.n_slots * prep_blocks, kPrepThreads, smem, s>>>(kp, t);
   ++*nk;
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = t.tc ? launch_tree_tc(kp, vp, t, s, nk) : launch_main(kp, vp, t, s, nk);
+  if (e != cudaSuccess) return e;
+  const int blocks = (t.rows + kCombineWarps - 1) / kCombineWarps;
+  ++*nk;
+  return launch_dependent(tree_combine_kernel, (unsigned)kp.n_slots * blocks, kCombineWarps * 32, 0,
+                          s, kp, vp, t);
 }
 
 }  // namespace kvc

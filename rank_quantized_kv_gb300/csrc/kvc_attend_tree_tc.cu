@@ -11,7 +11,7 @@
 //   producer (1 thread)   bulk-copies packed key and value rows into row stages;
 //   decoders (8 warps)    key codes -> fp16 A in TMEM (lane = token); value
 //                         codes -> fp16 V in shared memory;
-//   MMA (1 thread)        S(i+1) = A W^T, then O += V^T P(i) per row group;
+//   two MMA warps         S = A W^T, and O += V^T P;
 //   softmax (2 groups of 4 warps, each half of the rows' columns; lane = token)
 //                         S -> P in fp16 in shared memory, sums of P in fp32.
 //
@@ -33,6 +33,7 @@
 
 #include <algorithm>
 
+#include "kvc_launch.cuh"
 #include "kvc_sm100.cuh"
 #include "kvc_tc.h"
 
@@ -45,13 +46,13 @@ namespace {
 constexpr int kTile = kTreeTile;
 constexpr int kSoftWarps = 8, kDecWarps = 8;
 constexpr int kProdWarp = kSoftWarps + kDecWarps;
-constexpr int kMmaWarp = kProdWarp + 1;
+constexpr int kScoreWarp = kProdWarp + 1, kSumWarp = kProdWarp + 2;
 // 20 warps: setmaxnreg works on whole groups of four
 constexpr int kThreads = (kProdWarp + 4) * 32;
 constexpr int kDecThreads = kDecWarps * 32;
-// registers per thread: the launch gives 96; producer and MMA group, decoders
-// and softmax groups then hold 40, 72 and 144 (128 (40 + 2 72 + 2 144) <= 640 96)
-constexpr int kLaunchRegs = 96, kCtlRegs = 40, kDecRegs = 72, kSoftRegs = 144;
+// registers per thread: the launch gives 96; producer and MMA warps, decoders
+// and softmax groups then hold 48, 72 and 144 (128 (48 + 2 72 + 2 144) = 640 96)
+constexpr int kLaunchRegs = 96, kCtlRegs = 48, kDecRegs = 72, kSoftRegs = 144;
 static_assert(128 * (kCtlRegs + 2 * kDecRegs + 2 * kSoftRegs) <= kThreads * kLaunchRegs,
               "register split exceeds the launch's registers");
 constexpr int kMaxNS = 4;          // row stages
@@ -118,35 +119,68 @@ __device__ __forceinline__ uint4 int8_values(uint2 b) {
                     hsub2_bits(__byte_perm(y, 0x64646464u, 0x5342), sub));
 }
 
-// 2W bits at bit `off` of the words w (compile-time offsets).
+// Centroids of at most 8 levels as bytes: low bytes, then high bytes, of the
+// fp16 values of levels 0..3 and 4..7.
+struct Levels { uint32_t lo0, lo1, hi0, hi1; };
+
+// The fp16 centroids of the eight W-bit codes in the low bits of x (what lies
+// above them is ignored): the codes are spread to one per nibble (three steps
+// of halving, each a shift and a select), which is the selector that a byte
+// permute of the levels takes.  No table in shared memory: its bandwidth is
+// what the kernel has least of.
 template <int W>
-__device__ __forceinline__ uint32_t pair_field(const uint32_t (&w)[W], int off) {
-  const int i = off >> 5, sh = off & 31;
-  const uint32_t x =
-      sh + 2 * W <= 32 ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1 < W ? i + 1 : W - 1], sh);
-  return x & ((1u << (2 * W)) - 1u);
+__device__ __forceinline__ uint4 centroids8(uint32_t x, const Levels& t) {
+  auto select = [](uint32_t a, uint32_t b, uint32_t m) { return (a & m) | (b & ~m); };
+  x = select(x, x << (16 - 4 * W), 0x0000ffffu);
+  x = select(x, x << (8 - 2 * W), 0x00ff00ffu);
+  x = select(x, x << (4 - W), 0x0f0f0f0fu) & (0x11111111u * ((1u << W) - 1u));
+  const uint32_t y = x >> 16;
+  const uint32_t l0 = __byte_perm(t.lo0, t.lo1, x), h0 = __byte_perm(t.hi0, t.hi1, x);
+  const uint32_t l1 = __byte_perm(t.lo0, t.lo1, y), h1 = __byte_perm(t.hi0, t.hi1, y);
+  return make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362),
+                    __byte_perm(l1, h1, 0x5140), __byte_perm(l1, h1, 0x7362));
 }
 
-// Codes [k0, k0 + 32 nblk) of a row of W-bit codebook indices: two codes per
-// lookup in a pair table that holds each entry once per lane (no bank
-// conflicts), 8 values (4 TMEM columns) per store.
-template <int W>
-__device__ __forceinline__ void codebook_rows(const unsigned char* row, int k0, int nblk,
-                                              const uint32_t* tab, uint32_t a_tm) {
-  const uint32_t* cl = tab + (threadIdx.x & 31);
-  for (int b = 0; b < nblk; ++b) {
-    const int kb = k0 + 32 * b;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(row + kb / 8 * W);
-    uint32_t w[W];
+// The int8 values of one token block (8 rows of NV chunks of 8 bytes) as fp16 V.
+// Lane (octet, t8) takes token t8 and chunks (c0 + t8) mod NV: of eight lanes
+// no two meet in a bank, neither reading (rows 8 NV bytes apart) nor writing
+// (cores 128 bytes apart).
+template <int NV>
+__device__ __forceinline__ void int8_block(const unsigned char* row, unsigned char* dst, int c0, int t8) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = src[i];
+  for (int j = 0; j < NV / 2; j += 4) {
+    uint2 b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      b[u] = *reinterpret_cast<const uint2*>(row + ((c0 + t8 + j + u) & (NV - 1)) * 8);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<uint4*>(dst + ((c0 + t8 + j + u) & (NV - 1)) * 128) = int8_values(b[u]);
+  }
+}
+
+// 64 consecutive codes (2 W words, 8-byte aligned) of a row of W-bit indices
+// into 32 TMEM columns.
+template <int W>
+__device__ __forceinline__ void codebook64(const unsigned char* src, const Levels& t, uint32_t a_tm) {
+  uint32_t w[2 * W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const uint2 v = reinterpret_cast<const uint2*>(src)[i];
+    w[2 * i] = v.x;
+    w[2 * i + 1] = v.y;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r[16];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = cl[pair_field<W>(w, W * (8 * c + 2 * i)) * 32];
-      tmem_st4(a_tm + (kb / 8 + c) * 4, make_uint4(o[0], o[1], o[2], o[3]));
+      const int bit = (4 * h + c) * 8 * W, i = bit >> 5, sh = bit & 31;
+      const uint32_t x = sh + 8 * W <= 32 ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1], sh);
+      const uint4 v = centroids8<W>(x, t);
+      r[4 * c] = v.x; r[4 * c + 1] = v.y; r[4 * c + 2] = v.z; r[4 * c + 3] = v.w;
     }
+    tmem_st16(a_tm + h * 16, r);
   }
 }
 
@@ -171,17 +205,19 @@ __device__ __forceinline__ uint64_t desc_mnmajor(uint32_t saddr, uint32_t k_stri
 }
 constexpr uint32_t kTransposeAB = (1u << 15) | (1u << 16);  // both operands MN-major
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 template <int REGS> __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 template <int REGS> __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-
-__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t (&r)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    tmem_st4(taddr + 4 * i, make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -275,11 +311,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* Ps = smem + z.off_p;
   unsigned char* Vs = smem + z.off_v;
   unsigned char* Rs = smem + z.off_stage;
-  uint32_t* tab = reinterpret_cast<uint32_t*>(smem + z.off_tab);
+  uint32_t* tab = reinterpret_cast<uint32_t*>(smem + z.off_tab);  // codebooks of 16 or 256 levels
   const int w_piece = z.n * z.K * 2;
-  const int p_bytes = kTile * NC * 2, v_bytes = z.mt * kTile * 256;
+  const int v_bytes = z.mt * kTile * 256;
 
-  if (warp == kMmaWarp) tmem_alloc(&tmem_base, z.cols);
+  if (warp == kScoreWarp) tmem_alloc(&tmem_base, z.cols);
   if (tid == 0) {
     for (int i = 0; i < z.ns; ++i) { mbar_init(&row_full[i], 1); mbar_init(&row_empty[i], kDecWarps); }
     for (int i = 0; i < 2; ++i) {
@@ -293,22 +329,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_empty[i], 1);
     }
     mbar_init(&w_full, z.nwg);
-    mbar_init(&done_bar, 1);
+    mbar_init(&done_bar, 2);
     fence_mbar_init();
     abort_flag = 0;
   }
-  if (KMODE == KVC_MODE_CODEBOOK) {  // fp16 centroids: per lane pairs, pairs, or single
-    const int L = kp.cb_levels, wb = kp.cb_bits;
+  if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits >= 4) {  // pairs of 16 levels, or 256 levels
+    const int pair = kp.cb_bits == 4;
     auto half_of = [&](int c) {
       return (uint32_t)__half_as_ushort(__float2half_rn(kp.codebook[c] * t.cb_mul));
     };
-    if (wb <= 3)
-      for (int j = tid; j < L * L * 32; j += kThreads)
-        tab[j] = half_of((j >> 5) & (L - 1)) | (half_of(j >> (5 + wb)) << 16);
-    else if (wb == 4)
-      for (int j = tid; j < 256; j += kThreads) tab[j] = half_of(j & 15) | (half_of(j >> 4) << 16);
-    else
-      for (int j = tid; j < 256; j += kThreads) tab[j] = half_of(j);
+    for (int j = tid; j < 256; j += kThreads)
+      tab[j] = pair ? half_of(j & 15) | (half_of(j >> 4) << 16) : half_of(j);
   }
   tc_fence_before();
   __syncthreads();
@@ -316,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm = tmem_base;
   Walk walk(t);
   Segment g;
+  grid_dependency_wait();  // the key weights come from the launch before
 
   if (warp >= kProdWarp) {
     regs_dec<kCtlRegs>();
@@ -344,28 +376,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // copies still in flight (after a time-out) land before the CTA exits
       for (int j = max(0, issued - z.ns); j < issued; ++j)
         mbar_wait_bounded(&row_full[j % z.ns], (j / z.ns) & 1, kWaitNs);
-    } else if (warp == kMmaWarp && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
-      const uint32_t id_s = idesc_f16(kTile, z.n, 0);
-      const uint32_t id_o = idesc_f16(kTile, NC, 0) | kTransposeAB;
-      const uint32_t sbo = (uint32_t)z.KC * 128, v_k = (uint32_t)z.mt * 2048, p_k = NC / 8 * 128;
-      const uint32_t w0 = smem_u32(Ws), p0 = smem_u32(Ps), v0 = smem_u32(Vs);
-      auto weighted_sum = [&](int j, bool first) {  // O += V^T P of tile j
-        const int vb = j % z.nv;
-        wait_or_abort(&v_full[vb], (j / z.nv) & 1, &abort_flag);
-        for (int wg = 0; wg < z.nwg; ++wg) {
-          wait_or_abort(&p_full[wg], j & 1, &abort_flag);
-          tc_fence_after();
-          for (int m = 0; m < z.mt; ++m)
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              umma_f16(tm + z.o_col + m * z.n + wg * NC,
-                       desc_mnmajor(v0 + vb * v_bytes + m * 2048 + ks * 2 * v_k, v_k, 128),
-                       desc_mnmajor(p0 + wg * p_bytes + ks * 2 * p_k, p_k, 128), id_o,
-                       first && ks == 0 ? 0u : 1u);
-          umma_commit(&p_empty[wg]);
-        }
-        umma_commit(&v_empty[vb]);
-      };
+    } else if (warp == kScoreWarp) {
+      // ---------------------------------------------------------- S = A W^T
+      // The whole warp walks and waits, one elected lane issues, so that
+      // descriptors stay in uniform registers; the two products have a warp
+      // each.  (One lane walking and issuing both took 160 cycles per MMA.)
+      const bool leader = elect_one();
+      const uint32_t id = idesc_f16(kTile, z.n, 0);
+      const uint64_t w_desc = desc_kmajor_noswizzle(smem_u32(Ws), 128, (uint32_t)z.KC * 128);
       int it = 0, segs = 0;
       while (walk.next(t, kp.H, g)) {
         if (g.tile0 == g.tile1) continue;
@@ -373,23 +391,78 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++segs;
         for (int tile = g.tile0; tile < g.tile1; ++tile, ++it) {
           const int s = it & 1;
-          wait_or_abort(&a_full[s], (it >> 1) & 1, &abort_flag);
           if (it >= 2) wait_or_abort(&s_empty[s], ((it >> 1) - 1) & 1, &abort_flag);
+          wait_or_abort(&a_full[s], (it >> 1) & 1, &abort_flag);
+          __syncwarp();
           tc_fence_after();
-          const uint32_t a0 = tm + s * z.a_cols;
-          for (int p = 0; p < 2; ++p)
-            for (int ks = 0; ks < z.K / 16; ++ks)  // 16 fp16 of K: 8 TMEM columns of A
-              umma_f16_tmem_a(tm + z.s_col + s * z.n, a0 + ks * 8,
-                              desc_kmajor_noswizzle(w0 + p * w_piece + ks * 256, 128, sbo), id_s,
-                              p + ks > 0 ? 1u : 0u);
-          umma_commit(&s_full[s]);
-          umma_commit(&a_empty[s]);
-          if (tile > g.tile0) weighted_sum(it - 1, tile - 1 == g.tile0);
+          if (leader) {
+            const uint32_t a0 = tm + s * z.a_cols, d0 = tm + z.s_col + s * z.n;
+            umma_f16_tmem_a(d0, a0, w_desc, id, 0u);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {  // the two pieces of W
+              const uint64_t wd = w_desc + ((p * w_piece) >> 4);
+#pragma unroll 8
+              for (int ks = 1 - p; ks < z.K / 16; ++ks)  // 16 fp16 of K: 8 TMEM columns of A
+                umma_f16_tmem_a(d0, a0 + ks * 8, wd + ks * 16, id, 1u);
+            }
+            umma_commit(&s_full[s]);
+            umma_commit(&a_empty[s]);
+          }
+          __syncwarp();
         }
-        weighted_sum(it - 1, g.tile1 - 1 == g.tile0);
       }
-      umma_commit(&done_bar);  // TMEM is released only after every MMA has finished
-      mbar_wait_bounded(&done_bar, 0, kWaitNs);
+      if (leader) {
+        umma_commit(&done_bar);  // TMEM is released only after every MMA has finished
+        mbar_wait_bounded(&done_bar, 0, kWaitNs);
+      }
+      __syncwarp();
+    } else if (warp == kSumWarp) {
+      // ---------------------------------------------------------- O += V^T P
+      // One product over both groups' columns, or, where the groups hold 64
+      // each, one per group as its weights arrive.
+      const bool leader = elect_one();
+      const int parts = NC == 64 ? z.nwg : 1;
+      const uint32_t pn = NC == 64 ? NC : z.n;
+      const uint32_t id = idesc_f16(kTile, pn, 0) | kTransposeAB;
+      const uint32_t v_k = (uint32_t)z.mt * 2048, p_k = (uint32_t)z.n * 16;
+      const uint64_t v_desc = desc_mnmajor(smem_u32(Vs), v_k, 128);
+      const uint64_t p_desc = desc_mnmajor(smem_u32(Ps), p_k, 128);
+      const uint64_t v_step = (2 * v_k) >> 4, p_step = (2 * p_k) >> 4;
+      int it = 0;
+      Ring rv(z.nv);
+      while (walk.next(t, kp.H, g)) {
+        for (int tile = g.tile0; tile < g.tile1; ++tile, ++it, rv.next()) {
+          wait_or_abort(&v_full[rv.slot], rv.phase, &abort_flag);
+          for (int h = 0; h < parts; ++h) {
+            for (int wg = h; wg < (parts == 1 ? z.nwg : h + 1); ++wg)
+              wait_or_abort(&p_full[wg], it & 1, &abort_flag);
+            __syncwarp();
+            tc_fence_after();
+            if (leader) {
+              for (int m = 0; m < z.mt; ++m) {
+                const uint32_t o = tm + z.o_col + m * z.n + h * pn;
+                uint64_t vd = v_desc + ((rv.slot * v_bytes + m * 2048) >> 4);
+                uint64_t pd = p_desc + h * (NC / 8 * 128 >> 4);
+                umma_f16(o, vd, pd, id, tile > g.tile0 ? 1u : 0u);
+#pragma unroll
+                for (int ks = 1; ks < kTile / 16; ++ks) {
+                  vd += v_step;
+                  pd += p_step;
+                  umma_f16(o, vd, pd, id, 1u);
+                }
+              }
+              for (int wg = h; wg < (parts == 1 ? z.nwg : h + 1); ++wg) umma_commit(&p_empty[wg]);
+              if (h == parts - 1) umma_commit(&v_empty[rv.slot]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (leader) {
+        umma_commit(&done_bar);
+        mbar_wait_bounded(&done_bar, 0, kWaitNs);
+      }
+      __syncwarp();
     }
   } else if (warp >= kSoftWarps) {
     // ------------------------------------------------------------ decoders
@@ -402,6 +475,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (cores 128 bytes apart) meet in a bank
     const int octet = lane >> 3, t8 = lane & 7;
     const int vblk = (warp - kSoftWarps) * 2 + (octet >> 1);
+    Levels levels{};
+    if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits <= 3) {
+      uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t h =
+            j < kp.cb_levels ? __half_as_ushort(__float2half_rn(kp.codebook[j] * t.cb_mul)) : 0u;
+        lo[j >> 2] |= (h & 0xffu) << (8 * (j & 3));
+        hi[j >> 2] |= (h >> 8) << (8 * (j & 3));
+      }
+      levels = Levels{lo[0], lo[1], hi[0], hi[1]};
+    }
     Ring rr(z.ns), rv(z.nv);
     int it = 0;
     while (walk.next(t, kp.H, g)) {
@@ -423,13 +508,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         const unsigned char* st = Rs + rr.slot * z.stage;
         const uint32_t a_tm = tm + lane_base + a * z.a_cols;
-        if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits <= 3 && z.K % 64 == 0 && z.K == kp.D) {
-          const unsigned char* row = st + tt * Pk;
-          const int nq = z.K / 64;
-          if (kp.cb_bits == 3) codebook_rows<3>(row, half * (z.K / 2), nq, tab, a_tm);
-          else if (kp.cb_bits == 2) codebook_rows<2>(row, half * (z.K / 2), nq, tab, a_tm);
-          else codebook_rows<1>(row, half * (z.K / 2), nq, tab, a_tm);
+        if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits <= 3 && kp.D == 128) {
+          const int W = kp.cb_bits;
+          const unsigned char* src = st + tt * Pk + half * 8 * W;
+          if (W == 3) codebook64<3>(src, levels, a_tm + half * 32);
+          else if (W == 2) codebook64<2>(src, levels, a_tm + half * 32);
+          else codebook64<1>(src, levels, a_tm + half * 32);
         } else {
+#pragma unroll 4
           for (int c = half; c < z.KC; c += 2) {
             const uint32_t ent = kch[c];
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -438,17 +524,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint2 b = bits_at(st, tt * Pk + (int)(ent & 0xffffu));
               if (KMODE == KVC_MODE_UNIFORM) {
                 v = centred_codes(b, w);
+              } else if (w <= 3) {
+                v = w == 3 ? centroids8<3>(b.x, levels) : w == 2 ? centroids8<2>(b.x, levels)
+                                                                 : centroids8<1>(b.x, levels);
               } else {
-                uint32_t o[4];
-                const uint64_t bits = (uint64_t)b.x | ((uint64_t)b.y << 32);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const uint32_t x = (uint32_t)(bits >> (2 * w * q));
-                  if (w <= 3) o[q] = tab[(x & ((1u << (2 * w)) - 1u)) * 32 + lane];
-                  else if (w == 4) o[q] = tab[x & 255u];
-                  else o[q] = tab[x & 255u] | (tab[(x >> 8) & 255u] << 16);
-                }
-                v = make_uint4(o[0], o[1], o[2], o[3]);
+                const int pair = w == 4;
+                auto two = [&](uint32_t x) {
+                  return pair ? tab[x & 255u] : tab[x & 255u] | (tab[(x >> 8) & 255u] << 16);
+                };
+                v = pair ? make_uint4(two(b.x), two(b.x >> 8), two(b.x >> 16), two(b.x >> 24))
+                         : make_uint4(two(b.x), two(b.x >> 16), two(b.y), two(b.y >> 16));
               }
             }
             tmem_st4(a_tm + c * 4, v);
@@ -464,19 +549,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned char* raw = st + z.krow;
           const int tok = vblk * 8 + t8;
           unsigned char* dst = Vs + rv.slot * v_bytes + vblk * z.mt * 2048 + t8 * 16;
-          for (int j = 0; j < vhalf; ++j) {
-            const int c0 = j + (octet & 1) * vhalf;
-            if (c0 >= nv) continue;
-            int c = c0 + t8;
-            while (c >= nv) c -= nv;
-            uint4 v;
-            if (VU) {
-              const uint32_t ent = vch[c];
-              v = centred_codes(bits_at(raw, tok * Pv + (int)(ent & 0xffffu)), (int)(ent >> 16));
-            } else {
-              v = int8_values(*reinterpret_cast<const uint2*>(raw + tok * Pv + c * 8));
+          const int c0 = (octet & 1) * vhalf;
+          if (!VU && nv == 16) {
+            int8_block<16>(raw + tok * 128, dst, c0, t8);
+          } else if (!VU && nv == 8) {
+            int8_block<8>(raw + tok * 64, dst, c0, t8);
+          } else {
+            const int cend = min(nv, c0 + vhalf);
+            for (int j = c0; j < cend; ++j) {
+              int c = j + t8;
+              while (c >= nv) c -= nv;
+              uint4 v;
+              if (VU) {
+                const uint32_t ent = vch[c];
+                v = centred_codes(bits_at(raw, tok * Pv + (int)(ent & 0xffffu)), (int)(ent >> 16));
+              } else {
+                v = int8_values(*reinterpret_cast<const uint2*>(raw + tok * Pv + c * 8));
+              }
+              *reinterpret_cast<uint4*>(dst + c * 128) = v;
             }
-            *reinterpret_cast<uint4*>(dst + c * 128) = v;
           }
         }
         fence_proxy_async_smem();  // V is read by the tensor core
@@ -494,11 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t o_tm = tm + lane_off + z.o_col + wg * NC;
     float* cn = cneg[wg];
-    unsigned char* pst = Ps + wg * p_bytes + ((quarter * 32 + lane) >> 3) * (NC / 8 * 128) + (lane & 7) * 16;
-    const int stride = 2 + t.Dv;
+    unsigned char* pst = Ps + ((quarter * 32 + lane) >> 3) * (z.n * 16) + wg * (NC / 8 * 128) + (lane & 7) * 16;
     int it = 0;
     while (walk.next(t, kp.H, g)) {
-      const int64_t first = t.first ? t.first[g.b] : 0;
+      const int64_t first = t.first ? max(t.first[g.b], 0) : 0;
       const int col0 = wg * NC, ncol = max(0, min(NC, g.nr - col0));  // rows of this group
       const size_t row0 = (size_t)g.slot * t.rows + g.r0 + col0;
       float post = 1.f;
@@ -550,8 +640,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(bar, 128);
         if (ltid == 0) mbar_arrive(&w_full);
       }
-      const __half* knorm = reinterpret_cast<const __half*>(kp.store + kp.side_off[g.slot]);
-      const __half* vscale = reinterpret_cast<const __half*>(vp.store + vp.side_off[g.slot]);
       const uint8_t* mask = t.mask ? t.mask + g.b * t.mask_sb : nullptr;
       float2 l[NC / 2];
 #pragma unroll
@@ -559,28 +647,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t unseen = ncol ? (1u << NCH) - 1u : 0u;  // column chunks with rows that saw nothing yet
       float sref = VU ? 1.f : 0.f, inv_sref = VU ? 1.f : 0.f;
       const int lt = quarter * 32 + lane;
-      auto side_of = [&](const __half* p, int tile) {
-        const int64_t tok = (int64_t)tile * kTile + lt;
-        return tok < t.S ? __half2float(p[tok]) : 0.f;
-      };
-      float nt_next = 1.f, st_next = 1.f;
-      if (g.tile0 < g.tile1) {
-        if (KMODE == KVC_MODE_CODEBOOK) nt_next = side_of(knorm, g.tile0);
-        if (!VU) st_next = side_of(vscale, g.tile0);
+      // this lane's norm and scale, loaded one tile ahead and converted at use
+      // (converting them at the load would wait for it)
+      const unsigned short* knorm = reinterpret_cast<const unsigned short*>(kp.store + kp.side_off[g.slot]);
+      const unsigned short* vscale = reinterpret_cast<const unsigned short*>(vp.store + vp.side_off[g.slot]);
+      const int live_tiles = (int)((t.S - lt + kTile - 1) / kTile);  // tiles in which this lane has a token
+      const unsigned short* kn = knorm + (int64_t)g.tile0 * kTile + lt;
+      const unsigned short* vsc = vscale + (int64_t)g.tile0 * kTile + lt;
+      unsigned short nt_next = 0, st_next = 0;
+      if (g.tile0 < g.tile1 && g.tile0 < live_tiles) {
+        if (KMODE == KVC_MODE_CODEBOOK) nt_next = *kn;
+        if (!VU) st_next = *vsc;
       }
+      // tiles [plain0, plain1) hold visible context alone
+      const int plain0 = (int)min((int64_t)t.tps, (first + kTile - 1) / kTile), plain1 = (int)(t.ctx / kTile);
       for (int tile = g.tile0; tile < g.tile1; ++tile, ++it) {
         const int s = it & 1;
-        const float nt = nt_next * post, st = st_next;
-        if (tile + 1 < g.tile1) {  // the next tile's norms and scales
-          if (KMODE == KVC_MODE_CODEBOOK) nt_next = side_of(knorm, tile + 1);
-          if (!VU) st_next = side_of(vscale, tile + 1);
+        const float nt = KMODE == KVC_MODE_CODEBOOK ? __half2float(__ushort_as_half(nt_next)) * post : post;
+        const float st = VU ? 1.f : __half2float(__ushort_as_half(st_next));
+        kn += kTile;
+        vsc += kTile;
+        if (tile + 1 < g.tile1 && tile + 1 < live_tiles) {  // the next tile's norms and scales
+          if (KMODE == KVC_MODE_CODEBOOK) nt_next = *kn;
+          if (!VU) st_next = *vsc;
+        } else {
+          nt_next = st_next = 0;
         }
         // which of the group's rows see this lane's token
-        const int64_t t0 = (int64_t)tile * kTile, tok = t0 + lt;
-        const bool special = t0 + kTile > t.ctx || t0 < first;
+        const bool special = tile < plain0 || tile >= plain1;
         uint64_t vis = ~0ull;
         if (special) {
-          const int64_t draft = tok - t.ctx;
+          const int64_t tok = (int64_t)tile * kTile + lt, draft = tok - t.ctx;
           if (draft < 0) {
             vis = tok >= first ? ~0ull : 0ull;
           } else {
@@ -695,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int i = 0; i < 16; ++i)
                     o[i] = __float_as_uint(__uint_as_float(o[i]) * (mine ? corr[wg][c + i] * ratio : ratio));
-                  tmem_st_n(o_tm + m * z.n + c, o);
+                  tmem_st16(o_tm + m * z.n + c, o);
                 }
               tmem_wait_st();
             }
@@ -752,12 +849,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       named_bar_sync(bar, 128);
-      float* part = t.part + (((size_t)g.job + blockIdx.x) * t.rt + col0) * stride;
+      const size_t prow = ((size_t)g.job + blockIdx.x) * t.rt + col0;
+      float* part = t.part + prow * t.Dvp;
       if (ltid < ncol) {
         const bool sn = seen[wg][ltid] != 0;
-        part[(size_t)ltid * stride] = sn ? mref[wg][ltid] : -INFINITY;
-        part[(size_t)ltid * stride + 1] =
-            sn ? (red[wg][0][ltid] + red[wg][1][ltid]) + (red[wg][2][ltid] + red[wg][3][ltid]) : 0.f;
+        t.ml[prow + ltid] = make_float2(
+            sn ? mref[wg][ltid] : -INFINITY,
+            sn ? (red[wg][0][ltid] + red[wg][1][ltid]) + (red[wg][2][ltid] + red[wg][3][ltid]) : 0.f);
       }
       for (int m = 0; m < z.mt; ++m) {
         const int d = m * 128 + quarter * 32 + lane;
@@ -771,16 +869,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (c + i < ncol)
-                part[(size_t)(c + i) * stride + 2 + d] = any ? __uint_as_float(o[i]) * sref : 0.f;
+                part[(size_t)(c + i) * t.Dvp + d] = any ? __uint_as_float(o[i]) * sref : 0.f;
           }
         }
       }
       tc_fence_before();  // the next segment's first product overwrites O
     }
   }
+  grid_dependents_launch();
   __syncthreads();
   if (abort_flag && tid == 0) atomicCAS(kp.err, 0, kErrTimeout);
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tm, z.cols);
   }
@@ -826,7 +925,7 @@ bool shape_for(const Params& kp, const TreeArgs& t, int nc, int nwg, Shape* out)
   z.off_p = 2 * z.n * z.K * 2;
   z.off_v = z.off_p + z.n * kTile * 2;
   int tab = 0;
-  if (kp.mode == KVC_MODE_CODEBOOK) tab = kp.cb_bits <= 3 ? (1 << (2 * kp.cb_bits)) * 128 : 1024;
+  if (kp.mode == KVC_MODE_CODEBOOK && kp.cb_bits >= 4) tab = 1024;
   // two V buffers and four row stages, or what fits
   const int most = 220 * 1024;  // of 227 KB: the static arrays take 5
   for (z.nv = 2; z.nv >= 1; --z.nv)
@@ -877,9 +976,8 @@ cudaError_t launch_tree_tc(const Params& kp, const Params& vp, const TreeArgs& t
   if (fa.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, z.smem);
   if (e != cudaSuccess) return e;
-  k<<<(unsigned)t.grid, kThreads, (size_t)z.smem, s>>>(kp, vp, t, z);
   ++*nk;
-  return cudaGetLastError();
+  return launch_dependent(k, (unsigned)t.grid, kThreads, (size_t)z.smem, s, kp, vp, t, z);
 }
 
 }  // namespace kvc

@@ -136,6 +136,7 @@ struct TreeArgs {
   void* out = nullptr;
   int out_bf16 = 0;
   int64_t o_sb = 0, o_sh = 0, o_st = 0;
+  int o_vec = 0;                         // rows of out start at multiples of 8 bytes, D of 4
   int Hq = 0, rep = 0, N = 0;
   float scale_log2 = 0.f;                // score scale times log2(e)
   int64_t S = 0, ctx = 0;                // stored tokens; those before the drafts
@@ -150,7 +151,11 @@ struct TreeArgs {
   float* w = nullptr;                    // workspace: [n_slots rows][NCk] key weights
   float* c1 = nullptr;                   // workspace: [n_slots rows] score offsets
   float* wx = nullptr;                   // workspace: [n_slots rows][m + n_out]
-  float* part = nullptr;                 // workspace: [jobs + grid - 1][rt][2 + Dv]
+  // workspace: the partials [jobs + grid - 1][rt], per row its reference and
+  // sum of weights (ml) and its weighted sums (part, Dv padded to Dvp, a multiple of 4)
+  float2* ml = nullptr;
+  float* part = nullptr;
+  int Dvp = 0;
 };
 // Rows of a tensor-core job for these layers (kvc_attend_tree_tc.cu), 0 where
 // that kernel does not take them; its launcher.
