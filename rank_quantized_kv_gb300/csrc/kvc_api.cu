@@ -895,7 +895,8 @@ static kvc_status tree_check(const kvc_layer* K, const kvc_layer* V, int32_t Hq,
     return fail(KVC_EINVAL, "N %d drafted tokens: need 1 .. length (%lld)", N, (long long)K->len);
   if (K->ncpos > 256 || (V->mode == KVC_MODE_UNIFORM && V->ncpos > 256))
     return fail(KVC_EINVAL, "more than 256 packed positions");
-  // kernels number (slot, row) pairs and (job, CTA) pairs in 32 bits
+  // kernels number tokens, (slot, row) pairs and (job, CTA) pairs in 32 bits
+  if (K->len > INT32_MAX - 1024) return fail(KVC_EINVAL, "more than 2^31 - 1024 tokens");
   if ((int64_t)K->B * Hq * N > (1 << 30)) return fail(KVC_EINVAL, "too many query rows");
   t.Hq = Hq;
   t.rep = Hq / K->H;
@@ -917,9 +918,11 @@ static kvc_status tree_check(const kvc_layer* K, const kvc_layer* V, int32_t Hq,
   }
   DeviceGuard dg(K->device);
   if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
-  if (K->path == KVC_PATH_AUTO) t.tc = kvc::tree_tc_rows(K->p, V->p, t);
-  t.cb_mul = K->cb_mul;
-  t.w_mul = 1.f / K->cb_mul;
+  if (K->path == KVC_PATH_AUTO) t.tc = kvc::tree_tc_rows(K->p, V->p, t, &t.parts, &t.K);
+  if (t.tc) {
+    t.cb_mul = K->cb_mul;
+    t.w_mul = 1.f / K->cb_mul;
+  }
   *ws_bytes = kvc::tree_plan(K->p, t, kvc::sm_count());
   return KVC_OK;
 }

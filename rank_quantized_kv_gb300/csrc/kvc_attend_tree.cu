@@ -96,7 +96,8 @@ __device__ __forceinline__ float load_q(const TreeArgs& t, int64_t i) {
 
 // ---------------------------------------------------------------- prep
 
-// The key weights at every packed position, w_j = scale log2(e) u_j coef_j
+// The key weights at every packed position (for the tensor cores: split into two
+// fp16 pieces and laid out as their operand), w_j = scale log2(e) u_j coef_j
 // (coef = step in uniform mode, 1 for a codebook), and c1.  One block per (slot,
 // 32 rows): u = q V as a register-tiled product, 8 rows x 2 columns a thread,
 // over 128 columns at a time; q stays in shared memory, V passes through it 32
@@ -106,12 +107,16 @@ constexpr int kPrepCols = 128, kPrepK = 32;
 
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp, const TreeArgs t) {
   extern __shared__ __align__(16) float sm_f[];
-  const int D = kp.D, r = kp.r, tid = threadIdx.x;
-  const int blocks = (t.rows + kPrepRows - 1) / kPrepRows;
+  __shared__ int comp[256];       // packed position: component (-1: padding) and its factor
+  __shared__ float coef[256];
+  __shared__ float down[kPrepRows];  // power of two that brings a row into fp16's range
+  const int D = kp.D, r = kp.r, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int blocks = (t.prow + kPrepRows - 1) / kPrepRows;
   const int slot = blockIdx.x / blocks, r0 = (blockIdx.x - slot * blocks) * kPrepRows;
   const int b = slot / kp.H, h = slot - b * kp.H;
   const int beta = kp.basis_of[slot];
-  const int nr = min(kPrepRows, t.rows - r0);
+  const int nr = max(0, min(kPrepRows, t.rows - r0));  // rows of queries
+  const int np = min(kPrepRows, t.prow - r0);          // rows written
   float* qs = sm_f;                            // [D][32] rows of q, transposed
   float* vs = qs + D * kPrepRows;              // [2][32][128] rows of V
   float* us = vs + 2 * kPrepK * kPrepCols;     // [32][r] products
@@ -172,17 +177,17 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
   }
   __syncthreads();
   const bool uniform = kp.mode == KVC_MODE_UNIFORM;
-  const size_t row0 = (size_t)slot * t.rows + r0;
-  for (int j = tid; j < t.NCk; j += kPrepThreads) {  // this thread's positions of all rows
+  const size_t row0 = (size_t)slot * t.prow + r0;
+  for (int j = tid; j < 256; j += kPrepThreads) {
     int width = 0;
-    const int k = position_component(kp, beta, j, &width);
-    const float f = k < 0 ? 0.f : t.scale_log2 * (uniform ? kp.step[(size_t)beta * r + k] : 1.f);
-    for (int row = 0; row < nr; ++row) t.w[(row0 + row) * t.NCk + j] = k < 0 ? 0.f : f * us[row * r + k];
+    const int k = j < t.NCk ? position_component(kp, beta, j, &width) : -1;
+    comp[j] = k;
+    coef[j] = k < 0 ? 0.f : t.scale_log2 * t.w_mul * (uniform ? kp.step[(size_t)beta * r + k] : 1.f);
   }
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int row = warp; row < nr; row += kPrepThreads / 32) {  // c1, a warp a row
-    float c1 = 0.f;
-    if (uniform) {
+  __syncthreads();
+  for (int row = warp; row < np; row += kPrepThreads / 32) {  // a warp a row
+    float c1 = 0.f, mx = 0.f;
+    if (uniform && row < nr) {
       for (int k = lane; k < r; k += 32) {
         const size_t bk = (size_t)beta * r + k;
         const int width = kp.bits[bk];
@@ -191,7 +196,48 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
       for (int i = lane; i < D; i += 32) c1 = fmaf(qs[i * kPrepRows + row], kp.mean[(size_t)beta * D + i], c1);
     }
     c1 = warp_sum(c1);
-    if (lane == 0) t.c1[row0 + row] = t.scale_log2 * c1;
+    if (t.tc) {
+      for (int j = lane; j < t.NCk; j += 32)
+        if (comp[j] >= 0) {
+          const float v = fabsf(us[row * r + comp[j]] * coef[j]);
+          if (v <= 3.4e38f) mx = fmaxf(mx, v);  // NaN and infinities stay what they are
+        }
+      mx = warp_max(mx);
+    }
+    if (lane == 0) {
+      t.c1[row0 + row] = t.scale_log2 * c1;
+      if (t.tc) {
+        const int ex = max(0, (__float_as_int(mx) >> 23) - 127 - 13);
+        t.wscale[row0 + row] = __int_as_float((127 + ex) << 23);
+        down[row] = __int_as_float((127 - ex) << 23);
+      }
+    }
+  }
+  if (!t.tc) {
+    for (int j = tid; j < t.NCk; j += kPrepThreads)  // this thread's positions of all rows
+      for (int row = 0; row < nr; ++row)
+        t.w[(row0 + row) * t.NCk + j] = comp[j] < 0 ? 0.f : coef[j] * us[row * r + comp[j]];
+    return;
+  }
+  // two fp16 pieces in the layout of a K-major operand without swizzle: cores of
+  // 8 rows x 8 positions, 128 contiguous bytes, adjacent along K
+  __syncthreads();
+  const int KC = t.K / 8;
+  for (int e = tid; e < np * KC; e += kPrepThreads) {
+    const int c = e / np, row = e - c * np;
+    const int x = r0 + row, jt = x / t.rt, rr = x - jt * t.rt;
+    uint16_t* dst = t.w16 + ((size_t)slot * t.row_tiles + jt) * 2 * t.rt * t.K +
+                    (rr >> 3) * (KC * 64) + c * 64 + (rr & 7) * 8;
+    __half hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = comp[8 * c + i];
+      const float v = k < 0 || row >= nr ? 0.f : us[row * r + k] * coef[8 * c + i] * down[row];
+      hi[i] = __float2half_rn(v);
+      lo[i] = __float2half_rn(v - __half2float(hi[i]));
+    }
+    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(hi);
+    *reinterpret_cast<uint4*>(dst + t.rt * t.K) = *reinterpret_cast<const uint4*>(lo);
   }
 }
 
@@ -518,9 +564,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   while (run_begin(t, c0) > lo) --c0;
   int64_t c1 = c0;
   while (run_begin(t, c1 + 1) < hi) ++c1;
-  const int np = (int)(c1 - c0) + 1;
-  const float2* ml = t.ml + ((size_t)job + c0) * t.rt + rr;
-  const float* part = t.part + (((size_t)job + c0) * t.rt + rr) * t.Dvp;
+  const int np = ((int)(c1 - c0) + 1) * t.parts;
+  const size_t p0 = ((size_t)job + c0) * t.parts;
+  const float2* ml = t.ml + p0 * t.rt + rr;
+  const float* part = t.part + (p0 * t.rt + rr) * t.Dvp;
   // lanes take the partials' references and sums, 32 at a time
   float M = -INFINITY;
   for (int s = lane; s < np; s += 32) M = fmaxf(M, ml[(size_t)s * t.rt].x);
@@ -633,14 +680,15 @@ MainKernel main_kernel_for(int kmode, int vmode) {
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
+// key weights: fp32 (CUDA cores) or two fp16 pieces
 size_t w_bytes(const Params& kp, const TreeArgs& t) {
-  return align256((size_t)kp.n_slots * t.rows * t.NCk * 4);
+  return align256((size_t)kp.n_slots * t.prow * (t.tc ? t.K : t.NCk) * 4);
 }
-size_t c1_bytes(const Params& kp, const TreeArgs& t) {
-  return align256((size_t)kp.n_slots * t.rows * 4);
+size_t c1_bytes(const Params& kp, const TreeArgs& t) {  // score offsets; row scales
+  return align256((size_t)kp.n_slots * t.prow * 4);
 }
 size_t ml_bytes(int64_t jobs, const TreeArgs& t) {
-  return align256((size_t)(jobs + t.grid - 1) * t.rt * 8);
+  return align256((size_t)(jobs + t.grid - 1) * t.parts * t.rt * 8);
 }
 size_t wx_bytes(const Params& kp, const TreeArgs& t) {
   return align256((size_t)kp.n_slots * t.rows * (t.m + t.n_out) * 4);
@@ -665,22 +713,26 @@ cudaError_t launch_main(const Params& kp, const Params& vp, const TreeArgs& t, c
 size_t tree_plan(const Params& kp, TreeArgs& t, int sms) {
   t.rt = t.tc ? t.tc : kRows;
   t.row_tiles = (t.rows + t.rt - 1) / t.rt;
+  t.prow = t.tc ? t.row_tiles * t.rt : t.rows;
   const int64_t jobs = (int64_t)kp.n_slots * t.row_tiles;
   t.tps = (t.S + kTreeTile - 1) / kTreeTile;
   t.total = jobs * t.tps;
   // one CTA per SM on the tensor cores, else about twelve
   t.grid = (int)std::min<int64_t>(t.total, (t.tc ? 1 : 12) * (int64_t)sms);
   t.Dvp = (t.Dv + 3) / 4 * 4;
-  return w_bytes(kp, t) + c1_bytes(kp, t) + wx_bytes(kp, t) + ml_bytes(jobs, t) +
-         align256((size_t)(jobs + t.grid - 1) * t.rt * t.Dvp * 4);
+  return w_bytes(kp, t) + 2 * c1_bytes(kp, t) + wx_bytes(kp, t) + ml_bytes(jobs, t) +
+         align256((size_t)(jobs + t.grid - 1) * t.parts * t.rt * t.Dvp * 4);
 }
 
 cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, void* workspace,
                                cudaStream_t s, int* nk) {
   auto* ws = static_cast<unsigned char*>(workspace);
   t.w = reinterpret_cast<float*>(ws);
+  t.w16 = reinterpret_cast<uint16_t*>(ws);
   ws += w_bytes(kp, t);
   t.c1 = reinterpret_cast<float*>(ws);
+  ws += c1_bytes(kp, t);
+  t.wscale = reinterpret_cast<float*>(ws);
   ws += c1_bytes(kp, t);
   t.wx = reinterpret_cast<float*>(ws);
   ws += wx_bytes(kp, t);
@@ -698,7 +750,7 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
       (size_t)(kp.D * kPrepRows + 2 * kPrepK * kPrepCols + kPrepRows * kp.r) * sizeof(float);
   e = cudaFuncSetAttribute(tree_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int prep_blocks = (t.rows + kPrepRows - 1) / kPrepRows;
+  const int prep_blocks = (t.prow + kPrepRows - 1) / kPrepRows;
   tree_prep_kernel<<<(unsigned)kp.n_slots * prep_blocks, kPrepThreads, smem, s>>>(kp, t);
   ++*nk;
   e = cudaGetLastError();

@@ -9,11 +9,15 @@
 // One CTA per SM walks a run of (job, 128-token tile) pairs.  Roles, handing
 // tiles on through mbarrier rings:
 //   producer (1 thread)   bulk-copies packed key and value rows into row stages;
-//   decoders (8 warps)    key codes -> fp16 A in TMEM (lane = token); value
+//   decoders (8 or 16 warps; the second eight take every other tile)
+//                         key codes -> fp16 A in TMEM (lane = token); value
 //                         codes -> fp16 V in shared memory;
 //   two MMA warps         S = A W^T, and O += V^T P;
-//   softmax (2 groups of 4 warps, each half of the rows' columns; lane = token)
+//   softmax (2 groups of 4 warps; lane = token)
 //                         S -> P in fp16 in shared memory, sums of P in fp32.
+// Jobs of up to 64 rows: the softmax groups take alternate tiles, each with its
+// own references, sums and O, which the combine joins.  Jobs of 128 rows: TMEM
+// does not hold two O, so the groups take half of the columns each.
 //
 // Precision.  Codes are exact in fp16 (centred codes up to 128, int8 values).
 // Centroids are rounded to fp16 after a common scale, chosen at init so that
@@ -44,25 +48,43 @@ using namespace sm100;
 namespace {
 
 constexpr int kTile = kTreeTile;
-constexpr int kSoftWarps = 8, kDecWarps = 8;
-constexpr int kProdWarp = kSoftWarps + kDecWarps;
-constexpr int kScoreWarp = kProdWarp + 1, kSumWarp = kProdWarp + 2;
-// 20 warps: setmaxnreg works on whole groups of four
-constexpr int kThreads = (kProdWarp + 4) * 32;
-constexpr int kDecThreads = kDecWarps * 32;
-// registers per thread: the launch gives 96; producer and MMA warps, decoders
-// and softmax groups then hold 48, 72 and 144 (128 (48 + 2 72 + 2 144) = 640 96)
-constexpr int kLaunchRegs = 96, kCtlRegs = 48, kDecRegs = 72, kSoftRegs = 144;
-static_assert(128 * (kCtlRegs + 2 * kDecRegs + 2 * kSoftRegs) <= kThreads * kLaunchRegs,
-              "register split exceeds the launch's registers");
+constexpr int kSoftWarps = 8;      // two softmax groups of four warps
+constexpr int kGroupWarps = 8;     // warps of a decoder group
 constexpr int kMaxNS = 4;          // row stages
-constexpr int kDecBar = 1;         // named barriers: decoders; 2, 3: softmax groups
+// Side words (norms and scales of a tile) stay until the softmax has read them:
+// a tile's stage is loaded once the decoders are done with the tile kMaxNS
+// before, whose keys they decoded after the scores of the tile two before that
+// were issued, which waited for the softmax to have read S two tiles earlier;
+// so eight entries are never overwritten too soon.
+constexpr int kSideRing = 8;
+static_assert(kSideRing >= kMaxNS + 4, "side words overwritten before they are read");
+constexpr int kSoftBar = 1, kDecBar = 3;  // named barriers: softmax groups 1, 2; decoder groups 3, 4
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSet = 6.f;        // a reference is set this far below the maximum (log2)
 constexpr float kMove = 12.f;      // and moves when a score lies this far above it
 
+// Roles by warp: softmax 0..7, decoders 8.., then producer, S and O issuers and
+// one idle warp (setmaxnreg works on whole groups of four).  Up to 32 columns a
+// thread, two decoder groups take alternate tiles; 64 columns a thread need
+// the registers of the second group.  The registers of the launch
+// (65536 / threads, rounded down to 8) are split among the roles; ptxas is held
+// to them by the launch bounds and the host checks that it used them all.
+template <int NC>
+struct Roles {
+  static constexpr int dec_groups = NC <= 32 ? 2 : 1;
+  static constexpr int prod = kSoftWarps + dec_groups * kGroupWarps;
+  static constexpr int score = prod + 1, sum = prod + 2;
+  static constexpr int threads = (prod + 4) * 32;
+  static constexpr int launch_regs = 65536 / threads / 8 * 8;
+  static constexpr int ctl_regs = NC <= 32 ? 56 : 64;
+  static constexpr int dec_regs = NC <= 32 ? 56 : 72;
+  static constexpr int soft_regs = NC <= 32 ? 112 : 136;
+  static_assert(128 * (ctl_regs + 2 * dec_groups * dec_regs + 2 * soft_regs) <= threads * launch_regs,
+                "register split exceeds the launch's registers");
+};
+
 struct Shape {
-  int nc, nwg, n;        // columns of a softmax group, groups, columns (nc nwg)
+  int nc, halves, n;     // columns of a softmax thread; 2: the groups split the columns, 1: the tiles
   int K, KC;             // K of the score product, its 8-value chunks
   int mt;                // 128-channel tiles of O
   int a_cols, s_col, o_col, cols;  // TMEM layout
@@ -226,10 +248,23 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The larger of three (one instruction).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
+}
+// The same in one instruction (NaN only where every lane has NaN).
+__device__ __forceinline__ float warp_max_redux(float v) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
+  return y;
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -266,6 +301,26 @@ struct Walk {
   }
 };
 
+// A group's segment and place in the run, kept in shared memory so that they
+// take no registers in its loop; one thread of the group walks.
+struct Place {
+  Segment g;
+  int64_t at;
+  int more;            // 0: the run is at its end
+  // softmax
+  int plain0, plain1;  // tiles that hold visible context alone
+  int first;
+  const uint8_t* mask;
+  int scaled;          // some row's key weights were beyond fp16's range
+  int Pk, Pv;          // decoders: row bytes
+  __device__ void next(const TreeArgs& t, int H) {
+    Walk w(t);
+    w.at = at;
+    more = w.next(t, H, g);
+    at = w.at;
+  }
+};
+
 // Position in a ring of n buffers; next() moves on one use.
 struct Ring {
   int n, slot;
@@ -278,88 +333,107 @@ struct Ring {
 
 // Wait for a phase.  Once a wait of any role has run out (2 s) every further
 // wait returns at once, so that all roles walk to their ends and the named
-// barriers stay matched; the results are then undefined and the error word says so.
+// barriers stay matched; the results are then undefined and the error word says
+// so.  The first try may sleep in hardware: most waits need no second one.
 __device__ __forceinline__ void wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return;
+  if (mbar_try_wait_sleep(bar, parity, 1000000u)) return;
   const uint64_t t0 = global_timer_ns();
   while (!*abort_flag) {
-    if (mbar_try_wait_sleep(bar, parity, 100000u)) return;
+    if (mbar_try_wait_sleep(bar, parity, 1000000u)) return;
     if (global_timer_ns() - t0 > kWaitNs) *abort_flag = 1;
   }
 }
 
-template <int KMODE, int VMODE, int NC>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int KMODE, int VMODE, int NC, bool HALVES>
+__global__ void __launch_bounds__(Roles<NC>::threads, 1)
     tree_tc_kernel(const Params kp, const Params vp, const TreeArgs t, const Shape z) {
+  using R = Roles<NC>;
   constexpr bool VU = VMODE == KVC_MODE_UNIFORM;
-  constexpr int CH = NC < 32 ? NC : 32;  // columns handled at a time
+  constexpr int N = HALVES ? 2 * NC : NC;  // columns
+  constexpr int CH = NC < 32 ? NC : 32;    // columns handled at a time
   constexpr int NCH = NC / CH;
+  constexpr int DG = R::dec_groups;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t row_full[kMaxNS], row_empty[kMaxNS], a_full[2], a_empty[2], v_full[2],
-      v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], w_full, done_bar;
-  __shared__ uint32_t kch[32], vch[32];
+      v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], side_full[kSideRing], w_full, w_empty, done_bar;
+  __shared__ uint32_t kch[DG][32], vch[DG][32];  // chunk tables of the decoder groups
   // per softmax group and column: offset of the score (c1 - m), m, rescale
   // factor, seen a token; the warps' partial results
-  __shared__ __align__(16) float cneg[2][64];
-  __shared__ float mref[2][64], corr[2][64], red[2][4][64];
-  __shared__ int seen[2][64];
+  __shared__ __align__(16) float cneg[2][NC];
+  __shared__ float mref[2][NC], wscale[2][NC], corr[2][NC], red[2][4][NC];
+  __shared__ int seen[2][NC];
+  __shared__ Place place[2 + DG];  // softmax groups, decoder groups
+  __shared__ __align__(16) unsigned short side_s[kSideRing][2][kTile];  // norms, scales
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  unsigned char* Ws = smem;  // two pieces [n x K] fp16, K-major cores
+  unsigned char* Ws = smem;  // two pieces [N x K] fp16, K-major cores
   unsigned char* Ps = smem + z.off_p;
   unsigned char* Vs = smem + z.off_v;
   unsigned char* Rs = smem + z.off_stage;
   uint32_t* tab = reinterpret_cast<uint32_t*>(smem + z.off_tab);  // codebooks of 16 or 256 levels
-  const int w_piece = z.n * z.K * 2;
+  const int w_piece = N * z.K * 2;
+  constexpr int p_bytes = kTile * N * 2;  // P: one buffer per group, or one of both halves
   const int v_bytes = z.mt * kTile * 256;
 
-  if (warp == kScoreWarp) tmem_alloc(&tmem_base, z.cols);
+  if (warp == R::score) tmem_alloc(&tmem_base, z.cols);
   if (tid == 0) {
-    for (int i = 0; i < z.ns; ++i) { mbar_init(&row_full[i], 1); mbar_init(&row_empty[i], kDecWarps); }
+    for (int i = 0; i < z.ns; ++i) { mbar_init(&row_full[i], 1); mbar_init(&row_empty[i], kGroupWarps); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&a_full[i], kDecWarps);
+      mbar_init(&a_full[i], kGroupWarps);
       mbar_init(&a_empty[i], 1);
-      mbar_init(&v_full[i], kDecWarps);
+      mbar_init(&v_full[i], kGroupWarps);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], z.nwg * 4);
+      mbar_init(&s_empty[i], HALVES ? 8 : 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&p_empty[i], 1);
     }
-    mbar_init(&w_full, z.nwg);
+    for (int i = 0; i < kSideRing; ++i) mbar_init(&side_full[i], 1);
+    mbar_init(&w_full, 1);
+    mbar_init(&w_empty, 1);
     mbar_init(&done_bar, 2);
     fence_mbar_init();
     abort_flag = 0;
   }
+  if (tid < 2 + DG) place[tid].at = Walk(t).at;
   if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits >= 4) {  // pairs of 16 levels, or 256 levels
     const int pair = kp.cb_bits == 4;
     auto half_of = [&](int c) {
       return (uint32_t)__half_as_ushort(__float2half_rn(kp.codebook[c] * t.cb_mul));
     };
-    for (int j = tid; j < 256; j += kThreads)
+    for (int j = tid; j < 256; j += R::threads)
       tab[j] = pair ? half_of(j & 15) | (half_of(j >> 4) << 16) : half_of(j);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_base;
-  Walk walk(t);
-  Segment g;
   grid_dependency_wait();  // the key weights come from the launch before
 
-  if (warp >= kProdWarp) {
-    regs_dec<kCtlRegs>();
-    if (warp == kProdWarp && lane == 0) {
+  if (warp >= R::prod) {
+    regs_dec<R::ctl_regs>();
+    if (warp == R::prod && lane == 0) {
       // ---------------------------------------------------------- producer
+      Walk walk(t);
+      Segment g;
       Ring rr(z.ns);
-      int issued = 0;
+      int issued = 0, segs = 0;
       while (walk.next(t, kp.H, g)) {
+        if (g.tile0 == g.tile1) continue;
+        // the job's key weights, once the last segment's scores are done
+        if (segs) wait_or_abort(&w_empty, (segs - 1) & 1, &abort_flag);
+        if (abort_flag) break;
+        mbar_arrive_expect_tx(&w_full, 2 * w_piece);
+        bulk_load(Ws, t.w16 + (size_t)g.job * 2 * N * z.K, 2 * w_piece, &w_full);
+        ++segs;
         const int Pk = kp.P[kp.basis_of[g.slot]];
         const int Pv = VU ? vp.P[vp.basis_of[g.slot]] : vp.D;
         const unsigned char* ks = kp.store + kp.pay_off[g.slot];
         const unsigned char* vs = vp.store + vp.pay_off[g.slot];
+        const unsigned char* kn = kp.store + kp.side_off[g.slot];
+        const unsigned char* vsc = vp.store + vp.side_off[g.slot];
         for (int tile = g.tile0; tile < g.tile1; ++tile, ++issued, rr.next()) {
           if (issued >= z.ns) wait_or_abort(&row_empty[rr.slot], rr.phase ^ 1u, &abort_flag);
           if (abort_flag) break;
@@ -370,19 +444,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&row_full[rr.slot], kb + vb);
           if (kb) bulk_load(st, ks + t0 * Pk, kb, &row_full[rr.slot]);
           if (vb) bulk_load(st + z.krow, vs + t0 * Pv, vb, &row_full[rr.slot]);
+          const int sd = issued & (kSideRing - 1);
+          const uint32_t sb = (uint32_t)((2 * n + 15) & ~15);
+          mbar_arrive_expect_tx(&side_full[sd], (KMODE == KVC_MODE_CODEBOOK ? sb : 0) + (VU ? 0 : sb));
+          if (KMODE == KVC_MODE_CODEBOOK) bulk_load(side_s[sd][0], kn + t0 * 2, sb, &side_full[sd]);
+          if (!VU) bulk_load(side_s[sd][1], vsc + t0 * 2, sb, &side_full[sd]);
         }
         if (abort_flag) break;
       }
       // copies still in flight (after a time-out) land before the CTA exits
+      if (segs) mbar_wait_bounded(&w_full, (segs - 1) & 1, kWaitNs);
       for (int j = max(0, issued - z.ns); j < issued; ++j)
         mbar_wait_bounded(&row_full[j % z.ns], (j / z.ns) & 1, kWaitNs);
-    } else if (warp == kScoreWarp) {
+      for (int j = max(0, issued - kSideRing); j < issued; ++j)
+        mbar_wait_bounded(&side_full[j & (kSideRing - 1)], (j / kSideRing) & 1, kWaitNs);
+    } else if (warp == R::score) {
       // ---------------------------------------------------------- S = A W^T
       // The whole warp walks and waits, one elected lane issues, so that
       // descriptors stay in uniform registers; the two products have a warp
       // each.  (One lane walking and issuing both took 160 cycles per MMA.)
+      Walk walk(t);
+      Segment g;
       const bool leader = elect_one();
-      const uint32_t id = idesc_f16(kTile, z.n, 0);
+      constexpr uint32_t id = idesc_f16(kTile, N, 0);
       const uint64_t w_desc = desc_kmajor_noswizzle(smem_u32(Ws), 128, (uint32_t)z.KC * 128);
       int it = 0, segs = 0;
       while (walk.next(t, kp.H, g)) {
@@ -396,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tc_fence_after();
           if (leader) {
-            const uint32_t a0 = tm + s * z.a_cols, d0 = tm + z.s_col + s * z.n;
+            const uint32_t a0 = tm + s * z.a_cols, d0 = tm + z.s_col + s * N;
             umma_f16_tmem_a(d0, a0, w_desc, id, 0u);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {  // the two pieces of W
@@ -407,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             umma_commit(&s_full[s]);
             umma_commit(&a_empty[s]);
+            if (tile + 1 == g.tile1) umma_commit(&w_empty);
           }
           __syncwarp();
         }
@@ -416,34 +501,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(&done_bar, 0, kWaitNs);
       }
       __syncwarp();
-    } else if (warp == kSumWarp) {
+    } else if (warp == R::sum) {
       // ---------------------------------------------------------- O += V^T P
-      // One product over both groups' columns, or, where the groups hold 64
-      // each, one per group as its weights arrive.
+      // One product per tile, or, where the groups split the columns, one per
+      // group as its weights arrive.
+      Walk walk(t);
+      Segment g;
       const bool leader = elect_one();
-      const int parts = NC == 64 ? z.nwg : 1;
-      const uint32_t pn = NC == 64 ? NC : z.n;
-      const uint32_t id = idesc_f16(kTile, pn, 0) | kTransposeAB;
-      const uint32_t v_k = (uint32_t)z.mt * 2048, p_k = (uint32_t)z.n * 16;
+      constexpr uint32_t id = idesc_f16(kTile, NC, 0) | kTransposeAB;
+      constexpr uint32_t p_k = N * 16;  // bytes between P's cores along the tokens
+      const uint32_t v_k = (uint32_t)z.mt * 2048;
       const uint64_t v_desc = desc_mnmajor(smem_u32(Vs), v_k, 128);
       const uint64_t p_desc = desc_mnmajor(smem_u32(Ps), p_k, 128);
-      const uint64_t v_step = (2 * v_k) >> 4, p_step = (2 * p_k) >> 4;
+      const uint64_t v_step = (2 * v_k) >> 4;
+      constexpr uint64_t p_step = (2 * p_k) >> 4;
       int it = 0;
       Ring rv(z.nv);
       while (walk.next(t, kp.H, g)) {
         for (int tile = g.tile0; tile < g.tile1; ++tile, ++it, rv.next()) {
           wait_or_abort(&v_full[rv.slot], rv.phase, &abort_flag);
-          for (int h = 0; h < parts; ++h) {
-            for (int wg = h; wg < (parts == 1 ? z.nwg : h + 1); ++wg)
-              wait_or_abort(&p_full[wg], it & 1, &abort_flag);
+#pragma unroll
+          for (int h = 0; h < (HALVES ? 2 : 1); ++h) {
+            const int wg = HALVES ? h : it & 1;
+            wait_or_abort(&p_full[wg], (HALVES ? it : it >> 1) & 1, &abort_flag);
             __syncwarp();
             tc_fence_after();
             if (leader) {
+              // the group's first tile of the segment overwrites its O
+              const uint32_t add = tile - g.tile0 >= (HALVES ? 1 : 2) ? 1u : 0u;
               for (int m = 0; m < z.mt; ++m) {
-                const uint32_t o = tm + z.o_col + m * z.n + h * pn;
+                const uint32_t o = tm + z.o_col + (HALVES ? m * N + h * NC : (wg * z.mt + m) * N);
                 uint64_t vd = v_desc + ((rv.slot * v_bytes + m * 2048) >> 4);
-                uint64_t pd = p_desc + h * (NC / 8 * 128 >> 4);
-                umma_f16(o, vd, pd, id, tile > g.tile0 ? 1u : 0u);
+                uint64_t pd = p_desc + ((HALVES ? h * (NC / 8 * 128) : wg * p_bytes) >> 4);
+                umma_f16(o, vd, pd, id, add);
 #pragma unroll
                 for (int ks = 1; ks < kTile / 16; ++ks) {
                   vd += v_step;
@@ -451,8 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   umma_f16(o, vd, pd, id, 1u);
                 }
               }
-              for (int wg = h; wg < (parts == 1 ? z.nwg : h + 1); ++wg) umma_commit(&p_empty[wg]);
-              if (h == parts - 1) umma_commit(&v_empty[rv.slot]);
+              umma_commit(&p_empty[wg]);
+              if (!HALVES || h == 1) umma_commit(&v_empty[rv.slot]);
             }
             __syncwarp();
           }
@@ -466,15 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kSoftWarps) {
     // ------------------------------------------------------------ decoders
-    regs_dec<kDecRegs>();
-    const int dtid = tid - kSoftWarps * 32;
+    regs_dec<R::dec_regs>();
+    const int grp = (warp - kSoftWarps) / kGroupWarps;
+    const int dtid = tid - (kSoftWarps + grp * kGroupWarps) * 32;
     const int tt = dtid & (kTile - 1), half = dtid >> 7;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     // values: eight lanes take eight tokens of one block, each another chunk of
     // the row, so that neither the reads (rows 128 bytes apart) nor the writes
     // (cores 128 bytes apart) meet in a bank
     const int octet = lane >> 3, t8 = lane & 7;
-    const int vblk = (warp - kSoftWarps) * 2 + (octet >> 1);
+    const int vblk = (dtid >> 5) * 2 + (octet >> 1);
     Levels levels{};
     if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits <= 3) {
       uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
@@ -489,19 +580,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     Ring rr(z.ns), rv(z.nv);
     int it = 0;
-    while (walk.next(t, kp.H, g)) {
-      if (g.tile0 == g.tile1) continue;
-      const int kbeta = kp.basis_of[g.slot], vbeta = VU ? vp.basis_of[g.slot] : 0;
-      named_bar_sync(kDecBar, kDecThreads);  // the last segment's tables have been read
-      if (dtid < 32) kch[dtid] = chunk_entry(kp, kbeta, dtid);
-      else if (VU && dtid < 64) vch[dtid - 32] = chunk_entry(vp, vbeta, dtid - 32);
-      named_bar_sync(kDecBar, kDecThreads);
-      const int Pk = kp.P[kbeta], Pv = VU ? vp.P[vbeta] : vp.D;
+    Place& pl = place[2 + grp];
+    for (;;) {
+      named_bar_sync(kDecBar + grp, kGroupWarps * 32);  // the last segment's tables have been read
+      if (dtid == 0) {
+        pl.next(t, kp.H);
+        if (pl.more) {
+          pl.Pk = kp.P[kp.basis_of[pl.g.slot]];
+          pl.Pv = VU ? vp.P[vp.basis_of[pl.g.slot]] : vp.D;
+        }
+      }
+      named_bar_sync(kDecBar + grp, kGroupWarps * 32);
+      if (!pl.more) break;
+      if (dtid < 32) kch[grp][dtid] = chunk_entry(kp, kp.basis_of[pl.g.slot], dtid);
+      else if (VU && dtid < 64) vch[grp][dtid - 32] = chunk_entry(vp, vp.basis_of[pl.g.slot], dtid - 32);
+      named_bar_sync(kDecBar + grp, kGroupWarps * 32);
+      const int Pk = pl.Pk, Pv = pl.Pv;
       int nv = VU ? 0 : vp.D / 8;  // chunks of a value row
       if (VU)
-        while (nv < 32 && vch[nv]) ++nv;
+        while (nv < 32 && vch[grp][nv]) ++nv;
       const int vhalf = (nv + 1) / 2;
-      for (int tile = g.tile0; tile < g.tile1; ++tile, ++it, rr.next(), rv.next()) {
+      const int tile1 = pl.g.tile1;
+      for (int tile = pl.g.tile0; tile < tile1; ++tile, ++it, rr.next(), rv.next()) {
+        if (DG == 2 && (it & 1) != grp) continue;
         const int a = it & 1;
         wait_or_abort(&row_full[rr.slot], rr.phase, &abort_flag);
         if (it >= 2) wait_or_abort(&a_empty[a], ((it >> 1) - 1) & 1, &abort_flag);
@@ -515,9 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           else if (W == 2) codebook64<2>(src, levels, a_tm + half * 32);
           else codebook64<1>(src, levels, a_tm + half * 32);
         } else {
-#pragma unroll 4
           for (int c = half; c < z.KC; c += 2) {
-            const uint32_t ent = kch[c];
+            const uint32_t ent = kch[grp][c];
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (ent) {
               const int w = (int)(ent >> 16);
@@ -561,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               while (c >= nv) c -= nv;
               uint4 v;
               if (VU) {
-                const uint32_t ent = vch[c];
+                const uint32_t ent = vch[grp][c];
                 v = centred_codes(bits_at(raw, tok * Pv + (int)(ent & 0xffffu)), (int)(ent >> 16));
               } else {
                 v = int8_values(*reinterpret_cast<const uint2*>(raw + tok * Pv + c * 8));
@@ -578,255 +678,272 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < z.nwg * 4) {
+  } else {
     // ------------------------------------------------------------ softmax
-    regs_inc<kSoftRegs>();
-    const int wg = warp >> 2, quarter = warp & 3, ltid = tid & 127, bar = 2 + wg;
+    regs_inc<R::soft_regs>();
+    const int wg = warp >> 2, quarter = warp & 3, ltid = tid & 127, bar = kSoftBar + wg;
+    const int lt = quarter * 32 + lane;  // this lane's token of a tile
+    const int col0 = HALVES ? wg * NC : 0;  // the group's first column
+    constexpr int kStep = HALVES ? 1 : 2;   // tiles between two of the group's
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t o_tm = tm + lane_off + z.o_col + wg * NC;
+    const uint32_t o_tm = tm + lane_off + z.o_col + (HALVES ? col0 : wg * z.mt * N);
     float* cn = cneg[wg];
-    unsigned char* pst = Ps + ((quarter * 32 + lane) >> 3) * (z.n * 16) + wg * (NC / 8 * 128) + (lane & 7) * 16;
-    int it = 0;
-    while (walk.next(t, kp.H, g)) {
-      const int64_t first = t.first ? max(t.first[g.b], 0) : 0;
-      const int col0 = wg * NC, ncol = max(0, min(NC, g.nr - col0));  // rows of this group
-      const size_t row0 = (size_t)g.slot * t.rows + g.r0 + col0;
-      float post = 1.f;
-      named_bar_sync(bar, 128);  // the last segment's column state has been read
+    unsigned char* pst = Ps + (HALVES ? 0 : wg * p_bytes) + (lt >> 3) * (N * 16) + col0 * 16 + (lane & 7) * 16;
+    int it = 0;  // tiles of the run before the segment
+    Place& pl = place[wg];
+    for (;;) {
+      named_bar_sync(bar, 128);  // the last segment's state has been read
+      if (ltid == 0) {
+        pl.next(t, kp.H);
+        if (pl.more) {
+          const int first = t.first ? max(t.first[pl.g.b], 0) : 0;
+          pl.first = first;
+          pl.plain0 = (int)min(t.tps, ((int64_t)first + kTile - 1) / kTile);
+          pl.plain1 = (int)(t.ctx / kTile);
+          pl.mask = t.mask ? t.mask + pl.g.b * t.mask_sb : nullptr;
+        }
+      }
+      named_bar_sync(bar, 128);
+      if (!pl.more) break;
+      const int ncol = max(0, min(NC, pl.g.nr - col0));  // rows of this group
+      bool big = false;
       if (ltid < NC) {
-        cn[ltid] = ltid < ncol ? t.c1[row0 + ltid] : 0.f;
+        const size_t row = (size_t)pl.g.slot * t.prow + pl.g.r0 + col0 + ltid;
+        cn[ltid] = t.c1[row];
+        wscale[wg][ltid] = t.wscale[row];
+        big = t.wscale[row] != 1.f;
         mref[wg][ltid] = 0.f;
         seen[wg][ltid] = ltid >= ncol;
       }
-      if (g.tile0 < g.tile1) {
-        // key weights as two fp16 pieces, scaled into fp16's range by a power of two
-        const float* w = t.w + row0 * t.NCk;
-        float mx = 0.f;
-        for (int e = ltid; e < ncol * t.NCk; e += 128) {
-          const float v = fabsf(w[e]);
-          if (v <= 3.4e38f) mx = fmaxf(mx, v);
-        }
-        mx = warp_max(mx) * t.w_mul;
-        if (lane == 0) red[wg][quarter][0] = mx;
-        named_bar_sync(bar, 128);
-        mx = fmaxf(fmaxf(red[wg][0][0], red[wg][1][0]), fmaxf(red[wg][2][0], red[wg][3][0]));
-        const int ex = max(0, (__float_as_int(mx) >> 23) - 127 - 13);
-        post = __int_as_float((127 + ex) << 23);
-        const float pre = t.w_mul * __int_as_float((127 - ex) << 23);
-        for (int e = ltid; e < NC * z.KC; e += 128) {
-          const int r = e / z.KC, c = e - r * z.KC;
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = 0.f;
-          if (r < ncol && c * 8 < t.NCk) {
-            const float4* src = reinterpret_cast<const float4*>(w + (size_t)r * t.NCk + c * 8);
-            const float4 a = src[0], b = src[1];
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-          }
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i] * pre, b = x[2 * i + 1] * pre;
-            hi[i] = pack_half2(a, b);
-            const __half2 h = *reinterpret_cast<const __half2*>(&hi[i]);
-            lo[i] = pack_half2(a - __low2float(h), b - __high2float(h));
-          }
-          unsigned char* dst = Ws + ((col0 + r) >> 3) * (z.KC * 128) + c * 128 + (r & 7) * 16;
-          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(dst + w_piece) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        fence_proxy_async_smem();
-        named_bar_sync(bar, 128);
-        if (ltid == 0) mbar_arrive(&w_full);
-      }
-      const uint8_t* mask = t.mask ? t.mask + g.b * t.mask_sb : nullptr;
+      const bool scaled = named_bar_or(bar, 128, big);
+      if (ltid == 0) pl.scaled = scaled;
       float2 l[NC / 2];
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) l[i] = make_float2(0.f, 0.f);
-      uint32_t unseen = ncol ? (1u << NCH) - 1u : 0u;  // column chunks with rows that saw nothing yet
       float sref = VU ? 1.f : 0.f, inv_sref = VU ? 1.f : 0.f;
-      const int lt = quarter * 32 + lane;
-      // this lane's norm and scale, loaded one tile ahead and converted at use
-      // (converting them at the load would wait for it)
-      const unsigned short* knorm = reinterpret_cast<const unsigned short*>(kp.store + kp.side_off[g.slot]);
-      const unsigned short* vscale = reinterpret_cast<const unsigned short*>(vp.store + vp.side_off[g.slot]);
-      const int live_tiles = (int)((t.S - lt + kTile - 1) / kTile);  // tiles in which this lane has a token
-      const unsigned short* kn = knorm + (int64_t)g.tile0 * kTile + lt;
-      const unsigned short* vsc = vscale + (int64_t)g.tile0 * kTile + lt;
-      unsigned short nt_next = 0, st_next = 0;
-      if (g.tile0 < g.tile1 && g.tile0 < live_tiles) {
-        if (KMODE == KVC_MODE_CODEBOOK) nt_next = *kn;
-        if (!VU) st_next = *vsc;
-      }
-      // tiles [plain0, plain1) hold visible context alone
-      const int plain0 = (int)min((int64_t)t.tps, (first + kTile - 1) / kTile), plain1 = (int)(t.ctx / kTile);
-      for (int tile = g.tile0; tile < g.tile1; ++tile, ++it) {
-        const int s = it & 1;
-        const float nt = KMODE == KVC_MODE_CODEBOOK ? __half2float(__ushort_as_half(nt_next)) * post : post;
-        const float st = VU ? 1.f : __half2float(__ushort_as_half(st_next));
-        kn += kTile;
-        vsc += kTile;
-        if (tile + 1 < g.tile1 && tile + 1 < live_tiles) {  // the next tile's norms and scales
-          if (KMODE == KVC_MODE_CODEBOOK) nt_next = *kn;
-          if (!VU) st_next = *vsc;
-        } else {
-          nt_next = st_next = 0;
-        }
-        // which of the group's rows see this lane's token
-        const bool special = tile < plain0 || tile >= plain1;
-        uint64_t vis = ~0ull;
-        if (special) {
-          const int64_t tok = (int64_t)tile * kTile + lt, draft = tok - t.ctx;
-          if (draft < 0) {
-            vis = tok >= first ? ~0ull : 0ull;
-          } else {
-            vis = 0ull;
-            if (draft < t.N) {
-              int n = (g.r0 + col0) % t.N;
-              for (int c = 0; c < ncol; ++c) {
-                if (mask ? mask[(int64_t)n * t.N + draft] != 0 : draft <= n) vis |= 1ull << c;
-                if (++n == t.N) n = 0;
-              }
-            }
-          }
-        }
-        bool up = !VU && vis != 0ull && st > 4.f * sref && st <= 65504.f;
-        float su = 0.f;
-        wait_or_abort(&s_full[s], (it >> 1) & 1, &abort_flag);
-        __syncwarp();
-        tc_fence_after();
-#pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-          float2 x[CH / 2];
-          bool moved = false;
-          for (;;) {
-            uint32_t r[CH];
-            tmem_ld_n<CH>(tm + lane_off + z.s_col + s * z.n + col0 + ch * CH, r);
-            tmem_wait_ld();
-            const float2 nt2 = make_float2(nt, nt);
-            float mx = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < CH / 4; ++i) {
-              const float4 c = reinterpret_cast<const float4*>(cn + ch * CH)[i];
-              x[2 * i] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), nt2,
-                                    make_float2(c.x, c.y));
-              x[2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])),
-                                        nt2, make_float2(c.z, c.w));
-            }
-            if (special) {
-              const uint32_t v = (uint32_t)(vis >> (ch * CH));
-#pragma unroll
-              for (int i = 0; i < CH / 2; ++i) {
-                if (!(v >> (2 * i) & 1u)) x[i].x = -INFINITY;
-                if (!(v >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i) mx = fmaxf(mx, fmaxf(x[i].x, x[i].y));
-            if (moved || !named_bar_or(bar, 128, mx > kMove || up || (unseen >> ch & 1u))) break;
-            moved = true;
-            // The references move (rare).  Every thread of the group is here.
-            float ratio = 1.f;
-            if (!VU) {  // the value scales' reference: the next power of two
-              const float m = warp_max(up ? st : 0.f);
-              if (lane == 0) red[wg][quarter][0] = m;
-              named_bar_sync(bar, 128);
-              const float big = fmaxf(fmaxf(red[wg][0][0], red[wg][1][0]), fmaxf(red[wg][2][0], red[wg][3][0]));
-              if (big > 0.f) {
-                const float to = __int_as_float((__float_as_int(big) & 0x7f800000) + 0x00800000);
-                ratio = sref / to;
-                sref = to;
-                inv_sref = 1.f / to;
-              }
-              up = false;
-              named_bar_sync(bar, 128);
-            }
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i) {
-              const float a = warp_max(x[i].x), b = warp_max(x[i].y);
-              if (lane == 0) {
-                red[wg][quarter][2 * i] = a;
-                red[wg][quarter][2 * i + 1] = b;
-              }
-            }
-            named_bar_sync(bar, 128);
-            bool blind = false;
-            if (ltid < CH) {
-              const int c = ch * CH + ltid;
-              const float m = fmaxf(fmaxf(red[wg][0][ltid], red[wg][1][ltid]),
-                                    fmaxf(red[wg][2][ltid], red[wg][3][ltid]));
-              float d = 0.f, f = 1.f;
-              if (m != -INFINITY) {  // (a row of NaN counts as seen and stays NaN)
-                if (!seen[wg][c]) {  // nothing summed yet
-                  d = m - kSet;
-                  f = 0.f;
-                  seen[wg][c] = 1;
-                } else if (m > kSet) {
-                  d = m - kSet;
-                  f = ex2(-d);
-                }
-              }
-              mref[wg][c] += d;
-              cn[c] -= d;
-              corr[wg][c] = f;
-              blind = !seen[wg][c];
-            }
-            if (!named_bar_or(bar, 128, blind)) unseen &= ~(1u << ch);
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i) {
-              l[ch * CH / 2 + i].x *= corr[wg][ch * CH + 2 * i];
-              l[ch * CH / 2 + i].y *= corr[wg][ch * CH + 2 * i + 1];
-            }
-            if (tile > g.tile0) {  // O holds sums: rescale it once the last product is done
-              wait_or_abort(&p_empty[wg], (it - 1) & 1, &abort_flag);
-              __syncwarp();
-              tc_fence_after();
-              for (int m = 0; m < z.mt; ++m)
-                for (int c = 0; c < NC; c += 16) {
-                  const bool mine = c >= ch * CH && c < ch * CH + CH;
-                  if (!mine && ratio == 1.f) continue;
-                  uint32_t o[16];
-                  tmem_ld16(o_tm + m * z.n + c, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    o[i] = __float_as_uint(__uint_as_float(o[i]) * (mine ? corr[wg][c + i] * ratio : ratio));
-                  tmem_st16(o_tm + m * z.n + c, o);
-                }
-              tmem_wait_st();
-            }
-            named_bar_sync(bar, 128);  // corr and red have been read
-          }
-          if (ch == 0) {
-            su = vis != 0ull ? st * inv_sref : 0.f;
-            if (it > 0) wait_or_abort(&p_empty[wg], (it - 1) & 1, &abort_flag);  // P has been read
-            __syncwarp();
-          }
-          if (ch == NCH - 1) {  // S has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[s]);
-          }
+      // the group's tiles of the segment, and its tiles of the run before them
+      const int tile_first = pl.g.tile0 + (HALVES ? 0 : (it ^ wg) & 1);
+      int j = HALVES ? it : (it + 1 - wg) >> 1;
+      // tiles [fast0, fast1) hold visible context alone; column chunks with rows
+      // that saw nothing yet, or scaled rows, keep every tile on the general path
+      uint32_t unseen = ncol ? (1u << NCH) - 1u : 0u;
+      int fast0 = pl.plain0, fast1 = unseen || scaled ? 0 : pl.plain1;
+      const int tile1 = pl.g.tile1;
+      for (int tile = tile_first; tile < tile1; tile += kStep, ++j) {
+        const int s = HALVES ? j & 1 : wg;             // S buffer, and its phase
+        const uint32_t s_par = (HALVES ? j >> 1 : j) & 1;
+        const uint32_t s_tm = tm + lane_off + z.s_col + s * N + col0;
+        const int gt = HALVES ? j : 2 * j + wg;        // the tile's number in the run
+        const int sd = gt & (kSideRing - 1);
+        wait_or_abort(&side_full[sd], (gt / kSideRing) & 1, &abort_flag);
+        float nt = KMODE == KVC_MODE_CODEBOOK ? __half2float(__ushort_as_half(side_s[sd][0][lt])) : 1.f;
+        const float st = VU ? 1.f : __half2float(__ushort_as_half(side_s[sd][1][lt]));
+        if (!VU && st != st) nt = st;  // a scale of NaN: the weights of those who see it
+        // weights of one chunk of columns into P and the sums; a hidden token's
+        // scale may be anything: its weights are 0 and stay 0 under any finite su
+        auto weigh = [&](int ch, float2 (&x)[CH / 2], float su) {
           const float2 su2 = make_float2(su, su);
 #pragma unroll
           for (int q = 0; q < CH / 8; ++q) {
             uint32_t h[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int j = 4 * q + i;
-              const float2 p = make_float2(ex2(x[j].x), ex2(x[j].y));
-              l[ch * CH / 2 + j] = __fadd2_rn(l[ch * CH / 2 + j], p);
-              float2 u = VU ? p : __fmul2_rn(p, su2);
-              if (!VU && special) {  // a hidden token's scale may be anything
-                const uint32_t v = (uint32_t)(vis >> (ch * CH));
-                if (!(v >> (2 * j) & 1u)) u.x = 0.f;
-                if (!(v >> (2 * j + 1) & 1u)) u.y = 0.f;
-              }
+              const int e = 4 * q + i;
+              const float2 p = make_float2(ex2(x[e].x), ex2(x[e].y));
+              l[ch * CH / 2 + e] = __fadd2_rn(l[ch * CH / 2 + e], p);
+              const float2 u = VU ? p : __fmul2_rn(p, su2);
               h[i] = pack_half2(u.x, u.y);
             }
             *reinterpret_cast<uint4*>(pst + (ch * CH / 8 + q) * 128) = make_uint4(h[0], h[1], h[2], h[3]);
           }
+        };
+        auto scores = [&](int ch, float2 (&x)[CH / 2], bool scale_rows) {  // S nt + c1 - m
+          uint32_t r[CH];
+          tmem_ld_n<CH>(s_tm + ch * CH, r);
+          tmem_wait_ld();
+          if (scale_rows) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              r[i] = __float_as_uint(__uint_as_float(r[i]) * wscale[wg][ch * CH + i]);
+          }
+          const float2 nt2 = make_float2(nt, nt);
+#pragma unroll
+          for (int i = 0; i < CH / 4; ++i) {
+            const float4 c = reinterpret_cast<const float4*>(cn + ch * CH)[i];
+            x[2 * i] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), nt2,
+                                  make_float2(c.x, c.y));
+            x[2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])),
+                                      nt2, make_float2(c.z, c.w));
+          }
+        };
+        auto release_scores = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[s]);
+        };
+        wait_or_abort(&s_full[s], s_par, &abort_flag);
+        __syncwarp();
+        tc_fence_after();
+        int done = 0;  // chunks of columns weighed
+        if (tile >= fast0 && tile < fast1) {
+#pragma unroll
+          for (int ch = 0; ch < NCH; ++ch) {
+            if (done == ch) {
+              float2 x[CH / 2];
+              scores(ch, x, false);
+              float mx = max3(x[0].x, x[0].y, -INFINITY);
+#pragma unroll
+              for (int i = 1; i < CH / 2; ++i) mx = max3(mx, x[i].x, x[i].y);
+              if (!named_bar_or(bar, 128, mx > kMove || (!VU && st > 4.f * sref))) {
+                if (ch == NCH - 1) release_scores();
+                if (ch == 0) {
+                  if (j > 0) wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);  // P has been read
+                  __syncwarp();
+                }
+                weigh(ch, x, fmaxf(fminf(st * inv_sref, 3e38f), -3e38f));
+                done = ch + 1;
+              }
+            }
+          }
+        }
+        if (done < NCH) {
+          // The general path: tokens hidden from some rows, and references that
+          // move.  Every thread of the group is here.
+          const int first = pl.first;
+          uint64_t vis = ~0ull;  // which of the group's rows see this lane's token
+          const bool special = tile < pl.plain0 || tile >= pl.plain1;
+          if (special) {
+            const int64_t tok = (int64_t)tile * kTile + lt, draft = tok - t.ctx;
+            if (draft < 0) {
+              vis = tok >= first ? ~0ull : 0ull;
+            } else {
+              vis = 0ull;
+              if (draft < t.N) {
+                const int nc = min(NC, pl.g.nr - col0), n0 = (pl.g.r0 + col0) % t.N;
+                if (pl.mask) {
+                  const uint8_t* col = pl.mask + draft;
+                  int n = n0;
+                  for (int c0 = 0; c0 < nc; c0 += 16) {  // sixteen loads in flight
+                    uint8_t m[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                      m[c] = c0 + c < nc ? col[(int64_t)n * t.N] : 0;
+                      if (++n == t.N) n = 0;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                      if (m[c]) vis |= 1ull << (c0 + c);
+                  }
+                } else {
+                  int n = n0;
+                  for (int c = 0; c < nc; ++c) {
+                    if (draft <= n) vis |= 1ull << c;
+                    if (++n == t.N) n = 0;
+                  }
+                }
+              }
+            }
+          }
+          bool up = !VU && vis != 0ull && st > 4.f * sref && st <= 65504.f;
+#pragma unroll
+          for (int ch = 0; ch < NCH; ++ch) {
+            if (ch < done) continue;
+            float2 x[CH / 2];
+            bool moved = false;
+            for (;;) {
+              scores(ch, x, pl.scaled != 0);
+              if (special) {
+                const uint32_t v = (uint32_t)(vis >> (ch * CH));
+#pragma unroll
+                for (int i = 0; i < CH / 2; ++i) {
+                  if (!(v >> (2 * i) & 1u)) x[i].x = -INFINITY;
+                  if (!(v >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
+                }
+              }
+              float mx = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < CH / 2; ++i) mx = max3(mx, x[i].x, x[i].y);
+              if (moved || !named_bar_or(bar, 128, mx > kMove || up || (unseen >> ch & 1u))) break;
+              moved = true;
+              float ratio = 1.f;
+              if (!VU) {  // the value scales' reference: the next power of two
+                const float m = warp_max(up ? st : 0.f);
+                if (lane == 0) red[wg][quarter][0] = m;
+                named_bar_sync(bar, 128);
+                const float most = fmaxf(fmaxf(red[wg][0][0], red[wg][1][0]), fmaxf(red[wg][2][0], red[wg][3][0]));
+                if (most > 0.f) {
+                  const float to = __int_as_float((__float_as_int(most) & 0x7f800000) + 0x00800000);
+                  ratio = sref / to;
+                  sref = to;
+                  inv_sref = 1.f / to;
+                }
+                up = false;
+                named_bar_sync(bar, 128);
+              }
+#pragma unroll
+              for (int i = 0; i < CH / 2; ++i) {
+                const float a = warp_max_redux(x[i].x), b = warp_max_redux(x[i].y);
+                if (lane == 0) {
+                  red[wg][quarter][2 * i] = a;
+                  red[wg][quarter][2 * i + 1] = b;
+                }
+              }
+              named_bar_sync(bar, 128);
+              bool blind = false;
+              if (ltid < CH) {
+                const int c = ch * CH + ltid;
+                const float m = fmaxf(fmaxf(red[wg][0][ltid], red[wg][1][ltid]),
+                                      fmaxf(red[wg][2][ltid], red[wg][3][ltid]));
+                float d = 0.f, f = 1.f;
+                if (m != -INFINITY) {  // (a row of NaN counts as seen and stays NaN)
+                  if (!seen[wg][c]) {  // nothing summed yet
+                    d = m - kSet;
+                    f = 0.f;
+                    seen[wg][c] = 1;
+                  } else if (m > kSet) {
+                    d = m - kSet;
+                    f = ex2(-d);
+                  }
+                }
+                mref[wg][c] += d;
+                cn[c] -= d;
+                corr[wg][c] = f;
+                blind = !seen[wg][c];
+              }
+              if (!named_bar_or(bar, 128, blind)) unseen &= ~(1u << ch);
+#pragma unroll
+              for (int i = 0; i < CH / 2; ++i) {
+                l[ch * CH / 2 + i].x *= corr[wg][ch * CH + 2 * i];
+                l[ch * CH / 2 + i].y *= corr[wg][ch * CH + 2 * i + 1];
+              }
+              if (tile != tile_first) {  // O holds sums: rescale it once the last product is done
+                wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);
+                __syncwarp();
+                tc_fence_after();
+                for (int m = 0; m < z.mt; ++m)
+                  for (int c = 0; c < NC; c += 16) {
+                    const bool mine = c >= ch * CH && c < ch * CH + CH;
+                    if (!mine && ratio == 1.f) continue;
+                    uint32_t o[16];
+                    tmem_ld16(o_tm + m * N + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                      o[i] = __float_as_uint(__uint_as_float(o[i]) * (mine ? corr[wg][c + i] * ratio : ratio));
+                    tmem_st16(o_tm + m * N + c, o);
+                  }
+                tmem_wait_st();
+              }
+              named_bar_sync(bar, 128);  // corr and red have been read
+            }
+            if (ch == NCH - 1) release_scores();
+            if (ch == 0) {
+              if (j > 0) wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);  // P has been read
+              __syncwarp();
+            }
+            weigh(ch, x, fmaxf(fminf(st * inv_sref, 3e38f), -3e38f));
+          }
+          if (!unseen && !pl.scaled) fast1 = pl.plain1;
         }
         fence_proxy_async_smem();  // P is read by the tensor core
         tc_fence_before();         // and O, where it was rescaled
@@ -834,12 +951,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[wg]);
       }
       // the partial: per row m, l and the weighted sums
-      const bool any = g.tile0 < g.tile1;
+      const bool any = tile_first < tile1;
       if (any) {
-        wait_or_abort(&p_empty[wg], (it - 1) & 1, &abort_flag);
+        wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);
         __syncwarp();
         tc_fence_after();
       }
+      it += tile1 - pl.g.tile0;
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) {
         const float a = warp_sum(l[i].x), b = warp_sum(l[i].y);
@@ -849,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       named_bar_sync(bar, 128);
-      const size_t prow = ((size_t)g.job + blockIdx.x) * t.rt + col0;
+      const size_t prow = (HALVES ? ((size_t)pl.g.job + blockIdx.x) : 2 * ((size_t)pl.g.job + blockIdx.x) + wg) * t.rt + col0;
       float* part = t.part + prow * t.Dvp;
       if (ltid < ncol) {
         const bool sn = seen[wg][ltid] != 0;
@@ -858,11 +976,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             sn ? (red[wg][0][ltid] + red[wg][1][ltid]) + (red[wg][2][ltid] + red[wg][3][ltid]) : 0.f);
       }
       for (int m = 0; m < z.mt; ++m) {
-        const int d = m * 128 + quarter * 32 + lane;
+        const int d = m * 128 + lt;
         for (int c = 0; c < ncol; c += 16) {
           uint32_t o[16];
           if (any) {
-            tmem_ld16(o_tm + m * z.n + c, o);
+            tmem_ld16(o_tm + m * N + c, o);
             tmem_wait_ld();
           }
           if (d < t.Dv) {
@@ -879,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependents_launch();
   __syncthreads();
   if (abort_flag && tid == 0) atomicCAS(kp.err, 0, kErrTimeout);
-  if (warp == kScoreWarp) {
+  if (warp == R::score) {
     tc_fence_after();
     tmem_dealloc(tm, z.cols);
   }
@@ -888,46 +1006,56 @@ __global__ void __launch_bounds__(kThreads, 1)
 using TcKernel = void (*)(const Params, const Params, const TreeArgs, const Shape);
 
 template <int KMODE, int VMODE>
-TcKernel kernel_for_nc(int nc) {
-  switch (nc) {
-    case 16: return tree_tc_kernel<KMODE, VMODE, 16>;
-    case 32: return tree_tc_kernel<KMODE, VMODE, 32>;
-    default: return tree_tc_kernel<KMODE, VMODE, 64>;
+TcKernel kernel_for_shape(const Shape& z, int* threads, int* regs) {
+  auto use = [&](auto roles) {
+    *threads = decltype(roles)::threads;
+    *regs = decltype(roles)::launch_regs;
+  };
+  if (z.nc <= 32) use(Roles<32>{});
+  else use(Roles<64>{});
+  if (z.halves == 2) return tree_tc_kernel<KMODE, VMODE, 64, true>;
+  switch (z.nc) {
+    case 16: return tree_tc_kernel<KMODE, VMODE, 16, false>;
+    case 32: return tree_tc_kernel<KMODE, VMODE, 32, false>;
+    default: return tree_tc_kernel<KMODE, VMODE, 64, false>;
   }
 }
 
-TcKernel kernel_for(int kmode, int vmode, int nc) {
+TcKernel kernel_for(int kmode, int vmode, const Shape& z, int* threads, int* regs) {
   if (kmode == KVC_MODE_UNIFORM)
-    return vmode == KVC_MODE_UNIFORM ? kernel_for_nc<KVC_MODE_UNIFORM, KVC_MODE_UNIFORM>(nc)
-                                     : kernel_for_nc<KVC_MODE_UNIFORM, KVC_MODE_INT8>(nc);
-  return vmode == KVC_MODE_UNIFORM ? kernel_for_nc<KVC_MODE_CODEBOOK, KVC_MODE_UNIFORM>(nc)
-                                   : kernel_for_nc<KVC_MODE_CODEBOOK, KVC_MODE_INT8>(nc);
+    return vmode == KVC_MODE_UNIFORM
+               ? kernel_for_shape<KVC_MODE_UNIFORM, KVC_MODE_UNIFORM>(z, threads, regs)
+               : kernel_for_shape<KVC_MODE_UNIFORM, KVC_MODE_INT8>(z, threads, regs);
+  return vmode == KVC_MODE_UNIFORM
+             ? kernel_for_shape<KVC_MODE_CODEBOOK, KVC_MODE_UNIFORM>(z, threads, regs)
+             : kernel_for_shape<KVC_MODE_CODEBOOK, KVC_MODE_INT8>(z, threads, regs);
 }
 
-// Layout for n = nc nwg columns, or false when TMEM or shared memory does not hold it.
-bool shape_for(const Params& kp, const TreeArgs& t, int nc, int nwg, Shape* out) {
+// Layout for nc columns a softmax thread (halves = 2: 2 nc columns in all), or
+// false when TMEM or shared memory does not hold it.
+bool shape_for(const Params& kp, const TreeArgs& t, int nc, int halves, Shape* out) {
   Shape z{};
   z.nc = nc;
-  z.nwg = nwg;
-  z.n = nc * nwg;
+  z.halves = halves;
+  z.n = nc * halves;
   z.K = (t.NCk + 15) / 16 * 16;
   z.KC = z.K / 8;
   z.mt = (t.Dv + 127) / 128;
   z.a_cols = (z.K / 2 + 31) / 32 * 32;
   z.s_col = 2 * z.a_cols;
   z.o_col = z.s_col + 2 * z.n;
-  const int cols = z.o_col + z.mt * z.n;
+  const int groups = halves == 2 ? 1 : 2;  // O and P: one of both halves, or one per group
+  const int cols = z.o_col + groups * z.mt * z.n;
   if (cols > 512) return false;
   for (z.cols = 32; z.cols < cols; z.cols *= 2) {}
   auto up = [](int v) { return (v + 127) / 128 * 128; };
   z.krow = up(kTile * t.Pk_max + 16);
   z.stage = z.krow + up(kTile * t.Pv_max + 16);
   z.off_p = 2 * z.n * z.K * 2;
-  z.off_v = z.off_p + z.n * kTile * 2;
-  int tab = 0;
-  if (kp.mode == KVC_MODE_CODEBOOK && kp.cb_bits >= 4) tab = 1024;
+  z.off_v = z.off_p + groups * z.n * kTile * 2;
+  const int tab = kp.mode == KVC_MODE_CODEBOOK && kp.cb_bits >= 4 ? 1024 : 0;
   // two V buffers and four row stages, or what fits
-  const int most = 220 * 1024;  // of 227 KB: the static arrays take 5
+  const int most = 216 * 1024;  // of 227 KB: the static arrays take up to 10
   for (z.nv = 2; z.nv >= 1; --z.nv)
     for (z.ns = kMaxNS; z.ns >= 2; --z.ns) {
       z.off_stage = z.off_v + z.nv * z.mt * kTile * 256;
@@ -943,11 +1071,11 @@ bool shape_for(const Params& kp, const TreeArgs& t, int nc, int nwg, Shape* out)
 
 bool choose_shape(const Params& kp, const TreeArgs& t, Shape* z) {
   // the fewest columns that hold all rows, else the most that fit
-  static const int kShapes[4][2] = {{16, 1}, {16, 2}, {32, 2}, {64, 2}};
+  static const int kShapes[4][2] = {{16, 1}, {32, 1}, {64, 1}, {64, 2}};
   bool ok = false;
   for (const auto& s : kShapes) {
     Shape c;
-    if (!shape_for(kp, t, s[0], s[1], &c)) break;
+    if (!shape_for(kp, t, s[0], s[1], &c)) continue;
     *z = c;
     ok = true;
     if (c.n >= t.rows) break;
@@ -957,27 +1085,31 @@ bool choose_shape(const Params& kp, const TreeArgs& t, Shape* z) {
 
 }  // namespace
 
-int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t) {
+int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t, int* parts, int* K) {
   if (t.prod) return 0;
   if (vp.mode == KVC_MODE_INT8 && vp.D % 8) return 0;  // value rows are read 8 bytes at a time
   Shape z;
-  return choose_shape(kp, t, &z) ? z.n : 0;
+  if (!choose_shape(kp, t, &z)) return 0;
+  *parts = z.halves == 2 ? 1 : 2;
+  *K = z.K;
+  return z.n;
 }
 
 cudaError_t launch_tree_tc(const Params& kp, const Params& vp, const TreeArgs& t, cudaStream_t s,
                            int* nk) {
   Shape z;
   if (!choose_shape(kp, t, &z)) return cudaErrorInvalidValue;
-  TcKernel k = kernel_for(kp.mode, vp.mode, z.nc);
+  int threads = 0, regs = 0;
+  TcKernel k = kernel_for(kp.mode, vp.mode, z, &threads, &regs);
   // the register split draws on what the launch gives: never launch with less
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, k);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;
+  if (fa.numRegs != regs) return cudaErrorLaunchOutOfResources;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, z.smem);
   if (e != cudaSuccess) return e;
   ++*nk;
-  return launch_dependent(k, (unsigned)t.grid, kThreads, (size_t)z.smem, s, kp, vp, t, z);
+  return launch_dependent(k, (unsigned)t.grid, threads, (size_t)z.smem, s, kp, vp, t, z);
 }
 
 }  // namespace kvc

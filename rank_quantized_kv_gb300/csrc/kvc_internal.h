@@ -123,8 +123,8 @@ cudaError_t launch_attend(const Params& kp, const Params& vp, AttendArgs a, void
 // i % N.  They are cut into jobs of at most `rt` rows; a job walks its slot's
 // stored tokens in tiles of 128.  The tiles of all jobs are one line that is
 // cut into equal runs, one per CTA, so a CTA holds the ends of some jobs; each
-// (job, CTA) pair leaves one partial, number job + CTA (both only ever grow
-// along the line, so the number is unique).
+// (job, CTA) pair leaves `parts` partials from number (job + CTA) parts on (job
+// and CTA only ever grow along the line, so the numbers are unique).
 constexpr int kTreeTile = 128;
 struct TreeArgs {
   const void* q = nullptr;
@@ -148,18 +148,27 @@ struct TreeArgs {
   int prod = 0, m = 0, n_out = 0, kcode = 0, knw = 1;
   int tc = 0;                            // tensor-core kernel: its columns (rows of a job), 0: CUDA cores
   float cb_mul = 1.f, w_mul = 1.f;       // tensor cores: scale of the centroids, its inverse
-  float* w = nullptr;                    // workspace: [n_slots rows][NCk] key weights
-  float* c1 = nullptr;                   // workspace: [n_slots rows] score offsets
+  // workspace: the key weights, fp32 [n_slots rows][NCk] or, for the tensor
+  // cores, two fp16 pieces per job in the operand's layout [jobs][2][rt x K]; a
+  // power of two that multiplies a row's scores (1 but for weights beyond fp16's
+  // range); the score offsets.  Rows padded to prow per slot (whole jobs).
+  float* w = nullptr;
+  uint16_t* w16 = nullptr;
+  float* wscale = nullptr;
+  float* c1 = nullptr;
+  int K = 0, prow = 0;
   float* wx = nullptr;                   // workspace: [n_slots rows][m + n_out]
-  // workspace: the partials [jobs + grid - 1][rt], per row its reference and
+  int parts = 1;                         // partials that a CTA leaves of a job
+  // workspace: the partials [(jobs + grid - 1) parts][rt], per row its reference and
   // sum of weights (ml) and its weighted sums (part, Dv padded to Dvp, a multiple of 4)
   float2* ml = nullptr;
   float* part = nullptr;
   int Dvp = 0;
 };
-// Rows of a tensor-core job for these layers (kvc_attend_tree_tc.cu), 0 where
-// that kernel does not take them; its launcher.
-int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t);
+// Rows of a tensor-core job for these layers, the partials that a CTA leaves of a
+// job and the operand's K (kvc_attend_tree_tc.cu), 0 where that kernel does not take them; its
+// launcher.
+int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t, int* parts, int* K);
 cudaError_t launch_tree_tc(const Params& kp, const Params& vp, const TreeArgs& t, cudaStream_t s,
                            int* nk);
 // Fill the job fields of t (rows, jobs, tiles, CTAs); the workspace bytes.
