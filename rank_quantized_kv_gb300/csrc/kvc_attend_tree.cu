@@ -31,24 +31,26 @@ namespace {
 
 constexpr int kThreads = 128;      // 4 warps
 constexpr int kRows = 8;           // rows of a job
-constexpr int kPrepRows = 32, kPrepThreads = 256;  // rows and threads of a prep block
+constexpr int kPrepThreads = 256;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Packed position j of basis beta: component (-1: padding) and width.
 __device__ int position_component(const Params& p, int beta, int j, int* width) {
-  int nch = 0;
+  int4 e[kMaxSeg];  // start byte, width, first order slot, count; all read at once
+#pragma unroll
+  for (int s = 0; s < kMaxSeg; ++s)
+    e[s] = reinterpret_cast<const int4*>(p.seg)[(size_t)beta * kMaxSeg + s];
+  int at = -1, nch = 0;
+#pragma unroll
   for (int s = 0; s < kMaxSeg; ++s) {
-    const int32_t* e = p.seg + ((size_t)beta * kMaxSeg + s) * 4;
-    if (!e[3]) break;
-    const int n = (e[3] + 7) / 8;
-    if (j < (nch + n) * 8) {
-      const int m = j - nch * 8;
-      *width = e[1];
-      return m < e[3] ? p.order[(size_t)beta * p.r + e[2] + m] : -1;
+    const int m = j - nch * 8;
+    if (m >= 0 && m < e[s].w) {
+      at = e[s].z + m;
+      *width = e[s].y;
     }
-    nch += n;
+    nch += (e[s].w + 7) / 8;
   }
-  return -1;
+  return at < 0 ? -1 : p.order[(size_t)beta * p.r + at];
 }
 
 // Chunk c (8 packed positions) of basis beta: first byte | width << 16 |
@@ -99,13 +101,15 @@ __device__ __forceinline__ float load_q(const TreeArgs& t, int64_t i) {
 // The key weights at every packed position (for the tensor cores: split into two
 // fp16 pieces and laid out as their operand), w_j = scale log2(e) u_j coef_j
 // (coef = step in uniform mode, 1 for a codebook), and c1.  One block per (slot,
-// 32 rows): u = q V as a register-tiled product, 8 rows x 2 columns a thread,
+// 4 RT rows): u = q V as a register-tiled product, RT rows x 2 columns a thread,
 // over 128 columns at a time; q stays in shared memory, V passes through it 32
 // rows at a time.  Bound: fp32 FMA (rows D r of them) for wide trees, else the
-// latency of one pass.
+// latency of one pass, for which blocks of 8 rows spread few rows over the SMs.
 constexpr int kPrepCols = 128, kPrepK = 32;
 
+template <int RT>
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp, const TreeArgs t) {
+  constexpr int kPrepRows = 4 * RT;
   extern __shared__ __align__(16) float sm_f[];
   __shared__ int comp[256];       // packed position: component (-1: padding) and its factor
   __shared__ float coef[256];
@@ -117,15 +121,29 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
   const int beta = kp.basis_of[slot];
   const int nr = max(0, min(kPrepRows, t.rows - r0));  // rows of queries
   const int np = min(kPrepRows, t.prow - r0);          // rows written
+  const bool uniform = kp.mode == KVC_MODE_UNIFORM;
+  const int us_row = r | 1;                    // an odd stride: rows in different banks
   float* qs = sm_f;                            // [D][32] rows of q, transposed
   float* vs = qs + D * kPrepRows;              // [2][32][128] rows of V
-  float* us = vs + 2 * kPrepK * kPrepCols;     // [32][r] products
+  float* us = vs + 2 * kPrepK * kPrepCols;     // [32][us_row] products
   grid_dependents_launch();
   const float* V = kp.V + (size_t)beta * D * r;
   const int stages = (D + kPrepK - 1) / kPrepK;
-  // row k0 + i of V, columns c0 ..: one 4-byte asynchronous copy per element
-  // (a row of V starts at any multiple of 4 bytes)
+  // rows of V from 32 st, columns c0 ..: asynchronous copies of 16 bytes, or of
+  // 4 where a row starts at any multiple of 4
+  const bool wide = (r & 3) == 0;  // rows of V start at multiples of 16 bytes
   auto load_v = [&](int st, int c0, int buf) {
+    if (wide) {
+#pragma unroll
+      for (int u = 0; u < kPrepK * kPrepCols / 4 / kPrepThreads; ++u) {
+        const int e = (tid + u * kPrepThreads) * 4, i = e / kPrepCols, c = e - i * kPrepCols, k = st * kPrepK + i;
+        float* dst = vs + buf * kPrepK * kPrepCols + e;
+        if (k < D && c0 + c < r) __pipeline_memcpy_async(dst, V + (size_t)k * r + c0 + c, 16);
+        else *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      __pipeline_commit();
+      return;
+    }
     for (int e = tid; e < kPrepK * kPrepCols; e += kPrepThreads) {
       const int i = e / kPrepCols, c = e - i * kPrepCols, k = st * kPrepK + i;
       float* dst = vs + buf * kPrepK * kPrepCols + e;
@@ -135,63 +153,74 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
     __pipeline_commit();
   };
   load_v(0, 0, 0);
-  for (int e = tid; e < kPrepRows * D; e += kPrepThreads) {
-    const int row = e / D, i = e - row * D;
-    float v = 0.f;
-    if (row < nr) {
-      const int x = r0 + row, g = x / t.N, n = x - g * t.N;
-      v = load_q(t, b * t.q_sb + (int64_t)(h * t.rep + g) * t.q_sh + n * t.q_st + i);
-    }
-    qs[i * kPrepRows + row] = v;
-  }
-  const int ty = tid >> 6, tx = tid & 63;  // 4 row groups of 8, 64 column pairs
-  for (int c0 = 0; c0 < r; c0 += kPrepCols) {
-    float2 acc[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = make_float2(0.f, 0.f);
-    if (c0) load_v(0, c0, 0);
-    for (int st = 0; st < stages; ++st) {
-      if (st + 1 < stages) load_v(st + 1, c0, (st + 1) & 1);
-      __pipeline_wait_prior(st + 1 < stages ? 1 : 0);
-      __syncthreads();
-      const float* vb = vs + (st & 1) * kPrepK * kPrepCols + 2 * tx;
-      const float* qb = qs + st * kPrepK * kPrepRows + 8 * ty;
-      const int kn = min(kPrepK, D - st * kPrepK);
-#pragma unroll 8
-      for (int k = 0; k < kn; ++k) {
-        const float2 v = *reinterpret_cast<const float2*>(vb + k * kPrepCols);
-        const float4 q0 = *reinterpret_cast<const float4*>(qb + k * kPrepRows);
-        const float4 q1 = *reinterpret_cast<const float4*>(qb + k * kPrepRows + 4);
-        const float q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = __ffma2_rn(make_float2(q[e], q[e]), v, acc[e]);
-      }
-      __syncthreads();  // the other buffer is refilled next
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c0 + 2 * tx;
-      if (c < r) us[(8 * ty + e) * r + c] = acc[e].x;
-      if (c + 1 < r) us[(8 * ty + e) * r + c + 1] = acc[e].y;
-    }
-  }
-  __syncthreads();
-  const bool uniform = kp.mode == KVC_MODE_UNIFORM;
-  const size_t row0 = (size_t)slot * t.prow + r0;
   for (int j = tid; j < 256; j += kPrepThreads) {
     int width = 0;
     const int k = j < t.NCk ? position_component(kp, beta, j, &width) : -1;
     comp[j] = k;
     coef[j] = k < 0 ? 0.f : t.scale_log2 * t.w_mul * (uniform ? kp.step[(size_t)beta * r + k] : 1.f);
   }
+  // a warp takes four rows, each read 32 values at a time, all loads issued
+  // before the first is stored
+  for (int i0 = 0; i0 < D; i0 += 64) {
+    float v[kPrepRows / 8][2];
+#pragma unroll
+    for (int u = 0; u < kPrepRows / 8; ++u) {
+      const int row = warp + 8 * u, x = min(r0 + row, t.rows - 1), g = x / t.N, n = x - g * t.N;
+      const int64_t at = b * t.q_sb + (int64_t)(h * t.rep + g) * t.q_sh + n * t.q_st + i0 + lane;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        v[u][e] = row < nr && i0 + lane + 32 * e < D ? load_q(t, at + 32 * e) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kPrepRows / 8; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (i0 + lane + 32 * e < D) qs[(i0 + lane + 32 * e) * kPrepRows + warp + 8 * u] = v[u][e];
+  }
+  const int ty = tid >> 6, tx = tid & 63;  // 4 row groups of RT, 64 column pairs
+  for (int c0 = 0; c0 < r; c0 += kPrepCols) {
+    float2 acc[RT];
+#pragma unroll
+    for (int e = 0; e < RT; ++e) acc[e] = make_float2(0.f, 0.f);
+    if (c0) load_v(0, c0, 0);
+    for (int st = 0; st < stages; ++st) {
+      if (st + 1 < stages) load_v(st + 1, c0, (st + 1) & 1);
+      __pipeline_wait_prior(st + 1 < stages ? 1 : 0);
+      __syncthreads();
+      const float* vb = vs + (st & 1) * kPrepK * kPrepCols + 2 * tx;
+      const float* qb = qs + st * kPrepK * kPrepRows + RT * ty;
+      const int kn = min(kPrepK, D - st * kPrepK);
+#pragma unroll 8
+      for (int k = 0; k < kn; ++k) {
+        const float2 v = *reinterpret_cast<const float2*>(vb + k * kPrepCols);
+        float q[RT];
+#pragma unroll
+        for (int e = 0; e < RT; e += 2) {
+          const float2 qq = *reinterpret_cast<const float2*>(qb + k * kPrepRows + e);
+          q[e] = qq.x;
+          q[e + 1] = qq.y;
+        }
+#pragma unroll
+        for (int e = 0; e < RT; ++e) acc[e] = __ffma2_rn(make_float2(q[e], q[e]), v, acc[e]);
+      }
+      __syncthreads();  // the other buffer is refilled next
+    }
+#pragma unroll
+    for (int e = 0; e < RT; ++e) {
+      const int c = c0 + 2 * tx;
+      if (c < r) us[(RT * ty + e) * us_row + c] = acc[e].x;
+      if (c + 1 < r) us[(RT * ty + e) * us_row + c + 1] = acc[e].y;
+    }
+  }
   __syncthreads();
+  const size_t row0 = (size_t)slot * t.prow + r0;
   for (int row = warp; row < np; row += kPrepThreads / 32) {  // a warp a row
     float c1 = 0.f, mx = 0.f;
     if (uniform && row < nr) {
       for (int k = lane; k < r; k += 32) {
         const size_t bk = (size_t)beta * r + k;
         const int width = kp.bits[bk];
-        if (width) c1 = fmaf(us[row * r + k], fmaf((float)(1 << (width - 1)), kp.step[bk], kp.lo[bk]), c1);
+        if (width) c1 = fmaf(us[row * us_row + k], fmaf((float)(1 << (width - 1)), kp.step[bk], kp.lo[bk]), c1);
       }
       for (int i = lane; i < D; i += 32) c1 = fmaf(qs[i * kPrepRows + row], kp.mean[(size_t)beta * D + i], c1);
     }
@@ -199,7 +228,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
     if (t.tc) {
       for (int j = lane; j < t.NCk; j += 32)
         if (comp[j] >= 0) {
-          const float v = fabsf(us[row * r + comp[j]] * coef[j]);
+          const float v = fabsf(us[row * us_row + comp[j]] * coef[j]);
           if (v <= 3.4e38f) mx = fmaxf(mx, v);  // NaN and infinities stay what they are
         }
       mx = warp_max(mx);
@@ -216,7 +245,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
   if (!t.tc) {
     for (int j = tid; j < t.NCk; j += kPrepThreads)  // this thread's positions of all rows
       for (int row = 0; row < nr; ++row)
-        t.w[(row0 + row) * t.NCk + j] = comp[j] < 0 ? 0.f : coef[j] * us[row * r + comp[j]];
+        t.w[(row0 + row) * t.NCk + j] = comp[j] < 0 ? 0.f : coef[j] * us[row * us_row + comp[j]];
     return;
   }
   // two fp16 pieces in the layout of a K-major operand without swizzle: cores of
@@ -232,7 +261,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int k = comp[8 * c + i];
-      const float v = k < 0 || row >= nr ? 0.f : us[row * r + k] * coef[8 * c + i] * down[row];
+      const float v = k < 0 || row >= nr ? 0.f : us[row * us_row + k] * coef[8 * c + i] * down[row];
       hi[i] = __float2half_rn(v);
       lo[i] = __float2half_rn(v - __half2float(hi[i]));
     }
@@ -720,6 +749,7 @@ size_t tree_plan(const Params& kp, TreeArgs& t, int sms) {
   // one CTA per SM on the tensor cores, else about twelve
   t.grid = (int)std::min<int64_t>(t.total, (t.tc ? 1 : 12) * (int64_t)sms);
   t.Dvp = (t.Dv + 3) / 4 * 4;
+  t.sms = sms;
   return w_bytes(kp, t) + 2 * c1_bytes(kp, t) + wx_bytes(kp, t) + ml_bytes(jobs, t) +
          align256((size_t)(jobs + t.grid - 1) * t.parts * t.rt * t.Dvp * 4);
 }
@@ -746,12 +776,15 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
+  // 32-row blocks read V the least; where they do not fill the SMs twice, 8 rows
+  const bool few = (int64_t)kp.n_slots * ((t.prow + 31) / 32) < 2 * t.sms;
+  const int rows = few ? 8 : 32;
   const size_t smem =
-      (size_t)(kp.D * kPrepRows + 2 * kPrepK * kPrepCols + kPrepRows * kp.r) * sizeof(float);
-  e = cudaFuncSetAttribute(tree_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      (size_t)(kp.D * rows + 2 * kPrepK * kPrepCols + rows * (kp.r | 1)) * sizeof(float);
+  const auto prep = few ? tree_prep_kernel<2> : tree_prep_kernel<8>;
+  e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int prep_blocks = (t.prow + kPrepRows - 1) / kPrepRows;
-  tree_prep_kernel<<<(unsigned)kp.n_slots * prep_blocks, kPrepThreads, smem, s>>>(kp, t);
+  prep<<<(unsigned)kp.n_slots * ((t.prow + rows - 1) / rows), kPrepThreads, smem, s>>>(kp, t);
   ++*nk;
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

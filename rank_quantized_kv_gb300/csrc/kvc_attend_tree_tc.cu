@@ -54,10 +54,10 @@ constexpr int kMaxNS = 4;          // row stages
 // Side words (norms and scales of a tile) stay until the softmax has read them:
 // a tile's stage is loaded once the decoders are done with the tile kMaxNS
 // before, whose keys they decoded after the scores of the tile two before that
-// were issued, which waited for the softmax to have read S two tiles earlier;
-// so eight entries are never overwritten too soon.
-constexpr int kSideRing = 8;
-static_assert(kSideRing >= kMaxNS + 4, "side words overwritten before they are read");
+// were done, which waited for the softmax to have read S four tiles earlier; so
+// entries are never overwritten too soon.
+constexpr int kSideRing = 16;
+static_assert(kSideRing >= kMaxNS + 2 + 4, "side words overwritten before they are read");
 constexpr int kSoftBar = 1, kDecBar = 3;  // named barriers: softmax groups 1, 2; decoder groups 3, 4
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSet = 6.f;        // a reference is set this far below the maximum (log2)
@@ -168,16 +168,21 @@ __device__ __forceinline__ uint4 centroids8(uint32_t x, const Levels& t) {
 // no two meet in a bank, neither reading (rows 8 NV bytes apart) nor writing
 // (cores 128 bytes apart).
 template <int NV>
-__device__ __forceinline__ void int8_block(const unsigned char* row, unsigned char* dst, int c0, int t8) {
+__device__ __forceinline__ void int8_block(const unsigned char* row, unsigned char* dst, int c0) {
+  // chunk (c0 + j) mod NV: two ascending runs, so that the addresses are a base
+  // each and constants
+  const int k = NV - (c0 & (NV - 1));  // chunks before the wrap
+  const unsigned char* src = row + (c0 & (NV - 1)) * 8;
+  unsigned char* to = dst + (c0 & (NV - 1)) * 128;
 #pragma unroll
   for (int j = 0; j < NV / 2; j += 4) {
     uint2 b[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      b[u] = *reinterpret_cast<const uint2*>(row + ((c0 + t8 + j + u) & (NV - 1)) * 8);
+      b[u] = *reinterpret_cast<const uint2*>(src + (j + u) * 8 - (j + u >= k ? NV * 8 : 0));
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      *reinterpret_cast<uint4*>(dst + ((c0 + t8 + j + u) & (NV - 1)) * 128) = int8_values(b[u]);
+      *reinterpret_cast<uint4*>(to + (j + u) * 128 - (j + u >= k ? NV * 128 : 0)) = int8_values(b[u]);
   }
 }
 
@@ -255,47 +260,68 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-// The same in one instruction (NaN only where every lane has NaN).
+// The warp's maximum (NaN only where every lane has NaN).
 __device__ __forceinline__ float warp_max_redux(float v) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
   return y;
 }
-__device__ __forceinline__ float warp_sum(float v) {
+// Sums over the warp's lanes of 2 W columns: in each step a lane hands half of
+// its columns to the lane that differs in bit O and keeps the other half; past
+// one column the lanes just add.
+template <int W, int O, int M>
+__device__ __forceinline__ void sum_lanes(float (&v)[M], int lane) {
+  if constexpr (O >= 1) {
+    if constexpr (W >= 1) {
+      const bool hi = lane & O;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+      for (int i = 0; i < W; ++i) {
+        const float keep = hi ? v[i + W] : v[i], give = hi ? v[i] : v[i + W];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, O);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], O);
+    }
+    sum_lanes<W / 2, O / 2>(v, lane);
+  }
 }
 
-// A CTA's run of tiles, cut at the jobs' ends.
+// A CTA's run of tiles, cut at the jobs' ends.  Divisions by tiles and row tiles
+// are done once, for the run's first tile; the next segment starts the next job.
 struct Segment {
   int job, slot, r0, nr, b;
   int tile0, tile1;  // tiles of the job (hidden context skipped)
 };
 struct Walk {
-  int64_t at, end;
-  __device__ Walk(const TreeArgs& t)
-      : at(t.total * blockIdx.x / t.grid), end(t.total * (blockIdx.x + 1) / t.grid) {}
+  int64_t left;      // tiles of the run not yet walked
+  int job, slot, jt; // next segment's job: its slot and row tile
+  int a;             // and its first tile
+  __device__ explicit Walk(const TreeArgs& t) {
+    const int64_t at = t.total * blockIdx.x / t.grid;
+    left = t.total * (blockIdx.x + 1) / t.grid - at;
+    job = (int)(at / t.tps);
+    a = (int)(at - job * t.tps);
+    slot = job / t.row_tiles;
+    jt = job - slot * t.row_tiles;
+  }
   __device__ bool next(const TreeArgs& t, int H, Segment& g) {
-    if (at >= end) return false;
-    g.job = (int)(at / t.tps);
-    const int64_t a = at - g.job * t.tps;
-    const int64_t z = min(t.tps, a + (end - at));
-    at += z - a;
-    g.slot = g.job / t.row_tiles;
-    g.r0 = (g.job - g.slot * t.row_tiles) * t.rt;
+    if (left <= 0) return false;
+    const int z = (int)min(t.tps, a + left);
+    left -= z - a;
+    g.job = job;
+    g.slot = slot;
+    g.r0 = jt * t.rt;
     g.nr = min(t.rt, t.rows - g.r0);
-    g.b = g.slot / H;
-    g.tile0 = (int)a;
-    g.tile1 = (int)z;
-    if (t.first) {  // tiles of hidden context only
-      const int64_t f = min((int64_t)max(t.first[g.b], 0), t.ctx) / kTile;
-      g.tile0 = (int)min(z, max(a, f));
+    g.b = slot / H;
+    g.tile0 = a;
+    g.tile1 = z;
+    if (t.first)  // tiles of hidden context only
+      g.tile0 = min(z, max(a, (int)(min((int64_t)max(t.first[g.b], 0), t.ctx) / kTile)));
+    ++job;
+    a = 0;
+    if (++jt == t.row_tiles) {
+      jt = 0;
+      ++slot;
     }
     return true;
   }
@@ -304,8 +330,8 @@ struct Walk {
 // A group's segment and place in the run, kept in shared memory so that they
 // take no registers in its loop; one thread of the group walks.
 struct Place {
+  Walk w;
   Segment g;
-  int64_t at;
   int more;            // 0: the run is at its end
   // softmax
   int plain0, plain1;  // tiles that hold visible context alone
@@ -313,12 +339,7 @@ struct Place {
   const uint8_t* mask;
   int scaled;          // some row's key weights were beyond fp16's range
   int Pk, Pv;          // decoders: row bytes
-  __device__ void next(const TreeArgs& t, int H) {
-    Walk w(t);
-    w.at = at;
-    more = w.next(t, H, g);
-    at = w.at;
-  }
+  __device__ void next(const TreeArgs& t, int H) { more = w.next(t, H, g); }
 };
 
 // Position in a ring of n buffers; next() moves on one use.
@@ -332,15 +353,20 @@ struct Ring {
 };
 
 // Wait for a phase.  Once a wait of any role has run out (2 s) every further
-// wait returns at once, so that all roles walk to their ends and the named
+// wait returns soon, so that all roles walk to their ends and the named
 // barriers stay matched; the results are then undefined and the error word says
-// so.  The first try may sleep in hardware: most waits need no second one.
+// so.  The loop is short because a try returns early (waiting warps would take
+// issue slots from working ones): time and flag are looked at every 64 tries.
 __device__ __forceinline__ void wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait_sleep(bar, parity, 1000000u)) return;
-  const uint64_t t0 = global_timer_ns();
-  while (!*abort_flag) {
-    if (mbar_try_wait_sleep(bar, parity, 1000000u)) return;
-    if (global_timer_ns() - t0 > kWaitNs) *abort_flag = 1;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait_sleep(bar, parity, 10000000u)) return;
+    if (i % 64 == 0) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort_flag) return;
+      if (now - t0 > kWaitNs) *abort_flag = 1;
+    }
   }
 }
 
@@ -353,16 +379,19 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
   constexpr int CH = NC < 32 ? NC : 32;    // columns handled at a time
   constexpr int NCH = NC / CH;
   constexpr int DG = R::dec_groups;
+  constexpr int SB = HALVES ? 2 : 4;       // S buffers: two per tile that a softmax group holds
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t row_full[kMaxNS], row_empty[kMaxNS], a_full[2], a_empty[2], v_full[2],
-      v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], side_full[kSideRing], w_full, w_empty, done_bar;
+      v_empty[2], s_full[SB], s_empty[SB], p_full[2], p_empty[2], side_full[kSideRing], w_full, w_empty, done_bar;
   __shared__ uint32_t kch[DG][32], vch[DG][32];  // chunk tables of the decoder groups
   // per softmax group and column: offset of the score (c1 - m), m, rescale
   // factor, seen a token; the warps' partial results
   __shared__ __align__(16) float cneg[2][NC];
-  __shared__ float mref[2][NC], wscale[2][NC], corr[2][NC], red[2][4][NC];
+  __shared__ __align__(16) float corr[2][NC], red[2][4][NC];
+  __shared__ float mref[2][NC], wscale[2][NC];
   __shared__ int seen[2][NC];
-  __shared__ Place place[2 + DG];  // softmax groups, decoder groups
+  __shared__ __align__(16) unsigned char place_s[(2 + DG) * sizeof(Place)];  // softmax groups, decoder groups
+  Place* place = reinterpret_cast<Place*>(place_s);
   __shared__ __align__(16) unsigned short side_s[kSideRing][2][kTile];  // norms, scales
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
@@ -385,11 +414,10 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
       mbar_init(&a_empty[i], 1);
       mbar_init(&v_full[i], kGroupWarps);
       mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], HALVES ? 8 : 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&p_empty[i], 1);
     }
+    for (int i = 0; i < SB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], HALVES ? 8 : 4); }
     for (int i = 0; i < kSideRing; ++i) mbar_init(&side_full[i], 1);
     mbar_init(&w_full, 1);
     mbar_init(&w_empty, 1);
@@ -397,7 +425,7 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
     fence_mbar_init();
     abort_flag = 0;
   }
-  if (tid < 2 + DG) place[tid].at = Walk(t).at;
+  if (tid < 2 + DG) place[tid].w = Walk(t);
   if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits >= 4) {  // pairs of 16 levels, or 256 levels
     const int pair = kp.cb_bits == 4;
     auto half_of = [&](int c) {
@@ -410,13 +438,14 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_base;
+  Walk walk = place[0].w;  // (the MMA warps and the producer walk on their own)
+  __syncthreads();
   grid_dependency_wait();  // the key weights come from the launch before
 
   if (warp >= R::prod) {
     regs_dec<R::ctl_regs>();
     if (warp == R::prod && lane == 0) {
       // ---------------------------------------------------------- producer
-      Walk walk(t);
       Segment g;
       Ring rr(z.ns);
       int issued = 0, segs = 0;
@@ -463,7 +492,6 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
       // The whole warp walks and waits, one elected lane issues, so that
       // descriptors stay in uniform registers; the two products have a warp
       // each.  (One lane walking and issuing both took 160 cycles per MMA.)
-      Walk walk(t);
       Segment g;
       const bool leader = elect_one();
       constexpr uint32_t id = idesc_f16(kTile, N, 0);
@@ -474,13 +502,13 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
         wait_or_abort(&w_full, segs & 1, &abort_flag);
         ++segs;
         for (int tile = g.tile0; tile < g.tile1; ++tile, ++it) {
-          const int s = it & 1;
-          if (it >= 2) wait_or_abort(&s_empty[s], ((it >> 1) - 1) & 1, &abort_flag);
-          wait_or_abort(&a_full[s], (it >> 1) & 1, &abort_flag);
+          const int a = it & 1, s = it % SB;
+          if (it >= SB) wait_or_abort(&s_empty[s], (it / SB - 1) & 1, &abort_flag);
+          wait_or_abort(&a_full[a], (it >> 1) & 1, &abort_flag);
           __syncwarp();
           tc_fence_after();
           if (leader) {
-            const uint32_t a0 = tm + s * z.a_cols, d0 = tm + z.s_col + s * N;
+            const uint32_t a0 = tm + a * z.a_cols, d0 = tm + z.s_col + s * N;
             umma_f16_tmem_a(d0, a0, w_desc, id, 0u);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {  // the two pieces of W
@@ -490,7 +518,7 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
                 umma_f16_tmem_a(d0, a0 + ks * 8, wd + ks * 16, id, 1u);
             }
             umma_commit(&s_full[s]);
-            umma_commit(&a_empty[s]);
+            umma_commit(&a_empty[a]);
             if (tile + 1 == g.tile1) umma_commit(&w_empty);
           }
           __syncwarp();
@@ -505,7 +533,6 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
       // ---------------------------------------------------------- O += V^T P
       // One product per tile, or, where the groups split the columns, one per
       // group as its weights arrive.
-      Walk walk(t);
       Segment g;
       const bool leader = elect_one();
       constexpr uint32_t id = idesc_f16(kTile, NC, 0) | kTransposeAB;
@@ -651,9 +678,9 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
           unsigned char* dst = Vs + rv.slot * v_bytes + vblk * z.mt * 2048 + t8 * 16;
           const int c0 = (octet & 1) * vhalf;
           if (!VU && nv == 16) {
-            int8_block<16>(raw + tok * 128, dst, c0, t8);
+            int8_block<16>(raw + tok * 128, dst, c0 + t8);
           } else if (!VU && nv == 8) {
-            int8_block<8>(raw + tok * 64, dst, c0, t8);
+            int8_block<8>(raw + tok * 64, dst, c0 + t8);
           } else {
             const int cend = min(nv, c0 + vhalf);
             for (int j = c0; j < cend; ++j) {
@@ -709,9 +736,10 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
       bool big = false;
       if (ltid < NC) {
         const size_t row = (size_t)pl.g.slot * t.prow + pl.g.r0 + col0 + ltid;
-        cn[ltid] = t.c1[row];
-        wscale[wg][ltid] = t.wscale[row];
-        big = t.wscale[row] != 1.f;
+        const float c1 = t.c1[row], ws = t.wscale[row];
+        cn[ltid] = c1;
+        wscale[wg][ltid] = ws;
+        big = ws != 1.f;
         mref[wg][ltid] = 0.f;
         seen[wg][ltid] = ltid >= ncol;
       }
@@ -724,25 +752,204 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
       // the group's tiles of the segment, and its tiles of the run before them
       const int tile_first = pl.g.tile0 + (HALVES ? 0 : (it ^ wg) & 1);
       int j = HALVES ? it : (it + 1 - wg) >> 1;
-      // tiles [fast0, fast1) hold visible context alone; column chunks with rows
-      // that saw nothing yet, or scaled rows, keep every tile on the general path
-      uint32_t unseen = ncol ? (1u << NCH) - 1u : 0u;
-      int fast0 = pl.plain0, fast1 = unseen || scaled ? 0 : pl.plain1;
+      // tiles [fast0, fast1) hold visible context alone, of rows that have seen a
+      // token already
+      int fast0 = pl.plain0, fast1 = 0;
       const int tile1 = pl.g.tile1;
       for (int tile = tile_first; tile < tile1; tile += kStep, ++j) {
-        const int s = HALVES ? j & 1 : wg;             // S buffer, and its phase
-        const uint32_t s_par = (HALVES ? j >> 1 : j) & 1;
-        const uint32_t s_tm = tm + lane_off + z.s_col + s * N + col0;
         const int gt = HALVES ? j : 2 * j + wg;        // the tile's number in the run
+        const int s = gt % SB;                         // S buffer, and its phase
+        const uint32_t s_par = (gt / SB) & 1;
+        const uint32_t s_tm = tm + lane_off + z.s_col + s * N + col0;
         const int sd = gt & (kSideRing - 1);
         wait_or_abort(&side_full[sd], (gt / kSideRing) & 1, &abort_flag);
         float nt = KMODE == KVC_MODE_CODEBOOK ? __half2float(__ushort_as_half(side_s[sd][0][lt])) : 1.f;
         const float st = VU ? 1.f : __half2float(__ushort_as_half(side_s[sd][1][lt]));
         if (!VU && st != st) nt = st;  // a scale of NaN: the weights of those who see it
-        // weights of one chunk of columns into P and the sums; a hidden token's
-        // scale may be anything: its weights are 0 and stay 0 under any finite su
-        auto weigh = [&](int ch, float2 (&x)[CH / 2], float su) {
-          const float2 su2 = make_float2(su, su);
+        wait_or_abort(&s_full[s], s_par, &abort_flag);
+        __syncwarp();
+        tc_fence_after();
+        auto scores = [&](int ch, float2 (&x)[CH / 2]) {  // S nt + c1 - m
+          uint32_t r[CH];
+          tmem_ld_n<CH>(s_tm + ch * CH, r);
+          tmem_wait_ld();
+          const float2 nt2 = make_float2(nt, nt);
+#pragma unroll
+          for (int i = 0; i < CH / 4; ++i) {
+            const float4 c = reinterpret_cast<const float4*>(cn + ch * CH)[i];
+            x[2 * i] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), nt2,
+                                  make_float2(c.x, c.y));
+            x[2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])),
+                                      nt2, make_float2(c.z, c.w));
+          }
+        };
+        // Tiles of visible context alone only check that no score and no scale is
+        // too far above its reference.  The others, and those that fail, first
+        // take the general path below, once.
+        bool general = tile < fast0 || tile >= fast1;
+        uint64_t vis = ~0ull;  // which of the group's rows see this lane's token
+        float2 x[CH / 2];
+        for (;;) {
+          if (general) {
+            // Loops are kept rolled: this code runs about twice per job, and its
+            // instructions come from L2.
+            if (tile < pl.plain0 || tile >= pl.plain1) {
+              const int64_t tok = (int64_t)tile * kTile + lt, draft = tok - t.ctx;
+              if (draft < 0) {
+                vis = tok >= pl.first ? ~0ull : 0ull;
+              } else {
+                vis = 0ull;
+                if (draft < t.N) {
+                  const int nc = min(NC, pl.g.nr - col0);
+                  int n = (pl.g.r0 + col0) % t.N;
+                  const uint8_t* col = pl.mask + draft;
+#pragma unroll 1
+                  for (int c0 = 0; c0 < nc; c0 += 8) {  // eight loads in flight
+                    uint32_t m[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                      m[c] = c0 + c >= nc ? 0 : pl.mask ? col[(int64_t)n * t.N] : draft <= n;
+                      if (++n == t.N) n = 0;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) vis |= (uint64_t)(m[c] != 0) << (c0 + c);
+                  }
+                }
+              }
+            }
+            float ratio = 1.f;
+            if (!VU) {  // the value scales' reference: the next power of two
+              const bool up = vis != 0ull && st > 4.f * sref && st <= 65504.f;
+              const float m = warp_max_redux(up ? st : 0.f);
+              if (lane == 0) red[wg][quarter][0] = m;
+              named_bar_sync(bar, 128);
+              const float most = fmaxf(fmaxf(red[wg][0][0], red[wg][1][0]), fmaxf(red[wg][2][0], red[wg][3][0]));
+              if (most > 0.f) {
+                const float to = __int_as_float((__float_as_int(most) & 0x7f800000) + 0x00800000);
+                ratio = sref / to;
+                sref = to;
+                inv_sref = 1.f / to;
+              }
+              named_bar_sync(bar, 128);
+            }
+            // the tile's largest score of every column
+#pragma unroll 1
+            for (int c = 0; c < NC; c += 16) {
+              uint32_t r[16];
+              tmem_ld16(s_tm + c, r);
+              tmem_wait_ld();
+              const uint32_t v = (uint32_t)(vis >> c);
+              float m[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float f = fmaf(__uint_as_float(r[i]) * wscale[wg][c + i], nt, cn[c + i]);
+                m[i] = warp_max_redux(v >> i & 1u ? f : -INFINITY);
+              }
+              if (lane == 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  reinterpret_cast<float4*>(&red[wg][quarter][c])[i] =
+                      make_float4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
+            }
+            named_bar_sync(bar, 128);
+            bool blind = false;
+            if (ltid < NC) {
+              const float m = fmaxf(fmaxf(red[wg][0][ltid], red[wg][1][ltid]),
+                                    fmaxf(red[wg][2][ltid], red[wg][3][ltid]));
+              float d = 0.f, f = 1.f;
+              if (m != -INFINITY) {  // (a row of NaN counts as seen and stays NaN)
+                if (!seen[wg][ltid]) {  // nothing summed yet
+                  d = m - kSet;
+                  f = 0.f;
+                  seen[wg][ltid] = 1;
+                } else if (m > kMove) {
+                  d = m - kSet;
+                  f = ex2(-d);
+                } else if (m != m) {
+                  d = m;
+                }
+              }
+              mref[wg][ltid] += d;
+              cn[ltid] -= d;
+              corr[wg][ltid] = f;
+              blind = !seen[wg][ltid];
+            }
+            // rows that saw nothing yet keep every tile on this path
+            if (!named_bar_or(bar, 128, blind) && !pl.scaled) fast1 = pl.plain1;
+#pragma unroll
+            for (int i = 0; i < NC / 4; ++i) {
+              const float4 f = reinterpret_cast<const float4*>(corr[wg])[i];
+              l[2 * i] = __fmul2_rn(l[2 * i], make_float2(f.x, f.y));
+              l[2 * i + 1] = __fmul2_rn(l[2 * i + 1], make_float2(f.z, f.w));
+            }
+            if (tile != tile_first) {  // O holds sums: rescale it once the last product is done
+              wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int m = 0; m < z.mt; ++m)
+#pragma unroll 1
+                for (int c = 0; c < NC; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(o_tm + m * N + c, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) * (corr[wg][c + i] * ratio));
+                  tmem_st16(o_tm + m * N + c, o);
+                }
+              tmem_wait_st();
+            }
+            named_bar_sync(bar, 128);  // corr and red have been read
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int ch = NCH - 1; ch >= 0; --ch) {  // ends with the first chunk's scores in x
+            scores(ch, x);
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) mx = max3(mx, x[i].x, x[i].y);
+          }
+          if (general || !named_bar_or(bar, 128, mx > kMove || (!VU && st > 4.f * sref))) break;
+          general = true;
+        }
+        if (j > 0) wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);  // P has been read
+        __syncwarp();
+        // a hidden token's scale may be anything: its weights are 0 and stay 0
+        // under any finite factor
+        const float su = fmaxf(fminf(st * inv_sref, 3e38f), -3e38f);
+        const float2 su2 = make_float2(su, su);
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) {
+          if (ch) scores(ch, x);
+          if (ch == NCH - 1 && !pl.scaled) {  // S has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[s]);
+          }
+          if (general) {
+            if (pl.scaled) {  // rows of key weights beyond fp16's range
+              uint32_t r[CH];
+              tmem_ld_n<CH>(s_tm + ch * CH, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < CH / 2; ++i) {
+                const int c = ch * CH + 2 * i;
+                x[i].x = fmaf(__uint_as_float(r[2 * i]) * wscale[wg][c], nt, cn[c]);
+                x[i].y = fmaf(__uint_as_float(r[2 * i + 1]) * wscale[wg][c + 1], nt, cn[c + 1]);
+              }
+              if (ch == NCH - 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[s]);
+              }
+            }
+            const uint32_t v = (uint32_t)(vis >> (ch * CH));
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) {
+              if (!(v >> (2 * i) & 1u)) x[i].x = -INFINITY;
+              if (!(v >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
+            }
+          }
 #pragma unroll
           for (int q = 0; q < CH / 8; ++q) {
             uint32_t h[4];
@@ -756,194 +963,6 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
             }
             *reinterpret_cast<uint4*>(pst + (ch * CH / 8 + q) * 128) = make_uint4(h[0], h[1], h[2], h[3]);
           }
-        };
-        auto scores = [&](int ch, float2 (&x)[CH / 2], bool scale_rows) {  // S nt + c1 - m
-          uint32_t r[CH];
-          tmem_ld_n<CH>(s_tm + ch * CH, r);
-          tmem_wait_ld();
-          if (scale_rows) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-              r[i] = __float_as_uint(__uint_as_float(r[i]) * wscale[wg][ch * CH + i]);
-          }
-          const float2 nt2 = make_float2(nt, nt);
-#pragma unroll
-          for (int i = 0; i < CH / 4; ++i) {
-            const float4 c = reinterpret_cast<const float4*>(cn + ch * CH)[i];
-            x[2 * i] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), nt2,
-                                  make_float2(c.x, c.y));
-            x[2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])),
-                                      nt2, make_float2(c.z, c.w));
-          }
-        };
-        auto release_scores = [&]() {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[s]);
-        };
-        wait_or_abort(&s_full[s], s_par, &abort_flag);
-        __syncwarp();
-        tc_fence_after();
-        int done = 0;  // chunks of columns weighed
-        if (tile >= fast0 && tile < fast1) {
-#pragma unroll
-          for (int ch = 0; ch < NCH; ++ch) {
-            if (done == ch) {
-              float2 x[CH / 2];
-              scores(ch, x, false);
-              float mx = max3(x[0].x, x[0].y, -INFINITY);
-#pragma unroll
-              for (int i = 1; i < CH / 2; ++i) mx = max3(mx, x[i].x, x[i].y);
-              if (!named_bar_or(bar, 128, mx > kMove || (!VU && st > 4.f * sref))) {
-                if (ch == NCH - 1) release_scores();
-                if (ch == 0) {
-                  if (j > 0) wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);  // P has been read
-                  __syncwarp();
-                }
-                weigh(ch, x, fmaxf(fminf(st * inv_sref, 3e38f), -3e38f));
-                done = ch + 1;
-              }
-            }
-          }
-        }
-        if (done < NCH) {
-          // The general path: tokens hidden from some rows, and references that
-          // move.  Every thread of the group is here.
-          const int first = pl.first;
-          uint64_t vis = ~0ull;  // which of the group's rows see this lane's token
-          const bool special = tile < pl.plain0 || tile >= pl.plain1;
-          if (special) {
-            const int64_t tok = (int64_t)tile * kTile + lt, draft = tok - t.ctx;
-            if (draft < 0) {
-              vis = tok >= first ? ~0ull : 0ull;
-            } else {
-              vis = 0ull;
-              if (draft < t.N) {
-                const int nc = min(NC, pl.g.nr - col0), n0 = (pl.g.r0 + col0) % t.N;
-                if (pl.mask) {
-                  const uint8_t* col = pl.mask + draft;
-                  int n = n0;
-                  for (int c0 = 0; c0 < nc; c0 += 16) {  // sixteen loads in flight
-                    uint8_t m[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                      m[c] = c0 + c < nc ? col[(int64_t)n * t.N] : 0;
-                      if (++n == t.N) n = 0;
-                    }
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                      if (m[c]) vis |= 1ull << (c0 + c);
-                  }
-                } else {
-                  int n = n0;
-                  for (int c = 0; c < nc; ++c) {
-                    if (draft <= n) vis |= 1ull << c;
-                    if (++n == t.N) n = 0;
-                  }
-                }
-              }
-            }
-          }
-          bool up = !VU && vis != 0ull && st > 4.f * sref && st <= 65504.f;
-#pragma unroll
-          for (int ch = 0; ch < NCH; ++ch) {
-            if (ch < done) continue;
-            float2 x[CH / 2];
-            bool moved = false;
-            for (;;) {
-              scores(ch, x, pl.scaled != 0);
-              if (special) {
-                const uint32_t v = (uint32_t)(vis >> (ch * CH));
-#pragma unroll
-                for (int i = 0; i < CH / 2; ++i) {
-                  if (!(v >> (2 * i) & 1u)) x[i].x = -INFINITY;
-                  if (!(v >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
-                }
-              }
-              float mx = -INFINITY;
-#pragma unroll
-              for (int i = 0; i < CH / 2; ++i) mx = max3(mx, x[i].x, x[i].y);
-              if (moved || !named_bar_or(bar, 128, mx > kMove || up || (unseen >> ch & 1u))) break;
-              moved = true;
-              float ratio = 1.f;
-              if (!VU) {  // the value scales' reference: the next power of two
-                const float m = warp_max(up ? st : 0.f);
-                if (lane == 0) red[wg][quarter][0] = m;
-                named_bar_sync(bar, 128);
-                const float most = fmaxf(fmaxf(red[wg][0][0], red[wg][1][0]), fmaxf(red[wg][2][0], red[wg][3][0]));
-                if (most > 0.f) {
-                  const float to = __int_as_float((__float_as_int(most) & 0x7f800000) + 0x00800000);
-                  ratio = sref / to;
-                  sref = to;
-                  inv_sref = 1.f / to;
-                }
-                up = false;
-                named_bar_sync(bar, 128);
-              }
-#pragma unroll
-              for (int i = 0; i < CH / 2; ++i) {
-                const float a = warp_max_redux(x[i].x), b = warp_max_redux(x[i].y);
-                if (lane == 0) {
-                  red[wg][quarter][2 * i] = a;
-                  red[wg][quarter][2 * i + 1] = b;
-                }
-              }
-              named_bar_sync(bar, 128);
-              bool blind = false;
-              if (ltid < CH) {
-                const int c = ch * CH + ltid;
-                const float m = fmaxf(fmaxf(red[wg][0][ltid], red[wg][1][ltid]),
-                                      fmaxf(red[wg][2][ltid], red[wg][3][ltid]));
-                float d = 0.f, f = 1.f;
-                if (m != -INFINITY) {  // (a row of NaN counts as seen and stays NaN)
-                  if (!seen[wg][c]) {  // nothing summed yet
-                    d = m - kSet;
-                    f = 0.f;
-                    seen[wg][c] = 1;
-                  } else if (m > kSet) {
-                    d = m - kSet;
-                    f = ex2(-d);
-                  }
-                }
-                mref[wg][c] += d;
-                cn[c] -= d;
-                corr[wg][c] = f;
-                blind = !seen[wg][c];
-              }
-              if (!named_bar_or(bar, 128, blind)) unseen &= ~(1u << ch);
-#pragma unroll
-              for (int i = 0; i < CH / 2; ++i) {
-                l[ch * CH / 2 + i].x *= corr[wg][ch * CH + 2 * i];
-                l[ch * CH / 2 + i].y *= corr[wg][ch * CH + 2 * i + 1];
-              }
-              if (tile != tile_first) {  // O holds sums: rescale it once the last product is done
-                wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);
-                __syncwarp();
-                tc_fence_after();
-                for (int m = 0; m < z.mt; ++m)
-                  for (int c = 0; c < NC; c += 16) {
-                    const bool mine = c >= ch * CH && c < ch * CH + CH;
-                    if (!mine && ratio == 1.f) continue;
-                    uint32_t o[16];
-                    tmem_ld16(o_tm + m * N + c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                      o[i] = __float_as_uint(__uint_as_float(o[i]) * (mine ? corr[wg][c + i] * ratio : ratio));
-                    tmem_st16(o_tm + m * N + c, o);
-                  }
-                tmem_wait_st();
-              }
-              named_bar_sync(bar, 128);  // corr and red have been read
-            }
-            if (ch == NCH - 1) release_scores();
-            if (ch == 0) {
-              if (j > 0) wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);  // P has been read
-              __syncwarp();
-            }
-            weigh(ch, x, fmaxf(fminf(st * inv_sref, 3e38f), -3e38f));
-          }
-          if (!unseen && !pl.scaled) fast1 = pl.plain1;
         }
         fence_proxy_async_smem();  // P is read by the tensor core
         tc_fence_before();         // and O, where it was rescaled
@@ -958,13 +977,19 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
         tc_fence_after();
       }
       it += tile1 - pl.g.tile0;
+      // sums of the weights over the warp's lanes
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) {
-        const float a = warp_sum(l[i].x), b = warp_sum(l[i].y);
-        if (lane == 0) {
-          red[wg][quarter][2 * i] = a;
-          red[wg][quarter][2 * i + 1] = b;
+      for (int c0 = 0; c0 < NC; c0 += CH) {
+        float v[CH];
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+          v[2 * i] = l[c0 / 2 + i].x;
+          v[2 * i + 1] = l[c0 / 2 + i].y;
         }
+        sum_lanes<CH / 2, 16>(v, lane);
+        // lane bits 16, 8, .. chose the column's high bits
+        const int col = CH == 32 ? lane : lane >> 1;
+        if (CH == 32 || !(lane & 1)) red[wg][quarter][c0 + col] = v[0];
       }
       named_bar_sync(bar, 128);
       const size_t prow = (HALVES ? ((size_t)pl.g.job + blockIdx.x) : 2 * ((size_t)pl.g.job + blockIdx.x) + wg) * t.rt + col0;
@@ -1043,7 +1068,7 @@ bool shape_for(const Params& kp, const TreeArgs& t, int nc, int halves, Shape* o
   z.mt = (t.Dv + 127) / 128;
   z.a_cols = (z.K / 2 + 31) / 32 * 32;
   z.s_col = 2 * z.a_cols;
-  z.o_col = z.s_col + 2 * z.n;
+  z.o_col = z.s_col + (halves == 2 ? 2 : 4) * z.n;  // S buffers
   const int groups = halves == 2 ? 1 : 2;  // O and P: one of both halves, or one per group
   const int cols = z.o_col + groups * z.mt * z.n;
   if (cols > 512) return false;
@@ -1055,7 +1080,7 @@ bool shape_for(const Params& kp, const TreeArgs& t, int nc, int halves, Shape* o
   z.off_v = z.off_p + groups * z.n * kTile * 2;
   const int tab = kp.mode == KVC_MODE_CODEBOOK && kp.cb_bits >= 4 ? 1024 : 0;
   // two V buffers and four row stages, or what fits
-  const int most = 216 * 1024;  // of 227 KB: the static arrays take up to 10
+  const int most = 212 * 1024;  // of 227 KB: the static arrays take up to 14
   for (z.nv = 2; z.nv >= 1; --z.nv)
     for (z.ns = kMaxNS; z.ns >= 2; --z.ns) {
       z.off_stage = z.off_v + z.nv * z.mt * kTile * 256;

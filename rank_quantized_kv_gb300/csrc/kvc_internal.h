@@ -142,7 +142,7 @@ struct TreeArgs {
   int64_t S = 0, ctx = 0;                // stored tokens; those before the drafts
   int rows = 0, rt = 0, row_tiles = 0;   // rows of a slot, of a job; jobs of a slot
   int64_t tps = 0, total = 0;            // tiles of a job, of the line
-  int grid = 0;                          // CTAs
+  int grid = 0, sms = 0;                 // CTAs; the device's SMs
   int NCk = 0, Dv = 0;                   // as in AttendArgs
   int Pk_max = 0, Pv_max = 0;
   int prod = 0, m = 0, n_out = 0, kcode = 0, knw = 1;
