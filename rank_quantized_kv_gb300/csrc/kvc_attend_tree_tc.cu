@@ -90,7 +90,7 @@ struct Shape {
   int a_cols, s_col, o_col, cols;  // TMEM layout
   int nv, ns;            // V buffers, row stages
   int krow, stage;       // bytes of a stage's key rows; of a stage
-  int off_p, off_v, off_stage, off_tab;  // shared-memory offsets
+  int off_p, off_v, off_stage;  // shared-memory offsets
   int smem;
 };
 
@@ -186,10 +186,22 @@ __device__ __forceinline__ void int8_block(const unsigned char* row, unsigned ch
   }
 }
 
+// The 2 W bits at bit `off` of the words w as a byte offset into the pair table
+// below (a field f at bit 7: f * 128), other bits undefined.
+template <int W, int M>
+__device__ __forceinline__ uint32_t pair_offset(const uint32_t (&w)[M], int off) {
+  const int at = off - 7, i = at >> 5, sh = at & 31;
+  if (at < 0) return w[0] << -at;
+  return sh + 2 * W + 7 <= 32 || i + 1 >= M ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1], sh);
+}
+
 // 64 consecutive codes (2 W words, 8-byte aligned) of a row of W-bit indices
-// into 32 TMEM columns.
+// into 32 TMEM columns, two codes per lookup in a table that holds every pair of
+// centroids once per lane (no bank conflicts): a shift, a select that also adds
+// the lane (lane4: its number times 4), and a load per two codes.
 template <int W>
-__device__ __forceinline__ void codebook64(const unsigned char* src, const Levels& t, uint32_t a_tm) {
+__device__ __forceinline__ void codebook64(const unsigned char* src, const uint32_t* tab, uint32_t lane4,
+                                           uint32_t a_tm) {
   uint32_t w[2 * W];
 #pragma unroll
   for (int i = 0; i < W; ++i) {
@@ -197,15 +209,14 @@ __device__ __forceinline__ void codebook64(const unsigned char* src, const Level
     w[2 * i] = v.x;
     w[2 * i + 1] = v.y;
   }
+  constexpr uint32_t mask = ((1u << (2 * W)) - 1u) << 7;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t r[16];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int bit = (4 * h + c) * 8 * W, i = bit >> 5, sh = bit & 31;
-      const uint32_t x = sh + 8 * W <= 32 ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1], sh);
-      const uint4 v = centroids8<W>(x, t);
-      r[4 * c] = v.x; r[4 * c + 1] = v.y; r[4 * c + 2] = v.z; r[4 * c + 3] = v.w;
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t at = (pair_offset<W>(w, 2 * W * (16 * h + i)) & mask) | lane4;
+      r[i] = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const unsigned char*>(tab) + at);
     }
     tmem_st16(a_tm + h * 16, r);
   }
@@ -238,6 +249,39 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile(
       "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
   return p != 0;
+}
+
+// tcgen05.mma and commit by the lane that has `lead`, predicated and not in a
+// branch: the operands are then computed where the warp is converged and stay
+// in uniform registers.
+__device__ __forceinline__ void mma_tmem_a(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n}" ::"r"(lead),
+      "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_smem(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n}" ::"r"(lead),
+      "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}" ::"r"(lead),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Entries of the pair table that holds every pair of centroids once per lane:
+// for codebooks of at most 8 levels at D = 128, else none.
+__host__ __device__ constexpr int pair_entries(int cb_bits, int D) {
+  return cb_bits <= 3 && D == 128 ? 1 << (2 * cb_bits) : 0;
 }
 
 template <int REGS> __device__ __forceinline__ void regs_inc() {
@@ -393,6 +437,7 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
   __shared__ __align__(16) unsigned char place_s[(2 + DG) * sizeof(Place)];  // softmax groups, decoder groups
   Place* place = reinterpret_cast<Place*>(place_s);
   __shared__ __align__(16) unsigned short side_s[kSideRing][2][kTile];  // norms, scales
+  __shared__ uint32_t tab[KMODE == KVC_MODE_CODEBOOK ? 64 * 32 : 1];  // codebook tables
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
 
@@ -401,7 +446,6 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
   unsigned char* Ps = smem + z.off_p;
   unsigned char* Vs = smem + z.off_v;
   unsigned char* Rs = smem + z.off_stage;
-  uint32_t* tab = reinterpret_cast<uint32_t*>(smem + z.off_tab);  // codebooks of 16 or 256 levels
   const int w_piece = N * z.K * 2;
   constexpr int p_bytes = kTile * N * 2;  // P: one buffer per group, or one of both halves
   const int v_bytes = z.mt * kTile * 256;
@@ -426,13 +470,18 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
     abort_flag = 0;
   }
   if (tid < 2 + DG) place[tid].w = Walk(t);
-  if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits >= 4) {  // pairs of 16 levels, or 256 levels
-    const int pair = kp.cb_bits == 4;
+  if (KMODE == KVC_MODE_CODEBOOK) {  // pairs of 16 levels, 256 levels, or pairs once per lane
+    const int wb = kp.cb_bits, lm = (1 << wb) - 1, n = pair_entries(wb, kp.D) * 32;
     auto half_of = [&](int c) {
       return (uint32_t)__half_as_ushort(__float2half_rn(kp.codebook[c] * t.cb_mul));
     };
-    for (int j = tid; j < 256; j += R::threads)
-      tab[j] = pair ? half_of(j & 15) | (half_of(j >> 4) << 16) : half_of(j);
+    if (wb >= 4) {
+      for (int j = tid; j < 256; j += R::threads)
+        tab[j] = wb == 4 ? half_of(j & 15) | (half_of(j >> 4) << 16) : half_of(j);
+    } else {
+      for (int j = tid; j < n; j += R::threads)
+        tab[j] = half_of((j >> 5) & lm) | (half_of(j >> (5 + wb)) << 16);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -489,42 +538,40 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
         mbar_wait_bounded(&side_full[j & (kSideRing - 1)], (j / kSideRing) & 1, kWaitNs);
     } else if (warp == R::score) {
       // ---------------------------------------------------------- S = A W^T
-      // The whole warp walks and waits, one elected lane issues, so that
-      // descriptors stay in uniform registers; the two products have a warp
-      // each.  (One lane walking and issuing both took 160 cycles per MMA.)
+      // The whole warp walks and waits, one elected lane issues; the two products
+      // have a warp each.  (One lane walking and issuing both took 160 cycles per
+      // MMA, where the tensor core takes 27 to 64.)
       Segment g;
-      const bool leader = elect_one();
+      const uint32_t lead = elect_one();
       constexpr uint32_t id = idesc_f16(kTile, N, 0);
+      const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
       const uint64_t w_desc = desc_kmajor_noswizzle(smem_u32(Ws), 128, (uint32_t)z.KC * 128);
       int it = 0, segs = 0;
       while (walk.next(t, kp.H, g)) {
-        if (g.tile0 == g.tile1) continue;
+        const int tiles = __shfl_sync(0xffffffffu, g.tile1 - g.tile0, 0);
+        if (tiles == 0) continue;
         wait_or_abort(&w_full, segs & 1, &abort_flag);
         ++segs;
-        for (int tile = g.tile0; tile < g.tile1; ++tile, ++it) {
+        for (int i = 0; i < tiles; ++i, ++it) {
           const int a = it & 1, s = it % SB;
           if (it >= SB) wait_or_abort(&s_empty[s], (it / SB - 1) & 1, &abort_flag);
           wait_or_abort(&a_full[a], (it >> 1) & 1, &abort_flag);
           __syncwarp();
           tc_fence_after();
-          if (leader) {
-            const uint32_t a0 = tm + a * z.a_cols, d0 = tm + z.s_col + s * N;
-            umma_f16_tmem_a(d0, a0, w_desc, id, 0u);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {  // the two pieces of W
-              const uint64_t wd = w_desc + ((p * w_piece) >> 4);
-#pragma unroll 8
-              for (int ks = 1 - p; ks < z.K / 16; ++ks)  // 16 fp16 of K: 8 TMEM columns of A
-                umma_f16_tmem_a(d0, a0 + ks * 8, wd + ks * 16, id, 1u);
-            }
-            umma_commit(&s_full[s]);
-            umma_commit(&a_empty[a]);
-            if (tile + 1 == g.tile1) umma_commit(&w_empty);
+          const uint32_t a0 = tmu + a * z.a_cols, d0 = tmu + z.s_col + s * N;
+          // both pieces of W; 16 fp16 of K are 8 TMEM columns of A
+          for (int p = 0; p < 2; ++p) {
+            const uint64_t wd = w_desc + ((p * w_piece) >> 4);
+#pragma unroll 4
+            for (int ks = 0; ks < z.K / 16; ++ks)
+              mma_tmem_a(lead, d0, a0 + ks * 8, wd + ks * 16, id, p + ks > 0);
           }
-          __syncwarp();
+          commit_if(lead, &s_full[s]);
+          commit_if(lead, &a_empty[a]);
+          if (i + 1 == tiles) commit_if(lead, &w_empty);
         }
       }
-      if (leader) {
+      if (lead) {
         umma_commit(&done_bar);  // TMEM is released only after every MMA has finished
         mbar_wait_bounded(&done_bar, 0, kWaitNs);
       }
@@ -534,9 +581,10 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
       // One product per tile, or, where the groups split the columns, one per
       // group as its weights arrive.
       Segment g;
-      const bool leader = elect_one();
+      const uint32_t lead = elect_one();
       constexpr uint32_t id = idesc_f16(kTile, NC, 0) | kTransposeAB;
       constexpr uint32_t p_k = N * 16;  // bytes between P's cores along the tokens
+      const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
       const uint32_t v_k = (uint32_t)z.mt * 2048;
       const uint64_t v_desc = desc_mnmajor(smem_u32(Vs), v_k, 128);
       const uint64_t p_desc = desc_mnmajor(smem_u32(Ps), p_k, 128);
@@ -545,7 +593,8 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
       int it = 0;
       Ring rv(z.nv);
       while (walk.next(t, kp.H, g)) {
-        for (int tile = g.tile0; tile < g.tile1; ++tile, ++it, rv.next()) {
+        const int tiles = __shfl_sync(0xffffffffu, g.tile1 - g.tile0, 0);
+        for (int i = 0; i < tiles; ++i, ++it, rv.next()) {
           wait_or_abort(&v_full[rv.slot], rv.phase, &abort_flag);
 #pragma unroll
           for (int h = 0; h < (HALVES ? 2 : 1); ++h) {
@@ -553,29 +602,22 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
             wait_or_abort(&p_full[wg], (HALVES ? it : it >> 1) & 1, &abort_flag);
             __syncwarp();
             tc_fence_after();
-            if (leader) {
-              // the group's first tile of the segment overwrites its O
-              const uint32_t add = tile - g.tile0 >= (HALVES ? 1 : 2) ? 1u : 0u;
-              for (int m = 0; m < z.mt; ++m) {
-                const uint32_t o = tm + z.o_col + (HALVES ? m * N + h * NC : (wg * z.mt + m) * N);
-                uint64_t vd = v_desc + ((rv.slot * v_bytes + m * 2048) >> 4);
-                uint64_t pd = p_desc + ((HALVES ? h * (NC / 8 * 128) : wg * p_bytes) >> 4);
-                umma_f16(o, vd, pd, id, add);
+            // the group's first tile of the segment overwrites its O
+            const uint32_t add = i >= (HALVES ? 1 : 2);
+            for (int m = 0; m < z.mt; ++m) {
+              const uint32_t o = tmu + z.o_col + (HALVES ? m * N + h * NC : (wg * z.mt + m) * N);
+              const uint64_t vd = v_desc + ((rv.slot * v_bytes + m * 2048) >> 4);
+              const uint64_t pd = p_desc + ((HALVES ? h * (NC / 8 * 128) : wg * p_bytes) >> 4);
 #pragma unroll
-                for (int ks = 1; ks < kTile / 16; ++ks) {
-                  vd += v_step;
-                  pd += p_step;
-                  umma_f16(o, vd, pd, id, 1u);
-                }
-              }
-              umma_commit(&p_empty[wg]);
-              if (!HALVES || h == 1) umma_commit(&v_empty[rv.slot]);
+              for (int ks = 0; ks < kTile / 16; ++ks)
+                mma_smem(lead, o, vd + ks * v_step, pd + ks * p_step, id, ks ? 1u : add);
             }
-            __syncwarp();
+            commit_if(lead, &p_empty[wg]);
+            if (!HALVES || h == 1) commit_if(lead, &v_empty[rv.slot]);
           }
         }
       }
-      if (leader) {
+      if (lead) {
         umma_commit(&done_bar);
         mbar_wait_bounded(&done_bar, 0, kWaitNs);
       }
@@ -594,7 +636,7 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
     const int octet = lane >> 3, t8 = lane & 7;
     const int vblk = (dtid >> 5) * 2 + (octet >> 1);
     Levels levels{};
-    if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits <= 3) {
+    if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits <= 3 && kp.D != 128) {
       uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -639,9 +681,9 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
         if (KMODE == KVC_MODE_CODEBOOK && kp.cb_bits <= 3 && kp.D == 128) {
           const int W = kp.cb_bits;
           const unsigned char* src = st + tt * Pk + half * 8 * W;
-          if (W == 3) codebook64<3>(src, levels, a_tm + half * 32);
-          else if (W == 2) codebook64<2>(src, levels, a_tm + half * 32);
-          else codebook64<1>(src, levels, a_tm + half * 32);
+          if (W == 3) codebook64<3>(src, tab, 4 * lane, a_tm + half * 32);
+          else if (W == 2) codebook64<2>(src, tab, 4 * lane, a_tm + half * 32);
+          else codebook64<1>(src, tab, 4 * lane, a_tm + half * 32);
         } else {
           for (int c = half; c < z.KC; c += 2) {
             const uint32_t ent = kch[grp][c];
@@ -1058,7 +1100,7 @@ TcKernel kernel_for(int kmode, int vmode, const Shape& z, int* threads, int* reg
 
 // Layout for nc columns a softmax thread (halves = 2: 2 nc columns in all), or
 // false when TMEM or shared memory does not hold it.
-bool shape_for(const Params& kp, const TreeArgs& t, int nc, int halves, Shape* out) {
+bool shape_for(const Params& kp, bool vu, const TreeArgs& t, int nc, int halves, Shape* out) {
   Shape z{};
   z.nc = nc;
   z.halves = halves;
@@ -1075,17 +1117,15 @@ bool shape_for(const Params& kp, const TreeArgs& t, int nc, int halves, Shape* o
   for (z.cols = 32; z.cols < cols; z.cols *= 2) {}
   auto up = [](int v) { return (v + 127) / 128 * 128; };
   z.krow = up(kTile * t.Pk_max + 16);
-  z.stage = z.krow + up(kTile * t.Pv_max + 16);
+  z.stage = z.krow + up(kTile * t.Pv_max + (vu ? 16 : 0));
   z.off_p = 2 * z.n * z.K * 2;
   z.off_v = z.off_p + groups * z.n * kTile * 2;
-  const int tab = kp.mode == KVC_MODE_CODEBOOK && kp.cb_bits >= 4 ? 1024 : 0;
   // two V buffers and four row stages, or what fits
-  const int most = 212 * 1024;  // of 227 KB: the static arrays take up to 14
+  const int most = 227 * 1024 - 22 * 1024;  // the static arrays take up to 22 KB
   for (z.nv = 2; z.nv >= 1; --z.nv)
     for (z.ns = kMaxNS; z.ns >= 2; --z.ns) {
       z.off_stage = z.off_v + z.nv * z.mt * kTile * 256;
-      z.off_tab = z.off_stage + z.ns * z.stage;
-      z.smem = z.off_tab + tab;
+      z.smem = z.off_stage + z.ns * z.stage;
       if (z.smem <= most) {
         *out = z;
         return true;
@@ -1094,13 +1134,13 @@ bool shape_for(const Params& kp, const TreeArgs& t, int nc, int halves, Shape* o
   return false;
 }
 
-bool choose_shape(const Params& kp, const TreeArgs& t, Shape* z) {
+bool choose_shape(const Params& kp, const Params& vp, const TreeArgs& t, Shape* z) {
   // the fewest columns that hold all rows, else the most that fit
   static const int kShapes[4][2] = {{16, 1}, {32, 1}, {64, 1}, {64, 2}};
   bool ok = false;
   for (const auto& s : kShapes) {
     Shape c;
-    if (!shape_for(kp, t, s[0], s[1], &c)) continue;
+    if (!shape_for(kp, vp.mode == KVC_MODE_UNIFORM, t, s[0], s[1], &c)) continue;
     *z = c;
     ok = true;
     if (c.n >= t.rows) break;
@@ -1114,7 +1154,7 @@ int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t, int* par
   if (t.prod) return 0;
   if (vp.mode == KVC_MODE_INT8 && vp.D % 8) return 0;  // value rows are read 8 bytes at a time
   Shape z;
-  if (!choose_shape(kp, t, &z)) return 0;
+  if (!choose_shape(kp, vp, t, &z)) return 0;
   *parts = z.halves == 2 ? 1 : 2;
   *K = z.K;
   return z.n;
@@ -1123,7 +1163,7 @@ int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t, int* par
 cudaError_t launch_tree_tc(const Params& kp, const Params& vp, const TreeArgs& t, cudaStream_t s,
                            int* nk) {
   Shape z;
-  if (!choose_shape(kp, t, &z)) return cudaErrorInvalidValue;
+  if (!choose_shape(kp, vp, t, &z)) return cudaErrorInvalidValue;
   int threads = 0, regs = 0;
   TcKernel k = kernel_for(kp.mode, vp.mode, z, &threads, &regs);
   // the register split draws on what the launch gives: never launch with less
