@@ -272,7 +272,7 @@ kvc_status kvc_attend_workspace_bytes(const kvc_layer *keys, const kvc_layer *va
  *             q + b*q_stride_b + hq*q_stride_h + i*q_stride_t (elements); the D
  *             values of a row are contiguous.
  *  Hq         query heads, any multiple of H.
- *  N          drafts, 1 .. length.  N = 1 without a mask is a plain decode step.
+ *  N          drafts, 1 .. length, at most 65536.  N = 1 without a mask is a plain decode step.
  *  mask       device bytes [N][N] (row: the draft that looks, column: the one
  *             seen), entry b at mask + b*mask_stride_b (0: one mask for the
  *             batch); NULL: drafts form a chain, j <= i.

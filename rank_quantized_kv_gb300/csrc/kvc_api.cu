@@ -896,6 +896,7 @@ static kvc_status tree_check(const kvc_layer* K, const kvc_layer* V, int32_t Hq,
   if (K->ncpos > 256 || (V->mode == KVC_MODE_UNIFORM && V->ncpos > 256))
     return fail(KVC_EINVAL, "more than 256 packed positions");
   // kernels number tokens, (slot, row) pairs and (job, CTA) pairs in 32 bits
+  if (N > 65536) return fail(KVC_EINVAL, "more than 65536 drafts");
   if (K->len > INT32_MAX - 1024) return fail(KVC_EINVAL, "more than 2^31 - 1024 tokens");
   if ((int64_t)K->B * Hq * N > (1 << 30)) return fail(KVC_EINVAL, "too many query rows");
   t.Hq = Hq;

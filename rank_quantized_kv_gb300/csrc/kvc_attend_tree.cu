@@ -107,6 +107,22 @@ __device__ __forceinline__ float load_q(const TreeArgs& t, int64_t i) {
 // latency of one pass, for which blocks of 8 rows spread few rows over the SMs.
 constexpr int kPrepCols = 128, kPrepK = 32;
 
+// The mask as bits, transposed: word w of draft j holds the drafts 32 w .. that
+// see j.  One block per (mask, w, 256 drafts).
+__device__ void pack_mask(const TreeArgs& t, int block) {
+  const int words = (t.N + 31) / 32, cols = (t.N + kPrepThreads - 1) / kPrepThreads;
+  const int jb = block % cols, w = block / cols % words, b = block / cols / words;
+  const int j = jb * kPrepThreads + threadIdx.x;
+  grid_dependents_launch();
+  if (j >= t.N) return;
+  const uint8_t* m = t.mask + b * t.mask_sb + (int64_t)w * 32 * t.N + j;
+  uint32_t v = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (w * 32 + i < t.N && m[(int64_t)i * t.N]) v |= 1u << i;
+  t.mask_bits[((size_t)b * t.N + j) * words + w] = v;
+}
+
 template <int RT>
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp, const TreeArgs t) {
   constexpr int kPrepRows = 4 * RT;
@@ -116,6 +132,10 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
   __shared__ float down[kPrepRows];  // power of two that brings a row into fp16's range
   const int D = kp.D, r = kp.r, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int blocks = (t.prow + kPrepRows - 1) / kPrepRows;
+  if ((int)blockIdx.x >= blocks * kp.n_slots) {
+    pack_mask(t, blockIdx.x - blocks * kp.n_slots);
+    return;
+  }
   const int slot = blockIdx.x / blocks, r0 = (blockIdx.x - slot * blocks) * kPrepRows;
   const int b = slot / kp.H, h = slot - b * kp.H;
   const int beta = kp.basis_of[slot];
@@ -719,6 +739,9 @@ size_t c1_bytes(const Params& kp, const TreeArgs& t) {  // score offsets; row sc
 size_t ml_bytes(int64_t jobs, const TreeArgs& t) {
   return align256((size_t)(jobs + t.grid - 1) * t.parts * t.rt * 8);
 }
+size_t mask_bytes(const Params& kp, const TreeArgs& t) {
+  return t.tc ? align256((size_t)kp.B * t.N * ((t.N + 31) / 32) * 4) : 0;
+}
 size_t wx_bytes(const Params& kp, const TreeArgs& t) {
   return align256((size_t)kp.n_slots * t.rows * (t.m + t.n_out) * 4);
 }
@@ -750,7 +773,8 @@ size_t tree_plan(const Params& kp, TreeArgs& t, int sms) {
   t.grid = (int)std::min<int64_t>(t.total, (t.tc ? 1 : 12) * (int64_t)sms);
   t.Dvp = (t.Dv + 3) / 4 * 4;
   t.sms = sms;
-  return w_bytes(kp, t) + 2 * c1_bytes(kp, t) + wx_bytes(kp, t) + ml_bytes(jobs, t) +
+  return w_bytes(kp, t) + 2 * c1_bytes(kp, t) + wx_bytes(kp, t) + mask_bytes(kp, t) +
+         ml_bytes(jobs, t) +
          align256((size_t)(jobs + t.grid - 1) * t.parts * t.rt * t.Dvp * 4);
 }
 
@@ -766,6 +790,8 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
   ws += c1_bytes(kp, t);
   t.wx = reinterpret_cast<float*>(ws);
   ws += wx_bytes(kp, t);
+  t.mask_bits = reinterpret_cast<uint32_t*>(ws);
+  ws += mask_bytes(kp, t);
   t.ml = reinterpret_cast<float2*>(ws);
   ws += ml_bytes((int64_t)kp.n_slots * t.row_tiles, t);
   t.part = reinterpret_cast<float*>(ws);
@@ -784,7 +810,9 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
   const auto prep = few ? tree_prep_kernel<2> : tree_prep_kernel<8>;
   e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  prep<<<(unsigned)kp.n_slots * ((t.prow + rows - 1) / rows), kPrepThreads, smem, s>>>(kp, t);
+  const int masks = t.tc && t.mask ? (t.mask_sb ? kp.B : 1) : 0;  // blocks that pack the mask
+  const int pack = masks * ((t.N + 31) / 32) * ((t.N + kPrepThreads - 1) / kPrepThreads);
+  prep<<<(unsigned)kp.n_slots * ((t.prow + rows - 1) / rows) + pack, kPrepThreads, smem, s>>>(kp, t);
   ++*nk;
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -64,21 +64,21 @@ constexpr float kSet = 6.f;        // a reference is set this far below the maxi
 constexpr float kMove = 12.f;      // and moves when a score lies this far above it
 
 // Roles by warp: softmax 0..7, decoders 8.., then producer, S and O issuers and
-// one idle warp (setmaxnreg works on whole groups of four).  Up to 32 columns a
-// thread, two decoder groups take alternate tiles; 64 columns a thread need
-// the registers of the second group.  The registers of the launch
+// one idle warp (setmaxnreg works on whole groups of four).  Two decoder groups
+// take alternate tiles; jobs of 128 rows, which decode a tile for twice the rows,
+// give the second group's registers to the softmax.  The registers of the launch
 // (65536 / threads, rounded down to 8) are split among the roles; ptxas is held
 // to them by the launch bounds and the host checks that it used them all.
-template <int NC>
+template <int NC, bool HALVES>
 struct Roles {
-  static constexpr int dec_groups = NC <= 32 ? 2 : 1;
+  static constexpr int dec_groups = HALVES ? 1 : 2;
   static constexpr int prod = kSoftWarps + dec_groups * kGroupWarps;
   static constexpr int score = prod + 1, sum = prod + 2;
   static constexpr int threads = (prod + 4) * 32;
   static constexpr int launch_regs = 65536 / threads / 8 * 8;
-  static constexpr int ctl_regs = NC <= 32 ? 56 : 64;
-  static constexpr int dec_regs = NC <= 32 ? 56 : 72;
-  static constexpr int soft_regs = NC <= 32 ? 112 : 136;
+  static constexpr int ctl_regs = HALVES ? 64 : NC <= 32 ? 56 : 48;
+  static constexpr int dec_regs = HALVES ? 72 : NC <= 32 ? 56 : 48;
+  static constexpr int soft_regs = HALVES ? 136 : NC <= 32 ? 112 : 128;
   static_assert(128 * (ctl_regs + 2 * dec_groups * dec_regs + 2 * soft_regs) <= threads * launch_regs,
                 "register split exceeds the launch's registers");
 };
@@ -380,7 +380,7 @@ struct Place {
   // softmax
   int plain0, plain1;  // tiles that hold visible context alone
   int first;
-  const uint8_t* mask;
+  const uint32_t* mask;  // per draft, which drafts see it
   int scaled;          // some row's key weights were beyond fp16's range
   int Pk, Pv;          // decoders: row bytes
   __device__ void next(const TreeArgs& t, int H) { more = w.next(t, H, g); }
@@ -415,9 +415,9 @@ __device__ __forceinline__ void wait_or_abort(uint64_t* bar, uint32_t parity, vo
 }
 
 template <int KMODE, int VMODE, int NC, bool HALVES>
-__global__ void __launch_bounds__(Roles<NC>::threads, 1)
+__global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
     tree_tc_kernel(const Params kp, const Params vp, const TreeArgs t, const Shape z) {
-  using R = Roles<NC>;
+  using R = Roles<NC, HALVES>;
   constexpr bool VU = VMODE == KVC_MODE_UNIFORM;
   constexpr int N = HALVES ? 2 * NC : NC;  // columns
   constexpr int CH = NC < 32 ? NC : 32;    // columns handled at a time
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
           pl.first = first;
           pl.plain0 = (int)min(t.tps, ((int64_t)first + kTile - 1) / kTile);
           pl.plain1 = (int)(t.ctx / kTile);
-          pl.mask = t.mask ? t.mask + pl.g.b * t.mask_sb : nullptr;
+          pl.mask = t.mask ? t.mask_bits + (t.mask_sb ? (size_t)pl.g.b : 0) * t.N * ((t.N + 31) / 32) : nullptr;
         }
       }
       named_bar_sync(bar, 128);
@@ -842,19 +842,23 @@ __global__ void __launch_bounds__(Roles<NC>::threads, 1)
               } else {
                 vis = 0ull;
                 if (draft < t.N) {
-                  const int nc = min(NC, pl.g.nr - col0);
+                  // the drafts n that see this one: a bit each, repeated for
+                  // every query head of the group's columns
+                  const int nc = min(NC, pl.g.nr - col0), words = (t.N + 31) / 32;
+                  const uint32_t* bits = pl.mask ? pl.mask + draft * words : nullptr;
+                  const uint32_t only = bits && words == 1 ? bits[0] : 0u;
                   int n = (pl.g.r0 + col0) % t.N;
-                  const uint8_t* col = pl.mask + draft;
 #pragma unroll 1
-                  for (int c0 = 0; c0 < nc; c0 += 8) {  // eight loads in flight
-                    uint32_t m[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                      m[c] = c0 + c >= nc ? 0 : pl.mask ? col[(int64_t)n * t.N] : draft <= n;
-                      if (++n == t.N) n = 0;
-                    }
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) vis |= (uint64_t)(m[c] != 0) << (c0 + c);
+                  for (int c = 0; c < nc;) {
+                    const int take = min(min(t.N - n, nc - c), 32), w = n >> 5, sh = n & 31;
+                    uint32_t v;
+                    if (!bits) v = draft <= n ? ~0u : draft - n < 32 ? ~0u << (draft - n) : 0u;
+                    else if (words == 1) v = only >> sh;
+                    else v = __funnelshift_r(bits[w], w + 1 < words ? bits[w + 1] : 0u, sh);
+                    if (take < 32) v &= (1u << take) - 1u;
+                    vis |= (uint64_t)v << c;
+                    c += take;
+                    if ((n += take) == t.N) n = 0;
                   }
                 }
               }
@@ -1078,9 +1082,11 @@ TcKernel kernel_for_shape(const Shape& z, int* threads, int* regs) {
     *threads = decltype(roles)::threads;
     *regs = decltype(roles)::launch_regs;
   };
-  if (z.nc <= 32) use(Roles<32>{});
-  else use(Roles<64>{});
-  if (z.halves == 2) return tree_tc_kernel<KMODE, VMODE, 64, true>;
+  if (z.halves == 2) {
+    use(Roles<64, true>{});
+    return tree_tc_kernel<KMODE, VMODE, 64, true>;
+  }
+  use(Roles<64, false>{});
   switch (z.nc) {
     case 16: return tree_tc_kernel<KMODE, VMODE, 16, false>;
     case 32: return tree_tc_kernel<KMODE, VMODE, 32, false>;

@@ -152,6 +152,8 @@ struct TreeArgs {
   // cores, two fp16 pieces per job in the operand's layout [jobs][2][rt x K]; a
   // power of two that multiplies a row's scores (1 but for weights beyond fp16's
   // range); the score offsets.  Rows padded to prow per slot (whole jobs).
+  uint32_t* mask_bits = nullptr;         // tensor cores: [B or 1][N][N / 32] bits, bit n of
+                                         // draft j set where draft n sees j
   float* w = nullptr;
   uint16_t* w16 = nullptr;
   float* wscale = nullptr;
