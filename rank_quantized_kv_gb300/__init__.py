@@ -12,7 +12,6 @@ is no CPU fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -539,9 +538,10 @@ def attend_tree(keys: "KVCacheLayer", values: "KVCacheLayer", q, mask=None, firs
     layer's out_dtype, zero rows where a draft sees no token."""
     import torch
 
-    lib = load_library()
-    rev = {v: k for k, v in _torch_dtypes().items()}
-    if q.dim() != 4 or q.dtype not in rev or q.stride(3) != 1:
+    lib = keys._lib
+    dt = _torch_dtypes()
+    q_dtype = 0 if q.dtype == dt["f32"] else 1 if q.dtype == dt["f16"] else 2 if q.dtype == dt["bf16"] else -1
+    if q.dim() != 4 or q_dtype < 0 or q.stride(3) != 1:
         raise ValueError("q must be [B, Hq, N, D] fp32/fp16/bf16 with a contiguous last dimension")
     B, Hq, N, D = q.shape
     if B != keys.B or D != keys.D:
@@ -556,24 +556,30 @@ def attend_tree(keys: "KVCacheLayer", values: "KVCacheLayer", q, mask=None, firs
     if first is not None and (first.dtype != torch.int32 or tuple(first.shape) != (B,)
                               or not first.is_contiguous()):
         raise ValueError(f"first must be a contiguous int32 tensor [{B}]")
-    n = c_size_t()
-    _check(lib.kvc_attend_tree_workspace_bytes(keys._h, values._h, Hq, N, byref(n)))
-    # what the call allocates belongs to the stream that uses it
-    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-        if out is None:
-            out = torch.empty(B, Hq, N, D, dtype=_torch_dtypes()[values.out_dtype], device=keys.device)
-        if workspace is None:
-            workspace = torch.empty(int(n.value), dtype=torch.uint8, device=keys.device)
-    if (out.shape != q.shape or out.dtype != _torch_dtypes()[values.out_dtype]
-            or out.stride(3) != 1):
+    out_dt = dt[values.out_dtype]
+    if out is None or workspace is None:
+        # what the call allocates belongs to the stream that uses it
+        ctx = None if stream is None else torch.cuda.stream(stream)
+        if ctx is not None:
+            ctx.__enter__()
+        try:
+            if out is None:
+                out = torch.empty((B, Hq, N, D), dtype=out_dt, device=keys.device)
+            if workspace is None:
+                n = c_size_t()
+                _check(lib.kvc_attend_tree_workspace_bytes(keys._h, values._h, Hq, N, byref(n)))
+                workspace = torch.empty(n.value, dtype=torch.uint8, device=keys.device)
+        finally:
+            if ctx is not None:
+                ctx.__exit__(None, None, None)
+    if out.shape != q.shape or out.dtype != out_dt or out.stride(3) != 1:
         raise ValueError("out must be [B, Hq, N, D] of the value layer's out_dtype, last dimension contiguous")
-    d = _TreeDesc(q=q.data_ptr(), q_dtype=DTYPES[rev[q.dtype]], Hq=Hq, N=N, q_stride_b=q.stride(0),
-                  q_stride_h=q.stride(1), q_stride_t=q.stride(2),
-                  mask=None if mask is None else mask.data_ptr(), mask_stride_b=mask_stride,
-                  first=None if first is None else first.data_ptr(), scale=float(scale),
-                  out=out.data_ptr(), out_stride_b=out.stride(0), out_stride_h=out.stride(1),
-                  out_stride_t=out.stride(2))
-    _check(lib.kvc_attend_tree(keys._h, values._h, byref(d), c_void_p(workspace.data_ptr()),
+    qb, qh, qt, _ = q.stride()
+    ob, oh, ot, _ = out.stride()
+    d = _TreeDesc(q.data_ptr(), q_dtype, Hq, N, qb, qh, qt, None if mask is None else mask.data_ptr(),
+                  mask_stride, None if first is None else first.data_ptr(), scale, out.data_ptr(), ob,
+                  oh, ot)
+    _check(lib.kvc_attend_tree(keys._h, values._h, byref(d), workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(),
                                _stream_ptr(stream, keys.device)))
     return out

@@ -754,7 +754,7 @@ cudaError_t launch_main(const Params& kp, const Params& vp, const TreeArgs& t, c
                       4 * (size_t)(kstage + vstage + 32 * kRows * 4) +
                       4 * (size_t)kRows * (2 + t.Dv) * 4;
   MainKernel k = main_kernel_for(kp.mode, vp.mode);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), (int)smem);
   if (e != cudaSuccess) return e;
   ++*nk;
   return launch_dependent(k, (unsigned)t.grid, kThreads, smem, s, kp, vp, t, kstage, vstage);
@@ -808,7 +808,7 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
   const size_t smem =
       (size_t)(kp.D * rows + 2 * kPrepK * kPrepCols + rows * (kp.r | 1)) * sizeof(float);
   const auto prep = few ? tree_prep_kernel<2> : tree_prep_kernel<8>;
-  e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = prepare_kernel(reinterpret_cast<const void*>(prep), (int)smem);
   if (e != cudaSuccess) return e;
   const int masks = t.tc && t.mask ? (t.mask_sb ? kp.B : 1) : 0;  // blocks that pack the mask
   const int pack = masks * ((t.N + 31) / 32) * ((t.N + kPrepThreads - 1) / kPrepThreads);

@@ -1173,12 +1173,10 @@ cudaError_t launch_tree_tc(const Params& kp, const Params& vp, const TreeArgs& t
   int threads = 0, regs = 0;
   TcKernel k = kernel_for(kp.mode, vp.mode, z, &threads, &regs);
   // the register split draws on what the launch gives: never launch with less
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, k);
+  int has = 0;
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), z.smem, &has);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != regs) return cudaErrorLaunchOutOfResources;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, z.smem);
-  if (e != cudaSuccess) return e;
+  if (has != regs) return cudaErrorLaunchOutOfResources;
   ++*nk;
   return launch_dependent(k, (unsigned)t.grid, threads, (size_t)z.smem, s, kp, vp, t, z);
 }

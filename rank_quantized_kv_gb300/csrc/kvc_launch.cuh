@@ -18,6 +18,36 @@ __device__ __forceinline__ void grid_dependents_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Attributes of a kernel on the current device, asked for once per thread: its
+// registers, and the dynamic shared memory that it may use raised to `smem`.
+// (Both calls take about a microsecond, which a decode step notices.)
+inline cudaError_t prepare_kernel(const void* kernel, int smem, int* regs = nullptr) {
+  struct Entry { const void* kernel; int device, smem, regs; };
+  thread_local Entry cache[64];
+  thread_local int n = 0;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  Entry* at = nullptr;
+  for (int i = 0; i < n; ++i)
+    if (cache[i].kernel == kernel && cache[i].device == device) at = &cache[i];
+  Entry fresh{kernel, device, -1, 0};
+  if (!at) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    fresh.regs = fa.numRegs;
+    at = n < 64 ? &(cache[n++] = fresh) : &fresh;
+  }
+  if (smem > at->smem) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    at->smem = smem;
+  }
+  if (regs) *regs = at->regs;
+  return cudaSuccess;
+}
+
 template <class... Params, class... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
                              cudaStream_t stream, const Args&... args) {

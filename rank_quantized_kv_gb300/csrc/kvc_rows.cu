@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "kvc_internal.h"
+#include "kvc_launch.cuh"
 
 namespace kvc {
 
@@ -217,8 +218,7 @@ cudaError_t launch_accept(const Params& p, AcceptArgs a, int pmax, cudaStream_t 
   a.cw = accept_columns_per_block(a.n, widest);
   a.pay_chunks = (pmax + a.cw - 1) / a.cw;
   const int side_chunks = (p.side_bytes + a.cw - 1) / a.cw;
-  const cudaError_t e = cudaFuncSetAttribute(
-      accept_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAcceptStage);
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(accept_kernel), kAcceptStage);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)p.n_slots, (unsigned)(a.pay_chunks + side_chunks));
   accept_kernel<<<grid, kThreads, (size_t)a.n * a.cw, s>>>(p, a);
