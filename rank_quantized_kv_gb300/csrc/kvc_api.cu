@@ -981,7 +981,6 @@ kvc_status kvc_attend_tree(const kvc_layer* K, const kvc_layer* V, const kvc_tre
   t.o_sb = d->out_stride_b;
   t.o_sh = d->out_stride_h;
   t.o_st = d->out_stride_t;
-  t.o_vec = (uintptr_t)d->out % 8 == 0 && (D | t.o_sb | t.o_sh | t.o_st) % 4 == 0;
   const double sc = d->scale > 0.f ? (double)d->scale : 1.0 / std::sqrt((double)K->D);
   t.scale_log2 = (float)(sc * 1.4426950408889634);
   int nk = 0;

@@ -101,9 +101,9 @@ __device__ __forceinline__ float load_q(const TreeArgs& t, int64_t i) {
 // The key weights at every packed position (for the tensor cores: split into two
 // fp16 pieces and laid out as their operand), w_j = scale log2(e) u_j coef_j
 // (coef = step in uniform mode, 1 for a codebook), and c1.  One block per (slot,
-// 4 RT rows): u = q V as a register-tiled product, RT rows x 2 columns a thread,
-// over 128 columns at a time; q stays in shared memory, V passes through it 32
-// rows at a time.  Bound: fp32 FMA (rows D r of them) for wide trees, else the
+// 8 RT rows): u = q V as a register-tiled product, RT rows x 4 columns a thread, a
+// warp 128 columns; q stays in shared memory, V passes through it 32 rows at a
+// time.  Bound: fp32 FMA (rows D r of them) for wide trees, else the
 // latency of one pass, for which blocks of 8 rows spread few rows over the SMs.
 constexpr int kPrepCols = 128, kPrepK = 32;
 
@@ -125,7 +125,7 @@ __device__ void pack_mask(const TreeArgs& t, int block) {
 
 template <int RT>
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp, const TreeArgs t) {
-  constexpr int kPrepRows = 4 * RT;
+  constexpr int kPrepRows = 8 * RT;
   extern __shared__ __align__(16) float sm_f[];
   __shared__ int comp[256];       // packed position: component (-1: padding) and its factor
   __shared__ float coef[256];
@@ -143,9 +143,10 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
   const int np = min(kPrepRows, t.prow - r0);          // rows written
   const bool uniform = kp.mode == KVC_MODE_UNIFORM;
   const int us_row = r | 1;                    // an odd stride: rows in different banks
-  float* qs = sm_f;                            // [D][32] rows of q, transposed
-  float* vs = qs + D * kPrepRows;              // [2][32][128] rows of V
-  float* us = vs + 2 * kPrepK * kPrepCols;     // [32][us_row] products
+  constexpr int kQ = kPrepRows + 4;            // stores of q then meet four to a bank, not all
+  float* qs = sm_f;                            // [D][kQ] rows of q, transposed
+  float* vs = qs + D * kQ;              // [2][32][128] rows of V
+  float* us = vs + 2 * kPrepK * kPrepCols;     // [kPrepRows][us_row] products
   grid_dependents_launch();
   const float* V = kp.V + (size_t)beta * D * r;
   const int stages = (D + kPrepK - 1) / kPrepK;
@@ -179,8 +180,8 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
     comp[j] = k;
     coef[j] = k < 0 ? 0.f : t.scale_log2 * t.w_mul * (uniform ? kp.step[(size_t)beta * r + k] : 1.f);
   }
-  // a warp takes four rows, each read 32 values at a time, all loads issued
-  // before the first is stored
+  // a warp takes every eighth row, 32 values at a time, all loads issued before
+  // the first is stored
   for (int i0 = 0; i0 < D; i0 += 64) {
     float v[kPrepRows / 8][2];
 #pragma unroll
@@ -195,41 +196,54 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
     for (int u = 0; u < kPrepRows / 8; ++u)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        if (i0 + lane + 32 * e < D) qs[(i0 + lane + 32 * e) * kPrepRows + warp + 8 * u] = v[u][e];
+        if (i0 + lane + 32 * e < D) qs[(i0 + lane + 32 * e) * kQ + warp + 8 * u] = v[u][e];
   }
-  const int ty = tid >> 6, tx = tid & 63;  // 4 row groups of RT, 64 column pairs
   for (int c0 = 0; c0 < r; c0 += kPrepCols) {
-    float2 acc[RT];
+    float2 acc[RT][2];
 #pragma unroll
-    for (int e = 0; e < RT; ++e) acc[e] = make_float2(0.f, 0.f);
+    for (int e = 0; e < RT; ++e) acc[e][0] = acc[e][1] = make_float2(0.f, 0.f);
     if (c0) load_v(0, c0, 0);
     for (int st = 0; st < stages; ++st) {
       if (st + 1 < stages) load_v(st + 1, c0, (st + 1) & 1);
       __pipeline_wait_prior(st + 1 < stages ? 1 : 0);
       __syncthreads();
-      const float* vb = vs + (st & 1) * kPrepK * kPrepCols + 2 * tx;
-      const float* qb = qs + st * kPrepK * kPrepRows + RT * ty;
+      const float* vb = vs + (st & 1) * kPrepK * kPrepCols + 4 * lane;
+      const float* qb = qs + st * kPrepK * kQ + RT * warp;
       const int kn = min(kPrepK, D - st * kPrepK);
 #pragma unroll 8
       for (int k = 0; k < kn; ++k) {
-        const float2 v = *reinterpret_cast<const float2*>(vb + k * kPrepCols);
+        const float4 v = *reinterpret_cast<const float4*>(vb + k * kPrepCols);
         float q[RT];
+        if constexpr (RT % 4 == 0) {
 #pragma unroll
-        for (int e = 0; e < RT; e += 2) {
-          const float2 qq = *reinterpret_cast<const float2*>(qb + k * kPrepRows + e);
-          q[e] = qq.x;
-          q[e + 1] = qq.y;
+          for (int e = 0; e < RT; e += 4) {
+            const float4 qq = *reinterpret_cast<const float4*>(qb + k * kQ + e);
+            q[e] = qq.x;
+            q[e + 1] = qq.y;
+            q[e + 2] = qq.z;
+            q[e + 3] = qq.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < RT; ++e) q[e] = qb[k * kQ + e];
         }
 #pragma unroll
-        for (int e = 0; e < RT; ++e) acc[e] = __ffma2_rn(make_float2(q[e], q[e]), v, acc[e]);
+        for (int e = 0; e < RT; ++e) {
+          const float2 qq = make_float2(q[e], q[e]);
+          acc[e][0] = __ffma2_rn(qq, make_float2(v.x, v.y), acc[e][0]);
+          acc[e][1] = __ffma2_rn(qq, make_float2(v.z, v.w), acc[e][1]);
+        }
       }
       __syncthreads();  // the other buffer is refilled next
     }
+    const int c = c0 + 4 * lane;
 #pragma unroll
     for (int e = 0; e < RT; ++e) {
-      const int c = c0 + 2 * tx;
-      if (c < r) us[(RT * ty + e) * us_row + c] = acc[e].x;
-      if (c + 1 < r) us[(RT * ty + e) * us_row + c + 1] = acc[e].y;
+      float* u = us + (RT * warp + e) * us_row + c;
+      if (c < r) u[0] = acc[e][0].x;
+      if (c + 1 < r) u[1] = acc[e][0].y;
+      if (c + 2 < r) u[2] = acc[e][1].x;
+      if (c + 3 < r) u[3] = acc[e][1].y;
     }
   }
   __syncthreads();
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
         const int width = kp.bits[bk];
         if (width) c1 = fmaf(us[row * us_row + k], fmaf((float)(1 << (width - 1)), kp.step[bk], kp.lo[bk]), c1);
       }
-      for (int i = lane; i < D; i += 32) c1 = fmaf(qs[i * kPrepRows + row], kp.mean[(size_t)beta * D + i], c1);
+      for (int i = lane; i < D; i += 32) c1 = fmaf(qs[i * kQ + row], kp.mean[(size_t)beta * D + i], c1);
     }
     c1 = warp_sum(c1);
     if (t.tc) {
@@ -568,44 +582,33 @@ __global__ void __launch_bounds__(kThreads)
         }
       if (d == 0) t.ml[prow + g].x = v;
       else if (d == 1) t.ml[prow + g].y = v;
-      else t.part[(prow + g) * t.Dvp + d - 2] = v;
+      else t.part[prow * t.Dvp + (size_t)(d - 2) * t.rt + g] = v;
     }
   }
 }
 
 // ---------------------------------------------------------------- combine
 
-constexpr int kCombineWarps = 8;
+constexpr int kCombineRows = 8, kCombineThreads = 256, kFactors = 64;
 
-// One warp per row, eight rows of a slot per block: merge the partials of the
-// row's job, normalise and write the output row (uniform values: project the
-// weighted mean latent).  Lane l holds four consecutive sums from 4 l, and the
-// four of the next 128.
-__global__ void __launch_bounds__(kCombineWarps * 32)
+// Merge the partials of a job, normalise and write the output rows (uniform
+// values: project the weighted mean latent).  One block per (slot, 8 rows);
+// thread (d, q) holds channel d of rows 4 q .. 4 q + 3, which lie together in a
+// partial.
+__global__ void __launch_bounds__(kCombineThreads)
     tree_combine_kernel(const Params kp, const Params vp, const TreeArgs t) {
-  __shared__ float zb[kCombineWarps][256];
-  __shared__ short comp[256];       // uniform values: component of a packed position
+  __shared__ __align__(16) float fac[kFactors][kCombineRows];  // 2^(m - M) of the partials
+  __shared__ __align__(16) float zb[256][kCombineRows];  // uniform values: mean latents
+  __shared__ short comp[256];         // component of a packed position
   __shared__ float zs[256], zo[256];  // its step, and its offset lo + 2^(b-1) step
-  const int blocks = (t.rows + kCombineWarps - 1) / kCombineWarps;
-  const int slot = blockIdx.x / blocks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = (blockIdx.x - slot * blocks) * kCombineWarps + warp;
+  __shared__ float inv_s[kCombineRows];
+  const int blocks = (t.rows + kCombineRows - 1) / kCombineRows;
+  const int slot = blockIdx.x / blocks, row0 = (blockIdx.x - slot * blocks) * kCombineRows;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = slot / kp.H, h = slot - b * kp.H;
   const bool vu = vp.mode == KVC_MODE_UNIFORM;
   const int beta = vu ? vp.basis_of[slot] : 0;
-  if (vu) {
-    for (int j = threadIdx.x; j < t.Dv; j += kCombineWarps * 32) {
-      int width = 0;
-      const int k = position_component(vp, beta, j, &width);
-      const size_t bk = (size_t)beta * vp.r + (k < 0 ? 0 : k);
-      comp[j] = (short)k;
-      zs[j] = vp.step[bk];
-      zo[j] = k < 0 ? 0.f : fmaf((float)(1 << (width - 1)), vp.step[bk], vp.lo[bk]);
-    }
-    __syncthreads();
-  }
-  grid_dependency_wait();
-  if (row >= t.rows) return;
-  const int jt = row / t.rt, job = slot * t.row_tiles + jt, rr = row - jt * t.rt;
+  const int jt = row0 / t.rt, job = slot * t.row_tiles + jt, rr = row0 - jt * t.rt;
   // the CTAs whose runs hold the job's tiles
   const int64_t lo = job * t.tps, hi = lo + t.tps;
   int64_t c0 = lo * t.grid / t.total;
@@ -615,105 +618,99 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   while (run_begin(t, c1 + 1) < hi) ++c1;
   const int np = ((int)(c1 - c0) + 1) * t.parts;
   const size_t p0 = ((size_t)job + c0) * t.parts;
-  const float2* ml = t.ml + p0 * t.rt + rr;
-  const float* part = t.part + (p0 * t.rt + rr) * t.Dvp;
-  // lanes take the partials' references and sums, 32 at a time
-  float M = -INFINITY;
-  for (int s = lane; s < np; s += 32) M = fmaxf(M, ml[(size_t)s * t.rt].x);
+  if (vu)
+    for (int j = tid; j < t.Dv; j += kCombineThreads) {
+      int width = 0;
+      const int k = position_component(vp, beta, j, &width);
+      const size_t bk = (size_t)beta * vp.r + (k < 0 ? 0 : k);
+      comp[j] = (short)k;
+      zs[j] = vp.step[bk];
+      zo[j] = k < 0 ? 0.f : fmaf((float)(1 << (width - 1)), vp.step[bk], vp.lo[bk]);
+    }
+  grid_dependency_wait();
+  // row `warp`: the largest reference
+  const float2* ml = t.ml + p0 * t.rt + rr + warp;
+  const bool live = row0 + warp < t.rows;
+  float M = -INFINITY, L = 0.f;
+  if (live)
+    for (int s = lane; s < np; s += 32) M = fmaxf(M, ml[(size_t)s * t.rt].x);
   M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
+  const int d0 = tid & 127, q = tid >> 7;  // d0 and d0 + 128; row quad
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int s0 = 0; s0 < np; s0 += 32) {
-    const int s = s0 + lane;
-    float f = 0.f;
-    if (s < np) {
-      const float2 v = ml[(size_t)s * t.rt];
-      f = exp2f(v.x - ref);
+  for (int s0 = 0; s0 < np; s0 += kFactors) {
+    const int n = min(kFactors, np - s0);
+    __syncthreads();
+    for (int e = lane; e < n; e += 32) {
+      const float2 v = live ? ml[(size_t)(s0 + e) * t.rt] : make_float2(0.f, 0.f);
       // a run that saw nothing has l = 0 (and weighted sums of 0)
-      if (v.y == 0.f) f = 0.f;
-      else L = fmaf(f, v.y, L);
+      const float f = v.y == 0.f ? 0.f : exp2f(v.x - ref);
+      if (v.y != 0.f) L = fmaf(f, v.y, L);
+      fac[e][warp] = f;
     }
-    const int n = min(32, np - s0);
-#pragma unroll 4
-    for (int e = 0; e < n; ++e) {
-      const float fe = __shfl_sync(kFull, f, e);
-      const float* p = part + (size_t)(s0 + e) * t.rt * t.Dvp;
+    __syncthreads();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int d = 4 * lane + 128 * u;
-        if (d < t.Dvp) {
-          const float4 v = *reinterpret_cast<const float4*>(p + d);
-          acc[u].x = fmaf(fe, v.x, acc[u].x);
-          acc[u].y = fmaf(fe, v.y, acc[u].y);
-          acc[u].z = fmaf(fe, v.z, acc[u].z);
-          acc[u].w = fmaf(fe, v.w, acc[u].w);
-        }
+    for (int u = 0; u < 2; ++u) {
+      const int d = d0 + 128 * u;
+      if (d >= t.Dv) break;
+      const float* p = t.part + (p0 + s0) * t.rt * t.Dvp + (size_t)d * t.rt + rr + 4 * q;
+#pragma unroll 4
+      for (int e = 0; e < n; ++e) {
+        const float4 v = *reinterpret_cast<const float4*>(p + (size_t)e * t.rt * t.Dvp);
+        const float4 f = *reinterpret_cast<const float4*>(&fac[e][4 * q]);
+        acc[u].x = fmaf(f.x, v.x, acc[u].x);
+        acc[u].y = fmaf(f.y, v.y, acc[u].y);
+        acc[u].z = fmaf(f.z, v.z, acc[u].z);
+        acc[u].w = fmaf(f.w, v.w, acc[u].w);
       }
     }
   }
   L = warp_sum(L);
-  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // nothing visible: zero
-  const int g = row / t.N, n = row - g * t.N;
-  const int64_t o = b * t.o_sb + (int64_t)(h * t.rep + g) * t.o_sh + n * t.o_st;
-  auto put = [&](int d, float4 v) {  // four consecutive values
-    if (t.out_bf16) {
-      __nv_bfloat16 r[4] = {__float2bfloat16_rn(v.x), __float2bfloat16_rn(v.y), __float2bfloat16_rn(v.z),
-                            __float2bfloat16_rn(v.w)};
-      auto* out = reinterpret_cast<__nv_bfloat16*>(t.out) + o + d;
-      if (t.o_vec) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(r);
-      else
-        for (int e = 0; e < 4 && d + e < vp.D; ++e) out[e] = r[e];
-    } else {
-      __half r[4] = {__float2half_rn(v.x), __float2half_rn(v.y), __float2half_rn(v.z), __float2half_rn(v.w)};
-      auto* out = reinterpret_cast<__half*>(t.out) + o + d;
-      if (t.o_vec) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(r);
-      else
-        for (int e = 0; e < 4 && d + e < vp.D; ++e) out[e] = r[e];
-    }
-  };
-  if (!vu) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int d = 4 * lane + 128 * u;
-      if (d < vp.D)
-        put(d, make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv));
-    }
-    return;
-  }
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const float v[4] = {acc[u].x, acc[u].y, acc[u].z, acc[u].w};
+  if (lane == 0) inv_s[warp] = L > 0.f || L != L ? 1.f / L : 0.f;  // nothing visible: zero
+  __syncthreads();
+  auto put = [&](int d, float4 v) {  // channel d of the thread's four rows
+    const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int d = 4 * lane + 128 * u + e;
-      if (d < t.Dv) zb[warp][d] = fmaf(zs[d], v[e] * inv, zo[d]);  // the mean latent
+      const int row = row0 + 4 * q + e;
+      if (row >= t.rows) break;
+      const int g = row / t.N, n = row - g * t.N;
+      const int64_t o = b * t.o_sb + (int64_t)(h * t.rep + g) * t.o_sh + n * t.o_st + d;
+      if (t.out_bf16) reinterpret_cast<__nv_bfloat16*>(t.out)[o] = __float2bfloat16_rn(x[e]);
+      else reinterpret_cast<__half*>(t.out)[o] = __float2half_rn(x[e]);
     }
-  }
-  __syncwarp();
-  for (int i = 4 * lane; i < vp.D; i += 128) {
-    const float* mu = vp.mean + (size_t)beta * vp.D;
-    float v[4];
+  };
+  const float4 inv = *reinterpret_cast<const float4*>(&inv_s[4 * q]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = i + e < vp.D ? mu[i + e] : 0.f;
-#pragma unroll 4
+  for (int u = 0; u < 2; ++u) {
+    const int d = d0 + 128 * u;
+    if (d >= t.Dv) break;
+    const float4 v = make_float4(acc[u].x * inv.x, acc[u].y * inv.y, acc[u].z * inv.z, acc[u].w * inv.w);
+    if (!vu) put(d, v);
+    else
+      *reinterpret_cast<float4*>(&zb[d][4 * q]) =
+          make_float4(fmaf(zs[d], v.x, zo[d]), fmaf(zs[d], v.y, zo[d]), fmaf(zs[d], v.z, zo[d]),
+                      fmaf(zs[d], v.w, zo[d]));  // the mean latent
+  }
+  if (!vu) return;
+  __syncthreads();
+  for (int i = d0; i < vp.D; i += 128) {
+    const float mu = vp.mean[(size_t)beta * vp.D + i];
+    float4 v = make_float4(mu, mu, mu, mu);
+    const float* Vt = vp.Vt + (size_t)beta * vp.r * vp.D + i;
+#pragma unroll 8
     for (int j = 0; j < t.Dv; ++j) {
       const int k = comp[j];
-      if (k < 0) continue;
-      const float zj = zb[warp][j];
-      const float* col = vp.Vt + ((size_t)beta * vp.r + k) * vp.D + i;
-      if ((vp.D & 3) == 0) {
-        const float4 c = *reinterpret_cast<const float4*>(col);
-        v[0] = fmaf(zj, c.x, v[0]);
-        v[1] = fmaf(zj, c.y, v[1]);
-        v[2] = fmaf(zj, c.z, v[2]);
-        v[3] = fmaf(zj, c.w, v[3]);
-      } else {
-        for (int e = 0; e < 4 && i + e < vp.D; ++e) v[e] = fmaf(zj, col[e], v[e]);
-      }
+      const float c = k < 0 ? 0.f : Vt[(size_t)k * vp.D];
+      const float4 zz = *reinterpret_cast<const float4*>(&zb[j][4 * q]);
+      if (k < 0) continue;  // padding: its sums are whatever the codes' padding held
+      v.x = fmaf(zz.x, c, v.x);
+      v.y = fmaf(zz.y, c, v.y);
+      v.z = fmaf(zz.z, c, v.z);
+      v.w = fmaf(zz.w, c, v.w);
     }
-    if (inv == 0.f) v[0] = v[1] = v[2] = v[3] = 0.f;
-    put(i, make_float4(v[0], v[1], v[2], v[3]));
+    put(i, make_float4(inv.x == 0.f ? 0.f : v.x, inv.y == 0.f ? 0.f : v.y, inv.z == 0.f ? 0.f : v.z,
+                       inv.w == 0.f ? 0.f : v.w));
   }
 }
 
@@ -802,12 +799,12 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // 32-row blocks read V the least; where they do not fill the SMs twice, 8 rows
-  const bool few = (int64_t)kp.n_slots * ((t.prow + 31) / 32) < 2 * t.sms;
-  const int rows = few ? 8 : 32;
+  // 64-row blocks read V the least; where they do not fill the SMs, 8 rows
+  const bool few = (int64_t)kp.n_slots * ((t.prow + 63) / 64) < t.sms;
+  const int rows = few ? 8 : 64;
   const size_t smem =
-      (size_t)(kp.D * rows + 2 * kPrepK * kPrepCols + rows * (kp.r | 1)) * sizeof(float);
-  const auto prep = few ? tree_prep_kernel<2> : tree_prep_kernel<8>;
+      (size_t)(kp.D * (rows + 4) + 2 * kPrepK * kPrepCols + rows * (kp.r | 1)) * sizeof(float);
+  const auto prep = few ? tree_prep_kernel<1> : tree_prep_kernel<8>;
   e = prepare_kernel(reinterpret_cast<const void*>(prep), (int)smem);
   if (e != cudaSuccess) return e;
   const int masks = t.tc && t.mask ? (t.mask_sb ? kp.B : 1) : 0;  // blocks that pack the mask
@@ -818,10 +815,10 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
   if (e != cudaSuccess) return e;
   e = t.tc ? launch_tree_tc(kp, vp, t, s, nk) : launch_main(kp, vp, t, s, nk);
   if (e != cudaSuccess) return e;
-  const int blocks = (t.rows + kCombineWarps - 1) / kCombineWarps;
+  const int blocks = (t.rows + kCombineRows - 1) / kCombineRows;
   ++*nk;
-  return launch_dependent(tree_combine_kernel, (unsigned)kp.n_slots * blocks, kCombineWarps * 32, 0,
-                          s, kp, vp, t);
+  return launch_dependent(tree_combine_kernel, (unsigned)kp.n_slots * blocks, kCombineThreads, 0, s,
+                          kp, vp, t);
 }
 
 }  // namespace kvc

@@ -54,8 +54,9 @@ constexpr int kMaxNS = 4;          // row stages
 // Side words (norms and scales of a tile) stay until the softmax has read them:
 // a tile's stage is loaded once the decoders are done with the tile kMaxNS
 // before, whose keys they decoded after the scores of the tile two before that
-// were done, which waited for the softmax to have read S four tiles earlier; so
-// entries are never overwritten too soon.
+// were done, which waited for the softmax to have read S four tiles earlier (and
+// the side words of up to two tiles more); so entries are never overwritten too
+// soon, nor read too early.
 constexpr int kSideRing = 16;
 static_assert(kSideRing >= kMaxNS + 2 + 4, "side words overwritten before they are read");
 constexpr int kSoftBar = 1, kDecBar = 3;  // named barriers: softmax groups 1, 2; decoder groups 3, 4
@@ -798,15 +799,22 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
       // token already
       int fast0 = pl.plain0, fast1 = 0;
       const int tile1 = pl.g.tile1;
+      // this lane's norm and scale, read one tile ahead
+      unsigned short nt_next = 0, st_next = 0;
+      auto read_side = [&](int gt) {
+        const int sd = gt & (kSideRing - 1);
+        wait_or_abort(&side_full[sd], (gt / kSideRing) & 1, &abort_flag);
+        if (KMODE == KVC_MODE_CODEBOOK) nt_next = side_s[sd][0][lt];
+        if (!VU) st_next = side_s[sd][1][lt];
+      };
+      if (tile_first < tile1) read_side(HALVES ? j : 2 * j + wg);
       for (int tile = tile_first; tile < tile1; tile += kStep, ++j) {
         const int gt = HALVES ? j : 2 * j + wg;        // the tile's number in the run
         const int s = gt % SB;                         // S buffer, and its phase
         const uint32_t s_par = (gt / SB) & 1;
         const uint32_t s_tm = tm + lane_off + z.s_col + s * N + col0;
-        const int sd = gt & (kSideRing - 1);
-        wait_or_abort(&side_full[sd], (gt / kSideRing) & 1, &abort_flag);
-        float nt = KMODE == KVC_MODE_CODEBOOK ? __half2float(__ushort_as_half(side_s[sd][0][lt])) : 1.f;
-        const float st = VU ? 1.f : __half2float(__ushort_as_half(side_s[sd][1][lt]));
+        float nt = KMODE == KVC_MODE_CODEBOOK ? __half2float(__ushort_as_half(nt_next)) : 1.f;
+        const float st = VU ? 1.f : __half2float(__ushort_as_half(st_next));
         if (!VU && st != st) nt = st;  // a scale of NaN: the weights of those who see it
         wait_or_abort(&s_full[s], s_par, &abort_flag);
         __syncwarp();
@@ -960,6 +968,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
         }
         if (j > 0) wait_or_abort(&p_empty[wg], (j - 1) & 1, &abort_flag);  // P has been read
         __syncwarp();
+        if (tile + kStep < tile1) read_side(gt + kStep);
         // a hidden token's scale may be anything: its weights are 0 and stay 0
         // under any finite factor
         const float su = fmaxf(fminf(st * inv_sref, 3e38f), -3e38f);
@@ -1039,7 +1048,8 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
       }
       named_bar_sync(bar, 128);
       const size_t prow = (HALVES ? ((size_t)pl.g.job + blockIdx.x) : 2 * ((size_t)pl.g.job + blockIdx.x) + wg) * t.rt + col0;
-      float* part = t.part + prow * t.Dvp;
+      // weighted sums by channel, a partial's rows together: [Dvp][rt]
+      float* part = t.part + (prow - col0) * t.Dvp + col0;
       if (ltid < ncol) {
         const bool sn = seen[wg][ltid] != 0;
         t.ml[prow + ltid] = make_float2(
@@ -1048,7 +1058,8 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
       }
       for (int m = 0; m < z.mt; ++m) {
         const int d = m * 128 + lt;
-        for (int c = 0; c < ncol; c += 16) {
+        float4* to = reinterpret_cast<float4*>(part + (size_t)d * t.rt);
+        for (int c = 0; c < NC; c += 16) {
           uint32_t o[16];
           if (any) {
             tmem_ld16(o_tm + m * N + c, o);
@@ -1056,17 +1067,18 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
           }
           if (d < t.Dv) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c + i < ncol)
-                part[(size_t)(c + i) * t.Dvp + d] = any ? __uint_as_float(o[i]) * sref : 0.f;
+            for (int i = 0; i < 4; ++i)
+              to[c / 4 + i] = any ? make_float4(__uint_as_float(o[4 * i]) * sref, __uint_as_float(o[4 * i + 1]) * sref,
+                                                __uint_as_float(o[4 * i + 2]) * sref, __uint_as_float(o[4 * i + 3]) * sref)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
       }
       tc_fence_before();  // the next segment's first product overwrites O
     }
   }
-  grid_dependents_launch();
   __syncthreads();
+  grid_dependents_launch();  // (from the idle warp at the start, the combine's blocks came in the way)
   if (abort_flag && tid == 0) atomicCAS(kp.err, 0, kErrTimeout);
   if (warp == R::score) {
     tc_fence_after();

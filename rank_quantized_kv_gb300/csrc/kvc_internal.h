@@ -136,7 +136,6 @@ struct TreeArgs {
   void* out = nullptr;
   int out_bf16 = 0;
   int64_t o_sb = 0, o_sh = 0, o_st = 0;
-  int o_vec = 0;                         // rows of out start at multiples of 8 bytes, D of 4
   int Hq = 0, rep = 0, N = 0;
   float scale_log2 = 0.f;                // score scale times log2(e)
   int64_t S = 0, ctx = 0;                // stored tokens; those before the drafts
@@ -162,7 +161,8 @@ struct TreeArgs {
   float* wx = nullptr;                   // workspace: [n_slots rows][m + n_out]
   int parts = 1;                         // partials that a CTA leaves of a job
   // workspace: the partials [(jobs + grid - 1) parts][rt], per row its reference and
-  // sum of weights (ml) and its weighted sums (part, Dv padded to Dvp, a multiple of 4)
+  // sum of weights (ml), and its weighted sums (part: [Dvp][rt] per partial, Dvp
+  // being Dv padded to a multiple of 4)
   float2* ml = nullptr;
   float* part = nullptr;
   int Dvp = 0;
