@@ -37,6 +37,7 @@ struct kvc_layer {
   std::vector<int32_t> seg_host;     // [nb][kMaxSeg][4] width segments
   std::vector<int32_t> channels_host;  // [n_slots][n_out] outlier channels
   float cb_mul = 1.f;                // scale at which the centroids fall nearest to fp16 values
+  bool batch_free = true;            // bases and outlier channels of (b, h) are those of (0, h)
   uint64_t format[2] = {0, 0};       // hash of everything a stored row decodes by
   kvc::TcPlan tc{};                  // tensor-core path tables (kvc_tc.cu)
 };
@@ -662,6 +663,14 @@ static kvc_status init_from_geo(const kvc_layer_desc* d, Geo& g, kvc_layer** out
   L->side_host = g.side_off;
   L->channels_host = g.channels;
   format_hash(d, g, L->format);
+  for (int sl = g.Hg; sl < g.n_slots; ++sl) {
+    const int h = sl % g.Hg;
+    if (g.basis[sl] != g.basis[h] ||
+        !std::equal(g.channels.begin() + (size_t)sl * g.n_out,
+                    g.channels.begin() + (size_t)(sl + 1) * g.n_out,
+                    g.channels.begin() + (size_t)h * g.n_out))
+      L->batch_free = false;
+  }
   if (g.cb_levels) L->cb_mul = centroid_scale(d->codebook, g.cb_levels);
   *out = L;
   return succeed();
@@ -1001,17 +1010,19 @@ kvc_status kvc_gather(kvc_layer* dst, const kvc_layer* src, const int32_t* paren
     return fail(KVC_EINVAL, "the layers differ in heads or frozen parameters");
   if (!parent && dst->B != src->B) return fail(KVC_EINVAL, "layers of different batches need parent");
   // a row decodes by its slot's basis and outlier channels: they must agree for
-  // every pair of slots between which rows may move
+  // every pair of slots between which rows may move (one batch entry of each
+  // layer stands for all where they do not depend on the batch)
   const int Hg = dst->n_slots / dst->B, no = dst->p.n_out;
-  for (int b = 0; b < dst->B; ++b)
-    for (int s = parent ? 0 : b; s < (parent ? src->B : b + 1); ++s)
+  const bool alike = dst->batch_free && src->batch_free;
+  for (int b = 0; b < (alike ? 1 : dst->B); ++b)
+    for (int s = parent ? 0 : b; s < (alike ? 1 : parent ? src->B : b + 1); ++s)
       for (int h = 0; h < Hg; ++h) {
         const int ds = b * Hg + h, ss = s * Hg + h;
         if (dst->basis_host[ds] != src->basis_host[ss])
           return fail(KVC_EINVAL, "slot %d has another basis than the source's slot %d", ds, ss);
-        if (no && !std::equal(&dst->channels_host[(size_t)ds * no],
-                              &dst->channels_host[(size_t)ds * no] + no,
-                              &src->channels_host[(size_t)ss * no]))
+        if (!std::equal(dst->channels_host.begin() + (size_t)ds * no,
+                        dst->channels_host.begin() + (size_t)(ds + 1) * no,
+                        src->channels_host.begin() + (size_t)ss * no))
           return fail(KVC_EINVAL, "slot %d has other outlier channels than the source's slot %d", ds, ss);
       }
   if (!index && n > src->len - start)

@@ -98,15 +98,6 @@ __device__ __forceinline__ float load_q(const TreeArgs& t, int64_t i) {
 
 // ---------------------------------------------------------------- prep
 
-// The key weights at every packed position (for the tensor cores: split into two
-// fp16 pieces and laid out as their operand), w_j = scale log2(e) u_j coef_j
-// (coef = step in uniform mode, 1 for a codebook), and c1.  One block per (slot,
-// 8 RT rows): u = q V as a register-tiled product, RT rows x 4 columns a thread, a
-// warp 128 columns; q stays in shared memory, V passes through it 32 rows at a
-// time.  Bound: fp32 FMA (rows D r of them) for wide trees, else the
-// latency of one pass, for which blocks of 8 rows spread few rows over the SMs.
-constexpr int kPrepCols = 128, kPrepK = 32;
-
 // The mask as bits, transposed: word w of draft j holds the drafts 32 w .. that
 // see j.  One block per (mask, w, 256 drafts).
 __device__ void pack_mask(const TreeArgs& t, int block) {
@@ -123,168 +114,230 @@ __device__ void pack_mask(const TreeArgs& t, int block) {
   t.mask_bits[((size_t)b * t.N + j) * words + w] = v;
 }
 
-template <int RT>
+// The key weights at every packed position (for the tensor cores: split into two
+// fp16 pieces and laid out as their operand), w_j = scale log2(e) u_j coef_j
+// (coef = step in uniform mode, 1 for a codebook), and c1, for ROWS rows of a
+// slot per block; u = q V in fp32, by the block's 256 threads.
+//   64, 32    a register-tiled product, 8 or 4 rows x 4 columns a thread and 128
+//   rows      columns a warp, V through shared memory 32 rows at a time: bound by
+//             the fp32 FMA pipe (rows D r of them);
+//   8 rows    a thread takes one column and a share of the sum over D, V straight
+//             from global memory, each element read once: bound by latency.  For
+//             bases of up to 64 columns, which leave half of the tiles' columns
+//             empty, and for few rows, for which it gives more blocks.
+constexpr int kPrepCols = 128, kPrepK = 32, kPrepBufs = 2;
+
+template <int ROWS>
+constexpr size_t prep_smem(int D, int r) {
+  return (size_t)(D * (ROWS + 4) + (ROWS >= 32 ? kPrepBufs * kPrepK * kPrepCols : kPrepThreads * 8) +
+                  ROWS * (r | 1)) * sizeof(float);
+}
+
+template <int ROWS>
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp, const TreeArgs t) {
-  constexpr int kPrepRows = 8 * RT;
+  constexpr int RT = ROWS / 8;       // rows of a warp
+  constexpr int kQ = ROWS + 4;       // stores of q meet four to a bank, not all
   extern __shared__ __align__(16) float sm_f[];
-  __shared__ int comp[256];       // packed position: component (-1: padding) and its factor
-  __shared__ float coef[256];
-  __shared__ float down[kPrepRows];  // power of two that brings a row into fp16's range
+  __shared__ int comp[256];          // packed position: component (-1: padding)
+  __shared__ float coef[256];        // component: factor of its weight, 0 when dropped
+  __shared__ float off[256];         // component: lo + 2^(b-1) step
+  __shared__ int64_t q_row[ROWS];    // first element of a row of q, -1 past the last
+  __shared__ float down[ROWS];       // power of two that brings a row into fp16's range
   const int D = kp.D, r = kp.r, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int blocks = (t.prow + kPrepRows - 1) / kPrepRows;
+  const int blocks = (t.prow + ROWS - 1) / ROWS;
   if ((int)blockIdx.x >= blocks * kp.n_slots) {
     pack_mask(t, blockIdx.x - blocks * kp.n_slots);
     return;
   }
-  const int slot = blockIdx.x / blocks, r0 = (blockIdx.x - slot * blocks) * kPrepRows;
+  grid_dependents_launch();
+  const int slot = blockIdx.x / blocks, r0 = (blockIdx.x - slot * blocks) * ROWS;
   const int b = slot / kp.H, h = slot - b * kp.H;
   const int beta = kp.basis_of[slot];
-  const int nr = max(0, min(kPrepRows, t.rows - r0));  // rows of queries
-  const int np = min(kPrepRows, t.prow - r0);          // rows written
+  const int nr = max(0, min(ROWS, t.rows - r0));  // rows of queries
+  const int np = min(ROWS, t.prow - r0);          // rows written
   const bool uniform = kp.mode == KVC_MODE_UNIFORM;
-  const int us_row = r | 1;                    // an odd stride: rows in different banks
-  constexpr int kQ = kPrepRows + 4;            // stores of q then meet four to a bank, not all
-  float* qs = sm_f;                            // [D][kQ] rows of q, transposed
-  float* vs = qs + D * kQ;              // [2][32][128] rows of V
-  float* us = vs + 2 * kPrepK * kPrepCols;     // [kPrepRows][us_row] products
-  grid_dependents_launch();
+  const int us_row = r | 1;           // an odd stride: rows in different banks
+  float* qs = sm_f;                   // [D][kQ] rows of q, transposed
+  float* vs = qs + D * kQ;            // [2][32][128] rows of V; [share][8][columns] sums
+  float* us = vs + (ROWS >= 32 ? kPrepBufs * kPrepK * kPrepCols : kPrepThreads * 8);  // [ROWS][us_row] weights
   const float* V = kp.V + (size_t)beta * D * r;
   const int stages = (D + kPrepK - 1) / kPrepK;
   // rows of V from 32 st, columns c0 ..: asynchronous copies of 16 bytes, or of
   // 4 where a row starts at any multiple of 4
-  const bool wide = (r & 3) == 0;  // rows of V start at multiples of 16 bytes
-  auto load_v = [&](int st, int c0, int buf) {
-    if (wide) {
-#pragma unroll
-      for (int u = 0; u < kPrepK * kPrepCols / 4 / kPrepThreads; ++u) {
-        const int e = (tid + u * kPrepThreads) * 4, i = e / kPrepCols, c = e - i * kPrepCols, k = st * kPrepK + i;
-        float* dst = vs + buf * kPrepK * kPrepCols + e;
-        if (k < D && c0 + c < r) __pipeline_memcpy_async(dst, V + (size_t)k * r + c0 + c, 16);
-        else *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      __pipeline_commit();
-      return;
-    }
-    for (int e = tid; e < kPrepK * kPrepCols; e += kPrepThreads) {
+  auto load_v = [&](int st, int c0) {
+    const bool wide = (r & 3) == 0;
+    const int step = wide ? 4 : 1, buf = st % kPrepBufs;
+    for (int e = tid * step; st < stages && e < kPrepK * kPrepCols; e += kPrepThreads * step) {
       const int i = e / kPrepCols, c = e - i * kPrepCols, k = st * kPrepK + i;
       float* dst = vs + buf * kPrepK * kPrepCols + e;
-      if (k < D && c0 + c < r) __pipeline_memcpy_async(dst, V + (size_t)k * r + c0 + c, 4);
-      else *dst = 0.f;
+      const float* src = V + (size_t)k * r + c0 + c;
+      const bool in = k < D && c0 + c < r;
+      if (wide) {
+        if (in) __pipeline_memcpy_async(dst, src, 16);
+        else *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+        if (in) __pipeline_memcpy_async(dst, src, 4);
+        else *dst = 0.f;
+      }
     }
     __pipeline_commit();
   };
-  load_v(0, 0, 0);
-  for (int j = tid; j < 256; j += kPrepThreads) {
-    int width = 0;
-    const int k = j < t.NCk ? position_component(kp, beta, j, &width) : -1;
-    comp[j] = k;
-    coef[j] = k < 0 ? 0.f : t.scale_log2 * t.w_mul * (uniform ? kp.step[(size_t)beta * r + k] : 1.f);
+  if (ROWS >= 32)
+    for (int st = 0; st < kPrepBufs - 1; ++st) load_v(st, 0);
+  if (tid < ROWS) {
+    const int x = r0 + tid, g = x / t.N, n = x - g * t.N;
+    q_row[tid] = tid < nr ? b * t.q_sb + (int64_t)(h * t.rep + g) * t.q_sh + n * t.q_st : -1;
   }
-  // a warp takes every eighth row, 32 values at a time, all loads issued before
+  for (int k = tid; k < 256; k += kPrepThreads) {
+    int width = 0;
+    comp[k] = k < t.NCk ? position_component(kp, beta, k, &width) : -1;
+    float c = 0.f, o = 0.f;
+    if (k < r) {
+      const size_t bk = (size_t)beta * r + k;
+      width = kp.bits[bk];
+      if (width) c = t.scale_log2 * t.w_mul * (uniform ? kp.step[bk] : 1.f);
+      if (width && uniform) o = fmaf((float)(1 << (width - 1)), kp.step[bk], kp.lo[bk]);
+    }
+    coef[k] = c;
+    off[k] = o;
+  }
+  __syncthreads();
+  // a warp takes every eighth row, 64 values at a time, all loads issued before
   // the first is stored
   for (int i0 = 0; i0 < D; i0 += 64) {
-    float v[kPrepRows / 8][2];
+    float v[RT][2];
 #pragma unroll
-    for (int u = 0; u < kPrepRows / 8; ++u) {
-      const int row = warp + 8 * u, x = min(r0 + row, t.rows - 1), g = x / t.N, n = x - g * t.N;
-      const int64_t at = b * t.q_sb + (int64_t)(h * t.rep + g) * t.q_sh + n * t.q_st + i0 + lane;
+    for (int u = 0; u < RT; ++u) {
+      const int64_t at = q_row[warp + 8 * u] + i0 + lane;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        v[u][e] = row < nr && i0 + lane + 32 * e < D ? load_q(t, at + 32 * e) : 0.f;
+        v[u][e] = warp + 8 * u < nr && i0 + lane + 32 * e < D ? load_q(t, at + 32 * e) : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < kPrepRows / 8; ++u)
+    for (int u = 0; u < RT; ++u)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (i0 + lane + 32 * e < D) qs[(i0 + lane + 32 * e) * kQ + warp + 8 * u] = v[u][e];
   }
-  for (int c0 = 0; c0 < r; c0 += kPrepCols) {
-    float2 acc[RT][2];
+  // rows RT warp ..: largest weight and offset, over the lanes' columns
+  float mx[RT], c1[RT];
 #pragma unroll
-    for (int e = 0; e < RT; ++e) acc[e][0] = acc[e][1] = make_float2(0.f, 0.f);
-    if (c0) load_v(0, c0, 0);
-    for (int st = 0; st < stages; ++st) {
-      if (st + 1 < stages) load_v(st + 1, c0, (st + 1) & 1);
-      __pipeline_wait_prior(st + 1 < stages ? 1 : 0);
-      __syncthreads();
-      const float* vb = vs + (st & 1) * kPrepK * kPrepCols + 4 * lane;
-      const float* qb = qs + st * kPrepK * kQ + RT * warp;
-      const int kn = min(kPrepK, D - st * kPrepK);
+  for (int e = 0; e < RT; ++e) mx[e] = c1[e] = 0.f;
+  auto take = [&](int e, int k, float u) {  // column k of the warp's row e
+    const float w = u * coef[k];
+    us[(RT * warp + e) * us_row + k] = w;
+    if (fabsf(w) <= 3.4e38f) mx[e] = fmaxf(mx[e], fabsf(w));  // NaN and infinities stay what they are
+    c1[e] = fmaf(u, off[k], c1[e]);
+  };
+  if constexpr (ROWS >= 32) {
+    for (int c0 = 0; c0 < r; c0 += kPrepCols) {
+      float2 acc[RT][2];
+#pragma unroll
+      for (int e = 0; e < RT; ++e) acc[e][0] = acc[e][1] = make_float2(0.f, 0.f);
+      if (c0)
+        for (int st = 0; st < kPrepBufs - 1; ++st) load_v(st, c0);
+      for (int st = 0; st < stages; ++st) {
+        load_v(st + kPrepBufs - 1, c0);  // (past the last: an empty group)
+        __pipeline_wait_prior(kPrepBufs - 1);
+        __syncthreads();
+        const float* vb = vs + st % kPrepBufs * kPrepK * kPrepCols + 4 * lane;
+        const float* qb = qs + st * kPrepK * kQ + RT * warp;
+        const int kn = min(kPrepK, D - st * kPrepK);
 #pragma unroll 8
-      for (int k = 0; k < kn; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(vb + k * kPrepCols);
-        float q[RT];
-        if constexpr (RT % 4 == 0) {
+        for (int k = 0; k < kn; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(vb + k * kPrepCols);
+          const float4 q0 = *reinterpret_cast<const float4*>(qb + k * kQ);
+          const float4 q1 = *reinterpret_cast<const float4*>(qb + k * kQ + RT - 4);
+          const float q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
-          for (int e = 0; e < RT; e += 4) {
-            const float4 qq = *reinterpret_cast<const float4*>(qb + k * kQ + e);
-            q[e] = qq.x;
-            q[e + 1] = qq.y;
-            q[e + 2] = qq.z;
-            q[e + 3] = qq.w;
+          for (int e = 0; e < RT; ++e) {
+            const float2 qq = make_float2(q[e], q[e]);
+            acc[e][0] = __ffma2_rn(qq, make_float2(v.x, v.y), acc[e][0]);
+            acc[e][1] = __ffma2_rn(qq, make_float2(v.z, v.w), acc[e][1]);
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < RT; ++e) q[e] = qb[k * kQ + e];
         }
+        __syncthreads();  // this buffer is refilled next
+      }
+      const int c = c0 + 4 * lane;
 #pragma unroll
-        for (int e = 0; e < RT; ++e) {
-          const float2 qq = make_float2(q[e], q[e]);
-          acc[e][0] = __ffma2_rn(qq, make_float2(v.x, v.y), acc[e][0]);
-          acc[e][1] = __ffma2_rn(qq, make_float2(v.z, v.w), acc[e][1]);
+      for (int e = 0; e < RT; ++e) {
+        if (c < r) take(e, c, acc[e][0].x);
+        if (c + 1 < r) take(e, c + 1, acc[e][0].y);
+        if (c + 2 < r) take(e, c + 2, acc[e][1].x);
+        if (c + 3 < r) take(e, c + 3, acc[e][1].y);
+      }
+    }
+  } else {
+    __syncthreads();
+    // columns of a pass: 32, 64 or 128; the rest of the threads share the sum
+    const int cols = r <= 32 ? 32 : r <= 64 ? 64 : 128, shares = kPrepThreads / cols;
+    const int col = tid & (cols - 1), share = tid / cols;
+    const int per = (D + shares - 1) / shares, k0 = share * per, k1 = min(D, k0 + per);
+    for (int c0 = 0; c0 < r; c0 += cols) {
+      float2 acc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
+      if (c0 + col < r) {
+        const float* vc = V + c0 + col;
+        for (int kb = k0; kb < k1; kb += 16) {  // 16 loads in flight
+          float v[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) v[u] = kb + u < k1 ? vc[(size_t)(kb + u) * r] : 0.f;
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const float* qk = qs + min(kb + u, D - 1) * kQ;
+            const float4 q0 = *reinterpret_cast<const float4*>(qk);
+            const float4 q1 = *reinterpret_cast<const float4*>(qk + 4);
+            const float2 vv = make_float2(v[u], v[u]);
+            if (kb + u >= k1) continue;
+            acc[0] = __ffma2_rn(vv, make_float2(q0.x, q0.y), acc[0]);
+            acc[1] = __ffma2_rn(vv, make_float2(q0.z, q0.w), acc[1]);
+            acc[2] = __ffma2_rn(vv, make_float2(q1.x, q1.y), acc[2]);
+            acc[3] = __ffma2_rn(vv, make_float2(q1.z, q1.w), acc[3]);
+          }
         }
       }
-      __syncthreads();  // the other buffer is refilled next
-    }
-    const int c = c0 + 4 * lane;
 #pragma unroll
-    for (int e = 0; e < RT; ++e) {
-      float* u = us + (RT * warp + e) * us_row + c;
-      if (c < r) u[0] = acc[e][0].x;
-      if (c + 1 < r) u[1] = acc[e][0].y;
-      if (c + 2 < r) u[2] = acc[e][1].x;
-      if (c + 3 < r) u[3] = acc[e][1].y;
+      for (int e = 0; e < 4; ++e) {
+        vs[(share * 8 + 2 * e) * cols + col] = acc[e].x;
+        vs[(share * 8 + 2 * e + 1) * cols + col] = acc[e].y;
+      }
+      __syncthreads();
+      for (int c = lane; c < cols && c0 + c < r; c += 32) {
+        float u = 0.f;
+        for (int x = 0; x < shares; ++x) u += vs[(x * 8 + warp) * cols + c];
+        take(0, c0 + c, u);
+      }
+      __syncthreads();
     }
   }
-  __syncthreads();
   const size_t row0 = (size_t)slot * t.prow + r0;
-  for (int row = warp; row < np; row += kPrepThreads / 32) {  // a warp a row
-    float c1 = 0.f, mx = 0.f;
-    if (uniform && row < nr) {
-      for (int k = lane; k < r; k += 32) {
-        const size_t bk = (size_t)beta * r + k;
-        const int width = kp.bits[bk];
-        if (width) c1 = fmaf(us[row * us_row + k], fmaf((float)(1 << (width - 1)), kp.step[bk], kp.lo[bk]), c1);
-      }
-      for (int i = lane; i < D; i += 32) c1 = fmaf(qs[i * kQ + row], kp.mean[(size_t)beta * D + i], c1);
+#pragma unroll
+  for (int e = 0; e < RT; ++e) {
+    const int row = RT * warp + e;
+    if (uniform) {
+      for (int i = lane; i < D; i += 32) c1[e] = fmaf(qs[i * kQ + row], kp.mean[(size_t)beta * D + i], c1[e]);
+      c1[e] = warp_sum(c1[e]);
     }
-    c1 = warp_sum(c1);
-    if (t.tc) {
-      for (int j = lane; j < t.NCk; j += 32)
-        if (comp[j] >= 0) {
-          const float v = fabsf(us[row * us_row + comp[j]] * coef[j]);
-          if (v <= 3.4e38f) mx = fmaxf(mx, v);  // NaN and infinities stay what they are
-        }
-      mx = warp_max(mx);
-    }
-    if (lane == 0) {
-      t.c1[row0 + row] = t.scale_log2 * c1;
+    const float most = warp_max(mx[e]);
+    if (lane == 0 && row < np) {
+      t.c1[row0 + row] = t.scale_log2 * c1[e];
       if (t.tc) {
-        const int ex = max(0, (__float_as_int(mx) >> 23) - 127 - 13);
+        const int ex = max(0, (__float_as_int(most) >> 23) - 127 - 13);
         t.wscale[row0 + row] = __int_as_float((127 + ex) << 23);
         down[row] = __int_as_float((127 - ex) << 23);
       }
     }
   }
+  __syncthreads();
   if (!t.tc) {
     for (int j = tid; j < t.NCk; j += kPrepThreads)  // this thread's positions of all rows
       for (int row = 0; row < nr; ++row)
-        t.w[(row0 + row) * t.NCk + j] = comp[j] < 0 ? 0.f : coef[j] * us[row * us_row + comp[j]];
+        t.w[(row0 + row) * t.NCk + j] = comp[j] < 0 ? 0.f : us[row * us_row + comp[j]];
     return;
   }
   // two fp16 pieces in the layout of a K-major operand without swizzle: cores of
   // 8 rows x 8 positions, 128 contiguous bytes, adjacent along K
-  __syncthreads();
   const int KC = t.K / 8;
   for (int e = tid; e < np * KC; e += kPrepThreads) {
     const int c = e / np, row = e - c * np;
@@ -295,7 +348,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int k = comp[8 * c + i];
-      const float v = k < 0 || row >= nr ? 0.f : us[row * us_row + k] * coef[8 * c + i] * down[row];
+      const float v = k < 0 || row >= nr ? 0.f : us[row * us_row + k] * down[row];
       hi[i] = __float2half_rn(v);
       lo[i] = __float2half_rn(v - __half2float(hi[i]));
     }
@@ -799,12 +852,15 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // 64-row blocks read V the least; where they do not fill the SMs, 8 rows
-  const bool few = (int64_t)kp.n_slots * ((t.prow + 63) / 64) < t.sms;
-  const int rows = few ? 8 : 64;
-  const size_t smem =
-      (size_t)(kp.D * (rows + 4) + 2 * kPrepK * kPrepCols + rows * (kp.r | 1)) * sizeof(float);
-  const auto prep = few ? tree_prep_kernel<1> : tree_prep_kernel<8>;
+  // rows of a projection block (measured, us: 4096 rows of 128 columns 19 with 32,
+  // 26 with 8; 4096 rows of 32 columns 18 and 13)
+  const bool few = kp.r <= 64 || t.prow <= 16;
+  const bool many = (int64_t)kp.n_slots * ((t.prow + 63) / 64) >= t.sms;
+  const int rows = few ? 8 : many ? 64 : 32;
+  const size_t smem = few    ? prep_smem<8>(kp.D, kp.r)
+                      : many ? prep_smem<64>(kp.D, kp.r)
+                             : prep_smem<32>(kp.D, kp.r);
+  const auto prep = few ? tree_prep_kernel<8> : many ? tree_prep_kernel<64> : tree_prep_kernel<32>;
   e = prepare_kernel(reinterpret_cast<const void*>(prep), (int)smem);
   if (e != cudaSuccess) return e;
   const int masks = t.tc && t.mask ? (t.mask_sb ? kp.B : 1) : 0;  // blocks that pack the mask

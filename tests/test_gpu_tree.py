@@ -137,6 +137,22 @@ def test_rising_scores(kvc):
     check(o, reference(gk, rk, gv, rv, q.double().numpy(), 1 / math.sqrt(D), N))
 
 
+def test_dropped_components(kvc):
+    """Bases of which no component is kept: rows of no bytes, equal scores, the mean row."""
+    B, H, D, S, N = 1, 2, 64, 300, 3
+    rng = np.random.default_rng(0)
+    p = dict(V=rng.standard_normal((H, D, 4)), mean=rng.standard_normal((H, D)).astype(np.float32),
+             bits=np.zeros((H, 4), dtype=np.uint8), qmin=np.zeros((H, 4)), qstep=np.ones((H, 4)),
+             basis_of=np.arange(H))
+    lay = [kvc.KVCacheLayer("uniform", B, H, D, in_dtype="f16", capacity=S, device=DEV,
+                            path=tree_cases.PATH[0], **p) for _ in range(2)]
+    for x in lay:
+        x.append(torch.randn(B, H, S, D, device=DEV).half())
+    o = kvc.attend_tree(*lay, _q(B, 2 * H, N, D, 3).to(DEV)).float().cpu().numpy()
+    want = np.repeat(p["mean"], 2, 0)[None, :, None]
+    assert np.all(np.abs(o - want) <= 2.0 ** -11 * np.abs(want) + 2.0 ** -18 * np.abs(want) + 2.0 ** -25)
+
+
 def test_one_draft_is_a_decode_step(kvc):
     """N = 1 without a mask gives what kvc.attend gives, up to the output's rounding."""
     gk, gv, rk, rv = make_layers(kvc, "codebook", "int8", 2, 2, 128, 900, 21, dev=DEV)
