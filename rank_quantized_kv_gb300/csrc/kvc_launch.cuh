@@ -5,6 +5,8 @@
 
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 namespace kvc {
 
 // Until every launch that this one depends on has finished and its writes are
@@ -18,33 +20,36 @@ __device__ __forceinline__ void grid_dependents_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Attributes of a kernel on the current device, asked for once per thread: its
-// registers, and the dynamic shared memory that it may use raised to `smem`.
-// (Both calls take about a microsecond, which a decode step notices.)
+// Attributes of a kernel on the current device, asked for once: its registers,
+// and the dynamic shared memory that it may use raised to `smem`.  (Both calls
+// take about a microsecond, which a decode step notices.)  The limit belongs to
+// the kernel, not to the calling thread, so all threads share one table under a
+// lock and the limit only grows.
 inline cudaError_t prepare_kernel(const void* kernel, int smem, int* regs = nullptr) {
   struct Entry { const void* kernel; int device, smem, regs; };
-  thread_local Entry cache[64];
-  thread_local int n = 0;
+  static std::mutex lock;
+  constexpr int kEntries = 512;  // (kernel, device) pairs; the library has about 30 such kernels
+  static Entry cache[kEntries];
+  static int n = 0;
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  Entry* at = nullptr;
-  for (int i = 0; i < n; ++i)
-    if (cache[i].kernel == kernel && cache[i].device == device) at = &cache[i];
-  Entry fresh{kernel, device, -1, 0};
-  if (!at) {
+  std::lock_guard<std::mutex> held(lock);
+  int i = 0;
+  while (i < n && (cache[i].kernel != kernel || cache[i].device != device)) ++i;
+  if (i == n) {
+    if (n == kEntries) return cudaErrorMemoryAllocation;
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;
-    fresh.regs = fa.numRegs;
-    at = n < 64 ? &(cache[n++] = fresh) : &fresh;
+    cache[n++] = Entry{kernel, device, -1, fa.numRegs};
   }
-  if (smem > at->smem) {
+  if (smem > cache[i].smem) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    at->smem = smem;
+    cache[i].smem = smem;
   }
-  if (regs) *regs = at->regs;
+  if (regs) *regs = cache[i].regs;
   return cudaSuccess;
 }
 

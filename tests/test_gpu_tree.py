@@ -1,6 +1,8 @@
 """GPU parity of tree attention (kvc_attend_tree) against the float64 oracle on
 the GPU's own stored rows, within the allowance derived in tree_cases.py."""
+import concurrent.futures
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -230,6 +232,30 @@ def test_repeated_and_on_a_stream(kvc):
     torch.cuda.synchronize()
     assert torch.equal(a, b) and torch.equal(a, out) and not torch.equal(a, half)
     check(a, reference(gk, rk, gv, rv, q2.double().cpu().numpy(), 1 / math.sqrt(128), 6))
+
+
+def test_layers_of_two_sizes_on_two_threads(kvc):
+    """Two host threads call the same kernel with different amounts of shared
+    memory in turn: what one thread asks for does not undo what the other did."""
+    args = []
+    for D, seed in ((128, 81), (32, 82)):
+        gk, gv, _, _ = make_layers(kvc, "uniform", "int8", 1, 2, D, 200, seed, dev=DEV)
+        args.append((gk, gv, _q(1, 4, 4, D, seed).to(DEV)))
+    want = [kvc.attend_tree(*a) for a in args]
+    torch.cuda.synchronize()
+    got = []
+
+    def once(a):
+        t = threading.Thread(target=lambda: got.append(kvc.attend_tree(*a)))
+        t.start()
+        t.join()
+
+    with concurrent.futures.ThreadPoolExecutor(1) as first:  # a thread that lives on
+        got.append(first.submit(kvc.attend_tree, *args[0]).result())
+        once(args[1])
+        got.append(first.submit(kvc.attend_tree, *args[0]).result())
+    torch.cuda.synchronize()
+    assert len(got) == 3 and all(torch.equal(a, want[i]) for a, i in zip(got, (0, 1, 0)))
 
 
 def test_extreme_queries(kvc):
