@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstring>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include <cuda_fp16.h>
@@ -965,10 +966,19 @@ kvc_status kvc_attend_tree(const kvc_layer* K, const kvc_layer* V, const kvc_tre
   if (d->q_stride_b < 0 || d->q_stride_h < 0 || d->q_stride_t < 0 || d->mask_stride_b < 0)
     return fail(KVC_EINVAL, "strides must be >= 0");
   const int64_t D = K->D;
-  if ((K->B > 1 && d->out_stride_b < D) || (d->Hq > 1 && d->out_stride_h < D) ||
-      (d->N > 1 && d->out_stride_t < D) || d->out_stride_b < 0 || d->out_stride_h < 0 ||
-      d->out_stride_t < 0)
-    return fail(KVC_EINVAL, "rows of out overlap");
+  // rows of out: each dimension steps over all that the ones with smaller strides cover
+  if (d->out_stride_b < 0 || d->out_stride_h < 0 || d->out_stride_t < 0)
+    return fail(KVC_EINVAL, "strides must be >= 0");
+  std::pair<int64_t, int64_t> dim[3] = {
+      {d->out_stride_b, K->B}, {d->out_stride_h, d->Hq}, {d->out_stride_t, d->N}};
+  std::sort(dim, dim + 3);
+  int64_t covered = D;
+  for (const auto& m : dim) {
+    if (m.second == 1) continue;
+    if (m.first < covered) return fail(KVC_EINVAL, "rows of out overlap");
+    if (m.first > INT64_MAX / 4 / m.second) return fail(KVC_EINVAL, "out's strides are too large");
+    covered += m.first * (m.second - 1);
+  }
   if ((uintptr_t)d->q % (d->q_dtype == KVC_F32 ? 4 : 2) || (uintptr_t)d->out % 2 ||
       (uintptr_t)d->first % 4)
     return fail(KVC_EINVAL, "an array is not aligned to its element size");

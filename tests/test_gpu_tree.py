@@ -301,6 +301,9 @@ def test_refusals(kvc):
     refused(first=torch.zeros(B, dtype=torch.int32))
     refused(workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
     refused(out=torch.empty(1, 1, 1, D, dtype=torch.float16, device=DEV).expand(B, 2 * H, N, D))
+    flat = torch.empty(4 * H * N * D, dtype=torch.float16, device=DEV)
+    refused(out=flat.as_strided((B, 2 * H, N, D), (0, D, D, 1)))                # heads and drafts meet
+    refused(out=flat.as_strided((B, 2 * H, N, D), (0, (N - 1) * D, D, 1)))      # the last and the first draft
     gk.append(torch.randn(B, H, 1, D, device=DEV).half())
     refused()                                               # different lengths
     gk.trim(1)
