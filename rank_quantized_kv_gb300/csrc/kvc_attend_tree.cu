@@ -388,6 +388,12 @@ __device__ __forceinline__ int64_t run_begin(const TreeArgs& t, int64_t c) {
   return t.total * c / t.grid;
 }
 
+// CUDA cores: a warp takes 32 tokens at a time, a lane scores one of them for the
+// job's 8 rows (key weights broadcast from shared memory), then the lanes share
+// out the value channels.  Bound by shared-memory reads, four fp32 weights to a
+// load.  128 slots of 32 rows over 16384 tokens of 3-bit keys and int8 values:
+// 5.6 ms (the tensor cores 0.18); 2 slots of 8 rows over 84 tokens in 29 us, launches included.
+//
 // Dynamic shared memory: ws [NCk][8], wxs [m + n_out][8], per warp krow [32 Pk + 16] and vrow
 // [32 Pv + 16] (uniform values) and ps [32][8]; merge [4][8][2 + Dv].
 template <int KMODE, int VMODE>
@@ -644,6 +650,10 @@ __global__ void __launch_bounds__(kThreads)
 
 constexpr int kCombineRows = 8, kCombineThreads = 256, kFactors = 64;
 
+// Bound by the latency of the partials' reads, few CTAs being at work: 8 slots of
+// 20 rows x 128 channels, about 20 CTAs' partials a slot, take 16 us; 128 slots
+// of 128 rows 19 us.
+//
 // Merge the partials of a job, normalise and write the output rows (uniform
 // values: project the weighted mean latent).  One block per (slot, 8 rows);
 // thread (d, q) holds channel d of rows 4 q .. 4 q + 3, which lie together in a
@@ -853,7 +863,8 @@ cudaError_t launch_attend_tree(const Params& kp, const Params& vp, TreeArgs t, v
     if (e != cudaSuccess) return e;
   }
   // rows of a projection block (measured, us: 4096 rows of 128 columns 19 with 32,
-  // 26 with 8; 4096 rows of 32 columns 18 and 13)
+  // 26 with 8; 4096 rows of 32 columns 18 and 13; 16384 rows of 128 columns 34
+  // with 64, the whole call 8 more with 32)
   const bool few = kp.r <= 64 || t.prow <= 16;
   const bool many = (int64_t)kp.n_slots * ((t.prow + 63) / 64) >= t.sms;
   const int rows = few ? 8 : many ? 64 : 32;

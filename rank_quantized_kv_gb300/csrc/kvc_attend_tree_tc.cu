@@ -37,10 +37,11 @@
 // Bound.  A tile's path S -> softmax -> P -> O is a chain of latencies (TMEM
 // loads, 128 x N exponentials, shared stores, barriers), so a CTA keeps four
 // tiles in flight; what is left is issue slots of the softmax and the decoders,
-// not DRAM and not the tensor core.  Measured (this kernel alone, us): 64 x 2
-// sequences and heads, 32 rows, 8192 tokens of 3-bit keys and int8 values 155,
-// about 2350 cycles a tile; 128 rows 283 (5400 cycles a tile of four times the
-// scores); 16 sequences of 16384 tokens of the same 78.
+// not DRAM and not the tensor core.  Measured (this kernel alone, us): 16
+// sequences of 8 heads, 32 rows a head, 16384 tokens of 3-bit keys and int8 values
+// 155, about 2350 cycles a tile (0.36 of the rate at which HBM delivers the rows);
+// with 128 rows 283 (5400 cycles a tile of four times the scores); one sequence of
+// 130001 tokens, 20 rows a head 78.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -1183,8 +1184,9 @@ bool choose_shape(const Params& kp, const Params& vp, const TreeArgs& t, Shape* 
 int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t, int* parts, int* K) {
   // Scores of two sums (residual sketches, outliers) take the CUDA-core kernel.  All
   // else goes to the tensor cores at every size (us of the call, CUDA cores and
-  // here: 8 rows, 300 tokens 29 and 16; 16 rows, 2000 tokens 38 and 27; 64 rows, 4096
-  // tokens 274 and 59; 32 rows, 8192 tokens of 128 slots 5567 and 177).
+  // here: 2 slots of 8 rows, 84 tokens 29 and 16; 15 slots of 21 rows, 1777 tokens 38
+  // and 27; 64 slots of 64 rows, 4096 tokens 274 and 59; 128 slots of 32 rows, 16384
+  // tokens 5567 and 177).
   if (t.prod) return 0;
   if (vp.mode == KVC_MODE_INT8 && vp.D % 8) return 0;  // value rows are read 8 bytes at a time
   Shape z;
