@@ -263,6 +263,8 @@ kvc_status kvc_attend_workspace_bytes(const kvc_layer *keys, const kvc_layer *va
  * mask[b, i, j] != 0, with k_hat and v_hat as in kvc_attend (the codes are not
  * reconstructed).  A draft that sees no token gets a row of zeros; what a
  * hidden token stores, infinities and NaN among it, has no effect.
+ * A weight is rounded to fp16 (relative 2^-11), and what it adds is held to
+ * 2^-31 of the row's largest weight times the head's largest visible value.
  *
  *  keys       a KVC_MODE_UNIFORM or KVC_MODE_CODEBOOK layer (with or without a
  *             residual sketch and outlier stream), D at most 256.

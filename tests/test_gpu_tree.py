@@ -139,6 +139,49 @@ def test_rising_scores(kvc):
     check(o, reference(gk, rk, gv, rv, q.double().numpy(), 1 / math.sqrt(D), N))
 
 
+def test_falling_values(kvc):
+    """Value rows that shrink along the sequence, by 2^20 in all, under weights that grow."""
+    B, H, D, S, N = 1, 2, 64, 900, 3
+    gk, gv, rk, rv = make_layers(kvc, "codebook", "int8", B, H, D, 0, 6, capacity=S, dev=DEV)
+    g = torch.Generator().manual_seed(12)
+    base = torch.randn(D, generator=g)
+    k = torch.linspace(-2, 6, S)[None, None, :, None] * base + 0.3 * torch.randn(B, H, S, D, generator=g)
+    v = torch.randn(B, H, S, D, generator=g) * torch.logspace(10, -10, S, base=2.0)[None, None, :, None]
+    gk.append(k.half().to(DEV))
+    gv.append(v.half().to(DEV))
+    q = (base + 0.1 * torch.randn(B, 2 * H, N, D, generator=g)).float()
+    o = kvc.attend_tree(gk, gv, q.to(DEV))
+    check(o, reference(gk, rk, gv, rv, q.double().numpy(), 1 / math.sqrt(D), N))
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_many_drafts(kvc, shared):
+    """More drafts than the threads of a block, several words of mask bits a
+    draft, jobs that begin inside a word."""
+    B, H, rep, D, S, N = 2, 1, 2, 64, 700, 333
+    mask = random_tree(np.random.default_rng(9), 1 if shared else B, N, unused=0.1)
+    gk, gv, rk, rv = make_layers(kvc, "uniform", "int8", B, H, D, S, 91, dev=DEV)
+    q = _q(B, H * rep, N, D, 9)
+    o = kvc.attend_tree(gk, gv, q.to(DEV), mask=_dev(mask[0] if shared else mask))
+    check(o, reference(gk, rk, gv, rv, q.double().numpy(), 1 / math.sqrt(D), N,
+                       mask=np.repeat(mask, B, 0) if shared else mask))
+
+
+def test_two_streams_at_once(kvc):
+    """Calls that overlap on two streams, each with scratch of its own: the bits of calls one by one."""
+    gk, gv, _, _ = make_layers(kvc, "codebook", "int8", 2, 2, 128, 4000, 95, dev=DEV)
+    qs = [_q(2, 8, 5, 128, 100 + i).to(DEV) for i in range(2)]
+    want = [kvc.attend_tree(gk, gv, q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            got[i].append(kvc.attend_tree(gk, gv, qs[i], stream=st))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
+
+
 def test_dropped_components(kvc):
     """Bases of which no component is kept: rows of no bytes, equal scores, the mean row."""
     B, H, D, S, N = 1, 2, 64, 300, 3
