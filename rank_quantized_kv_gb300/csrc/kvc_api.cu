@@ -38,6 +38,7 @@ struct kvc_layer {
   std::vector<int32_t> seg_host;     // [nb][kMaxSeg][4] width segments
   std::vector<int32_t> channels_host;  // [n_slots][n_out] outlier channels
   float cb_mul = 1.f;                // scale at which the centroids fall nearest to fp16 values
+  float w_unit = 0.f;                // codebook: largest ||V_j||, u_j of a query of unit variance
   bool batch_free = true;            // bases and outlier channels of (b, h) are those of (0, h)
   uint64_t format[2] = {0, 0};       // hash of everything a stored row decodes by
   kvc::TcPlan tc{};                  // tensor-core path tables (kvc_tc.cu)
@@ -673,6 +674,10 @@ static kvc_status init_from_geo(const kvc_layer_desc* d, Geo& g, kvc_layer** out
       L->batch_free = false;
   }
   if (g.cb_levels) L->cb_mul = centroid_scale(d->codebook, g.cb_levels);
+  if (d->mode == KVC_MODE_CODEBOOK) {
+    const float* vnorm = reinterpret_cast<const float*>(im.bytes.data() + im.oVn);
+    L->w_unit = *std::max_element(vnorm, vnorm + (size_t)g.nb * g.r);
+  }
   *out = L;
   return succeed();
 }
@@ -1002,6 +1007,14 @@ kvc_status kvc_attend_tree(const kvc_layer* K, const kvc_layer* V, const kvc_tre
   t.o_st = d->out_stride_t;
   const double sc = d->scale > 0.f ? (double)d->scale : 1.0 / std::sqrt((double)K->D);
   t.scale_log2 = (float)(sc * 1.4426950408889634);
+  if (t.tc && K->mode == KVC_MODE_CODEBOOK) {
+    // the windows lie so that the largest of a row's weights falls into the middle
+    // of one for queries of about unit variance (three deviations)
+    const double typical = 3.0 * t.scale_log2 * t.w_mul * K->w_unit;
+    int e = 0;
+    if (typical > 0.0 && std::isfinite(typical)) std::frexp(typical, &e);
+    t.w_shift = 4 - e;
+  }
   int nk = 0;
   const cudaError_t e = kvc::launch_attend_tree(K->p, V->p, t, workspace,
                                                 static_cast<cudaStream_t>(stream), &nk);

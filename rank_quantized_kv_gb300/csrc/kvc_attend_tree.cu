@@ -114,10 +114,19 @@ __device__ void pack_mask(const TreeArgs& t, int block) {
   t.mask_bits[((size_t)b * t.N + j) * words + w] = v;
 }
 
-// The key weights at every packed position (for the tensor cores: split into two
-// fp16 pieces and laid out as their operand), w_j = scale log2(e) u_j coef_j
+// The key weights at every packed position, w_j = scale log2(e) u_j coef_j
 // (coef = step in uniform mode, 1 for a codebook), and c1, for ROWS rows of a
 // slot per block; u = q V in fp32, by the block's 256 threads.
+//
+// For the tensor cores a row's weights are split into two fp16 pieces and laid
+// out as their operand.  They are first divided by a power of two 2^ex that
+// brings the row's largest to [2^-6, 2^14), from where the pieces carry 22 bits
+// of the large weights and leave at most 2^-25, that is 2^-19 of the largest, of
+// any.  The softmax multiplies the products by 2^ex: at no cost where the rows of
+// a job have one ex (it goes into the token's norm), so ex is not taken to the
+// last bit but in steps of 20, windows that w_shift puts around the usual sizes.
+// Uniform keys have no norm that would multiply what the pieces leave, and codes of
+// at most 128: their small weights stay as they are (ex >= 0).
 //   64, 32    a register-tiled product, 8 or 4 rows x 4 columns a thread and 128
 //   rows      columns a warp, V through shared memory 32 rows at a time: bound by
 //             the fp32 FMA pipe (rows D r of them);
@@ -142,7 +151,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
   __shared__ float coef[256];        // component: factor of its weight, 0 when dropped
   __shared__ float off[256];         // component: lo + 2^(b-1) step
   __shared__ int64_t q_row[ROWS];    // first element of a row of q, -1 past the last
-  __shared__ float down[ROWS];       // power of two that brings a row into fp16's range
+  __shared__ float down[ROWS];       // power of two that brings a row into its window
   const int D = kp.D, r = kp.r, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int blocks = (t.prow + ROWS - 1) / ROWS;
   if ((int)blockIdx.x >= blocks * kp.n_slots) {
@@ -323,9 +332,11 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const Params kp
     if (lane == 0 && row < np) {
       t.c1[row0 + row] = t.scale_log2 * c1[e];
       if (t.tc) {
-        const int ex = max(0, (__float_as_int(most) >> 23) - 127 - 13);
-        t.wscale[row0 + row] = __int_as_float((127 + ex) << 23);
-        down[row] = __int_as_float((127 - ex) << 23);
+        const int at = (__float_as_int(most) >> 23) - 127 + t.w_shift + 6;
+        const int step = (at >= 0 ? at / 20 : -((19 - at) / 20)) * 20 - t.w_shift;
+        const int ex = min(126, max(uniform ? 0 : -126, step));
+        t.wscale[row0 + row] = most > 0.f ? __int_as_float((127 + ex) << 23) : 0.f;
+        down[row] = most > 0.f ? __int_as_float((127 - ex) << 23) : 1.f;
       }
     }
   }

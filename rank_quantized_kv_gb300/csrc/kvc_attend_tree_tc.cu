@@ -21,10 +21,13 @@
 //
 // Precision.  Codes are exact in fp16 (centred codes up to 128, int8 values).
 // Centroids are rounded to fp16 after a common scale, chosen at init so that
-// they fall nearest to fp16 values.  The key weights W carry two fp16 pieces
-// (22 bits).  P is rounded to fp16: one rounding of relative 2^-11 per weight,
-// independent between tokens, below the rounding of the 16-bit output.  S, O,
-// the sums and the softmax's reference are fp32.
+// they fall nearest to fp16 values (relative 2^-11 at most; 2^-14 for the eight
+// levels of a Gaussian).  The key weights W are two fp16 pieces of weights that
+// a power of two per row brings into fp16's upper range: 22 bits of the large
+// ones, an error of at most 2^-19 of the row's largest.  P is rounded to fp16:
+// one rounding of relative 2^-11 per weight, independent between tokens, below
+// the rounding of the 16-bit output.  S, O, the sums and the softmax's reference
+// are fp32.
 //
 // Softmax.  A weight is 2^(s - m) with m a reference per row, not the running
 // maximum itself: m is set to the tile's maximum less 6 when the row first sees
@@ -391,7 +394,8 @@ struct Place {
   int plain0, plain1;  // tiles that hold visible context alone
   int first;
   const uint32_t* mask;  // per draft, which drafts see it
-  int scaled;          // some row's key weights were beyond fp16's range
+  int scaled;          // the rows' products have different factors
+  float fold;          // codebook keys: their common factor, else 1
   int Pk, Pv;          // decoders: row bytes
   __device__ void next(const TreeArgs& t, int H) { more = w.next(t, H, g); }
 };
@@ -785,18 +789,29 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
       named_bar_sync(bar, 128);
       if (!pl.more) break;
       const int ncol = max(0, min(NC, pl.g.nr - col0));  // rows of this group
-      bool big = false;
+      // the rows' factors (0: any will do): one for all goes into the token's norm
+      float ws = 0.f, common = 1.f;
       if (ltid < NC) {
         const size_t row = (size_t)pl.g.slot * t.prow + pl.g.r0 + col0 + ltid;
-        const float c1 = t.c1[row], ws = t.wscale[row];
-        cn[ltid] = c1;
-        wscale[wg][ltid] = ws;
-        big = ws != 1.f;
+        cn[ltid] = t.c1[row];
+        if (ltid < ncol) ws = t.wscale[row];
         mref[wg][ltid] = 0.f;
         seen[wg][ltid] = ltid >= ncol;
       }
-      const bool scaled = named_bar_or(bar, 128, big);
-      if (ltid == 0) pl.scaled = scaled;
+      if (KMODE == KVC_MODE_CODEBOOK) {
+        const float m = warp_max_redux(ws);
+        if (lane == 0) red[wg][quarter][0] = m;
+        named_bar_sync(bar, 128);
+        const float most = fmaxf(fmaxf(red[wg][0][0], red[wg][1][0]), fmaxf(red[wg][2][0], red[wg][3][0]));
+        if (most != 0.f) common = most;
+      }
+      const bool scaled = named_bar_or(bar, 128, ws != 0.f && ws != common);
+      if (ltid < NC) wscale[wg][ltid] = !scaled ? 1.f : ws == 0.f ? common : ws;
+      if (ltid == 0) {
+        pl.scaled = scaled;
+        if (KMODE == KVC_MODE_CODEBOOK) pl.fold = scaled ? 1.f : common;
+      }
+      if (KMODE == KVC_MODE_CODEBOOK) named_bar_sync(bar, 128);
       float2 l[NC / 2];
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) l[i] = make_float2(0.f, 0.f);
@@ -822,7 +837,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
         const int s = gt % SB;                         // S buffer, and its phase
         const uint32_t s_par = (gt / SB) & 1;
         const uint32_t s_tm = tm + lane_off + z.s_col + s * N + col0;
-        float nt = KMODE == KVC_MODE_CODEBOOK ? __half2float(__ushort_as_half(nt_next)) : 1.f;
+        float nt = KMODE == KVC_MODE_CODEBOOK ? __half2float(__ushort_as_half(nt_next)) * pl.fold : 1.f;
         const float st = VU ? 1.f : __half2float(__ushort_as_half(st_next));
         if (!VU && st != st) nt = st;  // a scale of NaN: the weights of those who see it
         wait_or_abort(&s_full[s], s_par, &abort_flag);
@@ -991,7 +1006,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
             if (lane == 0) mbar_arrive(&s_empty[s]);
           }
           if (general) {
-            if (pl.scaled) {  // rows of key weights beyond fp16's range
+            if (pl.scaled) {  // a factor per row
               uint32_t r[CH];
               tmem_ld_n<CH>(s_tm + ch * CH, r);
               tmem_wait_ld();

@@ -147,10 +147,11 @@ struct TreeArgs {
   int prod = 0, m = 0, n_out = 0, kcode = 0, knw = 1;
   int tc = 0;                            // tensor-core kernel: its columns (rows of a job), 0: CUDA cores
   float cb_mul = 1.f, w_mul = 1.f;       // tensor cores: scale of the centroids, its inverse
+  int w_shift = 0;                       // tensor cores, codebook keys: place of the row factors' windows
   // workspace: the key weights, fp32 [n_slots rows][NCk] or, for the tensor
-  // cores, two fp16 pieces per job in the operand's layout [jobs][2][rt x K]; a
-  // power of two that multiplies a row's scores (1 but for weights beyond fp16's
-  // range); the score offsets.  Rows padded to prow per slot (whole jobs).
+  // cores, two fp16 pieces per job in the operand's layout [jobs][2][rt x K]; the
+  // power of two that multiplies a row's products (0: any will do, the row has no
+  // finite weight but 0); the score offsets.  Rows padded to prow per slot (whole jobs).
   uint32_t* mask_bits = nullptr;         // tensor cores: [B or 1][N][N / 32] bits, bit n of
                                          // draft j set where draft n sees j
   float* w = nullptr;
