@@ -15,7 +15,8 @@
 //            weight is 0 whatever its codes, norm or scale hold;
 //   output   int8 values    sum_t p_t s_t q8_t;
 //            uniform values (lo + 2^(b-1) step + step sum_t p_t c'_t) V^T + mean;
-//            zero for a row that sees no token.
+//            zero for a row that sees no token, NaN for one that sees a score
+//            of NaN or of +inf, or scores of -inf alone.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_pipeline.h>
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(kThreads)
           see = mask ? mask[(int64_t)n * t.N + draft] != 0 : draft <= n;
         }
         const float s = see ? sc[g] + c1s[g] : -INFINITY;
-        const float mn = fmaxf(m[g], warp_max(s));
+        const float mn = fmaxf(m[g], warp_max(see ? fmaxf(s, kTreeLowest) : -INFINITY));
         const float ref = mn == -INFINITY ? 0.f : mn;  // nothing visible yet
         const float corr = exp2f(m[g] - ref);
         const float pt = see ? exp2f(s - ref) : 0.f;
@@ -740,7 +741,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
   }
   L = warp_sum(L);
-  if (lane == 0) inv_s[warp] = L > 0.f || L != L ? 1.f / L : 0.f;  // nothing visible: zero
+  // nothing visible: zero; scores of -inf alone: NaN
+  if (lane == 0) inv_s[warp] = L > 0.f || L != L ? 1.f / L : M == -INFINITY ? 0.f : NAN;
   __syncthreads();
   auto put = [&](int d, float4 v) {  // channel d of the thread's four rows
     const float x[4] = {v.x, v.y, v.z, v.w};
@@ -783,8 +785,8 @@ __global__ void __launch_bounds__(kCombineThreads)
       v.z = fmaf(zz.z, c, v.z);
       v.w = fmaf(zz.w, c, v.w);
     }
-    put(i, make_float4(inv.x == 0.f ? 0.f : v.x, inv.y == 0.f ? 0.f : v.y, inv.z == 0.f ? 0.f : v.z,
-                       inv.w == 0.f ? 0.f : v.w));
+    auto row = [](float x, float f) { return f == 0.f ? 0.f : f != f ? f : x; };
+    put(i, make_float4(row(v.x, inv.x), row(v.y, inv.y), row(v.z, inv.z), row(v.w, inv.w)));
   }
 }
 

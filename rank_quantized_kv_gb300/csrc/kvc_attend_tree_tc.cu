@@ -317,10 +317,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
-// The warp's maximum (NaN only where every lane has NaN).
+// The larger of two, NaN where either is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// The warp's maximum, NaN where a lane has NaN.
 __device__ __forceinline__ float warp_max_redux(float v) {
   float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
   return y;
 }
 // Sums over the warp's lanes of 2 W columns: in each step a lane hands half of
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
   __shared__ __align__(16) float cneg[2][NC];
   __shared__ __align__(16) float corr[2][NC], red[2][4][NC];
   __shared__ float mref[2][NC], wscale[2][NC];
-  __shared__ int seen[2][NC];
+  __shared__ int seen[2][NC];  // 0: no token, 1: weights summed, 2: only scores of -inf
   __shared__ __align__(16) unsigned char place_s[(2 + DG) * sizeof(Place)];  // softmax groups, decoder groups
   Place* place = reinterpret_cast<Place*>(place_s);
   __shared__ __align__(16) unsigned short side_s[kSideRing][2][kTile];  // norms, scales
@@ -921,7 +928,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float f = fmaf(__uint_as_float(r[i]) * wscale[wg][c + i], nt, cn[c + i]);
-                m[i] = warp_max_redux(v >> i & 1u ? f : -INFINITY);
+                m[i] = warp_max_redux(v >> i & 1u ? max_nan(f, kTreeLowest) : -INFINITY);
               }
               if (lane == 0)
 #pragma unroll
@@ -932,14 +939,16 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
             named_bar_sync(bar, 128);
             bool blind = false;
             if (ltid < NC) {
-              const float m = fmaxf(fmaxf(red[wg][0][ltid], red[wg][1][ltid]),
-                                    fmaxf(red[wg][2][ltid], red[wg][3][ltid]));
+              const float m = max_nan(max_nan(red[wg][0][ltid], red[wg][1][ltid]),
+                                      max_nan(red[wg][2][ltid], red[wg][3][ltid]));
               float d = 0.f, f = 1.f;
-              if (m != -INFINITY) {  // (a row of NaN counts as seen and stays NaN)
-                if (!seen[wg][ltid]) {  // nothing summed yet
-                  d = m - kSet;
-                  f = 0.f;
-                  seen[wg][ltid] = 1;
+              if (m != -INFINITY) {  // (a row with a score of NaN counts as seen and stays NaN)
+                if (seen[wg][ltid] != 1) {  // nothing summed yet
+                  if (m != kTreeLowest) {
+                    d = m - kSet;
+                    f = 0.f;
+                  }
+                  seen[wg][ltid] = m != kTreeLowest ? 1 : 2;
                 } else if (m > kMove) {
                   d = m - kSet;
                   f = ex2(-d);
@@ -950,7 +959,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
               mref[wg][ltid] += d;
               cn[ltid] -= d;
               corr[wg][ltid] = f;
-              blind = !seen[wg][ltid];
+              blind = seen[wg][ltid] != 1;
             }
             // rows that saw nothing yet keep every tile on this path
             if (!named_bar_or(bar, 128, blind) && !pl.scaled) fast1 = pl.plain1;
@@ -1075,10 +1084,10 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
       // weighted sums by channel, a partial's rows together: [Dvp][rt]
       float* part = t.part + (prow - col0) * t.Dvp + col0;
       if (ltid < ncol) {
-        const bool sn = seen[wg][ltid] != 0;
+        const int sn = seen[wg][ltid];
         t.ml[prow + ltid] = make_float2(
-            sn ? mref[wg][ltid] : -INFINITY,
-            sn ? (red[wg][0][ltid] + red[wg][1][ltid]) + (red[wg][2][ltid] + red[wg][3][ltid]) : 0.f);
+            sn == 1 ? mref[wg][ltid] : sn ? kTreeLowest : -INFINITY,
+            sn == 1 ? (red[wg][0][ltid] + red[wg][1][ltid]) + (red[wg][2][ltid] + red[wg][3][ltid]) : 0.f);
       }
       for (int m = 0; m < z.mt; ++m) {
         const int d = m * 128 + lt;

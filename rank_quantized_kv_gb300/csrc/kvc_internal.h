@@ -126,6 +126,9 @@ cudaError_t launch_attend(const Params& kp, const Params& vp, AttendArgs a, void
 // (job, CTA) pair leaves `parts` partials from number (job + CTA) parts on (job
 // and CTA only ever grow along the line, so the numbers are unique).
 constexpr int kTreeTile = 128;
+// Reference of a row that has seen tokens, all with scores of -inf (below fp32's
+// range); one that has seen none has -inf.
+constexpr float kTreeLowest = -3.402823466e38f;
 struct TreeArgs {
   const void* q = nullptr;
   int q_dtype = 0;
