@@ -305,7 +305,9 @@ kvc_status kvc_attend_tree_workspace_bytes(const kvc_layer *keys, const kvc_laye
 
 /* Run it, asynchronously on `stream`.  workspace: device, 256-byte aligned.
  * KVC_EINVAL for unsupported modes or shapes, mismatched layers, overlapping
- * rows of out, host pointers or a short workspace; nothing is launched then. */
+ * rows of out, host pointers or a short workspace; nothing is launched then.
+ * kvc_sync_status(keys) reports KVC_ETIMEOUT, and out is undefined, where the
+ * kernel's limit ran out (kvc_set_wait_limit). */
 kvc_status kvc_attend_tree(const kvc_layer *keys, const kvc_layer *values,
                            const kvc_tree_desc *desc, void *workspace, size_t workspace_bytes,
                            void *stream);
@@ -488,12 +490,15 @@ kvc_status kvc_fit_uniform(const kvc_fit_desc *desc, void *workspace, size_t wor
 
 /* Limit, in nanoseconds, of the waits inside the warp-specialised tensor-core
  * append kernel (one role waiting for another: a tile loaded, an accumulator
- * written or released).  A kernel whose wait runs out stops its work, waits
- * for its copies and tensor-core work already in flight (up to 2 s), frees its
+ * written or released) and, for a key layer, of the time in which a CTA of
+ * kvc_attend_tree's tensor-core kernel finishes no tile of 128 tokens (looked at
+ * every 20 us or so).  A kernel whose limit runs out stops its work, waits for
+ * its copies and tensor-core work already in flight (up to 2 s), frees its
  * tensor memory and returns; kvc_sync_status then reports KVC_ETIMEOUT and the
- * rows of that call are undefined.  ns == 0 restores the default of 2 s; a
- * limit shorter than a kernel's normal waits makes every call time out.
- * Host-only.  KVC_EINVAL if ns < 0. */
+ * rows appended, or the output, of that call are undefined.  ns == 0 restores
+ * the default of 2 s; a limit shorter than a kernel's normal waits makes every
+ * call time out (tree attention: every call whose CTAs run for longer than that
+ * and 20 us).  Host-only.  KVC_EINVAL if ns < 0. */
 kvc_status kvc_set_wait_limit(kvc_layer *layer, int64_t ns);
 
 /* Synchronise `stream`, then read and clear the layer's device error word:

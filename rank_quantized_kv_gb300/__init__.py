@@ -460,7 +460,8 @@ class KVCacheLayer:
                 "params": e.params, "gain": e.gain}
 
     def set_wait_limit(self, ns: int):
-        """Limit (ns) of the append kernel's waits; 0 restores the default (2 s)."""
+        """Limit (ns) of the waits inside the append kernel and, for a key layer, the tree
+        attention; 0 restores the default (2 s)."""
         _check(self._lib.kvc_set_wait_limit(self._h, int(ns)))
 
     def sync_status(self, stream=None) -> int:

@@ -938,6 +938,7 @@ static kvc_status tree_check(const kvc_layer* K, const kvc_layer* V, int32_t Hq,
   if (t.tc) {
     t.cb_mul = K->cb_mul;
     t.w_mul = 1.f / K->cb_mul;
+    t.wait_ns = K->wait_ns;
   }
   *ws_bytes = kvc::tree_plan(K->p, t, kvc::sm_count());
   return KVC_OK;

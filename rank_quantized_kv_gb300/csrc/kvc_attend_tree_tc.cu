@@ -14,7 +14,8 @@
 //                         codes -> fp16 V in shared memory;
 //   two MMA warps         S = A W^T, and O += V^T P;
 //   softmax (2 groups of 4 warps; lane = token)
-//                         S -> P in fp16 in shared memory, sums of P in fp32.
+//                         S -> P in fp16 in shared memory, sums of P in fp32;
+//   watchdog (1 thread)   gives up, for all roles, when no tile gets done.
 // Jobs of up to 64 rows: the softmax groups take alternate tiles, each with its
 // own references, sums and O, which the combine joins.  Jobs of 128 rows: TMEM
 // does not hold two O, so the groups take half of the columns each.
@@ -72,12 +73,13 @@ constexpr int kMaxNS = 4;          // row stages
 constexpr int kSideRing = 16;
 static_assert(kSideRing >= kMaxNS + 2 + 4, "side words overwritten before they are read");
 constexpr int kSoftBar = 1, kDecBar = 3;  // named barriers: softmax groups 1, 2; decoder groups 3, 4
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = 2000000000ull;  // limit of the drains; the watchdog's is the layer's
+constexpr uint32_t kTryNs = 20000;             // a try sleeps so long at most
 constexpr float kSet = 6.f;        // a reference is set this far below the maximum (log2)
 constexpr float kMove = 12.f;      // and moves when a score lies this far above it
 
 // Roles by warp: softmax 0..7, decoders 8.., then producer, S and O issuers and
-// one idle warp (setmaxnreg works on whole groups of four).  Two decoder groups
+// watchdog (setmaxnreg works on whole groups of four).  Two decoder groups
 // take alternate tiles; jobs of 128 rows, which decode a tile for twice the rows,
 // give the second group's registers to the softmax.  The registers of the launch
 // (65536 / threads, rounded down to 8) are split among the roles; ptxas is held
@@ -417,22 +419,14 @@ struct Ring {
   }
 };
 
-// Wait for a phase.  Once a wait of any role has run out (2 s) every further
-// wait returns soon, so that all roles walk to their ends and the named
-// barriers stay matched; the results are then undefined and the error word says
-// so.  The loop is short because a try returns early (waiting warps would take
-// issue slots from working ones): time and flag are looked at every 64 tries.
+// Wait for a phase, or until the watchdog has given up.  From then on every wait
+// returns after one failed try, so that all roles walk to their ends and the
+// named barriers stay matched; the results are undefined and the error word says
+// so.  (The waits stand in every role's code and on the tiles' path: with a clock
+// in each the serving batch took 180 us to 190 in place of 176.)
 __device__ __forceinline__ void wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_sleep(bar, parity, 10000000u)) return;
-    if (i % 64 == 0) {
-      const uint64_t now = global_timer_ns();
-      if (t0 == 0) t0 = now;
-      if (*abort_flag) return;
-      if (now - t0 > kWaitNs) *abort_flag = 1;
-    }
-  }
+  while (!mbar_try_wait_sleep(bar, parity, kTryNs))
+    if (*abort_flag) return;
 }
 
 template <int KMODE, int VMODE, int NC, bool HALVES>
@@ -460,7 +454,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
   __shared__ __align__(16) unsigned short side_s[kSideRing][2][kTile];  // norms, scales
   __shared__ uint32_t tab[KMODE == KVC_MODE_CODEBOOK ? 64 * 32 : 1];  // codebook tables
   __shared__ uint32_t tmem_base;
-  __shared__ volatile int abort_flag;
+  __shared__ volatile int abort_flag, tiles_done;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char* Ws = smem;  // two pieces [N x K] fp16, K-major cores
@@ -488,7 +482,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
     mbar_init(&w_empty, 1);
     mbar_init(&done_bar, 2);
     fence_mbar_init();
-    abort_flag = 0;
+    abort_flag = tiles_done = 0;
   }
   if (tid < 2 + DG) place[tid].w = Walk(t);
   if (KMODE == KVC_MODE_CODEBOOK) {  // pairs of 16 levels, 256 levels, or pairs once per lane
@@ -636,6 +630,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
             commit_if(lead, &p_empty[wg]);
             if (!HALVES || h == 1) commit_if(lead, &v_empty[rv.slot]);
           }
+          tiles_done = it + 1;  // (every lane the same)
         }
       }
       if (lead) {
@@ -643,6 +638,23 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
         mbar_wait_bounded(&done_bar, 0, kWaitNs);
       }
       __syncwarp();
+    } else if (lane == 0) {
+      // ---------------------------------------------------------- watchdog
+      // Gives up when no tile has been summed for the limit, as it finds each time
+      // that the end has not come within a try.
+      int seen_done = 0;
+      uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait_sleep(&done_bar, 0, kTryNs)) {
+        const uint64_t now = global_timer_ns();
+        if (now - t0 > t.wait_ns) {
+          abort_flag = 1;
+          break;
+        }
+        if (tiles_done != seen_done) {
+          seen_done = tiles_done;
+          t0 = now;
+        }
+      }
     }
   } else if (warp >= kSoftWarps) {
     // ------------------------------------------------------------ decoders
@@ -1111,7 +1123,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
     }
   }
   __syncthreads();
-  grid_dependents_launch();  // (from the idle warp at the start, the combine's blocks came in the way)
+  grid_dependents_launch();  // (at the start, the combine's blocks came in the way)
   if (abort_flag && tid == 0) atomicCAS(kp.err, 0, kErrTimeout);
   if (warp == R::score) {
     tc_fence_after();

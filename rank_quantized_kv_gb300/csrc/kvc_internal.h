@@ -150,6 +150,7 @@ struct TreeArgs {
   int prod = 0, m = 0, n_out = 0, kcode = 0, knw = 1;
   int tc = 0;                            // tensor-core kernel: its columns (rows of a job), 0: CUDA cores
   float cb_mul = 1.f, w_mul = 1.f;       // tensor cores: scale of the centroids, its inverse
+  uint64_t wait_ns = 0;                  // tensor cores: limit of the time without a finished tile
   int w_shift = 0;                       // tensor cores, codebook keys: place of the row factors' windows
   // workspace: the key weights, fp32 [n_slots rows][NCk] or, for the tensor
   // cores, two fp16 pieces per job in the operand's layout [jobs][2][rt x K]; the
