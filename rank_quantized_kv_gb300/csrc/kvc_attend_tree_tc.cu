@@ -1217,16 +1217,27 @@ bool choose_shape(const Params& kp, const Params& vp, const TreeArgs& t, Shape* 
 
 }  // namespace
 
+// The kernel for a shape, with its shared memory allowed; null where the compiler
+// gave it other registers than the roles' split draws on (setmaxnreg would wait
+// for ever with fewer): it is never launched then.
+static TcKernel ready_kernel(const Params& kp, const Params& vp, const Shape& z, int* threads) {
+  int regs = 0, has = 0;
+  const TcKernel k = kernel_for(kp.mode, vp.mode, z, threads, &regs);
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), z.smem, &has);
+  return e == cudaSuccess && has == regs ? k : nullptr;
+}
+
 int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t, int* parts, int* K) {
-  // Scores of two sums (residual sketches, outliers) take the CUDA-core kernel.  All
-  // else goes to the tensor cores at every size (us of the call, CUDA cores and
-  // here: 2 slots of 8 rows, 84 tokens 29 and 16; 15 slots of 21 rows, 1777 tokens 38
-  // and 27; 64 slots of 64 rows, 4096 tokens 274 and 59; 128 slots of 32 rows, 16384
-  // tokens 5567 and 177).
+  // Scores of two sums (residual sketches, outliers) take the CUDA-core kernel, and
+  // layers for which there is no shape or no ready kernel.  All else goes to the
+  // tensor cores at every size (us of the call, CUDA cores and here: 2 slots of 8
+  // rows, 84 tokens 29 and 16; 15 slots of 21 rows, 1777 tokens 38 and 27; 64 slots of
+  // 64 rows, 4096 tokens 274 and 59; 128 slots of 32 rows, 16384 tokens 5567 and 177).
   if (t.prod) return 0;
   if (vp.mode == KVC_MODE_INT8 && vp.D % 8) return 0;  // value rows are read 8 bytes at a time
   Shape z;
-  if (!choose_shape(kp, vp, t, &z)) return 0;
+  int threads = 0;
+  if (!choose_shape(kp, vp, t, &z) || !ready_kernel(kp, vp, z, &threads)) return 0;
   *parts = z.halves == 2 ? 1 : 2;
   *K = z.K;
   return z.n;
@@ -1236,13 +1247,9 @@ cudaError_t launch_tree_tc(const Params& kp, const Params& vp, const TreeArgs& t
                            int* nk) {
   Shape z;
   if (!choose_shape(kp, vp, t, &z)) return cudaErrorInvalidValue;
-  int threads = 0, regs = 0;
-  TcKernel k = kernel_for(kp.mode, vp.mode, z, &threads, &regs);
-  // the register split draws on what the launch gives: never launch with less
-  int has = 0;
-  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), z.smem, &has);
-  if (e != cudaSuccess) return e;
-  if (has != regs) return cudaErrorLaunchOutOfResources;
+  int threads = 0;
+  const TcKernel k = ready_kernel(kp, vp, z, &threads);
+  if (!k) return cudaErrorLaunchOutOfResources;
   ++*nk;
   return launch_dependent(k, (unsigned)t.grid, threads, (size_t)z.smem, s, kp, vp, t, z);
 }

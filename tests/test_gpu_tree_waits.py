@@ -37,8 +37,11 @@ def _layer(kvc, mode, B, H, D, S):
 
 @pytest.mark.parametrize("kmode,vmode,D,rep,N,S", [("codebook", "int8", 128, 2, 4, 250000),
                                                    ("uniform", "uniform", 64, 4, 8, 250000),
+                                                   ("uniform", "int8", 128, 4, 15, 100000),
                                                    ("codebook", "uniform", 128, 8, 16, 100000)])
 def test_wait_limit_times_out_and_recovers(kvc, kmode, vmode, D, rep, N, S):
+    """16, 32, 64 and 128 columns.  (Only the tensor-core kernel can time out, so this
+    also shows that it is the one that runs.)"""
     B, H = 2, 4
     gk, gv = _layer(kvc, kmode, B, H, D, S), _layer(kvc, vmode, B, H, D, S)
     q = torch.randn(B, H * rep, N, D, generator=torch.Generator().manual_seed(9)).to(DEV)
