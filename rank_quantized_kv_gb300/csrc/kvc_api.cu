@@ -37,7 +37,7 @@ struct kvc_layer {
   std::vector<int64_t> pay_host, side_host;
   std::vector<int32_t> seg_host;     // [nb][kMaxSeg][4] width segments
   std::vector<int32_t> channels_host;  // [n_slots][n_out] outlier channels
-  float cb_mul = 1.f;                // scale at which the centroids fall nearest to fp16 values
+  float cb_mul = 1.f;                // scale at which the centroids fall nearest to fp16 values (0: none)
   float w_unit = 0.f;                // codebook: largest ||V_j||, u_j of a query of unit variance
   bool batch_free = true;            // bases and outlier channels of (b, h) are those of (0, h)
   uint64_t format[2] = {0, 0};       // hash of everything a stored row decodes by
@@ -526,14 +526,15 @@ kvc_status kvc_init_layer_prod(const kvc_layer_desc* d, const kvc_prod_desc* pro
 // (least sum of squares over the levels, relative to m): a kernel that
 // multiplies the centroids in fp16 takes m c and divides its other factor by m.
 // 4096 steps over a factor of two bring eight levels within about a seventh of
-// fp16's half step; the largest level is put in [16, 32), far from both ends of
-// fp16's range.
+// fp16's half step; the largest level is put in [8, 32), far from both ends of
+// fp16's range.  0 where fp32 does not hold m (levels below 2^-115).
 static float centroid_scale(const float* c, int n) {
   float big = 0.f;
   for (int j = 0; j < n; ++j) big = std::max(big, std::fabs(c[j]));
   if (!(big > 0.f)) return 1.f;
   int e;
   std::frexp(big, &e);  // big in [2^(e-1), 2^e)
+  if (e < -115) return 0.f;
   const float base = std::ldexp(1.f, 5 - e);
   float best = base;
   double least = INFINITY;
@@ -934,7 +935,8 @@ static kvc_status tree_check(const kvc_layer* K, const kvc_layer* V, int32_t Hq,
   }
   DeviceGuard dg(K->device);
   if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
-  if (K->path == KVC_PATH_AUTO) t.tc = kvc::tree_tc_rows(K->p, V->p, t, &t.parts, &t.K);
+  if (K->path == KVC_PATH_AUTO && K->cb_mul > 0.f)
+    t.tc = kvc::tree_tc_rows(K->p, V->p, t, &t.parts, &t.K);
   if (t.tc) {
     t.cb_mul = K->cb_mul;
     t.w_mul = 1.f / K->cb_mul;

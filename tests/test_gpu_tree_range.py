@@ -21,9 +21,10 @@ import pytest
 import torch
 
 import tree_cases
-from kvc_cases import fit_codebook
+from kvc_cases import fit_codebook, oracle_kwargs
 from oracle import codec
 from oracle.attend import attend_tree_rows, tree_visible
+from oracle.layer import OracleLayer
 from tree_cases import check, make_layers, random_tree, terms
 
 pytestmark = pytest.mark.gpu
@@ -173,3 +174,20 @@ def test_rounded_centroids_are_near(kvc):
     for bits in (1, 2, 3, 4):
         c = fit_codebook(128, bits)["codebook"].astype(np.float64)
         assert np.all(np.abs(rounded_centroids(c) - c) <= 2.0 ** -11 * np.abs(c) * (1 + 2.0 ** -20))
+
+
+@pytest.mark.parametrize("size", [2.0 ** -124, 2.0 ** 100])
+def test_very_small_and_large_codebooks(kvc, size):
+    """Centroids at the ends of fp32's range under queries that bring the scores back."""
+    B, H, rep, D, S, N = 1, 2, 2, 64, 300, 4
+    p = fit_codebook(D, 3)
+    p["codebook"] = (p["codebook"] * np.float32(size)).astype(np.float32)
+    gk = kvc.KVCacheLayer("codebook", B, H, D, in_dtype="f16", capacity=S, device=DEV,
+                          path=tree_cases.PATH[0], **p)
+    rk = OracleLayer("codebook", B, H, D, **oracle_kwargs(p))
+    _, gv, _, rv = make_layers(kvc, "codebook", "int8", B, H, D, S, 88, dev=DEV)
+    g = torch.Generator().manual_seed(4)
+    gk.append(torch.randn(B, H, S, D, generator=g).half().to(DEV))
+    q = torch.randn(B, H * rep, N, D, generator=g) * (0.5 / size)
+    o = kvc.attend_tree(gk, gv, q.to(DEV))
+    check(o, tree_cases.reference(gk, rk, gv, rv, q.double().numpy(), 1 / math.sqrt(D), N))
