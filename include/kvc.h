@@ -263,8 +263,17 @@ kvc_status kvc_attend_workspace_bytes(const kvc_layer *keys, const kvc_layer *va
  * mask[b, i, j] != 0, with k_hat and v_hat as in kvc_attend (the codes are not
  * reconstructed).  A draft that sees no token gets a row of zeros; what a
  * hidden token stores, infinities and NaN among it, has no effect.
- * A weight is rounded to fp16 (relative 2^-11), and what it adds is held to
- * 2^-31 of the row's largest weight times the head's largest visible value.
+ * A draft that sees a score of NaN or +inf, or scores of -inf alone (below
+ * fp32's range), gets a row of NaN.
+ * kvc_attend computes in fp32, and so does this call for a key layer on
+ * KVC_PATH_GENERIC, for keys with a residual sketch or outlier stream and for
+ * int8 values with D not a multiple of 8.  Elsewhere it works on the tensor
+ * cores, sums and softmax statistics in fp32, with these roundings: a codebook's
+ * centroids to fp16 after a common scale (relative 2^-11 at most, 2^-14 for eight
+ * Gaussian levels); the key weights of a row within 2^-19 of its largest (of
+ * uniform keys: or 2^-25 of a unit of log2 a code step); the softmax weights times
+ * value scales to fp16 (relative 2^-11, and what they add held to 2^-30 of the
+ * row's largest weight times the head's largest visible value).
  *
  *  keys       a KVC_MODE_UNIFORM or KVC_MODE_CODEBOOK layer (with or without a
  *             residual sketch and outlier stream), D at most 256.
@@ -299,7 +308,8 @@ typedef struct {
 } kvc_tree_desc;
 
 /* Workspace bytes kvc_attend_tree needs for these layers at their current
- * length, Hq query heads and N drafts (host-only). */
+ * length, Hq query heads and N drafts (host-only).  Room for the bits of a mask
+ * per batch entry, B N ceil(N / 32) 4 bytes, is counted with or without one. */
 kvc_status kvc_attend_tree_workspace_bytes(const kvc_layer *keys, const kvc_layer *values,
                                            int32_t Hq, int32_t N, size_t *out);
 

@@ -536,7 +536,9 @@ def attend_tree(keys: "KVCacheLayer", values: "KVCacheLayer", q, mask=None, firs
     [N, N] or [B, N, N], mask[.., i, j] true where draft i sees draft j
     (default: a chain, j <= i).  first: int32 [B], the first visible token of
     every batch entry (left padding).  Returns out [B, Hq, N, D] in the value
-    layer's out_dtype, zero rows where a draft sees no token."""
+    layer's out_dtype, zero rows where a draft sees no token and NaN where its
+    scores are not finite.  include/kvc.h lists what is rounded below fp32; a key
+    layer on path "generic" computes in fp32."""
     import torch
 
     lib = keys._lib

@@ -118,6 +118,13 @@ __device__ void pack_mask(const TreeArgs& t, int block) {
 // The key weights at every packed position, w_j = scale log2(e) u_j coef_j
 // (coef = step in uniform mode, 1 for a codebook), and c1, for ROWS rows of a
 // slot per block; u = q V in fp32, by the block's 256 threads.
+//   64, 32    a register-tiled product, 8 or 4 rows x 4 columns a thread and 128
+//   rows      columns a warp, V through shared memory 32 rows at a time: bound by
+//             the fp32 FMA pipe (rows D r of them);
+//   8 rows    a thread takes one column and a share of the sum over D, V straight
+//             from global memory, each element read once: bound by latency.  For
+//             bases of up to 64 columns, which leave half of the tiles' columns
+//             empty, and for few rows, for which it gives more blocks.
 //
 // For the tensor cores a row's weights are split into two fp16 pieces and laid
 // out as their operand.  They are first divided by a power of two 2^ex that
@@ -128,13 +135,6 @@ __device__ void pack_mask(const TreeArgs& t, int block) {
 // last bit but in steps of 20, windows that w_shift puts around the usual sizes.
 // Uniform keys have no norm that would multiply what the pieces leave, and codes of
 // at most 128: their small weights stay as they are (ex >= 0).
-//   64, 32    a register-tiled product, 8 or 4 rows x 4 columns a thread and 128
-//   rows      columns a warp, V through shared memory 32 rows at a time: bound by
-//             the fp32 FMA pipe (rows D r of them);
-//   8 rows    a thread takes one column and a share of the sum over D, V straight
-//             from global memory, each element read once: bound by latency.  For
-//             bases of up to 64 columns, which leave half of the tiles' columns
-//             empty, and for few rows, for which it gives more blocks.
 constexpr int kPrepCols = 128, kPrepK = 32, kPrepBufs = 2;
 
 template <int ROWS>

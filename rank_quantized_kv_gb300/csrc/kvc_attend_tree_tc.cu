@@ -40,12 +40,13 @@
 //
 // Bound.  A tile's path S -> softmax -> P -> O is a chain of latencies (TMEM
 // loads, 128 x N exponentials, shared stores, barriers), so a CTA keeps four
-// tiles in flight; what is left is issue slots of the softmax and the decoders,
-// not DRAM and not the tensor core.  Measured (this kernel alone, us): 16
+// tiles in flight; what is left is that chain and instruction fetch (three unrolled
+// loops, 82 % of the requests hit), with half of the issue slots used, a quarter
+// of DRAM and an eighth of the tensor core.  Measured (this kernel alone, us): 16
 // sequences of 8 heads, 32 rows a head, 16384 tokens of 3-bit keys and int8 values
-// 155, about 2350 cycles a tile (0.36 of the rate at which HBM delivers the rows);
-// with 128 rows 283 (5400 cycles a tile of four times the scores); one sequence of
-// 130001 tokens, 20 rows a head 78.
+// 152, about 2300 cycles a tile (0.37 of the rate at which HBM delivers the rows);
+// with 128 rows 258 (4900 cycles a tile of four times the scores); one sequence of
+// 130001 tokens, 20 rows a head 77.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -163,8 +164,7 @@ struct Levels { uint32_t lo0, lo1, hi0, hi1; };
 // The fp16 centroids of the eight W-bit codes in the low bits of x (what lies
 // above them is ignored): the codes are spread to one per nibble (three steps
 // of halving, each a shift and a select), which is the selector that a byte
-// permute of the levels takes.  No table in shared memory: its bandwidth is
-// what the kernel has least of.
+// permute of the levels takes.
 template <int W>
 __device__ __forceinline__ uint4 centroids8(uint32_t x, const Levels& t) {
   auto select = [](uint32_t a, uint32_t b, uint32_t m) { return (a & m) | (b & ~m); };
@@ -294,7 +294,9 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* bar) {
 }
 
 // Entries of the pair table that holds every pair of centroids once per lane:
-// for codebooks of at most 8 levels at D = 128, else none.
+// for codebooks of at most 8 levels at D = 128, else none, and the centroids come
+// from byte permutes (16 sequences of 8 heads, 32 rows a head, 16384 tokens of 3-bit
+// keys, the whole call: with the table 174 us, without 198; D = 64 without 146).
 __host__ __device__ constexpr int pair_entries(int cb_bits, int D) {
   return cb_bits <= 3 && D == 128 ? 1 << (2 * cb_bits) : 0;
 }
@@ -1200,9 +1202,9 @@ bool shape_for(const Params& kp, bool vu, const TreeArgs& t, int nc, int halves,
 bool choose_shape(const Params& kp, const Params& vp, const TreeArgs& t, Shape* z) {
   // The fewest columns that hold all rows, else the most that fit: the softmax
   // works on all columns of a tile, empty ones too, and a tile is decoded once per
-  // job.  Measured (us of the whole call): 32 rows 177 with 32 columns, 268 with
-  // 64; 8 rows 16.2 with 16, 17.1 with 32, 19.5 with 64; 128 rows 330 in one job
-  // of 128, 493 in two of 64.
+  // job.  Measured (us of the whole call): 32 rows 175 with 32 columns, 266 with
+  // 64; 8 rows 15.6 with 16, 16.6 with 32, 19.5 with 64; 128 rows 304 in one job
+  // of 128, 500 in two of 64.
   static const int kShapes[4][2] = {{16, 1}, {32, 1}, {64, 1}, {64, 2}};
   bool ok = false;
   for (const auto& s : kShapes) {
@@ -1232,7 +1234,7 @@ int tree_tc_rows(const Params& kp, const Params& vp, const TreeArgs& t, int* par
   // layers for which there is no shape or no ready kernel.  All else goes to the
   // tensor cores at every size (us of the call, CUDA cores and here: 2 slots of 8
   // rows, 84 tokens 29 and 16; 15 slots of 21 rows, 1777 tokens 38 and 27; 64 slots of
-  // 64 rows, 4096 tokens 274 and 59; 128 slots of 32 rows, 16384 tokens 5567 and 177).
+  // 64 rows, 4096 tokens 274 and 57; 128 slots of 32 rows, 16384 tokens 5567 and 175).
   if (t.prod) return 0;
   if (vp.mode == KVC_MODE_INT8 && vp.D % 8) return 0;  // value rows are read 8 bytes at a time
   Shape z;

@@ -10,11 +10,11 @@
 // is put together from pieces of V bytes, V the largest power of two (at most
 // 16) that keeps every piece inside one row and aligned on both sides.
 //
-// Measured: 128 slots of 16384 int8 rows (545 MB read and written) in 82 us, 0.97 of
-// the copy rate; 5461 chosen ones of 16384 rows of 48 bytes for 128 slots in 28 us,
-// 2.5 TB/s of the rows' own bytes (a row at random draws one or two 64-byte pieces
-// of DRAM, its norm another); accept of 17 of 64 rows for 128 slots within the
-// time of a launch.
+// Measured: 128 slots of 16384 int8 rows, 16 entries from about ten distinct parents
+// (448 MB that have to move), in 82 us, 0.8 of the copy rate; 5461 chosen ones of
+// 16384 rows of 48 bytes for 128 slots in 28 us, 2.5 TB/s of the rows' own bytes (a
+// row at random draws one or two 64-byte pieces of DRAM, its norm another); accept
+// of 17 of 64 rows for 128 slots 5 us, a launch.
 #include <algorithm>
 
 #include "kvc_internal.h"
