@@ -826,13 +826,16 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
         const float most = fmaxf(fmaxf(red[wg][0][0], red[wg][1][0]), fmaxf(red[wg][2][0], red[wg][3][0]));
         if (most != 0.f) common = most;
       }
+      // wscale is that of a row in jobs of several factors, 1 elsewhere: of uniform
+      // keys, whose common factor is 1, known before the vote and ordered by it
+      if (KMODE == KVC_MODE_UNIFORM && ltid < NC) wscale[wg][ltid] = ws == 0.f ? 1.f : ws;
       const bool scaled = named_bar_or(bar, 128, ws != 0.f && ws != common);
-      if (ltid < NC) wscale[wg][ltid] = !scaled ? 1.f : ws == 0.f ? common : ws;
-      if (ltid == 0) {
-        pl.scaled = scaled;
-        if (KMODE == KVC_MODE_CODEBOOK) pl.fold = scaled ? 1.f : common;
+      if (ltid == 0) pl.scaled = scaled;
+      if (KMODE == KVC_MODE_CODEBOOK) {
+        if (ltid < NC) wscale[wg][ltid] = !scaled ? 1.f : ws == 0.f ? common : ws;
+        if (ltid == 0) pl.fold = scaled ? 1.f : common;
+        named_bar_sync(bar, 128);
       }
-      if (KMODE == KVC_MODE_CODEBOOK) named_bar_sync(bar, 128);
       float2 l[NC / 2];
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) l[i] = make_float2(0.f, 0.f);

@@ -191,3 +191,18 @@ def test_very_small_and_large_codebooks(kvc, size):
     q = torch.randn(B, H * rep, N, D, generator=g) * (0.5 / size)
     o = kvc.attend_tree(gk, gv, q.to(DEV))
     check(o, tree_cases.reference(gk, rk, gv, rv, q.double().numpy(), 1 / math.sqrt(D), N))
+
+
+@pytest.mark.parametrize("kmode,vmode", [("uniform", "uniform"), ("uniform", "int8"), ("codebook", "uniform"),
+                                         ("codebook", "int8")])
+@pytest.mark.parametrize("H,rep,N", [(4, 128, 50), (4, 35, 64)])
+def test_jobs_of_different_sizes_in_turn(kvc, kmode, vmode, H, rep, N):
+    """Many short jobs, several to a CTA, with query heads of ordinary, very large and
+    very small size, alone and together in a job: none takes another's factors."""
+    B, D, S = 1, 64, 130
+    gk, gv, rk, rv = make_layers(kvc, kmode, vmode, B, H, D, S, 90, dev=DEV)
+    g = torch.Generator().manual_seed(6)
+    size = 2.0 ** torch.tensor([0, 0, 18, -24])[torch.randint(0, 4, (H * rep // 4 + 1,), generator=g)]
+    q = torch.randn(B, H * rep, N, D, generator=g) * size.repeat_interleave(4)[:H * rep, None, None]
+    o = kvc.attend_tree(gk, gv, q.to(DEV))
+    check(o, tree_cases.reference(gk, rk, gv, rv, q.double().numpy(), 1 / math.sqrt(D), N))
