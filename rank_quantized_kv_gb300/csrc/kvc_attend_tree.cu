@@ -133,6 +133,8 @@ __device__ void pack_mask(const TreeArgs& t, int block) {
 // any.  The softmax multiplies the products by 2^ex: at no cost where the rows of
 // a job have one ex (it goes into the token's norm), so ex is not taken to the
 // last bit but in steps of 20, windows that w_shift puts around the usual sizes.
+// (Jobs of several take a multiplication more a score: 16 sequences of 8 heads,
+// 16384 tokens, 128 rows a head 350 us in place of 316, 32 rows 175 of 173.)
 // Uniform keys have no norm that would multiply what the pieces leave, and codes of
 // at most 128: their small weights stay as they are (ex >= 0).
 constexpr int kPrepCols = 128, kPrepK = 32, kPrepBufs = 2;

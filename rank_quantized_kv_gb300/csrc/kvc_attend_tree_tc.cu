@@ -41,11 +41,11 @@
 // Bound.  A tile's path S -> softmax -> P -> O is a chain of latencies (TMEM
 // loads, 128 x N exponentials, shared stores, barriers), so a CTA keeps four
 // tiles in flight; what is left is that chain and instruction fetch (three unrolled
-// loops, 82 % of the requests hit), with half of the issue slots used, a quarter
+// loops, 85 % of the requests hit), with half of the issue slots used, a quarter
 // of DRAM and an eighth of the tensor core.  Measured (this kernel alone, us): 16
 // sequences of 8 heads, 32 rows a head, 16384 tokens of 3-bit keys and int8 values
-// 152, about 2300 cycles a tile (0.37 of the rate at which HBM delivers the rows);
-// with 128 rows 258 (4900 cycles a tile of four times the scores); one sequence of
+// 148, about 2250 cycles a tile (0.38 of the rate at which HBM delivers the rows);
+// with 128 rows 266 (5100 cycles a tile of four times the scores); one sequence of
 // 130001 tokens, 20 rows a head 77.
 #include <cuda_fp16.h>
 
@@ -405,7 +405,6 @@ struct Place {
   int plain0, plain1;  // tiles that hold visible context alone
   int first;
   const uint32_t* mask;  // per draft, which drafts see it
-  int scaled;          // the rows' products have different factors
   float fold;          // codebook keys: their common factor, else 1
   int Pk, Pv;          // decoders: row bytes
   __device__ void next(const TreeArgs& t, int H) { more = w.next(t, H, g); }
@@ -449,7 +448,8 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
   // factor, seen a token; the warps' partial results
   __shared__ __align__(16) float cneg[2][NC];
   __shared__ __align__(16) float corr[2][NC], red[2][4][NC];
-  __shared__ float mref[2][NC], wscale[2][NC];
+  __shared__ __align__(16) float wscale[2][NC];
+  __shared__ float mref[2][NC];
   __shared__ int seen[2][NC];  // 0: no token, 1: weights summed, 2: only scores of -inf
   __shared__ __align__(16) unsigned char place_s[(2 + DG) * sizeof(Place)];  // softmax groups, decoder groups
   Place* place = reinterpret_cast<Place*>(place_s);
@@ -830,7 +830,6 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
       // keys, whose common factor is 1, known before the vote and ordered by it
       if (KMODE == KVC_MODE_UNIFORM && ltid < NC) wscale[wg][ltid] = ws == 0.f ? 1.f : ws;
       const bool scaled = named_bar_or(bar, 128, ws != 0.f && ws != common);
-      if (ltid == 0) pl.scaled = scaled;
       if (KMODE == KVC_MODE_CODEBOOK) {
         if (ltid < NC) wscale[wg][ltid] = !scaled ? 1.f : ws == 0.f ? common : ws;
         if (ltid == 0) pl.fold = scaled ? 1.f : common;
@@ -867,10 +866,24 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
         wait_or_abort(&s_full[s], s_par, &abort_flag);
         __syncwarp();
         tc_fence_after();
-        auto scores = [&](int ch, float2 (&x)[CH / 2]) {  // S nt + c1 - m
+        auto scores = [&](int ch, float2 (&x)[CH / 2]) {  // S nt + c1 - m, S times the rows' factors
           uint32_t r[CH];
           tmem_ld_n<CH>(s_tm + ch * CH, r);
           tmem_wait_ld();
+          if (scaled) {  // a factor per row
+#pragma unroll
+            for (int i = 0; i < CH / 4; ++i) {
+              const float4 f = reinterpret_cast<const float4*>(wscale[wg] + ch * CH)[i];
+              const float2 a = __fmul2_rn(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])),
+                                          make_float2(f.x, f.y));
+              const float2 b = __fmul2_rn(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])),
+                                          make_float2(f.z, f.w));
+              r[4 * i] = __float_as_uint(a.x);
+              r[4 * i + 1] = __float_as_uint(a.y);
+              r[4 * i + 2] = __float_as_uint(b.x);
+              r[4 * i + 3] = __float_as_uint(b.y);
+            }
+          }
           const float2 nt2 = make_float2(nt, nt);
 #pragma unroll
           for (int i = 0; i < CH / 4; ++i) {
@@ -979,7 +992,7 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
               blind = seen[wg][ltid] != 1;
             }
             // rows that saw nothing yet keep every tile on this path
-            if (!named_bar_or(bar, 128, blind) && !pl.scaled) fast1 = pl.plain1;
+            if (!named_bar_or(bar, 128, blind)) fast1 = pl.plain1;
 #pragma unroll
             for (int i = 0; i < NC / 4; ++i) {
               const float4 f = reinterpret_cast<const float4*>(corr[wg])[i];
@@ -1026,28 +1039,12 @@ __global__ void __launch_bounds__(Roles<NC, HALVES>::threads, 1)
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
           if (ch) scores(ch, x);
-          if (ch == NCH - 1 && !pl.scaled) {  // S has been read
+          if (ch == NCH - 1) {  // S has been read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[s]);
           }
           if (general) {
-            if (pl.scaled) {  // a factor per row
-              uint32_t r[CH];
-              tmem_ld_n<CH>(s_tm + ch * CH, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < CH / 2; ++i) {
-                const int c = ch * CH + 2 * i;
-                x[i].x = fmaf(__uint_as_float(r[2 * i]) * wscale[wg][c], nt, cn[c]);
-                x[i].y = fmaf(__uint_as_float(r[2 * i + 1]) * wscale[wg][c + 1], nt, cn[c + 1]);
-              }
-              if (ch == NCH - 1) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[s]);
-              }
-            }
             const uint32_t v = (uint32_t)(vis >> (ch * CH));
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) {
