@@ -352,6 +352,111 @@ kvc_status kvc_gather(kvc_layer *dst, const kvc_layer *src, const int32_t *paren
  * n up to 98304. */
 kvc_status kvc_accept(kvc_layer *layer, int64_t N, const int32_t *index, int64_t n, void *stream);
 
+/* Attention of the last N stored tokens over a sliding window and the first
+ * tokens of the cache, which stay visible (sinks), computed from the codes as
+ * kvc_attend computes; and, where asked for, the softmax weights that the stored
+ * tokens receive, the measure by which kvc_evict chooses.  The N queries belong
+ * to the last N stored tokens (appended before the call): a decode step has one, a
+ * chunk of a prompt many.  Query i stands at position pos = length - N + i and sees
+ * the tokens t with
+ *   first[b] <= t <= pos  and  (window == 0 or t > pos - window or
+ *                               t < first[b] + sinks);
+ *   out[b, hq, i] = sum_t softmax_t(scale * q[b, hq, i] . k_hat[b, h, t]) v_hat[b, h, t]
+ *   weights[b, h, t] = decay * weights[b, h, t] + sum over hq of h and i of softmax_t
+ * with h = hq / (Hq / H).  A query that sees no token (padding) gets a row of zeros
+ * and gives no weight; one that sees a score of NaN or +inf, or scores of -inf alone
+ * (below fp32's range), gets a row of NaN and gives NaN to what it sees.  What a
+ * hidden token stores, infinities and NaN among it, has no effect.  Positions are
+ * places in the cache: after an eviction the kept tokens are neighbours.
+ *
+ *  keys       a KVC_MODE_UNIFORM or KVC_MODE_CODEBOOK layer (with or without a
+ *             residual sketch and outlier stream), D at most 256.
+ *  values     a KVC_MODE_INT8 or KVC_MODE_UNIFORM layer with the keys' B, H, D,
+ *             device and length.
+ *  q          device, q_dtype: query i of head hq of batch b starts at
+ *             q + b*q_stride_b + hq*q_stride_h + i*q_stride_t (elements); the D
+ *             values of a row are contiguous.
+ *  Hq         query heads, any multiple of H.
+ *  N          queries, 1 .. length, at most 65536.
+ *  window     tokens of the window, the query's own among them; 0: no limit.
+ *  sinks      first tokens that stay visible, counted from first[b].
+ *  first      device int32 [B], the first token of each entry (left padding before
+ *             it); NULL: 0.  Below 0 reads as 0.
+ *  scale      the score scale; 0 means 1 / sqrt(D).
+ *  out        device, the value layer's out_dtype, element strides as for q.
+ *  weights    device fp32 or NULL: token t of head h of batch b at
+ *             weights + b*weights_stride_b + h*weights_stride_h + t, 0 <= t < length.
+ *  decay      finite, >= 0.  1 adds to what is there, 0 does not read it (every
+ *             token's weight is then written, 0 for hidden ones).
+ * The workspace is caller-owned scratch, overwritten by the call: calls that
+ * may overlap need one each. */
+typedef struct {
+  const void *q;
+  int32_t q_dtype;
+  int32_t Hq, N;
+  int64_t q_stride_b, q_stride_h, q_stride_t;
+  int64_t window, sinks;
+  const int32_t *first;
+  float scale;
+  void *out;
+  int64_t out_stride_b, out_stride_h, out_stride_t;
+  float *weights;
+  int64_t weights_stride_b, weights_stride_h;
+  float decay;
+} kvc_window_desc;
+
+/* Workspace bytes kvc_attend_window needs for this descriptor at the layers'
+ * current length (host-only; Hq, N, window, sinks and whether weights is NULL
+ * are looked at). */
+kvc_status kvc_attend_window_workspace_bytes(const kvc_layer *keys, const kvc_layer *values,
+                                             const kvc_window_desc *desc, size_t *out);
+
+/* Run it, asynchronously on `stream`.  workspace: device, 256-byte aligned.
+ * KVC_EINVAL for unsupported modes or shapes, mismatched layers, overlapping rows
+ * of out or weights, host pointers or a short workspace; nothing is launched then. */
+kvc_status kvc_attend_window(const kvc_layer *keys, const kvc_layer *values,
+                             const kvc_window_desc *desc, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* Evict: of the `length` tokens of a key and a value layer keep `keep` in every
+ * (b, h), each head its own, in their order; the others are dropped.  Ranked from
+ * the top, the lower token first among equals:
+ *   the sinks first[b] .. first[b] + sinks - 1 and the last `recent` tokens;
+ *   the others from first[b] on, by weight, larger first (-0 equals 0, NaN below
+ *   -inf; all equal where weights is NULL);
+ *   the padding before first[b].
+ * In place (dst_keys and dst_values NULL) the layers' length becomes keep,
+ * weights[b, h, j] that of the j-th kept token for j < keep, and 0 from there to
+ * the old length, where later tokens will stand.  Else the kept rows are appended
+ * to dst_keys and dst_values (layers with the same frozen parameters, slot by slot,
+ * of equal length; their capacity may differ), the kept weights are written to
+ * dst_weights from the destination's old length on, and the source stays as it was.
+ * Rows move as they are stored.
+ *
+ *  keys, values  heads_per_group 1, equal B, H, device and length; any mode.
+ *  keep          1 .. length (none: kvc_trim); sinks + recent at most keep.
+ *  weights       device fp32, as kvc_attend_window leaves them, or NULL.
+ *  first         device int32 [B] or NULL: 0.
+ *  first_out     device int32 [B] or NULL: receives max(0, keep - (length - first[b])),
+ *                the first token of each entry after the eviction; not `first`.
+ *  index         device int32 [B*H][keep]: receives the kept tokens, ascending.
+ *  dst_weights   device fp32 or NULL; must not overlap weights.  Not in place.
+ * Asynchronous on `stream`.  KVC_ECAPACITY if the rows do not fit, KVC_EINVAL for
+ * mismatched layers, counts out of range or host pointers; nothing is written then. */
+typedef struct {
+  int64_t keep, sinks, recent;
+  float *weights;
+  int64_t weights_stride_b, weights_stride_h;
+  const int32_t *first;
+  int32_t *first_out;
+  int32_t *index;
+  kvc_layer *dst_keys, *dst_values;
+  float *dst_weights;
+  int64_t dst_weights_stride_b, dst_weights_stride_h;
+} kvc_evict_desc;
+
+kvc_status kvc_evict(kvc_layer *keys, kvc_layer *values, const kvc_evict_desc *desc, void *stream);
+
 /* Order-0 Huffman accounting of the stored codes (kvtc_cache page, module
  * docstring "Byte accounting" and KVTCKVCache.entropy_coding_gain).  Not on
  * the hot path: the store stays fixed width; these calls report what an

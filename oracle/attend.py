@@ -19,7 +19,8 @@ import math
 
 import numpy as np
 
-__all__ = ["softmax", "attend_rows", "attend", "tree_visible", "attend_tree_rows"]
+__all__ = ["softmax", "attend_rows", "attend", "tree_visible", "attend_tree_rows", "window_visible",
+           "evicted"]
 
 
 def softmax(s):
@@ -86,3 +87,32 @@ def attend_tree_rows(q, K, V, scale, visible):
         t = np.flatnonzero(p[i])
         out[i] = p[i, t] @ V[t]
     return out, p
+
+
+def window_visible(N, S, window=0, sinks=0, first=0):
+    """Which of S stored tokens each of the last N ones sees through a sliding
+    window (0: no limit) and ``sinks`` first tokens, bool [N, S]."""
+    first = max(int(first), 0)
+    pos, t = np.arange(S - N, S)[:, None], np.arange(S)[None]
+    see = (t >= first) & (t <= pos)
+    if window:
+        see &= (pos - t < window) | (t - first < sinks)
+    return see
+
+
+def evicted(weights, keep, sinks=0, recent=0, first=0):
+    """The tokens that an eviction keeps of one (b, h), ascending: weights [S] (or
+    a number of tokens, all weights equal).  Sorted by (class, weight, earlier
+    first), class 0 being the sinks and the most recent, 1 the others, 2 padding."""
+    w = np.zeros(weights) if isinstance(weights, int) else np.asarray(weights, dtype=np.float64)
+    S, first = len(w), min(max(int(first), 0), len(w))
+
+    def rank(t):
+        if t < first:
+            return (2, 0.0, t)
+        if t < first + sinks or t >= S - recent:
+            return (0, 0.0, t)
+        return (1, (1, 0.0) if np.isnan(w[t]) else (0, -w[t]), t)
+
+    order = sorted(range(S), key=rank)
+    return np.array(sorted(order[:keep]), dtype=np.int64)

@@ -21,7 +21,8 @@ import numpy as np
 
 __all__ = ["KVCacheLayer", "load_library", "library_path", "KvcError", "MODES", "DTYPES",
            "EXPORTED_SYMBOLS", "store_bytes", "attend", "attend_workspace_bytes", "fit_uniform",
-           "fit_outliers", "attend_tree", "attend_tree_workspace_bytes"]
+           "fit_outliers", "attend_tree", "attend_tree_workspace_bytes", "attend_window",
+           "attend_window_workspace_bytes", "evict"]
 
 MODES = {"uniform": 0, "group": 1, "codebook": 2, "int8": 3}
 DTYPES = {"f32": 0, "f16": 1, "bf16": 2}
@@ -38,7 +39,8 @@ EXPORTED_SYMBOLS = (
     "kvc_code_histogram_bytes", "kvc_code_histogram", "kvc_entropy_bytes",
     "kvc_fit_uniform_workspace_bytes", "kvc_fit_uniform", "kvc_store_bytes_prod",
     "kvc_init_layer_prod", "kvc_fit_outliers", "kvc_attend_tree_workspace_bytes",
-    "kvc_attend_tree", "kvc_gather", "kvc_accept",
+    "kvc_attend_tree", "kvc_gather", "kvc_accept", "kvc_attend_window_workspace_bytes",
+    "kvc_attend_window", "kvc_evict",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -93,6 +95,27 @@ class _TreeDesc(ctypes.Structure):
         ("mask", c_void_p), ("mask_stride_b", c_int64), ("first", c_void_p), ("scale", c_float),
         ("out", c_void_p), ("out_stride_b", c_int64), ("out_stride_h", c_int64),
         ("out_stride_t", c_int64),
+    ]
+
+
+class _WindowDesc(ctypes.Structure):
+    _fields_ = [
+        ("q", c_void_p), ("q_dtype", c_int32), ("Hq", c_int32), ("N", c_int32),
+        ("q_stride_b", c_int64), ("q_stride_h", c_int64), ("q_stride_t", c_int64),
+        ("window", c_int64), ("sinks", c_int64), ("first", c_void_p), ("scale", c_float),
+        ("out", c_void_p), ("out_stride_b", c_int64), ("out_stride_h", c_int64),
+        ("out_stride_t", c_int64), ("weights", c_void_p), ("weights_stride_b", c_int64),
+        ("weights_stride_h", c_int64), ("decay", c_float),
+    ]
+
+
+class _EvictDesc(ctypes.Structure):
+    _fields_ = [
+        ("keep", c_int64), ("sinks", c_int64), ("recent", c_int64), ("weights", c_void_p),
+        ("weights_stride_b", c_int64), ("weights_stride_h", c_int64), ("first", c_void_p),
+        ("first_out", c_void_p), ("index", c_void_p), ("dst_keys", c_void_p),
+        ("dst_values", c_void_p), ("dst_weights", c_void_p), ("dst_weights_stride_b", c_int64),
+        ("dst_weights_stride_h", c_int64),
     ]
 
 
@@ -155,6 +178,10 @@ def load_library():
             "kvc_attend_tree_workspace_bytes": (c_int32, [P, P, c_int32, c_int32,
                                                           POINTER(c_size_t)]),
             "kvc_attend_tree": (c_int32, [P, P, POINTER(_TreeDesc), P, c_size_t, P]),
+            "kvc_attend_window_workspace_bytes": (c_int32, [P, P, POINTER(_WindowDesc),
+                                                            POINTER(c_size_t)]),
+            "kvc_attend_window": (c_int32, [P, P, POINTER(_WindowDesc), P, c_size_t, P]),
+            "kvc_evict": (c_int32, [P, P, POINTER(_EvictDesc), P]),
             "kvc_gather": (c_int32, [P, P, P, P, c_int64, c_int64, P]),
             "kvc_accept": (c_int32, [P, c_int64, P, c_int64, P]),
             "kvc_sync_status": (c_int32, [P, P]),
@@ -586,6 +613,142 @@ def attend_tree(keys: "KVCacheLayer", values: "KVCacheLayer", q, mask=None, firs
                                workspace.numel() * workspace.element_size(),
                                _stream_ptr(stream, keys.device)))
     return out
+
+
+def _window_desc(keys, values, q, window, sinks, first, scale, weights, decay):
+    """Check the arguments of attend_window and put them into a descriptor (without out)."""
+    import torch
+
+    dt = _torch_dtypes()
+    q_dtype = 0 if q.dtype == dt["f32"] else 1 if q.dtype == dt["f16"] else 2 if q.dtype == dt["bf16"] else -1
+    if q.dim() != 4 or q_dtype < 0 or q.stride(3) != 1:
+        raise ValueError("q must be [B, Hq, N, D] fp32/fp16/bf16 with a contiguous last dimension")
+    B, Hq, N, D = q.shape
+    if B != keys.B or D != keys.D:
+        raise ValueError(f"q must be [{keys.B}, Hq, N, {keys.D}], got {tuple(q.shape)}")
+    if first is not None and (first.dtype != torch.int32 or tuple(first.shape) != (B,)
+                              or not first.is_contiguous()):
+        raise ValueError(f"first must be a contiguous int32 tensor [{B}]")
+    wb = wh = 0
+    if weights is not None:
+        wb, wh = _check_weights("weights", weights, keys, len(keys))
+    qb, qh, qt, _ = q.stride()
+    return _WindowDesc(q=q.data_ptr(), q_dtype=q_dtype, Hq=Hq, N=N, q_stride_b=qb, q_stride_h=qh,
+                       q_stride_t=qt, window=int(window or 0), sinks=int(sinks),
+                       first=None if first is None else first.data_ptr(), scale=scale,
+                       weights=None if weights is None else weights.data_ptr(),
+                       weights_stride_b=wb, weights_stride_h=wh, decay=decay)
+
+
+def _check_weights(name, weights, layer, n):
+    """Strides (batch, head) of accumulated weights [B, H, >= n]."""
+    import torch
+
+    if (weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[0] != layer.B
+            or weights.shape[1] != layer.H or weights.shape[2] < n
+            or (weights.shape[2] > 1 and weights.stride(2) != 1)):
+        raise ValueError(f"{name} must be an fp32 tensor [{layer.B}, {layer.H}, >= {n}] with a "
+                         "contiguous last dimension")
+    return weights.stride(0), weights.stride(1)
+
+
+def attend_window_workspace_bytes(keys: "KVCacheLayer", values: "KVCacheLayer", q, window=0,
+                                  sinks: int = 0, weights=None) -> int:
+    """Device workspace bytes that attend_window needs with these arguments at the
+    layers' current length."""
+    d = _window_desc(keys, values, q, window, sinks, None, 0.0, weights, 1.0)
+    n = c_size_t()
+    _check(load_library().kvc_attend_window_workspace_bytes(keys._h, values._h, byref(d), byref(n)))
+    return int(n.value)
+
+
+def attend_window(keys: "KVCacheLayer", values: "KVCacheLayer", q, window=0, sinks: int = 0,
+                  first=None, scale: float = 0.0, weights=None, decay: float = 1.0, out=None,
+                  workspace=None, stream=None):
+    """Attention of the last N stored tokens over a sliding window (kvc_attend_window):
+    q [B, Hq, N, D] (fp32, fp16 or bf16; last dimension contiguous) belongs to the
+    last N tokens of ``keys`` and ``values``; each query sees the ``window`` tokens
+    that end with its own (0 or None: all) and the first ``sinks`` ones.  first: int32
+    [B], the first token of every batch entry (left padding).  weights: fp32 [B, H,
+    >= length] (last dimension contiguous); becomes decay * weights + the softmax
+    weights that every token receives from the query heads of its key/value head
+    (decay 0: set, without being read).  Returns out [B, Hq, N, D] in the value
+    layer's out_dtype, zero rows where a query sees no token and NaN where its
+    scores are not finite."""
+    import torch
+
+    lib = keys._lib
+    d = _window_desc(keys, values, q, window, sinks, first, scale, weights, decay)
+    out_dt = _torch_dtypes()[values.out_dtype]
+    if out is None or workspace is None:
+        # what the call allocates belongs to the stream that uses it
+        ctx = None if stream is None else torch.cuda.stream(stream)
+        if ctx is not None:
+            ctx.__enter__()
+        try:
+            if out is None:
+                out = torch.empty(q.shape, dtype=out_dt, device=keys.device)
+            if workspace is None:
+                n = c_size_t()
+                _check(lib.kvc_attend_window_workspace_bytes(keys._h, values._h, byref(d), byref(n)))
+                workspace = torch.empty(n.value, dtype=torch.uint8, device=keys.device)
+        finally:
+            if ctx is not None:
+                ctx.__exit__(None, None, None)
+    if out.shape != q.shape or out.dtype != out_dt or out.stride(3) != 1:
+        raise ValueError("out must be [B, Hq, N, D] of the value layer's out_dtype, last dimension contiguous")
+    d.out = out.data_ptr()
+    d.out_stride_b, d.out_stride_h, d.out_stride_t, _ = out.stride()
+    _check(lib.kvc_attend_window(keys._h, values._h, byref(d), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(),
+                                 _stream_ptr(stream, keys.device)))
+    return out
+
+
+def evict(keys: "KVCacheLayer", values: "KVCacheLayer", weights, keep: int, sinks: int = 0,
+          recent: int = 0, first=None, into=None, stream=None):
+    """Keep ``keep`` of the stored tokens in every (b, h), each head its own, in their
+    order, and drop the others (kvc_evict): the first ``sinks`` and the last
+    ``recent`` ones, then those of the largest weight (fp32 [B, H, >= length], as
+    attend_window leaves them; None: the earlier ones), the lower token first among
+    equals; padding (before first, int32 [B]) goes first.  In place both layers
+    shrink to ``keep`` tokens and weights holds those of the kept ones, then zeros
+    up to the old length.  into=(keys, values, weights): the kept rows are appended
+    to other layers with the same frozen parameters instead, and their weights
+    written from those layers' old length on (weights may be None there).  Returns
+    (index, first): int32 [B, H, keep], the kept tokens, and the first token of
+    every entry afterwards (None if first is)."""
+    import torch
+
+    keep = int(keep)
+    if first is not None and (first.dtype != torch.int32 or tuple(first.shape) != (keys.B,)
+                              or not first.is_contiguous()):
+        raise ValueError(f"first must be a contiguous int32 tensor [{keys.B}]")
+    d = _EvictDesc(keep=keep, sinks=int(sinks), recent=int(recent),
+                   first=None if first is None else first.data_ptr())
+    if weights is not None:
+        d.weights_stride_b, d.weights_stride_h = _check_weights("weights", weights, keys, len(keys))
+        d.weights = weights.data_ptr()
+    if into is not None:
+        dk, dv, dw = into
+        d.dst_keys, d.dst_values = dk._h, dv._h
+        if dw is not None:
+            d.dst_weights_stride_b, d.dst_weights_stride_h = _check_weights(
+                "the destination's weights", dw, keys, len(dk) + keep)
+            d.dst_weights = dw.data_ptr()
+    ctx = None if stream is None else torch.cuda.stream(stream)
+    if ctx is not None:  # what the call allocates belongs to the stream that uses it
+        ctx.__enter__()
+    try:
+        index = torch.empty(keys.B, keys.H, max(keep, 0), dtype=torch.int32, device=keys.device)
+        first_out = None if first is None else torch.empty_like(first)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    d.index = index.data_ptr() if keep > 0 else None
+    d.first_out = None if first_out is None else first_out.data_ptr()
+    _check(keys._lib.kvc_evict(keys._h, values._h, byref(d), _stream_ptr(stream, keys.device)))
+    return index, first_out
 
 
 def fit_uniform(x, S_fit: int, r: int, choices, budget: int, stream=None):

@@ -1,6 +1,7 @@
 // Host side of libkvc: descriptor validation, store layout, the frozen
 // parameter block in kernel layouts, and the kvc_* C entry points.
 #include <algorithm>
+#include <array>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -893,6 +894,22 @@ kvc_status kvc_attend(const kvc_layer* K, const kvc_layer* V, const float* q, in
   return succeed();
 }
 
+// Rows of `width` elements, a count of them along each of three strides, must not
+// overlap: each dimension steps over all that the ones with smaller strides cover.
+static kvc_status rows_apart(const char* name, int64_t width, std::array<std::pair<int64_t, int64_t>, 3> dim) {
+  for (const auto& m : dim)
+    if (m.first < 0) return fail(KVC_EINVAL, "strides must be >= 0");
+  std::sort(dim.begin(), dim.end());
+  int64_t covered = width;
+  for (const auto& m : dim) {
+    if (m.second == 1) continue;
+    if (m.first < covered) return fail(KVC_EINVAL, "rows of %s overlap", name);
+    if (m.first > INT64_MAX / 4 / m.second) return fail(KVC_EINVAL, "%s's strides are too large", name);
+    covered += m.first * (m.second - 1);
+  }
+  return KVC_OK;
+}
+
 // Checks shared by the tree attention's entry points; fills the shape fields of t.
 static kvc_status tree_check(const kvc_layer* K, const kvc_layer* V, int32_t Hq, int32_t N,
                              kvc::TreeArgs& t, size_t* ws_bytes) {
@@ -974,19 +991,8 @@ kvc_status kvc_attend_tree(const kvc_layer* K, const kvc_layer* V, const kvc_tre
   if (d->q_stride_b < 0 || d->q_stride_h < 0 || d->q_stride_t < 0 || d->mask_stride_b < 0)
     return fail(KVC_EINVAL, "strides must be >= 0");
   const int64_t D = K->D;
-  // rows of out: each dimension steps over all that the ones with smaller strides cover
-  if (d->out_stride_b < 0 || d->out_stride_h < 0 || d->out_stride_t < 0)
-    return fail(KVC_EINVAL, "strides must be >= 0");
-  std::pair<int64_t, int64_t> dim[3] = {
-      {d->out_stride_b, K->B}, {d->out_stride_h, d->Hq}, {d->out_stride_t, d->N}};
-  std::sort(dim, dim + 3);
-  int64_t covered = D;
-  for (const auto& m : dim) {
-    if (m.second == 1) continue;
-    if (m.first < covered) return fail(KVC_EINVAL, "rows of out overlap");
-    if (m.first > INT64_MAX / 4 / m.second) return fail(KVC_EINVAL, "out's strides are too large");
-    covered += m.first * (m.second - 1);
-  }
+  const kvc_status rows = rows_apart("out", D, {{{d->out_stride_b, K->B}, {d->out_stride_h, d->Hq}, {d->out_stride_t, d->N}}});
+  if (rows) return rows;
   if ((uintptr_t)d->q % (d->q_dtype == KVC_F32 ? 4 : 2) || (uintptr_t)d->out % 2 ||
       (uintptr_t)d->first % 4)
     return fail(KVC_EINVAL, "an array is not aligned to its element size");
@@ -1026,22 +1032,15 @@ kvc_status kvc_attend_tree(const kvc_layer* K, const kvc_layer* V, const kvc_tre
   return succeed();
 }
 
-kvc_status kvc_gather(kvc_layer* dst, const kvc_layer* src, const int32_t* parent,
-                      const int32_t* index, int64_t start, int64_t n, void* stream) {
-  if (!dst || !src) return fail(KVC_ESTATE, "layer is NULL");
-  if (dst == src) return fail(KVC_EINVAL, "source and destination are the same layer");
-  if (n < 0 || start < 0) return fail(KVC_EINVAL, "n and start must be >= 0");
-  if (dst->device != src->device) return fail(KVC_EINVAL, "the layers are on different devices");
-  if (dst->H != src->H || dst->format[0] != src->format[0] || dst->format[1] != src->format[1])
-    return fail(KVC_EINVAL, "the layers differ in heads or frozen parameters");
-  if (!parent && dst->B != src->B) return fail(KVC_EINVAL, "layers of different batches need parent");
-  // a row decodes by its slot's basis and outlier channels: they must agree for
-  // every pair of slots between which rows may move (one batch entry of each
-  // layer stands for all where they do not depend on the batch)
+// A row decodes by its slot's basis and outlier channels: they must agree for
+// every pair of slots between which rows may move, those of any two batch entries
+// or of the same ones (one batch entry of each layer stands for all where they do
+// not depend on the batch).
+static kvc_status slots_alike(const kvc_layer* dst, const kvc_layer* src, bool any_entry) {
   const int Hg = dst->n_slots / dst->B, no = dst->p.n_out;
   const bool alike = dst->batch_free && src->batch_free;
   for (int b = 0; b < (alike ? 1 : dst->B); ++b)
-    for (int s = parent ? 0 : b; s < (alike ? 1 : parent ? src->B : b + 1); ++s)
+    for (int s = any_entry ? 0 : b; s < (alike ? 1 : any_entry ? src->B : b + 1); ++s)
       for (int h = 0; h < Hg; ++h) {
         const int ds = b * Hg + h, ss = s * Hg + h;
         if (dst->basis_host[ds] != src->basis_host[ss])
@@ -1051,6 +1050,20 @@ kvc_status kvc_gather(kvc_layer* dst, const kvc_layer* src, const int32_t* paren
                         src->channels_host.begin() + (size_t)ss * no))
           return fail(KVC_EINVAL, "slot %d has other outlier channels than the source's slot %d", ds, ss);
       }
+  return KVC_OK;
+}
+
+kvc_status kvc_gather(kvc_layer* dst, const kvc_layer* src, const int32_t* parent,
+                      const int32_t* index, int64_t start, int64_t n, void* stream) {
+  if (!dst || !src) return fail(KVC_ESTATE, "layer is NULL");
+  if (dst == src) return fail(KVC_EINVAL, "source and destination are the same layer");
+  if (n < 0 || start < 0) return fail(KVC_EINVAL, "n and start must be >= 0");
+  if (dst->device != src->device) return fail(KVC_EINVAL, "the layers are on different devices");
+  if (dst->H != src->H || dst->format[0] != src->format[0] || dst->format[1] != src->format[1])
+    return fail(KVC_EINVAL, "the layers differ in heads or frozen parameters");
+  if (!parent && dst->B != src->B) return fail(KVC_EINVAL, "layers of different batches need parent");
+  const kvc_status alike = slots_alike(dst, src, parent != nullptr);
+  if (alike) return alike;
   if (!index && n > src->len - start)
     return fail(KVC_EINVAL, "rows %lld .. %lld of a source of length %lld", (long long)start,
                 (long long)(start + n), (long long)src->len);
@@ -1105,6 +1118,212 @@ kvc_status kvc_accept(kvc_layer* L, int64_t N, const int32_t* index, int64_t n, 
     if (e != cudaSuccess) return cuda_fail(e, "accept launch");
   }
   L->len += n - N;
+  return succeed();
+}
+
+// Checks shared by the windowed attention's entry points; fills the shape fields of t.
+static kvc_status window_check(const kvc_layer* K, const kvc_layer* V, const kvc_window_desc* d,
+                               kvc::WindowArgs& t, size_t* ws_bytes) {
+  if (!K || !V) return fail(KVC_ESTATE, "key or value layer is NULL");
+  if (!d) return fail(KVC_EINVAL, "descriptor is NULL");
+  if (K->mode != KVC_MODE_UNIFORM && K->mode != KVC_MODE_CODEBOOK)
+    return fail(KVC_EINVAL, "keys must be a uniform or codebook layer");
+  if ((V->mode != KVC_MODE_INT8 && V->mode != KVC_MODE_UNIFORM) || V->p.prod)
+    return fail(KVC_EINVAL, "values must be an int8 or uniform layer");
+  if (K->B != V->B || K->H != V->H || K->D != V->D)
+    return fail(KVC_EINVAL, "key and value layers differ in B, H or D");
+  if (K->device != V->device) return fail(KVC_EINVAL, "key and value layers are on different devices");
+  if (K->len != V->len) return fail(KVC_EINVAL, "key and value layers hold different lengths");
+  if (K->D > 256) return fail(KVC_EINVAL, "D must be at most 256");
+  if (d->Hq < K->H || d->Hq % K->H) return fail(KVC_EINVAL, "Hq must be a multiple of H");
+  if (d->N < 1 || d->N > K->len)
+    return fail(KVC_EINVAL, "N %d queries: need 1 .. length (%lld)", d->N, (long long)K->len);
+  if (d->window < 0 || d->sinks < 0) return fail(KVC_EINVAL, "window and sinks must be >= 0");
+  if (K->ncpos > 256 || (V->mode == KVC_MODE_UNIFORM && V->ncpos > 256))
+    return fail(KVC_EINVAL, "more than 256 packed positions");
+  // kernels number tokens, rows and blocks in 32 bits
+  if (d->N > 65536) return fail(KVC_EINVAL, "more than 65536 queries");
+  if (K->len > INT32_MAX - 1024) return fail(KVC_EINVAL, "more than 2^31 - 1024 tokens");
+  if ((int64_t)K->B * d->Hq * d->N > (1 << 30)) return fail(KVC_EINVAL, "too many query rows");
+  if (d->weights && K->n_slots * ((K->len + 127) / 128) > INT32_MAX)
+    return fail(KVC_EINVAL, "too many tokens to keep weights of");
+  t.Hq = d->Hq;
+  t.rep = d->Hq / K->H;
+  t.N = d->N;
+  t.S = (int)K->len;
+  t.ctx = (int)(K->len - d->N);
+  t.window = d->window ? (int)std::min<int64_t>(d->window, K->len) : t.S;
+  t.sinks = (int)std::min<int64_t>(d->sinks, K->len);
+  t.rows = t.rep * t.N;
+  t.NCk = std::max(8, K->ncpos);
+  t.Dv = V->mode == KVC_MODE_INT8 ? V->D : std::max(8, V->ncpos);
+  t.out_bf16 = V->p.out_dtype == KVC_BF16 ? 1 : 0;
+  t.weights = d->weights;
+  if (K->p.prod) {
+    t.prod = 1;
+    t.m = K->p.m;
+    t.n_out = K->p.n_out;
+    t.kcode = K->p.code_bytes;
+    t.knw = K->side_bytes / 2;
+  }
+  DeviceGuard dg(K->device);
+  if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
+  *ws_bytes = kvc::window_plan(K->p, V->p, t, kvc::sm_count());
+  return KVC_OK;
+}
+
+kvc_status kvc_attend_window_workspace_bytes(const kvc_layer* K, const kvc_layer* V,
+                                             const kvc_window_desc* d, size_t* out) {
+  if (!out) return fail(KVC_EINVAL, "out is NULL");
+  kvc::WindowArgs t;
+  size_t n = 0;
+  const kvc_status st = window_check(K, V, d, t, &n);
+  if (st) return st;
+  *out = n;
+  return succeed();
+}
+
+kvc_status kvc_attend_window(const kvc_layer* K, const kvc_layer* V, const kvc_window_desc* d,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  kvc::WindowArgs t;
+  size_t need = 0;
+  kvc_status st = window_check(K, V, d, t, &need);
+  if (st) return st;
+  if (!(d->scale >= 0.f) || !std::isfinite(d->scale)) return fail(KVC_EINVAL, "scale must be finite and >= 0");
+  if (d->weights && (!(d->decay >= 0.f) || !std::isfinite(d->decay)))
+    return fail(KVC_EINVAL, "decay must be finite and >= 0");
+  if (d->q_dtype != KVC_F32 && d->q_dtype != KVC_F16 && d->q_dtype != KVC_BF16)
+    return fail(KVC_EINVAL, "q_dtype must be KVC_F32, KVC_F16 or KVC_BF16");
+  if (!d->q || !d->out) return fail(KVC_EINVAL, "q or out is NULL");
+  if (!workspace || workspace_bytes < need)
+    return fail(KVC_EINVAL, "workspace is NULL or below kvc_attend_window_workspace_bytes()");
+  if ((uintptr_t)workspace % 256) return fail(KVC_EINVAL, "workspace must be 256-byte aligned");
+  if (d->q_stride_b < 0 || d->q_stride_h < 0 || d->q_stride_t < 0)
+    return fail(KVC_EINVAL, "strides must be >= 0");
+  st = rows_apart("out", K->D, {{{d->out_stride_b, K->B}, {d->out_stride_h, d->Hq}, {d->out_stride_t, d->N}}});
+  if (st) return st;
+  if (d->weights) {
+    st = rows_apart("weights", K->len, {{{d->weights_stride_b, K->B}, {d->weights_stride_h, K->H}, {0, 1}}});
+    if (st) return st;
+  }
+  if ((uintptr_t)d->q % (d->q_dtype == KVC_F32 ? 4 : 2) || (uintptr_t)d->out % 2 ||
+      (uintptr_t)d->first % 4 || (uintptr_t)d->weights % 4)
+    return fail(KVC_EINVAL, "an array is not aligned to its element size");
+  DeviceGuard dg(K->device);
+  if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
+  const void* ptrs[] = {d->q, d->out, workspace, d->first, d->weights};
+  for (const void* p : ptrs)
+    if (p && !is_device_ptr(p, K->device))
+      return fail(KVC_EINVAL, "q, first, out, weights and the workspace must be device memory of the layers' device");
+  t.q = d->q;
+  t.q_dtype = d->q_dtype;
+  t.q_sb = d->q_stride_b;
+  t.q_sh = d->q_stride_h;
+  t.q_st = d->q_stride_t;
+  t.first = d->first;
+  t.out = d->out;
+  t.o_sb = d->out_stride_b;
+  t.o_sh = d->out_stride_h;
+  t.o_st = d->out_stride_t;
+  t.w_sb = d->weights_stride_b;
+  t.w_sh = d->weights_stride_h;
+  t.decay = d->decay;
+  const double sc = d->scale > 0.f ? (double)d->scale : 1.0 / std::sqrt((double)K->D);
+  t.scale_log2 = (float)(sc * 1.4426950408889634);
+  int nk = 0;
+  const cudaError_t e = kvc::launch_attend_window(K->p, V->p, t, workspace,
+                                                  static_cast<cudaStream_t>(stream), &nk);
+  const_cast<kvc_layer*>(K)->launches += nk;
+  if (e != cudaSuccess) return cuda_fail(e, "windowed attention launch");
+  return succeed();
+}
+
+kvc_status kvc_evict(kvc_layer* K, kvc_layer* V, const kvc_evict_desc* d, void* stream) {
+  if (!K || !V) return fail(KVC_ESTATE, "key or value layer is NULL");
+  if (!d) return fail(KVC_EINVAL, "descriptor is NULL");
+  kvc_layer *DK = d->dst_keys, *DV = d->dst_values;
+  if (!DK != !DV) return fail(KVC_EINVAL, "one destination layer is NULL");
+  if (K == V) return fail(KVC_EINVAL, "keys and values are the same layer");
+  if (K->B != V->B || K->H != V->H) return fail(KVC_EINVAL, "key and value layers differ in B or H");
+  if (K->hpg != 1 || V->hpg != 1) return fail(KVC_EINVAL, "layers of head groups are not evicted by head");
+  if (K->device != V->device) return fail(KVC_EINVAL, "key and value layers are on different devices");
+  if (K->len != V->len) return fail(KVC_EINVAL, "key and value layers hold different lengths");
+  if (d->keep < 1 || d->keep > K->len)
+    return fail(KVC_EINVAL, "keep %lld outside [1, length %lld]", (long long)d->keep, (long long)K->len);
+  if (d->sinks < 0 || d->recent < 0 || d->sinks > d->keep || d->recent > d->keep - d->sinks)
+    return fail(KVC_EINVAL, "sinks and recent must be >= 0 and at most keep together");
+  if (K->len > INT32_MAX - 65536) return fail(KVC_EINVAL, "more than 2^31 - 65536 tokens");
+  if (K->n_slots > 65535) return fail(KVC_EINVAL, "more than 65535 (batch, head) pairs");
+  if (d->weights) {
+    const kvc_status st = rows_apart("weights", K->len, {{{d->weights_stride_b, K->B}, {d->weights_stride_h, K->H}, {0, 1}}});
+    if (st) return st;
+  }
+  if (DK) {
+    if (DK == K || DV == V || DK == V || DV == K || DK == DV)
+      return fail(KVC_EINVAL, "source and destination are the same layer");
+    for (const auto& p : {std::make_pair(DK, K), std::make_pair(DV, V)}) {
+      if (p.first->device != p.second->device) return fail(KVC_EINVAL, "the layers are on different devices");
+      if (p.first->B != p.second->B || p.first->H != p.second->H || p.first->format[0] != p.second->format[0] ||
+          p.first->format[1] != p.second->format[1])
+        return fail(KVC_EINVAL, "the layers differ in batch, heads or frozen parameters");
+      const kvc_status st = slots_alike(p.first, p.second, false);
+      if (st) return st;
+    }
+    if (DK->len != DV->len) return fail(KVC_EINVAL, "the destination layers hold different lengths");
+    if (d->keep > std::min(DK->capacity, DV->capacity) - DK->len)
+      return fail(KVC_ECAPACITY, "%lld tokens exceed the destination's capacity %lld (length %lld)",
+                  (long long)d->keep, (long long)std::min(DK->capacity, DV->capacity), (long long)DK->len);
+    if (d->dst_weights) {
+      const kvc_status st = rows_apart("dst_weights", DK->len + d->keep,
+                                       {{{d->dst_weights_stride_b, K->B}, {d->dst_weights_stride_h, K->H}, {0, 1}}});
+      if (st) return st;
+      if (d->dst_weights == d->weights) return fail(KVC_EINVAL, "dst_weights are the weights");
+    }
+  } else if (d->dst_weights) {
+    return fail(KVC_EINVAL, "dst_weights go with destination layers");
+  }
+  if ((uintptr_t)d->weights % 4 || (uintptr_t)d->dst_weights % 4 || (uintptr_t)d->first % 4 ||
+      (uintptr_t)d->first_out % 4 || (uintptr_t)d->index % 4)
+    return fail(KVC_EINVAL, "an array is not aligned to its element size");
+  if (d->first_out && d->first_out == d->first) return fail(KVC_EINVAL, "first_out is first");
+  if (!d->index) return fail(KVC_EINVAL, "index is NULL");
+  DeviceGuard dg(K->device);
+  if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
+  const void* ptrs[] = {d->weights, d->dst_weights, d->first, d->first_out, d->index};
+  for (const void* p : ptrs)
+    if (p && !is_device_ptr(p, K->device))
+      return fail(KVC_EINVAL, "weights, first and index must be device memory of the layers' device");
+  kvc::EvictArgs a;
+  a.weights = d->weights;
+  a.w_sb = d->weights_stride_b;
+  a.w_sh = d->weights_stride_h;
+  a.dst_weights = d->dst_weights;
+  a.dw_sb = d->dst_weights_stride_b;
+  a.dw_sh = d->dst_weights_stride_h;
+  a.first = d->first;
+  a.first_out = d->first_out;
+  a.index = d->index;
+  a.B = K->B;
+  a.H = K->H;
+  a.n_slots = K->n_slots;
+  a.S = (int)K->len;
+  a.n = (int)d->keep;
+  a.sinks = (int)d->sinks;
+  a.recent = (int)d->recent;
+  a.in_place = !DK;
+  a.dst_row0 = DK ? DK->len : 0;
+  int nk = 0;
+  const cudaError_t e = kvc::launch_evict(K->p, V->p, DK ? DK->p : K->p, DV ? DV->p : V->p, a,
+                                          std::max(K->pmax, V->pmax), kvc::sm_count(),
+                                          static_cast<cudaStream_t>(stream), &nk);
+  K->launches += nk;
+  if (e != cudaSuccess) return cuda_fail(e, "evict launch");
+  if (DK) {
+    DK->len += d->keep;
+    DV->len += d->keep;
+  } else {
+    K->len = V->len = d->keep;
+  }
   return succeed();
 }
 

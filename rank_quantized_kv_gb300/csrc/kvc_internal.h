@@ -201,6 +201,63 @@ cudaError_t launch_gather(const Params& dp, const Params& sp, const GatherArgs& 
 int accept_columns_per_block(int64_t n, int widest);
 cudaError_t launch_accept(const Params& p, AcceptArgs a, int pmax, cudaStream_t s, int* nk);
 
+// Attention of the last N stored tokens over a sliding window and the first
+// tokens (kvc_window.cu).  A slot has rep * N query rows, row i being query head
+// h * rep + i % rep of query i / rep, so that neighbouring rows see nearly the same
+// tokens.  They are cut into jobs of rt rows; the tokens that some row of a job sees
+// are cut into `splits` runs of tiles, and each leaves a partial.
+struct WindowArgs {
+  const void* q = nullptr;
+  int q_dtype = 0;
+  int64_t q_sb = 0, q_sh = 0, q_st = 0;  // element strides of batch, head, token
+  const int32_t* first = nullptr;        // [B] first visible token (null: 0)
+  void* out = nullptr;
+  int out_bf16 = 0;
+  int64_t o_sb = 0, o_sh = 0, o_st = 0;
+  int Hq = 0, rep = 0, N = 0;
+  float scale_log2 = 0.f;                // score scale times log2(e)
+  int S = 0, ctx = 0;                    // stored tokens; those before the queries
+  int window = 0, sinks = 0;             // at most S each; window S: no limit
+  int rows = 0, rt = 0, row_tiles = 0;   // rows of a slot, of a job; jobs of a slot
+  int splits = 1;
+  int NCk = 0, Dv = 0, Dvp = 0;          // packed positions; value channels, padded to 4
+  int prod = 0, m = 0, n_out = 0, kcode = 0, knw = 1;
+  // weights [b][h][token] that the tokens receive (null: not asked for)
+  float* weights = nullptr;
+  int64_t w_sb = 0, w_sh = 0;
+  float decay = 1.f;
+  // workspace: key weights [n_slots][rows][NCk], sketch and outlier weights
+  // [n_slots][rows][m + n_out], score offsets [n_slots][rows][c1_parts]; partials
+  // [n_slots][row_tiles][splits]: references and sums [rt], weighted sums [Dvp][rt];
+  // per row its reference and the inverse of its sum
+  float *w = nullptr, *wx = nullptr, *c1 = nullptr;
+  int c1_parts = 1;
+  float2* ml = nullptr;
+  float* part = nullptr;
+  float2* stats = nullptr;
+};
+// Fill the job fields of t; the workspace bytes.
+size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, int sms);
+cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs t, void* workspace,
+                                 cudaStream_t s, int* nk);
+
+// Eviction (kvc_evict.cu): n of S rows of every slot kept, by weight.
+struct EvictArgs {
+  float* weights = nullptr;        // [b][h][S] (null: all equal)
+  int64_t w_sb = 0, w_sh = 0;
+  float* dst_weights = nullptr;    // where the kept rows' weights go (null: nowhere)
+  int64_t dw_sb = 0, dw_sh = 0;
+  const int32_t* first = nullptr;  // [B] first token that is not padding (null: 0)
+  int32_t* first_out = nullptr;    // [B] (null: not asked for)
+  int32_t* index = nullptr;        // [n_slots][n] kept rows, ascending
+  int B = 0, H = 0, n_slots = 0;
+  int S = 0, n = 0, sinks = 0, recent = 0;
+  int64_t dst_row0 = 0;            // first row written of the destination layers
+  bool in_place = false;
+};
+cudaError_t launch_evict(const Params& kp, const Params& vp, const Params& dkp, const Params& dvp,
+                         const EvictArgs& a, int pmax, int sms, cudaStream_t s, int* nk);
+
 // On-device prefill fit of the uniform mode (kvc_fit.cu).  Every pointer is
 // device memory; the float64 scratch lives in the caller's workspace.
 constexpr int kFitMaxD = 128;

@@ -1,0 +1,49 @@
+// Which tokens a query of the windowed attention sees, and the tiles of them
+// that a job walks.
+#pragma once
+
+#include "kvc_internal.h"
+
+namespace kvc {
+
+// The tokens visible to a query at position pos of a batch entry: those of
+// [first, pos] within the window or before sink_end.
+struct Sight {
+  int first, sink_end, window;
+  __device__ Sight(const WindowArgs& t, int b) {
+    first = t.first ? min(max(t.first[b], 0), t.S) : 0;
+    sink_end = (int)min((int64_t)first + t.sinks, (int64_t)t.S);
+    window = t.window;
+  }
+  __device__ bool sees(int tok, int pos) const {
+    return tok >= first && tok <= pos && (tok > pos - window || tok < sink_end);
+  }
+  // Whether queries p0 .. p1 all see tokens t0 .. t1.
+  __device__ bool all(int t0, int t1, int p0, int p1) const {
+    return t0 >= first && t1 <= p0 && (t0 > p1 - window || t1 < sink_end);
+  }
+};
+
+// The tiles of T tokens that hold what some query of p0 .. p1 sees: the sinks'
+// [a, a + na), then the window's [b, b + nb); one range where they meet.
+template <int T>
+struct Tiles {
+  int a = 0, na = 0, b = 0, nb = 0;
+  __device__ Tiles(const Sight& s, int p0, int p1) {
+    if (s.first > p1) return;
+    a = s.first / T;
+    const int sink_end = min(s.sink_end, p1 + 1);
+    if (sink_end > s.first) na = (sink_end + T - 1) / T - a;
+    b = max(s.first, p0 - s.window + 1) / T;
+    nb = p1 / T + 1 - b;
+    if (a + na >= b) {  // (no sinks: where the window starts with the first token)
+      nb += b - a;
+      b = a;
+      na = 0;
+    }
+  }
+  __device__ int count() const { return na + nb; }
+  __device__ int tile(int i) const { return i < na ? a + i : b + i - na; }
+};
+
+}  // namespace kvc
