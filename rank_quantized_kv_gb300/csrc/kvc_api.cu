@@ -1168,7 +1168,9 @@ static kvc_status window_check(const kvc_layer* K, const kvc_layer* V, const kvc
   }
   DeviceGuard dg(K->device);
   if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
-  *ws_bytes = kvc::window_plan(K->p, V->p, t, kvc::sm_count());
+  t.Pk_max = K->pmax;
+  t.Pv_max = V->pmax;
+  *ws_bytes = kvc::window_plan(K->p, V->p, t, K->path == KVC_PATH_GENERIC, kvc::sm_count());
   return KVC_OK;
 }
 

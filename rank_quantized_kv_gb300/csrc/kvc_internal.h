@@ -204,8 +204,15 @@ cudaError_t launch_accept(const Params& p, AcceptArgs a, int pmax, cudaStream_t 
 // Attention of the last N stored tokens over a sliding window and the first
 // tokens (kvc_window.cu).  A slot has rep * N query rows, row i being query head
 // h * rep + i % rep of query i / rep, so that neighbouring rows see nearly the same
-// tokens.  They are cut into jobs of rt rows; the tokens that some row of a job sees
-// are cut into `splits` runs of tiles, and each leaves a partial.
+// tokens.  They are cut into jobs of rt rows.  A job has at most tps tiles of tokens
+// that one of its rows sees; the jobs' tiles are one line that is cut into equal
+// runs, one per CTA, so a CTA holds the ends of some jobs.  (A job that has fewer
+// tiles shares them out in the proportions of its stretch of the line.)  Each (job,
+// CTA) pair leaves a partial, number job + CTA.
+constexpr int kWindowTile = 16;  // tokens of a tile of the tensor-core kernels
+// Reference of a row that has seen tokens, all with scores of -inf (below fp32's
+// range); one that has seen none has -inf.
+constexpr float kWindowLowest = -3.402823466e38f;
 struct WindowArgs {
   const void* q = nullptr;
   int q_dtype = 0;
@@ -219,8 +226,11 @@ struct WindowArgs {
   int S = 0, ctx = 0;                    // stored tokens; those before the queries
   int window = 0, sinks = 0;             // at most S each; window S: no limit
   int rows = 0, rt = 0, row_tiles = 0;   // rows of a slot, of a job; jobs of a slot
-  int splits = 1;
+  int64_t tps = 0, total = 0;            // tiles of a job, of the line
+  int grid = 0, sms = 0;                 // CTAs of the main kernel; the device's SMs
+  int mma = 0;                           // warp-level tensor cores: 8-row tiles of a job, 0: CUDA cores
   int NCk = 0, Dv = 0, Dvp = 0;          // packed positions; value channels, padded to 4
+  int Pk_max = 0, Pv_max = 0;            // largest packed key / value row
   int prod = 0, m = 0, n_out = 0, kcode = 0, knw = 1;
   // weights [b][h][token] that the tokens receive (null: not asked for)
   float* weights = nullptr;
@@ -228,18 +238,34 @@ struct WindowArgs {
   float decay = 1.f;
   // workspace: key weights [n_slots][rows][NCk], sketch and outlier weights
   // [n_slots][rows][m + n_out], score offsets [n_slots][rows][c1_parts]; partials
-  // [n_slots][row_tiles][splits]: references and sums [rt], weighted sums [Dvp][rt];
-  // per row its reference and the inverse of its sum
+  // [jobs + grid - 1]: references and sums [rt], weighted sums [Dvp][rt]; per row its
+  // reference and the inverse of its sum
   float *w = nullptr, *wx = nullptr, *c1 = nullptr;
   int c1_parts = 1;
   float2* ml = nullptr;
   float* part = nullptr;
   float2* stats = nullptr;
 };
-// Fill the job fields of t; the workspace bytes.
-size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, int sms);
+// Shared memory of the tensor-core kernels: where a warp's ring starts, the bytes
+// of one of its stages and where their parts start (key rows lie first).
+struct WindowShape {
+  int off_ring = 0, stage = 0, off_kside = 0, off_v = 0, off_vside = 0;
+};
+// Fill the job fields of t (generic: CUDA cores); the workspace bytes.
+size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool generic, int sms);
 cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs t, void* workspace,
                                  cudaStream_t s, int* nk);
+using WindowKernel = void (*)(const Params, const Params, const WindowArgs, const WindowShape);
+// The kernel for these layers and jobs of 8, 16 or 32 rows, null where there is none,
+// and the bytes of its tables in shared memory (kvc_window_mma1.cu, 2 and 4).
+WindowKernel window_kernel_8(const Params& kp, const Params& vp, int NCk, int* tables);
+WindowKernel window_kernel_16(const Params& kp, const Params& vp, int NCk, int* tables);
+WindowKernel window_kernel_32(const Params& kp, const Params& vp, int NCk, int* tables);
+// The warp-level tensor-core kernels (kvc_window_mma.cu) for jobs of 8 nt rows:
+// whether they take these layers and how many CTAs fit an SM; their launchers.
+int window_mma_ctas(const Params& kp, const Params& vp, const WindowArgs& t, int nt);
+cudaError_t launch_window_mma(const Params& kp, const Params& vp, const WindowArgs& t, cudaStream_t s, int* nk);
+cudaError_t launch_window_weights_mma(const Params& kp, const WindowArgs& t, cudaStream_t s, int* nk);
 
 // Eviction (kvc_evict.cu): n of S rows of every slot kept, by weight.
 struct EvictArgs {

@@ -42,10 +42,6 @@ constexpr int kThreads = 128;  // 4 warps
 constexpr int kRows = 8;       // rows of a job
 constexpr int kTile = 128;     // tokens of a tile: 32 a warp
 
-// Reference of a row that has seen tokens, all with scores of -inf (below fp32's
-// range); one that has seen none has -inf.
-constexpr float kLowest = -3.402823466e38f;
-
 __device__ __forceinline__ float load_q(const WindowArgs& t, int64_t i) {
   if (t.q_dtype == KVC_F32) return static_cast<const float*>(t.q)[i];
   if (t.q_dtype == KVC_F16) return __half2float(static_cast<const __half*>(t.q)[i]);
@@ -75,6 +71,7 @@ __global__ void __launch_bounds__(kPrepThreads) window_prep_kernel(const Params 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nr = min(kRows, t.rows - r0), D = kp.D, r = kp.r;
   const bool uniform = kp.mode == KVC_MODE_UNIFORM;
+  grid_dependents_launch();
   {
     const int64_t at = warp < nr ? q_at(t, b, h, r0 + warp) : 0;
     for (int i = lane; i < D; i += 32) qs[i][warp] = warp < nr ? load_q(t, at + i) : 0.f;
@@ -274,120 +271,126 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ float c1s[kRows];
   constexpr bool VU = VMODE == KVC_MODE_UNIFORM;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int job = blockIdx.x / t.splits, split = blockIdx.x - job * t.splits;
-  const int slot = job / t.row_tiles, r0 = (job - slot * t.row_tiles) * kRows;
-  const int nr = min(kRows, t.rows - r0), Dv = t.Dv, stride = 2 + Dv;
-  const int b = slot / kp.H;
-  const int kbeta = kp.basis_of[slot], vbeta = VU ? vp.basis_of[slot] : 0;
-  const int64_t Pk = kp.P[kbeta], Pv = VU ? vp.P[vbeta] : vp.D;
+  const int Dv = t.Dv, stride = 2 + Dv;
   JobTables jt;
   jt.ws = smf;
   jt.wxs = jt.ws + t.NCk * kRows;
   jt.c1s = c1s;
   float* ps = jt.wxs + (t.m + t.n_out) * kRows + warp * 32 * kRows;
   float* merge = jt.wxs + (t.m + t.n_out) * kRows + 4 * 32 * kRows;
-  if (VU && tid >= 32 && tid < 64) vch[tid - 32] = chunk_entry(vp, vbeta, tid - 32);
-  load_tables<KMODE>(kp, kbeta, cbv, kch, &jt);
   grid_dependency_wait();  // the key weights come from the launch before
-  load_job(kp, t, slot, r0, jt);
-  __syncthreads();
-  const unsigned char* kbase = kp.store + kp.pay_off[slot];
-  const __half* kside = reinterpret_cast<const __half*>(kp.store + kp.side_off[slot]);
-  const unsigned char* vbase = vp.store + vp.pay_off[slot];
-  const __half* vscale = reinterpret_cast<const __half*>(vp.store + vp.side_off[slot]);
+  const int64_t run1 = window_run(t, blockIdx.x + 1);
+  for (int64_t at = window_run(t, blockIdx.x); at < run1;) {
+    const int job = (int)(at / t.tps);
+    const int64_t a0 = at - job * t.tps, a1 = min(t.tps, a0 + (run1 - at));
+    at += a1 - a0;
+    const int slot = job / t.row_tiles, r0 = (job - slot * t.row_tiles) * kRows;
+    const int nr = min(kRows, t.rows - r0), b = slot / kp.H;
+    const int kbeta = kp.basis_of[slot], vbeta = VU ? vp.basis_of[slot] : 0;
+    const int64_t Pk = kp.P[kbeta], Pv = VU ? vp.P[vbeta] : vp.D;
+    __syncthreads();  // the last job's tables and partial have been read
+    if (VU && tid >= 32 && tid < 64) vch[tid - 32] = chunk_entry(vp, vbeta, tid - 32);
+    load_tables<KMODE>(kp, kbeta, cbv, kch, &jt);
+    load_job(kp, t, slot, r0, jt);
+    __syncthreads();
+    const unsigned char* kbase = kp.store + kp.pay_off[slot];
+    const __half* kside = reinterpret_cast<const __half*>(kp.store + kp.side_off[slot]);
+    const unsigned char* vbase = vp.store + vp.pay_off[slot];
+    const __half* vscale = reinterpret_cast<const __half*>(vp.store + vp.side_off[slot]);
 
-  float m[kRows], l[kRows], acc[kRows][8];
-#pragma unroll
-  for (int g = 0; g < kRows; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[g][e] = 0.f;
-  }
-  const Sight sight(t, b);
-  const Tiles<kTile> tiles(sight, t.ctx + r0 / t.rep, t.ctx + (r0 + nr - 1) / t.rep);
-  const int64_t count = tiles.count();
-  const int i1 = (int)(count * (split + 1) / t.splits);
-  for (int i = (int)(count * split / t.splits); i < i1; ++i) {
-    const int tb = tiles.tile(i) * kTile + 32 * warp, tok = tb + lane;
-    const int n = min(32, t.S - tb);
-    if (n <= 0) continue;
-    float sc[kRows], sv = 1.f;  // sv: the value's scale
-#pragma unroll
-    for (int g = 0; g < kRows; ++g) sc[g] = 0.f;
-    if (lane < n) {
-      score_token<KMODE>(kp, t, jt, kbase + tok * Pk, kside + (int64_t)tok * t.knw, sc);
-      if (!VU) sv = __half2float(vscale[tok]);
-    }
+    float m[kRows], l[kRows], acc[kRows][8];
 #pragma unroll
     for (int g = 0; g < kRows; ++g) {
-      const bool see = lane < n && g < nr && sight.sees(tok, t.ctx + (r0 + g) / t.rep);
-      const float mn = fmaxf(m[g], warp_max(see ? fmaxf(sc[g], kLowest) : -INFINITY));
-      const float ref = mn == -INFINITY ? 0.f : mn;  // nothing visible yet
-      const float corr = exp2f(m[g] - ref);
-      const float p = see ? exp2f(sc[g] - ref) : 0.f;
-      l[g] = l[g] * corr + warp_sum(p);
-      m[g] = mn;
+      m[g] = -INFINITY;
+      l[g] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[g][e] *= corr;
-      ps[lane * kRows + g] = see ? p * sv : 0.f;
+      for (int e = 0; e < 8; ++e) acc[g][e] = 0.f;
     }
-    __syncwarp();
-    // lane owns channels lane, lane + 32, ..
-    for (int tt = 0; tt < n; ++tt) {
-      const unsigned char* row = vbase + (tb + tt) * Pv;
-      const int mis = (int)(reinterpret_cast<uintptr_t>(row) & 3);
-      float pv[kRows];
+    const Sight sight(t, b);
+    const Tiles<kTile> tiles(sight, t.ctx + r0 / t.rep, t.ctx + (r0 + nr - 1) / t.rep);
+    const int64_t count = tiles.count();
+    const int i1 = (int)(count * a1 / t.tps);
+    for (int i = (int)(count * a0 / t.tps); i < i1; ++i) {
+      const int tb = tiles.tile(i) * kTile + 32 * warp, tok = tb + lane;
+      const int n = min(32, t.S - tb);
+      if (n <= 0) continue;
+      float sc[kRows], sv = 1.f;  // sv: the value's scale
 #pragma unroll
-      for (int g = 0; g < kRows; ++g) pv[g] = ps[tt * kRows + g];
+      for (int g = 0; g < kRows; ++g) sc[g] = 0.f;
+      if (lane < n) {
+        score_token<KMODE>(kp, t, jt, kbase + tok * Pk, kside + (int64_t)tok * t.knw, sc);
+        if (!VU) sv = __half2float(vscale[tok]);
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int d = lane + 32 * e;
-        if (d >= Dv) break;
-        float v;
-        if (VU) {
-          const uint32_t ent = vch[d >> 3];
-          if (!ent) continue;  // a basis with fewer positions than another one
-          const int w = (int)((ent >> 16) & 0xfu);
-          v = (float)((int)chunk_code(bits_at(row - mis, mis + (int)(ent & 0xffffu)), w, d & 7) -
-                      (1 << (w - 1)));
-        } else {
-          v = (float)reinterpret_cast<const int8_t*>(row)[d];
+      for (int g = 0; g < kRows; ++g) {
+        const bool see = lane < n && g < nr && sight.sees(tok, t.ctx + (r0 + g) / t.rep);
+        const float mn = fmaxf(m[g], warp_max(see ? fmaxf(sc[g], kWindowLowest) : -INFINITY));
+        const float ref = mn == -INFINITY ? 0.f : mn;  // nothing visible yet
+        const float corr = exp2f(m[g] - ref);
+        const float p = see ? exp2f(sc[g] - ref) : 0.f;
+        l[g] = l[g] * corr + warp_sum(p);
+        m[g] = mn;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[g][e] *= corr;
+        ps[lane * kRows + g] = see ? p * sv : 0.f;
+      }
+      __syncwarp();
+      // lane owns channels lane, lane + 32, ..
+      for (int tt = 0; tt < n; ++tt) {
+        const unsigned char* row = vbase + (tb + tt) * Pv;
+        const int mis = (int)(reinterpret_cast<uintptr_t>(row) & 3);
+        float pv[kRows];
+#pragma unroll
+        for (int g = 0; g < kRows; ++g) pv[g] = ps[tt * kRows + g];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = lane + 32 * e;
+          if (d >= Dv) break;
+          float v;
+          if (VU) {
+            const uint32_t ent = vch[d >> 3];
+            if (!ent) continue;  // a basis with fewer positions than another one
+            const int w = (int)((ent >> 16) & 0xfu);
+            v = (float)((int)chunk_code(bits_at(row - mis, mis + (int)(ent & 0xffffu)), w, d & 7) -
+                        (1 << (w - 1)));
+          } else {
+            v = (float)reinterpret_cast<const int8_t*>(row)[d];
+          }
+#pragma unroll
+          for (int g = 0; g < kRows; ++g) acc[g][e] = fmaf(pv[g], v, acc[g][e]);
         }
-#pragma unroll
-        for (int g = 0; g < kRows; ++g) acc[g][e] = fmaf(pv[g], v, acc[g][e]);
       }
+      __syncwarp();  // ps is rewritten by the next block
     }
-    __syncwarp();  // ps is rewritten by the next block
-  }
-  // the warps' states into one partial
+    // the warps' states into one partial
 #pragma unroll
-  for (int g = 0; g < kRows; ++g) {
-    float* mg = merge + (warp * kRows + g) * stride;
-    if (lane == 0) {
-      mg[0] = m[g];
-      mg[1] = l[g];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (lane + 32 * e < Dv) mg[2 + lane + 32 * e] = acc[g][e];
-  }
-  __syncthreads();
-  for (int e = tid; e < kRows * stride; e += kThreads) {
-    const int d = e / kRows, g = e - d * kRows;
-    float M = -INFINITY;
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, merge[(w * kRows + g) * stride]);
-    float v = d == 0 ? M : 0.f;
-    if (d)
-      for (int w = 0; w < 4; ++w) {
-        const float* mg = merge + (w * kRows + g) * stride;
-        // (a warp without tokens has l = 0; one with NaN scores has m = -inf too)
-        if (mg[1] != 0.f) v = fmaf(exp2f(mg[0] - M), mg[d], v);
+    for (int g = 0; g < kRows; ++g) {
+      float* mg = merge + (warp * kRows + g) * stride;
+      if (lane == 0) {
+        mg[0] = m[g];
+        mg[1] = l[g];
       }
-    const size_t at = blockIdx.x;
-    if (d == 0) t.ml[at * kRows + g].x = v;
-    else if (d == 1) t.ml[at * kRows + g].y = v;
-    else t.part[(at * t.Dvp + d - 2) * kRows + g] = v;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (lane + 32 * e < Dv) mg[2 + lane + 32 * e] = acc[g][e];
+    }
+    __syncthreads();
+    for (int e = tid; e < kRows * stride; e += kThreads) {
+      const int d = e / kRows, g = e - d * kRows;
+      float M = -INFINITY;
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, merge[(w * kRows + g) * stride]);
+      float v = d == 0 ? M : 0.f;
+      if (d)
+        for (int w = 0; w < 4; ++w) {
+          const float* mg = merge + (w * kRows + g) * stride;
+          // (a warp without tokens has l = 0; one with NaN scores has m = -inf too)
+          if (mg[1] != 0.f) v = fmaf(exp2f(mg[0] - M), mg[d], v);
+        }
+      const size_t part = (size_t)job + blockIdx.x;
+      if (d == 0) t.ml[part * kRows + g].x = v;
+      else if (d == 1) t.ml[part * kRows + g].y = v;
+      else t.part[(part * t.Dvp + d - 2) * kRows + g] = v;
+    }
   }
 }
 
@@ -412,7 +415,15 @@ __global__ void __launch_bounds__(kCombineThreads)
   const bool vu = vp.mode == KVC_MODE_UNIFORM;
   const int beta = vu ? vp.basis_of[slot] : 0;
   const int jt = row0 / t.rt, rr = row0 - jt * t.rt;
-  const size_t p0 = ((size_t)slot * t.row_tiles + jt) * t.splits;
+  // the CTAs whose runs hold the job's tiles
+  const int64_t job = (int64_t)slot * t.row_tiles + jt, lo = job * t.tps, hi = lo + t.tps;
+  int64_t c0 = lo * t.grid / t.total;
+  while (window_run(t, c0 + 1) <= lo) ++c0;
+  while (window_run(t, c0) > lo) --c0;
+  int64_t c1 = c0;
+  while (window_run(t, c1 + 1) < hi) ++c1;
+  const int splits = (int)(c1 - c0) + 1;
+  const size_t p0 = (size_t)(job + c0);
   if (vu)
     for (int j = tid; j < t.Dv; j += kCombineThreads) {
       int width = 0;
@@ -428,13 +439,13 @@ __global__ void __launch_bounds__(kCombineThreads)
   const bool live = row0 + warp < t.rows;
   float M = -INFINITY, L = 0.f;
   if (live)
-    for (int s = lane; s < t.splits; s += 32) M = fmaxf(M, ml[(size_t)s * t.rt].x);
+    for (int s = lane; s < splits; s += 32) M = fmaxf(M, ml[(size_t)s * t.rt].x);
   M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
   const int d0 = tid & 127, q = tid >> 7;  // d0 and d0 + 128; row quad
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int s0 = 0; s0 < t.splits; s0 += kFactors) {
-    const int n = min(kFactors, t.splits - s0);
+  for (int s0 = 0; s0 < splits; s0 += kFactors) {
+    const int n = min(kFactors, splits - s0);
     __syncthreads();
     for (int e = lane; e < n; e += 32) {
       const float2 v = live ? ml[(size_t)(s0 + e) * t.rt] : make_float2(0.f, 0.f);
@@ -576,7 +587,7 @@ MainKernel main_kernel_for(int kmode, int vmode) {
                                    : window_main_kernel<KVC_MODE_CODEBOOK, KVC_MODE_INT8>;
 }
 
-// Tiles of `tile` tokens that a job of rt rows walks at most.
+// Tiles of `tile` tokens that a job of rt rows sees at most.
 int64_t most_tiles(const WindowArgs& t, int tile) {
   const int64_t all = (t.S + tile - 1) / tile;
   const int64_t span = (int64_t)t.window + (t.rt + t.rep - 1) / t.rep + 1;  // the window's tokens
@@ -599,7 +610,7 @@ struct Take {
 // The workspace's arrays in t; its bytes.
 size_t lay_out(const Params& kp, WindowArgs& t, void* workspace) {
   const size_t rows = (size_t)kp.n_slots * t.rows;
-  const size_t parts = (size_t)kp.n_slots * t.row_tiles * t.splits;
+  const size_t parts = (size_t)kp.n_slots * t.row_tiles + t.grid - 1;
   Take take(workspace);
   t.w = take.operator()<float>(rows * t.NCk);
   t.wx = take.operator()<float>(rows * (t.m + t.n_out));
@@ -612,15 +623,28 @@ size_t lay_out(const Params& kp, WindowArgs& t, void* workspace) {
 
 }  // namespace
 
-size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, int sms) {
-  (void)vp;
-  t.rt = kRows;
+size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool generic, int sms) {
+  t.sms = sms;
+  t.mma = 0;
+  int ctas = 12;  // of an SM: the CUDA cores'
+  if (!generic && !t.prod) {
+    const int nt = t.rows <= 8 ? 1 : t.rows <= 16 ? 2 : 4;
+    const int n = window_mma_ctas(kp, vp, t, nt);
+    if (n) {
+      t.mma = nt;
+      ctas = n;
+    }
+  }
+  t.rt = t.mma ? 8 * t.mma : kRows;
   t.row_tiles = (t.rows + t.rt - 1) / t.rt;
   t.Dvp = (t.Dv + 3) / 4 * 4;
   t.c1_parts = (t.NCk + kPrepCols - 1) / kPrepCols;
   const int64_t jobs = (int64_t)kp.n_slots * t.row_tiles;
-  // about twelve blocks per SM
-  t.splits = (int)std::max<int64_t>(1, std::min<int64_t>(12 * (int64_t)sms / jobs, most_tiles(t, kTile)));
+  t.tps = most_tiles(t, t.mma ? kWindowTile : kTile);
+  t.total = jobs * t.tps;
+  // a warp of the tensor-core kernel takes a tile, of the CUDA cores a quarter
+  const int64_t runs = t.mma ? std::max<int64_t>(t.total / 8, 1) : t.total;
+  t.grid = (int)std::min<int64_t>(runs, ctas * (int64_t)sms);
   return lay_out(kp, t, nullptr);
 }
 
@@ -640,18 +664,21 @@ cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs 
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const size_t tables = (size_t)kRows * (t.NCk + t.m + t.n_out) * 4;
-  {
+  if (t.mma) {
+    e = launch_window_mma(kp, vp, t, s, nk);
+  } else {
     const size_t smem = tables + 4 * 32 * kRows * 4 + 4 * (size_t)kRows * (2 + t.Dv) * 4;
     const MainKernel k = main_kernel_for(kp.mode, vp.mode);
     e = prepare_kernel(reinterpret_cast<const void*>(k), (int)smem);
     if (e != cudaSuccess) return e;
     ++*nk;
-    e = launch_dependent(k, (unsigned)(kp.n_slots * t.row_tiles * t.splits), kThreads, smem, s, kp, vp, t);
-    if (e != cudaSuccess) return e;
+    e = launch_dependent(k, (unsigned)t.grid, kThreads, smem, s, kp, vp, t);
   }
+  if (e != cudaSuccess) return e;
   ++*nk;
   e = launch_dependent(window_combine_kernel, row_blocks, kCombineThreads, 0, s, kp, vp, t);
   if (e != cudaSuccess || !t.weights) return e;
+  if (t.mma) return launch_window_weights_mma(kp, t, s, nk);
   const auto k = kp.mode == KVC_MODE_UNIFORM ? window_weights_kernel<KVC_MODE_UNIFORM>
                                              : window_weights_kernel<KVC_MODE_CODEBOOK>;
   k<<<(unsigned)kp.n_slots * (unsigned)((t.S + kTile - 1) / kTile), kThreads, tables, s>>>(kp, t);

@@ -6,6 +6,9 @@
 
 namespace kvc {
 
+// The run of tiles of CTA c is [window_run(t, c), window_run(t, c + 1)).
+__device__ __forceinline__ int64_t window_run(const WindowArgs& t, int64_t c) { return t.total * c / t.grid; }
+
 // The tokens visible to a query at position pos of a batch entry: those of
 // [first, pos] within the window or before sink_end.
 struct Sight {

@@ -1,0 +1,275 @@
+// The windowed attention's warp-level tensor-core kernels: their choice and launch,
+// and the kernel for the weights that the tokens receive.
+#include <algorithm>
+
+#include "kvc_launch.cuh"
+#include "kvc_window.cuh"
+#include "kvc_window_mma.cuh"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32, kTile = kWindowTile, kStages = 3;
+constexpr int kChunkTiles = 16;  // 8-row tiles whose weights are in shared memory at a time
+
+// The weights that the tokens of a slot receive: the scores again, p = 2^(s - m) / l.
+// A warp decodes the keys of 16 tokens into operand registers once and meets all rows
+// of a chunk with them, whose weights lie in shared memory (ONE: 8 rows at most, in
+// registers); a token's sums stay in two registers of four lanes.  CTAs take runs of
+// the slots' tiles.  Where there are more rows than a chunk the keys are decoded again
+// for the next one, by the same warp, which then adds to what it wrote.
+template <int KB, int KS, bool ONE>
+__global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
+    window_weights_mma_kernel(const Params kp, const WindowArgs t, const WindowShape z) {
+  using K = Keys<KB, KS>;
+  constexpr int NT = ONE ? 1 : kChunkTiles;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(16) float4 rowc[8 * NT];  // per row: score factor, -m, 1 / l, position
+  __shared__ float row_mul[8 * NT];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  uint4* wfrag = reinterpret_cast<uint4*>(smem + K::kTable);  // [NT][step][32], unless in registers
+  unsigned char* ring = smem + z.off_ring + warp * kStages * z.stage;
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+  if (KB) K::fill(kp, smem, kThreads);
+  K keys;
+  keys.begin(smem);
+  const int64_t tps = (t.S + kTile - 1) / kTile, total = tps * kp.n_slots;
+  const int64_t run1 = total * (blockIdx.x + 1) / gridDim.x;
+  bool waited = false;
+  for (int64_t at = total * blockIdx.x / gridDim.x; at < run1;) {
+    const int slot = (int)(at / tps);
+    const int a0 = (int)(at - slot * tps), a1 = (int)min(tps, a0 + (run1 - at));
+    at += a1 - a0;
+    const int b = slot / kp.H, h = slot - b * kp.H, kbeta = kp.basis_of[slot], Pk = kp.P[kbeta];
+    const unsigned char* kbase = kp.store + kp.pay_off[slot];
+    const unsigned char* kside = kp.store + kp.side_off[slot];
+    float* wout = t.weights + b * t.w_sb + h * t.w_sh;
+    const Sight sight(t, b);
+    keys.basis(kp, kbeta);
+    for (int r0 = 0; r0 < t.rows; r0 += 8 * NT) {
+      const int nr = min(8 * NT, t.rows - r0), tiles = (nr + 7) / 8;
+      const int p0 = t.ctx + r0 / t.rep, p1 = t.ctx + (r0 + nr - 1) / t.rep;
+      const float decay = r0 ? 1.f : t.decay;
+      // tiles that some row sees; all of them where the old weights are scaled
+      auto idle = [&](int tile) {
+        const int t0 = tile * kTile;
+        return t0 > p1 || t0 + kTile <= sight.first ||
+               (t0 + kTile <= p0 - sight.window + 1 && t0 >= sight.sink_end);
+      };
+      auto next = [&](int tile) {
+        if (decay == 1.f)
+          while (tile < a1 && idle(tile)) tile += kWarps;
+        return tile;
+      };
+      auto load = [&](int tile, int st) {
+        if (tile < a1) {
+          const int64_t t0 = (int64_t)tile * kTile;
+          const int n = (int)min((int64_t)kTile, t.S - t0);
+          const uint32_t dst = ring_s + st * z.stage;
+          const unsigned char* src = kbase + t0 * Pk;
+          for (int e = lane; e < (n * Pk + 15) >> 4; e += 32) copy16(dst + 16 * e, src + 16 * e);
+          if (KB && lane < (2 * n + 15) >> 4) copy16(dst + z.off_kside + 16 * lane, kside + 2 * t0 + 16 * lane);
+        }
+        copy_commit();
+      };
+      __syncthreads();  // the last chunk's rows have been read
+      int tile = next(a0 + warp), ahead = tile;
+#pragma unroll
+      for (int s = 0; s < kStages - 1; ++s) {
+        load(ahead, s);
+        ahead = next(ahead + kWarps);
+      }
+      if (!waited) grid_dependency_wait();
+      waited = true;
+      const float tab_inv = KB ? 1.f / K::table_scale(kp) : 1.f;
+      const float* w0 = t.w + ((size_t)slot * t.rows + r0) * t.NCk;
+      for (int r = warp; r < 8 * tiles; r += kWarps) {
+        float most = 0.f;
+        if (r < nr)
+          for (int j = lane; j < t.NCk; j += 32) {
+            const float w = fabsf(w0[(size_t)r * t.NCk + j]);
+            if (w <= 3.4e38f) most = fmaxf(most, w);
+          }
+        const float mul = row_scale(warp_max(most));
+        if (lane == 0) {
+          row_mul[r] = mul;
+          const float2 s = r < nr ? t.stats[(size_t)slot * t.rows + r0 + r] : make_float2(0.f, 0.f);
+          rowc[r] = make_float4(tab_inv / mul, -s.x, s.y, __int_as_float(r < nr ? t.ctx + (r0 + r) / t.rep : -1));
+        }
+      }
+      __syncthreads();
+      auto fragment = [&](int s, int nt) {
+        const int r = 8 * nt + g, j = K::position(s, c);
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < nr && j < t.NCk) w = *reinterpret_cast<const float4*>(w0 + (size_t)r * t.NCk + j);
+        return weight_pieces(w, row_mul[r]);
+      };
+      uint4 wreg[ONE ? KS : 1];
+      if (ONE) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) wreg[ONE ? s : 0] = fragment(s, 0);
+      } else {
+        for (int e = warp; e < KS * tiles; e += kWarps) wfrag[e * 32 + lane] = fragment(e % KS, e / KS);
+        __syncthreads();
+      }
+      int st = 0;
+      while (tile < a1) {
+        copy_wait<kStages - 2>();
+        __syncwarp();
+        const unsigned char* sp = ring + st * z.stage;
+        load(ahead, st + kStages - 1 >= kStages ? st - 1 : st + kStages - 1);
+        ahead = next(ahead + kWarps);
+        const int t0 = tile * kTile;
+        float sum[2] = {0.f, 0.f};  // tokens g and g + 8
+        if (!idle(tile)) {
+          uint32_t hi[KS][4], lo[KB ? KS : 1][4];
+          {
+            const typename K::Row ra = keys.row(sp, g, Pk), rb = keys.row(sp, g + 8, Pk);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              uint32_t ha[2], la[2], hb[2], lb[2];
+              keys.step(ra, k, ha, la);
+              keys.step(rb, k, hb, lb);
+              hi[k][0] = ha[0]; hi[k][1] = hb[0]; hi[k][2] = ha[1]; hi[k][3] = hb[1];
+              if (KB) {
+                lo[KB ? k : 0][0] = la[0]; lo[KB ? k : 0][1] = lb[0];
+                lo[KB ? k : 0][2] = la[1]; lo[KB ? k : 0][3] = lb[1];
+              }
+            }
+          }
+          float na = 1.f, nb = 1.f;
+          if (KB) {
+            const __half* nm = reinterpret_cast<const __half*>(sp + z.off_kside);
+            na = __half2float(nm[g]);
+            nb = __half2float(nm[g + 8]);
+          }
+          const bool all = sight.all(t0, t0 + kTile - 1, p0, p1);
+#pragma unroll 1
+          for (int nt = 0; nt < (ONE ? 1 : tiles); ++nt) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              const uint4 w = ONE ? wreg[ONE ? k : 0] : wfrag[(nt * KS + k) * 32 + lane];
+              mma_f16(s, hi[k], w.x, w.y);
+              mma_f16(small, hi[k], w.z, w.w);
+              if (KB) mma_f16(small, lo[KB ? k : 0], w.x, w.y);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 rc = rowc[8 * nt + 2 * c + j];
+              const float pa = ex2(fmaf((s[j] + small[j]) * na, rc.x, rc.y)) * rc.z;
+              const float pb = ex2(fmaf((s[2 + j] + small[2 + j]) * nb, rc.x, rc.y)) * rc.z;
+              const int pos = __float_as_int(rc.w);
+              if (all || sight.sees(t0 + g, pos)) sum[0] += pa;
+              if (all || sight.sees(t0 + g + 8, pos)) sum[1] += pb;
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          sum[j] += __shfl_xor_sync(kFull, sum[j], 1);
+          sum[j] += __shfl_xor_sync(kFull, sum[j], 2);
+        }
+        const int tok = t0 + g + 8 * (c & 1);
+        const float add = c & 1 ? sum[1] : sum[0];
+        if (c < 2 && tok < t.S) {
+          if (decay == 0.f) wout[tok] = add;
+          else if (decay != 1.f || add != 0.f) wout[tok] = fmaf(decay, wout[tok], add);
+        }
+        tile = next(tile + kWarps);
+        if (++st == kStages) st = 0;
+      }
+      copy_wait<0>();
+    }
+  }
+}
+
+using WeightsKernel = void (*)(const Params, const WindowArgs, const WindowShape);
+
+template <bool ONE>
+WeightsKernel weights_kernel_for(const Params& kp, int NCk, int* tables) {
+  auto of = [&](auto keys, WeightsKernel k) {
+    using K = decltype(keys);
+    *tables = K::kTable + (ONE ? 0 : K::kSteps * kChunkTiles * 512);
+    return k;
+  };
+  if (kp.mode == KVC_MODE_UNIFORM) {
+    if (NCk <= 64) return of(Keys<0, 4>{}, window_weights_mma_kernel<0, 4, ONE>);
+    return of(Keys<0, 8>{}, window_weights_mma_kernel<0, 8, ONE>);
+  }
+  switch (kp.cb_bits * 1000 + kp.D) {
+    case 2064: return of(Keys<2, 4>{}, window_weights_mma_kernel<2, 4, ONE>);
+    case 3064: return of(Keys<3, 4>{}, window_weights_mma_kernel<3, 4, ONE>);
+    case 4064: return of(Keys<4, 4>{}, window_weights_mma_kernel<4, 4, ONE>);
+    case 2128: return of(Keys<2, 8>{}, window_weights_mma_kernel<2, 8, ONE>);
+    case 3128: return of(Keys<3, 8>{}, window_weights_mma_kernel<3, 8, ONE>);
+    default: return of(Keys<4, 8>{}, window_weights_mma_kernel<4, 8, ONE>);
+  }
+}
+
+WindowKernel main_kernel(const Params& kp, const Params& vp, int NCk, int nt, int* tables) {
+  return nt == 1   ? window_kernel_8(kp, vp, NCk, tables)
+         : nt == 2 ? window_kernel_16(kp, vp, NCk, tables)
+                   : window_kernel_32(kp, vp, NCk, tables);
+}
+
+// The layout of the rings behind `tables` bytes; the dynamic shared memory.
+int lay_out(const Params& kp, const Params* vp, const WindowArgs& t, int tables, WindowShape* z) {
+  auto up = [](int v) { return (v + 15) / 16 * 16; };
+  int at = up(kTile * t.Pk_max) + 16;  // (words are read past a row's end)
+  z->off_kside = at;
+  at += kTile * 2;
+  if (vp) {
+    z->off_v = at;
+    at += vp->mode == KVC_MODE_UNIFORM ? up(kTile * t.Pv_max) + 16 : kTile * (vp->D + 16);
+    z->off_vside = at;
+    at += kTile * 2;
+  }
+  z->stage = at;
+  z->off_ring = (tables + 127) / 128 * 128;
+  // the join of the warps' sums takes the rings' place
+  const int join = vp ? kWarps * (vp->mode == KVC_MODE_UNIFORM ? 128 : vp->D) * 32 : 0;
+  return z->off_ring + std::max(kWarps * kStages * z->stage, join);
+}
+
+}  // namespace
+
+int window_mma_ctas(const Params& kp, const Params& vp, const WindowArgs& t, int nt) {
+  if (kp.prod || kp.D > 128) return 0;
+  if (vp.mode == KVC_MODE_UNIFORM ? t.Dv > 128 : vp.D != 64 && vp.D != 128) return 0;
+  int tables = 0;
+  const WindowKernel k = main_kernel(kp, vp, t.NCk, nt, &tables);
+  if (!k) return 0;
+  WindowShape z;
+  const int smem = lay_out(kp, &vp, t, tables, &z);
+  if (smem > 200 * 1024) return 0;
+  return nt == 1 && 2 * smem <= 220 * 1024 ? 2 : 1;
+}
+
+cudaError_t launch_window_mma(const Params& kp, const Params& vp, const WindowArgs& t, cudaStream_t s, int* nk) {
+  int tables = 0;
+  const WindowKernel k = main_kernel(kp, vp, t.NCk, t.mma, &tables);
+  WindowShape z;
+  const int smem = lay_out(kp, &vp, t, tables, &z);
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);
+  if (e != cudaSuccess) return e;
+  ++*nk;
+  return launch_dependent(k, (unsigned)t.grid, kThreads, (size_t)smem, s, kp, vp, t, z);
+}
+
+cudaError_t launch_window_weights_mma(const Params& kp, const WindowArgs& t, cudaStream_t s, int* nk) {
+  int tables = 0;
+  const bool one = t.rows <= 8;
+  const WeightsKernel k = one ? weights_kernel_for<true>(kp, t.NCk, &tables) : weights_kernel_for<false>(kp, t.NCk, &tables);
+  WindowShape z;
+  const int smem = lay_out(kp, nullptr, t, tables, &z);
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);
+  if (e != cudaSuccess) return e;
+  const int64_t total = (t.S + kTile - 1) / kTile * (int64_t)kp.n_slots;
+  const int grid = (int)std::min<int64_t>(std::max<int64_t>(total / kWarps, 1), (one ? 2 : 1) * (int64_t)t.sms);
+  ++*nk;
+  return launch_dependent(k, (unsigned)grid, kThreads, (size_t)smem, s, kp, t, z);
+}
+
+}  // namespace kvc

@@ -1,0 +1,252 @@
+// Pieces of the windowed attention's warp-level tensor-core kernels: matrix
+// instructions, decoding of codes straight into their operand registers.
+//
+// m16n8k16 with tokens on the M side: lane (g, c) = (lane / 4, lane % 4) holds of A
+// rows g and g + 8, of B and of the result columns g and 2 c, 2 c + 1.  The order of
+// the K axis is free as long as both operands agree, so a lane takes a stretch of a
+// token's packed row and decodes it into the registers where it is needed.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kvc_codes.cuh"
+#include "kvc_internal.h"
+
+namespace kvc {
+
+namespace {
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values, two neighbours of a row per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two floats as bf16, x in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Centred codes 2 q and 2 q + 1 of a chunk of width w as fp16: 0x6400 | c is
+// 1024 + c exactly.
+__device__ __forceinline__ uint32_t centred_pair(uint2 b, int w, int q) {
+  const uint32_t sub = 0x64006400u | ((1u << (w - 1)) * 0x10001u);
+  if (w == 8) return sub_f16x2(__byte_perm(q < 2 ? b.x : b.y, 0x64646464u, q & 1 ? 0x5342 : 0x5140), sub);
+  const uint32_t mask = (1u << w) - 1u, x = b.x >> (2 * q * w);
+  return sub_f16x2((x & mask) | ((x << (16 - w)) & (mask << 16)) | 0x64006400u, sub);
+}
+
+// Byte e of two words, as the low bytes of 16-bit halves (the high bytes hold anything).
+template <int E>
+__device__ __forceinline__ uint32_t bytes_of(uint32_t a, uint32_t b) {
+  return __byte_perm(a, b, E | (E << 4) | ((4 + E) << 8) | ((4 + E) << 12));
+}
+// int8 values in the low bytes of the halves as bf16: 0x4300 | u is 128 + u for u of
+// 7 bits; the sign bit in its place makes 256 of the other 128.
+__device__ __forceinline__ uint32_t int8_bf16(uint32_t x) {
+  return sub_bf16x2((x & 0x007f007fu) | 0x43004300u, (x & 0x00800080u) | 0x43004300u);
+}
+// Code e of width w of two chunks, centred, as bf16.
+__device__ __forceinline__ uint32_t centred_bf16(uint2 a, uint2 b, int w, int e) {
+  if (w == 8) {
+    const uint32_t x = e < 4 ? a.x : a.y, y = e < 4 ? b.x : b.y;
+    const uint32_t at = e & 3;
+    return int8_bf16(__byte_perm(x, y, at | (at << 4) | ((4 + at) << 8) | ((4 + at) << 12)) ^ 0x00800080u);
+  }
+  const uint32_t mask = (1u << w) - 1u;
+  return sub_bf16x2(((a.x >> (w * e)) & mask) | (((b.x >> (w * e)) & mask) << 16) | 0x43004300u,
+                    0x43004300u | ((1u << (w - 1)) * 0x10001u));
+}
+
+// ---------------------------------------------------------------- keys
+
+// How a warp reads the keys of 16 tokens: KB > 0, a codebook of KB bits over 16 KS
+// components, else centred codes of up to 4 KS / 2 chunks (KS steps of 16).
+//
+// Scores carry fp32's precision: weights are two fp16 pieces of values that a power
+// of two per row brings up to 2^13 .. 2^14 (22 bits and more), uniform codes are
+// exact, and centroids two fp16 pieces of values in 8 .. 16; the products of the
+// small pieces are summed apart.
+template <int KB, int KS>
+struct Keys {
+  static constexpr int kSteps = KS;
+  static constexpr int kPieces = KB ? 2 : 1;            // of A
+  static constexpr int kCodes = 4 * KS;                 // a lane's codes of a token
+  static constexpr int kWords = KB ? (kCodes * KB + 31) / 32 : 1;
+  // Pairs of centroids, both pieces, once per lane (no bank conflicts), up to 3 bits;
+  // single ones at 4.
+  static constexpr int kTable = !KB ? 0 : KB <= 3 ? (1 << (2 * KB)) * 32 * 8 : 16 * 32 * 4;
+
+  const unsigned char* tab;  // this lane's copy
+  uint32_t ent[KS / 2];      // uniform: the lane's chunks
+
+  // The scale of the centroids: a power of two that brings the largest to [8, 16).
+  static __device__ float table_scale(const Params& kp) {
+    const float big = fmaxf(fabsf(kp.codebook[0]), fabsf(kp.codebook[kp.cb_levels - 1]));
+    if (!(big > 0.f) || big > 3.4e38f) return 1.f;
+    const int e = ((__float_as_int(big) >> 23) & 0xff) - 127;  // big in [2^e, 2^(e + 1))
+    return __int_as_float((min(126, max(-126, 3 - e)) + 127) << 23);
+  }
+  // Fill the table (all threads).  A lane reads entry x at x * 256 (KB <= 3) or x * 128.
+  static __device__ void fill(const Params& kp, unsigned char* table, int threads) {
+    const float mul = table_scale(kp);
+    auto pieces = [&](int c, uint32_t* hi, uint32_t* lo) {
+      const float v = kp.codebook[c] * mul;
+      const __half h = __float2half_rn(v);
+      *hi = __half_as_ushort(h);
+      *lo = __half_as_ushort(__float2half_rn(v - __half2float(h)));
+    };
+    constexpr int lm = KB ? (1 << KB) - 1 : 0;
+    for (int i = threadIdx.x; i < kTable / (KB <= 3 ? 8 : 4); i += threads) {
+      const int x = i >> 5;
+      uint32_t h0, l0, h1, l1;
+      pieces(x & lm, &h0, &l0);
+      if (KB <= 3) {
+        pieces(x >> KB, &h1, &l1);
+        reinterpret_cast<uint2*>(table)[i] = make_uint2(h0 | (h1 << 16), l0 | (l1 << 16));
+      } else {
+        reinterpret_cast<uint32_t*>(table)[i] = h0 | (l0 << 16);
+      }
+    }
+  }
+
+  __device__ void begin(const unsigned char* table) {
+    tab = table + (threadIdx.x & 31) * (KB <= 3 ? 8 : 4);
+  }
+  // A job's basis (uniform keys).
+  __device__ void basis(const Params& kp, int beta) {
+    if (!KB)
+#pragma unroll
+      for (int s = 0; s < KS / 2; ++s) ent[s] = chunk_entry(kp, beta, 4 * s + (threadIdx.x & 3));
+  }
+  // The packed position of the first of the four codes that lane c has of step s.
+  static __device__ int position(int s, int c) { return KB ? c * kCodes + 4 * s : 8 * (4 * (s / 2) + c) + 4 * (s & 1); }
+
+  // What a lane holds of a token's row: the words of its codes (codebook).
+  struct Row { uint32_t w[kWords]; const unsigned char* at; };
+  __device__ Row row(const unsigned char* rows, int token, int Pk) const {
+    Row r;
+    if (KB) {
+      const int a = token * Pk + (threadIdx.x & 3) * (kCodes * KB / 8);
+      if ((kCodes * KB / 8) % 4 == 0) {
+        const unsigned char* p = rows + a;
+        if (kWords == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p);
+          r.w[0] = v.x; r.w[1 % kWords] = v.y; r.w[2 % kWords] = v.z; r.w[3 % kWords] = v.w;
+        } else if (kWords == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          r.w[0] = v.x; r.w[1 % kWords] = v.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) r.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        }
+      } else {  // 6 bytes
+        const uint2 v = bits_at(rows, a);
+        r.w[0] = v.x; r.w[1 % kWords] = v.y;
+      }
+    } else {
+      r.at = rows + token * Pk;
+    }
+    return r;
+  }
+  // The lane's four codes of step s of a token as fp16 pairs: hi[0] the first two,
+  // hi[1] the others; their second pieces in lo.
+  __device__ void step(const Row& r, int s, uint32_t (&hi)[2], uint32_t (&lo)[2]) const {
+    if constexpr (KB == 0) {
+      const uint32_t e = ent[s / 2];
+      hi[0] = hi[1] = 0u;
+      if (e) {
+        const int mis = (int)(reinterpret_cast<uintptr_t>(r.at) & 3), w = (int)((e >> 16) & 0xfu);
+        const uint2 b = bits_at(r.at - mis, mis + (int)(e & 0xffffu));
+        hi[0] = centred_pair(b, w, 2 * (s & 1));
+        hi[1] = centred_pair(b, w, 2 * (s & 1) + 1);
+      }
+      lo[0] = lo[1] = 0u;
+    } else if constexpr (KB <= 3) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // the pair's field (2 KB bits) shifted to bit 8: a table offset
+        constexpr uint32_t mask = ((1u << (2 * KB)) - 1u) << 8;
+        const int off = KB * (4 * s + 2 * i) - 8, at = off >> 5, sh = off & 31;
+        uint32_t v;
+        if (off < 0) v = r.w[0] << -off;
+        else if (sh + 2 * KB + 8 <= 32 || at + 1 >= kWords) v = r.w[at] >> sh;
+        else v = __funnelshift_r(r.w[at], r.w[(at + 1) % kWords], sh);
+        const uint2 p = *reinterpret_cast<const uint2*>(tab + (v & mask));
+        hi[i] = p.x;
+        lo[i] = p.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t x = r.w[s / 2] >> (16 * (s & 1) + 8 * i);  // two codes in the low byte
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(tab + ((x & 15u) << 7));
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(tab + ((x & 0xf0u) << 3));
+        hi[i] = __byte_perm(a, b, 0x5410);
+        lo[i] = __byte_perm(a, b, 0x7632);
+      }
+    }
+  }
+};
+
+// The power of two by which a row's weights are multiplied (largest to [2^13, 2^14)),
+// given the largest of their magnitudes (finite ones).
+__device__ __forceinline__ float row_scale(float most) {
+  const int e = ((__float_as_int(most) >> 23) & 0xff) - 127;
+  return most > 0.f ? __int_as_float((min(126, 13 - e) + 127) << 23) : 1.f;
+}
+
+// Four weights of a row as fp16 pieces: {hi01, hi23, lo01, lo23}, the operand
+// registers of a step.
+__device__ __forceinline__ uint4 weight_pieces(float4 w, float scale) {
+  w.x *= scale; w.y *= scale; w.z *= scale; w.w *= scale;
+  const __half2 h0 = __floats2half2_rn(w.x, w.y), h1 = __floats2half2_rn(w.z, w.w);
+  const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+  return make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
+                    pack_f16(w.x - f0.x, w.y - f0.y), pack_f16(w.z - f1.x, w.w - f1.y));
+}
+
+}  // namespace
+
+}  // namespace kvc
