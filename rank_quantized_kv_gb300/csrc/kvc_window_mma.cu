@@ -62,14 +62,21 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
           while (tile < a1 && idle(tile)) tile += kWarps;
         return tile;
       };
+      const unsigned char* klane = kbase + 16 * lane;
       auto load = [&](int tile, int st) {
         if (tile < a1) {
-          const int64_t t0 = (int64_t)tile * kTile;
-          const int n = (int)min((int64_t)kTile, t.S - t0);
-          const uint32_t dst = ring_s + st * z.stage;
-          const unsigned char* src = kbase + t0 * Pk;
-          for (int e = lane; e < (n * Pk + 15) >> 4; e += 32) copy16(dst + 16 * e, src + 16 * e);
-          if (KB && lane < (2 * n + 15) >> 4) copy16(dst + z.off_kside + 16 * lane, kside + 2 * t0 + 16 * lane);
+          const int t0 = tile * kTile, n = min(kTile, t.S - t0);
+          const uint32_t dst = ring_s + st * z.stage + 16 * lane;
+          const unsigned char* ks = klane + (int64_t)t0 * Pk;
+          if (KB && n == kTile) {
+            constexpr int kPieces = 2 * KS * KB;
+#pragma unroll
+            for (int e = 0; e < (kPieces + 31) / 32; ++e)
+              if (32 * e + 32 <= kPieces || lane + 32 * e < kPieces) copy16(dst + 512 * e, ks + 512 * e);
+          } else {
+            for (int e = lane; e < (n * Pk + 15) >> 4; e += 32) copy16(dst + 16 * (e - lane), ks + 16 * (e - lane));
+          }
+          if (KB && lane < 2 && 8 * lane < n) copy16(dst + z.off_kside, kside + 2 * (int64_t)t0 + 16 * lane);
         }
         copy_commit();
       };
@@ -123,21 +130,14 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
         const int t0 = tile * kTile;
         float sum[2] = {0.f, 0.f};  // tokens g and g + 8
         if (!idle(tile)) {
-          uint32_t hi[KS][4], lo[KB ? KS : 1][4];
-          {
-            const typename K::Row ra = keys.row(sp, g, Pk), rb = keys.row(sp, g + 8, Pk);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              uint32_t ha[2], la[2], hb[2], lb[2];
-              keys.step(ra, k, ha, la);
-              keys.step(rb, k, hb, lb);
-              hi[k][0] = ha[0]; hi[k][1] = hb[0]; hi[k][2] = ha[1]; hi[k][3] = hb[1];
-              if (KB) {
-                lo[KB ? k : 0][0] = la[0]; lo[KB ? k : 0][1] = lb[0];
-                lo[KB ? k : 0][2] = la[1]; lo[KB ? k : 0][3] = lb[1];
-              }
-            }
-          }
+          const typename K::Row ra = keys.row(sp, g, Pk), rb = keys.row(sp, g + 8, Pk);
+          auto operand = [&](int k, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+            uint32_t ha[2], la[2], hb[2], lb[2];
+            keys.step(ra, k, ha, la);
+            keys.step(rb, k, hb, lb);
+            hi[0] = ha[0]; hi[1] = hb[0]; hi[2] = ha[1]; hi[3] = hb[1];
+            lo[0] = la[0]; lo[1] = lb[0]; lo[2] = la[1]; lo[3] = lb[1];
+          };
           float na = 1.f, nb = 1.f;
           if (KB) {
             const __half* nm = reinterpret_cast<const __half*>(sp + z.off_kside);
@@ -145,24 +145,51 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
             nb = __half2float(nm[g + 8]);
           }
           const bool all = sight.all(t0, t0 + kTile - 1, p0, p1);
-#pragma unroll 1
-          for (int nt = 0; nt < (ONE ? 1 : tiles); ++nt) {
-            float s[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              const uint4 w = ONE ? wreg[ONE ? k : 0] : wfrag[(nt * KS + k) * 32 + lane];
-              mma_f16(s, hi[k], w.x, w.y);
-              mma_f16(small, hi[k], w.z, w.w);
-              if (KB) mma_f16(small, lo[KB ? k : 0], w.x, w.y);
-            }
+          float s[4], small[4];
+          auto multiply = [&](uint4 w, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
+            mma_f16(s, hi, w.x, w.y);
+            mma_f16(small, hi, w.z, w.w);
+            if (KB) mma_f16(small, lo, w.x, w.y);
+          };
+          auto add = [&](int nt) {  // the weights of the tile's rows
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float4 rc = rowc[8 * nt + 2 * c + j];
               const float pa = ex2(fmaf((s[j] + small[j]) * na, rc.x, rc.y)) * rc.z;
               const float pb = ex2(fmaf((s[2 + j] + small[2 + j]) * nb, rc.x, rc.y)) * rc.z;
-              const int pos = __float_as_int(rc.w);
-              if (all || sight.sees(t0 + g, pos)) sum[0] += pa;
-              if (all || sight.sees(t0 + g + 8, pos)) sum[1] += pb;
+              if (all) {
+                sum[0] += pa;
+                sum[1] += pb;
+              } else {
+                const int pos = __float_as_int(rc.w);
+                if (sight.sees(t0 + g, pos)) sum[0] += pa;
+                if (sight.sees(t0 + g + 8, pos)) sum[1] += pb;
+              }
+            }
+          };
+          auto zero = [&] {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = small[e] = 0.f;
+          };
+          if constexpr (ONE) {
+            zero();
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              uint32_t hi[4], lo[4];
+              operand(k, hi, lo);
+              multiply(wreg[k], hi, lo);
+            }
+            add(0);
+          } else {
+            uint32_t hi[KS][4], lo[KS][4];
+#pragma unroll
+            for (int k = 0; k < KS; ++k) operand(k, hi[k], lo[k]);
+#pragma unroll 1
+            for (int nt = 0; nt < tiles; ++nt) {
+              zero();
+#pragma unroll
+              for (int k = 0; k < KS; ++k) multiply(wfrag[(nt * KS + k) * 32 + lane], hi[k], lo[k]);
+              add(nt);
             }
           }
         }

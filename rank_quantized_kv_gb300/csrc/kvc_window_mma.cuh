@@ -7,7 +7,6 @@
 // token's packed row and decodes it into the registers where it is needed.
 #pragma once
 
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "kvc_codes.cuh"
@@ -19,11 +18,6 @@ namespace {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -43,17 +37,6 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// Two floats as bf16, x in the low half.
-__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -68,36 +51,64 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Centred codes 2 q and 2 q + 1 of a chunk of width w as fp16: 0x6400 | c is
-// 1024 + c exactly.
-__device__ __forceinline__ uint32_t centred_pair(uint2 b, int w, int q) {
-  const uint32_t sub = 0x64006400u | ((1u << (w - 1)) * 0x10001u);
-  if (w == 8) return sub_f16x2(__byte_perm(q < 2 ? b.x : b.y, 0x64646464u, q & 1 ? 0x5342 : 0x5140), sub);
-  const uint32_t mask = (1u << w) - 1u, x = b.x >> (2 * q * w);
-  return sub_f16x2((x & mask) | ((x << (16 - w)) & (mask << 16)) | 0x64006400u, sub);
+// Four 8 x 8 matrices of 16-bit values from shared memory, transposed: lane i gives the
+// address of row i % 8 of matrix i / 8.
+__device__ __forceinline__ void load_transposed(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
-// Byte e of two words, as the low bytes of 16-bit halves (the high bytes hold anything).
-template <int E>
-__device__ __forceinline__ uint32_t bytes_of(uint32_t a, uint32_t b) {
-  return __byte_perm(a, b, E | (E << 4) | ((4 + E) << 8) | ((4 + E) << 12));
+// The larger of two and three, NaN where one is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
 }
-// int8 values in the low bytes of the halves as bf16: 0x4300 | u is 128 + u for u of
-// 7 bits; the sign bit in its place makes 256 of the other 128.
-__device__ __forceinline__ uint32_t int8_bf16(uint32_t x) {
-  return sub_bf16x2((x & 0x007f007fu) | 0x43004300u, (x & 0x00800080u) | 0x43004300u);
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
-// Code e of width w of two chunks, centred, as bf16.
-__device__ __forceinline__ uint32_t centred_bf16(uint2 a, uint2 b, int w, int e) {
-  if (w == 8) {
-    const uint32_t x = e < 4 ? a.x : a.y, y = e < 4 ? b.x : b.y;
-    const uint32_t at = e & 3;
-    return int8_bf16(__byte_perm(x, y, at | (at << 4) | ((4 + at) << 8) | ((4 + at) << 12)) ^ 0x00800080u);
+
+// Codes as fp16: 0x6400 | c is 1024 + c exactly, less 1024 + the centre.
+constexpr uint32_t kMagic = 0x64006400u;
+
+// int8 values in the low bytes of the halves (the high bytes hold anything).
+__device__ __forceinline__ uint32_t int8_f16(uint32_t x) {
+  return sub_f16x2((x & 0x00ff00ffu) ^ (kMagic | 0x00800080u), kMagic | 0x00800080u);
+}
+
+// A chunk's width as the decoders use it: eight codes of w bits, of which b.x holds
+// the first four and, after split(), b.y the others in its low bits, at any width.
+struct Width {
+  uint32_t w, mask, centre;  // mask: in both halves; centre: 1024 + 2^(w-1), in both
+  __device__ void set(uint32_t entry) {
+    w = entry ? (entry >> 16) & 0xfu : 1u;
+    mask = ((1u << w) - 1u) * 0x10001u;
+    centre = kMagic | ((1u << (w - 1)) * 0x10001u);
   }
-  const uint32_t mask = (1u << w) - 1u;
-  return sub_bf16x2(((a.x >> (w * e)) & mask) | (((b.x >> (w * e)) & mask) << 16) | 0x43004300u,
-                    0x43004300u | ((1u << (w - 1)) * 0x10001u));
-}
+  __device__ uint2 split(uint2 b) const { return make_uint2(b.x, w == 8 ? b.y : b.x >> (4 * w & 31)); }
+  // Codes 2 q and 2 q + 1 of split bits, centred.
+  __device__ uint32_t pair(uint2 b, int q) const {
+    uint32_t x = q < 2 ? b.x : b.y;
+    if (q & 1) x >>= 2 * w;
+    const uint32_t lo = (x & (mask & 0xffffu)) | kMagic;
+    return sub_f16x2(((x << (16 - w)) & (mask & 0xffff0000u)) | lo, centre);
+  }
+  // Codes 2 q and 2 q + 1 of two tokens, split: one code of both, then the other.
+  __device__ void both(uint2 a, uint2 b, int q, uint32_t* first, uint32_t* second) const {
+    uint32_t x = q < 2 ? a.x : a.y, y = q < 2 ? b.x : b.y;
+    if (q & 1) {
+      x >>= 2 * w;
+      y >>= 2 * w;
+    }
+    const uint32_t z = __byte_perm(x, y, 0x5410);
+    *first = sub_f16x2((z & mask) | kMagic, centre);
+    *second = sub_f16x2(((z >> w) & mask) | kMagic, centre);
+  }
+};
 
 // ---------------------------------------------------------------- keys
 
@@ -118,8 +129,10 @@ struct Keys {
   // single ones at 4.
   static constexpr int kTable = !KB ? 0 : KB <= 3 ? (1 << (2 * KB)) * 32 * 8 : 16 * 32 * 4;
 
-  const unsigned char* tab;  // this lane's copy
-  uint32_t ent[KS / 2];      // uniform: the lane's chunks
+  const unsigned char* tab;  // the table
+  uint32_t lane_at;          // where this lane's copy starts in an entry
+  uint32_t off[KS / 2];      // uniform: first bytes of the lane's chunks, ~0 past the last
+  Width width[KS / 2];
 
   // The scale of the centroids: a power of two that brings the largest to [8, 16).
   static __device__ float table_scale(const Params& kp) {
@@ -152,19 +165,24 @@ struct Keys {
   }
 
   __device__ void begin(const unsigned char* table) {
-    tab = table + (threadIdx.x & 31) * (KB <= 3 ? 8 : 4);
+    tab = table;
+    lane_at = (threadIdx.x & 31) * (KB <= 3 ? 8 : 4);
   }
   // A job's basis (uniform keys).
   __device__ void basis(const Params& kp, int beta) {
     if (!KB)
 #pragma unroll
-      for (int s = 0; s < KS / 2; ++s) ent[s] = chunk_entry(kp, beta, 4 * s + (threadIdx.x & 3));
+      for (int s = 0; s < KS / 2; ++s) {
+        const uint32_t e = chunk_entry(kp, beta, 4 * s + (threadIdx.x & 3));
+        off[s] = e ? e & 0xffffu : ~0u;
+        width[s].set(e);
+      }
   }
   // The packed position of the first of the four codes that lane c has of step s.
   static __device__ int position(int s, int c) { return KB ? c * kCodes + 4 * s : 8 * (4 * (s / 2) + c) + 4 * (s & 1); }
 
   // What a lane holds of a token's row: the words of its codes (codebook).
-  struct Row { uint32_t w[kWords]; const unsigned char* at; };
+  struct Row { uint32_t w[kWords]; const unsigned char* rows; int at; };
   __device__ Row row(const unsigned char* rows, int token, int Pk) const {
     Row r;
     if (KB) {
@@ -186,7 +204,8 @@ struct Keys {
         r.w[0] = v.x; r.w[1 % kWords] = v.y;
       }
     } else {
-      r.at = rows + token * Pk;
+      r.rows = rows;
+      r.at = token * Pk;
     }
     return r;
   }
@@ -194,13 +213,12 @@ struct Keys {
   // hi[1] the others; their second pieces in lo.
   __device__ void step(const Row& r, int s, uint32_t (&hi)[2], uint32_t (&lo)[2]) const {
     if constexpr (KB == 0) {
-      const uint32_t e = ent[s / 2];
       hi[0] = hi[1] = 0u;
-      if (e) {
-        const int mis = (int)(reinterpret_cast<uintptr_t>(r.at) & 3), w = (int)((e >> 16) & 0xfu);
-        const uint2 b = bits_at(r.at - mis, mis + (int)(e & 0xffffu));
-        hi[0] = centred_pair(b, w, 2 * (s & 1));
-        hi[1] = centred_pair(b, w, 2 * (s & 1) + 1);
+      if (off[s / 2] != ~0u) {
+        const Width& w = width[s / 2];
+        const uint2 b = w.split(bits_at(r.rows, r.at + (int)off[s / 2]));
+        hi[0] = w.pair(b, 2 * (s & 1));
+        hi[1] = w.pair(b, 2 * (s & 1) + 1);
       }
       lo[0] = lo[1] = 0u;
     } else if constexpr (KB <= 3) {
@@ -213,7 +231,7 @@ struct Keys {
         if (off < 0) v = r.w[0] << -off;
         else if (sh + 2 * KB + 8 <= 32 || at + 1 >= kWords) v = r.w[at] >> sh;
         else v = __funnelshift_r(r.w[at], r.w[(at + 1) % kWords], sh);
-        const uint2 p = *reinterpret_cast<const uint2*>(tab + (v & mask));
+        const uint2 p = *reinterpret_cast<const uint2*>(tab + ((v & mask) | lane_at));
         hi[i] = p.x;
         lo[i] = p.y;
       }
@@ -221,8 +239,8 @@ struct Keys {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t x = r.w[s / 2] >> (16 * (s & 1) + 8 * i);  // two codes in the low byte
-        const uint32_t a = *reinterpret_cast<const uint32_t*>(tab + ((x & 15u) << 7));
-        const uint32_t b = *reinterpret_cast<const uint32_t*>(tab + ((x & 0xf0u) << 3));
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(tab + (((x & 15u) << 7) | lane_at));
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(tab + (((x & 0xf0u) << 3) | lane_at));
         hi[i] = __byte_perm(a, b, 0x5410);
         lo[i] = __byte_perm(a, b, 0x7632);
       }

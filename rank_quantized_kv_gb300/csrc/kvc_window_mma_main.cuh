@@ -9,11 +9,12 @@
 //   O[channel][row] += V[token][channel]^T P[token][row]
 // P goes from the layout of a result to that of an operand by movmatrix.
 //
-// Scores are exact to fp32's rounding (Keys); weights are bf16 pairs (16 bits at
-// least, fp32's range, so no value scale can overflow them); codes are exact.
-// The reference of a row moves only when a score exceeds it by 60 (in log2): bf16
-// and fp32 hold weights up to 2^127.  The row's constant c1 cancels in the softmax
-// and is left out.
+// Scores are exact to fp32's rounding (Keys), codes exact in fp16.  Weights times
+// value scales are two fp16 pieces (22 bits; 2^-25 of the reference at least).  The
+// reference of a row is its first maximum less 4 and moves only when a score exceeds
+// it by 8 (in log2); the value scales are divided by a power of two (sref) that moves
+// only when a scale exceeds it four times: weights stay below 2^10.  The row's
+// constant c1 cancels in the softmax and is left out.
 //
 // What bounds it: see window_mma_rows().
 #pragma once
@@ -28,12 +29,11 @@ namespace {
 
 constexpr int kMmaWarps = 8, kMmaThreads = kMmaWarps * 32;
 constexpr int kMmaTile = kWindowTile, kStages = 3;
-constexpr float kMove = 60.f;
+constexpr float kSet = 4.f, kMove = 8.f;
 
 // VK: head size of int8 values (64 or 128), 0 for uniform ones (up to 128 positions).
 template <int VK>
 struct Values {
-  static constexpr int kBytes = VK / 8;                // a lane's bytes of an int8 row
   static constexpr int kTiles = VK ? VK / 16 : 8;      // tiles of 16 channels
   static constexpr int kStride = VK + 16;              // rows in shared memory, no bank conflicts
   static constexpr bool kUniform = VK == 0;
@@ -80,29 +80,39 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
     const unsigned char* vbase = vp.store + vp.pay_off[slot];
     const unsigned char* vside = vp.store + vp.side_off[slot];
 
-    // copies of the tile numbered i into a stage: whole 16-byte pieces that hold rows
+    // Copies of the tile numbered i into a stage: whole 16-byte pieces that hold rows.
+    // Lanes 0, 1 take the keys' side words, 2, 3 the values'.
+    const unsigned char* klane = kbase + 16 * lane;
+    const unsigned char* vlane = vbase + 16 * lane;
+    const unsigned char* slane = (lane & 2 ? vside : kside) + 16 * (lane & 1);
+    const int sdst = (lane & 2 ? z.off_vside : z.off_kside) + 16 * (lane & 1);
+    const bool has_side = lane < 4 && (lane & 2 ? !V::kUniform : KB > 0);
+    constexpr int kRow = VK ? VK / 16 : 1;  // pieces of an int8 row
+    const int vdst = V::kUniform ? z.off_v + 16 * lane : z.off_v + lane / kRow * V::kStride + 16 * (lane % kRow);
     auto load = [&](int i, int st) {
       if (i < i1) {
-        const int64_t t0 = (int64_t)tiles.tile(i) * kMmaTile;
-        const int n = (int)min((int64_t)kMmaTile, t.S - t0);
+        const int t0 = tiles.tile(i) * kMmaTile;
         const uint32_t dst = ring_s + st * z.stage;
-        const unsigned char* src = kbase + t0 * Pk;
-        for (int e = lane; e < (n * Pk + 15) >> 4; e += 32) copy16(dst + 16 * e, src + 16 * e);
-        const int words = (2 * n + 15) >> 4;  // side words: 2 bytes a token
-        if (KB && lane < words) copy16(dst + z.off_kside + 16 * lane, kside + 2 * t0 + 16 * lane);
-        if (!V::kUniform) {
-          if (lane >= 2 && lane - 2 < words)
-            copy16(dst + z.off_vside + 16 * (lane - 2), vside + 2 * t0 + 16 * (lane - 2));
-          constexpr int kRow = VK ? VK / 16 : 1;  // pieces of a row
-          const unsigned char* vs = vbase + t0 * VK;
+        const int n = min(kMmaTile, t.S - t0);
+        const unsigned char* ks = klane + (int64_t)t0 * Pk;
+        if (KB && n == kMmaTile) {
+          constexpr int kPieces = 2 * KS * KB;
 #pragma unroll
-          for (int e = 0; e < kRow / 2; ++e) {
-            const int x = lane + 32 * e, row = x / kRow, piece = x - row * kRow;
-            if (row < n) copy16(dst + z.off_v + row * V::kStride + 16 * piece, vs + 16 * x);
-          }
+          for (int e = 0; e < (kPieces + 31) / 32; ++e)
+            if (32 * e + 32 <= kPieces || lane + 32 * e < kPieces) copy16(dst + 16 * lane + 512 * e, ks + 512 * e);
         } else {
-          const unsigned char* vs = vbase + t0 * Pv;
-          for (int e = lane; e < (n * Pv + 15) >> 4; e += 32) copy16(dst + z.off_v + 16 * e, vs + 16 * e);
+          for (int e = lane; e < (n * Pk + 15) >> 4; e += 32) copy16(dst + 16 * e, ks + 16 * (e - lane));
+        }
+        if (has_side && 8 * (lane & 1) < n) copy16(dst + sdst, slane + 2 * (int64_t)t0);  // 2 bytes a token
+        if (!V::kUniform) {
+          const unsigned char* vs = vlane + (int64_t)t0 * VK;
+#pragma unroll
+          for (int e = 0; e < kRow / 2; ++e)
+            if (n == kMmaTile || lane / kRow + 32 / kRow * e < n)
+              copy16(dst + vdst + 32 / kRow * e * V::kStride, vs + 512 * e);
+        } else {
+          const unsigned char* vs = vlane + (int64_t)t0 * Pv;
+          for (int e = lane; e < (n * Pv + 15) >> 4; e += 32) copy16(dst + z.off_v + 16 * e, vs + 16 * (e - lane));
         }
       }
       copy_commit();
@@ -161,11 +171,21 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
         for (int e = 0; e < 4; ++e) o[nt][m][e] = 0.f;
     }
     keys.basis(kp, kbeta);
-    uint32_t vent[V::kUniform ? 2 : 1];
-    if (V::kUniform) {
-      vent[0] = vch[g];
-      vent[V::kUniform ? 1 : 0] = vch[8 + g];
-    }
+    // uniform values: a lane has chunks g and 8 + g of a row
+    Width vwidth[V::kUniform ? 2 : 1];
+    int voff[V::kUniform ? 2 : 1];
+    if (V::kUniform)
+#pragma unroll
+      for (int e = 0; e < (V::kUniform ? 2 : 1); ++e) {
+        const uint32_t x = vch[8 * e + g];
+        vwidth[e].set(x);
+        voff[e] = x ? (int)(x & 0xffffu) : -1;
+      }
+    float sref = V::kUniform ? 1.f : 0.f, inv_sref = sref;
+    // tiles that all rows see whole: t0 >= see0 and t0 <= see1, and t0 > see2 or t0 < see3
+    const int see0 = sight.first, see1 = p0 - (kMmaTile - 1), see2 = p1 - sight.window,
+              see3 = sight.sink_end - (kMmaTile - 1);
+    const uint32_t vmat = (uint32_t)((lane & 15) * V::kStride + 16 * (lane >> 4));  // ldmatrix: this lane's row
 
     int st = 0;
     for (; i < i1; i += kMmaWarps) {
@@ -216,8 +236,19 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
       }
       // ---- softmax: x = s rs - m
       const int t0 = tiles.tile(i) * kMmaTile;
-      const bool all = sight.all(t0, t0 + kMmaTile - 1, p0, p1);
+      const bool all = t0 >= see0 && t0 <= see1 && (t0 > see2 || t0 < see3);
+      float va = 1.f, vb = 1.f;
+      if (!V::kUniform) {
+        const __half* vs = reinterpret_cast<const __half*>(sp + z.off_vside);
+        va = __half2float(vs[g]);
+        vb = __half2float(vs[g + 8]);
+      }
       uint32_t seen = ~0u;  // bit 4 nt + e
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], rs[nt][e & 1], negm[nt][e & 1]);
       if (!all) {
         seen = 0u;
 #pragma unroll
@@ -231,31 +262,57 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
               if (sight.sees(t0 + g + 8, pos)) seen |= 1u << (4 * nt + 2 + j);
             }
           }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(seen >> (4 * nt + e) & 1u)) x[nt][e] = -INFINITY;
       }
-      float x[NT][4];
-      bool move = false;
+      float top = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = fmaf(s[nt][e], rs[nt][e & 1], negm[nt][e & 1]);
-          x[nt][e] = all || (seen >> (4 * nt + e) & 1u) ? v : -INFINITY;
-          move |= !(x[nt][e] <= kMove);
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        top = max_nan(top, x[nt][0], x[nt][1]);
+        top = max_nan(top, x[nt][2], x[nt][3]);
+      }
+      bool move = !(top <= kMove);
+      if (!V::kUniform) move |= fmaxf(va, vb) > 4.f * sref;
       if (__any_sync(kFull, move)) {  // (a row's first token, too: its reference is -inf)
+        float ratio = 1.f;
+        if (!V::kUniform) {  // the value scales' reference: the next power of two
+          uint32_t any = 0u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) any |= seen >> (4 * nt);
+          float m = 0.f;
+          if ((any & 3u) && va > 4.f * sref && va <= 65504.f) m = va;
+          if ((any & 12u) && vb > 4.f * sref && vb <= 65504.f) m = fmaxf(m, vb);
+          m = warp_max(m);
+          if (m > 0.f) {
+            const float to = __int_as_float((__float_as_int(m) & 0x7f800000) + 0x00800000);
+            ratio = sref / to;
+            sref = to;
+            inv_sref = 1.f / to;
+          }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float va = s[nt][j] * rs[nt][j], vb = s[nt][2 + j] * rs[nt][j];
+            const float ya = s[nt][j] * rs[nt][j], yb = s[nt][2 + j] * rs[nt][j];
             const bool sa = seen >> (4 * nt + j) & 1u, sb = seen >> (4 * nt + 2 + j) & 1u;
-            float m = fmaxf(sa ? fmaxf(va, kWindowLowest) : -INFINITY, sb ? fmaxf(vb, kWindowLowest) : -INFINITY);
+            float m = fmaxf(sa ? fmaxf(ya, kWindowLowest) : -INFINITY, sb ? fmaxf(yb, kWindowLowest) : -INFINITY);
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-            const float old = -negm[nt][j], now = fmaxf(old, m);
-            const float f = now == -INFINITY ? 1.f : ex2(old - now);
+            const float old = -negm[nt][j];
+            float now = old, f = 1.f;
+            if (m != -INFINITY && (m - old > kMove || !(old > kWindowLowest))) {
+              // the first reference, or a new one (the lowest: scores of -inf alone so far)
+              now = m > kWindowLowest ? m - kSet : fmaxf(old, m);
+              f = ex2(old - now);
+              if (old == now) f = 1.f;
+            }
             l[nt][j] *= f;
+            f *= ratio;
 #pragma unroll
             for (int q = 0; q < MT; ++q) {
               o[nt][q][j] *= f;
@@ -266,81 +323,68 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
             x[nt][2 + j] = sb ? fmaf(s[nt][2 + j], rs[nt][j], -now) : -INFINITY;
           }
       }
-      uint32_t ph[NT][2], pl[NT][2];  // P as an operand, in two bf16 pieces
-      {
-        float va = 1.f, vb = 1.f;
-        if (!V::kUniform) {
-          const __half* vs = reinterpret_cast<const __half*>(sp + z.off_vside);
-          va = __half2float(vs[g]);
-          vb = __half2float(vs[g + 8]);
+      va *= inv_sref;
+      vb *= inv_sref;
+      uint32_t ph[NT][2], pl[NT][2];  // P as an operand, in two fp16 pieces
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = ex2(x[nt][e]);
+          l[nt][e & 1] += p[e];
+          if (!V::kUniform) p[e] *= e < 2 ? va : vb;
+        }
+        if (!V::kUniform && !all) {  // a hidden token's scale may be anything
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(seen >> (4 * nt + e) & 1u)) p[e] = 0.f;
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(x[nt][e]);
-            l[nt][e & 1] += p[e];
-            if (!V::kUniform) p[e] *= e < 2 ? va : vb;
-            // a hidden token's scale may be anything
-            if (!V::kUniform && !all && !(seen >> (4 * nt + e) & 1u)) p[e] = 0.f;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t hi = pack_bf16(p[2 * h], p[2 * h + 1]);
-            const uint32_t lo = pack_bf16(p[2 * h] - __uint_as_float(hi << 16),
-                                          p[2 * h + 1] - __uint_as_float(hi & 0xffff0000u));
-            ph[nt][h] = transpose8(hi);
-            pl[nt][h] = transpose8(lo);
-          }
+        for (int h = 0; h < 2; ++h) {
+          const __half2 hi = __floats2half2_rn(p[2 * h], p[2 * h + 1]);
+          const float2 back = __half22float2(hi);
+          ph[nt][h] = transpose8(*reinterpret_cast<const uint32_t*>(&hi));
+          pl[nt][h] = transpose8(pack_f16(p[2 * h] - back.x, p[2 * h + 1] - back.y));
         }
       }
       // ---- values: tokens 2 c, 2 c + 1 and 8 more are this lane's K indices
       auto product = [&](int m, const uint32_t (&a)[4]) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_bf16(o[nt][m], a, ph[nt][0], ph[nt][1]);
-          mma_bf16(o[nt][m], a, pl[nt][0], pl[nt][1]);
+          mma_f16(o[nt][m], a, ph[nt][0], ph[nt][1]);
+          mma_f16(o[nt][m], a, pl[nt][0], pl[nt][1]);
         }
       };
-      const unsigned char* vr = sp + z.off_v;
       if constexpr (!V::kUniform) {
-        constexpr int W = VK ? V::kBytes / 4 : 1;
-        uint32_t v[4][W];
+        // two bytes of a token make a 16-bit element: its low bytes are rows g of a
+        // tile of 16 channels, its high bytes rows g + 8
+        const uint32_t va0 = ring_s + st * z.stage + z.off_v + vmat;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const unsigned char* p = vr + (2 * c + (q & 1) + 8 * (q >> 1)) * V::kStride + g * V::kBytes;
-          if (W == 4) {
-            const uint4 y = *reinterpret_cast<const uint4*>(p);
-            v[q][0] = y.x; v[q][1 % W] = y.y; v[q][2 % W] = y.z; v[q][3 % W] = y.w;
-          } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(p);
-            v[q][0] = y.x; v[q][1 % W] = y.y;
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < W; ++q) {
-          const uint32_t a01[4] = {int8_bf16(bytes_of<0>(v[0][q], v[1][q])), int8_bf16(bytes_of<1>(v[0][q], v[1][q])),
-                                   int8_bf16(bytes_of<0>(v[2][q], v[3][q])), int8_bf16(bytes_of<1>(v[2][q], v[3][q]))};
-          product(2 * q, a01);
-          const uint32_t a23[4] = {int8_bf16(bytes_of<2>(v[0][q], v[1][q])), int8_bf16(bytes_of<3>(v[0][q], v[1][q])),
-                                   int8_bf16(bytes_of<2>(v[2][q], v[3][q])), int8_bf16(bytes_of<3>(v[2][q], v[3][q]))};
-          product(2 * q + 1, a23);
+        for (int q = 0; q < VK / 32; ++q) {
+          uint32_t v[4];
+          load_transposed(v, va0 + 32 * q);
+          const uint32_t a0[4] = {int8_f16(v[0]), int8_f16(v[0] >> 8), int8_f16(v[1]), int8_f16(v[1] >> 8)};
+          product(2 * q, a0);
+          const uint32_t a1[4] = {int8_f16(v[2]), int8_f16(v[2] >> 8), int8_f16(v[3]), int8_f16(v[3] >> 8)};
+          product(2 * q + 1, a1);
         }
       } else {
+        const unsigned char* vr = sp + z.off_v;
 #pragma unroll
         for (int set = 0; set < 2; ++set) {
           if (!vch[8 * set]) break;  // (the same for all lanes)
-          const uint32_t e = vent[V::kUniform ? set : 0];
+          const int e = V::kUniform ? set : 0;
           uint2 v[4];
-          const int w = e ? (int)((e >> 16) & 0xfu) : 1;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            v[q] = e ? bits_at(vr, (2 * c + (q & 1) + 8 * (q >> 1)) * Pv + (int)(e & 0xffffu)) : make_uint2(0u, 0u);
+            v[q] = voff[e] < 0 ? make_uint2(0u, 0u)
+                               : vwidth[e].split(bits_at(vr, (2 * c + (q & 1) + 8 * (q >> 1)) * Pv + voff[e]));
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const uint32_t a[4] = {centred_bf16(v[0], v[1], w, 2 * m), centred_bf16(v[0], v[1], w, 2 * m + 1),
-                                   centred_bf16(v[2], v[3], w, 2 * m), centred_bf16(v[2], v[3], w, 2 * m + 1)};
+            uint32_t a[4];
+            vwidth[e].both(v[0], v[1], m, &a[0], &a[1]);
+            vwidth[e].both(v[2], v[3], m, &a[2], &a[3]);
             product(4 * set + m, a);
           }
         }
@@ -396,9 +440,9 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               // channel of row g + 8 (e >> 1) of tile m
-              const int d = VK ? g * V::kBytes + 2 * m + (e >> 1)
+              const int d = VK ? 16 * m + 2 * g + (e >> 1)
                                : 8 * (8 * (m >> 2) + g) + 2 * (m & 3) + (e >> 1);
-              ob[warp * OW + d * 8 + 2 * c + (e & 1)] = o[n2][m][e] * f[n2][e & 1];
+              ob[warp * OW + d * 8 + 2 * c + (e & 1)] = o[n2][m][e] * (f[n2][e & 1] * sref);
             }
       __syncthreads();
       for (int e = tid; e < t.Dv * 8; e += kMmaThreads) {
