@@ -227,6 +227,7 @@ struct WindowArgs {
   int window = 0, sinks = 0;             // at most S each; window S: no limit
   int rows = 0, rt = 0, row_tiles = 0;   // rows of a slot, of a job; jobs of a slot
   int64_t tps = 0, total = 0;            // tiles of a job, of the line
+  int64_t wtps = 0;                      // tensor cores: tiles of a slot that the weights' pass walks
   int grid = 0, sms = 0;                 // CTAs of the main kernel; the device's SMs
   int mma = 0;                           // warp-level tensor cores: 8-row tiles of a job, 0: CUDA cores
   int NCk = 0, Dv = 0, Dvp = 0;          // packed positions; value channels, padded to 4

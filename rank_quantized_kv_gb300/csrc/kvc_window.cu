@@ -587,10 +587,10 @@ MainKernel main_kernel_for(int kmode, int vmode) {
                                    : window_main_kernel<KVC_MODE_CODEBOOK, KVC_MODE_INT8>;
 }
 
-// Tiles of `tile` tokens that a job of rt rows sees at most.
-int64_t most_tiles(const WindowArgs& t, int tile) {
+// Tiles of `tile` tokens that a job of `rows` rows sees at most.
+int64_t most_tiles(const WindowArgs& t, int tile, int rows) {
   const int64_t all = (t.S + tile - 1) / tile;
-  const int64_t span = (int64_t)t.window + (t.rt + t.rep - 1) / t.rep + 1;  // the window's tokens
+  const int64_t span = (int64_t)t.window + (rows + t.rep - 1) / t.rep + 1;  // the window's tokens
   return std::min<int64_t>(all, (span + tile - 1) / tile + 1 + (t.sinks ? (t.sinks + tile - 1) / tile + 1 : 0));
 }
 
@@ -640,7 +640,7 @@ size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool gener
   t.Dvp = (t.Dv + 3) / 4 * 4;
   t.c1_parts = (t.NCk + kPrepCols - 1) / kPrepCols;
   const int64_t jobs = (int64_t)kp.n_slots * t.row_tiles;
-  t.tps = most_tiles(t, t.mma ? kWindowTile : kTile);
+  t.tps = most_tiles(t, t.mma ? kWindowTile : kTile, t.rt);
   t.total = jobs * t.tps;
   // a warp of the tensor-core kernel takes a tile, of the CUDA cores a quarter
   const int64_t runs = t.mma ? std::max<int64_t>(t.total / 8, 1) : t.total;
@@ -651,6 +651,7 @@ size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool gener
 cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs t, void* workspace,
                                  cudaStream_t s, int* nk) {
   lay_out(kp, t, workspace);
+  t.wtps = t.decay == 1.f ? most_tiles(t, kWindowTile, t.rows) : (t.S + kWindowTile - 1) / kWindowTile;
   cudaError_t e;
   if (t.prod) {
     window_prep_prod_kernel<<<(unsigned)(kp.n_slots * t.rows), kThreads, 0, s>>>(kp, t);

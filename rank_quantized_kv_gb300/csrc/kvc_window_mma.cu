@@ -34,38 +34,37 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
   if (KB) K::fill(kp, smem, kThreads);
   K keys;
   keys.begin(smem);
-  const int64_t tps = (t.S + kTile - 1) / kTile, total = tps * kp.n_slots;
+  // the tiles that some row sees; all of them where the old weights are scaled
+  const bool every = t.decay != 1.f;
+  const int64_t tps = t.wtps, total = tps * kp.n_slots;
   const int64_t run1 = total * (blockIdx.x + 1) / gridDim.x;
   bool waited = false;
   for (int64_t at = total * blockIdx.x / gridDim.x; at < run1;) {
     const int slot = (int)(at / tps);
-    const int a0 = (int)(at - slot * tps), a1 = (int)min(tps, a0 + (run1 - at));
+    const int64_t a0 = at - slot * tps, a1 = min(tps, a0 + (run1 - at));
     at += a1 - a0;
     const int b = slot / kp.H, h = slot - b * kp.H, kbeta = kp.basis_of[slot], Pk = kp.P[kbeta];
     const unsigned char* kbase = kp.store + kp.pay_off[slot];
     const unsigned char* kside = kp.store + kp.side_off[slot];
     float* wout = t.weights + b * t.w_sb + h * t.w_sh;
     const Sight sight(t, b);
+    const Tiles<kTile> tiles_seen(sight, t.ctx, t.S - 1);
+    const int64_t count = every ? tps : tiles_seen.count();
+    const int i0 = (int)(count * a0 / tps), i1 = (int)(count * a1 / tps);
+    auto tile_of = [&](int i) { return every ? i : tiles_seen.tile(i); };
     keys.basis(kp, kbeta);
     for (int r0 = 0; r0 < t.rows; r0 += 8 * NT) {
       const int nr = min(8 * NT, t.rows - r0), tiles = (nr + 7) / 8;
       const int p0 = t.ctx + r0 / t.rep, p1 = t.ctx + (r0 + nr - 1) / t.rep;
       const float decay = r0 ? 1.f : t.decay;
-      // tiles that some row sees; all of them where the old weights are scaled
-      auto idle = [&](int tile) {
-        const int t0 = tile * kTile;
-        return t0 > p1 || t0 + kTile <= sight.first ||
-               (t0 + kTile <= p0 - sight.window + 1 && t0 >= sight.sink_end);
-      };
-      auto next = [&](int tile) {
-        if (decay == 1.f)
-          while (tile < a1 && idle(tile)) tile += kWarps;
-        return tile;
-      };
+      // tiles that no row of the chunk sees, and those that all see whole
+      const int last = p1, hidden = sight.first - kTile, gap0 = sight.sink_end, gap1 = p0 - sight.window + 1 - kTile;
+      const int see0 = sight.first, see1 = p0 - (kTile - 1), see2 = p1 - sight.window,
+                see3 = sight.sink_end - (kTile - 1);
       const unsigned char* klane = kbase + 16 * lane;
-      auto load = [&](int tile, int st) {
-        if (tile < a1) {
-          const int t0 = tile * kTile, n = min(kTile, t.S - t0);
+      auto load = [&](int i, int st) {
+        if (i < i1) {
+          const int t0 = tile_of(i) * kTile, n = min(kTile, t.S - t0);
           const uint32_t dst = ring_s + st * z.stage + 16 * lane;
           const unsigned char* ks = klane + (int64_t)t0 * Pk;
           if (KB && n == kTile) {
@@ -81,12 +80,9 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
         copy_commit();
       };
       __syncthreads();  // the last chunk's rows have been read
-      int tile = next(a0 + warp), ahead = tile;
+      int i = i0 + warp;
 #pragma unroll
-      for (int s = 0; s < kStages - 1; ++s) {
-        load(ahead, s);
-        ahead = next(ahead + kWarps);
-      }
+      for (int s = 0; s < kStages - 1; ++s) load(i + s * kWarps, s);
       if (!waited) grid_dependency_wait();
       waited = true;
       const float tab_inv = KB ? 1.f / K::table_scale(kp) : 1.f;
@@ -121,15 +117,18 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
         __syncthreads();
       }
       int st = 0;
-      while (tile < a1) {
+      for (; i < i1; i += kWarps) {
         copy_wait<kStages - 2>();
         __syncwarp();
         const unsigned char* sp = ring + st * z.stage;
-        load(ahead, st + kStages - 1 >= kStages ? st - 1 : st + kStages - 1);
-        ahead = next(ahead + kWarps);
-        const int t0 = tile * kTile;
+        load(i + (kStages - 1) * kWarps, st + kStages - 1 >= kStages ? st - 1 : st + kStages - 1);
+        const int t0 = tile_of(i) * kTile;
+        // lanes 0 and 1 of a quad write tokens g and g + 8: what is there, in time
+        const int tok = t0 + g + 8 * c;
+        const bool mine = c < 2 && tok < t.S;
+        const float old = mine && decay != 0.f ? wout[tok] : 0.f;
         float sum[2] = {0.f, 0.f};  // tokens g and g + 8
-        if (!idle(tile)) {
+        if (t0 <= last && t0 > hidden && (t0 > gap1 || t0 < gap0)) {
           const typename K::Row ra = keys.row(sp, g, Pk), rb = keys.row(sp, g + 8, Pk);
           auto operand = [&](int k, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
             uint32_t ha[2], la[2], hb[2], lb[2];
@@ -144,19 +143,21 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
             na = __half2float(nm[g]);
             nb = __half2float(nm[g + 8]);
           }
-          const bool all = sight.all(t0, t0 + kTile - 1, p0, p1);
-          float s[4], small[4];
+          const bool all = t0 >= see0 && t0 <= see1 && (t0 > see2 || t0 < see3);
+          float s[4], small[4], other[4];
           auto multiply = [&](uint4 w, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
             mma_f16(s, hi, w.x, w.y);
             mma_f16(small, hi, w.z, w.w);
-            if (KB) mma_f16(small, lo, w.x, w.y);
+            if (KB) mma_f16(other, lo, w.x, w.y);
           };
           auto add = [&](int nt) {  // the weights of the tile's rows
 #pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += KB ? small[e] + other[e] : small[e];
+#pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float4 rc = rowc[8 * nt + 2 * c + j];
-              const float pa = ex2(fmaf((s[j] + small[j]) * na, rc.x, rc.y)) * rc.z;
-              const float pb = ex2(fmaf((s[2 + j] + small[2 + j]) * nb, rc.x, rc.y)) * rc.z;
+              const float pa = ex2(fmaf(s[j] * na, rc.x, rc.y)) * rc.z;
+              const float pb = ex2(fmaf(s[2 + j] * nb, rc.x, rc.y)) * rc.z;
               if (all) {
                 sum[0] += pa;
                 sum[1] += pb;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
           };
           auto zero = [&] {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = small[e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[e] = small[e] = other[e] = 0.f;
           };
           if constexpr (ONE) {
             zero();
@@ -198,13 +199,8 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
           sum[j] += __shfl_xor_sync(kFull, sum[j], 1);
           sum[j] += __shfl_xor_sync(kFull, sum[j], 2);
         }
-        const int tok = t0 + g + 8 * (c & 1);
-        const float add = c & 1 ? sum[1] : sum[0];
-        if (c < 2 && tok < t.S) {
-          if (decay == 0.f) wout[tok] = add;
-          else if (decay != 1.f || add != 0.f) wout[tok] = fmaf(decay, wout[tok], add);
-        }
-        tile = next(tile + kWarps);
+        const float add = c ? sum[1] : sum[0];
+        if (mine && (decay != 1.f || add != 0.f)) wout[tok] = fmaf(decay, old, add);
         if (++st == kStages) st = 0;
       }
       copy_wait<0>();
@@ -293,7 +289,7 @@ cudaError_t launch_window_weights_mma(const Params& kp, const WindowArgs& t, cud
   const int smem = lay_out(kp, nullptr, t, tables, &z);
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
-  const int64_t total = (t.S + kTile - 1) / kTile * (int64_t)kp.n_slots;
+  const int64_t total = t.wtps * kp.n_slots;
   const int grid = (int)std::min<int64_t>(std::max<int64_t>(total / kWarps, 1), (one ? 2 : 1) * (int64_t)t.sms);
   ++*nk;
   return launch_dependent(k, (unsigned)grid, kThreads, (size_t)smem, s, kp, t, z);

@@ -125,8 +125,10 @@ struct Keys {
   static constexpr int kPieces = KB ? 2 : 1;            // of A
   static constexpr int kCodes = 4 * KS;                 // a lane's codes of a token
   static constexpr int kWords = KB ? (kCodes * KB + 31) / 32 : 1;
-  // Pairs of centroids, both pieces, once per lane (no bank conflicts), up to 3 bits;
-  // single ones at 4.
+  // Pairs of centroids once per lane (no bank conflicts), up to 3 bits: the first
+  // pieces, then the second ones, so that each is loaded into its place in an operand;
+  // at 4 bits single ones, both pieces in a word.
+  static constexpr int kHalf = KB && KB <= 3 ? (1 << (2 * KB)) * 32 * 4 : 0;
   static constexpr int kTable = !KB ? 0 : KB <= 3 ? (1 << (2 * KB)) * 32 * 8 : 16 * 32 * 4;
 
   const unsigned char* tab;  // the table
@@ -141,7 +143,7 @@ struct Keys {
     const int e = ((__float_as_int(big) >> 23) & 0xff) - 127;  // big in [2^e, 2^(e + 1))
     return __int_as_float((min(126, max(-126, 3 - e)) + 127) << 23);
   }
-  // Fill the table (all threads).  A lane reads entry x at x * 256 (KB <= 3) or x * 128.
+  // Fill the table (all threads).  A lane reads entry x at x * 128.
   static __device__ void fill(const Params& kp, unsigned char* table, int threads) {
     const float mul = table_scale(kp);
     auto pieces = [&](int c, uint32_t* hi, uint32_t* lo) {
@@ -151,13 +153,14 @@ struct Keys {
       *lo = __half_as_ushort(__float2half_rn(v - __half2float(h)));
     };
     constexpr int lm = KB ? (1 << KB) - 1 : 0;
-    for (int i = threadIdx.x; i < kTable / (KB <= 3 ? 8 : 4); i += threads) {
+    for (int i = threadIdx.x; i < (kHalf ? kHalf : kTable) / 4; i += threads) {
       const int x = i >> 5;
       uint32_t h0, l0, h1, l1;
       pieces(x & lm, &h0, &l0);
       if (KB <= 3) {
         pieces(x >> KB, &h1, &l1);
-        reinterpret_cast<uint2*>(table)[i] = make_uint2(h0 | (h1 << 16), l0 | (l1 << 16));
+        reinterpret_cast<uint32_t*>(table)[i] = h0 | (h1 << 16);
+        reinterpret_cast<uint32_t*>(table + kHalf)[i] = l0 | (l1 << 16);
       } else {
         reinterpret_cast<uint32_t*>(table)[i] = h0 | (l0 << 16);
       }
@@ -166,7 +169,7 @@ struct Keys {
 
   __device__ void begin(const unsigned char* table) {
     tab = table;
-    lane_at = (threadIdx.x & 31) * (KB <= 3 ? 8 : 4);
+    lane_at = (threadIdx.x & 31) * 4;
   }
   // A job's basis (uniform keys).
   __device__ void basis(const Params& kp, int beta) {
@@ -224,16 +227,16 @@ struct Keys {
     } else if constexpr (KB <= 3) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        // the pair's field (2 KB bits) shifted to bit 8: a table offset
-        constexpr uint32_t mask = ((1u << (2 * KB)) - 1u) << 8;
-        const int off = KB * (4 * s + 2 * i) - 8, at = off >> 5, sh = off & 31;
+        // the pair's field (2 KB bits) shifted to bit 7: a table offset
+        constexpr uint32_t mask = ((1u << (2 * KB)) - 1u) << 7;
+        const int off = KB * (4 * s + 2 * i) - 7, at = off >> 5, sh = off & 31;
         uint32_t v;
         if (off < 0) v = r.w[0] << -off;
-        else if (sh + 2 * KB + 8 <= 32 || at + 1 >= kWords) v = r.w[at] >> sh;
+        else if (sh + 2 * KB + 7 <= 32 || at + 1 >= kWords) v = r.w[at] >> sh;
         else v = __funnelshift_r(r.w[at], r.w[(at + 1) % kWords], sh);
-        const uint2 p = *reinterpret_cast<const uint2*>(tab + ((v & mask) | lane_at));
-        hi[i] = p.x;
-        lo[i] = p.y;
+        const unsigned char* p = tab + ((v & mask) | lane_at);
+        hi[i] = *reinterpret_cast<const uint32_t*>(p);
+        lo[i] = *reinterpret_cast<const uint32_t*>(p + kHalf);
       }
     } else {
 #pragma unroll

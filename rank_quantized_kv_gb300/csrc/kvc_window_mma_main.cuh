@@ -201,11 +201,11 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
       float s[NT][4];
       {
         const typename K::Row ra = keys.row(sp, g, Pk), rb = keys.row(sp, g + 8, Pk);
-        float small[NT][4];
+        float small[NT][4], other[NT][4];  // (sums apart: shorter chains)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] = small[nt][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[nt][e] = small[nt][e] = other[nt][e] = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           uint32_t ha[2], la[2], hb[2], lb[2];
@@ -217,13 +217,13 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
             const uint4 w = WREG ? wreg[WREG ? k : 0] : wfrag[(k * NT + nt) * 32 + lane];
             mma_f16(s[nt], hi, w.x, w.y);
             mma_f16(small[nt], hi, w.z, w.w);
-            if (KB) mma_f16(small[nt], lo, w.x, w.y);
+            if (KB) mma_f16(other[nt], lo, w.x, w.y);
           }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] += small[nt][e];
+          for (int e = 0; e < 4; ++e) s[nt][e] += KB ? small[nt][e] + other[nt][e] : small[nt][e];
       }
       if (KB) {  // norms
         const __half* nm = reinterpret_cast<const __half*>(sp + z.off_kside);
