@@ -257,8 +257,10 @@ size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool gener
 cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs t, void* workspace,
                                  cudaStream_t s, int* nk);
 using WindowKernel = void (*)(const Params, const Params, const WindowArgs, const WindowShape);
-// The kernel for these layers and jobs of 8, 16 or 32 rows, null where there is none,
-// and the bytes of its tables in shared memory (kvc_window_mma1.cu, 2 and 4).
+// The kernel for these layers and jobs of at most 4, of 8, 16 or 32 rows, null where
+// there is none, and the bytes of its tables in shared memory (kvc_window_mma0.cu, 1, 2
+// and 4).
+WindowKernel window_kernel_4(const Params& kp, const Params& vp, int NCk, int* tables);
 WindowKernel window_kernel_8(const Params& kp, const Params& vp, int NCk, int* tables);
 WindowKernel window_kernel_16(const Params& kp, const Params& vp, int NCk, int* tables);
 WindowKernel window_kernel_32(const Params& kp, const Params& vp, int NCk, int* tables);

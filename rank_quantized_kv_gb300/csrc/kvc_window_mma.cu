@@ -15,19 +15,21 @@ constexpr int kChunkTiles = 16;  // 8-row tiles whose weights are in shared memo
 
 // The weights that the tokens of a slot receive: the scores again, p = 2^(s - m) / l.
 // A warp decodes the keys of 16 tokens into operand registers once and meets all rows
-// of a chunk with them, whose weights lie in shared memory (ONE: 8 rows at most, in
-// registers); a token's sums stay in two registers of four lanes.  CTAs take runs of
+// of a chunk with them, whose weights lie in shared memory (ROWS 8 or 4: that many at
+// most, in registers, as in the main kernel); a token's sums stay in two registers of four lanes.  CTAs take runs of
 // the slots' tiles.  Where there are more rows than a chunk the keys are decoded again
 // for the next one, by the same warp, which then adds to what it wrote.
-template <int KB, int KS, bool ONE>
-__global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
+template <int KB, int KS, int ROWS>
+__global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
     window_weights_mma_kernel(const Params kp, const WindowArgs t, const WindowShape z) {
   using K = Keys<KB, KS>;
+  constexpr bool ONE = ROWS != 0, HALF = ROWS == 4;
   constexpr int NT = ONE ? 1 : kChunkTiles;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(16) float4 rowc[8 * NT];  // per row: score factor, -m, 1 / l, position
   __shared__ float row_mul[8 * NT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int cr = HALF ? 2 * (c & 1) : 2 * c;
   uint4* wfrag = reinterpret_cast<uint4*>(smem + K::kTable);  // [NT][step][32], unless in registers
   unsigned char* ring = smem + z.off_ring + warp * kStages * z.stage;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
@@ -103,15 +105,19 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
       }
       __syncthreads();
       auto fragment = [&](int s, int nt) {
-        const int r = 8 * nt + g, j = K::position(s, c);
+        const int r = HALF ? g & 3 : 8 * nt + g, j = K::position(s, c);
         float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < nr && j < t.NCk) w = *reinterpret_cast<const float4*>(w0 + (size_t)r * t.NCk + j);
         return weight_pieces(w, row_mul[r]);
       };
-      uint4 wreg[ONE ? KS : 1];
-      if (ONE) {
+      uint4 wreg[ONE && !HALF ? KS : 1];
+      uint2 whalf[HALF ? KS : 1];
+      if (HALF) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) wreg[ONE ? s : 0] = fragment(s, 0);
+        for (int s = 0; s < KS; ++s) whalf[HALF ? s : 0] = one_piece(fragment(s, 0), g >= 4);
+      } else if (ONE) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) wreg[ONE && !HALF ? s : 0] = fragment(s, 0);
       } else {
         for (int e = warp; e < KS * tiles; e += kWarps) wfrag[e * 32 + lane] = fragment(e % KS, e / KS);
         __syncthreads();
@@ -152,10 +158,17 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
           };
           auto add = [&](int nt) {  // the weights of the tile's rows
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] += KB ? small[e] + other[e] : small[e];
+            for (int e = 0; e < 4; ++e) {
+              if (HALF) {
+                if (KB) s[e] += other[e];
+                s[e] += __shfl_xor_sync(kFull, s[e], 2);
+              } else {
+                s[e] += KB ? small[e] + other[e] : small[e];
+              }
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float4 rc = rowc[8 * nt + 2 * c + j];
+              const float4 rc = rowc[8 * nt + cr + j];
               const float pa = ex2(fmaf(s[j] * na, rc.x, rc.y)) * rc.z;
               const float pb = ex2(fmaf(s[2 + j] * nb, rc.x, rc.y)) * rc.z;
               if (all) {
@@ -178,7 +191,13 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
             for (int k = 0; k < KS; ++k) {
               uint32_t hi[4], lo[4];
               operand(k, hi, lo);
-              multiply(wreg[k], hi, lo);
+              if (HALF) {
+                const uint2 w = whalf[HALF ? k : 0];
+                mma_f16(s, hi, w.x, w.y);
+                if (KB) mma_f16(other, lo, w.x, w.y);
+              } else {
+                multiply(wreg[ONE && !HALF ? k : 0], hi, lo);
+              }
             }
             add(0);
           } else {
@@ -197,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           sum[j] += __shfl_xor_sync(kFull, sum[j], 1);
-          sum[j] += __shfl_xor_sync(kFull, sum[j], 2);
+          if (!HALF) sum[j] += __shfl_xor_sync(kFull, sum[j], 2);
         }
         const float add = c ? sum[1] : sum[0];
         if (mine && (decay != 1.f || add != 0.f)) wout[tok] = fmaf(decay, old, add);
@@ -210,29 +229,30 @@ __global__ void __launch_bounds__(kThreads, ONE ? 2 : 1)
 
 using WeightsKernel = void (*)(const Params, const WindowArgs, const WindowShape);
 
-template <bool ONE>
+template <int ROWS>
 WeightsKernel weights_kernel_for(const Params& kp, int NCk, int* tables) {
   auto of = [&](auto keys, WeightsKernel k) {
     using K = decltype(keys);
-    *tables = K::kTable + (ONE ? 0 : K::kSteps * kChunkTiles * 512);
+    *tables = K::kTable + (ROWS ? 0 : K::kSteps * kChunkTiles * 512);
     return k;
   };
   if (kp.mode == KVC_MODE_UNIFORM) {
-    if (NCk <= 64) return of(Keys<0, 4>{}, window_weights_mma_kernel<0, 4, ONE>);
-    return of(Keys<0, 8>{}, window_weights_mma_kernel<0, 8, ONE>);
+    if (NCk <= 64) return of(Keys<0, 4>{}, window_weights_mma_kernel<0, 4, ROWS>);
+    return of(Keys<0, 8>{}, window_weights_mma_kernel<0, 8, ROWS>);
   }
   switch (kp.cb_bits * 1000 + kp.D) {
-    case 2064: return of(Keys<2, 4>{}, window_weights_mma_kernel<2, 4, ONE>);
-    case 3064: return of(Keys<3, 4>{}, window_weights_mma_kernel<3, 4, ONE>);
-    case 4064: return of(Keys<4, 4>{}, window_weights_mma_kernel<4, 4, ONE>);
-    case 2128: return of(Keys<2, 8>{}, window_weights_mma_kernel<2, 8, ONE>);
-    case 3128: return of(Keys<3, 8>{}, window_weights_mma_kernel<3, 8, ONE>);
-    default: return of(Keys<4, 8>{}, window_weights_mma_kernel<4, 8, ONE>);
+    case 2064: return of(Keys<2, 4>{}, window_weights_mma_kernel<2, 4, ROWS>);
+    case 3064: return of(Keys<3, 4>{}, window_weights_mma_kernel<3, 4, ROWS>);
+    case 4064: return of(Keys<4, 4>{}, window_weights_mma_kernel<4, 4, ROWS>);
+    case 2128: return of(Keys<2, 8>{}, window_weights_mma_kernel<2, 8, ROWS>);
+    case 3128: return of(Keys<3, 8>{}, window_weights_mma_kernel<3, 8, ROWS>);
+    default: return of(Keys<4, 8>{}, window_weights_mma_kernel<4, 8, ROWS>);
   }
 }
 
-WindowKernel main_kernel(const Params& kp, const Params& vp, int NCk, int nt, int* tables) {
-  return nt == 1   ? window_kernel_8(kp, vp, NCk, tables)
+WindowKernel main_kernel(const Params& kp, const Params& vp, int rows, int NCk, int nt, int* tables) {
+  return rows <= 4 ? window_kernel_4(kp, vp, NCk, tables)
+         : nt == 1 ? window_kernel_8(kp, vp, NCk, tables)
          : nt == 2 ? window_kernel_16(kp, vp, NCk, tables)
                    : window_kernel_32(kp, vp, NCk, tables);
 }
@@ -262,7 +282,7 @@ int window_mma_ctas(const Params& kp, const Params& vp, const WindowArgs& t, int
   if (kp.prod || kp.D > 128) return 0;
   if (vp.mode == KVC_MODE_UNIFORM ? t.Dv > 128 : vp.D != 64 && vp.D != 128) return 0;
   int tables = 0;
-  const WindowKernel k = main_kernel(kp, vp, t.NCk, nt, &tables);
+  const WindowKernel k = main_kernel(kp, vp, t.rows, t.NCk, nt, &tables);
   if (!k) return 0;
   WindowShape z;
   const int smem = lay_out(kp, &vp, t, tables, &z);
@@ -272,7 +292,7 @@ int window_mma_ctas(const Params& kp, const Params& vp, const WindowArgs& t, int
 
 cudaError_t launch_window_mma(const Params& kp, const Params& vp, const WindowArgs& t, cudaStream_t s, int* nk) {
   int tables = 0;
-  const WindowKernel k = main_kernel(kp, vp, t.NCk, t.mma, &tables);
+  const WindowKernel k = main_kernel(kp, vp, t.rows, t.NCk, t.mma, &tables);
   WindowShape z;
   const int smem = lay_out(kp, &vp, t, tables, &z);
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);
@@ -284,7 +304,9 @@ cudaError_t launch_window_mma(const Params& kp, const Params& vp, const WindowAr
 cudaError_t launch_window_weights_mma(const Params& kp, const WindowArgs& t, cudaStream_t s, int* nk) {
   int tables = 0;
   const bool one = t.rows <= 8;
-  const WeightsKernel k = one ? weights_kernel_for<true>(kp, t.NCk, &tables) : weights_kernel_for<false>(kp, t.NCk, &tables);
+  const WeightsKernel k = t.rows <= 4 ? weights_kernel_for<4>(kp, t.NCk, &tables)
+                          : one       ? weights_kernel_for<8>(kp, t.NCk, &tables)
+                                      : weights_kernel_for<0>(kp, t.NCk, &tables);
   WindowShape z;
   const int smem = lay_out(kp, nullptr, t, tables, &z);
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);

@@ -268,6 +268,9 @@ __device__ __forceinline__ uint4 weight_pieces(float4 w, float scale) {
                     pack_f16(w.x - f0.x, w.y - f0.y), pack_f16(w.z - f1.x, w.w - f1.y));
 }
 
+// Of four weights' pieces the large or the small ones.
+__device__ __forceinline__ uint2 one_piece(uint4 w, bool small) { return small ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y); }
+
 }  // namespace
 
 }  // namespace kvc

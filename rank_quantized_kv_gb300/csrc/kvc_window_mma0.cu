@@ -1,0 +1,11 @@
+// The windowed attention's tensor-core kernels for at most four rows (a file of its own, to
+// compile beside the others).
+#include "kvc_window_mma_main.cuh"
+
+namespace kvc {
+
+WindowKernel window_kernel_4(const Params& kp, const Params& vp, int NCk, int* tables) {
+  return mma_kernel_for<1, true>(kp, vp, NCk, tables);
+}
+
+}  // namespace kvc

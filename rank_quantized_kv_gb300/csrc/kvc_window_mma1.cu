@@ -5,7 +5,7 @@
 namespace kvc {
 
 WindowKernel window_kernel_8(const Params& kp, const Params& vp, int NCk, int* tables) {
-  return mma_kernel_for<1>(kp, vp, NCk, tables);
+  return mma_kernel_for<1, false>(kp, vp, NCk, tables);
 }
 
 }  // namespace kvc

@@ -16,7 +16,11 @@
 // only when a scale exceeds it four times: weights stay below 2^10.  The row's
 // constant c1 cancels in the softmax and is left out.
 //
-// What bounds it: see window_mma_rows().
+// At most four rows (HALF) fill half of the N side: the other half takes the second
+// pieces, the weights' in one product and P's in the other, and sums meet by a shuffle
+// or at the end.
+//
+// What bounds it: see window_mma_ctas().
 #pragma once
 
 #include "kvc_launch.cuh"
@@ -39,7 +43,7 @@ struct Values {
   static constexpr bool kUniform = VK == 0;
 };
 
-template <int KB, int KS, int VK, int NT>
+template <int KB, int KS, int VK, int NT, bool HALF>
 __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
     window_mma_kernel(const Params kp, const Params vp, const WindowArgs t, const WindowShape z) {
   using K = Keys<KB, KS>;
@@ -47,11 +51,13 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
   constexpr int R = 8 * NT;
   constexpr bool WREG = NT == 1;  // weights in registers, else in shared memory
   constexpr int MT = V::kTiles;
+  static_assert(!HALF || NT == 1, "half a tile of rows");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float row_mul[R], row_inv[R];    // 2^x that a row's weights were multiplied by
   __shared__ float wm[kMmaWarps][R], wl[kMmaWarps][R];
   __shared__ uint32_t vch[16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int cr = HALF ? 2 * (c & 1) : 2 * c;  // this lane's rows of a result: cr and cr + 1
   unsigned char* table = smem;
   uint4* wfrag = reinterpret_cast<uint4*>(smem + K::kTable);  // [step][NT][32], unless in registers
   unsigned char* ring = smem + z.off_ring + warp * kStages * z.stage;
@@ -142,15 +148,19 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
     if (V::kUniform && tid < 16) vch[tid] = chunk_entry(vp, vbeta, tid);
     __syncthreads();
     auto fragment = [&](int s, int nt) {
-      const int r = 8 * nt + g, j = K::position(s, c);
+      const int r = HALF ? g & 3 : 8 * nt + g, j = K::position(s, c);
       float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < nr && j < t.NCk) w = *reinterpret_cast<const float4*>(w0 + (size_t)r * t.NCk + j);
       return weight_pieces(w, row_mul[r]);
     };
-    uint4 wreg[WREG ? KS : 1];
-    if (WREG) {
+    uint4 wreg[WREG && !HALF ? KS : 1];
+    uint2 whalf[HALF ? KS : 1];
+    if (HALF) {
 #pragma unroll
-      for (int s = 0; s < KS; ++s) wreg[WREG ? s : 0] = fragment(s, 0);
+      for (int s = 0; s < KS; ++s) whalf[HALF ? s : 0] = one_piece(fragment(s, 0), g >= 4);
+    } else if (WREG) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) wreg[WREG && !HALF ? s : 0] = fragment(s, 0);
     } else {
       for (int e = warp; e < KS * NT; e += kMmaWarps) wfrag[e * 32 + lane] = fragment(e / NT, e % NT);
       __syncthreads();
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        rs[nt][j] = row_inv[8 * nt + 2 * c + j] * tab_inv;
+        rs[nt][j] = row_inv[8 * nt + cr + j] * tab_inv;
         negm[nt][j] = INFINITY;  // the reference is -inf: nothing seen
         l[nt][j] = 0.f;
       }
@@ -214,7 +224,13 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
           const uint32_t hi[4] = {ha[0], hb[0], ha[1], hb[1]}, lo[4] = {la[0], lb[0], la[1], lb[1]};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint4 w = WREG ? wreg[WREG ? k : 0] : wfrag[(k * NT + nt) * 32 + lane];
+            if (HALF) {
+              const uint2 w = whalf[HALF ? k : 0];
+              mma_f16(s[nt], hi, w.x, w.y);
+              if (KB) mma_f16(small[nt], lo, w.x, w.y);
+              continue;
+            }
+            const uint4 w = WREG ? wreg[WREG && !HALF ? k : 0] : wfrag[(k * NT + nt) * 32 + lane];
             mma_f16(s[nt], hi, w.x, w.y);
             mma_f16(small[nt], hi, w.z, w.w);
             if (KB) mma_f16(other[nt], lo, w.x, w.y);
@@ -223,7 +239,14 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] += KB ? small[nt][e] + other[nt][e] : small[nt][e];
+          for (int e = 0; e < 4; ++e) {
+            if (HALF) {
+              if (KB) s[nt][e] += small[nt][e];
+              s[nt][e] += __shfl_xor_sync(kFull, s[nt][e], 2);  // the weights' second pieces
+            } else {
+              s[nt][e] += KB ? small[nt][e] + other[nt][e] : small[nt][e];
+            }
+          }
       }
       if (KB) {  // norms
         const __half* nm = reinterpret_cast<const __half*>(sp + z.off_kside);
@@ -255,7 +278,7 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int r = r0 + 8 * nt + 2 * c + j;
+            const int r = r0 + 8 * nt + cr + j;
             const int pos = t.ctx + r / t.rep;
             if (r < t.rows) {
               if (sight.sees(t0 + g, pos)) seen |= 1u << (4 * nt + j);
@@ -344,8 +367,14 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
         for (int h = 0; h < 2; ++h) {
           const __half2 hi = __floats2half2_rn(p[2 * h], p[2 * h + 1]);
           const float2 back = __half22float2(hi);
-          ph[nt][h] = transpose8(*reinterpret_cast<const uint32_t*>(&hi));
-          pl[nt][h] = transpose8(pack_f16(p[2 * h] - back.x, p[2 * h + 1] - back.y));
+          const uint32_t large = *reinterpret_cast<const uint32_t*>(&hi);
+          const uint32_t rest = pack_f16(p[2 * h] - back.x, p[2 * h + 1] - back.y);
+          if (HALF) {
+            ph[nt][h] = transpose8(c < 2 ? large : rest);
+          } else {
+            ph[nt][h] = transpose8(large);
+            pl[nt][h] = transpose8(rest);
+          }
         }
       }
       // ---- values: tokens 2 c, 2 c + 1 and 8 more are this lane's K indices
@@ -353,7 +382,7 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_f16(o[nt][m], a, ph[nt][0], ph[nt][1]);
-          mma_f16(o[nt][m], a, pl[nt][0], pl[nt][1]);
+          if (!HALF) mma_f16(o[nt][m], a, pl[nt][0], pl[nt][1]);
         }
       };
       if constexpr (!V::kUniform) {
@@ -402,9 +431,9 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
         v += __shfl_xor_sync(kFull, v, 4);
         v += __shfl_xor_sync(kFull, v, 8);
         v += __shfl_xor_sync(kFull, v, 16);
-        if (g == 0) {
-          wm[warp][8 * nt + 2 * c + j] = -negm[nt][j];
-          wl[warp][8 * nt + 2 * c + j] = v;
+        if (g == 0 && (!HALF || c < 2)) {
+          wm[warp][8 * nt + cr + j] = -negm[nt][j];
+          wl[warp][8 * nt + cr + j] = v;
         }
       }
     __syncthreads();
@@ -414,13 +443,13 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int r = 8 * nt + 2 * c + j;
+        const int r = 8 * nt + cr + j;
         float M = -INFINITY;
         for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, wm[w][r]);
         // (a warp that summed nothing has l = 0)
         f[nt][j] = wl[warp][r] == 0.f ? 0.f : ex2(wm[warp][r] - M);
       }
-    if (tid < R) {
+    if (tid < (HALF ? 4 : R)) {
       float M = -INFINITY, L = 0.f;
       for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, wm[w][tid]);
       for (int w = 0; w < kMmaWarps; ++w)
@@ -449,6 +478,11 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kMmaWarps; ++w) v += ob[w * OW + e];
+        if (HALF) {
+          if (e & 4) continue;
+#pragma unroll
+          for (int w = 0; w < kMmaWarps; ++w) v += ob[w * OW + e + 4];
+        }
         t.part[(part * t.Dvp + (e >> 3)) * R + 8 * nt + (e & 7)] = v;
       }
     }
@@ -456,19 +490,19 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
   grid_dependents_launch();
 }
 
-template <int KB, int KS, int NT>
+template <int KB, int KS, int NT, bool HALF>
 WindowKernel mma_kernel_for_values(bool uniform, int D) {
-  if (uniform) return window_mma_kernel<KB, KS, 0, NT>;
+  if (uniform) return window_mma_kernel<KB, KS, 0, NT, HALF>;
   if constexpr (KB == 0 || KS == 4)
-    if (D == 64) return window_mma_kernel<KB, KS, 64, NT>;
+    if (D == 64) return window_mma_kernel<KB, KS, 64, NT, HALF>;
   if constexpr (KB == 0 || KS == 8)
-    if (D == 128) return window_mma_kernel<KB, KS, 128, NT>;
+    if (D == 128) return window_mma_kernel<KB, KS, 128, NT, HALF>;
   return nullptr;
 }
 
 // The kernel for these layers, null where there is none, and the bytes of its table
 // and weights in shared memory.
-template <int NT>
+template <int NT, bool HALF>
 WindowKernel mma_kernel_for(const Params& kp, const Params& vp, int NCk, int* tables) {
   const bool vu = vp.mode == KVC_MODE_UNIFORM;
   const int D = kp.D;
@@ -478,17 +512,17 @@ WindowKernel mma_kernel_for(const Params& kp, const Params& vp, int NCk, int* ta
     return k;
   };
   if (kp.mode == KVC_MODE_UNIFORM) {
-    if (NCk <= 64) return of(Keys<0, 4>{}, mma_kernel_for_values<0, 4, NT>(vu, D));
-    if (NCk <= 128) return of(Keys<0, 8>{}, mma_kernel_for_values<0, 8, NT>(vu, D));
+    if (NCk <= 64) return of(Keys<0, 4>{}, mma_kernel_for_values<0, 4, NT, HALF>(vu, D));
+    if (NCk <= 128) return of(Keys<0, 8>{}, mma_kernel_for_values<0, 8, NT, HALF>(vu, D));
     return nullptr;
   }
   switch (kp.cb_bits * 1000 + D) {
-    case 2064: return of(Keys<2, 4>{}, mma_kernel_for_values<2, 4, NT>(vu, D));
-    case 3064: return of(Keys<3, 4>{}, mma_kernel_for_values<3, 4, NT>(vu, D));
-    case 4064: return of(Keys<4, 4>{}, mma_kernel_for_values<4, 4, NT>(vu, D));
-    case 2128: return of(Keys<2, 8>{}, mma_kernel_for_values<2, 8, NT>(vu, D));
-    case 3128: return of(Keys<3, 8>{}, mma_kernel_for_values<3, 8, NT>(vu, D));
-    case 4128: return of(Keys<4, 8>{}, mma_kernel_for_values<4, 8, NT>(vu, D));
+    case 2064: return of(Keys<2, 4>{}, mma_kernel_for_values<2, 4, NT, HALF>(vu, D));
+    case 3064: return of(Keys<3, 4>{}, mma_kernel_for_values<3, 4, NT, HALF>(vu, D));
+    case 4064: return of(Keys<4, 4>{}, mma_kernel_for_values<4, 4, NT, HALF>(vu, D));
+    case 2128: return of(Keys<2, 8>{}, mma_kernel_for_values<2, 8, NT, HALF>(vu, D));
+    case 3128: return of(Keys<3, 8>{}, mma_kernel_for_values<3, 8, NT, HALF>(vu, D));
+    case 4128: return of(Keys<4, 8>{}, mma_kernel_for_values<4, 8, NT, HALF>(vu, D));
     default: return nullptr;
   }
 }
