@@ -209,7 +209,7 @@ cudaError_t launch_accept(const Params& p, AcceptArgs a, int pmax, cudaStream_t 
 // runs, one per CTA, so a CTA holds the ends of some jobs.  (A job that has fewer
 // tiles shares them out in the proportions of its stretch of the line.)  Each (job,
 // CTA) pair leaves a partial, number job + CTA.
-constexpr int kWindowTile = 16;  // tokens of a tile of the tensor-core kernels
+constexpr int kWindowTile = 32;  // tokens of a tile of the tensor-core kernels
 // Reference of a row that has seen tokens, all with scores of -inf (below fp32's
 // range); one that has seen none has -inf.
 constexpr float kWindowLowest = -3.402823466e38f;

@@ -10,11 +10,11 @@ namespace kvc {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32, kTile = kWindowTile, kStages = 3;
+constexpr int kWarps = 8, kThreads = kWarps * 32, kTile = kWindowTile, kStages = 2;
 constexpr int kChunkTiles = 16;  // 8-row tiles whose weights are in shared memory at a time
 
 // The weights that the tokens of a slot receive: the scores again, p = 2^(s - m) / l.
-// A warp decodes the keys of 16 tokens into operand registers once and meets all rows
+// A warp decodes the keys of 16 tokens at a time into operand registers once and meets all rows
 // of a chunk with them, whose weights lie in shared memory (ROWS 8 or 4: that many at
 // most, in registers, as in the main kernel); a token's sums stay in two registers of four lanes.  CTAs take runs of
 // the slots' tiles.  Where there are more rows than a chunk the keys are decoded again
@@ -22,8 +22,8 @@ constexpr int kChunkTiles = 16;  // 8-row tiles whose weights are in shared memo
 template <int KB, int KS, int ROWS>
 __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
     window_weights_mma_kernel(const Params kp, const WindowArgs t, const WindowShape z) {
-  using K = Keys<KB, KS>;
   constexpr bool ONE = ROWS != 0, HALF = ROWS == 4;
+  using K = Keys<KB, KS, ONE>;
   constexpr int NT = ONE ? 1 : kChunkTiles;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(16) float4 rowc[8 * NT];  // per row: score factor, -m, 1 / l, position
@@ -70,14 +70,13 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
           const uint32_t dst = ring_s + st * z.stage + 16 * lane;
           const unsigned char* ks = klane + (int64_t)t0 * Pk;
           if (KB && n == kTile) {
-            constexpr int kPieces = 2 * KS * KB;
 #pragma unroll
-            for (int e = 0; e < (kPieces + 31) / 32; ++e)
-              if (32 * e + 32 <= kPieces || lane + 32 * e < kPieces) copy16(dst + 512 * e, ks + 512 * e);
+            for (int e = 0; e < 4 * KS * KB; e += 32)
+              if (e + 32 <= 4 * KS * KB || lane + e < 4 * KS * KB) copy16(dst + 16 * e, ks + 16 * e);
           } else {
             for (int e = lane; e < (n * Pk + 15) >> 4; e += 32) copy16(dst + 16 * (e - lane), ks + 16 * (e - lane));
           }
-          if (KB && lane < 2 && 8 * lane < n) copy16(dst + z.off_kside, kside + 2 * (int64_t)t0 + 16 * lane);
+          if (KB && lane < 4 && 8 * lane < n) copy16(dst + z.off_kside, kside + 2 * (int64_t)t0 + 16 * lane);
         }
         copy_commit();
       };
@@ -127,100 +126,120 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
         copy_wait<kStages - 2>();
         __syncwarp();
         const unsigned char* sp = ring + st * z.stage;
-        load(i + (kStages - 1) * kWarps, st + kStages - 1 >= kStages ? st - 1 : st + kStages - 1);
+        load(i + (kStages - 1) * kWarps, st ^ 1);
         const int t0 = tile_of(i) * kTile;
-        // lanes 0 and 1 of a quad write tokens g and g + 8: what is there, in time
+        // lanes of a quad write tokens g, g + 8, g + 16 and g + 24: what is there, in time
         const int tok = t0 + g + 8 * c;
-        const bool mine = c < 2 && tok < t.S;
-        const float old = mine && decay != 0.f ? wout[tok] : 0.f;
-        float sum[2] = {0.f, 0.f};  // tokens g and g + 8
+        const float old = tok < t.S && decay != 0.f ? wout[tok] : 0.f;
+        float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // halves of the tile: tokens g and g + 8
         if (t0 <= last && t0 > hidden && (t0 > gap1 || t0 < gap0)) {
-          const typename K::Row ra = keys.row(sp, g, Pk), rb = keys.row(sp, g + 8, Pk);
-          auto operand = [&](int k, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-            uint32_t ha[2], la[2], hb[2], lb[2];
-            keys.step(ra, k, ha, la);
-            keys.step(rb, k, hb, lb);
-            hi[0] = ha[0]; hi[1] = hb[0]; hi[2] = ha[1]; hi[3] = hb[1];
-            lo[0] = la[0]; lo[1] = lb[0]; lo[2] = la[1]; lo[3] = lb[1];
-          };
-          float na = 1.f, nb = 1.f;
-          if (KB) {
-            const __half* nm = reinterpret_cast<const __half*>(sp + z.off_kside);
-            na = __half2float(nm[g]);
-            nb = __half2float(nm[g + 8]);
-          }
           const bool all = t0 >= see0 && t0 <= see1 && (t0 > see2 || t0 < see3);
-          float s[4], small[4], other[4];
-          auto multiply = [&](uint4 w, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
-            mma_f16(s, hi, w.x, w.y);
-            mma_f16(small, hi, w.z, w.w);
-            if (KB) mma_f16(other, lo, w.x, w.y);
-          };
-          auto add = [&](int nt) {  // the weights of the tile's rows
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (HALF) {
-                if (KB) s[e] += other[e];
-                s[e] += __shfl_xor_sync(kFull, s[e], 2);
-              } else {
-                s[e] += KB ? small[e] + other[e] : small[e];
-              }
-            }
+          auto add = [&](int h, int nt, const float (&s)[4], float na, float nb) {  // the weights of a tile of rows
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float4 rc = rowc[8 * nt + cr + j];
               const float pa = ex2(fmaf(s[j] * na, rc.x, rc.y)) * rc.z;
               const float pb = ex2(fmaf(s[2 + j] * nb, rc.x, rc.y)) * rc.z;
               if (all) {
-                sum[0] += pa;
-                sum[1] += pb;
+                sum[h][0] += pa;
+                sum[h][1] += pb;
               } else {
                 const int pos = __float_as_int(rc.w);
-                if (sight.sees(t0 + g, pos)) sum[0] += pa;
-                if (sight.sees(t0 + g + 8, pos)) sum[1] += pb;
+                if (sight.sees(t0 + 16 * h + g, pos)) sum[h][0] += pa;
+                if (sight.sees(t0 + 16 * h + g + 8, pos)) sum[h][1] += pb;
               }
             }
           };
-          auto zero = [&] {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = small[e] = other[e] = 0.f;
-          };
-          if constexpr (ONE) {
-            zero();
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              uint32_t hi[4], lo[4];
-              operand(k, hi, lo);
-              if (HALF) {
-                const uint2 w = whalf[HALF ? k : 0];
-                mma_f16(s, hi, w.x, w.y);
-                if (KB) mma_f16(other, lo, w.x, w.y);
-              } else {
-                multiply(wreg[ONE && !HALF ? k : 0], hi, lo);
-              }
+          auto half = [&](int h) {
+            const int tk = 16 * h + g;
+            const typename K::Row ra = keys.row(sp, tk, Pk), rb = keys.row(sp, tk + 8, Pk);
+            float na = 1.f, nb = 1.f;
+            if (KB) {
+              const __half* nm = reinterpret_cast<const __half*>(sp + z.off_kside) + tk;
+              na = __half2float(nm[0]);
+              nb = __half2float(nm[8]);
             }
-            add(0);
-          } else {
-            uint32_t hi[KS][4], lo[KS][4];
+            float s[4];
+            if constexpr (ONE && KB) {
+              float d[2][4], small[2][4];
 #pragma unroll
-            for (int k = 0; k < KS; ++k) operand(k, hi[k], lo[k]);
+              for (int e = 0; e < 4; ++e) d[0][e] = d[1][e] = small[0][e] = small[1][e] = 0.f;
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  uint32_t hi[2], lo[2];
+                  keys.step(q ? rb : ra, k, hi, lo);
+                  const uint32_t a[4] = {hi[0], lo[0], hi[1], lo[1]};
+                  if (HALF) {
+                    mma_f16(d[q], a, whalf[HALF ? k : 0].x, whalf[HALF ? k : 0].y);
+                  } else {
+                    const uint4 w = wreg[HALF ? 0 : k];
+                    mma_f16(d[q], a, w.x, w.y);
+                    mma_f16(small[q], a, w.z, w.w);
+                  }
+                }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int q = e >> 1, j = e & 1;
+                s[e] = d[q][j] + (HALF ? d[q][2 + j] : d[q][2 + j] + small[q][j] + small[q][2 + j]);
+                if (HALF) s[e] += __shfl_xor_sync(kFull, s[e], 2);
+              }
+              add(h, 0, s, na, nb);
+            } else {
+              constexpr int HK = ONE ? 1 : KS;  // steps whose operands are kept
+              uint32_t hi[HK][4], lo[HK][4];
+              auto operand = [&](int k) {
+                uint32_t ha[2], la[2], hb[2], lb[2];
+                keys.step(ra, k, ha, la);
+                keys.step(rb, k, hb, lb);
+                const int x = ONE ? 0 : k;
+                hi[x][0] = ha[0]; hi[x][1] = hb[0]; hi[x][2] = ha[1]; hi[x][3] = hb[1];
+                lo[x][0] = la[0]; lo[x][1] = lb[0]; lo[x][2] = la[1]; lo[x][3] = lb[1];
+              };
+              if (!ONE)
+#pragma unroll
+                for (int k = 0; k < KS; ++k) operand(k);
 #pragma unroll 1
-            for (int nt = 0; nt < tiles; ++nt) {
-              zero();
+              for (int nt = 0; nt < (ONE ? 1 : tiles); ++nt) {
+                float small[4], other[4];
 #pragma unroll
-              for (int k = 0; k < KS; ++k) multiply(wfrag[(nt * KS + k) * 32 + lane], hi[k], lo[k]);
-              add(nt);
+                for (int e = 0; e < 4; ++e) s[e] = small[e] = other[e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                  if (ONE) operand(k);
+                  const int x = ONE ? 0 : k;
+                  if (HALF) {
+                    mma_f16(s, hi[x], whalf[HALF ? k : 0].x, whalf[HALF ? k : 0].y);
+                  } else {
+                    const uint4 w = ONE ? wreg[ONE && !HALF ? k : 0] : wfrag[(nt * KS + k) * 32 + lane];
+                    mma_f16(s, hi[x], w.x, w.y);
+                    mma_f16(small, hi[x], w.z, w.w);
+                    if (KB) mma_f16(other, lo[x], w.x, w.y);
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (HALF) s[e] += __shfl_xor_sync(kFull, s[e], 2);
+                  else s[e] += KB ? small[e] + other[e] : small[e];
+                }
+                add(h, nt, s, na, nb);
+              }
             }
-          }
+          };
+          half(0);
+          half(1);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          sum[j] += __shfl_xor_sync(kFull, sum[j], 1);
-          if (!HALF) sum[j] += __shfl_xor_sync(kFull, sum[j], 2);
-        }
-        const float add = c ? sum[1] : sum[0];
-        if (mine && (decay != 1.f || add != 0.f)) wout[tok] = fmaf(decay, old, add);
-        if (++st == kStages) st = 0;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            sum[h][j] += __shfl_xor_sync(kFull, sum[h][j], 1);
+            if (!HALF) sum[h][j] += __shfl_xor_sync(kFull, sum[h][j], 2);
+          }
+        const float add = c < 2 ? c ? sum[0][1] : sum[0][0] : c == 2 ? sum[1][0] : sum[1][1];
+        if (tok < t.S && (decay != 1.f || add != 0.f)) wout[tok] = fmaf(decay, old, add);
+        st ^= 1;
       }
       copy_wait<0>();
     }
@@ -237,16 +256,16 @@ WeightsKernel weights_kernel_for(const Params& kp, int NCk, int* tables) {
     return k;
   };
   if (kp.mode == KVC_MODE_UNIFORM) {
-    if (NCk <= 64) return of(Keys<0, 4>{}, window_weights_mma_kernel<0, 4, ROWS>);
-    return of(Keys<0, 8>{}, window_weights_mma_kernel<0, 8, ROWS>);
+    if (NCk <= 64) return of(Keys<0, 4, ROWS != 0>{}, window_weights_mma_kernel<0, 4, ROWS>);
+    return of(Keys<0, 8, ROWS != 0>{}, window_weights_mma_kernel<0, 8, ROWS>);
   }
   switch (kp.cb_bits * 1000 + kp.D) {
-    case 2064: return of(Keys<2, 4>{}, window_weights_mma_kernel<2, 4, ROWS>);
-    case 3064: return of(Keys<3, 4>{}, window_weights_mma_kernel<3, 4, ROWS>);
-    case 4064: return of(Keys<4, 4>{}, window_weights_mma_kernel<4, 4, ROWS>);
-    case 2128: return of(Keys<2, 8>{}, window_weights_mma_kernel<2, 8, ROWS>);
-    case 3128: return of(Keys<3, 8>{}, window_weights_mma_kernel<3, 8, ROWS>);
-    default: return of(Keys<4, 8>{}, window_weights_mma_kernel<4, 8, ROWS>);
+    case 2064: return of(Keys<2, 4, ROWS != 0>{}, window_weights_mma_kernel<2, 4, ROWS>);
+    case 3064: return of(Keys<3, 4, ROWS != 0>{}, window_weights_mma_kernel<3, 4, ROWS>);
+    case 4064: return of(Keys<4, 4, ROWS != 0>{}, window_weights_mma_kernel<4, 4, ROWS>);
+    case 2128: return of(Keys<2, 8, ROWS != 0>{}, window_weights_mma_kernel<2, 8, ROWS>);
+    case 3128: return of(Keys<3, 8, ROWS != 0>{}, window_weights_mma_kernel<3, 8, ROWS>);
+    default: return of(Keys<4, 8, ROWS != 0>{}, window_weights_mma_kernel<4, 8, ROWS>);
   }
 }
 
@@ -265,11 +284,11 @@ int lay_out(const Params& kp, const Params* vp, const WindowArgs& t, int tables,
   at += kTile * 2;
   if (vp) {
     z->off_v = at;
-    at += vp->mode == KVC_MODE_UNIFORM ? up(kTile * t.Pv_max) + 16 : kTile * (vp->D + 16);
+    at += vp->mode == KVC_MODE_UNIFORM ? up(kTile * t.Pv_max) + 16 : kTile * vp->D;
     z->off_vside = at;
     at += kTile * 2;
   }
-  z->stage = at;
+  z->stage = (at + 127) / 128 * 128;
   z->off_ring = (tables + 127) / 128 * 128;
   // the join of the warps' sums takes the rings' place
   const int join = vp ? kWarps * (vp->mode == KVC_MODE_UNIFORM ? 128 : vp->D) * 32 : 0;

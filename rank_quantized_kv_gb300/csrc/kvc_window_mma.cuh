@@ -113,27 +113,32 @@ struct Width {
 // ---------------------------------------------------------------- keys
 
 // How a warp reads the keys of 16 tokens: KB > 0, a codebook of KB bits over 16 KS
-// components, else centred codes of up to 4 KS / 2 chunks (KS steps of 16).
+// components, else centred codes of up to 2 KS chunks (KS steps of 16).
 //
 // Scores carry fp32's precision: weights are two fp16 pieces of values that a power
 // of two per row brings up to 2^13 .. 2^14 (22 bits and more), uniform codes are
 // exact, and centroids two fp16 pieces of values in 8 .. 16; the products of the
 // small pieces are summed apart.
-template <int KB, int KS>
+//
+// PAIRED: the two pieces of a token's codes are rows g and g + 8 of one operand, so
+// that a lookup of both lands in neighbouring registers of it; else a lookup for each,
+// and tokens g and g + 8 make an operand of either piece (for many rows: three
+// products of 16 tokens in place of four).
+template <int KB, int KS, bool PAIRED>
 struct Keys {
-  static constexpr int kSteps = KS;
-  static constexpr int kPieces = KB ? 2 : 1;            // of A
   static constexpr int kCodes = 4 * KS;                 // a lane's codes of a token
+  static constexpr int kSteps = KS;
   static constexpr int kWords = KB ? (kCodes * KB + 31) / 32 : 1;
-  // Pairs of centroids once per lane (no bank conflicts), up to 3 bits: the first
-  // pieces, then the second ones, so that each is loaded into its place in an operand;
-  // at 4 bits single ones, both pieces in a word.
-  static constexpr int kHalf = KB && KB <= 3 ? (1 << (2 * KB)) * 32 * 4 : 0;
-  static constexpr int kTable = !KB ? 0 : KB <= 3 ? (1 << (2 * KB)) * 32 * 8 : 16 * 32 * 4;
+  static constexpr bool kPairs = KB && KB <= 3;         // the table holds pairs of centroids
+  // The table, once per lane (no bank conflicts): pairs of centroids up to 3 bits, both
+  // pieces together (PAIRED) or all first ones before the second ones; at 4 bits single
+  // ones, both pieces in a word.
+  static constexpr int kTable = !KB ? 0 : kPairs ? (1 << (2 * KB)) * 32 * 8 : 16 * 32 * 4;
+  static constexpr int kShift = PAIRED && kPairs ? 8 : 7;  // log2 of the bytes of an entry's copies
 
-  const unsigned char* tab;  // the table
-  uint32_t lane_at;          // where this lane's copy starts in an entry
-  uint32_t off[KS / 2];      // uniform: first bytes of the lane's chunks, ~0 past the last
+  uint32_t tab;         // the table in shared memory
+  uint32_t lane_at;     // where this lane's copy starts in an entry
+  int off[KS / 2];      // uniform: first bytes of the lane's chunks, -1 past the last
   Width width[KS / 2];
 
   // The scale of the centroids: a power of two that brings the largest to [8, 16).
@@ -143,7 +148,7 @@ struct Keys {
     const int e = ((__float_as_int(big) >> 23) & 0xff) - 127;  // big in [2^e, 2^(e + 1))
     return __int_as_float((min(126, max(-126, 3 - e)) + 127) << 23);
   }
-  // Fill the table (all threads).  A lane reads entry x at x * 128.
+  // Fill the table (all threads).
   static __device__ void fill(const Params& kp, unsigned char* table, int threads) {
     const float mul = table_scale(kp);
     auto pieces = [&](int c, uint32_t* hi, uint32_t* lo) {
@@ -153,14 +158,19 @@ struct Keys {
       *lo = __half_as_ushort(__float2half_rn(v - __half2float(h)));
     };
     constexpr int lm = KB ? (1 << KB) - 1 : 0;
-    for (int i = threadIdx.x; i < (kHalf ? kHalf : kTable) / 4; i += threads) {
+    for (int i = threadIdx.x; i < kTable / (kPairs ? 8 : 4); i += threads) {
       const int x = i >> 5;
       uint32_t h0, l0, h1, l1;
       pieces(x & lm, &h0, &l0);
-      if (KB <= 3) {
+      if (kPairs) {
         pieces(x >> KB, &h1, &l1);
-        reinterpret_cast<uint32_t*>(table)[i] = h0 | (h1 << 16);
-        reinterpret_cast<uint32_t*>(table + kHalf)[i] = l0 | (l1 << 16);
+        const uint32_t hi = h0 | (h1 << 16), lo = l0 | (l1 << 16);
+        if (PAIRED) {
+          reinterpret_cast<uint2*>(table)[i] = make_uint2(hi, lo);
+        } else {
+          reinterpret_cast<uint32_t*>(table)[i] = hi;
+          reinterpret_cast<uint32_t*>(table + kTable / 2)[i] = lo;
+        }
       } else {
         reinterpret_cast<uint32_t*>(table)[i] = h0 | (l0 << 16);
       }
@@ -168,8 +178,8 @@ struct Keys {
   }
 
   __device__ void begin(const unsigned char* table) {
-    tab = table;
-    lane_at = (threadIdx.x & 31) * 4;
+    tab = (uint32_t)__cvta_generic_to_shared(table);
+    lane_at = (threadIdx.x & 31) * (kShift == 8 ? 8 : 4);
   }
   // A job's basis (uniform keys).
   __device__ void basis(const Params& kp, int beta) {
@@ -177,7 +187,7 @@ struct Keys {
 #pragma unroll
       for (int s = 0; s < KS / 2; ++s) {
         const uint32_t e = chunk_entry(kp, beta, 4 * s + (threadIdx.x & 3));
-        off[s] = e ? e & 0xffffu : ~0u;
+        off[s] = e ? (int)(e & 0xffffu) : -1;
         width[s].set(e);
       }
   }
@@ -189,7 +199,7 @@ struct Keys {
   __device__ Row row(const unsigned char* rows, int token, int Pk) const {
     Row r;
     if (KB) {
-      const int a = token * Pk + (threadIdx.x & 3) * (kCodes * KB / 8);
+      const int a = token * (2 * KS * KB) + (threadIdx.x & 3) * (kCodes * KB / 8);
       if ((kCodes * KB / 8) % 4 == 0) {
         const unsigned char* p = rows + a;
         if (kWords == 4) {
@@ -217,33 +227,38 @@ struct Keys {
   __device__ void step(const Row& r, int s, uint32_t (&hi)[2], uint32_t (&lo)[2]) const {
     if constexpr (KB == 0) {
       hi[0] = hi[1] = 0u;
-      if (off[s / 2] != ~0u) {
+      if (off[s / 2] >= 0) {
         const Width& w = width[s / 2];
-        const uint2 b = w.split(bits_at(r.rows, r.at + (int)off[s / 2]));
+        const uint2 b = w.split(bits_at(r.rows, r.at + off[s / 2]));
         hi[0] = w.pair(b, 2 * (s & 1));
         hi[1] = w.pair(b, 2 * (s & 1) + 1);
       }
       lo[0] = lo[1] = 0u;
-    } else if constexpr (KB <= 3) {
+    } else if constexpr (kPairs) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        // the pair's field (2 KB bits) shifted to bit 7: a table offset
-        constexpr uint32_t mask = ((1u << (2 * KB)) - 1u) << 7;
-        const int off = KB * (4 * s + 2 * i) - 7, at = off >> 5, sh = off & 31;
+        // the pair's field (2 KB bits) shifted to where it is an offset
+        constexpr uint32_t mask = ((1u << (2 * KB)) - 1u) << kShift;
+        const int bit = KB * (4 * s + 2 * i) - kShift, at = bit >> 5, sh = bit & 31;
         uint32_t v;
-        if (off < 0) v = r.w[0] << -off;
-        else if (sh + 2 * KB + 7 <= 32 || at + 1 >= kWords) v = r.w[at] >> sh;
+        if (bit < 0) v = r.w[0] << -bit;
+        else if (sh + 2 * KB + kShift <= 32 || at + 1 >= kWords) v = r.w[at] >> sh;
         else v = __funnelshift_r(r.w[at], r.w[(at + 1) % kWords], sh);
-        const unsigned char* p = tab + ((v & mask) | lane_at);
-        hi[i] = *reinterpret_cast<const uint32_t*>(p);
-        lo[i] = *reinterpret_cast<const uint32_t*>(p + kHalf);
+        const uint32_t p = tab + ((v & mask) | lane_at);
+        if (PAIRED) {
+          asm("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(hi[i]), "=r"(lo[i]) : "r"(p));
+        } else {
+          asm("ld.shared.u32 %0, [%1];" : "=r"(hi[i]) : "r"(p));
+          asm("ld.shared.u32 %0, [%1 + %2];" : "=r"(lo[i]) : "r"(p), "n"(kTable / 2));
+        }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t x = r.w[s / 2] >> (16 * (s & 1) + 8 * i);  // two codes in the low byte
-        const uint32_t a = *reinterpret_cast<const uint32_t*>(tab + (((x & 15u) << 7) | lane_at));
-        const uint32_t b = *reinterpret_cast<const uint32_t*>(tab + (((x & 0xf0u) << 3) | lane_at));
+        uint32_t a, b;
+        asm("ld.shared.u32 %0, [%1];" : "=r"(a) : "r"(tab + (((x & 15u) << 7) | lane_at)));
+        asm("ld.shared.u32 %0, [%1];" : "=r"(b) : "r"(tab + (((x & 0xf0u) << 3) | lane_at)));
         hi[i] = __byte_perm(a, b, 0x5410);
         lo[i] = __byte_perm(a, b, 0x7632);
       }

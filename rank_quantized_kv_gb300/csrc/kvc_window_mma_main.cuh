@@ -1,6 +1,6 @@
 // The windowed attention's kernel for few rows (the mathematics: kvc_window.cu).
 //
-// A warp takes 16 tokens at a time and is alone with them: it copies their rows to
+// A warp takes 32 tokens at a time and is alone with them: it copies their rows to
 // its ring in shared memory, decodes the codes into operand registers, and keeps
 // references, sums and weighted sums of its own, which the CTA's warps join at the
 // end of a job's run.  Tokens lie on the M side of both products, the job's rows (8
@@ -32,21 +32,26 @@ namespace kvc {
 namespace {
 
 constexpr int kMmaWarps = 8, kMmaThreads = kMmaWarps * 32;
-constexpr int kMmaTile = kWindowTile, kStages = 3;
+constexpr int kMmaTile = kWindowTile, kStages = 2;
 constexpr float kSet = 4.f, kMove = 8.f;
 
 // VK: head size of int8 values (64 or 128), 0 for uniform ones (up to 128 positions).
 template <int VK>
 struct Values {
   static constexpr int kTiles = VK ? VK / 16 : 8;      // tiles of 16 channels
-  static constexpr int kStride = VK + 16;              // rows in shared memory, no bank conflicts
+  // Pieces of 16 bytes of a row; piece p of a token lies in place p ^ swizzle, so that
+  // eight tokens' equal pieces do not meet in a bank.
+  static constexpr int kPieces = VK ? VK / 16 : 1;
+  static __device__ int swizzle(int token) { return VK == 128 ? token & 7 : (token >> 1) & 3; }
   static constexpr bool kUniform = VK == 0;
 };
 
 template <int KB, int KS, int VK, int NT, bool HALF>
 __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
     window_mma_kernel(const Params kp, const Params vp, const WindowArgs t, const WindowShape z) {
-  using K = Keys<KB, KS>;
+  constexpr bool PAIRED = NT == 1;
+  constexpr int HB = NT == 1 ? 2 : 1;  // halves of a tile (16 tokens) handled at a time
+  using K = Keys<KB, KS, PAIRED>;
   using V = Values<VK>;
   constexpr int R = 8 * NT;
   constexpr bool WREG = NT == 1;  // weights in registers, else in shared memory
@@ -87,14 +92,14 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
     const unsigned char* vside = vp.store + vp.side_off[slot];
 
     // Copies of the tile numbered i into a stage: whole 16-byte pieces that hold rows.
-    // Lanes 0, 1 take the keys' side words, 2, 3 the values'.
+    // Lanes 0 .. 3 take the keys' side words, 4 .. 7 the values'.
     const unsigned char* klane = kbase + 16 * lane;
     const unsigned char* vlane = vbase + 16 * lane;
-    const unsigned char* slane = (lane & 2 ? vside : kside) + 16 * (lane & 1);
-    const int sdst = (lane & 2 ? z.off_vside : z.off_kside) + 16 * (lane & 1);
-    const bool has_side = lane < 4 && (lane & 2 ? !V::kUniform : KB > 0);
-    constexpr int kRow = VK ? VK / 16 : 1;  // pieces of an int8 row
-    const int vdst = V::kUniform ? z.off_v + 16 * lane : z.off_v + lane / kRow * V::kStride + 16 * (lane % kRow);
+    const unsigned char* slane = (lane & 4 ? vside : kside) + 16 * (lane & 3);
+    const int sdst = (lane & 4 ? z.off_vside : z.off_kside) + 16 * (lane & 3);
+    const bool has_side = lane < 8 && (lane & 4 ? !V::kUniform : KB > 0);
+    constexpr int kRow = V::kPieces, kRows32 = 32 / kRow;  // rows that the warp's pieces make
+    const int vrow = lane / kRow, vpiece = lane % kRow;
     auto load = [&](int i, int st) {
       if (i < i1) {
         const int t0 = tiles.tile(i) * kMmaTile;
@@ -102,20 +107,21 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
         const int n = min(kMmaTile, t.S - t0);
         const unsigned char* ks = klane + (int64_t)t0 * Pk;
         if (KB && n == kMmaTile) {
-          constexpr int kPieces = 2 * KS * KB;
 #pragma unroll
-          for (int e = 0; e < (kPieces + 31) / 32; ++e)
-            if (32 * e + 32 <= kPieces || lane + 32 * e < kPieces) copy16(dst + 16 * lane + 512 * e, ks + 512 * e);
+          for (int e = 0; e < 4 * KS * KB; e += 32)
+            if (e + 32 <= 4 * KS * KB || lane + e < 4 * KS * KB) copy16(dst + 16 * (lane + e), ks + 16 * e);
         } else {
           for (int e = lane; e < (n * Pk + 15) >> 4; e += 32) copy16(dst + 16 * e, ks + 16 * (e - lane));
         }
-        if (has_side && 8 * (lane & 1) < n) copy16(dst + sdst, slane + 2 * (int64_t)t0);  // 2 bytes a token
+        if (has_side && 8 * (lane & 3) < n) copy16(dst + sdst, slane + 2 * (int64_t)t0);  // 2 bytes a token
         if (!V::kUniform) {
           const unsigned char* vs = vlane + (int64_t)t0 * VK;
 #pragma unroll
-          for (int e = 0; e < kRow / 2; ++e)
-            if (n == kMmaTile || lane / kRow + 32 / kRow * e < n)
-              copy16(dst + vdst + 32 / kRow * e * V::kStride, vs + 512 * e);
+          for (int e = 0; e < kRow; ++e) {
+            const int row = vrow + kRows32 * e;
+            if (n == kMmaTile || row < n)
+              copy16(dst + z.off_v + row * VK + 16 * (vpiece ^ V::swizzle(row)), vs + 512 * e);
+          }
         } else {
           const unsigned char* vs = vlane + (int64_t)t0 * Pv;
           for (int e = lane; e < (n * Pv + 15) >> 4; e += 32) copy16(dst + z.off_v + 16 * e, vs + 16 * (e - lane));
@@ -195,230 +201,281 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
     // tiles that all rows see whole: t0 >= see0 and t0 <= see1, and t0 > see2 or t0 < see3
     const int see0 = sight.first, see1 = p0 - (kMmaTile - 1), see2 = p1 - sight.window,
               see3 = sight.sink_end - (kMmaTile - 1);
-    const uint32_t vmat = (uint32_t)((lane & 15) * V::kStride + 16 * (lane >> 4));  // ldmatrix: this lane's row
+    // ldmatrix: this lane's row and piece
+    const uint32_t vmat = (uint32_t)((lane & 15) * VK), vflip = (uint32_t)((V::swizzle(lane & 15) ^ (lane >> 4)) * 16);
 
     int st = 0;
     for (; i < i1; i += kMmaWarps) {
       copy_wait<kStages - 2>();
       __syncwarp();
       const unsigned char* sp = ring + st * z.stage;
-      {
-        int to = st + kStages - 1;
-        if (to >= kStages) to -= kStages;
-        load(i + (kStages - 1) * kMmaWarps, to);
-      }
-      // ---- scores
-      float s[NT][4];
-      {
-        const typename K::Row ra = keys.row(sp, g, Pk), rb = keys.row(sp, g + 8, Pk);
-        float small[NT][4], other[NT][4];  // (sums apart: shorter chains)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] = small[nt][e] = other[nt][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t ha[2], la[2], hb[2], lb[2];
-          keys.step(ra, k, ha, la);
-          keys.step(rb, k, hb, lb);
-          const uint32_t hi[4] = {ha[0], hb[0], ha[1], hb[1]}, lo[4] = {la[0], lb[0], la[1], lb[1]};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (HALF) {
-              const uint2 w = whalf[HALF ? k : 0];
-              mma_f16(s[nt], hi, w.x, w.y);
-              if (KB) mma_f16(small[nt], lo, w.x, w.y);
-              continue;
-            }
-            const uint4 w = WREG ? wreg[WREG && !HALF ? k : 0] : wfrag[(k * NT + nt) * 32 + lane];
-            mma_f16(s[nt], hi, w.x, w.y);
-            mma_f16(small[nt], hi, w.z, w.w);
-            if (KB) mma_f16(other[nt], lo, w.x, w.y);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (HALF) {
-              if (KB) s[nt][e] += small[nt][e];
-              s[nt][e] += __shfl_xor_sync(kFull, s[nt][e], 2);  // the weights' second pieces
-            } else {
-              s[nt][e] += KB ? small[nt][e] + other[nt][e] : small[nt][e];
-            }
-          }
-      }
-      if (KB) {  // norms
-        const __half* nm = reinterpret_cast<const __half*>(sp + z.off_kside);
-        const float na = __half2float(nm[g]), nb = __half2float(nm[g + 8]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          s[nt][0] *= na; s[nt][1] *= na;
-          s[nt][2] *= nb; s[nt][3] *= nb;
-        }
-      }
-      // ---- softmax: x = s rs - m
+      load(i + (kStages - 1) * kMmaWarps, st ^ 1);
       const int t0 = tiles.tile(i) * kMmaTile;
       const bool all = t0 >= see0 && t0 <= see1 && (t0 > see2 || t0 < see3);
-      float va = 1.f, vb = 1.f;
-      if (!V::kUniform) {
-        const __half* vs = reinterpret_cast<const __half*>(sp + z.off_vside);
-        va = __half2float(vs[g]);
-        vb = __half2float(vs[g + 8]);
-      }
-      uint32_t seen = ~0u;  // bit 4 nt + e
-      float x[NT][4];
+#pragma unroll 1
+      for (int h0 = 0; h0 < 2; h0 += HB) {  // halves of the tile
+        // ---- scores: s[half][rows][e], token 16 half + g + 8 (e >> 1), row cr + (e & 1)
+        float s[HB][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int h = 0; h < HB; ++h) {
+          const int tok = 16 * (h0 + h) + g;
+          const typename K::Row ra = keys.row(sp, tok, Pk), rb = keys.row(sp, tok + 8, Pk);
+          if constexpr (PAIRED && KB) {
+            float d[2][4], small[2][4];  // of tokens g, of tokens g + 8: both pieces of their codes
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], rs[nt][e & 1], negm[nt][e & 1]);
-      if (!all) {
-        seen = 0u;
+            for (int e = 0; e < 4; ++e) d[0][e] = d[1][e] = small[0][e] = small[1][e] = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r = r0 + 8 * nt + cr + j;
-            const int pos = t.ctx + r / t.rep;
-            if (r < t.rows) {
-              if (sight.sees(t0 + g, pos)) seen |= 1u << (4 * nt + j);
-              if (sight.sees(t0 + g + 8, pos)) seen |= 1u << (4 * nt + 2 + j);
+              for (int q = 0; q < 2; ++q) {
+                uint32_t hi[2], lo[2];
+                keys.step(q ? rb : ra, k, hi, lo);
+                const uint32_t a[4] = {hi[0], lo[0], hi[1], lo[1]};
+                if (HALF) {
+                  mma_f16(d[q], a, whalf[HALF ? k : 0].x, whalf[HALF ? k : 0].y);
+                } else {
+                  const uint4 w = wreg[HALF || !WREG ? 0 : k];
+                  mma_f16(d[q], a, w.x, w.y);
+                  mma_f16(small[q], a, w.z, w.w);
+                }
+              }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int q = e >> 1, j = e & 1;
+              s[h][0][e] = d[q][j] + (HALF ? d[q][2 + j] : d[q][2 + j] + small[q][j] + small[q][2 + j]);
+              if (HALF) s[h][0][e] += __shfl_xor_sync(kFull, s[h][0][e], 2);  // the weights' second pieces
             }
-          }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!(seen >> (4 * nt + e) & 1u)) x[nt][e] = -INFINITY;
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        top = max_nan(top, x[nt][0], x[nt][1]);
-        top = max_nan(top, x[nt][2], x[nt][3]);
-      }
-      bool move = !(top <= kMove);
-      if (!V::kUniform) move |= fmaxf(va, vb) > 4.f * sref;
-      if (__any_sync(kFull, move)) {  // (a row's first token, too: its reference is -inf)
-        float ratio = 1.f;
-        if (!V::kUniform) {  // the value scales' reference: the next power of two
-          uint32_t any = 0u;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) any |= seen >> (4 * nt);
-          float m = 0.f;
-          if ((any & 3u) && va > 4.f * sref && va <= 65504.f) m = va;
-          if ((any & 12u) && vb > 4.f * sref && vb <= 65504.f) m = fmaxf(m, vb);
-          m = warp_max(m);
-          if (m > 0.f) {
-            const float to = __int_as_float((__float_as_int(m) & 0x7f800000) + 0x00800000);
-            ratio = sref / to;
-            sref = to;
-            inv_sref = 1.f / to;
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float ya = s[nt][j] * rs[nt][j], yb = s[nt][2 + j] * rs[nt][j];
-            const bool sa = seen >> (4 * nt + j) & 1u, sb = seen >> (4 * nt + 2 + j) & 1u;
-            float m = fmaxf(sa ? fmaxf(ya, kWindowLowest) : -INFINITY, sb ? fmaxf(yb, kWindowLowest) : -INFINITY);
-            m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-            const float old = -negm[nt][j];
-            float now = old, f = 1.f;
-            if (m != -INFINITY && (m - old > kMove || !(old > kWindowLowest))) {
-              // the first reference, or a new one (the lowest: scores of -inf alone so far)
-              now = m > kWindowLowest ? m - kSet : fmaxf(old, m);
-              f = ex2(old - now);
-              if (old == now) f = 1.f;
-            }
-            l[nt][j] *= f;
-            f *= ratio;
-#pragma unroll
-            for (int q = 0; q < MT; ++q) {
-              o[nt][q][j] *= f;
-              o[nt][q][2 + j] *= f;
-            }
-            negm[nt][j] = -now;
-            x[nt][j] = sa ? fmaf(s[nt][j], rs[nt][j], -now) : -INFINITY;
-            x[nt][2 + j] = sb ? fmaf(s[nt][2 + j], rs[nt][j], -now) : -INFINITY;
-          }
-      }
-      va *= inv_sref;
-      vb *= inv_sref;
-      uint32_t ph[NT][2], pl[NT][2];  // P as an operand, in two fp16 pieces
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = ex2(x[nt][e]);
-          l[nt][e & 1] += p[e];
-          if (!V::kUniform) p[e] *= e < 2 ? va : vb;
-        }
-        if (!V::kUniform && !all) {  // a hidden token's scale may be anything
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!(seen >> (4 * nt + e) & 1u)) p[e] = 0.f;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const __half2 hi = __floats2half2_rn(p[2 * h], p[2 * h + 1]);
-          const float2 back = __half22float2(hi);
-          const uint32_t large = *reinterpret_cast<const uint32_t*>(&hi);
-          const uint32_t rest = pack_f16(p[2 * h] - back.x, p[2 * h + 1] - back.y);
-          if (HALF) {
-            ph[nt][h] = transpose8(c < 2 ? large : rest);
           } else {
-            ph[nt][h] = transpose8(large);
-            pl[nt][h] = transpose8(rest);
+            float small[NT][4], other[NT][4];  // (sums apart: shorter chains)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[h][nt][e] = small[nt][e] = other[nt][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              uint32_t ha[2], la[2], hb[2], lb[2];
+              keys.step(ra, k, ha, la);
+              keys.step(rb, k, hb, lb);
+              const uint32_t hi[4] = {ha[0], hb[0], ha[1], hb[1]}, lo[4] = {la[0], lb[0], la[1], lb[1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (HALF) {
+                  mma_f16(s[h][nt], hi, whalf[HALF ? k : 0].x, whalf[HALF ? k : 0].y);
+                } else {
+                  const uint4 w = WREG ? wreg[WREG && !HALF ? k : 0] : wfrag[(k * NT + nt) * 32 + lane];
+                  mma_f16(s[h][nt], hi, w.x, w.y);
+                  mma_f16(small[nt], hi, w.z, w.w);
+                  if (KB) mma_f16(other[nt], lo, w.x, w.y);
+                }
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (HALF) s[h][nt][e] += __shfl_xor_sync(kFull, s[h][nt][e], 2);
+                else s[h][nt][e] += KB ? small[nt][e] + other[nt][e] : small[nt][e];
+              }
+          }
+          if (KB) {  // norms
+            const __half* nm = reinterpret_cast<const __half*>(sp + z.off_kside) + tok;
+            const float na = __half2float(nm[0]), nb = __half2float(nm[8]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              s[h][nt][0] *= na; s[h][nt][1] *= na;
+              s[h][nt][2] *= nb; s[h][nt][3] *= nb;
+            }
+          }
+        }
+        // ---- softmax: x = s rs - m
+        float sv[HB][2];  // value scales
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          sv[h][0] = sv[h][1] = 1.f;
+          if (!V::kUniform) {
+            const __half* vs = reinterpret_cast<const __half*>(sp + z.off_vside) + 16 * (h0 + h) + g;
+            sv[h][0] = __half2float(vs[0]);
+            sv[h][1] = __half2float(vs[8]);
+          }
+        }
+        uint32_t seen = ~0u;  // bit 4 (h NT + nt) + e
+        float x[HB][NT][4];
+#pragma unroll
+        for (int h = 0; h < HB; ++h)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[h][nt][e] = fmaf(s[h][nt][e], rs[nt][e & 1], negm[nt][e & 1]);
+        if (!all) {
+          seen = 0u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int r = r0 + 8 * nt + cr + j;
+              const int pos = t.ctx + r / t.rep;
+              if (r < t.rows)
+#pragma unroll
+                for (int h = 0; h < HB; ++h)
+#pragma unroll
+                  for (int q = 0; q < 2; ++q)
+                    if (sight.sees(t0 + 16 * (h0 + h) + g + 8 * q, pos)) seen |= 1u << (4 * (h * NT + nt) + 2 * q + j);
+            }
+#pragma unroll
+          for (int h = 0; h < HB; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!(seen >> (4 * (h * NT + nt) + e) & 1u)) x[h][nt][e] = -INFINITY;
+        }
+        float top = -INFINITY, most = 0.f;
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            top = max_nan(top, x[h][nt][0], x[h][nt][1]);
+            top = max_nan(top, x[h][nt][2], x[h][nt][3]);
+          }
+          most = fmaxf(most, fmaxf(sv[h][0], sv[h][1]));
+        }
+        bool move = !(top <= kMove);
+        if (!V::kUniform) move |= most > 4.f * sref;
+        if (__any_sync(kFull, move)) {  // (a row's first token, too: its reference is -inf)
+          float ratio = 1.f;
+          if (!V::kUniform) {  // the value scales' reference: the next power of two
+            float m = 0.f;
+#pragma unroll
+            for (int h = 0; h < HB; ++h)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                uint32_t any = 0u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) any |= seen >> (4 * (h * NT + nt) + 2 * q);
+                if ((any & 3u) && sv[h][q] > 4.f * sref && sv[h][q] <= 65504.f) m = fmaxf(m, sv[h][q]);
+              }
+            m = warp_max(m);
+            if (m > 0.f) {
+              const float to = __int_as_float((__float_as_int(m) & 0x7f800000) + 0x00800000);
+              ratio = sref / to;
+              sref = to;
+              inv_sref = 1.f / to;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float m = -INFINITY;
+#pragma unroll
+              for (int h = 0; h < HB; ++h)
+#pragma unroll
+                for (int e = j; e < 4; e += 2)
+                  if (seen >> (4 * (h * NT + nt) + e) & 1u) m = fmaxf(m, fmaxf(s[h][nt][e] * rs[nt][j], kWindowLowest));
+              m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+              const float old = -negm[nt][j];
+              float now = old, f = 1.f;
+              if (m != -INFINITY && (m - old > kMove || !(old > kWindowLowest))) {
+                // the first reference, or a new one (the lowest: scores of -inf alone so far)
+                now = m > kWindowLowest ? m - kSet : fmaxf(old, m);
+                f = old == now ? 1.f : ex2(old - now);
+              }
+              l[nt][j] *= f;
+              f *= ratio;
+#pragma unroll
+              for (int q = 0; q < MT; ++q) {
+                o[nt][q][j] *= f;
+                o[nt][q][2 + j] *= f;
+              }
+              negm[nt][j] = -now;
+#pragma unroll
+              for (int h = 0; h < HB; ++h)
+#pragma unroll
+                for (int e = j; e < 4; e += 2)
+                  x[h][nt][e] = seen >> (4 * (h * NT + nt) + e) & 1u ? fmaf(s[h][nt][e], rs[nt][j], -now) : -INFINITY;
+            }
+        }
+        uint32_t ph[HB][NT][2], pl[HB][NT][2];  // P as an operand, in two fp16 pieces
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          const float va = sv[h][0] * inv_sref, vb = sv[h][1] * inv_sref;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              p[e] = ex2(x[h][nt][e]);
+              l[nt][e & 1] += p[e];
+              if (!V::kUniform) p[e] *= e < 2 ? va : vb;
+            }
+            if (!V::kUniform && !all) {  // a hidden token's scale may be anything
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!(seen >> (4 * (h * NT + nt) + e) & 1u)) p[e] = 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const __half2 hi = __floats2half2_rn(p[2 * q], p[2 * q + 1]);
+              const float2 back = __half22float2(hi);
+              const uint32_t large = *reinterpret_cast<const uint32_t*>(&hi);
+              const uint32_t rest = pack_f16(p[2 * q] - back.x, p[2 * q + 1] - back.y);
+              if (HALF) {
+                ph[h][nt][q] = transpose8(c < 2 ? large : rest);
+              } else {
+                ph[h][nt][q] = transpose8(large);
+                pl[h][nt][q] = transpose8(rest);
+              }
+            }
+          }
+        }
+        // ---- values: tokens 2 c, 2 c + 1 and 8 more of a half are this lane's K indices
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          auto product = [&](int m, const uint32_t (&a)[4]) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(o[nt][m], a, ph[h][nt][0], ph[h][nt][1]);
+              if (!HALF) mma_f16(o[nt][m], a, pl[h][nt][0], pl[h][nt][1]);
+            }
+          };
+          if constexpr (!V::kUniform) {
+            // two bytes of a token make a 16-bit element: its low bytes are rows g of a
+            // tile of 16 channels, its high bytes rows g + 8
+            const uint32_t va0 = ring_s + st * z.stage + z.off_v + vmat + 16 * (h0 + h) * VK;
+#pragma unroll
+            for (int q = 0; q < VK / 32; ++q) {
+              uint32_t v[4];
+              load_transposed(v, va0 + (vflip ^ (32 * q)));
+              const uint32_t a0[4] = {int8_f16(v[0]), int8_f16(v[0] >> 8), int8_f16(v[1]), int8_f16(v[1] >> 8)};
+              product(2 * q, a0);
+              const uint32_t a1[4] = {int8_f16(v[2]), int8_f16(v[2] >> 8), int8_f16(v[3]), int8_f16(v[3] >> 8)};
+              product(2 * q + 1, a1);
+            }
+          } else {
+            const unsigned char* vr = sp + z.off_v;
+#pragma unroll
+            for (int set = 0; set < 2; ++set) {
+              if (!vch[8 * set]) break;  // (the same for all lanes)
+              const int e = V::kUniform ? set : 0;
+              uint2 v[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                v[q] = voff[e] < 0 ? make_uint2(0u, 0u)
+                                   : vwidth[e].split(bits_at(vr, (16 * (h0 + h) + 2 * c + (q & 1) + 8 * (q >> 1)) * Pv + voff[e]));
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                uint32_t a[4];
+                vwidth[e].both(v[0], v[1], m, &a[0], &a[1]);
+                vwidth[e].both(v[2], v[3], m, &a[2], &a[3]);
+                product(4 * set + m, a);
+              }
+            }
           }
         }
       }
-      // ---- values: tokens 2 c, 2 c + 1 and 8 more are this lane's K indices
-      auto product = [&](int m, const uint32_t (&a)[4]) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(o[nt][m], a, ph[nt][0], ph[nt][1]);
-          if (!HALF) mma_f16(o[nt][m], a, pl[nt][0], pl[nt][1]);
-        }
-      };
-      if constexpr (!V::kUniform) {
-        // two bytes of a token make a 16-bit element: its low bytes are rows g of a
-        // tile of 16 channels, its high bytes rows g + 8
-        const uint32_t va0 = ring_s + st * z.stage + z.off_v + vmat;
-#pragma unroll
-        for (int q = 0; q < VK / 32; ++q) {
-          uint32_t v[4];
-          load_transposed(v, va0 + 32 * q);
-          const uint32_t a0[4] = {int8_f16(v[0]), int8_f16(v[0] >> 8), int8_f16(v[1]), int8_f16(v[1] >> 8)};
-          product(2 * q, a0);
-          const uint32_t a1[4] = {int8_f16(v[2]), int8_f16(v[2] >> 8), int8_f16(v[3]), int8_f16(v[3] >> 8)};
-          product(2 * q + 1, a1);
-        }
-      } else {
-        const unsigned char* vr = sp + z.off_v;
-#pragma unroll
-        for (int set = 0; set < 2; ++set) {
-          if (!vch[8 * set]) break;  // (the same for all lanes)
-          const int e = V::kUniform ? set : 0;
-          uint2 v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            v[q] = voff[e] < 0 ? make_uint2(0u, 0u)
-                               : vwidth[e].split(bits_at(vr, (2 * c + (q & 1) + 8 * (q >> 1)) * Pv + voff[e]));
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            uint32_t a[4];
-            vwidth[e].both(v[0], v[1], m, &a[0], &a[1]);
-            vwidth[e].both(v[2], v[3], m, &a[2], &a[3]);
-            product(4 * set + m, a);
-          }
-        }
-      }
-      if (++st == kStages) st = 0;
+      st ^= 1;
     }
     copy_wait<0>();
 
@@ -512,17 +569,17 @@ WindowKernel mma_kernel_for(const Params& kp, const Params& vp, int NCk, int* ta
     return k;
   };
   if (kp.mode == KVC_MODE_UNIFORM) {
-    if (NCk <= 64) return of(Keys<0, 4>{}, mma_kernel_for_values<0, 4, NT, HALF>(vu, D));
-    if (NCk <= 128) return of(Keys<0, 8>{}, mma_kernel_for_values<0, 8, NT, HALF>(vu, D));
+    if (NCk <= 64) return of(Keys<0, 4, NT == 1>{}, mma_kernel_for_values<0, 4, NT, HALF>(vu, D));
+    if (NCk <= 128) return of(Keys<0, 8, NT == 1>{}, mma_kernel_for_values<0, 8, NT, HALF>(vu, D));
     return nullptr;
   }
   switch (kp.cb_bits * 1000 + D) {
-    case 2064: return of(Keys<2, 4>{}, mma_kernel_for_values<2, 4, NT, HALF>(vu, D));
-    case 3064: return of(Keys<3, 4>{}, mma_kernel_for_values<3, 4, NT, HALF>(vu, D));
-    case 4064: return of(Keys<4, 4>{}, mma_kernel_for_values<4, 4, NT, HALF>(vu, D));
-    case 2128: return of(Keys<2, 8>{}, mma_kernel_for_values<2, 8, NT, HALF>(vu, D));
-    case 3128: return of(Keys<3, 8>{}, mma_kernel_for_values<3, 8, NT, HALF>(vu, D));
-    case 4128: return of(Keys<4, 8>{}, mma_kernel_for_values<4, 8, NT, HALF>(vu, D));
+    case 2064: return of(Keys<2, 4, NT == 1>{}, mma_kernel_for_values<2, 4, NT, HALF>(vu, D));
+    case 3064: return of(Keys<3, 4, NT == 1>{}, mma_kernel_for_values<3, 4, NT, HALF>(vu, D));
+    case 4064: return of(Keys<4, 4, NT == 1>{}, mma_kernel_for_values<4, 4, NT, HALF>(vu, D));
+    case 2128: return of(Keys<2, 8, NT == 1>{}, mma_kernel_for_values<2, 8, NT, HALF>(vu, D));
+    case 3128: return of(Keys<3, 8, NT == 1>{}, mma_kernel_for_values<3, 8, NT, HALF>(vu, D));
+    case 4128: return of(Keys<4, 8, NT == 1>{}, mma_kernel_for_values<4, 8, NT, HALF>(vu, D));
     default: return nullptr;
   }
 }
