@@ -26,16 +26,17 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
   using K = Keys<KB, KS, ONE>;
   constexpr int NT = ONE ? 1 : kChunkTiles;
   extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(256) unsigned char table[K::kTable ? K::kTable : 16];
   __shared__ __align__(16) float4 rowc[8 * NT];  // per row: score factor, -m, 1 / l, position
   __shared__ float row_mul[8 * NT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int cr = HALF ? 2 * (c & 1) : 2 * c;
-  uint4* wfrag = reinterpret_cast<uint4*>(smem + K::kTable);  // [NT][step][32], unless in registers
+  uint4* wfrag = reinterpret_cast<uint4*>(smem);  // [NT][step][32], unless in registers
   unsigned char* ring = smem + z.off_ring + warp * kStages * z.stage;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
-  if (KB) K::fill(kp, smem, kThreads);
+  if (KB) K::fill(kp, table, kThreads);
   K keys;
-  keys.begin(smem);
+  keys.begin(table);
   // the tiles that some row sees; all of them where the old weights are scaled
   const bool every = t.decay != 1.f;
   const int64_t tps = t.wtps, total = tps * kp.n_slots;
@@ -252,7 +253,7 @@ template <int ROWS>
 WeightsKernel weights_kernel_for(const Params& kp, int NCk, int* tables) {
   auto of = [&](auto keys, WeightsKernel k) {
     using K = decltype(keys);
-    *tables = K::kTable + (ROWS ? 0 : K::kSteps * kChunkTiles * 512);
+    *tables = ROWS ? 0 : K::kSteps * kChunkTiles * 512;
     return k;
   };
   if (kp.mode == KVC_MODE_UNIFORM) {
@@ -306,7 +307,7 @@ int window_mma_ctas(const Params& kp, const Params& vp, const WindowArgs& t, int
   WindowShape z;
   const int smem = lay_out(kp, &vp, t, tables, &z);
   if (smem > 200 * 1024) return 0;
-  return nt == 1 && 2 * smem <= 220 * 1024 ? 2 : 1;
+  return nt == 1 && 2 * smem <= 188 * 1024 ? 2 : 1;
 }
 
 cudaError_t launch_window_mma(const Params& kp, const Params& vp, const WindowArgs& t, cudaStream_t s, int* nk) {

@@ -75,9 +75,15 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
 // Codes as fp16: 0x6400 | c is 1024 + c exactly, less 1024 + the centre.
 constexpr uint32_t kMagic = 0x64006400u;
 
+// (a & b) ^ c in one instruction (with two constants the compiler makes two of it).
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 // int8 values in the low bytes of the halves (the high bytes hold anything).
 __device__ __forceinline__ uint32_t int8_f16(uint32_t x) {
-  return sub_f16x2((x & 0x00ff00ffu) ^ (kMagic | 0x00800080u), kMagic | 0x00800080u);
+  return sub_f16x2(and_xor(x, 0x00ff00ffu, kMagic | 0x00800080u), kMagic | 0x00800080u);
 }
 
 // A chunk's width as the decoders use it: eight codes of w bits, of which b.x holds
@@ -136,7 +142,7 @@ struct Keys {
   static constexpr int kTable = !KB ? 0 : kPairs ? (1 << (2 * KB)) * 32 * 8 : 16 * 32 * 4;
   static constexpr int kShift = PAIRED && kPairs ? 8 : 7;  // log2 of the bytes of an entry's copies
 
-  uint32_t tab;         // the table in shared memory
+  const unsigned char* tab;  // the table in shared memory
   uint32_t lane_at;     // where this lane's copy starts in an entry
   int off[KS / 2];      // uniform: first bytes of the lane's chunks, -1 past the last
   Width width[KS / 2];
@@ -178,7 +184,7 @@ struct Keys {
   }
 
   __device__ void begin(const unsigned char* table) {
-    tab = (uint32_t)__cvta_generic_to_shared(table);
+    tab = table;
     lane_at = (threadIdx.x & 31) * (kShift == 8 ? 8 : 4);
   }
   // A job's basis (uniform keys).
@@ -244,21 +250,22 @@ struct Keys {
         if (bit < 0) v = r.w[0] << -bit;
         else if (sh + 2 * KB + kShift <= 32 || at + 1 >= kWords) v = r.w[at] >> sh;
         else v = __funnelshift_r(r.w[at], r.w[(at + 1) % kWords], sh);
-        const uint32_t p = tab + ((v & mask) | lane_at);
+        const unsigned char* p = tab + ((v & mask) | lane_at);
         if (PAIRED) {
-          asm("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(hi[i]), "=r"(lo[i]) : "r"(p));
+          const uint2 both = *reinterpret_cast<const uint2*>(p);
+          hi[i] = both.x;
+          lo[i] = both.y;
         } else {
-          asm("ld.shared.u32 %0, [%1];" : "=r"(hi[i]) : "r"(p));
-          asm("ld.shared.u32 %0, [%1 + %2];" : "=r"(lo[i]) : "r"(p), "n"(kTable / 2));
+          hi[i] = *reinterpret_cast<const uint32_t*>(p);
+          lo[i] = *reinterpret_cast<const uint32_t*>(p + kTable / 2);
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t x = r.w[s / 2] >> (16 * (s & 1) + 8 * i);  // two codes in the low byte
-        uint32_t a, b;
-        asm("ld.shared.u32 %0, [%1];" : "=r"(a) : "r"(tab + (((x & 15u) << 7) | lane_at)));
-        asm("ld.shared.u32 %0, [%1];" : "=r"(b) : "r"(tab + (((x & 0xf0u) << 3) | lane_at)));
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(tab + (((x & 15u) << 7) | lane_at));
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(tab + (((x & 0xf0u) << 3) | lane_at));
         hi[i] = __byte_perm(a, b, 0x5410);
         lo[i] = __byte_perm(a, b, 0x7632);
       }

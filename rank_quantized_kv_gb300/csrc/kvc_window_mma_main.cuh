@@ -58,13 +58,13 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
   constexpr int MT = V::kTiles;
   static_assert(!HALF || NT == 1, "half a tile of rows");
   extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(256) unsigned char table[K::kTable ? K::kTable : 16];  // (at an address known to the compiler)
   __shared__ float row_mul[R], row_inv[R];    // 2^x that a row's weights were multiplied by
   __shared__ float wm[kMmaWarps][R], wl[kMmaWarps][R];
   __shared__ uint32_t vch[16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int cr = HALF ? 2 * (c & 1) : 2 * c;  // this lane's rows of a result: cr and cr + 1
-  unsigned char* table = smem;
-  uint4* wfrag = reinterpret_cast<uint4*>(smem + K::kTable);  // [step][NT][32], unless in registers
+  uint4* wfrag = reinterpret_cast<uint4*>(smem);  // [step][NT][32], unless in registers
   unsigned char* ring = smem + z.off_ring + warp * kStages * z.stage;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
   if (KB) K::fill(kp, table, kMmaThreads);
@@ -565,7 +565,7 @@ WindowKernel mma_kernel_for(const Params& kp, const Params& vp, int NCk, int* ta
   const int D = kp.D;
   auto of = [&](auto keys, WindowKernel k) {
     using K = decltype(keys);
-    *tables = K::kTable + (NT == 1 ? 0 : K::kSteps * NT * 512);
+    *tables = NT == 1 ? 0 : K::kSteps * NT * 512;
     return k;
   };
   if (kp.mode == KVC_MODE_UNIFORM) {
