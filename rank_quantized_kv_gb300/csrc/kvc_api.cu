@@ -1316,7 +1316,7 @@ kvc_status kvc_evict(kvc_layer* K, kvc_layer* V, const kvc_evict_desc* d, void* 
   a.dst_row0 = DK ? DK->len : 0;
   int nk = 0;
   const cudaError_t e = kvc::launch_evict(K->p, V->p, DK ? DK->p : K->p, DV ? DV->p : V->p, a,
-                                          std::max(K->pmax, V->pmax), kvc::sm_count(),
+                                          K->pmax, V->pmax, kvc::sm_count(),
                                           static_cast<cudaStream_t>(stream), &nk);
   K->launches += nk;
   if (e != cudaSuccess) return cuda_fail(e, "evict launch");

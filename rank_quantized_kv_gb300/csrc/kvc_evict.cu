@@ -6,9 +6,10 @@
 // and among equals the lower token first.
 //
 // Select: a cluster per slot, its CTAs sharing the tokens out.  A weight becomes a
-// 32-bit key of the same order; three passes over the keys (11, 11 and 10 bits)
-// find the n-th largest by histograms that the cluster adds up through distributed
-// shared memory; a last pass numbers the kept tokens by a scan and writes them.
+// 32-bit key of the same order, in registers (16 a thread; more tokens are read again
+// in every pass); three passes over the keys (11, 11 and 10 bits) find the n-th
+// largest by histograms that the cluster adds up through distributed shared memory; a
+// last one numbers the kept tokens by a scan and writes them.
 // Move: kept rows, payload and side words of both layers, in 16-byte chunks of the
 // destination put together from the largest pieces that stay inside a row.
 //
@@ -22,6 +23,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvc_codes.cuh"
 #include "kvc_internal.h"
@@ -33,7 +35,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 512, kPer = 4, kSelStep = kSelThreads * kPer;
+constexpr int kSelThreads = 1024, kPer = 16, kSelStep = kSelThreads * kPer;
 constexpr int kBins = 2048;
 constexpr uint32_t kForced = 0xffffffffu, kNaNKey = 1u, kPadKey = 0u;
 
@@ -47,10 +49,10 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 struct Slot {
   const float* w;
   int S, first, sink_end, recent0;
-  __device__ uint32_t key(int t) const {
+  __device__ uint32_t key(int t, float weight) const {
     if (t < first) return kPadKey;
     if (t < sink_end || t >= recent0) return kForced;
-    return w ? order_key(w[t]) : 0x80000000u;
+    return order_key(weight);
   }
 };
 
@@ -65,26 +67,30 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, 
   __syncthreads();  // the last scan's sums have been read
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  uint32_t before = 0, all = 0;
+  static_assert(kSelThreads == 1024, "a sum per lane");
+  uint32_t x = warp_sums[lane];  // every warp scans the warps' sums
 #pragma unroll
-  for (int i = 0; i < kSelThreads / 32; ++i) {
-    const uint32_t x = warp_sums[i];
-    if (i < warp) before += x;
-    all += x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
   }
-  *total = all;
-  return v + before;
+  *total = __shfl_sync(kFull, x, 31);
+  const uint32_t before = __shfl_sync(kFull, x, warp > 0 ? warp - 1 : 0);
+  return v + (warp > 0 ? before : 0u);
 }
 
-// grid: clusters of gridDim.x CTAs, one per slot (y)
+// grid: clusters of gridDim.x CTAs, one per slot (y).  A warp takes PER times 32
+// consecutive tokens at a time, a lane every 32nd of them.  RESIDENT: the CTA's tokens
+// are one step, whose keys stay in registers.
+template <int PER, bool RESIDENT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
   __shared__ uint32_t hist[3][kBins];
-  __shared__ uint32_t sum[kBins];
   __shared__ uint32_t warp_sums[kSelThreads / 32];
   __shared__ uint32_t counts[2];  // keys above the threshold, equal to it
   __shared__ uint32_t digit_s, left_s;
+  constexpr int kStep = kSelThreads * PER;
   cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = (int)gridDim.x, me = (int)blockIdx.x, tid = threadIdx.x;
+  const int ctas = (int)gridDim.x, me = (int)blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const int slot = blockIdx.y, b = slot / a.H, h = slot - b * a.H;
   Slot s;
   s.w = a.weights ? a.weights + b * a.w_sb + h * a.w_sh : nullptr;
@@ -94,8 +100,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   s.recent0 = a.S - a.recent;
   if (h == 0 && me == 0 && tid == 0 && a.first_out) a.first_out[b] = max(0, a.n - (a.S - s.first));
   // this CTA's tokens
-  const int seg = ((a.S + ctas - 1) / ctas + kPer - 1) / kPer * kPer;
+  const int seg = (a.S + ctas - 1) / ctas;
   const int t0 = (int)min((int64_t)a.S, (int64_t)me * seg), t1 = (int)min((int64_t)a.S, (int64_t)t0 + seg);
+  uint32_t key[PER];  // of tokens t + 32 u
+  auto read = [&](int t) {
+    float w[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) w[u] = s.w && t + 32 * u < t1 ? s.w[t + 32 * u] : 0.f;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) key[u] = s.key(t + 32 * u, w[u]);
+  };
+  // f(first token of the thread) for every step of the CTA's tokens
+  const int lead = (tid & ~31) * PER + lane;
+  auto each = [&](auto f) {
+    if (RESIDENT) {
+      f(t0 + lead);
+    } else {
+      for (int tb = t0; tb < t1; tb += kStep) {
+        read(tb + lead);
+        f(tb + lead);
+      }
+    }
+  };
+  if (RESIDENT) read(t0 + lead);
   for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0u;
   __syncthreads();
   // the key of the n-th largest, digit by digit: `known` bits fixed so far
@@ -105,32 +132,37 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   for (int pass = 0; pass < 3; ++pass) {
     const int bits = pass < 2 ? 11 : 10, shift = 32 - known - bits;
     uint32_t* hp = hist[pass];
-    for (int t = t0 + tid; t < t1; t += kSelThreads) {
-      const uint32_t k = s.key(t);
-      if (known == 0 || (k >> (32 - known)) == (thr >> (32 - known)))
-        atomicAdd(&hp[(k >> shift) & ((1u << bits) - 1u)], 1u);
-    }
-    cluster.sync();
-    for (int i = tid; i < kBins; i += kSelThreads) {
-      uint32_t v = 0;
-      for (int c = 0; c < ctas; ++c) v += cluster.map_shared_rank(hp, c)[i];
-      sum[i] = v;
-    }
-    __syncthreads();
-    // from the top: the digit at which the running count reaches `left`
-    uint32_t v = 0, mine[kBins / kSelThreads];
+    const uint32_t high = known ? ~0u << (32 - known) : 0u;  // the bits that must agree
+    each([&](int t) {
 #pragma unroll
-    for (int u = 0; u < kBins / kSelThreads; ++u) {
-      mine[u] = sum[kBins - 1 - (tid * (kBins / kSelThreads) + u)];
+      for (int u = 0; u < PER; ++u)
+        if (t + 32 * u < t1 && ((key[u] ^ thr) & high) == 0u)
+          atomicAdd(&hp[(key[u] >> shift) & ((1u << bits) - 1u)], 1u);
+    });
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+    constexpr int kMine = kBins / kSelThreads;
+    uint32_t v = 0, mine[kMine];  // bins of this thread, from the top
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int bin = kBins - 1 - (tid * kMine + u);
+      mine[u] = hp[bin];
+      if (ctas > 1) {
+        mine[u] = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < ctas) mine[u] += cluster.map_shared_rank(hp, c)[bin];
+      }
       v += mine[u];
     }
+    // the digit at which the running count reaches `left`
     uint32_t total;
     const uint32_t end = block_scan(v, warp_sums, &total);
     uint32_t at = end - v;
 #pragma unroll
-    for (int u = 0; u < kBins / kSelThreads; ++u) {
+    for (int u = 0; u < kMine; ++u) {
       if (at < left && at + mine[u] >= left) {
-        digit_s = kBins - 1 - (tid * (kBins / kSelThreads) + u);
+        digit_s = kBins - 1 - (tid * kMine + u);
         left_s = left - at;
       }
       at += mine[u];
@@ -141,63 +173,71 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     known += bits;
     __syncthreads();
   }
-  // keys above thr, and the first `left` of those equal to it, are kept
-  uint32_t gt = 0, eq = 0;
-  for (int t = t0 + tid; t < t1; t += kSelThreads) {
-    const uint32_t k = s.key(t);
-    gt += k > thr;
-    eq += k == thr;
-  }
-  uint32_t n_gt, n_eq;
-  block_scan(gt, warp_sums, &n_gt);
-  block_scan(eq, warp_sums, &n_eq);
-  if (tid == 0) {
-    counts[0] = n_gt;
-    counts[1] = n_eq;
-  }
-  cluster.sync();
+  // Keys above thr, and the first `left` of those equal to it, are kept.  Counts of both
+  // of a step in halves of a word: at most 16384 each.
+  auto count = [&](int t) {  // of the warp's tokens, in lane 0
+    uint32_t v = 0;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const bool in = t + 32 * u < t1;
+      v += __popc(__ballot_sync(kFull, in && key[u] > thr)) + (__popc(__ballot_sync(kFull, in && key[u] == thr)) << 16);
+    }
+    return lane == 0 ? v : 0u;
+  };
   uint32_t gt0 = 0, eq0 = 0;  // of the CTAs before this one
-  for (int c = 0; c < me; ++c) {
-    const uint32_t* p = cluster.map_shared_rank(counts, c);
-    gt0 += p[0];
-    eq0 += p[1];
+  if (ctas > 1) {
+    uint32_t gt = 0, eq = 0;
+    each([&](int t) {
+      const uint32_t v = count(t);
+      gt += v & 0xffffu;
+      eq += v >> 16;
+    });
+    uint32_t n_gt, n_eq;
+    block_scan(gt, warp_sums, &n_gt);
+    block_scan(eq, warp_sums, &n_eq);
+    if (tid == 0) {
+      counts[0] = n_gt;
+      counts[1] = n_eq;
+    }
+    cluster.sync();
+    for (int c = 0; c < me; ++c) {
+      const uint32_t* p = cluster.map_shared_rank(counts, c);
+      gt0 += p[0];
+      eq0 += p[1];
+    }
   }
   grid_dependents_launch();
   int32_t* index = a.index + (int64_t)slot * a.n;
   float* dw = a.dst_weights && !a.in_place ? a.dst_weights + b * a.dw_sb + h * a.dw_sh + a.dst_row0 : nullptr;
-#pragma unroll 1
-  for (int tb = t0; tb < t1; tb += kSelStep) {
-    const int t = tb + tid * kPer;
-    uint32_t k[kPer], v = 0;  // counts of both in halves of a word: at most 2048 each
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      k[u] = t + u < t1 ? s.key(t + u) : 0u;
-      if (t + u < t1) v += k[u] > thr ? 1u : k[u] == thr ? 0x10000u : 0u;
-    }
+  const uint32_t before = (1u << lane) - 1u;
+  each([&](int t) {
     uint32_t total;
-    uint32_t at = block_scan(v, warp_sums, &total) - v;
+    const uint32_t v = count(t);
+    const uint32_t at = __shfl_sync(kFull, block_scan(v, warp_sums, &total) - v, 0);
     uint32_t g = gt0 + (at & 0xffffu), e = eq0 + (at >> 16);
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      if (t + u >= t1) break;
-      const bool above = k[u] > thr, equal = k[u] == thr;
-      if (above || (equal && e < left)) {
-        const uint32_t to = g + min(e, left);
-        index[to] = t + u;
-        if (dw) dw[to] = s.w ? s.w[t + u] : 0.f;
+    for (int u = 0; u < PER; ++u) {
+      const bool in = t + 32 * u < t1, above = in && key[u] > thr, equal = in && key[u] == thr;
+      const uint32_t ma = __ballot_sync(kFull, above), me2 = __ballot_sync(kFull, equal);
+      const uint32_t mine = e + __popc(me2 & before);  // equal ones before this token
+      if (above || (equal && mine < left)) {
+        const uint32_t to = g + __popc(ma & before) + min(mine, left);
+        index[to] = t + 32 * u;
+        if (dw) dw[to] = s.w ? s.w[t + 32 * u] : 0.f;
       }
-      g += above;
-      e += equal;
+      g += __popc(ma);
+      e += __popc(me2);
     }
     gt0 += total & 0xffffu;
     eq0 += total >> 16;
-  }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
+  });
+  if (ctas > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
 // ---------------------------------------------------------------- move
 
-constexpr int kMoveThreads = 256, kChunks = 4;  // chunks of 16 bytes a thread has in flight
+constexpr int kMoveThreads = 256, kChunks = 4;  // 16-byte chunks of a stretch that a thread has
+constexpr int kStretch = kMoveThreads * kChunks * 16;
 
 template <int V> struct Piece;
 template <> struct Piece<16> { using T = uint4; };
@@ -214,28 +254,33 @@ struct Move {
   int64_t P, n, dst0;
 };
 
-__device__ __forceinline__ int64_t row_of(int64_t x, int64_t P) {
-  // 32-bit division where it suffices: the 64-bit one is a subroutine
-  return x < ((int64_t)1 << 32) ? (int64_t)((uint32_t)x / (uint32_t)P) : x / P;
+template <int V>
+__device__ __forceinline__ void copy_piece(uint32_t dst, const uint8_t* src) {
+  if constexpr (V == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(V) : "memory");
 }
 
-// CTA `me` of `ctas`; `barrier` separates the reads of a stretch from its writes.
-template <int V, class Barrier>
-__device__ void move_rows(const Move& q, int me, int ctas, Barrier barrier) {
+// CTA `me` of `ctas`; `barrier` separates the reads of a stretch from its writes.  A
+// thread puts its chunks together in its own places of two stages, by asynchronous
+// copies where the pieces are of 4 bytes or more; the next stretch's reads are on
+// their way while this one is written.  BIG: byte numbers past 32 bits.
+template <int V, bool BIG, class Barrier>
+__device__ void move_rows(const Move& q, uint4* stage, int me, int ctas, Barrier barrier) {
   using T = typename Piece<V>::T;
-  const int64_t total = q.P * q.n, lead = q.dst0 & 15;
+  using Num = typename std::conditional<BIG, int64_t, uint32_t>::type;
+  const int64_t total = q.P * q.n;
+  const int lead = (int)(q.dst0 & 15);
   uint8_t* out = q.dst + (q.dst0 - lead);  // 16-byte aligned
   const int64_t chunks = (lead + total + 15) >> 4;
   const int64_t step = (int64_t)ctas * kMoveThreads;
-  for (int64_t c0 = 0; c0 < chunks; c0 += step * kChunks) {
-    union { uint8_t b[16]; T t[16 / V]; uint4 w; } v[kChunks];
+  auto read = [&](int64_t c0, uint4* buf) {
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) {
-      const int64_t c = c0 + u * step + (int64_t)me * kMoveThreads + threadIdx.x;
-      const int64_t x = c * 16 - lead;
-      if (c >= chunks) continue;
+      const int64_t c = c0 + u * step, x = c * 16 - lead;
+      if (c >= chunks) break;
+      uint4* to = buf + u * kMoveThreads;
       if (x >= 0 && x + 16 <= total) {
-        int64_t row = row_of(x, q.P);
+        int64_t row = (Num)x / (Num)q.P;
         int at = (int)(x - row * q.P);
         const uint8_t* from = q.src + q.idx[row] * q.P;
 #pragma unroll
@@ -244,52 +289,73 @@ __device__ void move_rows(const Move& q, int me, int ctas, Barrier barrier) {
             at = 0;
             from = q.src + q.idx[++row] * q.P;
           }
-          v[u].t[e] = *reinterpret_cast<const T*>(from + at);
+          if constexpr (V >= 4) copy_piece<V>((uint32_t)__cvta_generic_to_shared(to) + e * V, from + at);
+          else reinterpret_cast<T*>(to)[e] = *reinterpret_cast<const T*>(from + at);
           at += V;
         }
       } else {  // an edge of the range: byte by byte
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < 16; ++e)
           if (x + e >= 0 && x + e < total) {
-            const int64_t row = row_of(x + e, q.P);
-            v[u].b[e] = q.src[q.idx[row] * q.P + (x + e - row * q.P)];
+            const int64_t row = (Num)(x + e) / (Num)q.P;
+            reinterpret_cast<uint8_t*>(to)[e] = q.src[q.idx[row] * q.P + (x + e - row * q.P)];
           }
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int64_t first = (int64_t)me * kMoveThreads + threadIdx.x;
+  uint4* mine = stage + threadIdx.x;
+  constexpr int kStage = kChunks * kMoveThreads;
+  read(first, mine);
+  int at = 0;
+  for (int64_t c0 = 0; c0 < chunks; c0 += step * kChunks, at ^= 1) {
+    read(c0 + step * kChunks + first, mine + (at ^ 1) * kStage);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     barrier();
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) {
-      const int64_t c = c0 + u * step + (int64_t)me * kMoveThreads + threadIdx.x;
-      const int64_t x = c * 16 - lead;
-      if (c >= chunks) continue;
+      const int64_t c = c0 + first + u * step, x = c * 16 - lead;
+      if (c >= chunks) break;
+      const uint4* from = mine + at * kStage + u * kMoveThreads;
       if (x >= 0 && x + 16 <= total) {
-        *reinterpret_cast<uint4*>(out + c * 16) = v[u].w;
+        *reinterpret_cast<uint4*>(out + c * 16) = *from;
       } else {
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < 16; ++e)
-          if (x + e >= 0 && x + e < total) out[c * 16 + e] = v[u].b[e];
+          if (x + e >= 0 && x + e < total) out[c * 16 + e] = reinterpret_cast<const uint8_t*>(from)[e];
       }
     }
   }
 }
 
-template <class Barrier>
-__device__ void move_any(const Move& q, int me, int ctas, Barrier barrier) {
+template <bool BIG, class Barrier>
+__device__ void move_pieces(const Move& q, uint4* stage, int me, int ctas, Barrier barrier) {
   switch ((int)min((int64_t)16, q.P & -q.P)) {  // rows start at multiples of P
-    case 16: move_rows<16>(q, me, ctas, barrier); break;
-    case 8: move_rows<8>(q, me, ctas, barrier); break;
-    case 4: move_rows<4>(q, me, ctas, barrier); break;
-    case 2: move_rows<2>(q, me, ctas, barrier); break;
-    default: move_rows<1>(q, me, ctas, barrier);
+    case 16: move_rows<16, BIG>(q, stage, me, ctas, barrier); break;
+    case 8: move_rows<8, BIG>(q, stage, me, ctas, barrier); break;
+    case 4: move_rows<4, BIG>(q, stage, me, ctas, barrier); break;
+    case 2: move_rows<2, BIG>(q, stage, me, ctas, barrier); break;
+    default: move_rows<1, BIG>(q, stage, me, ctas, barrier);
   }
 }
+template <class Barrier>
+__device__ void move_any(const Move& q, uint4* stage, int me, int ctas, Barrier barrier) {
+  if (q.P * q.n < ((int64_t)1 << 32) - 64) move_pieces<false>(q, stage, me, ctas, barrier);
+  else move_pieces<true>(q, stage, me, ctas, barrier);
+}
 
-// grid: (CTAs of a range, slots, ranges): key and value payload, key and value side
-// words and, in place, the weights.  In place the CTAs of a range are a cluster.
+// Ranges of a slot: key and value payload, key and value side words and, in place, the
+// weights.  grid: (CTAs, slots); in place a range's CTAs are a cluster, blockIdx.z the
+// range; else the CTAs of all ranges stand in a row, those of range r from start[r] on.
+struct Ranges { int start[5]; };
 template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMoveThreads)
-    evict_move_kernel(const Params kp, const Params vp, const Params dkp, const Params dvp, const EvictArgs a) {
-  const int slot = blockIdx.y, range = blockIdx.z;
+    evict_move_kernel(const Params kp, const Params vp, const Params dkp, const Params dvp, const EvictArgs a,
+                      const Ranges ranges) {
+  __shared__ uint4 stage[2 * kChunks * kMoveThreads];
+  const int slot = blockIdx.y, x = blockIdx.x;
+  const int range = IN_PLACE ? (int)blockIdx.z : x < ranges.start[1] ? 0 : x < ranges.start[2] ? 1 : x < ranges.start[3] ? 2 : 3;
   const bool weights = range == 4, values = range & 1, side = range >= 2;
   const Params& sp = values ? vp : kp;
   const Params& dp = values ? dvp : dkp;
@@ -316,7 +382,7 @@ __global__ void __launch_bounds__(kMoveThreads)
   if (q.P == 0) return;    // (every CTA of the cluster)
   if (IN_PLACE) {
     cg::cluster_group cluster = cg::this_cluster();
-    move_any(q, (int)blockIdx.x, (int)gridDim.x, [&] { cluster.sync(); });
+    move_any(q, stage, (int)blockIdx.x, (int)gridDim.x, [&] { cluster.sync(); });
     if (!weights) return;
     // tokens to come start at zero; the dropped weights above n have been read
     cluster.sync();
@@ -324,7 +390,7 @@ __global__ void __launch_bounds__(kMoveThreads)
          t += (int64_t)gridDim.x * kMoveThreads)
       w[t] = 0.f;
   } else {
-    move_any(q, (int)blockIdx.x, (int)gridDim.x, [] {});
+    move_any(q, stage, x - ranges.start[range], ranges.start[range + 1] - ranges.start[range], [] {});
   }
 }
 
@@ -349,30 +415,48 @@ cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, unsigned block, unsi
 }  // namespace
 
 cudaError_t launch_evict(const Params& kp, const Params& vp, const Params& dkp, const Params& dvp,
-                         const EvictArgs& a, int pmax, int sms, cudaStream_t s, int* nk) {
-  // CTAs of a slot's cluster: as many as there is a step of tokens for, at most
-  // eight (the portable size), and not far more than the device holds at once
-  auto pick = [&](int64_t work, int64_t clusters, int most) {
+                         const EvictArgs& a, int pk, int pv, int sms, cudaStream_t s, int* nk) {
+  // CTAs of a cluster: as many as there is work for, at most eight (the portable size),
+  // and not far more than the device holds at once
+  auto pick = [&](int64_t work, int64_t clusters, int64_t most) {
     int c = 1;
     while (c < 8 && c < work && 2 * c * clusters <= most) c *= 2;
     return c;
   };
-  const int sel = pick((a.S + kSelStep - 1) / kSelStep, a.n_slots, 4 * sms);
-  cudaError_t e = launch_cluster(evict_select_kernel, dim3(sel, a.n_slots), kSelThreads, sel, false, s, a);
+  // select: one CTA where the keys of all tokens fit its registers (a cluster costs
+  // its barriers and remote reads: 128 slots of 16384 tokens SELECT_A us, SELECT_B with
+  // two CTAs each)
+  const int sel = pick((a.S + kSelStep - 1) / kSelStep, 1, 8);
+  const int64_t per = (a.S + (int64_t)sel * kSelThreads - 1) / ((int64_t)sel * kSelThreads);
+  const auto kernel = per <= 4    ? evict_select_kernel<4, true>
+                      : per <= 8  ? evict_select_kernel<8, true>
+                      : per <= 16 ? evict_select_kernel<kPer, true>
+                                  : evict_select_kernel<kPer, false>;
+  cudaError_t e = launch_cluster(kernel, dim3(sel, a.n_slots), kSelThreads, sel, false, s, a);
   ++*nk;
   if (e != cudaSuccess) return e;
-  const int widest = std::max(pmax, std::max(kp.side_bytes, vp.side_bytes));
-  const int64_t steps = ((int64_t)a.n * std::max(widest, 4) + 16 * kMoveThreads * kChunks - 1) / (16 * kMoveThreads * kChunks);
-  const int ranges = a.in_place && a.weights ? 5 : kp.side_bytes || vp.side_bytes ? 4 : 2;
+  // move: about six CTAs per SM, shared out among the slots' ranges by their bytes
+  const int rows[4] = {pk, pv, kp.side_bytes, vp.side_bytes};
+  const int64_t all = std::max(1, rows[0] + rows[1] + rows[2] + rows[3]);
+  const int64_t ctas = std::max<int64_t>(1, 6 * (int64_t)sms / a.n_slots);
+  Ranges r{};
+  int widest = 4;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t most = ((int64_t)a.n * rows[i] + 15 + kStretch) / kStretch;  // stretches of the range
+    const int64_t share = std::max<int64_t>(1, (ctas * rows[i] + all / 2) / all);
+    r.start[i + 1] = r.start[i] + (rows[i] ? (int)std::min(most, share) : 0);
+    widest = std::max(widest, rows[i]);
+  }
   ++*nk;
   if (a.in_place) {
-    const int c = pick(steps, (int64_t)a.n_slots * 2, 8 * sms);
-    return launch_cluster(evict_move_kernel<true>, dim3(c, a.n_slots, ranges), kMoveThreads, c, true, s, kp, vp,
-                          dkp, dvp, a);
+    const int64_t n = ((int64_t)a.n * widest + kStretch - 1) / kStretch;
+    const int c = pick(n, (int64_t)a.n_slots * 2, 8 * (int64_t)sms);
+    return launch_cluster(evict_move_kernel<true>, dim3(c, a.n_slots, a.weights ? 5 : 4), kMoveThreads, c, true, s,
+                          kp, vp, dkp, dvp, a, r);
   }
-  const int64_t most = std::max<int64_t>(1, 4 * (int64_t)sms / a.n_slots);
-  return launch_cluster(evict_move_kernel<false>, dim3((unsigned)std::min(steps, most), a.n_slots, ranges),
-                        kMoveThreads, 1, true, s, kp, vp, dkp, dvp, a);
+  if (r.start[4] == 0) return cudaSuccess;  // rows of no bytes
+  return launch_cluster(evict_move_kernel<false>, dim3((unsigned)r.start[4], a.n_slots), kMoveThreads, 1, true, s,
+                        kp, vp, dkp, dvp, a, r);
 }
 
 }  // namespace kvc

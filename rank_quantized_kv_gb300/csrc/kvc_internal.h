@@ -285,7 +285,7 @@ struct EvictArgs {
   bool in_place = false;
 };
 cudaError_t launch_evict(const Params& kp, const Params& vp, const Params& dkp, const Params& dvp,
-                         const EvictArgs& a, int pmax, int sms, cudaStream_t s, int* nk);
+                         const EvictArgs& a, int pk, int pv, int sms, cudaStream_t s, int* nk);
 
 // On-device prefill fit of the uniform mode (kvc_fit.cu).  Every pointer is
 // device memory; the float64 scratch lives in the caller's workspace.
