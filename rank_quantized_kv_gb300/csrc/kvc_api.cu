@@ -1170,6 +1170,9 @@ static kvc_status window_check(const kvc_layer* K, const kvc_layer* V, const kvc
   if (!dg.ok) return fail(KVC_ECUDA, "cannot select the layer's device");
   t.Pk_max = K->pmax;
   t.Pv_max = V->pmax;
+  t.cb_mul = K->cb_mul;
+  t.w_mul = 1.f / K->cb_mul;
+  t.wait_ns = K->wait_ns;
   *ws_bytes = kvc::window_plan(K->p, V->p, t, K->path == KVC_PATH_GENERIC, kvc::sm_count());
   return KVC_OK;
 }

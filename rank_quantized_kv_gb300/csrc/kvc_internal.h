@@ -229,7 +229,11 @@ struct WindowArgs {
   int64_t tps = 0, total = 0;            // tiles of a job, of the line
   int64_t wtps = 0;                      // tensor cores: tiles of a slot that the weights' pass walks
   int grid = 0, sms = 0;                 // CTAs of the main kernel; the device's SMs
-  int mma = 0;                           // warp-level tensor cores: 8-row tiles of a job, 0: CUDA cores
+  int mma = 0;                           // warp-level tensor cores: 8-row tiles of a job, 0: not
+  int tc = 0;                            // tcgen05: 1; with mma 0: CUDA cores
+  int K = 0;                             // tcgen05: the operand's K
+  float cb_mul = 1.f, w_mul = 1.f;       // tcgen05: scale of the centroids, its inverse
+  uint64_t wait_ns = 0;                  // tcgen05: limit of the time without a finished tile
   int NCk = 0, Dv = 0, Dvp = 0;          // packed positions; value channels, padded to 4
   int Pk_max = 0, Pv_max = 0;            // largest packed key / value row
   int prod = 0, m = 0, n_out = 0, kcode = 0, knw = 1;
@@ -240,8 +244,12 @@ struct WindowArgs {
   // workspace: key weights [n_slots][rows][NCk], sketch and outlier weights
   // [n_slots][rows][m + n_out], score offsets [n_slots][rows][c1_parts]; partials
   // [jobs + grid - 1]: references and sums [rt], weighted sums [Dvp][rt]; per row its
-  // reference and the inverse of its sum
+  // reference and the inverse of its sum.  tcgen05: the key weights as two fp16 pieces
+  // per job in the operand's layout [jobs][2][rt x K], per row [jobs][rt] the factor of
+  // its products
   float *w = nullptr, *wx = nullptr, *c1 = nullptr;
+  uint16_t* w16 = nullptr;
+  float* wscale = nullptr;
   int c1_parts = 1;
   float2* ml = nullptr;
   float* part = nullptr;
@@ -256,6 +264,14 @@ struct WindowShape {
 size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool generic, int sms);
 cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs t, void* workspace,
                                  cudaStream_t s, int* nk);
+// The tcgen05 kernel for jobs of 128 rows (kvc_window_tc.cu): the operand's K, 0 where
+// it does not take these layers; its launcher.
+int window_tc_k(const Params& kp, const Params& vp, const WindowArgs& t);
+cudaError_t launch_window_tc(const Params& kp, const Params& vp, const WindowArgs& t, cudaStream_t s, int* nk);
+// The queries in the keys' basis for many rows (kvc_window_prep.cu): whether it takes
+// these layers; its launcher.
+bool window_projects(const Params& kp, const WindowArgs& t);
+cudaError_t launch_window_project(const Params& kp, const WindowArgs& t, cudaStream_t s, int* nk);
 using WindowKernel = void (*)(const Params, const Params, const WindowArgs, const WindowShape);
 // The kernel for these layers and jobs of at most 4, of 8, 16 or 32 rows, null where
 // there is none, and the bytes of its tables in shared memory (kvc_window_mma0.cu, 1, 2

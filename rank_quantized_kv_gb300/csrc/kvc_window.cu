@@ -38,6 +38,7 @@ namespace kvc {
 
 namespace {
 
+constexpr int kTcRows = 32;    // more rows of a slot take the tcgen05 kernel
 constexpr int kThreads = 128;  // 4 warps
 constexpr int kRows = 8;       // rows of a job
 constexpr int kTile = 128;     // tokens of a tile: 32 a warp
@@ -423,6 +424,10 @@ __global__ void __launch_bounds__(kCombineThreads)
   int64_t c1 = c0;
   while (window_run(t, c1 + 1) < hi) ++c1;
   const int splits = (int)(c1 - c0) + 1;
+  if (t.tc && !vu && splits == 1) {  // the job's CTA has written its rows itself
+    grid_dependency_wait();          // (who waits for this launch waits for that one)
+    return;
+  }
   const size_t p0 = (size_t)(job + c0);
   if (vu)
     for (int j = tid; j < t.Dv; j += kCombineThreads) {
@@ -612,11 +617,14 @@ size_t lay_out(const Params& kp, WindowArgs& t, void* workspace) {
   const size_t rows = (size_t)kp.n_slots * t.rows;
   const size_t parts = (size_t)kp.n_slots * t.row_tiles + t.grid - 1;
   Take take(workspace);
-  t.w = take.operator()<float>(rows * t.NCk);
+  t.w = take.operator()<float>(t.tc && !t.weights ? 0 : rows * t.NCk);
   t.wx = take.operator()<float>(rows * (t.m + t.n_out));
   t.c1 = take.operator()<float>(rows * t.c1_parts);
   t.ml = take.operator()<float2>(parts * t.rt);
   t.part = take.operator()<float>(parts * t.rt * t.Dvp);
+  const size_t jobs = t.tc ? (size_t)kp.n_slots * t.row_tiles : 0;
+  t.w16 = take.operator()<uint16_t>(jobs * 2 * t.rt * t.K);
+  t.wscale = take.operator()<float>(jobs * t.rt);
   t.stats = t.weights ? take.operator()<float2>(rows) : nullptr;
   return take.used;
 }
@@ -625,17 +633,26 @@ size_t lay_out(const Params& kp, WindowArgs& t, void* workspace) {
 
 size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool generic, int sms) {
   t.sms = sms;
-  t.mma = 0;
+  t.mma = t.tc = 0;
   int ctas = 12;  // of an SM: the CUDA cores'
   if (!generic && !t.prod) {
-    const int nt = t.rows <= 8 ? 1 : t.rows <= 16 ? 2 : 4;
-    const int n = window_mma_ctas(kp, vp, t, nt);
-    if (n) {
-      t.mma = nt;
-      ctas = n;
+    // Many rows: tcgen05, whose jobs cost the same from one row to 128.  Weights take
+    // scores to fp32's precision, which codebooks have in the other kernel alone.
+    if (t.rows > kTcRows && t.cb_mul > 0.f && (!t.weights || kp.mode == KVC_MODE_UNIFORM))
+      t.K = window_tc_k(kp, vp, t);
+    if (t.K) {
+      t.tc = 1;
+      ctas = 1;
+    } else {
+      const int nt = t.rows <= 8 ? 1 : t.rows <= 16 ? 2 : 4;
+      const int n = window_mma_ctas(kp, vp, t, nt);
+      if (n) {
+        t.mma = nt;
+        ctas = n;
+      }
     }
   }
-  t.rt = t.mma ? 8 * t.mma : kRows;
+  t.rt = t.tc ? 128 : t.mma ? 8 * t.mma : kRows;
   t.row_tiles = (t.rows + t.rt - 1) / t.rt;
   t.Dvp = (t.Dv + 3) / 4 * 4;
   t.c1_parts = (t.NCk + kPrepCols - 1) / kPrepCols;
@@ -660,12 +677,20 @@ cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs 
     if (e != cudaSuccess) return e;
   }
   const unsigned row_blocks = (unsigned)(kp.n_slots * ((t.rows + kRows - 1) / kRows));
-  window_prep_kernel<<<dim3(row_blocks, (unsigned)t.c1_parts), kPrepThreads, 0, s>>>(kp, t);
-  ++*nk;
-  e = cudaGetLastError();
+  // (projection of 64 slots of 128 rows, 32 columns: PROJ_A us on the tensor cores, 19.5
+  // in fp32; few rows are latency, and the fp32 kernel has more blocks for them)
+  if (t.tc || (t.mma && t.rows > 32 && window_projects(kp, t))) {
+    e = launch_window_project(kp, t, s, nk);
+  } else {
+    window_prep_kernel<<<dim3(row_blocks, (unsigned)t.c1_parts), kPrepThreads, 0, s>>>(kp, t);
+    ++*nk;
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   const size_t tables = (size_t)kRows * (t.NCk + t.m + t.n_out) * 4;
-  if (t.mma) {
+  if (t.tc) {
+    e = launch_window_tc(kp, vp, t, s, nk);
+  } else if (t.mma) {
     e = launch_window_mma(kp, vp, t, s, nk);
   } else {
     const size_t smem = tables + 4 * 32 * kRows * 4 + 4 * (size_t)kRows * (2 + t.Dv) * 4;
@@ -679,7 +704,7 @@ cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs 
   ++*nk;
   e = launch_dependent(window_combine_kernel, row_blocks, kCombineThreads, 0, s, kp, vp, t);
   if (e != cudaSuccess || !t.weights) return e;
-  if (t.mma) return launch_window_weights_mma(kp, t, s, nk);
+  if (t.mma || t.tc) return launch_window_weights_mma(kp, t, s, nk);
   const auto k = kp.mode == KVC_MODE_UNIFORM ? window_weights_kernel<KVC_MODE_UNIFORM>
                                              : window_weights_kernel<KVC_MODE_CODEBOOK>;
   k<<<(unsigned)kp.n_slots * (unsigned)((t.S + kTile - 1) / kTile), kThreads, tables, s>>>(kp, t);
