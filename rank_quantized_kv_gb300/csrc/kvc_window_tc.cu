@@ -112,7 +112,7 @@ __device__ __forceinline__ void wait_loaded(uint32_t (&v)[32]) {
 // returns after one failed try, so that all roles walk to their ends and the named
 // barriers stay matched; the results are undefined and the error word says so.
 __device__ __forceinline__ void wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  while (!mbar_try_wait_sleep(bar, parity, kTryNs))
+  while (!mbar_try_wait(bar, parity))
     if (*abort_flag) return;
 }
 
@@ -569,17 +569,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           seen = true;
         }
         // 32 columns at a time: P's 16 columns go where columns of S that have been read
-        // were.
-        uint32_t v[2][32];
-        tmem_ld32(s_tm, v[0]);
-#pragma unroll
+        // were.  (The loop is kept rolled: unrolled, its instructions came from L2.)
+        uint32_t v[32];
+        tmem_ld32(s_tm, v);
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
-          wait_loaded(v[q & 1]);
-          if (q < 3) tmem_ld32(s_tm + 32 * (q + 1), v[(q + 1) & 1]);
+          wait_loaded(v);
           float2 y[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            y[e] = make_float2(__uint_as_float(v[q & 1][2 * e]), __uint_as_float(v[q & 1][2 * e + 1]));
+          for (int e = 0; e < 16; ++e) y[e] = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
           if (CB || !VU) {  // (uniform keys: 1, or NaN beside a scale of NaN)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -588,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               y[2 * e + 1] = __fmul2_rn(y[2 * e + 1], make_float2(f.z, f.w));
             }
           }
+          if (q < 3) tmem_ld32(s_tm + 32 * (q + 1), v);
           if (!all) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
