@@ -222,6 +222,22 @@ __device__ __forceinline__ uint4 int8_values(uint2 b) {
   return make_uint4(sub_f16x2(__byte_perm(x, 0x64646464u, 0x5140), sub), sub_f16x2(__byte_perm(x, 0x64646464u, 0x5342), sub),
                     sub_f16x2(__byte_perm(y, 0x64646464u, 0x5140), sub), sub_f16x2(__byte_perm(y, 0x64646464u, 0x5342), sub));
 }
+// The int8 values of one token block (8 rows of NV chunks of 8 bytes) as fp16: lane
+// (octet, t8) takes token t8 and NV / 2 chunks from first on, modulo NV; all loads first.
+template <int NV>
+__device__ __forceinline__ void int8_block(const unsigned char* row, unsigned char* dst, int first) {
+  uint2 b[NV / 2];
+#pragma unroll
+  for (int j = 0; j < NV / 2; ++j) b[j] = *reinterpret_cast<const uint2*>(row + ((first + j) & (NV - 1)) * 8);
+#pragma unroll
+  for (int j = 0; j < NV / 2; ++j)
+    *reinterpret_cast<uint4*>(dst + ((first + j) & (NV - 1)) * 128) = int8_values(b[j]);
+}
+// Bits [lo, hi] of a word, those of them that it has.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  if (hi < 0 || lo > 31 || lo > hi) return 0u;
+  return (~0u << max(lo, 0)) & (~0u >> (31 - min(hi, 31)));
+}
 // Eight centred codes of a chunk as fp16.
 __device__ __forceinline__ uint4 centred(uint2 bits, uint32_t entry) {
   Width w;
@@ -456,18 +472,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned char* raw = st + z.krow;
           const int tok = vblk * 8 + t8, nv = z.DV / 8;
           unsigned char* dst = Vs + vb * v_bytes + vblk * (z.DV * 16) + t8 * 16;
-          const int c0 = (octet & 1) * (nv / 2);
-          for (int j = 0; j < nv / 2; ++j) {
-            int c = c0 + j + t8;
-            while (c >= nv) c -= nv;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (VU) {
-              const uint32_t e = vch[c];
-              if (e) v = centred(bits_at(raw, tok * Pv + (int)(e & 0xffffu)), e);
-            } else {
-              v = int8_values(*reinterpret_cast<const uint2*>(raw + tok * Pv + c * 8));
+          const int c0 = (octet & 1) * (nv / 2) + t8;
+          if (!VU && nv == 16) {
+            int8_block<16>(raw + tok * 128, dst, c0);
+          } else if (!VU && nv == 8) {
+            int8_block<8>(raw + tok * 64, dst, c0);
+          } else {
+            for (int j = 0; j < nv / 2; ++j) {
+              int c = c0 + j;
+              while (c >= nv) c -= nv;
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (VU) {
+                const uint32_t e = vch[c];
+                if (e) v = centred(bits_at(raw, tok * Pv + (int)(e & 0xffffu)), e);
+              } else {
+                v = int8_values(*reinterpret_cast<const uint2*>(raw + tok * Pv + c * 8));
+              }
+              *reinterpret_cast<uint4*>(dst + c * 128) = v;
             }
-            *reinterpret_cast<uint4*>(dst + c * 128) = v;
           }
         }
         fence_proxy_async_smem();
@@ -494,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = vg.n, x = vg.r0 + min(r, vg.nr - 1), pos = t.ctx + x / t.rep;  // (rows past the last: its sight)
       const float rs = t.wscale[(size_t)vg.job * kRows + r];
       float m = -INFINITY;
-      float2 l2 = make_float2(0.f, 0.f);
+      float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool seen = false;
       float sref = VU ? 1.f : 0.f, inv_sref = sref;
       int mine = 0;  // the group's tiles of the segment
@@ -552,19 +574,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_or_abort(&s_full[wg], par, &abort_flag);
         __syncwarp();
         tc_fence_after();
-        // Visible columns, where not all are: [ca, ca + na] and [cb, cb + nb].
-        int ca = 0, cb = 0;
-        uint32_t na = ~0u, nb = 0u;
-        bool ha = true, hb = false;
+        // visible columns, where not all are: [ca, ca1] and [cb, cb1]
+        int ca = 0, ca1 = kTile - 1, cb = 0, cb1 = -1;
         if (!all) {
-          const int first = vg.first, lo = max(first, pos - vg.window + 1), b1 = min(vg.sink_end, pos + 1) - 1;
-          ca = lo - t0;
+          const int first = vg.first;
+          ca = max(first, pos - vg.window + 1) - t0;
+          ca1 = pos - t0;
           cb = first - t0;
-          ha = pos >= lo;
-          hb = b1 >= first;
-          na = ha ? (uint32_t)(pos - lo) : 0u;
-          nb = hb ? (uint32_t)(b1 - first) : 0u;
-          seen |= (ha && max(ca, 0) <= min(ca + (int)na, kTile - 1)) || (hb && max(cb, 0) <= min(cb + (int)nb, kTile - 1));
+          cb1 = min(vg.sink_end, pos + 1) - 1 - t0;
+          seen |= max(ca, 0) <= min(ca1, kTile - 1) || max(cb, 0) <= min(cb1, kTile - 1);
         } else {
           seen = true;
         }
@@ -588,17 +606,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (q < 3) tmem_ld32(s_tm + 32 * (q + 1), v);
           if (!all) {
+            const uint32_t see = bits_between(ca - 32 * q, ca1 - 32 * q) | bits_between(cb - 32 * q, cb1 - 32 * q);
+            if (__any_sync(kFull, see != ~0u)) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int c0 = 32 * q + 2 * e;
-              if (!((ha && (uint32_t)(c0 - ca) <= na) || (hb && (uint32_t)(c0 - cb) <= nb))) y[e].x = -INFINITY;
-              if (!((ha && (uint32_t)(c0 + 1 - ca) <= na) || (hb && (uint32_t)(c0 + 1 - cb) <= nb))) y[e].y = -INFINITY;
+              for (int e = 0; e < 16; ++e) {
+                if (!(see >> (2 * e) & 1u)) y[e].x = -INFINITY;
+                if (!(see >> (2 * e + 1) & 1u)) y[e].y = -INFINITY;
+              }
             }
           }
-          float top[2] = {-INFINITY, -INFINITY};
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 16; ++e) top[e & 1] = max_nan(top[e & 1], y[e].x, y[e].y);
-          const float most = max_nan(top[0], top[1]) * rs;
+          for (int e = 0; e < 16; ++e) top[e & 3] = max_nan(top[e & 3], y[e].x, y[e].y);
+          const float most = max_nan(max_nan(top[0], top[1]), max_nan(top[2], top[3])) * rs;
           const bool need = most > -INFINITY && !(most - m <= kMove);
           if (__any_sync(kFull, need)) {
             // the first reference, or a new one, whole steps of log2 away
@@ -608,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               f = ex2(m - now);
             }
             m = now;
-            l2.x *= f;
-            l2.y *= f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) l2[e] = __fmul2_rn(l2[e], make_float2(f, f));
             const __half2 fh = __float2half2_rn(f);
 #pragma unroll 1
             for (int c = 0; c < q; ++c) {  // the tile's weights so far
@@ -646,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < 2; ++u) {
               const float2 xx = __ffma2_rn(y[2 * e + u], rs2, neg2);
               const float2 p = make_float2(ex2(xx.x), ex2(xx.y));
-              l2 = __fadd2_rn(l2, p);
+              l2[u] = __fadd2_rn(l2[u], p);
               const float2 w = VU ? p : __fmul2_rn(p, u ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
               h[2 * e + u] = pack_f16(w.x, w.y);
             }
@@ -659,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[wg]);
       }
       // ---- the groups' states into one
-      const float l = l2.x + l2.y;
+      const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
       if (mine) {
         wait_or_abort(&o_done[wg], ((it0 + n - 1 - ((it0 + n - 1 - wg) & 1)) >> 1) & 1, &abort_flag);
         __syncwarp();
@@ -688,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int b = vg.slot / kp.H, h = vg.slot - b * kp.H, nq = x / t.rep;
       const int64_t o0 = b * t.o_sb + (int64_t)(h * t.rep + x - nq * t.rep) * t.o_sh + nq * t.o_st;
+#pragma unroll 1
       for (int c0 = 0; c0 < z.DV / 2; c0 += 16) {
         const int c = wg * (z.DV / 2) + c0;
         float v[16];
