@@ -399,6 +399,11 @@ __global__ void __launch_bounds__(kThreads)
 
 constexpr int kCombineThreads = 256, kFactors = 64;
 
+// Jobs that lie in one CTA are written by it: only those that are cut are left.
+__host__ __device__ __forceinline__ bool combines_cuts(const Params& vp, const WindowArgs& t) {
+  return t.tc && vp.mode != KVC_MODE_UNIFORM;
+}
+
 // Join the partials of eight rows, normalise and write the output rows (uniform
 // values: project the weighted mean latent), and what the weights' pass needs of
 // a row.  Thread (d, q) holds channel d of rows 4 q .. 4 q + 3.
@@ -410,7 +415,19 @@ __global__ void __launch_bounds__(kCombineThreads)
   __shared__ float zs[256], zo[256];                    // its step, its offset
   __shared__ __align__(16) float inv_s[kRows];
   const int blocks = (t.rows + kRows - 1) / kRows;
-  const int slot = blockIdx.x / blocks, row0 = (blockIdx.x - slot * blocks) * kRows;
+  int slot = blockIdx.x / blocks, row0 = (blockIdx.x - slot * blocks) * kRows;
+  if (combines_cuts(vp, t)) {
+    // block (cut, 8 rows): the job that the first run after it begins in; the cuts
+    // before it must not lie in the same job
+    const int per = t.rt / kRows, cut = 1 + blockIdx.x / per;
+    const int64_t at = window_run(t, cut), job = at / t.tps, start = job * t.tps;
+    slot = (int)(job / t.row_tiles);
+    row0 = (int)(job - (int64_t)slot * t.row_tiles) * t.rt + (blockIdx.x % per) * kRows;
+    if (at == start || window_run(t, cut - 1) > start || row0 >= t.rows) {
+      grid_dependency_wait();  // (who waits for this launch waits for the one before)
+      return;
+    }
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = slot / kp.H, h = slot - b * kp.H;
   const bool vu = vp.mode == KVC_MODE_UNIFORM;
@@ -424,10 +441,6 @@ __global__ void __launch_bounds__(kCombineThreads)
   int64_t c1 = c0;
   while (window_run(t, c1 + 1) < hi) ++c1;
   const int splits = (int)(c1 - c0) + 1;
-  if (t.tc && !vu && splits == 1) {  // the job's CTA has written its rows itself
-    grid_dependency_wait();          // (who waits for this launch waits for that one)
-    return;
-  }
   const size_t p0 = (size_t)(job + c0);
   if (vu)
     for (int j = tid; j < t.Dv; j += kCombineThreads) {
@@ -701,9 +714,13 @@ cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs 
     e = launch_dependent(k, (unsigned)t.grid, kThreads, smem, s, kp, vp, t);
   }
   if (e != cudaSuccess) return e;
-  ++*nk;
-  e = launch_dependent(window_combine_kernel, row_blocks, kCombineThreads, 0, s, kp, vp, t);
-  if (e != cudaSuccess || !t.weights) return e;
+  const unsigned combines = combines_cuts(vp, t) ? (unsigned)(t.grid - 1) * (unsigned)(t.rt / kRows) : row_blocks;
+  if (combines) {
+    ++*nk;
+    e = launch_dependent(window_combine_kernel, combines, kCombineThreads, 0, s, kp, vp, t);
+    if (e != cudaSuccess) return e;
+  }
+  if (!t.weights) return cudaSuccess;
   if (t.mma || t.tc) return launch_window_weights_mma(kp, t, s, nk);
   const auto k = kp.mode == KVC_MODE_UNIFORM ? window_weights_kernel<KVC_MODE_UNIFORM>
                                              : window_weights_kernel<KVC_MODE_CODEBOOK>;

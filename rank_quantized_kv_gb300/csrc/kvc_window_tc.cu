@@ -133,36 +133,60 @@ struct Segment {
   }
 };
 // A softmax group's segment and place in the run, in shared memory so that they take no
-// registers in its loop; one thread of the group walks.
+// registers in its loop; one thread of the group walks, a segment ahead.  Divisions are
+// done for the run's first and last segments alone: the others are whole jobs.
 struct Place {
-  int64_t at;
   int more;  // 0: the run is at its end
-  int job, slot, r0, nr, n, p0, p1;
-  bool whole;
+  int job, slot, jt, r0, nr, n, p0, p1;
+  int whole;
   int first, sink_end, window;
   int a, na, b, i0;  // tiles, as in Tiles, from number i0 on
-  __device__ void next(const Params& kp, const WindowArgs& t) {
-    const int64_t run1 = window_run(t, blockIdx.x + 1);
+  int64_t at, run1;
+  __device__ void begin(const Params& kp, const WindowArgs& t) {
+    at = window_run(t, blockIdx.x);
+    run1 = window_run(t, blockIdx.x + 1);
+    job = (int)(at / t.tps);
+    slot = job / t.row_tiles;
+    jt = job - slot * t.row_tiles;
+    fill(kp, t);
+  }
+  __device__ void fill(const Params& kp, const WindowArgs& t) {
     more = at < run1;
     if (!more) return;
-    job = (int)(at / t.tps);
-    const int64_t end = min(run1, (job + 1) * t.tps);
-    const Segment g(kp, t, at, end, job);
-    at = end;
-    slot = g.slot;
-    r0 = g.r0;
-    nr = g.nr;
-    n = g.i1 - g.i0;
+    const int64_t start = job * t.tps, end = min(run1, start + t.tps);
+    r0 = jt * kRows;
+    nr = min(kRows, t.rows - r0);
     p0 = t.ctx + r0 / t.rep;
     p1 = t.ctx + (r0 + nr - 1) / t.rep;
-    whole = g.whole;
-    first = g.sight.first;
-    sink_end = g.sight.sink_end;
-    window = g.sight.window;
-    a = g.tiles.a;
-    na = g.tiles.na;
-    b = g.tiles.b;
-    i0 = g.i0;
+    const Sight s(t, slot / kp.H);
+    const Tiles<kTile> tiles(s, p0, p1);
+    first = s.first;
+    sink_end = s.sink_end;
+    window = s.window;
+    a = tiles.a;
+    na = tiles.na;
+    b = tiles.b;
+    i0 = 0;
+    n = tiles.count();
+    whole = at == start && end == start + t.tps;
+    if (!whole) {
+      i0 = (int)((int64_t)n * (at - start) / t.tps);
+      n = (int)((int64_t)n * (end - start) / t.tps) - i0;
+    }
+    at = end;
+  }
+  // This place's successor, into `to`.
+  __device__ void next(const Params& kp, const WindowArgs& t, Place& to) const {
+    to.at = at;
+    to.run1 = run1;
+    to.job = job + 1;
+    to.slot = slot;
+    to.jt = jt + 1;
+    if (to.jt == t.row_tiles) {
+      to.jt = 0;
+      ++to.slot;
+    }
+    to.fill(kp, t);
   }
   __device__ int token(int i) const {  // the first of tile i of the segment
     const int x = i0 + i;
@@ -258,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) float cn[2][2][kTile], cs[2][2][kTile];  // per group and turn: norms, scales over sref
   __shared__ float gm[2][kRows], gl[2][kRows], gs[2], red[2][4];  // the groups' references and sums, srefs
   __shared__ __align__(256) unsigned char tab[CB ? 64 * 32 * 4 : 16];
-  __shared__ __align__(8) unsigned char place_s[2 * sizeof(Place)];
+  __shared__ __align__(8) unsigned char place_s[4 * sizeof(Place)];  // per group this one and the next
   Place* place = reinterpret_cast<Place*>(place_s);
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag, tiles_done;
@@ -289,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     abort_flag = tiles_done = 0;
   }
-  if (tid < 2) place[tid].at = window_run(t, blockIdx.x);
+  if (tid < 2) place[2 * tid].begin(kp, t);
   if (CB) {
     const int wb = kp.cb_bits, lm = (1 << wb) - 1, n = (wb <= 3 ? 1 << (2 * wb) : 16) * 32;
     auto half_of = [&](int c) { return (uint32_t)__half_as_ushort(__float2half_rn(kp.codebook[c] * t.cb_mul)); };
@@ -506,13 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_tm = tm + lane_off + s_col + wg * kTile, o_tm = tm + lane_off + o_col;
     int it0 = 0, turn = 0;  // tiles of the run before the segment; the group's tiles so far
-    volatile Place& vg = place[wg];
-    for (;;) {
-      named_bar_sync(bar, 128);  // the last segment's place has been read
-      if (r == 0) place[wg].next(kp, t);
-      named_bar_sync(bar, 128);
+    for (int turns = 0;; ++turns) {
+      volatile Place& vg = place[2 * wg + (turns & 1)];
       if (!vg.more) break;
-      const Place& g = place[wg];
+      const Place& g = place[2 * wg + (turns & 1)];
       const int n = vg.n, x = vg.r0 + min(r, vg.nr - 1), pos = t.ctx + x / t.rep;  // (rows past the last: its sight)
       const float rs = t.wscale[(size_t)vg.job * kRows + r];
       float m = -INFINITY;
@@ -679,6 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[wg]);
       }
       // ---- the groups' states into one
+      if (r == 0) g.next(kp, t, place[2 * wg + (~turns & 1)]);  // (read after the barriers below)
       const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
       if (mine) {
         wait_or_abort(&o_done[wg], ((it0 + n - 1 - ((it0 + n - 1 - wg) & 1)) >> 1) & 1, &abort_flag);
