@@ -228,6 +228,7 @@ struct WindowArgs {
   int rows = 0, rt = 0, row_tiles = 0;   // rows of a slot, of a job; jobs of a slot
   int64_t tps = 0, total = 0;            // tiles of a job, of the line
   int64_t wtps = 0;                      // tensor cores: tiles of a slot that the weights' pass walks
+  int wsplits = 1;                       // and the shares of the rows that blocks of their own take
   int grid = 0, sms = 0;                 // CTAs of the main kernel; the device's SMs
   int mma = 0;                           // warp-level tensor cores: 8-row tiles of a job, 0: not
   int tc = 0;                            // tcgen05: 1; with mma 0: CUDA cores
@@ -254,6 +255,7 @@ struct WindowArgs {
   float2* ml = nullptr;
   float* part = nullptr;
   float2* stats = nullptr;
+  float* wpart = nullptr;                // workspace: weights of each share of the rows [wsplits][n_slots][S]
 };
 // Shared memory of the tensor-core kernels: where a warp's ring starts, the bytes
 // of one of its stages and where their parts start (key rows lie first).
@@ -284,6 +286,7 @@ WindowKernel window_kernel_32(const Params& kp, const Params& vp, int NCk, int* 
 // whether they take these layers and how many CTAs fit an SM; their launchers.
 int window_mma_ctas(const Params& kp, const Params& vp, const WindowArgs& t, int nt);
 cudaError_t launch_window_mma(const Params& kp, const Params& vp, const WindowArgs& t, cudaStream_t s, int* nk);
+int window_weights_splits(const Params& kp, const WindowArgs& t);
 cudaError_t launch_window_weights_mma(const Params& kp, const WindowArgs& t, cudaStream_t s, int* nk);
 
 // Eviction (kvc_evict.cu): n of S rows of every slot kept, by weight.

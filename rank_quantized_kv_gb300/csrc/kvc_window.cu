@@ -639,6 +639,7 @@ size_t lay_out(const Params& kp, WindowArgs& t, void* workspace) {
   t.w16 = take.operator()<uint16_t>(jobs * 2 * t.rt * t.K);
   t.wscale = take.operator()<float>(jobs * t.rt);
   t.stats = t.weights ? take.operator()<float2>(rows) : nullptr;
+  t.wpart = take.operator()<float>(t.wsplits > 1 ? (size_t)t.wsplits * kp.n_slots * t.S : 0);
   return take.used;
 }
 
@@ -672,16 +673,19 @@ size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool gener
   const int64_t jobs = (int64_t)kp.n_slots * t.row_tiles;
   t.tps = most_tiles(t, t.mma ? kWindowTile : kTile, t.rt);
   t.total = jobs * t.tps;
-  // a warp of the tensor-core kernel takes a tile, of the CUDA cores a quarter
-  const int64_t runs = t.mma ? std::max<int64_t>(t.total / 8, 1) : t.total;
+  // a warp of the tensor-core kernel takes a tile, of the CUDA cores a quarter; jobs of
+  // few tiles have a CTA each all the same
+  const int64_t runs = t.mma ? std::max<int64_t>(t.total / 8, jobs) : t.total;
   t.grid = (int)std::min<int64_t>(runs, ctas * (int64_t)sms);
+  t.wsplits = t.weights && (t.mma || t.tc) ? window_weights_splits(kp, t) : 1;
   return lay_out(kp, t, nullptr);
 }
 
 cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs t, void* workspace,
                                  cudaStream_t s, int* nk) {
   lay_out(kp, t, workspace);
-  t.wtps = t.decay == 1.f ? most_tiles(t, kWindowTile, t.rows) : (t.S + kWindowTile - 1) / kWindowTile;
+  t.wtps = t.decay == 1.f && t.wsplits == 1 ? most_tiles(t, kWindowTile, t.rows)
+                                            : (t.S + kWindowTile - 1) / kWindowTile;
   cudaError_t e;
   if (t.prod) {
     window_prep_prod_kernel<<<(unsigned)(kp.n_slots * t.rows), kThreads, 0, s>>>(kp, t);

@@ -38,28 +38,32 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
   K keys;
   keys.begin(table);
   // the tiles that some row sees; all of them where the old weights are scaled
-  const bool every = t.decay != 1.f;
+  const bool every = t.decay != 1.f || t.wsplits > 1;
   const int64_t tps = t.wtps, total = tps * kp.n_slots;
-  const int64_t run1 = total * (blockIdx.x + 1) / gridDim.x;
+  const int ctas = gridDim.x / t.wsplits, share = blockIdx.x / ctas, cta = blockIdx.x - share * ctas;
+  const int chunks = (t.rows + 8 * NT - 1) / (8 * NT);
+  const int row0 = (int)((int64_t)chunks * share / t.wsplits) * 8 * NT;
+  const int row1 = min(t.rows, (int)((int64_t)chunks * (share + 1) / t.wsplits) * 8 * NT);
+  const int64_t run1 = total * (cta + 1) / ctas;
   bool waited = false;
-  for (int64_t at = total * blockIdx.x / gridDim.x; at < run1;) {
+  for (int64_t at = total * cta / ctas; at < run1;) {
     const int slot = (int)(at / tps);
     const int64_t a0 = at - slot * tps, a1 = min(tps, a0 + (run1 - at));
     at += a1 - a0;
     const int b = slot / kp.H, h = slot - b * kp.H, kbeta = kp.basis_of[slot], Pk = kp.P[kbeta];
     const unsigned char* kbase = kp.store + kp.pay_off[slot];
     const unsigned char* kside = kp.store + kp.side_off[slot];
-    float* wout = t.weights + b * t.w_sb + h * t.w_sh;
+    float* wout = t.wsplits > 1 ? t.wpart + ((size_t)share * kp.n_slots + slot) * t.S : t.weights + b * t.w_sb + h * t.w_sh;
     const Sight sight(t, b);
     const Tiles<kTile> tiles_seen(sight, t.ctx, t.S - 1);
     const int64_t count = every ? tps : tiles_seen.count();
     const int i0 = (int)(count * a0 / tps), i1 = (int)(count * a1 / tps);
     auto tile_of = [&](int i) { return every ? i : tiles_seen.tile(i); };
     keys.basis(kp, kbeta);
-    for (int r0 = 0; r0 < t.rows; r0 += 8 * NT) {
-      const int nr = min(8 * NT, t.rows - r0), tiles = (nr + 7) / 8;
+    for (int r0 = row0; r0 < row1; r0 += 8 * NT) {
+      const int nr = min(8 * NT, row1 - r0), tiles = (nr + 7) / 8;
       const int p0 = t.ctx + r0 / t.rep, p1 = t.ctx + (r0 + nr - 1) / t.rep;
-      const float decay = r0 ? 1.f : t.decay;
+      const float decay = r0 > row0 ? 1.f : t.wsplits > 1 ? 0.f : t.decay;
       // tiles that no row of the chunk sees, and those that all see whole
       const int last = p1, hidden = sight.first - kTile, gap0 = sight.sink_end, gap1 = p0 - sight.window + 1 - kTile;
       const int see0 = sight.first, see1 = p0 - (kTile - 1), see2 = p1 - sight.window,
@@ -89,19 +93,38 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
       waited = true;
       const float tab_inv = KB ? 1.f / K::table_scale(kp) : 1.f;
       const float* w0 = t.w + ((size_t)slot * t.rows + r0) * t.NCk;
-      for (int r = warp; r < 8 * tiles; r += kWarps) {
-        float most = 0.f;
-        if (r < nr)
-          for (int j = lane; j < t.NCk; j += 32) {
-            const float w = fabsf(w0[(size_t)r * t.NCk + j]);
-            if (w <= 3.4e38f) most = fmaxf(most, w);
-          }
-        const float mul = row_scale(warp_max(most));
-        if (lane == 0) {
-          row_mul[r] = mul;
-          const float2 s = r < nr ? t.stats[(size_t)slot * t.rows + r0 + r] : make_float2(0.f, 0.f);
-          rowc[r] = make_float4(tab_inv / mul, -s.x, s.y, __int_as_float(r < nr ? t.ctx + (r0 + r) / t.rep : -1));
+      // four rows of a warp at a time, their loads first
+#pragma unroll 1
+      for (int rb = warp; rb < 8 * tiles; rb += 4 * kWarps) {
+        float w[4][K::kSteps / 2], most[4];
+        float2 st[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = rb + u * kWarps;
+          st[u] = r < nr ? t.stats[(size_t)slot * t.rows + r0 + r] : make_float2(0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < K::kSteps / 2; ++j)
+            w[u][j] = r < nr && lane + 32 * j < t.NCk ? fabsf(w0[(size_t)r * t.NCk + lane + 32 * j]) : 0.f;
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          most[u] = 0.f;
+#pragma unroll
+          for (int j = 0; j < K::kSteps / 2; ++j)
+            if (w[u][j] <= 3.4e38f) most[u] = fmaxf(most[u], w[u][j]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) most[u] = warp_max(most[u]);
+        if (lane == 0)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = rb + u * kWarps;
+            if (r >= 8 * tiles) break;
+            const float mul = row_scale(most[u]);
+            row_mul[r] = mul;
+            rowc[r] = make_float4(tab_inv / mul, -st[u].x, st[u].y,
+                                  __int_as_float(r < nr ? t.ctx + (r0 + r) / t.rep : -1));
+          }
       }
       __syncthreads();
       auto fragment = [&](int s, int nt) {
@@ -119,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
 #pragma unroll
         for (int s = 0; s < KS; ++s) wreg[ONE && !HALF ? s : 0] = fragment(s, 0);
       } else {
+#pragma unroll 4
         for (int e = warp; e < KS * tiles; e += kWarps) wfrag[e * 32 + lane] = fragment(e % KS, e / KS);
         __syncthreads();
       }
@@ -201,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
               if (!ONE)
 #pragma unroll
                 for (int k = 0; k < KS; ++k) operand(k);
-#pragma unroll 1
+#pragma unroll(ONE ? 1 : 2)
               for (int nt = 0; nt < (ONE ? 1 : tiles); ++nt) {
                 float small[4], other[4];
 #pragma unroll
@@ -244,6 +268,20 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
       }
       copy_wait<0>();
     }
+  }
+}
+
+// The shares' weights added up.
+__global__ void __launch_bounds__(256) window_add_weights_kernel(const Params kp, const WindowArgs t) {
+  grid_dependency_wait();
+  const int64_t words = (int64_t)kp.n_slots * t.S;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < words; i += gridDim.x * 256ll) {
+    const int slot = (int)(i / t.S), tok = (int)(i - (int64_t)slot * t.S), b = slot / kp.H, h = slot - b * kp.H;
+    float v = 0.f;
+    for (int x = 0; x < t.wsplits; ++x) v += t.wpart[x * words + i];
+    float* w = t.weights + b * t.w_sb + h * t.w_sh + tok;
+    if (t.decay == 0.f) *w = v;
+    else if (t.decay != 1.f || v != 0.f) *w = fmaf(t.decay, *w, v);
   }
 }
 
@@ -321,6 +359,19 @@ cudaError_t launch_window_mma(const Params& kp, const Params& vp, const WindowAr
   return launch_dependent(k, (unsigned)t.grid, kThreads, (size_t)smem, s, kp, vp, t, z);
 }
 
+// CTAs that share out the tokens of the weights' pass.
+static int weights_ctas(const Params& kp, const WindowArgs& t, int64_t tiles) {
+  const int64_t total = tiles * kp.n_slots;
+  return (int)std::min<int64_t>(std::max<int64_t>(total / kWarps, kp.n_slots), (t.rows <= 8 ? 2 : 1) * (int64_t)t.sms);
+}
+
+int window_weights_splits(const Params& kp, const WindowArgs& t) {
+  if (t.rows <= 8 * kChunkTiles) return 1;
+  const int ctas = weights_ctas(kp, t, (t.S + kTile - 1) / kTile);
+  const int chunks = (t.rows + 8 * kChunkTiles - 1) / (8 * kChunkTiles);
+  return std::max(1, std::min(chunks, t.sms / ctas));
+}
+
 cudaError_t launch_window_weights_mma(const Params& kp, const WindowArgs& t, cudaStream_t s, int* nk) {
   int tables = 0;
   const bool one = t.rows <= 8;
@@ -331,10 +382,14 @@ cudaError_t launch_window_weights_mma(const Params& kp, const WindowArgs& t, cud
   const int smem = lay_out(kp, nullptr, t, tables, &z);
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
-  const int64_t total = t.wtps * kp.n_slots;
-  const int grid = (int)std::min<int64_t>(std::max<int64_t>(total / kWarps, 1), (one ? 2 : 1) * (int64_t)t.sms);
+  const int grid = weights_ctas(kp, t, t.wtps) * t.wsplits;
   ++*nk;
-  return launch_dependent(k, (unsigned)grid, kThreads, (size_t)smem, s, kp, t, z);
+  const cudaError_t f = launch_dependent(k, (unsigned)grid, kThreads, (size_t)smem, s, kp, t, z);
+  if (f != cudaSuccess || t.wsplits == 1) return f;
+  ++*nk;
+  const int64_t words = (int64_t)kp.n_slots * t.S;
+  return launch_dependent(window_add_weights_kernel, (unsigned)std::min<int64_t>((words + 255) / 256, 8 * t.sms), 256u, 0, s,
+                          kp, t);
 }
 
 }  // namespace kvc

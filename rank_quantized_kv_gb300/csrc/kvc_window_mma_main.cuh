@@ -138,18 +138,30 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
 
     // the rows' weights: scaled, split, in the operand's layout
     const float* w0 = t.w + ((size_t)slot * t.rows + r0) * t.NCk;
-    for (int r = warp; r < R; r += kMmaWarps) {
-      float most = 0.f;
-      if (r < nr)
-        for (int j = lane; j < t.NCk; j += 32) {
-          const float w = fabsf(w0[(size_t)r * t.NCk + j]);
-          if (w <= 3.4e38f) most = fmaxf(most, w);  // NaN and infinities stay what they are
+    {  // NT rows of a warp, their loads first
+      float w[NT][KS / 2], most[NT];
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) {
+          const int r = warp + u * kMmaWarps, k = lane + 32 * j;
+          w[u][j] = r < nr && k < t.NCk ? fabsf(w0[(size_t)r * t.NCk + k]) : 0.f;
         }
-      const float mul = row_scale(warp_max(most));
-      if (lane == 0) {
-        row_mul[r] = mul;
-        row_inv[r] = 1.f / mul;
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        most[u] = 0.f;
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j)
+          if (w[u][j] <= 3.4e38f) most[u] = fmaxf(most[u], w[u][j]);  // NaN and infinities stay what they are
+        most[u] = warp_max(most[u]);
       }
+      if (lane == 0)
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          const float mul = row_scale(most[u]);
+          row_mul[warp + u * kMmaWarps] = mul;
+          row_inv[warp + u * kMmaWarps] = 1.f / mul;
+        }
     }
     if (V::kUniform && tid < 16) vch[tid] = chunk_entry(vp, vbeta, tid);
     __syncthreads();
@@ -168,7 +180,9 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
 #pragma unroll
       for (int s = 0; s < KS; ++s) wreg[WREG && !HALF ? s : 0] = fragment(s, 0);
     } else {
-      for (int e = warp; e < KS * NT; e += kMmaWarps) wfrag[e * 32 + lane] = fragment(e / NT, e % NT);
+#pragma unroll
+      for (int e0 = 0; e0 < KS * NT; e0 += kMmaWarps)
+        if (const int e = e0 + warp; e < KS * NT) wfrag[e * 32 + lane] = fragment(e / NT, e % NT);
       __syncthreads();
     }
     const float tab_inv = KB ? 1.f / K::table_scale(kp) : 1.f;
