@@ -11,6 +11,7 @@ namespace kvc {
 namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32, kTile = kWindowTile, kStages = 2;
+constexpr int kManyWarps = 16;   // of the weights' kernel for many rows: one CTA per SM
 constexpr int kChunkTiles = 16;  // 8-row tiles whose weights are in shared memory at a time
 
 // The weights that the tokens of a slot receive: the scores again, p = 2^(s - m) / l.
@@ -20,11 +21,11 @@ constexpr int kChunkTiles = 16;  // 8-row tiles whose weights are in shared memo
 // the slots' tiles.  Where there are more rows than a chunk the keys are decoded again
 // for the next one, by the same warp, which then adds to what it wrote.
 template <int KB, int KS, int ROWS>
-__global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
+__global__ void __launch_bounds__((ROWS ? kWarps : kManyWarps) * 32, ROWS ? 2 : 1)
     window_weights_mma_kernel(const Params kp, const WindowArgs t, const WindowShape z) {
   constexpr bool ONE = ROWS != 0, HALF = ROWS == 4;
   using K = Keys<KB, KS, ONE>;
-  constexpr int NT = ONE ? 1 : kChunkTiles;
+  constexpr int NT = ONE ? 1 : kChunkTiles, WARPS = ONE ? kWarps : kManyWarps;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(256) unsigned char table[K::kTable ? K::kTable : 16];
   __shared__ __align__(16) float4 rowc[8 * NT];  // per row: score factor, -m, 1 / l, position
@@ -34,7 +35,7 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
   uint4* wfrag = reinterpret_cast<uint4*>(smem);  // [NT][step][32], unless in registers
   unsigned char* ring = smem + z.off_ring + warp * kStages * z.stage;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
-  if (KB) K::fill(kp, table, kThreads);
+  if (KB) K::fill(kp, table, WARPS * 32);
   K keys;
   keys.begin(table);
   // the tiles that some row sees; all of them where the old weights are scaled
@@ -88,19 +89,19 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
       __syncthreads();  // the last chunk's rows have been read
       int i = i0 + warp;
 #pragma unroll
-      for (int s = 0; s < kStages - 1; ++s) load(i + s * kWarps, s);
+      for (int s = 0; s < kStages - 1; ++s) load(i + s * WARPS, s);
       if (!waited) grid_dependency_wait();
       waited = true;
       const float tab_inv = KB ? 1.f / K::table_scale(kp) : 1.f;
       const float* w0 = t.w + ((size_t)slot * t.rows + r0) * t.NCk;
       // four rows of a warp at a time, their loads first
 #pragma unroll 1
-      for (int rb = warp; rb < 8 * tiles; rb += 4 * kWarps) {
+      for (int rb = warp; rb < 8 * tiles; rb += 4 * WARPS) {
         float w[4][K::kSteps / 2], most[4];
         float2 st[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int r = rb + u * kWarps;
+          const int r = rb + u * WARPS;
           st[u] = r < nr ? t.stats[(size_t)slot * t.rows + r0 + r] : make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < K::kSteps / 2; ++j)
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
         if (lane == 0)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const int r = rb + u * kWarps;
+            const int r = rb + u * WARPS;
             if (r >= 8 * tiles) break;
             const float mul = row_scale(most[u]);
             row_mul[r] = mul;
@@ -143,15 +144,15 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 2 : 1)
         for (int s = 0; s < KS; ++s) wreg[ONE && !HALF ? s : 0] = fragment(s, 0);
       } else {
 #pragma unroll 4
-        for (int e = warp; e < KS * tiles; e += kWarps) wfrag[e * 32 + lane] = fragment(e % KS, e / KS);
+        for (int e = warp; e < KS * tiles; e += WARPS) wfrag[e * 32 + lane] = fragment(e % KS, e / KS);
         __syncthreads();
       }
       int st = 0;
-      for (; i < i1; i += kWarps) {
+      for (; i < i1; i += WARPS) {
         copy_wait<kStages - 2>();
         __syncwarp();
         const unsigned char* sp = ring + st * z.stage;
-        load(i + (kStages - 1) * kWarps, st ^ 1);
+        load(i + (kStages - 1) * WARPS, st ^ 1);
         const int t0 = tile_of(i) * kTile;
         // lanes of a quad write tokens g, g + 8, g + 16 and g + 24: what is there, in time
         const int tok = t0 + g + 8 * c;
@@ -316,7 +317,7 @@ WindowKernel main_kernel(const Params& kp, const Params& vp, int rows, int NCk, 
 }
 
 // The layout of the rings behind `tables` bytes; the dynamic shared memory.
-int lay_out(const Params& kp, const Params* vp, const WindowArgs& t, int tables, WindowShape* z) {
+int lay_out(const Params& kp, const Params* vp, const WindowArgs& t, int tables, int warps, WindowShape* z) {
   auto up = [](int v) { return (v + 15) / 16 * 16; };
   int at = up(kTile * t.Pk_max) + 16;  // (words are read past a row's end)
   z->off_kside = at;
@@ -331,7 +332,7 @@ int lay_out(const Params& kp, const Params* vp, const WindowArgs& t, int tables,
   z->off_ring = (tables + 127) / 128 * 128;
   // the join of the warps' sums takes the rings' place
   const int join = vp ? kWarps * (vp->mode == KVC_MODE_UNIFORM ? 128 : vp->D) * 32 : 0;
-  return z->off_ring + std::max(kWarps * kStages * z->stage, join);
+  return z->off_ring + std::max(warps * kStages * z->stage, join);
 }
 
 }  // namespace
@@ -343,7 +344,7 @@ int window_mma_ctas(const Params& kp, const Params& vp, const WindowArgs& t, int
   const WindowKernel k = main_kernel(kp, vp, t.rows, t.NCk, nt, &tables);
   if (!k) return 0;
   WindowShape z;
-  const int smem = lay_out(kp, &vp, t, tables, &z);
+  const int smem = lay_out(kp, &vp, t, tables, kWarps, &z);
   if (smem > 200 * 1024) return 0;
   return nt == 1 && 2 * smem <= 188 * 1024 ? 2 : 1;
 }
@@ -352,17 +353,20 @@ cudaError_t launch_window_mma(const Params& kp, const Params& vp, const WindowAr
   int tables = 0;
   const WindowKernel k = main_kernel(kp, vp, t.rows, t.NCk, t.mma, &tables);
   WindowShape z;
-  const int smem = lay_out(kp, &vp, t, tables, &z);
+  const int smem = lay_out(kp, &vp, t, tables, kWarps, &z);
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
   ++*nk;
   return launch_dependent(k, (unsigned)t.grid, kThreads, (size_t)smem, s, kp, vp, t, z);
 }
 
-// CTAs that share out the tokens of the weights' pass.
+// CTAs that share out the tokens of the weights' pass.  Of many rows a chunk takes
+// about 10 us to bring in, so that a warp should have four tiles for it.
 static int weights_ctas(const Params& kp, const WindowArgs& t, int64_t tiles) {
   const int64_t total = tiles * kp.n_slots;
-  return (int)std::min<int64_t>(std::max<int64_t>(total / kWarps, kp.n_slots), (t.rows <= 8 ? 2 : 1) * (int64_t)t.sms);
+  const bool many = t.rows > 8 * kChunkTiles;
+  const int64_t per = t.rows <= 8 ? kWarps : many ? 4 * kManyWarps : kManyWarps;
+  return (int)std::min<int64_t>(std::max<int64_t>(total / per, kp.n_slots), (t.rows <= 8 ? 2 : 1) * (int64_t)t.sms);
 }
 
 int window_weights_splits(const Params& kp, const WindowArgs& t) {
@@ -379,12 +383,12 @@ cudaError_t launch_window_weights_mma(const Params& kp, const WindowArgs& t, cud
                           : one       ? weights_kernel_for<8>(kp, t.NCk, &tables)
                                       : weights_kernel_for<0>(kp, t.NCk, &tables);
   WindowShape z;
-  const int smem = lay_out(kp, nullptr, t, tables, &z);
+  const int warps = one ? kWarps : kManyWarps, smem = lay_out(kp, nullptr, t, tables, warps, &z);
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
   const int grid = weights_ctas(kp, t, t.wtps) * t.wsplits;
   ++*nk;
-  const cudaError_t f = launch_dependent(k, (unsigned)grid, kThreads, (size_t)smem, s, kp, t, z);
+  const cudaError_t f = launch_dependent(k, (unsigned)grid, (unsigned)warps * 32, (size_t)smem, s, kp, t, z);
   if (f != cudaSuccess || t.wsplits == 1) return f;
   ++*nk;
   const int64_t words = (int64_t)kp.n_slots * t.S;
