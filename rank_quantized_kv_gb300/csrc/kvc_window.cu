@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---------------------------------------------------------------- combine
 
-constexpr int kCombineThreads = 256, kFactors = 64;
+constexpr int kFactors = 64;
 
 // Jobs that lie in one CTA are written by it: only those that are cut are left.
 __host__ __device__ __forceinline__ bool combines_cuts(const Params& vp, const WindowArgs& t) {
@@ -406,14 +406,20 @@ __host__ __device__ __forceinline__ bool combines_cuts(const Params& vp, const W
 
 // Join the partials of eight rows, normalise and write the output rows (uniform
 // values: project the weighted mean latent), and what the weights' pass needs of
-// a row.  Thread (d, q) holds channel d of rows 4 q .. 4 q + 3.
-__global__ void __launch_bounds__(kCombineThreads)
+// a row.  Thread (d, q) of a group of 256 holds channel d of rows 4 q .. 4 q + 3; the
+// groups share the partials and, of uniform values, the sum over components.  Bound by
+// the latency of the partials' reads where few blocks are at work: one sequence of 8
+// heads, 38 partials a row COMB_A us with four groups, 15 with one.
+template <int GROUPS>
+__global__ void __launch_bounds__(256 * GROUPS)
     window_combine_kernel(const Params kp, const Params vp, const WindowArgs t) {
   __shared__ __align__(16) float fac[kFactors][kRows];  // 2^(m - M) of the partials
   __shared__ __align__(16) float zb[256][kRows];        // uniform values: mean latents
   __shared__ short comp[256];                           // component of a packed position
   __shared__ float zs[256], zo[256];                    // its step, its offset
   __shared__ __align__(16) float inv_s[kRows];
+  __shared__ float4 gsum[GROUPS > 1 ? GROUPS - 1 : 1][2][256];  // the other groups' sums
+  constexpr int kCombineThreads = 256 * GROUPS;
   const int blocks = (t.rows + kRows - 1) / kRows;
   int slot = blockIdx.x / blocks, row0 = (blockIdx.x - slot * blocks) * kRows;
   if (combines_cuts(vp, t)) {
@@ -453,19 +459,19 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
   grid_dependency_wait();
   // row `warp`: the largest reference
-  const float2* ml = t.ml + p0 * t.rt + rr + warp;
-  const bool live = row0 + warp < t.rows;
+  const float2* ml = t.ml + p0 * t.rt + rr + (warp & 7);
+  const bool live = warp < kRows && row0 + warp < t.rows;  // (the first eight warps)
   float M = -INFINITY, L = 0.f;
   if (live)
     for (int s = lane; s < splits; s += 32) M = fmaxf(M, ml[(size_t)s * t.rt].x);
   M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
-  const int d0 = tid & 127, q = tid >> 7;  // d0 and d0 + 128; row quad
+  const int group = tid >> 8, d0 = tid & 127, q = (tid >> 7) & 1;  // d0 and d0 + 128; row quad
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
   for (int s0 = 0; s0 < splits; s0 += kFactors) {
     const int n = min(kFactors, splits - s0);
     __syncthreads();
-    for (int e = lane; e < n; e += 32) {
+    for (int e = lane; warp < kRows && e < n; e += 32) {
       const float2 v = live ? ml[(size_t)(s0 + e) * t.rt] : make_float2(0.f, 0.f);
       // a run that saw nothing has l = 0 (and weighted sums of 0)
       const float f = v.y == 0.f ? 0.f : exp2f(v.x - ref);
@@ -479,7 +485,7 @@ __global__ void __launch_bounds__(kCombineThreads)
       if (d >= t.Dv) break;
       const float* p = t.part + ((p0 + s0) * t.Dvp + d) * t.rt + rr + 4 * q;
 #pragma unroll 4
-      for (int e = 0; e < n; ++e) {
+      for (int e = group; e < n; e += GROUPS) {
         const float4 v = *reinterpret_cast<const float4*>(p + (size_t)e * t.rt * t.Dvp);
         const float4 f = *reinterpret_cast<const float4*>(&fac[e][4 * q]);
         acc[u].x = fmaf(f.x, v.x, acc[u].x);
@@ -489,8 +495,13 @@ __global__ void __launch_bounds__(kCombineThreads)
       }
     }
   }
+  if (GROUPS > 1) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (group) gsum[group - 1][u][tid & 255] = acc[u];
+  }
   L = warp_sum(L);
-  if (lane == 0) {
+  if (lane == 0 && warp < kRows) {
     // nothing visible: zero; scores of -inf alone: NaN
     const float inv = L > 0.f || L != L ? 1.f / L : M == -INFINITY ? 0.f : NAN;
     inv_s[warp] = inv;
@@ -498,6 +509,17 @@ __global__ void __launch_bounds__(kCombineThreads)
   }
   __syncthreads();
   grid_dependents_launch();
+  if (GROUPS > 1 && group == 0)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int x = 0; x < GROUPS - 1; ++x) {
+        const float4 v = gsum[x][u][tid];
+        acc[u].x += v.x;
+        acc[u].y += v.y;
+        acc[u].z += v.z;
+        acc[u].w += v.w;
+      }
   auto put = [&](int d, float4 v) {  // channel d of the thread's four rows
     const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -511,25 +533,28 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
   };
   const float4 inv = *reinterpret_cast<const float4*>(&inv_s[4 * q]);
+  if (group == 0)
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int d = d0 + 128 * u;
-    if (d >= t.Dv) break;
-    const float4 v = make_float4(acc[u].x * inv.x, acc[u].y * inv.y, acc[u].z * inv.z, acc[u].w * inv.w);
-    if (!vu) put(d, v);
-    else
-      *reinterpret_cast<float4*>(&zb[d][4 * q]) =
-          make_float4(fmaf(zs[d], v.x, zo[d]), fmaf(zs[d], v.y, zo[d]), fmaf(zs[d], v.z, zo[d]),
-                      fmaf(zs[d], v.w, zo[d]));  // the mean latent
-  }
+    for (int u = 0; u < 2; ++u) {
+      const int d = d0 + 128 * u;
+      if (d >= t.Dv) break;
+      const float4 v = make_float4(acc[u].x * inv.x, acc[u].y * inv.y, acc[u].z * inv.z, acc[u].w * inv.w);
+      if (!vu) put(d, v);
+      else
+        *reinterpret_cast<float4*>(&zb[d][4 * q]) =
+            make_float4(fmaf(zs[d], v.x, zo[d]), fmaf(zs[d], v.y, zo[d]), fmaf(zs[d], v.z, zo[d]),
+                        fmaf(zs[d], v.w, zo[d]));  // the mean latent
+    }
   if (!vu) return;
   __syncthreads();
-  for (int i = d0; i < vp.D; i += 128) {
-    const float mu = vp.mean[(size_t)beta * vp.D + i];
-    float4 v = make_float4(mu, mu, mu, mu);
-    const float* Vt = vp.Vt + (size_t)beta * vp.r * vp.D + i;
+#pragma unroll 1
+  for (int i0 = 0; i0 < vp.D; i0 += 128) {
+    const int i = i0 + d0;
+    const bool in = i < vp.D;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* Vt = vp.Vt + (size_t)beta * vp.r * vp.D + (in ? i : 0);
 #pragma unroll 8
-    for (int j = 0; j < t.Dv; ++j) {
+    for (int j = group; j < t.Dv; j += GROUPS) {
       const int k = comp[j];
       const float c = k < 0 ? 0.f : Vt[(size_t)k * vp.D];
       const float4 zz = *reinterpret_cast<const float4*>(&zb[j][4 * q]);
@@ -539,8 +564,25 @@ __global__ void __launch_bounds__(kCombineThreads)
       v.z = fmaf(zz.z, c, v.z);
       v.w = fmaf(zz.w, c, v.w);
     }
-    auto row = [](float x, float f) { return f == 0.f ? 0.f : f != f ? f : x; };
-    put(i, make_float4(row(v.x, inv.x), row(v.y, inv.y), row(v.z, inv.z), row(v.w, inv.w)));
+    if (GROUPS > 1) {
+      if (group) gsum[group - 1][0][tid & 255] = v;
+      __syncthreads();
+      if (group == 0)
+#pragma unroll
+        for (int x = 0; x < GROUPS - 1; ++x) {
+          const float4 y = gsum[x][0][tid];
+          v.x += y.x;
+          v.y += y.y;
+          v.z += y.z;
+          v.w += y.w;
+        }
+      __syncthreads();  // (the next columns' sums take the place)
+    }
+    if (group == 0 && in) {
+      const float mu = vp.mean[(size_t)beta * vp.D + i];
+      auto row = [](float x, float f) { return f == 0.f ? 0.f : f != f ? f : x; };
+      put(i, make_float4(row(v.x + mu, inv.x), row(v.y + mu, inv.y), row(v.z + mu, inv.z), row(v.w + mu, inv.w)));
+    }
   }
 }
 
@@ -721,7 +763,10 @@ cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs 
   const unsigned combines = combines_cuts(vp, t) ? (unsigned)(t.grid - 1) * (unsigned)(t.rt / kRows) : row_blocks;
   if (combines) {
     ++*nk;
-    e = launch_dependent(window_combine_kernel, combines, kCombineThreads, 0, s, kp, vp, t);
+    // four groups of threads where a row has many partials (at most total / jobs runs)
+    const bool many = (int64_t)t.grid > 6 * (int64_t)kp.n_slots * t.row_tiles;
+    e = many ? launch_dependent(window_combine_kernel<4>, combines, 1024u, 0, s, kp, vp, t)
+             : launch_dependent(window_combine_kernel<1>, combines, 256u, 0, s, kp, vp, t);
     if (e != cudaSuccess) return e;
   }
   if (!t.weights) return cudaSuccess;

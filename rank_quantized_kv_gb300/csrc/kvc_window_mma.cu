@@ -60,7 +60,7 @@ __global__ void __launch_bounds__((ROWS ? kWarps : kManyWarps) * 32, ROWS ? 2 : 
     const int64_t count = every ? tps : tiles_seen.count();
     const int i0 = (int)(count * a0 / tps), i1 = (int)(count * a1 / tps);
     auto tile_of = [&](int i) { return every ? i : tiles_seen.tile(i); };
-    keys.basis(kp, kbeta);
+    keys.basis(kp, kbeta, Pk);
     for (int r0 = row0; r0 < row1; r0 += 8 * NT) {
       const int nr = min(8 * NT, row1 - r0), tiles = (nr + 7) / 8;
       const int p0 = t.ctx + r0 / t.rep, p1 = t.ctx + (r0 + nr - 1) / t.rep;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__((ROWS ? kWarps : kManyWarps) * 32, ROWS ? 2 : 
           };
           auto half = [&](int h) {
             const int tk = 16 * h + g;
-            const typename K::Row ra = keys.row(sp, tk, Pk), rb = keys.row(sp, tk + 8, Pk);
+            const typename K::Row ra = keys.row(sp, 16 * h, Pk), rb = keys.row(sp, 16 * h + 8, Pk);
             float na = 1.f, nb = 1.f;
             if (KB) {
               const __half* nm = reinterpret_cast<const __half*>(sp + z.off_kside) + tk;

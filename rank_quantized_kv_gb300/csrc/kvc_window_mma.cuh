@@ -116,6 +116,28 @@ struct Width {
   }
 };
 
+// Where a lane reads a chunk of a token's row: words from byte `at` on, shifted right by
+// `shift`.  Tokens eight further on lie 8 P bytes further on, a multiple of 4, so that
+// neither depends on them.  A chunk that does not exist reads the row's first bytes:
+// what it gives meets weights of zero, or a sum that nobody reads.
+struct ChunkPlace {
+  uint32_t at, shift;
+  __device__ void set(int byte) {
+    at = (uint32_t)byte & ~3u;
+    shift = 8 * ((uint32_t)byte & 3u);
+  }
+  // wide: the chunk may have eight bytes.
+  __device__ uint2 read(const unsigned char* rows, bool wide) const {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(rows + at);
+    uint2 b;
+    const uint32_t w1 = p[1];
+    b.x = __funnelshift_r(p[0], w1, shift);
+    b.y = 0u;
+    if (wide) b.y = __funnelshift_r(w1, p[2], shift);
+    return b;
+  }
+};
+
 // ---------------------------------------------------------------- keys
 
 // How a warp reads the keys of 16 tokens: KB > 0, a codebook of KB bits over 16 KS
@@ -144,8 +166,9 @@ struct Keys {
 
   const unsigned char* tab;  // the table in shared memory
   uint32_t lane_at;     // where this lane's copy starts in an entry
-  int off[KS / 2];      // uniform: first bytes of the lane's chunks, -1 past the last
+  ChunkPlace place[KS / 2];  // uniform: the lane's chunks of token g
   Width width[KS / 2];
+  bool wide[KS / 2];    // some lane's has eight-bit codes
 
   // The scale of the centroids: a power of two that brings the largest to [8, 16).
   static __device__ float table_scale(const Params& kp) {
@@ -187,25 +210,27 @@ struct Keys {
     tab = table;
     lane_at = (threadIdx.x & 31) * (kShift == 8 ? 8 : 4);
   }
-  // A job's basis (uniform keys).
-  __device__ void basis(const Params& kp, int beta) {
+  // A job's basis (uniform keys): rows of Pk bytes.
+  __device__ void basis(const Params& kp, int beta, int Pk) {
     if (!KB)
 #pragma unroll
       for (int s = 0; s < KS / 2; ++s) {
         const uint32_t e = chunk_entry(kp, beta, 4 * s + (threadIdx.x & 3));
-        off[s] = e ? (int)(e & 0xffffu) : -1;
+        place[s].set((int)((threadIdx.x & 31) >> 2) * Pk + (int)(e & 0xffffu));
         width[s].set(e);
+        wide[s] = __any_sync(kFull, width[s].w == 8);
       }
   }
   // The packed position of the first of the four codes that lane c has of step s.
   static __device__ int position(int s, int c) { return KB ? c * kCodes + 4 * s : 8 * (4 * (s / 2) + c) + 4 * (s & 1); }
 
   // What a lane holds of a token's row: the words of its codes (codebook).
-  struct Row { uint32_t w[kWords]; const unsigned char* rows; int at; };
-  __device__ Row row(const unsigned char* rows, int token, int Pk) const {
+  struct Row { uint32_t w[kWords]; const unsigned char* rows; };
+  // (token g + `ahead`, a multiple of 8)
+  __device__ Row row(const unsigned char* rows, int ahead, int Pk) const {
     Row r;
     if (KB) {
-      const int a = token * (2 * KS * KB) + (threadIdx.x & 3) * (kCodes * KB / 8);
+      const int a = (ahead + (int)((threadIdx.x & 31) >> 2)) * (2 * KS * KB) + (threadIdx.x & 3) * (kCodes * KB / 8);
       if ((kCodes * KB / 8) % 4 == 0) {
         const unsigned char* p = rows + a;
         if (kWords == 4) {
@@ -223,8 +248,7 @@ struct Keys {
         r.w[0] = v.x; r.w[1 % kWords] = v.y;
       }
     } else {
-      r.rows = rows;
-      r.at = token * Pk;
+      r.rows = rows + ahead * Pk;
     }
     return r;
   }
@@ -232,13 +256,10 @@ struct Keys {
   // hi[1] the others; their second pieces in lo.
   __device__ void step(const Row& r, int s, uint32_t (&hi)[2], uint32_t (&lo)[2]) const {
     if constexpr (KB == 0) {
-      hi[0] = hi[1] = 0u;
-      if (off[s / 2] >= 0) {
-        const Width& w = width[s / 2];
-        const uint2 b = w.split(bits_at(r.rows, r.at + off[s / 2]));
-        hi[0] = w.pair(b, 2 * (s & 1));
-        hi[1] = w.pair(b, 2 * (s & 1) + 1);
-      }
+      const Width& w = width[s / 2];
+      const uint2 b = w.split(place[s / 2].read(r.rows, wide[s / 2]));
+      hi[0] = w.pair(b, 2 * (s & 1));
+      hi[1] = w.pair(b, 2 * (s & 1) + 1);
       lo[0] = lo[1] = 0u;
     } else if constexpr (kPairs) {
 #pragma unroll

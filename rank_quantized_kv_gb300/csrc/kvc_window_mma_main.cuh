@@ -200,16 +200,21 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][m][e] = 0.f;
     }
-    keys.basis(kp, kbeta);
-    // uniform values: a lane has chunks g and 8 + g of a row
-    Width vwidth[V::kUniform ? 2 : 1];
-    int voff[V::kUniform ? 2 : 1];
+    keys.basis(kp, kbeta, Pk);
+    // uniform values: a lane has chunks g and 8 + g of tokens 2 c and 2 c + 1 (and 8 more)
+    constexpr int SETS = V::kUniform ? 2 : 1;
+    Width vwidth[SETS];
+    ChunkPlace vplace[SETS][2];
+    bool vwide[SETS];
+    const bool two = V::kUniform && vch[8];
     if (V::kUniform)
 #pragma unroll
-      for (int e = 0; e < (V::kUniform ? 2 : 1); ++e) {
+      for (int e = 0; e < SETS; ++e) {
         const uint32_t x = vch[8 * e + g];
         vwidth[e].set(x);
-        voff[e] = x ? (int)(x & 0xffffu) : -1;
+        vwide[e] = __any_sync(kFull, vwidth[e].w == 8);
+        vplace[e][0].set(2 * c * Pv + (int)(x & 0xffffu));
+        vplace[e][1].set((2 * c + 1) * Pv + (int)(x & 0xffffu));
       }
     float sref = V::kUniform ? 1.f : 0.f, inv_sref = sref;
     // tiles that all rows see whole: t0 >= see0 and t0 <= see1, and t0 > see2 or t0 < see3
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
           const int tok = 16 * (h0 + h) + g;
-          const typename K::Row ra = keys.row(sp, tok, Pk), rb = keys.row(sp, tok + 8, Pk);
+          const typename K::Row ra = keys.row(sp, 16 * (h0 + h), Pk), rb = keys.row(sp, 16 * (h0 + h) + 8, Pk);
           if constexpr (PAIRED && KB) {
             float d[2][4], small[2][4];  // of tokens g, of tokens g + 8: both pieces of their codes
 #pragma unroll
@@ -468,22 +473,20 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
               product(2 * q + 1, a1);
             }
           } else {
-            const unsigned char* vr = sp + z.off_v;
+            const unsigned char* vr = sp + z.off_v + 16 * (h0 + h) * Pv;
 #pragma unroll
-            for (int set = 0; set < 2; ++set) {
-              if (!vch[8 * set]) break;  // (the same for all lanes)
-              const int e = V::kUniform ? set : 0;
+            for (int e = 0; e < SETS; ++e) {
+              if (e && !two) break;
               uint2 v[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                v[q] = voff[e] < 0 ? make_uint2(0u, 0u)
-                                   : vwidth[e].split(bits_at(vr, (16 * (h0 + h) + 2 * c + (q & 1) + 8 * (q >> 1)) * Pv + voff[e]));
+                v[q] = vwidth[e].split(vplace[e][q & 1].read(vr + (q >> 1) * 8 * Pv, vwide[e]));
 #pragma unroll
               for (int m = 0; m < 4; ++m) {
                 uint32_t a[4];
                 vwidth[e].both(v[0], v[1], m, &a[0], &a[1]);
                 vwidth[e].both(v[2], v[3], m, &a[2], &a[3]);
-                product(4 * set + m, a);
+                product(4 * e + m, a);
               }
             }
           }
