@@ -444,8 +444,9 @@ __global__ void __launch_bounds__(256 * GROUPS)
   int64_t c0 = lo * t.grid / t.total;
   while (window_run(t, c0 + 1) <= lo) ++c0;
   while (window_run(t, c0) > lo) --c0;
-  int64_t c1 = c0;
+  int64_t c1 = max(c0, (hi * t.grid - 1) / t.total);
   while (window_run(t, c1 + 1) < hi) ++c1;
+  while (window_run(t, c1) >= hi) --c1;
   const int splits = (int)(c1 - c0) + 1;
   const size_t p0 = (size_t)(job + c0);
   if (vu)
@@ -692,15 +693,20 @@ size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool gener
   t.mma = t.tc = 0;
   int ctas = 12;  // of an SM: the CUDA cores'
   if (!generic && !t.prod) {
-    // Many rows: tcgen05, whose jobs cost the same from one row to 128.  Weights take
-    // scores to fp32's precision, which codebooks have in the other kernel alone.
-    if (t.rows > kTcRows && t.cb_mul > 0.f && (!t.weights || kp.mode == KVC_MODE_UNIFORM))
+    // Small calls are latency: jobs of eight rows while all of their tiles find a warp
+    // twice (15 slots of 21 rows, 500 tokens: main kernel SMALL_A us, SMALL_B in jobs of
+    // 32).  Many rows: tcgen05, whose jobs cost the same from one row to 128.  Weights
+    // take scores to fp32's precision, which codebooks have in the other kernel alone.
+    t.rt = 8;
+    const int64_t tiles8 = (int64_t)kp.n_slots * ((t.rows + 7) / 8) * most_tiles(t, kWindowTile, t.rt);
+    const bool small = tiles8 <= 2 * 2 * 8 * (int64_t)sms;
+    if (!small && t.rows > kTcRows && t.cb_mul > 0.f && (!t.weights || kp.mode == KVC_MODE_UNIFORM))
       t.K = window_tc_k(kp, vp, t);
     if (t.K) {
       t.tc = 1;
       ctas = 1;
     } else {
-      const int nt = t.rows <= 8 ? 1 : t.rows <= 16 ? 2 : 4;
+      const int nt = small || t.rows <= 8 ? 1 : t.rows <= 16 ? 2 : 4;
       const int n = window_mma_ctas(kp, vp, t, nt);
       if (n) {
         t.mma = nt;
@@ -736,9 +742,9 @@ cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs 
     if (e != cudaSuccess) return e;
   }
   const unsigned row_blocks = (unsigned)(kp.n_slots * ((t.rows + kRows - 1) / kRows));
-  // (projection of 64 slots of 128 rows, 32 columns: PROJ_A us on the tensor cores, 19.5
+  // (projection of 64 slots of 128 rows, 32 columns: 10.5 us on the tensor cores, 19.5
   // in fp32; few rows are latency, and the fp32 kernel has more blocks for them)
-  if (t.tc || (t.mma && t.rows > 32 && window_projects(kp, t))) {
+  if (t.tc || (t.mma && t.rows > 32 && (int64_t)kp.n_slots * t.rows >= 4096 && window_projects(kp, t))) {
     e = launch_window_project(kp, t, s, nk);
   } else {
     window_prep_kernel<<<dim3(row_blocks, (unsigned)t.c1_parts), kPrepThreads, 0, s>>>(kp, t);
