@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from contextlib import nullcontext
 from ctypes import POINTER, byref, c_float, c_int32, c_int64, c_size_t, c_uint8, c_void_p
 
 import numpy as np
@@ -279,6 +280,9 @@ def store_bytes(mode, B, H, D, *, capacity, r=None, V=None, bits=None, qmin=None
 def _stream_ptr(stream, device):
     import torch
 
+    if stream is None and device.type == "cuda" and device.index is not None:
+        # the raw handle: building a Stream object costs 2 us a call
+        return c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return c_void_p(stream.cuda_stream)
@@ -617,18 +621,15 @@ def attend_tree(keys: "KVCacheLayer", values: "KVCacheLayer", q, mask=None, firs
 
 def _window_desc(keys, values, q, window, sinks, first, scale, weights, decay):
     """Check the arguments of attend_window and put them into a descriptor (without out)."""
-    import torch
-
     dt = _torch_dtypes()
-    q_dtype = 0 if q.dtype == dt["f32"] else 1 if q.dtype == dt["f16"] else 2 if q.dtype == dt["bf16"] else -1
+    t = q.dtype
+    q_dtype = 0 if t == dt["f32"] else 1 if t == dt["f16"] else 2 if t == dt["bf16"] else -1
     if q.dim() != 4 or q_dtype < 0 or q.stride(3) != 1:
         raise ValueError("q must be [B, Hq, N, D] fp32/fp16/bf16 with a contiguous last dimension")
     B, Hq, N, D = q.shape
     if B != keys.B or D != keys.D:
         raise ValueError(f"q must be [{keys.B}, Hq, N, {keys.D}], got {tuple(q.shape)}")
-    if first is not None and (first.dtype != torch.int32 or tuple(first.shape) != (B,)
-                              or not first.is_contiguous()):
-        raise ValueError(f"first must be a contiguous int32 tensor [{B}]")
+    _check_first(first, B)
     wb = wh = 0
     if weights is not None:
         wb, wh = _check_weights("weights", weights, keys, len(keys))
@@ -640,16 +641,29 @@ def _window_desc(keys, values, q, window, sinks, first, scale, weights, decay):
                        weights_stride_b=wb, weights_stride_h=wh, decay=decay)
 
 
-def _check_weights(name, weights, layer, n):
-    """Strides (batch, head) of accumulated weights [B, H, >= n]."""
+def _check_first(first, B):
     import torch
 
-    if (weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[0] != layer.B
-            or weights.shape[1] != layer.H or weights.shape[2] < n
-            or (weights.shape[2] > 1 and weights.stride(2) != 1)):
-        raise ValueError(f"{name} must be an fp32 tensor [{layer.B}, {layer.H}, >= {n}] with a "
-                         "contiguous last dimension")
-    return weights.stride(0), weights.stride(1)
+    if first is not None and (first.dtype != torch.int32 or first.shape != (B,) or not first.is_contiguous()):
+        raise ValueError(f"first must be a contiguous int32 tensor [{B}]")
+
+
+def _check_weights(name, weights, layer, n):
+    """Strides (batch, head) of accumulated weights [B, H, >= n]."""
+    if weights.dtype == _torch_dtypes()["f32"] and weights.dim() == 3:
+        B, H, S = weights.shape
+        sb, sh, st = weights.stride()
+        if B == layer.B and H == layer.H and S >= n and (S <= 1 or st == 1):
+            return sb, sh
+    raise ValueError(f"{name} must be an fp32 tensor [{layer.B}, {layer.H}, >= {n}] with a "
+                     "contiguous last dimension")
+
+
+def _on_stream(stream):
+    """What a call allocates belongs to the stream that uses it."""
+    import torch
+
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def attend_window_workspace_bytes(keys: "KVCacheLayer", values: "KVCacheLayer", q, window=0,
@@ -680,27 +694,18 @@ def attend_window(keys: "KVCacheLayer", values: "KVCacheLayer", q, window=0, sin
     lib = keys._lib
     d = _window_desc(keys, values, q, window, sinks, first, scale, weights, decay)
     out_dt = _torch_dtypes()[values.out_dtype]
-    if out is None or workspace is None:
-        # what the call allocates belongs to the stream that uses it
-        ctx = None if stream is None else torch.cuda.stream(stream)
-        if ctx is not None:
-            ctx.__enter__()
-        try:
-            if out is None:
-                out = torch.empty(q.shape, dtype=out_dt, device=keys.device)
-            if workspace is None:
-                n = c_size_t()
-                _check(lib.kvc_attend_window_workspace_bytes(keys._h, values._h, byref(d), byref(n)))
-                workspace = torch.empty(n.value, dtype=torch.uint8, device=keys.device)
-        finally:
-            if ctx is not None:
-                ctx.__exit__(None, None, None)
-    if out.shape != q.shape or out.dtype != out_dt or out.stride(3) != 1:
+    if out is not None and (out.shape != q.shape or out.dtype != out_dt or out.stride(3) != 1):
         raise ValueError("out must be [B, Hq, N, D] of the value layer's out_dtype, last dimension contiguous")
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dt, device=keys.device)
+        if workspace is None:
+            n = c_size_t()
+            _check(lib.kvc_attend_window_workspace_bytes(keys._h, values._h, byref(d), byref(n)))
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=keys.device)
     d.out = out.data_ptr()
     d.out_stride_b, d.out_stride_h, d.out_stride_t, _ = out.stride()
-    _check(lib.kvc_attend_window(keys._h, values._h, byref(d), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(),
+    _check(lib.kvc_attend_window(keys._h, values._h, byref(d), workspace.data_ptr(), workspace.nbytes,
                                  _stream_ptr(stream, keys.device)))
     return out
 
@@ -721,9 +726,7 @@ def evict(keys: "KVCacheLayer", values: "KVCacheLayer", weights, keep: int, sink
     import torch
 
     keep = int(keep)
-    if first is not None and (first.dtype != torch.int32 or tuple(first.shape) != (keys.B,)
-                              or not first.is_contiguous()):
-        raise ValueError(f"first must be a contiguous int32 tensor [{keys.B}]")
+    _check_first(first, keys.B)
     d = _EvictDesc(keep=keep, sinks=int(sinks), recent=int(recent),
                    first=None if first is None else first.data_ptr())
     if weights is not None:
@@ -736,15 +739,9 @@ def evict(keys: "KVCacheLayer", values: "KVCacheLayer", weights, keep: int, sink
             d.dst_weights_stride_b, d.dst_weights_stride_h = _check_weights(
                 "the destination's weights", dw, keys, len(dk) + keep)
             d.dst_weights = dw.data_ptr()
-    ctx = None if stream is None else torch.cuda.stream(stream)
-    if ctx is not None:  # what the call allocates belongs to the stream that uses it
-        ctx.__enter__()
-    try:
-        index = torch.empty(keys.B, keys.H, max(keep, 0), dtype=torch.int32, device=keys.device)
+    with _on_stream(stream):
+        index = torch.empty((keys.B, keys.H, max(keep, 0)), dtype=torch.int32, device=keys.device)
         first_out = None if first is None else torch.empty_like(first)
-    finally:
-        if ctx is not None:
-            ctx.__exit__(None, None, None)
     d.index = index.data_ptr() if keep > 0 else None
     d.first_out = None if first_out is None else first_out.data_ptr()
     _check(keys._lib.kvc_evict(keys._h, values._h, byref(d), _stream_ptr(stream, keys.device)))
