@@ -256,6 +256,7 @@ struct WindowArgs {
   float* part = nullptr;
   float2* stats = nullptr;
   float* wpart = nullptr;                // workspace: weights of each share of the rows [wsplits][n_slots][S]
+  float* scores = nullptr;               // workspace: scores of up to 8 rows [n_slots][tps][32][4 or 8], log2
 };
 // Shared memory of the tensor-core kernels: where a warp's ring starts, the bytes
 // of one of its stages and where their parts start (key rows lie first).

@@ -683,6 +683,8 @@ size_t lay_out(const Params& kp, WindowArgs& t, void* workspace) {
   t.wscale = take.operator()<float>(jobs * t.rt);
   t.stats = t.weights ? take.operator()<float2>(rows) : nullptr;
   t.wpart = take.operator()<float>(t.wsplits > 1 ? (size_t)t.wsplits * kp.n_slots * t.S : 0);
+  const size_t scores = (size_t)kp.n_slots * t.tps * kWindowTile * (t.rows <= 4 ? 4 : 8);
+  t.scores = t.weights && t.mma && t.rows <= 8 ? take.operator()<float>(scores) : nullptr;
   return take.used;
 }
 

@@ -47,6 +47,10 @@ struct Tiles {
   }
   __device__ int count() const { return na + nb; }
   __device__ int tile(int i) const { return i < na ? a + i : b + i - na; }
+  // Tile t's place among them, -1: not one of them.
+  __device__ int index(int t) const {
+    return t >= b && t < b + nb ? na + t - b : t >= a && t < a + na ? t - a : -1;
+  }
 };
 
 }  // namespace kvc

@@ -16,23 +16,22 @@ constexpr int kChunkTiles = 16;  // 8-row tiles whose weights are in shared memo
 
 // The weights that the tokens of a slot receive: the scores again, p = 2^(s - m) / l.
 // A warp decodes the keys of 16 tokens at a time into operand registers once and meets all rows
-// of a chunk with them, whose weights lie in shared memory (ROWS 8 or 4: that many at
-// most, in registers, as in the main kernel); a token's sums stay in two registers of four lanes.  CTAs take runs of
+// of a chunk with them, whose weights lie in shared memory; a token's sums stay in two
+// registers of four lanes.  CTAs take runs of
 // the slots' tiles.  Where there are more rows than a chunk the keys are decoded again
 // for the next one, by the same warp, which then adds to what it wrote.
-template <int KB, int KS, int ROWS>
-__global__ void __launch_bounds__((ROWS ? kWarps : kManyWarps) * 32, ROWS ? 2 : 1)
+template <int KB, int KS>
+__global__ void __launch_bounds__(kManyWarps * 32, 1)
     window_weights_mma_kernel(const Params kp, const WindowArgs t, const WindowShape z) {
-  constexpr bool ONE = ROWS != 0, HALF = ROWS == 4;
-  using K = Keys<KB, KS, ONE>;
-  constexpr int NT = ONE ? 1 : kChunkTiles, WARPS = ONE ? kWarps : kManyWarps;
+  using K = Keys<KB, KS, false>;
+  constexpr int NT = kChunkTiles, WARPS = kManyWarps;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(256) unsigned char table[K::kTable ? K::kTable : 16];
   __shared__ __align__(16) float4 rowc[8 * NT];  // per row: score factor, -m, 1 / l, position
   __shared__ float row_mul[8 * NT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int cr = HALF ? 2 * (c & 1) : 2 * c;
-  uint4* wfrag = reinterpret_cast<uint4*>(smem);  // [NT][step][32], unless in registers
+  const int cr = 2 * c;
+  uint4* wfrag = reinterpret_cast<uint4*>(smem);  // [NT][step][32]
   unsigned char* ring = smem + z.off_ring + warp * kStages * z.stage;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
   if (KB) K::fill(kp, table, WARPS * 32);
@@ -129,24 +128,14 @@ __global__ void __launch_bounds__((ROWS ? kWarps : kManyWarps) * 32, ROWS ? 2 : 
       }
       __syncthreads();
       auto fragment = [&](int s, int nt) {
-        const int r = HALF ? g & 3 : 8 * nt + g, j = K::position(s, c);
+        const int r = 8 * nt + g, j = K::position(s, c);
         float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < nr && j < t.NCk) w = *reinterpret_cast<const float4*>(w0 + (size_t)r * t.NCk + j);
         return weight_pieces(w, row_mul[r]);
       };
-      uint4 wreg[ONE && !HALF ? KS : 1];
-      uint2 whalf[HALF ? KS : 1];
-      if (HALF) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) whalf[HALF ? s : 0] = one_piece(fragment(s, 0), g >= 4);
-      } else if (ONE) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) wreg[ONE && !HALF ? s : 0] = fragment(s, 0);
-      } else {
 #pragma unroll 4
-        for (int e = warp; e < KS * tiles; e += WARPS) wfrag[e * 32 + lane] = fragment(e % KS, e / KS);
-        __syncthreads();
-      }
+      for (int e = warp; e < KS * tiles; e += WARPS) wfrag[e * 32 + lane] = fragment(e % KS, e / KS);
+      __syncthreads();
       int st = 0;
       for (; i < i1; i += WARPS) {
         copy_wait<kStages - 2>();
@@ -185,72 +174,30 @@ __global__ void __launch_bounds__((ROWS ? kWarps : kManyWarps) * 32, ROWS ? 2 : 
               na = __half2float(nm[0]);
               nb = __half2float(nm[8]);
             }
-            float s[4];
-            if constexpr (ONE && KB) {
-              float d[2][4], small[2][4];
+            uint32_t hi[KS][4], lo[KS][4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) d[0][e] = d[1][e] = small[0][e] = small[1][e] = 0.f;
+            for (int k = 0; k < KS; ++k) {
+              uint32_t ha[2], la[2], hb[2], lb[2];
+              keys.step(ra, k, ha, la);
+              keys.step(rb, k, hb, lb);
+              hi[k][0] = ha[0]; hi[k][1] = hb[0]; hi[k][2] = ha[1]; hi[k][3] = hb[1];
+              lo[k][0] = la[0]; lo[k][1] = lb[0]; lo[k][2] = la[1]; lo[k][3] = lb[1];
+            }
+#pragma unroll 2
+            for (int nt = 0; nt < tiles; ++nt) {
+              float s[4], small[4], other[4];
 #pragma unroll
-              for (int k = 0; k < KS; ++k)
+              for (int e = 0; e < 4; ++e) s[e] = small[e] = other[e] = 0.f;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  uint32_t hi[2], lo[2];
-                  keys.step(q ? rb : ra, k, hi, lo);
-                  const uint32_t a[4] = {hi[0], lo[0], hi[1], lo[1]};
-                  if (HALF) {
-                    mma_f16(d[q], a, whalf[HALF ? k : 0].x, whalf[HALF ? k : 0].y);
-                  } else {
-                    const uint4 w = wreg[HALF ? 0 : k];
-                    mma_f16(d[q], a, w.x, w.y);
-                    mma_f16(small[q], a, w.z, w.w);
-                  }
-                }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int q = e >> 1, j = e & 1;
-                s[e] = d[q][j] + (HALF ? d[q][2 + j] : d[q][2 + j] + small[q][j] + small[q][2 + j]);
-                if (HALF) s[e] += __shfl_xor_sync(kFull, s[e], 2);
+              for (int k = 0; k < KS; ++k) {
+                const uint4 w = wfrag[(nt * KS + k) * 32 + lane];
+                mma_f16(s, hi[k], w.x, w.y);
+                mma_f16(small, hi[k], w.z, w.w);
+                if (KB) mma_f16(other, lo[k], w.x, w.y);
               }
-              add(h, 0, s, na, nb);
-            } else {
-              constexpr int HK = ONE ? 1 : KS;  // steps whose operands are kept
-              uint32_t hi[HK][4], lo[HK][4];
-              auto operand = [&](int k) {
-                uint32_t ha[2], la[2], hb[2], lb[2];
-                keys.step(ra, k, ha, la);
-                keys.step(rb, k, hb, lb);
-                const int x = ONE ? 0 : k;
-                hi[x][0] = ha[0]; hi[x][1] = hb[0]; hi[x][2] = ha[1]; hi[x][3] = hb[1];
-                lo[x][0] = la[0]; lo[x][1] = lb[0]; lo[x][2] = la[1]; lo[x][3] = lb[1];
-              };
-              if (!ONE)
 #pragma unroll
-                for (int k = 0; k < KS; ++k) operand(k);
-#pragma unroll(ONE ? 1 : 2)
-              for (int nt = 0; nt < (ONE ? 1 : tiles); ++nt) {
-                float small[4], other[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = small[e] = other[e] = 0.f;
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                  if (ONE) operand(k);
-                  const int x = ONE ? 0 : k;
-                  if (HALF) {
-                    mma_f16(s, hi[x], whalf[HALF ? k : 0].x, whalf[HALF ? k : 0].y);
-                  } else {
-                    const uint4 w = ONE ? wreg[ONE && !HALF ? k : 0] : wfrag[(nt * KS + k) * 32 + lane];
-                    mma_f16(s, hi[x], w.x, w.y);
-                    mma_f16(small, hi[x], w.z, w.w);
-                    if (KB) mma_f16(other, lo[x], w.x, w.y);
-                  }
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if (HALF) s[e] += __shfl_xor_sync(kFull, s[e], 2);
-                  else s[e] += KB ? small[e] + other[e] : small[e];
-                }
-                add(h, nt, s, na, nb);
-              }
+              for (int e = 0; e < 4; ++e) s[e] += KB ? small[e] + other[e] : small[e];
+              add(h, nt, s, na, nb);
             }
           };
           half(0);
@@ -261,7 +208,7 @@ __global__ void __launch_bounds__((ROWS ? kWarps : kManyWarps) * 32, ROWS ? 2 : 
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             sum[h][j] += __shfl_xor_sync(kFull, sum[h][j], 1);
-            if (!HALF) sum[h][j] += __shfl_xor_sync(kFull, sum[h][j], 2);
+            sum[h][j] += __shfl_xor_sync(kFull, sum[h][j], 2);
           }
         const float add = c < 2 ? c ? sum[0][1] : sum[0][0] : c == 2 ? sum[1][0] : sum[1][1];
         if (tok < t.S && (decay != 1.f || add != 0.f)) wout[tok] = fmaf(decay, old, add);
@@ -270,6 +217,55 @@ __global__ void __launch_bounds__((ROWS ? kWarps : kManyWarps) * 32, ROWS ? 2 : 
       copy_wait<0>();
     }
   }
+}
+
+// The weights from the scores that the main kernel kept, of R rows at most: a lane has a
+// token of each of four tiles.  Bound by the scores' bytes, most of which still lie in L2.
+constexpr int kKeptTiles = 4;
+
+template <int R>
+__global__ void __launch_bounds__(256) window_weights_kept_kernel(const Params kp, const WindowArgs t) {
+  const int chunks = (int)((t.wtps + kKeptTiles - 1) / kKeptTiles);
+  const int64_t at = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  const int slot = (int)(at / chunks), i0 = (int)(at - (int64_t)slot * chunks) * kKeptTiles, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  if (slot >= kp.n_slots) return;
+  const int b = slot / kp.H, h = slot - b * kp.H;
+  const bool every = t.decay != 1.f;  // the old weights of all tokens are scaled
+  const Sight sight(t, b);
+  const Tiles<kTile> seen(sight, t.ctx, t.S - 1);
+  float* wout = t.weights + b * t.w_sb + h * t.w_sh;
+  const float4* scores = reinterpret_cast<const float4*>(t.scores) + (size_t)slot * t.tps * kTile * (R / 4);
+  int tok[kKeptTiles];
+  float4 y[kKeptTiles][R / 4];
+  float old[kKeptTiles], sum[kKeptTiles];
+  bool any[kKeptTiles];
+#pragma unroll
+  for (int u = 0; u < kKeptTiles; ++u) {
+    const int e = i0 + u, tile = every ? e : seen.tile(e), i = every ? seen.index(e) : e < seen.count() ? e : -1;
+    tok[u] = tile * kTile + lane;
+    any[u] = i >= 0 && tok[u] < t.S;
+    old[u] = (every || any[u]) && tok[u] < t.S && t.decay != 0.f ? wout[tok[u]] : 0.f;
+#pragma unroll
+    for (int x = 0; x < R / 4; ++x)
+      y[u][x] = any[u] ? scores[((size_t)i * kTile + lane) * (R / 4) + x] : make_float4(0.f, 0.f, 0.f, 0.f);
+    sum[u] = 0.f;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < t.rows) {
+      const float2 st = t.stats[(size_t)slot * t.rows + r];
+      const int pos = t.ctx + r / t.rep;
+#pragma unroll
+      for (int u = 0; u < kKeptTiles; ++u) {
+        const float4 v = y[u][r / 4];
+        const float s = r % 4 == 0 ? v.x : r % 4 == 1 ? v.y : r % 4 == 2 ? v.z : v.w;
+        if (any[u] && sight.sees(tok[u], pos)) sum[u] = fmaf(ex2(s - st.x), st.y, sum[u]);
+      }
+    }
+#pragma unroll
+  for (int u = 0; u < kKeptTiles; ++u)
+    if ((every || any[u]) && tok[u] < t.S && (every || sum[u] != 0.f)) wout[tok[u]] = fmaf(t.decay, old[u], sum[u]);
 }
 
 // The shares' weights added up.
@@ -288,24 +284,23 @@ __global__ void __launch_bounds__(256) window_add_weights_kernel(const Params kp
 
 using WeightsKernel = void (*)(const Params, const WindowArgs, const WindowShape);
 
-template <int ROWS>
 WeightsKernel weights_kernel_for(const Params& kp, int NCk, int* tables) {
   auto of = [&](auto keys, WeightsKernel k) {
     using K = decltype(keys);
-    *tables = ROWS ? 0 : K::kSteps * kChunkTiles * 512;
+    *tables = K::kSteps * kChunkTiles * 512;
     return k;
   };
   if (kp.mode == KVC_MODE_UNIFORM) {
-    if (NCk <= 64) return of(Keys<0, 4, ROWS != 0>{}, window_weights_mma_kernel<0, 4, ROWS>);
-    return of(Keys<0, 8, ROWS != 0>{}, window_weights_mma_kernel<0, 8, ROWS>);
+    if (NCk <= 64) return of(Keys<0, 4, false>{}, window_weights_mma_kernel<0, 4>);
+    return of(Keys<0, 8, false>{}, window_weights_mma_kernel<0, 8>);
   }
   switch (kp.cb_bits * 1000 + kp.D) {
-    case 2064: return of(Keys<2, 4, ROWS != 0>{}, window_weights_mma_kernel<2, 4, ROWS>);
-    case 3064: return of(Keys<3, 4, ROWS != 0>{}, window_weights_mma_kernel<3, 4, ROWS>);
-    case 4064: return of(Keys<4, 4, ROWS != 0>{}, window_weights_mma_kernel<4, 4, ROWS>);
-    case 2128: return of(Keys<2, 8, ROWS != 0>{}, window_weights_mma_kernel<2, 8, ROWS>);
-    case 3128: return of(Keys<3, 8, ROWS != 0>{}, window_weights_mma_kernel<3, 8, ROWS>);
-    default: return of(Keys<4, 8, ROWS != 0>{}, window_weights_mma_kernel<4, 8, ROWS>);
+    case 2064: return of(Keys<2, 4, false>{}, window_weights_mma_kernel<2, 4>);
+    case 3064: return of(Keys<3, 4, false>{}, window_weights_mma_kernel<3, 4>);
+    case 4064: return of(Keys<4, 4, false>{}, window_weights_mma_kernel<4, 4>);
+    case 2128: return of(Keys<2, 8, false>{}, window_weights_mma_kernel<2, 8>);
+    case 3128: return of(Keys<3, 8, false>{}, window_weights_mma_kernel<3, 8>);
+    default: return of(Keys<4, 8, false>{}, window_weights_mma_kernel<4, 8>);
   }
 }
 
@@ -364,9 +359,8 @@ cudaError_t launch_window_mma(const Params& kp, const Params& vp, const WindowAr
 // about 10 us to bring in, so that a warp should have four tiles for it.
 static int weights_ctas(const Params& kp, const WindowArgs& t, int64_t tiles) {
   const int64_t total = tiles * kp.n_slots;
-  const bool many = t.rows > 8 * kChunkTiles;
-  const int64_t per = t.rows <= 8 ? kWarps : many ? 4 * kManyWarps : kManyWarps;
-  return (int)std::min<int64_t>(std::max<int64_t>(total / per, kp.n_slots), (t.rows <= 8 ? 2 : 1) * (int64_t)t.sms);
+  const int64_t per = (t.rows > 8 * kChunkTiles ? 4 : 1) * kManyWarps;
+  return (int)std::min<int64_t>(std::max<int64_t>(total / per, kp.n_slots), t.sms);
 }
 
 int window_weights_splits(const Params& kp, const WindowArgs& t) {
@@ -377,18 +371,21 @@ int window_weights_splits(const Params& kp, const WindowArgs& t) {
 }
 
 cudaError_t launch_window_weights_mma(const Params& kp, const WindowArgs& t, cudaStream_t s, int* nk) {
+  if (t.scores) {
+    const int64_t warps = kp.n_slots * ((t.wtps + kKeptTiles - 1) / kKeptTiles);
+    ++*nk;
+    return launch_dependent(t.rows <= 4 ? window_weights_kept_kernel<4> : window_weights_kept_kernel<8>,
+                            (unsigned)((warps + 7) / 8), 256u, 0, s, kp, t);
+  }
   int tables = 0;
-  const bool one = t.rows <= 8;
-  const WeightsKernel k = t.rows <= 4 ? weights_kernel_for<4>(kp, t.NCk, &tables)
-                          : one       ? weights_kernel_for<8>(kp, t.NCk, &tables)
-                                      : weights_kernel_for<0>(kp, t.NCk, &tables);
+  const WeightsKernel k = weights_kernel_for(kp, t.NCk, &tables);
   WindowShape z;
-  const int warps = one ? kWarps : kManyWarps, smem = lay_out(kp, nullptr, t, tables, warps, &z);
+  const int smem = lay_out(kp, nullptr, t, tables, kManyWarps, &z);
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
   const int grid = weights_ctas(kp, t, t.wtps) * t.wsplits;
   ++*nk;
-  const cudaError_t f = launch_dependent(k, (unsigned)grid, (unsigned)warps * 32, (size_t)smem, s, kp, t, z);
+  const cudaError_t f = launch_dependent(k, (unsigned)grid, kManyWarps * 32u, (size_t)smem, s, kp, t, z);
   if (f != cudaSuccess || t.wsplits == 1) return f;
   ++*nk;
   const int64_t words = (int64_t)kp.n_slots * t.S;

@@ -317,6 +317,23 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
             sv[h][1] = __half2float(vs[8]);
           }
         }
+        if constexpr (NT == 1)
+          if (t.scores) {  // kept for the weights' pass: [token][R or 4 rows]
+            float* at = t.scores + (((size_t)slot * t.tps + i) * kMmaTile + g) * (HALF ? 4 : 8) + cr;
+#pragma unroll
+            for (int h = 0; h < HB; ++h) {
+              if (HALF) {  // (lanes c and c + 2 hold the same: a token each)
+                const bool q = c & 2;
+                const float2 y = make_float2((q ? s[h][0][2] : s[h][0][0]) * rs[0][0], (q ? s[h][0][3] : s[h][0][1]) * rs[0][1]);
+                *reinterpret_cast<float2*>(at + 4 * (16 * h + 4 * (c & 2))) = y;
+              } else {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                  *reinterpret_cast<float2*>(at + 8 * (16 * h + 8 * q)) =
+                      make_float2(s[h][0][2 * q] * rs[0][0], s[h][0][2 * q + 1] * rs[0][1]);
+              }
+            }
+          }
         uint32_t seen = ~0u;  // bit 4 (h NT + nt) + e
         float x[HB][NT][4];
 #pragma unroll
