@@ -41,9 +41,10 @@ __device__ __forceinline__ float larger(float most, float v) {
 
 // KD: steps of 16 over the head size.  OPERAND: two fp16 pieces in the layout of a
 // K-major operand without swizzle (cores of 8 rows x 8 positions, 128 contiguous bytes,
-// adjacent along K), per row the inverse of its power of two; else fp32 weights.
-template <int KD, bool OPERAND>
-__global__ void __launch_bounds__(kThreads) window_project_kernel(const Params kp, const WindowArgs t) {
+// adjacent along K), per row the inverse of its power of two; else fp32 weights.  REST:
+// fp32 queries; those of 16 bits have no second piece to speak of.
+template <int KD, bool OPERAND, bool REST>
+__global__ void __launch_bounds__(kThreads, REST ? 1 : 2) window_project_kernel(const Params kp, const WindowArgs t) {
   constexpr int D = 16 * KD, kStride = D + 8;  // (padding: a step's columns in different banks)
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int comp[128];
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) window_project_kernel(const Params k
     const int slot = job / blocks, r0 = (job - slot * blocks) * kRows;
     const int b = slot / kp.H, h = slot - b * kp.H, beta = kp.basis_of[slot];
     // this lane's rows of q: 16 warp + g and 8 more
-    uint32_t ah[KD][4], al[KD][4];
+    uint32_t ah[KD][4], al[REST ? KD : 1][4];
     float inv[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -104,7 +105,9 @@ __global__ void __launch_bounds__(kThreads) window_project_kernel(const Params k
       for (int k = 0; k < KD; ++k) {
         const uint4 p = weight_pieces(make_float4(v[k][0], v[k][1], v[k][2], v[k][3]), mul);
         ah[k][e] = p.x; ah[k][2 + e] = p.y;
-        al[k][e] = p.z; al[k][2 + e] = p.w;
+        if (REST) {
+          al[REST ? k : 0][e] = p.z; al[REST ? k : 0][2 + e] = p.w;
+        }
       }
     }
     if (beta != loaded) {
@@ -153,7 +156,6 @@ __global__ void __launch_bounds__(kThreads) window_project_kernel(const Params k
       __syncthreads();
     }
     const int tiles = t.NCk / 8;
-    const bool rest = t.q_dtype == KVC_F32;  // 16-bit queries have no second piece to speak of
     float u[16][4], most[2] = {0.f, 0.f};
 #pragma unroll
     for (int nt = 0; nt < 16; ++nt) {
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) window_project_kernel(const Params k
           const uint32_t l0 = *reinterpret_cast<const uint32_t*>(bl + at), l1 = *reinterpret_cast<const uint32_t*>(bl + at + 8);
           mma_f16(acc, ah[k], h0, h1);
           mma_f16(small, ah[k], l0, l1);
-          if (rest) mma_f16(small, al[k], h0, h1);
+          if (REST) mma_f16(small, al[REST ? k : 0], h0, h1);
         }
       }
 #pragma unroll
@@ -214,14 +216,16 @@ bool window_projects(const Params& kp, const WindowArgs& t) {
 
 cudaError_t launch_window_project(const Params& kp, const WindowArgs& t, cudaStream_t s, int* nk) {
   const int smem = 2 * t.NCk * (kp.D + 8) * 2;
-  const bool operand = t.tc != 0;
-  const auto k = kp.D == 64 ? operand ? window_project_kernel<4, true> : window_project_kernel<4, false>
-                            : operand ? window_project_kernel<8, true> : window_project_kernel<8, false>;
+  const bool operand = t.tc != 0, rest = t.q_dtype == KVC_F32;
+  const auto k = kp.D == 64 ? operand ? rest ? window_project_kernel<4, true, true> : window_project_kernel<4, true, false>
+                                      : rest ? window_project_kernel<4, false, true> : window_project_kernel<4, false, false>
+                 : operand  ? rest ? window_project_kernel<8, true, true> : window_project_kernel<8, true, false>
+                            : rest ? window_project_kernel<8, false, true> : window_project_kernel<8, false, false>;
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
   ++*nk;
   const int64_t jobs = (int64_t)kp.n_slots * ((t.rows + kRows - 1) / kRows);
-  k<<<(unsigned)std::min<int64_t>(jobs, t.sms), kThreads, smem, s>>>(kp, t);
+  k<<<(unsigned)std::min<int64_t>(jobs, (rest ? 1 : 2) * t.sms), kThreads, smem, s>>>(kp, t);
   return cudaGetLastError();
 }
 
