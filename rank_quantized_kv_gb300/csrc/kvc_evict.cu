@@ -84,7 +84,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, 
 // are one step, whose keys stay in registers.
 template <int PER, bool RESIDENT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ uint32_t hist[3][kBins];
+  __shared__ __align__(8) uint32_t hist[3][kBins];
   __shared__ uint32_t warp_sums[kSelThreads / 32];
   __shared__ uint32_t counts[2];  // keys above the threshold, equal to it
   __shared__ uint32_t digit_s, left_s;
@@ -142,19 +142,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (ctas > 1) cluster.sync();
     else __syncthreads();
     constexpr int kMine = kBins / kSelThreads;
-    uint32_t v = 0, mine[kMine];  // bins of this thread, from the top
+    static_assert(kMine == 2, "a thread's bins in one load");
+    uint2 two = *reinterpret_cast<const uint2*>(hp + kBins - 2 - 2 * tid);  // bins of this thread
+    if (ctas > 1) {
+      two = make_uint2(0u, 0u);
 #pragma unroll
-    for (int u = 0; u < kMine; ++u) {
-      const int bin = kBins - 1 - (tid * kMine + u);
-      mine[u] = hp[bin];
-      if (ctas > 1) {
-        mine[u] = 0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c < ctas) mine[u] += cluster.map_shared_rank(hp, c)[bin];
-      }
-      v += mine[u];
+      for (int c = 0; c < 8; ++c)
+        if (c < ctas) {
+          const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hp, c) + kBins - 2 - 2 * tid);
+          two.x += x.x;
+          two.y += x.y;
+        }
     }
+    const uint32_t mine[kMine] = {two.y, two.x}, v = two.x + two.y;  // from the top
     // the digit at which the running count reaches `left`
     uint32_t total;
     const uint32_t end = block_scan(v, warp_sums, &total);
