@@ -353,9 +353,9 @@ kvc_status kvc_gather(kvc_layer *dst, const kvc_layer *src, const int32_t *paren
 kvc_status kvc_accept(kvc_layer *layer, int64_t N, const int32_t *index, int64_t n, void *stream);
 
 /* Attention of the last N stored tokens over a sliding window and the first
- * tokens of the cache, which stay visible (sinks), computed from the codes as
- * kvc_attend computes; and, where asked for, the softmax weights that the stored
- * tokens receive, the measure by which kvc_evict chooses.  The N queries belong
+ * tokens of the cache, which stay visible (sinks), computed from the codes; and,
+ * where asked for, the softmax weights that the stored tokens receive, the measure
+ * by which kvc_evict chooses.  The N queries belong
  * to the last N stored tokens (appended before the call): a decode step has one, a
  * chunk of a prompt many.  Query i stands at position pos = length - N + i and sees
  * the tokens t with
@@ -368,6 +368,12 @@ kvc_status kvc_accept(kvc_layer *layer, int64_t N, const int32_t *index, int64_t
  * (below fp32's range), gets a row of NaN and gives NaN to what it sees.  What a
  * hidden token stores, infinities and NaN among it, has no effect.  Positions are
  * places in the cache: after an eviction the kept tokens are neighbours.
+ * All of it is computed in fp32, or on the tensor cores with sums and softmax
+ * statistics in fp32 and scores to fp32's precision (both factors held to 22 bits or
+ * more), the softmax weights times value scales to 22 bits (2^-25 of the row's
+ * largest at least).  Calls of more than 32 rows (Hq / H * N) a slot, unless they are
+ * short or ask for weights of codebook keys, have the roundings that
+ * kvc_attend_tree lists, but for its generic path and its layers in fp32.
  *
  *  keys       a KVC_MODE_UNIFORM or KVC_MODE_CODEBOOK layer (with or without a
  *             residual sketch and outlier stream), D at most 256.
@@ -389,7 +395,9 @@ kvc_status kvc_accept(kvc_layer *layer, int64_t N, const int32_t *index, int64_t
  *  decay      finite, >= 0.  1 adds to what is there, 0 does not read it (every
  *             token's weight is then written, 0 for hidden ones).
  * The workspace is caller-owned scratch, overwritten by the call: calls that
- * may overlap need one each. */
+ * may overlap need one each.  With weights and at most eight rows a slot it holds a
+ * score of every row and visible token (16 or 32 bytes a token).  A captured call
+ * keeps the layers' length of its capture. */
 typedef struct {
   const void *q;
   int32_t q_dtype;
@@ -413,7 +421,9 @@ kvc_status kvc_attend_window_workspace_bytes(const kvc_layer *keys, const kvc_la
 
 /* Run it, asynchronously on `stream`.  workspace: device, 256-byte aligned.
  * KVC_EINVAL for unsupported modes or shapes, mismatched layers, overlapping rows
- * of out or weights, host pointers or a short workspace; nothing is launched then. */
+ * of out or weights, host pointers or a short workspace; nothing is launched then.
+ * kvc_sync_status(keys) reports KVC_ETIMEOUT, and out and weights are undefined, where
+ * the limit of the kernel for many rows ran out (kvc_set_wait_limit). */
 kvc_status kvc_attend_window(const kvc_layer *keys, const kvc_layer *values,
                              const kvc_window_desc *desc, void *workspace, size_t workspace_bytes,
                              void *stream);
@@ -441,7 +451,8 @@ kvc_status kvc_attend_window(const kvc_layer *keys, const kvc_layer *values,
  *                the first token of each entry after the eviction; not `first`.
  *  index         device int32 [B*H][keep]: receives the kept tokens, ascending.
  *  dst_weights   device fp32 or NULL; must not overlap weights.  Not in place.
- * Asynchronous on `stream`.  KVC_ECAPACITY if the rows do not fit, KVC_EINVAL for
+ * Asynchronous on `stream`; the lengths change on the host at once, and a captured
+ * call keeps those of its capture.  KVC_ECAPACITY if the rows do not fit, KVC_EINVAL for
  * mismatched layers, counts out of range or host pointers; nothing is written then. */
 typedef struct {
   int64_t keep, sinks, recent;
@@ -606,14 +617,14 @@ kvc_status kvc_fit_uniform(const kvc_fit_desc *desc, void *workspace, size_t wor
 /* Limit, in nanoseconds, of the waits inside the warp-specialised tensor-core
  * append kernel (one role waiting for another: a tile loaded, an accumulator
  * written or released) and, for a key layer, of the time in which a CTA of
- * kvc_attend_tree's tensor-core kernel finishes no tile of 128 tokens (looked at
- * every 20 us or so).  A kernel whose limit runs out stops its work, waits for
+ * kvc_attend_tree's tensor-core kernel, or of kvc_attend_window's for many rows,
+ * finishes no tile of 128 tokens (looked at every 20 us or so).  A kernel whose limit runs out stops its work, waits for
  * its copies and tensor-core work already in flight (up to 2 s), frees its
  * tensor memory and returns; kvc_sync_status then reports KVC_ETIMEOUT and the
  * rows appended, or the output, of that call are undefined.  ns == 0 restores
  * the default of 2 s; a limit shorter than a kernel's normal waits makes every
- * call time out (tree attention: every call whose CTAs run for longer than that
- * and 20 us).  Host-only.  KVC_EINVAL if ns < 0. */
+ * call time out (the attention kernels: every call whose CTAs run for longer than
+ * that and 20 us).  Host-only.  KVC_EINVAL if ns < 0. */
 kvc_status kvc_set_wait_limit(kvc_layer *layer, int64_t ns);
 
 /* Synchronise `stream`, then read and clear the layer's device error word:

@@ -18,8 +18,11 @@
 // stretch of chunks at a time, reads before a cluster barrier and writes after it:
 // what it writes lies below the sources of all later stretches.
 //
-// Bound: HBM, the weights read once (and twice more from L2) and the kept rows read
-// and written; for small caches two launches.
+// Bound: the move by HBM's sectors, kept rows that start and end inside them: 128
+// slots, 4096 of 16384 rows of 48 + 128 bytes kept, 94 MB of rows each way in 50 us,
+// with 138 MB read in sectors.  Select by the latency of its passes: 128 slots of 16384
+// tokens 16 us; 8 slots of 130001 tokens, eight CTAs each, 25.5, of which the cluster's
+// exchanges take about half.  Small caches are two launches (6 + 4 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -424,8 +427,7 @@ cudaError_t launch_evict(const Params& kp, const Params& vp, const Params& dkp, 
     return c;
   };
   // select: one CTA where the keys of all tokens fit its registers (a cluster costs
-  // its barriers and remote reads: 128 slots of 16384 tokens SELECT_A us, SELECT_B with
-  // two CTAs each)
+  // its barriers and remote reads: 128 slots of 16384 tokens 16 us, 30 with two CTAs each)
   const int sel = pick((a.S + kSelStep - 1) / kSelStep, 1, 8);
   const int64_t per = (a.S + (int64_t)sel * kSelThreads - 1) / ((int64_t)sel * kSelThreads);
   const auto kernel = per <= 4    ? evict_select_kernel<4, true>

@@ -17,9 +17,12 @@
 //            zero for a row that sees no token, NaN for one that sees a score of
 //            NaN or of +inf, or scores of -inf alone;
 //   weights  w[t] = decay w[t] + sum of p_t over the rows of a slot.  p needs the
-//            row's whole sum, so it takes a second pass over the keys: scores are
-//            computed again from the codes (50 bytes a token at most widths, where
-//            stored scores of four rows would take 16 written and 16 read).  Tokens
+//            row's whole sum, so it takes a second pass.  Of at most eight rows the
+//            tensor-core kernel keeps its scores for it (16 or 32 bytes a token,
+//            mostly still in L2 when they are read: 128 slots, 4 rows, 16384 tokens
+//            11.7 us and 3 more in the main kernel; computed again from the 50 bytes of
+//            a token's codes 56).  Of more rows, whose scores would outgrow the codes
+//            and L2, they are computed again.  Tokens
 //            are split over blocks and a token's rows are added in order: no atomics.
 //
 // This file: the queries' projection, the CUDA-core kernels, which take every layer
@@ -409,7 +412,7 @@ __host__ __device__ __forceinline__ bool combines_cuts(const Params& vp, const W
 // a row.  Thread (d, q) of a group of 256 holds channel d of rows 4 q .. 4 q + 3; the
 // groups share the partials and, of uniform values, the sum over components.  Bound by
 // the latency of the partials' reads where few blocks are at work: one sequence of 8
-// heads, 38 partials a row COMB_A us with four groups, 15 with one.
+// heads, 38 partials a row 9.9 us with four groups, 12 with one.
 template <int GROUPS>
 __global__ void __launch_bounds__(256 * GROUPS)
     window_combine_kernel(const Params kp, const Params vp, const WindowArgs t) {
@@ -696,8 +699,10 @@ size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool gener
   int ctas = 12;  // of an SM: the CUDA cores'
   if (!generic && !t.prod) {
     // Small calls are latency: jobs of eight rows while all of their tiles find a warp
-    // twice (15 slots of 21 rows, 500 tokens: main kernel SMALL_A us, SMALL_B in jobs of
-    // 32).  Many rows: tcgen05, whose jobs cost the same from one row to 128.  Weights
+    // twice (15 slots of 21 rows, 500 tokens, 4-bit keys: main kernel 13.9 us, 28.7 in
+    // jobs of 32).  Many rows: tcgen05, whose jobs cost the same from one row to 128 (32
+    // slots of 36 rows, 4096 tokens: 63 us in all, 72 on the warps' tensor cores; of 128
+    // rows 69 and 118).  Weights
     // take scores to fp32's precision, which codebooks have in the other kernel alone.
     t.rt = 8;
     const int64_t tiles8 = (int64_t)kp.n_slots * ((t.rows + 7) / 8) * most_tiles(t, kWindowTile, t.rt);
@@ -744,7 +749,7 @@ cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs 
     if (e != cudaSuccess) return e;
   }
   const unsigned row_blocks = (unsigned)(kp.n_slots * ((t.rows + kRows - 1) / kRows));
-  // (projection of 64 slots of 128 rows, 32 columns: 10.5 us on the tensor cores, 19.5
+  // (projection of 64 slots of 128 rows, 32 columns: 9.1 us on the tensor cores, 19.5
   // in fp32; few rows are latency, and the fp32 kernel has more blocks for them)
   if (t.tc || (t.mma && t.rows > 32 && (int64_t)kp.n_slots * t.rows >= 4096 && window_projects(kp, t))) {
     e = launch_window_project(kp, t, s, nk);

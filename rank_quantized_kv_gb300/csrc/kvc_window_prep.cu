@@ -6,8 +6,10 @@
 // 22 bits of what an fp32 sum would; the small ones are summed apart.
 //
 // A CTA takes runs of 128 rows of a slot, a warp 16 of them with all columns; V lies in
-// shared memory, a column's values together, until another basis is needed.  8 heads of 8192 rows, 128 x 128: see the
-// design's table (the fp32 product took 225 us).
+// shared memory, a column's values together, until another basis is needed.  Bound by
+// latency: a warp loads, converts, multiplies and stores in turn, so that a second CTA
+// on an SM counts for most (8 heads of 8192 rows, 128 x 128, bf16: 28 us, one CTA 45;
+// the fp32 product took 225).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
