@@ -20,7 +20,7 @@ constexpr int kChunkTiles = 16;  // 8-row tiles whose weights are in shared memo
 // registers of four lanes.  CTAs take runs of the slots' tiles.  Where there are more
 // rows than a chunk the keys are decoded again for the next one, by the same warp, which
 // then adds to what it wrote.  Bound by its products and exponentials: 64 slots, 128 rows,
-// 4096 tokens of 32 components 54 us, of which the exponentials alone would take 7.
+// 4096 tokens of 32 components 50 us (40 positions in three steps; in four 54), of which the exponentials alone would take 7.
 template <int KB, int KS>
 __global__ void __launch_bounds__(kManyWarps * 32, 1)
     window_weights_mma_kernel(const Params kp, const WindowArgs t, const WindowShape z) {
@@ -97,21 +97,21 @@ __global__ void __launch_bounds__(kManyWarps * 32, 1)
       // four rows of a warp at a time, their loads first
 #pragma unroll 1
       for (int rb = warp; rb < 8 * tiles; rb += 4 * WARPS) {
-        float w[4][K::kSteps / 2], most[4];
+        float w[4][(KS + 1) / 2], most[4];
         float2 st[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = rb + u * WARPS;
           st[u] = r < nr ? t.stats[(size_t)slot * t.rows + r0 + r] : make_float2(0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < K::kSteps / 2; ++j)
+          for (int j = 0; j < (KS + 1) / 2; ++j)
             w[u][j] = r < nr && lane + 32 * j < t.NCk ? fabsf(w0[(size_t)r * t.NCk + lane + 32 * j]) : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           most[u] = 0.f;
 #pragma unroll
-          for (int j = 0; j < K::kSteps / 2; ++j)
+          for (int j = 0; j < (KS + 1) / 2; ++j)
             if (w[u][j] <= 3.4e38f) most[u] = fmaxf(most[u], w[u][j]);
         }
 #pragma unroll
@@ -293,6 +293,8 @@ WeightsKernel weights_kernel_for(const Params& kp, int NCk, int* tables) {
     return k;
   };
   if (kp.mode == KVC_MODE_UNIFORM) {
+    if (NCk <= 32) return of(Keys<0, 2, false>{}, window_weights_mma_kernel<0, 2>);
+    if (NCk <= 48) return of(Keys<0, 3, false>{}, window_weights_mma_kernel<0, 3>);
     if (NCk <= 64) return of(Keys<0, 4, false>{}, window_weights_mma_kernel<0, 4>);
     return of(Keys<0, 8, false>{}, window_weights_mma_kernel<0, 8>);
   }

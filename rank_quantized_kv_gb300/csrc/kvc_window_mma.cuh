@@ -141,7 +141,8 @@ struct ChunkPlace {
 // ---------------------------------------------------------------- keys
 
 // How a warp reads the keys of 16 tokens: KB > 0, a codebook of KB bits over 16 KS
-// components, else centred codes of up to 2 KS chunks (KS steps of 16).
+// components, else centred codes of up to 2 KS chunks (KS steps of 16): two steps take
+// a chunk of each of four lanes, the last of an odd number the halves of two chunks.
 //
 // Scores carry fp32's precision: weights are two fp16 pieces of values that a power
 // of two per row brings up to 2^13 .. 2^14 (22 bits and more), uniform codes are
@@ -156,6 +157,8 @@ template <int KB, int KS, bool PAIRED>
 struct Keys {
   static constexpr int kCodes = 4 * KS;                 // a lane's codes of a token
   static constexpr int kSteps = KS;
+  static constexpr int kPlaces = (KS + 1) / 2;          // a lane's chunks (uniform)
+  static_assert(!KB || KS % 2 == 0, "codebooks: 64 or 128 components");
   static constexpr int kWords = KB ? (kCodes * KB + 31) / 32 : 1;
   static constexpr bool kPairs = KB && KB <= 3;         // the table holds pairs of centroids
   // The table, once per lane (no bank conflicts): pairs of centroids up to 3 bits, both
@@ -166,9 +169,9 @@ struct Keys {
 
   const unsigned char* tab;  // the table in shared memory
   uint32_t lane_at;     // where this lane's copy starts in an entry
-  ChunkPlace place[KS / 2];  // uniform: the lane's chunks of token g
-  Width width[KS / 2];
-  bool wide[KS / 2];    // some lane's has eight-bit codes
+  ChunkPlace place[kPlaces];  // uniform: the lane's chunks of token g
+  Width width[kPlaces];
+  bool wide[kPlaces];   // some lane's has eight-bit codes
 
   // The scale of the centroids: a power of two that brings the largest to [8, 16).
   static __device__ float table_scale(const Params& kp) {
@@ -214,15 +217,19 @@ struct Keys {
   __device__ void basis(const Params& kp, int beta, int Pk) {
     if (!KB)
 #pragma unroll
-      for (int s = 0; s < KS / 2; ++s) {
-        const uint32_t e = chunk_entry(kp, beta, 4 * s + (threadIdx.x & 3));
+      for (int s = 0; s < kPlaces; ++s) {
+        const int c = threadIdx.x & 3;
+        const uint32_t e = chunk_entry(kp, beta, 4 * s + (2 * s + 1 < KS ? c : c >> 1));
         place[s].set((int)((threadIdx.x & 31) >> 2) * Pk + (int)(e & 0xffffu));
         width[s].set(e);
         wide[s] = __any_sync(kFull, width[s].w == 8);
       }
   }
   // The packed position of the first of the four codes that lane c has of step s.
-  static __device__ int position(int s, int c) { return KB ? c * kCodes + 4 * s : 8 * (4 * (s / 2) + c) + 4 * (s & 1); }
+  static __device__ int position(int s, int c) {
+    if (KB) return c * kCodes + 4 * s;
+    return (s | 1) < KS ? 8 * (4 * (s / 2) + c) + 4 * (s & 1) : 16 * s + 4 * c;
+  }
 
   // What a lane holds of a token's row: the words of its codes (codebook).
   struct Row { uint32_t w[kWords]; const unsigned char* rows; };
@@ -257,7 +264,8 @@ struct Keys {
   __device__ void step(const Row& r, int s, uint32_t (&hi)[2], uint32_t (&lo)[2]) const {
     if constexpr (KB == 0) {
       const Width& w = width[s / 2];
-      const uint2 b = w.split(place[s / 2].read(r.rows, wide[s / 2]));
+      uint2 b = w.split(place[s / 2].read(r.rows, wide[s / 2]));
+      if ((s | 1) >= KS && (threadIdx.x & 1)) b.x = b.y;  // (odd lanes: the chunk's second half)
       hi[0] = w.pair(b, 2 * (s & 1));
       hi[1] = w.pair(b, 2 * (s & 1) + 1);
       lo[0] = lo[1] = 0u;

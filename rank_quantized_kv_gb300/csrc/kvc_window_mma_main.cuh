@@ -24,7 +24,7 @@
 // about 376 instructions for 16 tokens of up to eight rows, most of them to decode: 128
 // slots, 4 rows, 16384 tokens in 92 us, with half of HBM's rate and the ALU pipe busy
 // for 48 % of the time; a window of 4096 of them in 39; uniform codes of 32 components,
-// 8 slots of 100064 tokens, in 31.  Two CTAs per SM of eight warps for one tile of rows
+// 8 slots of 100064 tokens, in 29 (40 packed positions in three steps; in four 31).  Two CTAs per SM of eight warps for one tile of rows
 // (the weights in registers), one for more.
 #pragma once
 
@@ -144,11 +144,11 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
     // the rows' weights: scaled, split, in the operand's layout
     const float* w0 = t.w + ((size_t)slot * t.rows + r0) * t.NCk;
     {  // NT rows of a warp, their loads first
-      float w[NT][KS / 2], most[NT];
+      float w[NT][(KS + 1) / 2], most[NT];
 #pragma unroll
       for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int j = 0; j < KS / 2; ++j) {
+        for (int j = 0; j < (KS + 1) / 2; ++j) {
           const int r = warp + u * kMmaWarps, k = lane + 32 * j;
           w[u][j] = r < nr && k < t.NCk ? fabsf(w0[(size_t)r * t.NCk + k]) : 0.f;
         }
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
       for (int u = 0; u < NT; ++u) {
         most[u] = 0.f;
 #pragma unroll
-        for (int j = 0; j < KS / 2; ++j)
+        for (int j = 0; j < (KS + 1) / 2; ++j)
           if (w[u][j] <= 3.4e38f) most[u] = fmaxf(most[u], w[u][j]);  // NaN and infinities stay what they are
         most[u] = warp_max(most[u]);
       }
@@ -608,6 +608,8 @@ WindowKernel mma_kernel_for(const Params& kp, const Params& vp, int NCk, int* ta
     return k;
   };
   if (kp.mode == KVC_MODE_UNIFORM) {
+    if (NCk <= 32) return of(Keys<0, 2, NT == 1>{}, mma_kernel_for_values<0, 2, NT, HALF>(vu, D));
+    if (NCk <= 48) return of(Keys<0, 3, NT == 1>{}, mma_kernel_for_values<0, 3, NT, HALF>(vu, D));
     if (NCk <= 64) return of(Keys<0, 4, NT == 1>{}, mma_kernel_for_values<0, 4, NT, HALF>(vu, D));
     if (NCk <= 128) return of(Keys<0, 8, NT == 1>{}, mma_kernel_for_values<0, 8, NT, HALF>(vu, D));
     return nullptr;
