@@ -20,7 +20,8 @@ constexpr int kChunkTiles = 16;  // 8-row tiles whose weights are in shared memo
 // registers of four lanes.  CTAs take runs of the slots' tiles.  Where there are more
 // rows than a chunk the keys are decoded again for the next one, by the same warp, which
 // then adds to what it wrote.  Bound by its products and exponentials: 64 slots, 128 rows,
-// 4096 tokens of 32 components 50 us (40 positions in three steps; in four 54), of which the exponentials alone would take 7.
+// 4096 tokens of 32 components 50 us (40 positions in three steps; in four 54), of which
+// the exponentials alone would take 7.
 template <int KB, int KS>
 __global__ void __launch_bounds__(kManyWarps * 32, 1)
     window_weights_mma_kernel(const Params kp, const WindowArgs t, const WindowShape z) {

@@ -24,8 +24,9 @@
 // about 376 instructions for 16 tokens of up to eight rows, most of them to decode: 128
 // slots, 4 rows, 16384 tokens in 92 us, with half of HBM's rate and the ALU pipe busy
 // for 48 % of the time; a window of 4096 of them in 39; uniform codes of 32 components,
-// 8 slots of 100064 tokens, in 29 (40 packed positions in three steps; in four 31).  Two CTAs per SM of eight warps for one tile of rows
-// (the weights in registers), one for more.
+// 8 slots of 100064 tokens, in 29 (40 packed positions in three steps; in four 31).
+// Two CTAs per SM of eight warps for one tile of rows (the weights in registers), one
+// for more.
 #pragma once
 
 #include "kvc_launch.cuh"
