@@ -21,7 +21,7 @@
 // Bound: the move by HBM's sectors, kept rows that start and end inside them: 128
 // slots, 4096 of 16384 rows of 48 + 128 bytes kept, 94 MB of rows each way in 50 us,
 // with 138 MB read in sectors.  Select by the latency of its passes: 128 slots of 16384
-// tokens 16 us; 8 slots of 130001 tokens, eight CTAs each, 25.5, of which the cluster's
+// tokens 16 us; 8 slots of 130001 tokens, eight CTAs each, 24, of which the cluster's
 // exchanges take about half.  Small caches are two launches (6 + 4 us).
 #include <cooperative_groups.h>
 
@@ -82,6 +82,10 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, 
   return v + (warp > 0 ? before : 0u);
 }
 
+// The halves of a cluster barrier (all threads).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // grid: clusters of gridDim.x CTAs, one per slot (y).  A warp takes PER times 32
 // consecutive tokens at a time, a lane every 32nd of them.  RESIDENT: the CTA's tokens
 // are one step, whose keys stay in registers.
@@ -89,8 +93,7 @@ template <int PER, bool RESIDENT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
   __shared__ __align__(8) uint32_t hist[3][kBins];
   __shared__ uint32_t warp_sums[kSelThreads / 32];
-  __shared__ uint32_t counts[2];  // keys above the threshold, equal to it
-  __shared__ uint32_t digit_s, left_s;
+  __shared__ uint32_t digit_s, left_s, equal_s;
   constexpr int kStep = kSelThreads * PER;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = (int)gridDim.x, me = (int)blockIdx.x, tid = threadIdx.x, lane = tid & 31;
@@ -130,6 +133,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   __syncthreads();
   // the key of the n-th largest, digit by digit: `known` bits fixed so far
   uint32_t thr = 0u, left = (uint32_t)a.n;  // (n >= 1)
+  uint32_t above = 0u;  // of the CTAs before this one, in this thread's bins: keys above the n-th largest
   int known = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
@@ -147,6 +151,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     constexpr int kMine = kBins / kSelThreads;
     static_assert(kMine == 2, "a thread's bins in one load");
     uint2 two = *reinterpret_cast<const uint2*>(hp + kBins - 2 - 2 * tid);  // bins of this thread
+    uint2 pre = make_uint2(0u, 0u);                                         // in the CTAs before this one
     if (ctas > 1) {
       two = make_uint2(0u, 0u);
 #pragma unroll
@@ -155,6 +160,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
           const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hp, c) + kBins - 2 - 2 * tid);
           two.x += x.x;
           two.y += x.y;
+          if (c < me) {
+            pre.x += x.x;
+            pre.y += x.y;
+          }
         }
     }
     const uint32_t mine[kMine] = {two.y, two.x}, v = two.x + two.y;  // from the top
@@ -171,6 +180,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       at += mine[u];
     }
     __syncthreads();
+    const int high_bin = kBins - 1 - 2 * tid, digit = (int)digit_s;
+    above += (high_bin > digit ? pre.y : 0u) + (high_bin - 1 > digit ? pre.x : 0u);
+    if (high_bin == digit) equal_s = pre.y;
+    if (high_bin - 1 == digit) equal_s = pre.x;
     thr |= digit_s << shift;
     left = left_s;
     known += bits;
@@ -189,25 +202,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   };
   uint32_t gt0 = 0, eq0 = 0;  // of the CTAs before this one
   if (ctas > 1) {
-    uint32_t gt = 0, eq = 0;
-    each([&](int t) {
-      const uint32_t v = count(t);
-      gt += v & 0xffffu;
-      eq += v >> 16;
-    });
-    uint32_t n_gt, n_eq;
-    block_scan(gt, warp_sums, &n_gt);
-    block_scan(eq, warp_sums, &n_eq);
-    if (tid == 0) {
-      counts[0] = n_gt;
-      counts[1] = n_eq;
-    }
-    cluster.sync();
-    for (int c = 0; c < me; ++c) {
-      const uint32_t* p = cluster.map_shared_rank(counts, c);
-      gt0 += p[0];
-      eq0 += p[1];
-    }
+    cluster_arrive();  // this CTA has read the others' shared memory
+    block_scan(above, warp_sums, &gt0);
+    eq0 = equal_s;
   }
   grid_dependents_launch();
   int32_t* index = a.index + (int64_t)slot * a.n;
@@ -234,7 +231,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     gt0 += total & 0xffffu;
     eq0 += total >> 16;
   });
-  if (ctas > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
+  if (ctas > 1) cluster_wait();  // no CTA leaves while another reads its shared memory
 }
 
 // ---------------------------------------------------------------- move
