@@ -441,7 +441,8 @@ kvc_status kvc_attend_window(const kvc_layer *keys, const kvc_layer *values,
  * to dst_keys and dst_values (layers with the same frozen parameters, slot by slot,
  * of equal length; their capacity may differ), the kept weights are written to
  * dst_weights from the destination's old length on, and the source stays as it was.
- * Rows move as they are stored.
+ * Rows move as they are stored; keys appended later to a layer with an outlier stream
+ * are split by their index after the eviction (split_from).
  *
  *  keys, values  heads_per_group 1, equal B, H, device and length; any mode.
  *  keep          1 .. length (none: kvc_trim); sinks + recent at most keep.

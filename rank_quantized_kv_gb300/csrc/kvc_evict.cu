@@ -22,7 +22,7 @@
 // slots, 4096 of 16384 rows of 48 + 128 bytes kept, 94 MB of rows each way in 50 us,
 // with 138 MB read in sectors.  Select by the latency of its passes: 128 slots of 16384
 // tokens 16 us; 8 slots of 130001 tokens, eight CTAs each, 24, of which the cluster's
-// exchanges take about half.  Small caches are two launches (6 + 4 us).
+// exchanges take a third.  Small caches are two launches (6 + 4 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -20,7 +20,7 @@ D = 128
 
 # components by width: {width: count}; a width's components fill chunks of eight
 WIDTHS = {8: {4: 5}, 16: {4: 16}, 32: {8: 8, 3: 13, 1: 3}, 40: {8: 4, 4: 20, 2: 8}, 48: {8: 7, 3: 17, 1: 16},
-          56: {2: 56}, 64: {8: 3, 4: 40, 1: 9}, 80: {8: 3, 2: 65}, 128: {8: 1, 1: 120}}
+          56: {2: 56}, 120: {8: 120}, 64: {8: 3, 4: 40, 1: 9}, 80: {8: 3, 2: 65}, 128: {8: 1, 1: 120}}
 
 
 @pytest.fixture(scope="module")
