@@ -714,7 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       gm[wg][r] = l != 0.f ? m : seen ? kWindowLowest : -INFINITY;
       gl[wg][r] = l;
       if (r == 0) gs[wg] = mine ? sref : 0.f;
+      // each group reads the other's sums below: the reads come after the products that
+      // the other one has waited for
+      tc_fence_before();
       named_bar_sync(kSoftBar, kSoftWarps * 32);
+      tc_fence_after();
       const float ma = gm[0][r], mb = gm[1][r], la = gl[0][r], lb = gl[1][r];
       const float M = fmaxf(ma, mb);
       float fa = la != 0.f ? ex2(ma - M) : 0.f, fb = lb != 0.f ? ex2(mb - M) : 0.f;
@@ -786,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       named_bar_sync(kSoftBar, kSoftWarps * 32);  // the next segment overwrites O and the exchange
+      tc_fence_after();
       it0 += n;
     }
   }
