@@ -21,9 +21,11 @@
 //
 // Precision: that of kvc_attend_tree (include/kvc.h).  Codes are exact in fp16,
 // centroids rounded to fp16 after a common scale (2^-14 for eight Gaussian levels); W
-// keeps 22 bits; P times the value scale is rounded to fp16.  References move lazily:
-// a row's is its first maximum less 4, and moves when a score exceeds it by 8; the
-// value scales are divided by a power of two that moves when one exceeds it four times.
+// keeps 22 bits; P times the value scale is rounded to fp16.  References move lazily and
+// are a row's own: that of the scores is its first maximum less 4, and moves when a score
+// exceeds it by 8; that of the value scales the power of two above the largest that the
+// row sees, moved when one exceeds it four times.  Their sum is one exponent, so a scale
+// costs the loop nothing.
 //
 // Bound: a tile's 16384 exponentials take 1024 cycles of the SM's 16 a cycle, its MMAs
 // 768, softmax and decoding about 1000 issue slots a scheduler.  8 slots of 8192 rows,
@@ -60,6 +62,7 @@ constexpr int kGroupBar = 1, kSoftBar = 3, kDecBar = 4;  // named barriers: grou
 constexpr uint64_t kDrainNs = 2000000000ull;  // limit of the drains; the watchdog's is the layer's
 constexpr uint32_t kTryNs = 20000;            // a try sleeps so long at most
 constexpr float kSet = 4.f, kMove = 8.f;      // log2
+constexpr float kScaleLowest = -24.f;         // log2 of the smallest positive scale
 constexpr uint32_t kTransposeB = 1u << 16;
 
 struct TcShape {
@@ -283,8 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       o_done[2], side_full[kSideRing], w_full, w_empty, done_bar;
   __shared__ uint32_t kch[32], vch[32];
   __shared__ __align__(16) unsigned short side_s[kSideRing][2][kTile];  // norms, scales
-  __shared__ __align__(16) float cn[2][2][kTile], cs[2][2][kTile];  // per group and turn: norms, scales over sref
-  __shared__ float gm[2][kRows], gl[2][kRows], gs[2], red[2][4];  // the groups' references and sums, srefs
+  __shared__ __align__(16) float cn[2][2][kTile], cs[2][2][kTile];  // per group and turn: norms, scales
+  __shared__ __align__(16) float red[2][2][4];  // per group and turn: the warps' largest scales
+  __shared__ float gm[2][kRows], gl[2][kRows];  // the groups' references and sums
   __shared__ __align__(256) unsigned char tab[CB ? 64 * 32 * 4 : 16];
   __shared__ __align__(8) unsigned char place_s[4 * sizeof(Place)];  // per group this one and the next
   Place* place = reinterpret_cast<Place*>(place_s);
@@ -540,65 +544,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Place& g = place[2 * wg + (turns & 1)];
       const int n = vg.n, x = vg.r0 + min(r, vg.nr - 1), pos = t.ctx + x / t.rep;  // (rows past the last: its sight)
       const float rs = t.wscale[(size_t)vg.job * kRows + r];
-      float m = -INFINITY;
+      // The row's l and O are in units of 2^ref, ref = score reference + sref, where sref
+      // (log2) is that of the value scales: nothing of it depends on what other rows see.
+      float ref = -INFINITY, sref = VU ? 0.f : kScaleLowest;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool seen = false;
-      float sref = VU ? 1.f : 0.f, inv_sref = sref;
       int mine = 0;  // the group's tiles of the segment
       for (int i = (it0 ^ wg) & 1; i < n; i += 2, ++turn, ++mine) {
         const int it = it0 + i, t0 = g.token(i), buf = turn & 1;
         const uint32_t par = (it >> 1) & 1;
         const int t1 = t0 + kTile - 1;
         const bool all = t0 >= vg.first && t1 <= vg.p0 && (t0 > vg.p1 - vg.window || t1 < vg.sink_end);
-        // this thread's column: its norm and scale for all rows
-        float scale = 1.f;
-        bool up = false;
-        if (CB || !VU) {
-          const int sd = it % kSideRing, tok = t0 + r;
-          wait_or_abort(&side_full[sd], (it / kSideRing) & 1, &abort_flag);
-          float norm = CB ? __half2float(__ushort_as_half(side_s[sd][0][r])) : 1.f;
-          if (!VU) {
-            scale = __half2float(__ushort_as_half(side_s[sd][1][r]));
-            // a token that no row sees may hold anything; a visible scale of NaN makes
-            // the scores of those who see it NaN
-            if (tok >= t.S || tok < vg.first) scale = 0.f;
-            if (scale != scale) norm = scale;
-            up = scale > 4.f * sref && scale <= 65504.f;
-            cs[wg][buf][r] = fmaxf(fminf(scale * inv_sref, 3e38f), -3e38f);
-          }
-          if (CB || !VU) cn[wg][buf][r] = norm;
-        }
-        if (CB || !VU) {
-          if (named_bar_or(bar, 128, up)) {  // the value scales' reference: the next power of two
-            const float most = warp_max(up ? scale : 0.f);
-            if (lane == 0) red[wg][quarter] = most;
-            named_bar_sync(bar, 128);
-            const float big = fmaxf(fmaxf(red[wg][0], red[wg][1]), fmaxf(red[wg][2], red[wg][3]));
-            const float to = __int_as_float((__float_as_int(big) & 0x7f800000) + 0x00800000);
-            const float ratio = sref / to;
-            sref = to;
-            inv_sref = 1.f / to;
-            cs[wg][buf][r] = fmaxf(fminf(scale * inv_sref, 3e38f), -3e38f);
-            if (mine) {  // O holds sums: the last product is done once S has been written
-              wait_or_abort(&s_full[wg], par, &abort_flag);
-              __syncwarp();
-              tc_fence_after();
-              for (int c = 0; c < z.DV; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(o_tm + wg * kTile + c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ratio);
-                tmem_st16(o_tm + wg * kTile + c, o);
-              }
-              tmem_wait_st();
-            }
-            named_bar_sync(bar, 128);
-          }
-        }
-        wait_or_abort(&s_full[wg], par, &abort_flag);
-        __syncwarp();
-        tc_fence_after();
         // visible columns, where not all are: [ca, ca1] and [cb, cb1]
         int ca = 0, ca1 = kTile - 1, cb = 0, cb1 = -1;
         if (!all) {
@@ -611,6 +567,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           seen = true;
         }
+        // this thread's column: its norm and scale for all rows
+        if (CB || !VU) {
+          const int sd = it % kSideRing, tok = t0 + r;
+          wait_or_abort(&side_full[sd], (it / kSideRing) & 1, &abort_flag);
+          float norm = CB ? __half2float(__ushort_as_half(side_s[sd][0][r])) : 1.f;
+          if (!VU) {
+            float scale = __half2float(__ushort_as_half(side_s[sd][1][r]));
+            // a token that no row sees may hold anything; a visible scale of NaN makes
+            // the scores of those who see it NaN
+            if (tok >= t.S || tok < vg.first) scale = 0.f;
+            if (scale != scale) norm = scale;
+            cs[wg][buf][r] = fmaxf(fminf(scale, 3e38f), -3e38f);
+            const uint32_t big = __reduce_max_sync(kFull, __float_as_uint(scale > 0.f && scale <= 65504.f ? scale : 0.f));
+            if (lane == 0) red[wg][buf][quarter] = __uint_as_float(big);
+          }
+          cn[wg][buf][r] = norm;
+        }
+        if (CB || !VU) named_bar_sync(bar, 128);
+        if (!VU) {
+          // the row's reference of the scales: the power of two above the largest finite one
+          // that it sees, once one exceeds it four times (before S is waited for: the first
+          // tiles of a segment, which move it, wait for S in any case)
+          const float4 warps = *reinterpret_cast<const float4*>(red[wg][buf]);
+          float most = fmaxf(fmaxf(warps.x, warps.y), fmaxf(warps.z, warps.w));
+          const float limit = __int_as_float(((int)sref + 2 + 127) << 23);
+          if (__any_sync(kFull, most > limit)) {
+            if (!all) {  // the largest may be hidden from this row
+              most = 0.f;
+#pragma unroll 1
+              for (int c = 0; c < kTile; c += 16) {
+                const uint32_t see = bits_between(ca - c, ca1 - c) | bits_between(cb - c, cb1 - c);
+                if (!__any_sync(kFull, see & 0xffffu)) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float4 f = *reinterpret_cast<const float4*>(&cs[wg][buf][c + 4 * e]);
+                  if ((see >> (4 * e) & 1u) && f.x <= 65504.f) most = fmaxf(most, f.x);
+                  if ((see >> (4 * e) & 2u) && f.y <= 65504.f) most = fmaxf(most, f.y);
+                  if ((see >> (4 * e) & 4u) && f.z <= 65504.f) most = fmaxf(most, f.z);
+                  if ((see >> (4 * e) & 8u) && f.w <= 65504.f) most = fmaxf(most, f.w);
+                }
+              }
+            }
+            float f = 1.f;
+            if (most > limit) {
+              const float to = (float)((__float_as_int(most) >> 23) - 126), now = ref + (to - sref);
+              if (ref != -INFINITY) f = ex2(ref - now);
+              ref = now;
+              sref = to;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) l2[e] = __fmul2_rn(l2[e], make_float2(f, f));
+            if (mine && __any_sync(kFull, f != 1.f)) {  // O holds sums: the last product is done once S has been written
+              wait_or_abort(&s_full[wg], par, &abort_flag);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < z.DV; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_tm + wg * kTile + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_tm + wg * kTile + c, o);
+              }
+              tmem_wait_st();
+            }
+          }
+        }
+        wait_or_abort(&s_full[wg], par, &abort_flag);
+        __syncwarp();
+        tc_fence_after();
         // 32 columns at a time: P's 16 columns go where columns of S that have been read
         // were.  (The loop is kept rolled: unrolled, its instructions came from L2.)
         uint32_t v[32];
@@ -644,15 +671,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) top[e & 3] = max_nan(top[e & 3], y[e].x, y[e].y);
           const float most = max_nan(max_nan(top[0], top[1]), max_nan(top[2], top[3])) * rs;
-          const bool need = most > -INFINITY && !(most - m <= kMove);
+          const bool need = most > -INFINITY && !(most - ref <= kMove - sref);
           if (__any_sync(kFull, need)) {
             // the first reference, or a new one, whole steps of log2 away
-            float now = m, f = 1.f;
+            float now = ref, f = 1.f;
             if (need && most > kWindowLowest) {
-              now = m == -INFINITY ? most - kSet : m + ceilf(most - kSet - m);
-              f = ex2(m - now);
+              const float to = most - kSet + sref;
+              now = ref == -INFINITY ? to : ref + ceilf(to - ref);
+              f = ex2(ref - now);
             }
-            m = now;
+            ref = now;
 #pragma unroll
             for (int e = 0; e < 2; ++e) l2[e] = __fmul2_rn(l2[e], make_float2(f, f));
             const __half2 fh = __float2half2_rn(f);
@@ -680,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             tmem_wait_st();
           }
-          const float neg = m == -INFINITY ? 0.f : -m;
+          const float neg = ref == -INFINITY ? 0.f : -ref;
           const float2 rs2 = make_float2(rs, rs), neg2 = make_float2(neg, neg);
           uint32_t h[16];
 #pragma unroll
@@ -711,9 +739,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_after();
       }
-      gm[wg][r] = l != 0.f ? m : seen ? kWindowLowest : -INFINITY;
+      gm[wg][r] = l != 0.f ? ref : seen ? kWindowLowest : -INFINITY;
       gl[wg][r] = l;
-      if (r == 0) gs[wg] = mine ? sref : 0.f;
       // each group reads the other's sums below: the reads come after the products that
       // the other one has waited for
       tc_fence_before();
@@ -721,12 +748,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float ma = gm[0][r], mb = gm[1][r], la = gl[0][r], lb = gl[1][r];
       const float M = fmaxf(ma, mb);
-      float fa = la != 0.f ? ex2(ma - M) : 0.f, fb = lb != 0.f ? ex2(mb - M) : 0.f;
+      const float fa = la != 0.f ? ex2(ma - M) : 0.f, fb = lb != 0.f ? ex2(mb - M) : 0.f;
       const float L = (la != 0.f ? fa * la : 0.f) + (lb != 0.f ? fb * lb : 0.f);
       // tiles of either group in the segment
       const bool has_a = n > 1 || (n == 1 && !(it0 & 1)), has_b = n > 1 || (n == 1 && (it0 & 1));
-      fa *= gs[0];
-      fb *= gs[1];
       const float inv = L > 0.f || L != L ? 1.f / L : M == -INFINITY ? 0.f : NAN;
       const bool direct = vg.whole && !VU;
       const size_t part = (size_t)vg.job + blockIdx.x;
