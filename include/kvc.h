@@ -366,14 +366,17 @@ kvc_status kvc_accept(kvc_layer *layer, int64_t N, const int32_t *index, int64_t
  * with h = hq / (Hq / H).  A query that sees no token (padding) gets a row of zeros
  * and gives no weight; one that sees a score of NaN or +inf, or scores of -inf alone
  * (below fp32's range), gets a row of NaN and gives NaN to what it sees.  What a
- * hidden token stores, infinities and NaN among it, has no effect.  Positions are
+ * hidden token stores, infinities and NaN among it, has no effect: the rows of the
+ * queries that do not see it are the same to the bit.  Positions are
  * places in the cache: after an eviction the kept tokens are neighbours.
  * All of it is computed in fp32, or on the tensor cores with sums and softmax
  * statistics in fp32 and scores to fp32's precision (both factors held to 22 bits or
- * more), the softmax weights times value scales to 22 bits (2^-25 of the row's
- * largest at least).  Calls of more than 32 rows (Hq / H * N) a slot, unless they are
- * short or ask for weights of codebook keys, have the roundings that
- * kvc_attend_tree lists, but for its generic path and its layers in fp32.
+ * more), the softmax weights times value scales to 22 bits (and to 2^-25 of the row's
+ * largest weight times the largest scale that it sees).  Calls of more than 32 rows
+ * (Hq / H * N) a slot, unless they are short or ask for weights of codebook keys, have
+ * the roundings that kvc_attend_tree lists, but for its generic path and its layers in
+ * fp32, and with weights times value scales below fp16's normal range held to 2^-28 of
+ * the row's largest weight times the largest scale that it sees.
  *
  *  keys       a KVC_MODE_UNIFORM or KVC_MODE_CODEBOOK layer (with or without a
  *             residual sketch and outlier stream), D at most 256.

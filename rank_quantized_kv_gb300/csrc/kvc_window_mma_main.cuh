@@ -12,9 +12,10 @@
 // Scores are exact to fp32's rounding (Keys), codes exact in fp16.  Weights times
 // value scales are two fp16 pieces (22 bits; 2^-25 of the reference at least).  The
 // reference of a row is its first maximum less 4 and moves only when a score exceeds
-// it by 8 (in log2); the value scales are divided by a power of two (sref) that moves
-// only when a scale exceeds it four times: weights stay below 2^10.  The row's
-// constant c1 cancels in the softmax and is left out.
+// it by 8 (in log2); that of the value scales (sref), the row's own too, is the power of
+// two above the largest that it sees and moves when one exceeds it four times.  Their sum
+// is one exponent: weights times scales stay below 2^10, and nothing of a row depends on
+// what other rows see.  The row's constant c1 cancels in the softmax and is left out.
 //
 // At most four rows (HALF) fill half of the N side: the other half takes the second
 // pieces, the weights' in one product and P's in the other, and sums meet by a shuffle
@@ -41,6 +42,10 @@ namespace {
 constexpr int kMmaWarps = 8, kMmaThreads = kMmaWarps * 32;
 constexpr int kMmaTile = kWindowTile, kStages = 2;
 constexpr float kSet = 4.f, kMove = 8.f;
+constexpr float kScaleLowest = -24.f;  // log2 of the smallest positive value scale
+
+// 2^e of a whole number e.
+__device__ __forceinline__ float exp2i(float e) { return __int_as_float(((int)e + 127) << 23); }
 
 // VK: head size of int8 values (64 or 128), 0 for uniform ones (up to 128 positions).
 template <int VK>
@@ -223,7 +228,16 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
         vplace[e][0].set(2 * c * Pv + (int)(x & 0xffffu));
         vplace[e][1].set((2 * c + 1) * Pv + (int)(x & 0xffffu));
       }
-    float sref = V::kUniform ? 1.f : 0.f, inv_sref = sref;
+    // A row's l and o are in units of 2^(score reference + sref), sref (log2) being that of
+    // its value scales; negm is minus their sum.  Above high[j] in log2 and above limit a
+    // score or a scale may have to move the reference of one of the lane's rows.
+    float sref[NT][2], high[2], limit = INFINITY;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      high[j] = kMove;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sref[nt][j] = V::kUniform ? 0.f : kScaleLowest;
+    }
     // tiles that all rows see whole: t0 >= see0 and t0 <= see1, and t0 > see2 or t0 < see3
     const int see0 = sight.first, see1 = p0 - (kMmaTile - 1), see2 = p1 - sight.window,
               see3 = sight.sink_end - (kMmaTile - 1);
@@ -372,66 +386,56 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
               for (int e = 0; e < 4; ++e)
                 if (!(seen >> (4 * (h * NT + nt) + e) & 1u)) x[h][nt][e] = -INFINITY;
         }
-        float top = -INFINITY, most = 0.f;
+        float top[2] = {-INFINITY, -INFINITY}, most = 0.f;
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            top = max_nan(top, x[h][nt][0], x[h][nt][1]);
-            top = max_nan(top, x[h][nt][2], x[h][nt][3]);
+            top[0] = max_nan(top[0], x[h][nt][0], x[h][nt][2]);
+            top[1] = max_nan(top[1], x[h][nt][1], x[h][nt][3]);
           }
           most = fmaxf(most, fmaxf(sv[h][0], sv[h][1]));
         }
-        bool move = !(top <= kMove);
-        if (!V::kUniform) move |= most > 4.f * sref;
+        bool move = !(top[0] <= high[0]) || !(top[1] <= high[1]);
+        if (!V::kUniform) move |= most > limit;
         if (__any_sync(kFull, move)) {  // (a row's first token, too: its reference is -inf)
-          float ratio = 1.f;
-          if (!V::kUniform) {  // the value scales' reference: the next power of two
-            float m = 0.f;
-#pragma unroll
-            for (int h = 0; h < HB; ++h)
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                uint32_t any = 0u;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) any |= seen >> (4 * (h * NT + nt) + 2 * q);
-                if ((any & 3u) && sv[h][q] > 4.f * sref && sv[h][q] <= 65504.f) m = fmaxf(m, sv[h][q]);
-              }
-            m = warp_max(m);
-            if (m > 0.f) {
-              const float to = __int_as_float((__float_as_int(m) & 0x7f800000) + 0x00800000);
-              ratio = sref / to;
-              sref = to;
-              inv_sref = 1.f / to;
-            }
-          }
+          limit = INFINITY;
+          high[0] = high[1] = INFINITY;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float m = -INFINITY;
+              // the row's largest visible score and scale (finite)
+              float m = -INFINITY, big = 0.f;
 #pragma unroll
               for (int h = 0; h < HB; ++h)
 #pragma unroll
                 for (int e = j; e < 4; e += 2)
-                  if (seen >> (4 * (h * NT + nt) + e) & 1u) m = fmaxf(m, fmaxf(s[h][nt][e] * rs[nt][j], kWindowLowest));
-              m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
-              m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
-              m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-              const float old = -negm[nt][j];
-              float now = old, f = 1.f;
-              if (m != -INFINITY && (m - old > kMove || !(old > kWindowLowest))) {
-                // the first reference, or a new one (the lowest: scores of -inf alone so far)
-                now = m > kWindowLowest ? m - kSet : fmaxf(old, m);
-                f = old == now ? 1.f : ex2(old - now);
+                  if (seen >> (4 * (h * NT + nt) + e) & 1u) {
+                    m = fmaxf(m, fmaxf(s[h][nt][e] * rs[nt][j], kWindowLowest));
+                    if (!V::kUniform && sv[h][e >> 1] <= 65504.f) big = fmaxf(big, sv[h][e >> 1]);
+                  }
+#pragma unroll
+              for (int d = 4; d < 32; d *= 2) {
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+                if (!V::kUniform) big = fmaxf(big, __shfl_xor_sync(kFull, big, d));
               }
+              const float old = -negm[nt][j], was = sref[nt][j];
+              if (!V::kUniform && big > exp2i(was + 2.f))  // the next power of two
+                sref[nt][j] = (float)((__float_as_int(big) >> 23) - 126);
+              float now = old + (sref[nt][j] - was);
+              if (m != -INFINITY && (m - old > kMove - was || !(old > kWindowLowest)))
+                // the first reference, or a new one (the lowest: scores of -inf alone so far)
+                now = m > kWindowLowest ? m - kSet + sref[nt][j] : fmaxf(old, m);
+              const float f = old == now ? 1.f : ex2(old - now);
               l[nt][j] *= f;
-              f *= ratio;
 #pragma unroll
               for (int q = 0; q < MT; ++q) {
                 o[nt][q][j] *= f;
                 o[nt][q][2 + j] *= f;
               }
+              if (!V::kUniform && now != -INFINITY) limit = fminf(limit, exp2i(sref[nt][j] + 2.f));
+              high[j] = fminf(high[j], kMove - sref[nt][j]);
               negm[nt][j] = -now;
 #pragma unroll
               for (int h = 0; h < HB; ++h)
@@ -443,7 +447,6 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
         uint32_t ph[HB][NT][2], pl[HB][NT][2];  // P as an operand, in two fp16 pieces
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
-          const float va = sv[h][0] * inv_sref, vb = sv[h][1] * inv_sref;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float p[4];
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
             for (int e = 0; e < 4; ++e) {
               p[e] = ex2(x[h][nt][e]);
               l[nt][e & 1] += p[e];
-              if (!V::kUniform) p[e] *= e < 2 ? va : vb;
+              if (!V::kUniform) p[e] *= sv[h][e >> 1];
             }
             if (!V::kUniform && !all) {  // a hidden token's scale may be anything
 #pragma unroll
@@ -569,7 +572,7 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
               // channel of row g + 8 (e >> 1) of tile m
               const int d = VK ? 16 * m + 2 * g + (e >> 1)
                                : 8 * (8 * (m >> 2) + g) + 2 * (m & 3) + (e >> 1);
-              ob[warp * OW + d * 8 + 2 * c + (e & 1)] = o[n2][m][e] * (f[n2][e & 1] * sref);
+              ob[warp * OW + d * 8 + 2 * c + (e & 1)] = o[n2][m][e] * f[n2][e & 1];
             }
       __syncthreads();
       for (int e = tid; e < t.Dv * 8; e += kMmaThreads) {

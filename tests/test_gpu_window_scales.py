@@ -81,7 +81,7 @@ def test_scales_that_no_query_sees(kvc, size, kmode, weights, value):
     assert not weights or torch.equal(wa, wb)
 
 
-@pytest.mark.parametrize("size", ["128 rows"])
+@pytest.mark.parametrize("size", list(SIZES))
 @pytest.mark.parametrize("kmode", ["codebook", "uniform"])
 @pytest.mark.parametrize("value", [65504.0, float("inf"), float("nan")])
 def test_scales_that_other_queries_see(kvc, size, kmode, value):
@@ -142,3 +142,24 @@ def test_rows_are_as_exact_as_what_they_see(kvc, size, kmode, pattern):
     fits = np.abs(want) < 65000.0  # (a value past fp16's range is an infinity)
     assert fits.mean() > 0.5
     check(torch.where(torch.from_numpy(fits).to(DEV), o, torch.zeros_like(o)), np.where(fits, want, 0.0), tol, pattern)
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+@pytest.mark.parametrize("kmode,vmode,path", [("codebook", "int8", "auto"), ("uniform", "uniform", "auto"),
+                                              ("prod", "int8", "auto"), ("codebook", "int8", "generic")])
+def test_later_queries_tokens_hold_anything(kvc, size, kmode, vmode, path):
+    """Codes, norms and scales of the last token, which the last query alone sees."""
+    rep, N, S, window = SIZES[size]
+    tree_cases.PATH[0] = path
+    gk, gv, _, _ = make_layers(kvc, kmode, vmode, B, H, D, S, 43, dev=DEV)
+    tree_cases.PATH[0] = "auto"
+    q = torch.randn(B, H * rep, N, D, generator=torch.Generator().manual_seed(S)).to(DEV)
+    a = kvc.attend_window(gk, gv, q, window, SINKS)
+    for lay in (gk, gv):
+        for slot in range(B * H):
+            rows, side = lay.slot_rows(slot)
+            rows[S - 1] = 0xA7
+            if side is not None:
+                side[S - 1].view(torch.float16).fill_(float("inf") if slot % 2 else float("nan"))
+    b = kvc.attend_window(gk, gv, q, window, SINKS)
+    assert torch.equal(a[:, :, :N - 1], b[:, :, :N - 1])
