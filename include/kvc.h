@@ -367,8 +367,9 @@ kvc_status kvc_accept(kvc_layer *layer, int64_t N, const int32_t *index, int64_t
  * and gives no weight; one that sees a score of NaN or +inf, or scores of -inf alone
  * (below fp32's range), gets a row of NaN and gives NaN to what it sees.  What a
  * hidden token stores, infinities and NaN among it, has no effect: the rows of the
- * queries that do not see it are the same to the bit.  Positions are
- * places in the cache: after an eviction the kept tokens are neighbours.
+ * queries that do not see it are the same to the bit.  A value scale of NaN makes the
+ * rows that see it NaN; weights do not depend on the values.  Positions are places in
+ * the cache: after an eviction the kept tokens are neighbours.
  * All of it is computed in fp32, or on the tensor cores with sums and softmax
  * statistics in fp32 and scores to fp32's precision (both factors held to 22 bits or
  * more), the softmax weights times value scales to 22 bits (and to 2^-25 of the row's

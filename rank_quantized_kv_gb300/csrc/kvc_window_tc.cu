@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) unsigned short side_s[kSideRing][2][kTile];  // norms, scales
   __shared__ __align__(16) float cn[2][2][kTile], cs[2][2][kTile];  // per group and turn: norms, scales
   __shared__ __align__(16) float red[2][2][4];  // per group and turn: the warps' largest scales
-  __shared__ float gm[2][kRows], gl[2][kRows];  // the groups' references and sums
+  __shared__ float gm[2][kRows], gl[2][kRows], gx[2][kRows];  // the groups' references and sums; NaN: spoilt rows
   __shared__ __align__(256) unsigned char tab[CB ? 64 * 32 * 4 : 16];
   __shared__ __align__(8) unsigned char place_s[4 * sizeof(Place)];  // per group this one and the next
   Place* place = reinterpret_cast<Place*>(place_s);
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (log2) is that of the value scales: nothing of it depends on what other rows see.
       float ref = -INFINITY, sref = VU ? 0.f : kScaleLowest;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      bool seen = false;
+      bool seen = false, spoilt = false;  // the row sees a token; one with a value scale of NaN
       int mine = 0;  // the group's tiles of the segment
       for (int i = (it0 ^ wg) & 1; i < n; i += 2, ++turn, ++mine) {
         const int it = it0 + i, t0 = g.token(i), buf = turn & 1;
@@ -567,22 +567,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           seen = true;
         }
-        // this thread's column: its norm and scale for all rows
+        // this thread's column: its norm (codebook keys) and scale for all rows
         if (CB || !VU) {
           const int sd = it % kSideRing, tok = t0 + r;
           wait_or_abort(&side_full[sd], (it / kSideRing) & 1, &abort_flag);
-          float norm = CB ? __half2float(__ushort_as_half(side_s[sd][0][r])) : 1.f;
           if (!VU) {
             float scale = __half2float(__ushort_as_half(side_s[sd][1][r]));
-            // a token that no row sees may hold anything; a visible scale of NaN makes
-            // the scores of those who see it NaN
+            // a token that no row sees may hold anything; a scale of NaN counts as 0 in the
+            // product, and the rows that see it are marked below
             if (tok >= t.S || tok < vg.first) scale = 0.f;
-            if (scale != scale) norm = scale;
+            float level = scale > 0.f && scale <= 65504.f ? scale : 0.f;
+            if (scale != scale) {
+              level = INFINITY;
+              scale = 0.f;
+            }
             cs[wg][buf][r] = fmaxf(fminf(scale, 3e38f), -3e38f);
-            const uint32_t big = __reduce_max_sync(kFull, __float_as_uint(scale > 0.f && scale <= 65504.f ? scale : 0.f));
+            const uint32_t big = __reduce_max_sync(kFull, __float_as_uint(level));
             if (lane == 0) red[wg][buf][quarter] = __uint_as_float(big);
           }
-          cn[wg][buf][r] = norm;
+          if (CB) cn[wg][buf][r] = __half2float(__ushort_as_half(side_s[sd][0][r]));
         }
         if (CB || !VU) named_bar_sync(bar, 128);
         if (!VU) {
@@ -593,7 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           float most = fmaxf(fmaxf(warps.x, warps.y), fmaxf(warps.z, warps.w));
           const float limit = __int_as_float(((int)sref + 2 + 127) << 23);
           if (__any_sync(kFull, most > limit)) {
-            if (!all) {  // the largest may be hidden from this row
+            const bool odd = most == INFINITY;  // (for all rows) a column has a scale of NaN
+            if (odd)
+#pragma unroll 1
+              for (int c = 0; c < kTile && !spoilt; ++c)
+                spoilt = ((c >= ca && c <= ca1) || (c >= cb && c <= cb1)) &&
+                         __hisnan(__ushort_as_half(side_s[it % kSideRing][1][c]));
+            if (!all || odd) {  // the largest may be hidden from this row
               most = 0.f;
 #pragma unroll 1
               for (int c = 0; c < kTile; c += 16) {
@@ -648,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float2 y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) y[e] = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-          if (CB || !VU) {  // (uniform keys: 1, or NaN beside a scale of NaN)
+          if (CB) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float4 f = *reinterpret_cast<const float4*>(&cn[wg][buf][32 * q + 4 * e]);
@@ -741,13 +750,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       gm[wg][r] = l != 0.f ? ref : seen ? kWindowLowest : -INFINITY;
       gl[wg][r] = l;
+      gx[wg][r] = spoilt ? NAN : 0.f;
       // each group reads the other's sums below: the reads come after the products that
       // the other one has waited for
       tc_fence_before();
       named_bar_sync(kSoftBar, kSoftWarps * 32);
       tc_fence_after();
       const float ma = gm[0][r], mb = gm[1][r], la = gl[0][r], lb = gl[1][r];
-      const float M = fmaxf(ma, mb);
+      const float M = fmaxf(ma, mb), add = gx[0][r] + gx[1][r];
       const float fa = la != 0.f ? ex2(ma - M) : 0.f, fb = lb != 0.f ? ex2(mb - M) : 0.f;
       const float L = (la != 0.f ? fa * la : 0.f) + (lb != 0.f ? fb * lb : 0.f);
       // tiles of either group in the segment
@@ -768,13 +778,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = wg * (z.DV / 2) + c0;
         float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        for (int e = 0; e < 16; ++e) v[e] = add;
         if (has_a) {
           uint32_t o[16];
           tmem_ld16(o_tm + c, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * fa;
+          for (int e = 0; e < 16; ++e) v[e] = fmaf(__uint_as_float(o[e]), fa, v[e]);
         }
         if (has_b) {
           uint32_t o[16];

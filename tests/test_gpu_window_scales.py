@@ -163,3 +163,27 @@ def test_later_queries_tokens_hold_anything(kvc, size, kmode, vmode, path):
                 side[S - 1].view(torch.float16).fill_(float("inf") if slot % 2 else float("nan"))
     b = kvc.attend_window(gk, gv, q, window, SINKS)
     assert torch.equal(a[:, :, :N - 1], b[:, :, :N - 1])
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+@pytest.mark.parametrize("kmode,path", [("uniform", "auto"), ("codebook", "auto"), ("codebook", "generic")])
+@pytest.mark.parametrize("at", ["last token", "a token that all see", "a sink", "tokens around a tile's end"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_weights_do_not_depend_on_the_values(kvc, size, kmode, path, at, value):
+    """A value scale of NaN makes the rows that see it NaN, one of infinity not finite;
+    the weights stay what they are."""
+    layers, q, rep, N, S, window = _case(kvc, size, kmode, path=path)
+    a, wa = _run(kvc, layers, q, window, weights=True)
+    tokens = {"last token": [S - 1], "a token that all see": [S - N - 7], "a sink": [SINKS - 1],
+              "tokens around a tile's end": [S // 128 * 128 - 1, S // 128 * 128]}[at]
+    for slot in range(B * H):
+        _scales(layers[1], slot)[tokens] = value
+    b, wb = _run(kvc, layers, q, window, weights=True)
+    assert bool(torch.isfinite(wa).all()) and torch.equal(wa, wb)
+    seen = torch.from_numpy(window_visible(N, S, window, SINKS))[:, tokens].any(1)
+    assert torch.equal(a[:, :, ~seen], b[:, :, ~seen])
+    hit = b[:, :, seen]
+    if value != value:
+        assert bool(torch.isnan(hit).all())
+    else:
+        assert not bool(torch.isfinite(hit).all(-1).any())
