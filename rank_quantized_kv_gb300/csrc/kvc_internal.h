@@ -208,7 +208,9 @@ cudaError_t launch_accept(const Params& p, AcceptArgs a, int pmax, cudaStream_t 
 // that one of its rows sees; the jobs' tiles are one line that is cut into equal
 // runs, one per CTA, so a CTA holds the ends of some jobs.  (A job that has fewer
 // tiles shares them out in the proportions of its stretch of the line.)  Each (job,
-// CTA) pair leaves a partial, number job + CTA.
+// CTA) pair leaves a partial, number job + CTA; where jobs that lie in one CTA are
+// written by it (cuts), the cut ones alone do, with numbers below twice the CTAs
+// (window_part).
 constexpr int kWindowTile = 32;  // tokens of a tile of the tensor-core kernels
 // Reference of a row that has seen tokens, all with scores of -inf (below fp32's
 // range); one that has seen none has -inf.
@@ -232,6 +234,7 @@ struct WindowArgs {
   int grid = 0, sms = 0;                 // CTAs of the main kernel; the device's SMs
   int mma = 0;                           // warp-level tensor cores: 8-row tiles of a job, 0: not
   int tc = 0;                            // tcgen05: 1; with mma 0: CUDA cores
+  int cuts = 0;                          // only jobs that are cut between CTAs leave partials
   int K = 0;                             // tcgen05: the operand's K
   float cb_mul = 1.f, w_mul = 1.f;       // tcgen05: scale of the centroids, its inverse
   uint64_t wait_ns = 0;                  // tcgen05: limit of the time without a finished tile
@@ -244,7 +247,7 @@ struct WindowArgs {
   float decay = 1.f;
   // workspace: key weights [n_slots][rows][NCk], sketch and outlier weights
   // [n_slots][rows][m + n_out], score offsets [n_slots][rows][c1_parts]; partials
-  // [jobs + grid - 1]: references and sums [rt], weighted sums [Dvp][rt]; per row its
+  // [jobs + grid - 1, cuts: 2 grid]: references and sums [rt], weighted sums [Dvp][rt]; per row its
   // reference and the inverse of its sum.  tcgen05: the key weights as two fp16 pieces
   // per job in the operand's layout [jobs][2][rt x K], per row [jobs][rt] the factor of
   // its products

@@ -402,11 +402,6 @@ __global__ void __launch_bounds__(kThreads)
 
 constexpr int kFactors = 64;
 
-// Jobs that lie in one CTA are written by it: only those that are cut are left.
-__host__ __device__ __forceinline__ bool combines_cuts(const Params& vp, const WindowArgs& t) {
-  return t.tc && vp.mode != KVC_MODE_UNIFORM;
-}
-
 // Join the partials of eight rows, normalise and write the output rows (uniform
 // values: project the weighted mean latent), and what the weights' pass needs of
 // a row.  Thread (d, q) of a group of 256 holds channel d of rows 4 q .. 4 q + 3; the
@@ -425,7 +420,7 @@ __global__ void __launch_bounds__(256 * GROUPS)
   constexpr int kCombineThreads = 256 * GROUPS;
   const int blocks = (t.rows + kRows - 1) / kRows;
   int slot = blockIdx.x / blocks, row0 = (blockIdx.x - slot * blocks) * kRows;
-  if (combines_cuts(vp, t)) {
+  if (t.cuts) {
     // block (cut, 8 rows): the job that the first run after it begins in; the cuts
     // before it must not lie in the same job
     const int per = t.rt / kRows, cut = 1 + blockIdx.x / per;
@@ -443,15 +438,10 @@ __global__ void __launch_bounds__(256 * GROUPS)
   const int beta = vu ? vp.basis_of[slot] : 0;
   const int jt = row0 / t.rt, rr = row0 - jt * t.rt;
   // the CTAs whose runs hold the job's tiles
-  const int64_t job = (int64_t)slot * t.row_tiles + jt, lo = job * t.tps, hi = lo + t.tps;
-  int64_t c0 = lo * t.grid / t.total;
-  while (window_run(t, c0 + 1) <= lo) ++c0;
-  while (window_run(t, c0) > lo) --c0;
-  int64_t c1 = max(c0, (hi * t.grid - 1) / t.total);
-  while (window_run(t, c1 + 1) < hi) ++c1;
-  while (window_run(t, c1) >= hi) --c1;
+  const int64_t job = (int64_t)slot * t.row_tiles + jt, lo = job * t.tps;
+  const int64_t c0 = window_cta(t, lo), c1 = window_cta(t, lo + t.tps - 1);
   const int splits = (int)(c1 - c0) + 1;
-  const size_t p0 = (size_t)(job + c0);
+  const size_t p0 = (size_t)window_part(t, job, c0);
   if (vu)
     for (int j = tid; j < t.Dv; j += kCombineThreads) {
       int width = 0;
@@ -674,7 +664,7 @@ struct Take {
 // The workspace's arrays in t; its bytes.
 size_t lay_out(const Params& kp, WindowArgs& t, void* workspace) {
   const size_t rows = (size_t)kp.n_slots * t.rows;
-  const size_t parts = (size_t)kp.n_slots * t.row_tiles + t.grid - 1;
+  const size_t parts = t.cuts ? 2 * (size_t)t.grid : (size_t)kp.n_slots * t.row_tiles + t.grid - 1;
   Take take(workspace);
   t.w = take.operator()<float>(t.tc && !t.weights ? 0 : rows * t.NCk);
   t.wx = take.operator()<float>(rows * (t.m + t.n_out));
@@ -732,6 +722,7 @@ size_t window_plan(const Params& kp, const Params& vp, WindowArgs& t, bool gener
   // few tiles have a CTA each all the same
   const int64_t runs = t.mma ? std::max<int64_t>(t.total / 8, jobs) : t.total;
   t.grid = (int)std::min<int64_t>(runs, ctas * (int64_t)sms);
+  t.cuts = t.tc && vp.mode != KVC_MODE_UNIFORM;
   t.wsplits = t.weights && (t.mma || t.tc) ? window_weights_splits(kp, t) : 1;
   return lay_out(kp, t, nullptr);
 }
@@ -773,7 +764,7 @@ cudaError_t launch_attend_window(const Params& kp, const Params& vp, WindowArgs 
     e = launch_dependent(k, (unsigned)t.grid, kThreads, smem, s, kp, vp, t);
   }
   if (e != cudaSuccess) return e;
-  const unsigned combines = combines_cuts(vp, t) ? (unsigned)(t.grid - 1) * (unsigned)(t.rt / kRows) : row_blocks;
+  const unsigned combines = t.cuts ? (unsigned)(t.grid - 1) * (unsigned)(t.rt / kRows) : row_blocks;
   if (combines) {
     ++*nk;
     // four groups of threads where a row has many partials (at most total / jobs runs)

@@ -8,6 +8,20 @@ namespace kvc {
 
 // The run of tiles of CTA c is [window_run(t, c), window_run(t, c + 1)).
 __device__ __forceinline__ int64_t window_run(const WindowArgs& t, int64_t c) { return t.total * c / t.grid; }
+// The CTA whose run holds place `at` of the line.
+__device__ inline int64_t window_cta(const WindowArgs& t, int64_t at) {
+  int64_t c = at * t.grid / t.total;
+  while (window_run(t, c + 1) <= at) ++c;
+  while (window_run(t, c) > at) --c;
+  return c;
+}
+// Number of the first partial of a job whose tiles begin in CTA c0; those of the CTAs
+// after it follow.  Where only cut jobs leave partials they are numbered by CTA: one that
+// begins behind another job's end takes the odd number, and a job that begins in the CTA
+// where the last one ended always does.
+__device__ __forceinline__ int64_t window_part(const WindowArgs& t, int64_t job, int64_t c0) {
+  return t.cuts ? 2 * c0 + (window_run(t, c0) < job * t.tps) : job + c0;
+}
 
 // The tokens visible to a query at position pos of a batch entry: those of
 // [first, pos] within the window or before sink_end.

@@ -147,6 +147,7 @@ struct Place {
   int job, slot, jt, r0, nr, n, p0, p1;
   int whole;
   int first, sink_end, window;
+  int part;          // number of the partial, where it leaves one
   int a, na, b, i0;  // tiles, as in Tiles, from number i0 on
   int64_t at, run1;
   __device__ void begin(const Params& kp, const WindowArgs& t) {
@@ -176,6 +177,11 @@ struct Place {
     i0 = 0;
     n = tiles.count();
     whole = at == start && end == start + t.tps;
+    part = job + (int)blockIdx.x;
+    if (t.cuts && !whole) {
+      const int64_t c0 = at == start ? blockIdx.x : window_cta(t, start);
+      part = (int)(window_part(t, job, c0) + blockIdx.x - c0);
+    }
     if (!whole) {
       i0 = (int)((int64_t)n * (at - start) / t.tps);
       n = (int)((int64_t)n * (end - start) / t.tps) - i0;
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool has_a = n > 1 || (n == 1 && !(it0 & 1)), has_b = n > 1 || (n == 1 && (it0 & 1));
       const float inv = L > 0.f || L != L ? 1.f / L : M == -INFINITY ? 0.f : NAN;
       const bool direct = vg.whole && !VU;
-      const size_t part = (size_t)vg.job + blockIdx.x;
+      const size_t part = vg.part;
       if (direct) {
         if (wg == 0 && r < vg.nr && t.stats)
           t.stats[(size_t)vg.slot * t.rows + vg.r0 + r] = make_float2(M == -INFINITY ? 0.f : M, inv);
