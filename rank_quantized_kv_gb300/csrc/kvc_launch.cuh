@@ -5,7 +5,11 @@
 
 #include <cuda_runtime.h>
 
+#include <functional>
 #include <mutex>
+#include <new>
+#include <unordered_map>
+#include <utility>
 
 namespace kvc {
 
@@ -24,33 +28,40 @@ __device__ __forceinline__ void grid_dependents_launch() {
 // and the dynamic shared memory that it may use raised to `smem`.  (Both calls
 // take about a microsecond, which a decode step notices.)  The limit belongs to
 // the kernel, not to the calling thread, so all threads share one table under a
-// lock and the limit only grows.
+// lock and the limit only grows.  The library has some 150 such kernels, and a table
+// has an entry for each device: it grows with them.
 inline cudaError_t prepare_kernel(const void* kernel, int smem, int* regs = nullptr) {
-  struct Entry { const void* kernel; int device, smem, regs; };
+  struct Entry { int smem, regs; };
+  struct Hash {
+    size_t operator()(const std::pair<const void*, int>& k) const {
+      return std::hash<const void*>()(k.first) + 0x9e3779b9u * (size_t)k.second;
+    }
+  };
   static std::mutex lock;
-  constexpr int kEntries = 512;  // (kernel, device) pairs; the library has about 30 such kernels
-  static Entry cache[kEntries];
-  static int n = 0;
+  static auto* const table = new std::unordered_map<std::pair<const void*, int>, Entry, Hash>;  // (lives as long as the process)
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> held(lock);
-  int i = 0;
-  while (i < n && (cache[i].kernel != kernel || cache[i].device != device)) ++i;
-  if (i == n) {
-    if (n == kEntries) return cudaErrorMemoryAllocation;
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess) return e;
-    cache[n++] = Entry{kernel, device, -1, fa.numRegs};
+  try {
+    std::lock_guard<std::mutex> held(lock);
+    const auto key = std::make_pair(kernel, device);
+    auto at = table->find(key);
+    if (at == table->end()) {
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kernel);
+      if (e != cudaSuccess) return e;
+      at = table->emplace(key, Entry{-1, fa.numRegs}).first;
+    }
+    if (smem > at->second.smem) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      at->second.smem = smem;
+    }
+    if (regs) *regs = at->second.regs;
+    return cudaSuccess;
+  } catch (const std::bad_alloc&) {
+    return cudaErrorMemoryAllocation;
   }
-  if (smem > cache[i].smem) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    cache[i].smem = smem;
-  }
-  if (regs) *regs = cache[i].regs;
-  return cudaSuccess;
 }
 
 template <class... Params, class... Args>
