@@ -1171,7 +1171,9 @@ static kvc_status window_check(const kvc_layer* K, const kvc_layer* V, const kvc
   t.Pk_max = K->pmax;
   t.Pv_max = V->pmax;
   t.cb_mul = K->cb_mul;
-  t.w_mul = 1.f / K->cb_mul;
+  int exponent = 1;
+  t.w_frac = K->cb_mul > 0.f ? 2.f * std::frexp(1.f / K->cb_mul, &exponent) : 1.f;
+  t.w_pow = std::ldexp(1.f, exponent - 1);
   t.wait_ns = K->wait_ns;
   *ws_bytes = kvc::window_plan(K->p, V->p, t, K->path == KVC_PATH_GENERIC, kvc::sm_count());
   return KVC_OK;

@@ -236,7 +236,8 @@ struct WindowArgs {
   int tc = 0;                            // tcgen05: 1; with mma 0: CUDA cores
   int cuts = 0;                          // only jobs that are cut between CTAs leave partials
   int K = 0;                             // tcgen05: the operand's K
-  float cb_mul = 1.f, w_mul = 1.f;       // tcgen05: scale of the centroids, its inverse
+  float cb_mul = 1.f;                    // tcgen05: scale of the centroids
+  float w_frac = 1.f, w_pow = 1.f;       // and its inverse: in [1, 2) (uniform keys: 1), times a power of two
   uint64_t wait_ns = 0;                  // tcgen05: limit of the time without a finished tile
   int NCk = 0, Dv = 0, Dvp = 0;          // packed positions; value channels, padded to 4
   int Pk_max = 0, Pv_max = 0;            // largest packed key / value row

@@ -424,9 +424,11 @@ __global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 2 : 1)
               if (!V::kUniform && big > exp2i(was + 2.f))  // the next power of two
                 sref[nt][j] = (float)((__float_as_int(big) >> 23) - 126);
               float now = old + (sref[nt][j] - was);
-              if (m != -INFINITY && (m - old > kMove - was || !(old > kWindowLowest)))
+              if (m != -INFINITY && (m - old > kMove - was || !(old > kWindowLowest))) {
                 // the first reference, or a new one (the lowest: scores of -inf alone so far)
                 now = m > kWindowLowest ? m - kSet + sref[nt][j] : fmaxf(old, m);
+                if (m - now > kMove - sref[nt][j]) now = m;  // (past 2^27 fp32 has no such steps)
+              }
               const float f = old == now ? 1.f : ex2(old - now);
               l[nt][j] *= f;
 #pragma unroll

@@ -43,7 +43,8 @@ __device__ __forceinline__ float larger(float most, float v) {
 
 // KD: steps of 16 over the head size.  OPERAND: two fp16 pieces in the layout of a
 // K-major operand without swizzle (cores of 8 rows x 8 positions, 128 contiguous bytes,
-// adjacent along K), per row the inverse of its power of two; else fp32 weights.  REST:
+// adjacent along K), per row a power of two, the only factor from its products to its
+// scores, so that these are exact; else fp32 weights.  REST:
 // fp32 queries; those of 16 bits have no second piece to speak of.
 template <int KD, bool OPERAND, bool REST>
 __global__ void __launch_bounds__(kThreads, REST ? 1 : 2) window_project_kernel(const Params kp, const WindowArgs t) {
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, REST ? 1 : 2) window_project_kernel(
           const size_t bk = (size_t)beta * kp.r + k;
           s = row_scale(kp.vnorm[bk]);
           f = t.scale_log2 * (uniform ? kp.step[bk] : 1.f) / s;
+          if (OPERAND) f *= t.w_frac;  // (the fraction here, so that a row's factor is a power of two)
         }
         up[j] = s;
         down[j] = f;
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, REST ? 1 : 2) window_project_kernel(
     for (int e = 0; e < 2; ++e) {
       const float mul = row_scale(quad_max(most[e]));
       const int r = 16 * warp + g + 8 * e;
-      if (c == 0) t.wscale[(size_t)job * kRows + r] = t.w_mul / mul;
+      if (c == 0) t.wscale[(size_t)job * kRows + r] = t.w_pow / mul;
       uint32_t* w = reinterpret_cast<uint32_t*>(t.w16 + (size_t)job * 2 * kRows * t.K) + (r >> 3) * (KC * 32) + (r & 7) * 4 + c;
 #pragma unroll
       for (int nt = 0; nt < 16; ++nt)

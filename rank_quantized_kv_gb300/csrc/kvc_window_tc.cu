@@ -691,8 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the first reference, or a new one, whole steps of log2 away
             float now = ref, f = 1.f;
             if (need && most > kWindowLowest) {
-              const float to = most - kSet + sref;
-              now = ref == -INFINITY ? to : ref + ceilf(to - ref);
+              const float to = most - kSet + sref, up = to - ref;
+              now = up < 1048576.f ? ref + ceilf(up) : to;
+              if (most - now > kMove - sref) now = most;  // (past 2^27 fp32 has no such steps)
               f = ex2(ref - now);
             }
             ref = now;
