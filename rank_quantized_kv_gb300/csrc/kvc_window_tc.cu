@@ -27,12 +27,16 @@
 // row sees, moved when one exceeds it four times.  Their sum is one exponent, so a scale
 // costs the loop nothing.
 //
-// Bound: a tile's 16384 exponentials take 1024 cycles of the SM's 16 a cycle, its MMAs
-// 768, softmax and decoding about 1000 issue slots a scheduler.  8 slots of 8192 rows,
-// a window of 2048 tokens, 3-bit keys and int8 values of 128 channels: 208 us, 3600 to
-// 4400 cycles for the two tiles that the groups have in hand.  The score product of a tile
-// takes 1280, both operands read from shared memory, a group's softmax 4400, and a change
-// of jobs 10000.
+// Bound: latency in the softmax groups; no unit is near its rate.  8 slots of 8192 rows,
+// a window of 2048 tokens, 3-bit keys and int8 values of 128 channels: 212 us, 61 tiles
+// a CTA at 6000 cycles each, of which the tensor pipe works 1530 (three products of
+// 128^3), a scheduler issues 2600 instructions and the XU pipe is busy for a tenth.  With
+// clocks read in every role (15 % slower): a group is in the loop over a tile's columns for
+// 36 to 50 % of its time (5000 to 6700 cycles for each of its 31 tiles), at the ends of
+// segments for 13 % (11000 each, five a CTA), with the tile's scales for 5 % (mostly cold
+// code at a segment's first tiles) and waits for scores for 2 to 12 %, the rest lies
+// between these; the score products' warp waits for the groups for 63 %, the decoders for
+// a place for values for 45 %.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -281,6 +285,32 @@ __device__ __forceinline__ uint4 centred(uint2 bits, uint32_t entry) {
   w.set(entry);
   const uint2 b = w.split(bits);
   return make_uint4(w.pair(b, 0), w.pair(b, 1), w.pair(b, 2), w.pair(b, 3));
+}
+
+// The largest finite scale of the columns in [ca, ca1] and [cb, cb1], a row's own, of 32
+// at a time: a lane holds one for the warp's rows.  (Kept short: it runs twice a segment,
+// and its instructions come from L2.)
+__device__ __forceinline__ float largest_seen(const float* scale, int ca, int ca1, int cb, int cb1) {
+  float most = 0.f;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t see = bits_between(ca - 32 * q, ca1 - 32 * q) | bits_between(cb - 32 * q, cb1 - 32 * q);
+    if (!__any_sync(kFull, see)) continue;
+    const float x = scale[32 * q + lane];
+    const float y = x > 0.f && x <= 65504.f ? x : 0.f;
+    if (__all_sync(kFull, see == 0u || see == ~0u)) {
+      const uint32_t u = __reduce_max_sync(kFull, __float_as_uint(y));
+      if (see) most = fmaxf(most, __uint_as_float(u));
+    } else {
+#pragma unroll 4
+      for (int e = 0; e < 32; ++e) {
+        const float w = __shfl_sync(kFull, y, e);
+        if (see >> e & 1u) most = fmaxf(most, w);
+      }
+    }
+  }
+  return most;
 }
 
 template <int KMODE, int VMODE>
@@ -609,20 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 spoilt = ((c >= ca && c <= ca1) || (c >= cb && c <= cb1)) &&
                          __hisnan(__ushort_as_half(side_s[it % kSideRing][1][c]));
             if (!all || odd) {  // the largest may be hidden from this row
-              most = 0.f;
-#pragma unroll 1
-              for (int c = 0; c < kTile; c += 16) {
-                const uint32_t see = bits_between(ca - c, ca1 - c) | bits_between(cb - c, cb1 - c);
-                if (!__any_sync(kFull, see & 0xffffu)) continue;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 f = *reinterpret_cast<const float4*>(&cs[wg][buf][c + 4 * e]);
-                  if ((see >> (4 * e) & 1u) && f.x <= 65504.f) most = fmaxf(most, f.x);
-                  if ((see >> (4 * e) & 2u) && f.y <= 65504.f) most = fmaxf(most, f.y);
-                  if ((see >> (4 * e) & 4u) && f.z <= 65504.f) most = fmaxf(most, f.z);
-                  if ((see >> (4 * e) & 8u) && f.w <= 65504.f) most = fmaxf(most, f.w);
-                }
-              }
+              most = largest_seen(cs[wg][buf], ca, ca1, cb, cb1);
             }
             float f = 1.f;
             if (most > limit) {
