@@ -23,10 +23,12 @@
 //
 // What bounds it: the instructions of the decoding, on the four warps that a scheduler
 // has at 128 registers a thread.  3-bit keys and int8 values of 128 channels take about
-// 400 for 16 tokens of up to eight rows: 128 slots, 4 rows, 16384 tokens in 92 us, with
-// 54 % of the issue slots used, the ALU pipe busy for 45 % of the time, shared memory's
-// for 54, the tensor pipe for 25, and HBM at 52 % of its rate; a window of 4096 of them in 39; uniform codes of 32 components,
-// 8 slots of 100064 tokens, in 29 (40 packed positions in three steps; in four 31).
+// 400 for 16 tokens of up to eight rows: 128 slots, 4 rows, 16384 tokens in 94 us with
+// their scores kept, 54 % of the issue slots used, the ALU pipe busy for 46 % of the time,
+// shared memory's for 54, the tensor pipe for 25, and HBM at 53 % of its rate.  A window
+// of 4096 of them takes 38, of which the decoding is some 24: the rest is a CTA's start,
+// changes of jobs and joins.  Uniform codes of 32 components, 8 slots of 100064 tokens, 29
+// (40 packed positions in three steps; in four 31).
 // Two CTAs per SM of eight warps for one tile of rows (the weights in registers), one
 // for more.
 #pragma once

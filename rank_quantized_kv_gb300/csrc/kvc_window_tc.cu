@@ -29,8 +29,8 @@
 //
 // Bound: latency in the softmax groups; no unit is near its rate.  8 slots of 8192 rows,
 // a window of 2048 tokens, 3-bit keys and int8 values of 128 channels: 212 us, 61 tiles
-// a CTA at 6000 cycles each, of which the tensor pipe works 1530 (three products of
-// 128^3), a scheduler issues 2600 instructions and the XU pipe is busy for a tenth.  With
+// a CTA at 6100 cycles each, of which the tensor pipe works 1535 (three products of
+// 128^3), a scheduler issues 2660 instructions and the XU pipe is busy for a tenth.  With
 // clocks read in every role (15 % slower): a group is in the loop over a tile's columns for
 // 36 to 50 % of its time (5000 to 6700 cycles for each of its 31 tiles), at the ends of
 // segments for 13 % (11000 each, five a CTA), with the tile's scales for 5 % (mostly cold
